@@ -36,6 +36,8 @@
  *                    stored
  *      cu_seqlens_q  int32 [num_seqs+1], prefix sums of new-token counts
  *      cu_seqlens_k  int32 [num_seqs+1], prefix sums of (cached + new) counts
+ *      key_weights   fp32 [num_blocks, Hkv, block_size]: for each slot and kv
+ *                    head, the attention weight its key has received so far
  *  - GQA: query head h reads kv head h / (Hq / Hkv).
  *  - Pointers to bf16 data must be 16-byte aligned.
  *  - Every call is asynchronous on `stream` (a cudaStream_t; NULL = the
@@ -278,6 +280,138 @@ pkv_status pkv_paged_prefill_attn(uint16_t *out, const uint16_t *q, const uint16
 size_t pkv_prefill_workspace_size(void);
 
 /*
+ * Key weights and eviction -- the pages' engine frees whole sequences when its
+ * blocks run out (CSDN essay, Mountain 1: basic preemption, no swap); these
+ * calls let a sequence go on in fewer blocks instead, by giving up the keys
+ * that have received the least attention.  key_weights holds, beside every
+ * key of the cache, the softmax weight it has received, summed over queries
+ * and over the query heads of its kv head:
+ *   pkv_paged_prefill_weights       adds the weights of a prompt chunk's last queries,
+ *   pkv_paged_decode_weights_attn   attends one new token and adds its weights,
+ *   pkv_kv_evict                    keeps the heaviest keys and the most recent.
+ * A key's sum starts when its token arrives: the call that brings the token
+ * sets the sum, later calls add to it, so key_weights needs no clearing when a
+ * block changes hands.  Sums are fp32; a slot held by one sequence gets one
+ * addition per call, so its sum does not depend on the order of anything.  A
+ * block that several sequences of the batch share collects the weights of all
+ * of them, by atomic additions whose order (hence last bit) can differ.
+ */
+
+/*
+ * Bytes of device workspace paged_decode_weights_attn needs (split-K partials
+ * and the logits of max_total_blocks blocks).  Returns 0 for invalid sizes
+ * and for sizes whose workspace would not fit a size_t.
+ */
+size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int64_t max_total_blocks);
+
+/*
+ * paged_decode_weights_attn -- decode attention that collects key weights.
+ *
+ * out as for paged_decode_attn (with new_k, new_v and slot_mapping: as for
+ * paged_decode_store_attn, storing the new tokens too; all three NULL: no
+ * store), and with w[s,h,p] the softmax weight of query head h for position p,
+ * a[s,j,p] = sum of w[s,h,p] over the heads h of kv head j's group:
+ *   key_weights(slot of p, j) += a[s,j,p]  for p < context_lens[s] - 1
+ *   key_weights(slot of p, j)  = a[s,j,p]  for p = context_lens[s] - 1
+ * (the newest token is this call's own: its slot's old sum was another's).
+ * fp32 logits and statistics; the weights are rounded to bf16 for the product
+ * with V alone (as the tensor cores take them).
+ *
+ * workspace: device memory of at least pkv_decode_weights_workspace_size(...)
+ * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that
+ * overlap on the device must not share a workspace.
+ *
+ * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its
+ * row of out is left as it was; one that is longer than its table is flagged
+ * and clamped, and all of its weights are added.  A block id out of range is
+ * flagged, its weights are dropped and the sequence's output is undefined.
+ * More blocks than max_total_blocks: PKV_DEV_WORKSPACE, nothing is written.
+ *
+ * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in
+ * {64, 128, 256, 512}; num_seqs <= 16384.
+ */
+pkv_status pkv_paged_decode_weights_attn(
+    uint16_t *out, float *key_weights, const uint16_t *q, const uint16_t *new_k,
+    const uint16_t *new_v, const int32_t *slot_mapping, uint16_t *k_cache, uint16_t *v_cache,
+    const int32_t *block_tables, const int32_t *context_lens, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    int64_t max_total_blocks, float scale, void *workspace, size_t workspace_bytes,
+    int32_t *dev_status, void *stream);
+
+/* Bytes of device workspace paged_prefill_weights needs (0 for invalid sizes
+ * and for sizes whose workspace would not fit a size_t). */
+size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max_seqlen_q,
+                                          int window, int num_q_heads, int num_kv_heads,
+                                          int max_blocks_per_seq, int block_size);
+
+/*
+ * paged_prefill_weights -- the key weights of a prompt chunk's last queries.
+ *
+ * q, k_cache, block_tables and cu_seqlens as for paged_prefill_attn, beside
+ * which it is called (the chunk's K must be in the cache).  For a sequence of
+ * n new queries of which the last R = min(window, n) count, c cached tokens,
+ * query i at position c + i attending to keys 0 .. c + i:
+ *   a[j,p] = sum of softmax_p(scale * <q_i,h, K_s[p, j]>) over the counted
+ *            queries i with c + i >= p and the heads h of kv head j's group
+ *   key_weights(slot of p, j) += a[j,p]  for p < c
+ *   key_weights(slot of p, j)  = a[j,p]  for p >= c   (the chunk's own keys)
+ * window >= max_seqlen_q counts every query.  A sequence with n = 0 changes
+ * nothing.  One whose lengths do not fit (n > max_seqlen_q, n > len_k, more
+ * keys than its table holds) is flagged, PKV_DEV_BAD_SEQLEN, and left out; a
+ * block id out of range is flagged and its keys' sums are left as they were.
+ *
+ * workspace: device memory of at least pkv_prefill_weights_workspace_size(...)
+ * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that
+ * overlap on the device must not share a workspace.
+ *
+ * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in
+ * {64, 128, 256, 512}.
+ */
+pkv_status pkv_paged_prefill_weights(
+    float *key_weights, const uint16_t *q, const uint16_t *k_cache, const int32_t *block_tables,
+    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int num_seqs, int64_t total_q,
+    int max_seqlen_q, int window, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int max_blocks_per_seq, int64_t num_blocks, float scale, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * kv_evict -- shorten sequences to `budget` tokens, in place.
+ *
+ * For every sequence s with L = context_lens[s] > budget, and every kv head j
+ * by itself: of the positions before the last `recent`, the H = budget -
+ * recent with the largest key_weights are kept (a NaN counts as -inf, -0 as
+ * +0; of equal ones the lowest position), and the last `recent` are kept.
+ * Kept positions below H stay where they are; those behind, in order, take
+ * the places below H that are not kept, in order; the recent ones follow in
+ * order at H .. budget - 1.  K, V and key_weights move together.  Places
+ * from `budget` on, and blocks past the first ceil(budget / block_size), are
+ * left as they were and are the caller's to reuse (pkv_bm_evict).
+ *   kept      int32 [num_seqs, Hkv, budget]: the position, before the call,
+ *             of the token now at each place (-1 past a shorter sequence's end)
+ *   new_lens  int32 [num_seqs]: min(L, budget); must not be context_lens itself
+ * Sequences of at most `budget` tokens are not touched.  Decode does not
+ * depend on the order of the keys, so attention goes on with new_lens as the
+ * context length; the positions that the model encodes count on from the old
+ * length.  No block may belong to two sequences of the call, nor to one
+ * outside it that still needs its keys (a shared prefix): its rows move.
+ *
+ * A negative context length, or one longer than the table, is flagged
+ * (PKV_DEV_BAD_CONTEXT), a block id out of range among the sequence's blocks
+ * too (PKV_DEV_BAD_BLOCK): the sequence is left as it was, its kept is all -1
+ * and its new_lens its old length.
+ *
+ * Two launches, no workspace.  Requires 0 <= recent <= budget, budget > 0;
+ * head_dim in {64, 128}; block_size in {64, 128, 256, 512}; budget and
+ * max_blocks_per_seq * block_size at most 2^20 (PKV_ERR_UNSUPPORTED).
+ */
+pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *key_weights,
+                        const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
+                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                        int64_t num_blocks, int budget, int recent, int32_t *kept,
+                        int32_t *new_lens, int32_t *dev_status, void *stream);
+
+/*
  * w4a16_dequant -- W4A16-G128 weight dequantisation (s1nh.org post on
  * upgrading nano-vllm to big-vLLM, section on quantisation: every int32 of
  * weight_packed holds eight 4-bit values; int32 -> u4 unpack -> s4
@@ -335,6 +469,17 @@ pkv_status pkv_bm_allocate(pkv_block_manager *m, int64_t seq_id, const int32_t *
 pkv_status pkv_bm_append(pkv_block_manager *m, int64_t seq_id, int32_t token);
 /* Release the sequence's blocks (reference count - 1 each). */
 pkv_status pkv_bm_free(pkv_block_manager *m, int64_t seq_id);
+
+/* The sequence has been cut to its first keep_tokens > 0 places, by pkv_kv_evict
+ * on its block table as it was before this call: releases the blocks past
+ * them.  The rest lose their content keys, and the sequence's later blocks get
+ * none: what they hold is no longer the prompt's tokens in order.  Nothing
+ * changes for a sequence of at most keep_tokens tokens.  PKV_ERR_UNSUPPORTED,
+ * with nothing changed, when one of the first ceil(keep_tokens / block_size)
+ * blocks is shared with another sequence: evicting would move the other's
+ * keys, so ask before launching pkv_kv_evict.  Released blocks can be handed
+ * out at once; work that writes them must follow the eviction on its stream. */
+pkv_status pkv_bm_evict(pkv_block_manager *m, int64_t seq_id, int keep_tokens);
 
 /* Tokens held by the sequence, or -1 if unknown. */
 int pkv_bm_num_tokens(const pkv_block_manager *m, int64_t seq_id);

@@ -28,3 +28,9 @@ from .dequant import (  # noqa: F401
     w4a16_dequant,
     w4a16_dequant_bf16,
 )
+from .weights import (  # noqa: F401
+    decode_weights,
+    evict_map,
+    kv_evict,
+    prefill_weights,
+)

@@ -12,6 +12,13 @@ has not been built, `load()` raises.
                           scale, workspace, max_total_blocks)
     pkv.paged_prefill_attn(out, q, k_cache, v_cache, block_tables, cu_q, cu_k,
                            max_seqlen_q, scale)   # workspace: one per stream, cached
+    # a bounded cache: collect the weight each key receives, keep the heaviest
+    pkv.paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_q, cu_k,
+                              max_seqlen_q, window, scale, prompt_workspace)
+    pkv.paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_tables,
+                                  context_lens, scale, workspace, max_total_blocks)
+    pkv.kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget,
+                 recent, kept, new_lens)
 """
 from __future__ import annotations
 
@@ -54,6 +61,17 @@ SIGNATURES = {
                                         _c_sz, _p, _p]),
     "pkv_prefill_workspace_size": (_c_sz, []),
     "pkv_test_decode_fault": (_c_int, [_c_i64, _c_int]),
+    "pkv_decode_weights_workspace_size": (_c_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_i64]),
+    "pkv_paged_decode_weights_attn": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_int,
+                                               _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
+                                               _c_i64, _c_f, _p, _c_sz, _p, _p]),
+    "pkv_prefill_weights_workspace_size": (_c_sz, [_c_int, _c_i64, _c_int, _c_int, _c_int, _c_int,
+                                                   _c_int, _c_int]),
+    "pkv_paged_prefill_weights": (_c_int, [_p, _p, _p, _p, _p, _p, _c_int, _c_i64, _c_int, _c_int,
+                                           _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f,
+                                           _p, _c_sz, _p, _p]),
+    "pkv_kv_evict": (_c_int, [_p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
+                              _c_int, _c_int, _p, _p, _p, _p]),
     "pkv_w4a16_dequant": (_c_int, [_p, _p, _p, _c_i64, _c_i64, _c_int, _p]),
     "pkv_bm_create": (_p, [_c_int, _c_int]),
     "pkv_bm_destroy": (None, [_p]),
@@ -61,6 +79,7 @@ SIGNATURES = {
     "pkv_bm_allocate": (_c_int, [_p, _c_i64, _p, _c_int, ctypes.POINTER(_c_int)]),
     "pkv_bm_append": (_c_int, [_p, _c_i64, ctypes.c_int32]),
     "pkv_bm_free": (_c_int, [_p, _c_i64]),
+    "pkv_bm_evict": (_c_int, [_p, _c_i64, _c_int]),
     "pkv_bm_num_tokens": (_c_int, [_p, _c_i64]),
     "pkv_bm_block_table": (_c_int, [_p, _c_i64, _p, _c_int]),
     "pkv_bm_slots": (_c_int, [_p, _c_i64, _c_int, _c_int, _p]),
@@ -298,6 +317,167 @@ def paged_prefill_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_
     _check(st, "pkv_paged_prefill_attn")
 
 
+def _need_key_weights(key_weights, k_cache):
+    import torch
+
+    NB, BS, Hkv, _ = k_cache.shape
+    _need(key_weights, torch.float32, "key_weights", 3)
+    if tuple(key_weights.shape) != (NB, Hkv, BS):
+        raise ValueError(f"key_weights: expected [num_blocks, Hkv, block_size] = {(NB, Hkv, BS)}")
+
+
+def _need_status(dev_status):
+    import torch
+
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+
+
+def _same_device(what, *tensors):
+    """Every tensor on the first one's device, which must be the current one
+    (the library launches on the current device)."""
+    import torch
+
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or devices.pop().index != torch.cuda.current_device():
+        raise ValueError(f"{what}: all tensors must be on the current CUDA device")
+
+
+def _workspace(n, what, device):
+    import torch
+
+    if n == 0:
+        raise ValueError(f"{what}: no workspace for these sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_weights_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                             max_total_blocks, device="cuda"):
+    """Allocate a zero-filled workspace for paged_decode_weights_attn."""
+    n = int(load().pkv_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                     head_dim, block_size, max_total_blocks))
+    return _workspace(n, "decode_weights_workspace", device)
+
+
+def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_tables, context_lens,
+                              scale, workspace, max_total_blocks, k=None, v=None,
+                              slot_mapping=None, dev_status=None, stream=None) -> None:
+    """paged_decode_attn (with k, v [S, Hkv, D] and slot_mapping [S]:
+    paged_decode_store_attn) that also adds the weight each key received to
+    key_weights [NB, Hkv, BS] (fp32) and sets the newest key's."""
+    import torch
+
+    lib = load()
+    store = (k, v, slot_mapping)
+    if any(t is None for t in store) and any(t is not None for t in store):
+        raise ValueError("paged_decode_weights_attn: k, v and slot_mapping go together")
+    for name, t, dt, nd in (("out", out, torch.bfloat16, 3), ("q", q, torch.bfloat16, 3),
+                            ("k", k, torch.bfloat16, 3), ("v", v, torch.bfloat16, 3),
+                            ("slot_mapping", slot_mapping, torch.int32, 1),
+                            ("k_cache", k_cache, torch.bfloat16, 4),
+                            ("v_cache", v_cache, torch.bfloat16, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("context_lens", context_lens, torch.int32, 1),
+                            ("workspace", workspace, torch.uint8, 1)):
+        if t is not None:
+            _need(t, dt, name, nd)
+    _need_key_weights(key_weights, k_cache)
+    _need_status(dev_status)
+    S, Hq, D = q.shape
+    NB, BS, Hkv, Dc = k_cache.shape
+    if Dc != D or tuple(out.shape) != (S, Hq, D) or block_tables.shape[0] != S or \
+            context_lens.shape[0] != S or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("paged_decode_weights_attn: inconsistent shapes")
+    if k is not None and (tuple(k.shape) != (S, Hkv, D) or tuple(v.shape) != (S, Hkv, D) or
+                          slot_mapping.shape[0] != S):
+        raise ValueError("paged_decode_weights_attn: inconsistent shapes of the new tokens")
+    _same_device("paged_decode_weights_attn", out, key_weights, q, k_cache, v_cache, block_tables,
+                 context_lens, workspace, k, v, slot_mapping, dev_status)
+    st = lib.pkv_paged_decode_weights_attn(
+        _ptr(out), _ptr(key_weights), _ptr(q), _ptr(k), _ptr(v), _ptr(slot_mapping),
+        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Hq, Hkv, D, BS,
+        block_tables.shape[1], NB, int(max_total_blocks), float(scale), _ptr(workspace),
+        workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(st, "pkv_paged_decode_weights_attn")
+
+
+def prefill_weights_workspace(num_seqs, total_q, max_seqlen_q, window, num_q_heads, num_kv_heads,
+                              max_blocks_per_seq, block_size, device="cuda"):
+    """Allocate a zero-filled workspace for paged_prefill_weights."""
+    n = int(load().pkv_prefill_weights_workspace_size(
+        num_seqs, total_q, max_seqlen_q, _window(window), num_q_heads, num_kv_heads,
+        max_blocks_per_seq, block_size))
+    return _workspace(n, "prefill_weights_workspace", device)
+
+
+def _window(window) -> int:
+    return min(int(window), 0x7FFFFFFF)
+
+
+def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, cu_seqlens_k,
+                          max_seqlen_q, window, scale, workspace, dev_status=None,
+                          stream=None) -> None:
+    """Adds to key_weights [NB, Hkv, BS] (fp32) the weight that the last
+    `window` queries of each prompt chunk give to the keys cached before it,
+    and sets the sums of the chunk's own keys (arguments as for
+    paged_prefill_attn, beside which it is called)."""
+    import torch
+
+    lib = load()
+    for name, t, dt, nd in (("q", q, torch.bfloat16, 3), ("k_cache", k_cache, torch.bfloat16, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("cu_seqlens_q", cu_seqlens_q, torch.int32, 1),
+                            ("cu_seqlens_k", cu_seqlens_k, torch.int32, 1),
+                            ("workspace", workspace, torch.uint8, 1)):
+        _need(t, dt, name, nd)
+    _need_key_weights(key_weights, k_cache)
+    _need_status(dev_status)
+    T, Hq, D = q.shape
+    NB, BS, Hkv, Dc = k_cache.shape
+    S = cu_seqlens_q.shape[0] - 1
+    if Dc != D or block_tables.shape[0] != S or cu_seqlens_k.shape[0] != S + 1:
+        raise ValueError("paged_prefill_weights: inconsistent shapes")
+    _same_device("paged_prefill_weights", key_weights, q, k_cache, block_tables, cu_seqlens_q,
+                 cu_seqlens_k, workspace, dev_status)
+    st = lib.pkv_paged_prefill_weights(
+        _ptr(key_weights), _ptr(q), _ptr(k_cache), _ptr(block_tables), _ptr(cu_seqlens_q),
+        _ptr(cu_seqlens_k), S, T, int(max_seqlen_q), _window(window), Hq, Hkv, D, BS,
+        block_tables.shape[1], NB, float(scale), _ptr(workspace), workspace.numel(),
+        _ptr(dev_status), _stream(stream))
+    _check(st, "pkv_paged_prefill_weights")
+
+
+def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, recent, kept,
+             new_lens, dev_status=None, stream=None) -> None:
+    """Shortens every sequence longer than `budget` to its last `recent` tokens
+    and, per kv head, the heaviest others by key_weights, in place.
+    kept [S, Hkv, budget] int32: the old position of what is now at each place;
+    new_lens [S] int32: the new context lengths (see include/pkv.h)."""
+    import torch
+
+    lib = load()
+    for name, t, dt, nd in (("k_cache", k_cache, torch.bfloat16, 4),
+                            ("v_cache", v_cache, torch.bfloat16, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("context_lens", context_lens, torch.int32, 1),
+                            ("kept", kept, torch.int32, 3), ("new_lens", new_lens, torch.int32, 1)):
+        _need(t, dt, name, nd)
+    _need_key_weights(key_weights, k_cache)
+    _need_status(dev_status)
+    NB, BS, Hkv, D = k_cache.shape
+    S = block_tables.shape[0]
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or context_lens.shape[0] != S or \
+            new_lens.shape[0] != S or tuple(kept.shape) != (S, Hkv, int(budget)):
+        raise ValueError("kv_evict: inconsistent shapes")
+    _same_device("kv_evict", k_cache, v_cache, key_weights, block_tables, context_lens, kept,
+                 new_lens, dev_status)
+    st = lib.pkv_kv_evict(_ptr(k_cache), _ptr(v_cache), _ptr(key_weights), _ptr(block_tables),
+                          _ptr(context_lens), S, Hkv, D, BS, block_tables.shape[1], NB,
+                          int(budget), int(recent), _ptr(kept), _ptr(new_lens), _ptr(dev_status),
+                          _stream(stream))
+    _check(st, "pkv_kv_evict")
+
+
 def w4a16_dequant(out, packed, scales, group_size=128, stream=None) -> None:
     """out [N, K] bf16 <- packed [N, K/8] int32 (eight 4-bit values per word,
     lowest nibble first, value = nibble - 8) times scales [N, K/128] bf16."""
@@ -359,6 +539,12 @@ class BlockManager:
 
     def free(self, seq_id: int) -> None:
         _check(self._lib.pkv_bm_free(self._h, int(seq_id)), "pkv_bm_free")
+
+    def evict(self, seq_id: int, keep_tokens: int) -> None:
+        """The sequence is cut to its first keep_tokens places by kv_evict on
+        its table as it was before this call; raises, changing nothing, when
+        another sequence shares one of the blocks that eviction would rewrite."""
+        _check(self._lib.pkv_bm_evict(self._h, int(seq_id), int(keep_tokens)), "pkv_bm_evict")
 
     def num_tokens(self, seq_id: int) -> int:
         return int(self._lib.pkv_bm_num_tokens(self._h, int(seq_id)))

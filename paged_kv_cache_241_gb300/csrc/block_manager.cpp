@@ -43,6 +43,7 @@ uint64_t block_key(uint64_t parent, const int32_t *tokens, int n) {
 struct Seq {
   std::vector<int32_t> table;   // physical block of each logical block
   std::vector<int32_t> tokens;  // all tokens so far (keys of blocks that fill up)
+  bool cut = false;             // evicted: places no longer hold the tokens in order
 };
 
 }  // namespace
@@ -81,13 +82,16 @@ struct pkv_block_manager {
     if (free_head < 0) return -1;
     const int b = free_head;
     unlink_free(b);
-    if (key[b] != 0) {
-      auto it = by_key.find(key[b]);
-      if (it != by_key.end() && it->second == b) by_key.erase(it);
-      key[b] = 0;
-    }
+    drop_key(b);
     ref[b] = 1;
     return b;
+  }
+  // The block no longer holds the tokens that it was keyed for.
+  void drop_key(int b) {
+    if (key[b] == 0) return;
+    auto it = by_key.find(key[b]);
+    if (it != by_key.end() && it->second == b) by_key.erase(it);
+    key[b] = 0;
   }
   // The keyed block holding exactly these tokens after `parent`, or -1.
   int lookup(uint64_t k, const int32_t *tokens) const {
@@ -196,7 +200,7 @@ extern "C" pkv_status pkv_bm_append(pkv_block_manager *m, int64_t seq_id, int32_
     s.table.push_back(m->take_fresh());
   }
   s.tokens.push_back(token);
-  if ((len + 1) % bs == 0) {  // a block just filled up: key it for later sequences
+  if ((len + 1) % bs == 0 && !s.cut) {  // a block just filled up: key it for later sequences
     const int i = (len + 1) / bs - 1;
     const int b = s.table[i];
     if (m->key[b] == 0) {
@@ -214,6 +218,23 @@ extern "C" pkv_status pkv_bm_free(pkv_block_manager *m, int64_t seq_id) {
   // Last block first, so that a sequence's tail is reused before its prefix.
   for (int i = (int)it->second.table.size() - 1; i >= 0; --i) m->release(it->second.table[i]);
   m->seqs.erase(it);
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_bm_evict(pkv_block_manager *m, int64_t seq_id, int keep_tokens) {
+  if (m == nullptr || keep_tokens <= 0) return PKV_ERR_INVALID_ARG;
+  auto it = m->seqs.find(seq_id);
+  if (it == m->seqs.end()) return PKV_ERR_INVALID_ARG;
+  Seq &s = it->second;
+  if ((int)s.tokens.size() <= keep_tokens) return PKV_OK;
+  const int keep = (keep_tokens + m->block_size - 1) / m->block_size;
+  for (int i = 0; i < keep; ++i)
+    if (m->ref[s.table[i]] != 1) return PKV_ERR_UNSUPPORTED;
+  for (int i = (int)s.table.size() - 1; i >= keep; --i) m->release(s.table[i]);
+  s.table.resize(keep);
+  s.tokens.resize(keep_tokens);
+  s.cut = true;
+  for (int b : s.table) m->drop_key(b);
   return PKV_OK;
 }
 
