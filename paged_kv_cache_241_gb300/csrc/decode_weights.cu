@@ -21,10 +21,13 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarpsMost = 8;        // warps per CTA (one CTA per SM)
+constexpr int kStages = 3;           // ring of tiles per warp
 constexpr int kMaxSeqs = 16384;
-constexpr int kMaxChunk = 512;
+constexpr int kMaxChunk = 256;
+constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
+constexpr int kJoinThreads = 256;
+constexpr int kJoinTokens = 2048;    // tokens per CTA of the second launch
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightsParams {
@@ -44,7 +47,7 @@ struct WeightsParams {
   uint16_t *v_cache_w;
   int32_t *chunk_prefix;  // [num_seqs + 1]: first chunk of each sequence
   float *part_ml;         // [chunks, Hkv, G, 2]   (max in log2 units, sum)
-  float *part_o;          // [chunks, Hkv, G, D]
+  float *part_o;          // [chunks, Hkv, D, G]
   float *logits;          // [chunks, Hkv, chunk, G]
   int32_t *status;
   int64_t num_blocks;
@@ -56,17 +59,6 @@ struct WeightsParams {
   int max_blocks_per_seq;
   float qscale;  // scale * log2(e)
 };
-
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 
 // Visible tokens of a sequence: context_lens, at most what its table holds.
 __device__ __forceinline__ int visible(const WeightsParams &p, int s) {
@@ -80,7 +72,7 @@ __device__ __forceinline__ int visible(const WeightsParams &p, int s) {
 __device__ int scan_chunks(const WeightsParams &p, int *prefix, int *warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
-  const int per = (S + kThreads - 1) / kThreads;
+  const int per = (S + blockDim.x - 1) / blockDim.x;
   const int begin = min(tid * per, S), end = min(begin + per, S);
   int local = 0;
   for (int s = begin; s < end; ++s) local += (visible(p, s) + p.chunk - 1) / p.chunk;
@@ -93,7 +85,7 @@ __device__ int scan_chunks(const WeightsParams &p, int *prefix, int *warp_sums) 
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   int run = incl - local, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
     if (w < warp) run += warp_sums[w];
     total += warp_sums[w];
   }
@@ -117,169 +109,468 @@ __device__ __forceinline__ int seq_of(const int *prefix, int S, int c) {
   return lo;
 }
 
+// 16-byte asynchronous copy; zeros instead when !take.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool take, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(take ? 16 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// d (16 x 8, fp32) += a (16 x 16, bf16) * b (16 x 8, bf16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Shared memory of one warp: a ring of tiles (kRows tokens of K, then of V),
+// and as many places for the query rows of the items in flight.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsParams p) {
-  extern __shared__ int prefix[];  // [S + 1]
-  __shared__ float qs[G][D];
-  __shared__ float lg[kMaxChunk][G];
-  __shared__ int64_t slots[kMaxChunk];
-  __shared__ float stat[2][G];
-  __shared__ int warp_sums[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int S = p.num_seqs, Hkv = p.num_kv_heads, C = p.chunk;
+struct WarpSmem {
+  static constexpr int kRows = 2048 / D;          // 16 tokens of 128 dims, 32 of 64
+  static constexpr int kHalf = kRows * D * 2;     // 4 KiB of K or V
+  static constexpr int kQ = G * D * 2;
+  static constexpr int bytes = kStages * (2 * kHalf + kQ);
+};
+
+// Byte offset of 16-byte column c of row r in a tile of rows of D values: the
+// columns of eight consecutive rows are spread over the banks.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
+}
+
+// First launch.  A warp is by itself: it takes items (a chunk of a sequence's
+// tokens, one kv head) and streams their K and V through its own ring with
+// cp.async, up to two tiles ahead and across items, so nothing in the loop
+// waits for another warp.  Per 16 tokens the products are m16n8k16: S = K q^T
+// (tokens x dims x heads; the G heads of the group are the columns, of 8) and
+// O^T += V^T P (dims x tokens x heads), in which a lane's two heads are the
+// same in S, in P and in O, so maximum and rescaling need no exchange of O.
+// Decode moves D * 4 bytes for 4 G D operations, far below what these products
+// run at: the loop is there to keep loads in flight (128 KB per SM).
+template <int D, int G>
+__global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(const WeightsParams p) {
+  using W = WarpSmem<D, G>;
+  constexpr int kCols = D / 8;              // 16-byte columns per row
+  constexpr int kRowsPer = 32 / kCols;      // rows per warp-wide copy
+  constexpr int kSlices = W::kRows / 16;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ int warp_sums[kWarpsMost];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
+  uint8_t *mine = smem_raw + warp * W::bytes;
+  int *prefix = reinterpret_cast<int *>(smem_raw + warps * W::bytes);  // [S + 1]
+  const uint32_t tiles = smem_u32(mine);
+  const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
+  const int S = p.num_seqs, Hkv = p.num_kv_heads, C = p.chunk, shift = p.block_shift;
+
   const int total = scan_chunks(p, prefix, warp_sums);
+  const bool over = total > p.max_chunks;
   if (blockIdx.x == 0) {
-    for (int s = tid; s < S; s += kThreads) {
+    for (int s = threadIdx.x; s < S; s += blockDim.x) {
       const int L = p.context_lens[s];
       if (L <= 0 || L != visible(p, s)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
     }
-    const bool over = total > p.max_chunks;
-    if (over && tid == 0) flag_status(p.status, PKV_DEV_WORKSPACE);
-    for (int s = tid; s <= S; s += kThreads) p.chunk_prefix[s] = over ? 0 : prefix[s];
+    if (over && threadIdx.x == 0) flag_status(p.status, PKV_DEV_WORKSPACE);
+    for (int s = threadIdx.x; s <= S; s += blockDim.x) p.chunk_prefix[s] = over ? 0 : prefix[s];
   }
-  if (total > p.max_chunks) return;
-  for (int64_t item = blockIdx.x; item < (int64_t)total * Hkv; item += gridDim.x) {
-    const int c = (int)(item / Hkv), j = (int)(item - (int64_t)c * Hkv);
-    const int s = seq_of(prefix, S, c);
-    const int first = (c - prefix[s]) * C;
-    const int L = visible(p, s);
-    const int valid = min(C, L - first);
-    const int newest = p.new_k != nullptr && L == p.context_lens[s] ? L - 1 - first : -1;
-    const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-    __syncthreads();
-    for (int e = tid; e < G * D; e += kThreads)
-      qs[e / D][e % D] = bf16lo(p.q[((int64_t)s * Hkv + j) * G * D + e]) * p.qscale;
-    for (int t = tid; t < valid; t += kThreads) {
-      const int i = first + t;
-      int blk = bt[i >> p.block_shift];
-      if (blk < 0 || blk >= p.num_blocks) {
-        flag_status(p.status, PKV_DEV_BAD_BLOCK);
-        blk = 0;
-      }
-      slots[t] = ((int64_t)blk << p.block_shift) + (i & ((1 << p.block_shift) - 1));
-    }
-    __syncthreads();
-    for (int t = tid; t < valid; t += kThreads) {
-      const uint16_t *k = t == newest ? p.new_k + ((int64_t)s * Hkv + j) * D
-                                      : p.k_cache + (slots[t] * Hkv + j) * D;
-      float acc[G];
-      for (int g = 0; g < G; ++g) acc[g] = 0.f;
-      for (int d = 0; d < D; ++d)
-        for (int g = 0; g < G; ++g) acc[g] = fmaf(bf16lo(k[d]), qs[g][d], acc[g]);
-      for (int g = 0; g < G; ++g) {
-        lg[t][g] = acc[g];
-        p.logits[(item * C + t) * G + g] = acc[g];
-      }
-    }
-    __syncthreads();
-    for (int g = warp; g < G; g += kWarps) {
-      float m = -INFINITY;
-      for (int t = lane; t < valid; t += 32) m = fmaxf(m, lg[t][g]);
-      m = warp_max(m);
-      float l = 0.f;
-      for (int t = lane; t < valid; t += 32) {
-        const float e = exp2f(lg[t][g] - m);
-        lg[t][g] = e;
-        l += e;
-      }
-      l = warp_sum(l);
-      if (lane == 0) {
-        stat[0][g] = m;
-        stat[1][g] = l;
-      }
-    }
-    __syncthreads();
-    for (int e = tid; e < G * D; e += kThreads) {
-      const int g = e / D, d = e - g * D;
-      float acc = 0.f;
-      for (int t = 0; t < valid; ++t) {
-        const uint16_t *v = t == newest ? p.new_v + ((int64_t)s * Hkv + j) * D
-                                        : p.v_cache + (slots[t] * Hkv + j) * D;
-        acc = fmaf(lg[t][g], bf16lo(v[d]), acc);
-      }
-      p.part_o[item * G * D + e] = acc;
-    }
-    if (tid < G) {
-      p.part_ml[(item * G + tid) * 2] = stat[0][tid];
-      p.part_ml[(item * G + tid) * 2 + 1] = stat[1][tid];
-    }
-    if (newest >= 0 && newest < valid) {
-      const int64_t slot = p.new_slots[s];
-      if (slot >= 0 && slot < p.num_blocks << p.block_shift) {
-        for (int d = tid; d < D; d += kThreads) {
-          p.k_cache_w[(slot * Hkv + j) * D + d] = p.new_k[((int64_t)s * Hkv + j) * D + d];
-          p.v_cache_w[(slot * Hkv + j) * D + d] = p.new_v[((int64_t)s * Hkv + j) * D + d];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (over) return;
+
+  const int64_t items = (int64_t)total * Hkv;
+  const int64_t stride = (int64_t)gridDim.x * warps;
+  const uint64_t policy = l2_policy_evict_first();
+
+  // Where an item's tokens are; lane l holds the l-th block id of the chunk.
+  struct Item {
+    int64_t id;
+    int s, j, first, valid, newest, blk;
+  };
+  auto locate = [&](int64_t id, Item &x) {
+    x.id = id;
+    if (id >= items) return;
+    const int c = (int)(id / Hkv);
+    x.j = (int)(id - (int64_t)c * Hkv);
+    x.s = seq_of(prefix, S, c);
+    x.first = (c - prefix[x.s]) * C;
+    const int L = visible(p, x.s);
+    x.valid = min(C, L - x.first);
+    // (a chunk's newest token, as an index into the chunk; only with a store to do)
+    x.newest = p.new_k != nullptr && L == p.context_lens[x.s] ? L - 1 - x.first : -1;
+  };
+  auto fetch_blocks = [&](Item &x) {
+    x.blk = 0;
+    if (x.id < items && lane * 64 < C) {
+      const int i = x.first + (lane << 6);  // (64 tokens are always in one block)
+      if (lane * 64 < x.valid) {
+        x.blk = p.block_tables[(int64_t)x.s * p.max_blocks_per_seq + (i >> shift)];
+        if (x.blk < 0 || x.blk >= p.num_blocks) {
+          flag_status(p.status, PKV_DEV_BAD_BLOCK);
+          x.blk = 0;
         }
-      } else if (slot != -1 && tid == 0) {
+      }
+    }
+  };
+
+  // The loading side, ahead of the consuming side by up to two tiles.
+  Item in, in_next;
+  int in_tok = 0, in_slot = 0, in_q = 0;
+  locate((int64_t)blockIdx.x * warps + warp, in);
+  fetch_blocks(in);
+  locate(in.id + stride, in_next);
+  fetch_blocks(in_next);
+  const int col = lane % kCols, row0 = lane / kCols;
+  auto issue = [&]() {
+    if (in.id < items) {
+      if (in_tok == 0) {
+        const uint16_t *q = p.q + ((int64_t)in.s * Hkv + in.j) * G * D;
+        for (int x = lane; x < G * kCols; x += 32)
+          copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
+        in_q = in_q + 1 == kStages ? 0 : in_q + 1;
+      }
+      const int blk = __shfl_sync(0xffffffffu, in.blk, in_tok >> 6);
+      const int64_t slot = ((int64_t)blk << shift) + ((in.first + in_tok) & ((1 << shift) - 1));
+      const int64_t at = ((slot + row0) * Hkv + in.j) * D + col * 8;
+      const int64_t step = (int64_t)kRowsPer * Hkv * D;
+      const int64_t fresh = ((int64_t)in.s * Hkv + in.j) * D + col * 8;
+      const uint32_t dst = tiles + in_slot * 2 * W::kHalf;
+#pragma unroll
+      for (int i = 0; i < W::kRows / kRowsPer; ++i) {
+        const int t = in_tok + row0 + i * kRowsPer;
+        const uint32_t to = dst + tile_at<D>(row0 + i * kRowsPer, col);
+        const bool is_new = t == in.newest;
+        copy16(to, is_new ? p.new_k + fresh : p.k_cache + at + i * step, t < in.valid, policy);
+        copy16(to + W::kHalf, is_new ? p.new_v + fresh : p.v_cache + at + i * step, t < in.valid, policy);
+      }
+      in_tok += W::kRows;
+      if (in_tok >= in.valid) {
+        in_tok = 0;
+        in = in_next;
+        locate(in.id + stride, in_next);
+        fetch_blocks(in_next);
+      }
+      in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue();
+
+  // The consuming side.
+  const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
+  const bool owner = h0 < G;      // (of the 8 columns only G are heads)
+  int slot = 0, qslot = 0;
+  Item x;
+  for (int64_t id = (int64_t)blockIdx.x * warps + warp; id < items; id += stride) {
+    locate(id, x);
+    uint32_t qf[D / 16][2];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float *lg = p.logits + id * C * G;
+    for (int tok = 0; tok < x.valid; tok += W::kRows) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // every lane's copies are in, and the slot filled next is read out
+      issue();
+      if (tok == 0) {
+        // q as the second operand: lane (head, dim pair) per 8 dims.  Rows past
+        // G repeat the last one (their columns are not used).
+        const uint32_t qa = qslots + qslot * W::kQ;
+        const int r = min(lane & 7, G - 1);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t f[4];
+          ldmatrix4(f, qa + tile_at<D>(r, i * 4 + (lane >> 3)));
+          qf[2 * i][0] = f[0];
+          qf[2 * i][1] = f[1];
+          qf[2 * i + 1][0] = f[2];
+          qf[2 * i + 1][1] = f[3];
+        }
+        qslot = qslot + 1 == kStages ? 0 : qslot + 1;
+      }
+      const uint32_t ka = tiles + slot * 2 * W::kHalf, va = ka + W::kHalf;
+#pragma unroll
+      for (int sl = 0; sl < kSlices; ++sl) {
+        // S: rows are tokens (lane / 4 and + 8), columns the lane's two heads.
+        float s_even[4] = {0.f, 0.f, 0.f, 0.f}, s_odd[4] = {0.f, 0.f, 0.f, 0.f};
+        const int r = sl * 16 + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t a[4];
+          ldmatrix4(a, ka + tile_at<D>(r, 2 * i + (lane >> 4)));
+          if (i & 1) mma16816(s_odd, a, qf[i][0], qf[i][1]);
+          else mma16816(s_even, a, qf[i][0], qf[i][1]);
+        }
+        const int t0 = tok + sl * 16 + (lane >> 2), t1 = t0 + 8;
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = (s_even[i] + s_odd[i]) * p.qscale;
+        if (owner) {
+          if (G == 1) {
+            if (t0 < x.valid) lg[t0] = z[0];
+            if (t1 < x.valid) lg[t1] = z[2];
+          } else {
+            if (t0 < x.valid) *reinterpret_cast<float2 *>(lg + t0 * G + h0) = make_float2(z[0], z[1]);
+            if (t1 < x.valid) *reinterpret_cast<float2 *>(lg + t1 * G + h0) = make_float2(z[2], z[3]);
+          }
+        }
+        if (t0 >= x.valid) z[0] = z[1] = -INFINITY;
+        if (t1 >= x.valid) z[2] = z[3] = -INFINITY;
+        float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, k));
+          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, k));
+        }
+        n0 = fmaxf(n0, m0);
+        n1 = fmaxf(n1, m1);
+        // (a maximum of -inf: every weight so far is zero, whatever the reference)
+        const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+        const float a0 = fast_exp2(m0 - r0), a1 = fast_exp2(m1 - r1);
+        m0 = n0;
+        m1 = n1;
+        const float p0 = fast_exp2(z[0] - r0), p1 = fast_exp2(z[1] - r1);
+        const float p2 = fast_exp2(z[2] - r0), p3 = fast_exp2(z[3] - r1);
+        l0 = fmaf(l0, a0, p0 + p2);
+        l1 = fmaf(l1, a1, p1 + p3);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a1;
+          o[i][2] *= a0;
+          o[i][3] *= a1;
+        }
+        // P as the second operand of the next product: rounded to bf16 there,
+        // as the tensor cores take it; the sums keep the fp32 weights.
+        const uint32_t b0 = transpose8x8(pack_bf16x2(p0, p1));
+        const uint32_t b1 = transpose8x8(pack_bf16x2(p2, p3));
+        // V^T: two 8-token halves by two 8-dim columns, transposed on the way.
+        const int vr = sl * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t a[4];
+          ldmatrix4_trans(a, va + tile_at<D>(vr, 2 * i + ((lane >> 3) & 1)));
+          mma16816(o[i], a, b0, b1);
+        }
+      }
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, k);
+    }
+    if (owner) {
+      float *po = p.part_o + id * G * D;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int d = i * 16 + (lane >> 2);
+        if (G == 1) {
+          po[d] = o[i][0];
+          po[d + 8] = o[i][2];
+        } else {
+          *reinterpret_cast<float2 *>(po + d * G + h0) = make_float2(o[i][0], o[i][1]);
+          *reinterpret_cast<float2 *>(po + (d + 8) * G + h0) = make_float2(o[i][2], o[i][3]);
+        }
+      }
+      if (lane < 4) {
+        float *ml = p.part_ml + (id * G + h0) * 2;
+        ml[0] = m0;
+        ml[1] = l0;
+        if (G > 1) {
+          ml[2] = m1;
+          ml[3] = l1;
+        }
+      }
+    }
+    // The chunk with the newest token stores it (no item of the call reads its slot).
+    if (x.newest >= 0 && x.newest < x.valid) {
+      const int64_t to = p.new_slots[x.s];
+      if (to >= 0 && to < p.num_blocks << shift) {
+        if (lane < kCols) {
+          const int64_t from = ((int64_t)x.s * Hkv + x.j) * kCols + lane;
+          const int64_t at = (to * Hkv + x.j) * kCols + lane;
+          reinterpret_cast<uint4 *>(p.k_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_k)[from];
+          reinterpret_cast<uint4 *>(p.v_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_v)[from];
+        }
+      } else if (to != -1 && lane == 0) {
         flag_status(p.status, PKV_DEV_BAD_SLOT);
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Second launch: one CTA per (sequence, kv head, kJoinTokens tokens).  It joins
+// the maxima and sums of all of its sequence's chunks, then adds the weights of
+// its own tokens and writes its share of the output.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) decode_weights_join_kernel(const WeightsParams p) {
-  __shared__ float stat[2][G];
+__global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const WeightsParams p) {
+  constexpr int kJoinWarps = kJoinThreads / 32;
+  __shared__ float red[2][kJoinWarps][G];
+  __shared__ float stat[2][G];   // maximum, 1 / sum
+  __shared__ float4 acc_s[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int S = p.num_seqs, Hkv = p.num_kv_heads, C = p.chunk;
+  const int Hkv = p.num_kv_heads, C = p.chunk, shift = p.block_shift;
+  const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
+  const int L = visible(p, s);  // an input of the call: the first launch does not write it
+  const int begin = blockIdx.y * kJoinTokens;
+  if (begin >= L) return;
+  const int newest = p.context_lens[s] - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = p.chunk_prefix[S];
-  for (int64_t item = blockIdx.x; item < (int64_t)total * Hkv; item += gridDim.x) {
-    const int c = (int)(item / Hkv), j = (int)(item - (int64_t)c * Hkv);
-    const int s = seq_of(p.chunk_prefix, S, c);
-    const int c0 = p.chunk_prefix[s], n = p.chunk_prefix[s + 1] - c0;
-    const int first = (c - c0) * C;
-    const int L = visible(p, s);
-    const int valid = min(C, L - first);
-    const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-    __syncthreads();
-    for (int g = warp; g < G; g += kWarps) {
-      float m = -INFINITY, l = 0.f;
-      for (int r = lane; r < n; r += 32)
-        m = fmaxf(m, p.part_ml[(((int64_t)(c0 + r) * Hkv + j) * G + g) * 2]);
-      m = warp_max(m);
-      for (int r = lane; r < n; r += 32) {
-        const float *ml = p.part_ml + (((int64_t)(c0 + r) * Hkv + j) * G + g) * 2;
-        l += exp2f(ml[0] - m) * ml[1];
-      }
-      l = warp_sum(l);
-      if (lane == 0) {
-        stat[0][g] = m;
-        stat[1][g] = 1.f / l;
-      }
+  if (p.chunk_prefix[p.num_seqs] == 0) return;  // the call was refused for want of workspace
+  const int c0 = p.chunk_prefix[s];
+  const int n = (L + C - 1) / C;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + ((int64_t)c0 * Hkv + j) * G;
+  const int64_t ml_step = (int64_t)Hkv * G;
+  // Thread (chunk, head): running maximum and sum over its chunks.
+  {
+    const int g = tid % G;
+    float m = -INFINITY, l = 0.f;
+    for (int r = tid / G; r < n; r += kJoinThreads / G) {
+      const float2 x = __ldcg(ml + r * ml_step + g);
+      const float mn = fmaxf(m, x.x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - ref) + x.y * fast_exp2(x.x - ref);
+      m = mn;
+    }
+#pragma unroll
+    for (int k = G; k < 32; k <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, k);
+      const float l2 = __shfl_xor_sync(0xffffffffu, l, k);
+      const float mn = fmaxf(m, m2);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
+      m = mn;
+    }
+    if (lane < G) {
+      red[0][warp][lane] = m;
+      red[1][warp][lane] = l;
     }
     __syncthreads();
-    if (c == c0) {
-      for (int e = tid; e < G * D; e += kThreads) {
-        const int g = e / D;
-        float acc = 0.f;
-        for (int r = 0; r < n; ++r) {
-          const int64_t it = (int64_t)(c0 + r) * Hkv + j;
-          acc = fmaf(exp2f(p.part_ml[(it * G + g) * 2] - stat[0][g]), p.part_o[it * G * D + e], acc);
-        }
-        p.out[((int64_t)s * Hkv + j) * G * D + e] = (uint16_t)pack_bf16x2(acc * stat[1][g], 0.f);
-      }
+    if (tid < G) {
+      m = -INFINITY;
+      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[0][w][tid]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+      for (int w = 0; w < kJoinWarps; ++w) l += red[1][w][tid] * fast_exp2(red[0][w][tid] - ref);
+      stat[0][tid] = m;
+      stat[1][tid] = 1.f / l;
     }
-    for (int t = tid; t < valid; t += kThreads) {
-      const int i = first + t;
-      const int blk = bt[i >> p.block_shift];
-      if (blk < 0 || blk >= p.num_blocks) continue;
-      float a = 0.f;
-      for (int g = 0; g < G; ++g)
-        a = fmaf(exp2f(p.logits[(item * C + t) * G + g] - stat[0][g]), stat[1][g], a);
-      float *w = p.key_weights + ((((int64_t)blk * Hkv + j) << p.block_shift) +
-                                  (i & ((1 << p.block_shift) - 1)));
-      if (i == p.context_lens[s] - 1) *w = a;
+    __syncthreads();
+  }
+  // Weights: a thread takes a token.
+  float M[G], inv[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    M[g] = stat[0][g];
+    inv[g] = stat[1][g];
+  }
+  const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+  const int end = min(L, begin + kJoinTokens);
+#pragma unroll 2
+  for (int i = begin + tid; i < end; i += kJoinThreads) {
+    const int c = i / C;
+    const float *lg = p.logits + (((int64_t)(c0 + c) * Hkv + j) * C + (i - c * C)) * G;
+    float z[G];
+    if constexpr (G >= 4) {
+#pragma unroll
+      for (int g = 0; g < G; g += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
+        z[g] = y.x;
+        z[g + 1] = y.y;
+        z[g + 2] = y.z;
+        z[g + 3] = y.w;
+      }
+    } else if constexpr (G == 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
+      z[0] = y.x;
+      z[1] = y.y;
+    } else {
+      z[0] = __ldcg(lg);
+    }
+    const int blk = bt[i >> shift];
+    float a = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[g] - M[g]), inv[g], a);
+    if (blk >= 0 && blk < p.num_blocks) {
+      float *w = p.key_weights + ((((int64_t)blk * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
+      if (i == newest) *w = a;
       else atomicAdd(w, a);
+    }
+  }
+  // Output: the sequence's CTAs share the D * G values in runs of four; the
+  // threads of a CTA share the chunks.
+  constexpr int kQuads = D * G / 4;
+  const int parts = (L + kJoinTokens - 1) / kJoinTokens;
+  const int per = (kQuads + parts - 1) / parts;
+  const int q0 = min((int)blockIdx.y * per, kQuads), q1 = min(q0 + per, kQuads);
+  const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + ((int64_t)c0 * Hkv + j) * kQuads;
+  for (int qb = q0; qb < q1; qb += kJoinThreads) {
+    const int width = min(q1 - qb, kJoinThreads);
+    const int lanes = kJoinThreads / width;  // threads per quad
+    const int q = qb + tid % width, r0 = tid / width;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int e = q * 4;  // value e is dim e / G of head e % G
+    if (r0 < lanes) {
+#pragma unroll 4
+      for (int r = r0; r < n; r += lanes) {
+        const float4 y = __ldcg(po + (int64_t)r * Hkv * kQuads + q);
+        const float *mr = reinterpret_cast<const float *>(ml + r * ml_step);
+        acc.x = fmaf(fast_exp2(__ldcg(mr + 2 * (e % G)) - M[e % G]), y.x, acc.x);
+        acc.y = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 1) % G)) - M[(e + 1) % G]), y.y, acc.y);
+        acc.z = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 2) % G)) - M[(e + 2) % G]), y.z, acc.z);
+        acc.w = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 3) % G)) - M[(e + 3) % G]), y.w, acc.w);
+      }
+    }
+    __syncthreads();
+    acc_s[tid] = acc;
+    __syncthreads();
+    if (tid < width) {
+      for (int k = 1; k < lanes; ++k) {
+        const float4 y = acc_s[k * width + tid];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+      uint16_t *out = p.out + ((int64_t)s * Hkv + j) * G * D;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int g = (e + k) % G, d = (e + k) / G;
+        out[g * D + d] = (uint16_t)pack_bf16x2(v[k] * stat[1][g], 0.f);
+      }
     }
   }
 }
 
-// Tokens per item: the largest chunk that still leaves some 2000 items, for
+// Tokens per item: the largest chunk that still leaves some 4000 items (a GPU runs 1216 warps), for
 // which a batch's context lengths count as long as its block bound allows.
 int chunk_for(int64_t max_total_blocks, int block_size, int num_kv_heads) {
   int c = kMaxChunk;
-  while (c > 64 && max_total_blocks * block_size / c * num_kv_heads < 2048) c >>= 1;
+  while (c > 64 && max_total_blocks * block_size / c * num_kv_heads < 4096) c >>= 1;
   return c;
 }
 
@@ -303,21 +594,37 @@ struct Workspace {
 
 template <int D, int G>
 pkv_status launch(const WeightsParams &prm, cudaStream_t stream) {
-  const int smem = (prm.num_seqs + 1) * 4;
-  int ctas = 0;
-  if (!kernel_smem_setup((const void *)decode_weights_kernel<D, G>, kThreads, smem, &ctas))
-    return PKV_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
-  int64_t items = (int64_t)prm.num_seqs * (((int64_t)prm.max_blocks_per_seq << prm.block_shift) + prm.chunk - 1) / prm.chunk;
+  const int prefix = (prm.num_seqs + 1) * 4;
+  int warps = (kMaxDynamicSmem - 1024 - prefix) / WarpSmem<D, G>::bytes;
+  if (warps > kWarpsMost) warps = kWarpsMost;
+  static_assert((kMaxDynamicSmem - 1024 - (kMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
+  const int smem = warps * WarpSmem<D, G>::bytes + prefix;
+  int ctas = 0;
+  if (!kernel_smem_setup((const void *)decode_weights_kernel<D, G>, warps * 32, smem, &ctas))
+    return PKV_ERR_CUDA;
+  const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
+  int64_t items = (int64_t)prm.num_seqs * ((room + prm.chunk - 1) / prm.chunk);
   if (items > prm.max_chunks) items = prm.max_chunks;
   items *= prm.num_kv_heads;
-  if (items < 1) items = 1;
-  int64_t grid = (int64_t)sms * ctas;
-  if (grid > items) grid = items;
-  decode_weights_kernel<D, G><<<(unsigned)grid, kThreads, smem, stream>>>(prm);
+  int64_t grid = (items + warps - 1) / warps;
+  if (grid > sms) grid = sms;
+  if (grid < 1) grid = 1;
+  decode_weights_kernel<D, G><<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  decode_weights_join_kernel<D, G><<<(unsigned)grid, kThreads, 0, stream>>>(prm);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(prm.num_seqs * prm.num_kv_heads),
+                     (unsigned)((room + kJoinTokens - 1) / kJoinTokens));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_weights_join_kernel<D, G>, prm) != cudaSuccess)
+    return PKV_ERR_CUDA;
   return launch_status();
 }
 
@@ -361,6 +668,10 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
   if (block_size != 64 && block_size != 128 && block_size != 256 && block_size != 512)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
+  // (the second launch's grid: sequences and heads by parts of kJoinTokens)
+  if ((int64_t)num_seqs * num_kv_heads > 0x7FFFFFFFLL ||
+      (int64_t)max_blocks_per_seq * block_size > (int64_t)65535 * kJoinTokens)
+    return PKV_ERR_UNSUPPORTED;
   if (!isfinite(scale)) return PKV_ERR_INVALID_ARG;  // NaN or infinite
   if (num_seqs == 0) return PKV_OK;
   if (!out || !key_weights || !q || !k_cache || !v_cache || !block_tables || !context_lens)
