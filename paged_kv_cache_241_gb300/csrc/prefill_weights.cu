@@ -13,15 +13,21 @@
 //  1. Rows: S = Q K^T with the rows in the lanes of tensor memory (M = 128 rows:
 //     128 / G queries of the G heads that share the keys; N = 128 keys).  A
 //     thread owns a row (for half of a tile's keys) and keeps its running maximum
-//     and sum over the unit's key tiles.  Long rows are split over several units.
+//     and sum over the row's key tiles.
 //  2. Keys: S^T = K Q^T with the keys in the lanes, so that summing a key's
-//     weights over the rows is a sum inside one thread.  One unit holds all row
-//     tiles of its keys: no sum is shared between CTAs and no order varies.
-// Both are the same persistent kernel: warp 0 loads tiles (TMA, 128-byte
+//     weights over the rows is a sum inside one thread.
+// A step is one 128 x 128 product of a key tile and a row tile that sees any of
+// it.  All steps of the call, in the order (sequence, kv head, row tile, key
+// tile) or, second pass, (sequence, kv head, key tile, row tile), are cut into
+// one run of equal length per CTA, whatever the lengths of the sequences.  A row
+// tile (key tile) whose steps fall to several CTAs is joined by the last of them
+// to finish (a counter; nothing waits), from the parts in their order, so the
+// result does not depend on which one that is.
+// Both passes are the same persistent kernel: warp 0 loads tiles (TMA, 128-byte
 // swizzle, through the block table), warp 1 issues tcgen05.mma into four
-// 128-column buffers of tensor memory, warps 2 and 3 prepare the rows'
+// 128-column buffers of tensor memory, warps 2 and 3 fetch the rows'
 // denominators (second pass), warps 4-11 exponentiate and sum.  Loads, products
-// and exponentials of different tiles overlap, across units too.
+// and exponentials of different steps overlap.
 #include <math.h>
 
 #include "host_common.h"
@@ -34,10 +40,8 @@ constexpr int kTile = 128;       // rows and keys per tile
 constexpr int kThreads = 384;
 constexpr int kEpilogue = 256;   // threads of warps 4-11
 constexpr int kBufs = 4;         // S buffers of 128 columns: all of tensor memory
-constexpr int kQSlots = 2;
-constexpr int kStatSlots = 3;    // row statistics (second pass)
-constexpr int kMaxSplitTiles = 8;
-constexpr int kUnitsWanted = 304;  // two units per SM, where the work allows
+constexpr int kQSlots = 2;       // row tiles, with their denominators
+constexpr int kMaxCtas = 512;    // places for cut tiles in the workspace (CTAs of a grid at most)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -47,13 +51,13 @@ struct Layout {
   static constexpr int q = 0;
   static constexpr int k = q + kQSlots * kTileBytes;
   static constexpr int bars = k + kKSlots * kTileBytes;
-  // q_full/q_empty[Q], k_full/k_empty[K], s_full/s_empty[B], st_full/st_empty[T], drain
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kKSlots + 2 * kBufs + 2 * kStatSlots + 1;
-  static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [T][128] -log2 denominators
-  static constexpr int qpos = stat + kStatSlots * kTile * 4;     // [T][128] last visible key, -1: no row
-  static constexpr int red = qpos + kStatSlots * kTile * 4;      // [2][2][128] exchange between halves
-  static constexpr int misc = red + 4 * kTile * 4;               // tensor memory address, abort flag
-  static constexpr int total = misc + 16;
+  // q_full/q_empty[Q], k_full/k_empty[K], s_full/s_empty[B], st_full/st_empty[Q], drain
+  static constexpr int kNumBars = 4 * kQSlots + 2 * kKSlots + 2 * kBufs + 1;
+  static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [Q][128] -log2 denominators
+  static constexpr int qpos = stat + kQSlots * kTile * 4;        // [Q][128] last visible key, -1: no row
+  static constexpr int red = qpos + kQSlots * kTile * 4;         // [2][2][128] exchange between halves
+  static constexpr int misc = red + 4 * kTile * 4;  // tensor memory address, abort, last, start, scan
+  static constexpr int total = misc + 256;
   // One CTA per SM (it takes all of tensor memory): more than half of an SM's
   // shared memory, so that a second one never waits for tensor memory.
   static_assert(total + 1024 <= 232448 && total > 114 * 1024, "shared memory");
@@ -64,11 +68,12 @@ struct PromptParams {
   const int32_t *block_tables;
   const int32_t *cu_q;
   const int32_t *cu_k;
-  float2 *part;  // [splits, stat rows, Hq]: (maximum in log2 units, sum) of a row over a split
+  float *neg_lse;           // [stat rows, Hq]: -log2 of a row's softmax denominator
+  float2 *parts;            // [CTA][2][128]: parts of tiles cut between CTAs
+  unsigned int *tickets;    // [2][kMaxCtas]: parts of a cut tile that are done, by its first CTA
   int32_t *status;
   int64_t num_blocks;
   int64_t total_q;
-  int64_t stat_rows;
   int num_seqs;
   int num_q_heads;
   int num_kv_heads;
@@ -80,91 +85,186 @@ struct PromptParams {
   int window;
   int rows;          // min(window, max_seqlen_q): counted queries per sequence at most
   int by_query;      // a row's statistics are filed under its query (else sequence and rank)
-  int row_tiles;     // row tiles of a sequence, at most
-  int splits;        // splits of a row's keys, at most
-  int split_tiles;   // key tiles per split (first pass)
-  int groups;        // groups of key tiles of a sequence, at most (second pass)
-  int group_tiles;   // key tiles per group
-  int64_t units;
   float qscale;
 };
 
-// One sequence of the call; false when it has no queries or its lengths do not
-// fit (then flagged, if told to).
+// One sequence of the call: its last R queries count, from position base on.
 struct Seq {
-  int q_begin, n, c, len_k, R;
+  int q_first;  // the first counted query's row of q
+  int R, c, len_k, base;
+  int nrt, nkt;  // row tiles, key tiles
 };
+
+// False when the sequence has no queries or its lengths do not fit (then
+// flagged, if told to).
 __device__ __forceinline__ bool seq_at(const PromptParams &p, int s, Seq &q, bool tell) {
-  q.q_begin = p.cu_q[s];
-  q.n = p.cu_q[s + 1] - q.q_begin;
+  const int q_begin = p.cu_q[s];
+  const int n = p.cu_q[s + 1] - q_begin;
   q.len_k = p.cu_k[s + 1] - p.cu_k[s];
-  q.c = q.len_k - q.n;
-  q.R = min(q.n, p.window);
-  if (q.n == 0) return false;
-  if (q.n < 0 || q.n > p.max_seqlen_q || q.c < 0 || q.q_begin < 0 ||
+  q.c = q.len_k - n;
+  if (n == 0) return false;
+  if (n < 0 || n > p.max_seqlen_q || q.c < 0 || q_begin < 0 ||
       q.len_k > ((int64_t)p.max_blocks_per_seq << p.block_shift) ||
-      (int64_t)q.q_begin + q.n > p.total_q) {
+      (int64_t)q_begin + n > p.total_q) {
     if (tell) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
     return false;
   }
+  q.R = min(n, p.window);
+  q.q_first = q_begin + n - q.R;
+  q.base = q.len_k - q.R;
+  const int tq = kTile >> p.group_shift;
+  q.nrt = (q.R + tq - 1) / tq;
+  q.nkt = (q.len_k + kTile - 1) / kTile;
   return true;
 }
 
-// A unit of work: row tiles [rt0, rt1) against key tiles [kt0, kt1) of kv head
-// j of a sequence; of those, a key tile kt takes part with row tiles from
-// first_rt(kt) on (the ones that see any of it).
-struct Unit {
-  Seq q;
-  int s, j, rt0, rt1, kt0, kt1, tq;
-  // Queries of a row tile, counted from the first that counts; the last one's position.
-  __device__ __forceinline__ int last_pos(int rt) const {
-    return q.c + q.n - q.R + min((rt + 1) * tq, q.R) - 1;
+// Key tiles that row tile rt sees: up to its last query's position.
+__device__ __forceinline__ int tiles_seen(const PromptParams &p, const Seq &q, int rt) {
+  return (q.base + min((rt + 1) * (kTile >> p.group_shift), q.R) - 1) / kTile + 1;
+}
+// The first row tile that sees any of key tile kt.
+__device__ __forceinline__ int first_rt(const PromptParams &p, const Seq &q, int kt) {
+  const int over = kt * kTile - q.base;  // queries before this one see none of it
+  return over <= 0 ? 0 : over / (kTile >> p.group_shift);
+}
+// Steps of the first m row tiles.  Row tile rt + G starts 128 positions later
+// than rt, so it sees one tile more: whole turns of G row tiles sum in closed form.
+__device__ __forceinline__ int64_t steps_of_rows(const PromptParams &p, const Seq &q, int m) {
+  int64_t extra = 0;
+  if (m == q.nrt) {  // (the last row tile can be short)
+    extra = q.nkt;
+    --m;
   }
-  __device__ __forceinline__ int first_pos(int rt) const { return q.c + q.n - q.R + rt * tq; }
-  __device__ __forceinline__ int first_rt(int kt) const {
-    const int over = kt * kTile - (q.c + q.n - q.R);  // queries before this one see none of it
-    return over <= 0 ? rt0 : max(rt0, over / tq);
+  const int G = p.group;
+  const int64_t turns = m >> p.group_shift;
+  const int rest = m & (G - 1);
+  int64_t sum = (int64_t)G * (turns * (turns - 1) / 2) + turns * rest;
+  for (int r = 0; r < G; ++r) {
+    const int64_t seen = (q.base + (r + 1) * (kTile >> p.group_shift) - 1) / kTile + 1;
+    sum += seen * (turns + (r < rest ? 1 : 0));
   }
+  return sum + extra;
+}
+// Steps of the first k key tiles (second pass): row tiles from first_rt on, which
+// grows by G with every key tile once it is past zero.
+__device__ __forceinline__ int64_t steps_of_keys(const PromptParams &p, const Seq &q, int k) {
+  const int tq = kTile >> p.group_shift;
+  const int64_t e = (q.base + tq - 1) / tq;                 // first_rt(kt) = max(0, G kt - e)
+  const int64_t k1 = min((e + p.group - 1) >> p.group_shift, (int64_t)k);
+  const int64_t n = k - k1;
+  const int64_t skipped = p.group * (k1 * n + n * (n - 1) / 2) - e * n;
+  return (int64_t)k * q.nrt - skipped;
+}
+__device__ __forceinline__ int64_t steps_of(const PromptParams &p, const Seq &q) {
+  return steps_of_rows(p, q, q.nrt);
+}
+
+// Where a CTA's run of steps starts (found once, by all threads).
+struct Start {
+  int64_t begin, end;  // steps of the call
+  int64_t run;         // steps per CTA
+  int64_t offset;      // of `begin` within its sequence
+  int s;
 };
 
-// Unit number -> unit; heads innermost, so that concurrent CTAs read the same tokens' rows.
+// A role's walk over its CTA's steps.
 template <int PASS>
-__device__ __forceinline__ bool unit_at(const PromptParams &p, int64_t idx, Unit &u) {
-  u.j = (int)(idx % p.num_kv_heads);
-  idx /= p.num_kv_heads;
-  u.tq = kTile >> p.group_shift;
-  if (PASS == 1) {
-    const int rt = (int)(idx % p.row_tiles);
-    idx /= p.row_tiles;
-    const int split = (int)(idx % p.splits);
-    u.s = (int)(idx / p.splits);
-    if (!seq_at(p, u.s, u.q, u.j == 0 && rt == 0 && split == 0)) return false;
-    if (rt * u.tq >= u.q.R) return false;
-    u.rt0 = rt;
-    u.rt1 = rt + 1;
-    u.kt0 = split * p.split_tiles;
-    u.kt1 = min(u.kt0 + p.split_tiles, u.last_pos(rt) / kTile + 1);
-  } else {
-    const int g = (int)(idx % p.groups);
-    u.s = (int)(idx / p.groups);
-    if (!seq_at(p, u.s, u.q, false)) return false;
-    u.rt0 = 0;
-    u.rt1 = (u.q.R + u.tq - 1) / u.tq;
-    u.kt0 = g * p.group_tiles;
-    u.kt1 = min(u.kt0 + p.group_tiles, (u.q.len_k + kTile - 1) / kTile);
+struct Walk {
+  const PromptParams &p;
+  int64_t pos, end, run;
+  Seq q;
+  int s, j, rt, kt, tq;
+  int loaded;     // second pass, few row tiles: those in their slots for this (sequence, head)
+  bool cut_left;  // the current tile's first steps are another CTA's
+
+  __device__ Walk(const PromptParams &prm, const Start &st) : p(prm) {
+    pos = st.begin;
+    end = st.end;
+    run = st.run;
+    s = st.s;
+    j = rt = kt = loaded = 0;
+    cut_left = false;
+    tq = kTile >> p.group_shift;
+    if (pos >= end) return;
+    seq_at(p, s, q, false);
+    const int64_t each = steps_of(p, q);
+    j = (int)(st.offset / each);
+    const int64_t at = st.offset - j * each;
+    int lo = 0, hi = (PASS == 1 ? q.nrt : q.nkt) - 1;  // the last tile that starts at or before `at`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((PASS == 1 ? steps_of_rows(p, q, mid) : steps_of_keys(p, q, mid)) <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    const int in = (int)(at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo)));
+    cut_left = in > 0;
+    if (PASS == 1) {
+      rt = lo;
+      kt = in;
+    } else {
+      kt = lo;
+      rt = first_rt(p, q, kt) + in;
+    }
   }
-  return u.kt0 < u.kt1;
-}
-
-// The statistics' row of the r-th counted query.
-__device__ __forceinline__ int64_t stat_row(const PromptParams &p, const Unit &u, int r) {
-  return p.by_query ? (int64_t)u.q.q_begin + u.q.n - u.q.R + r : (int64_t)u.s * p.rows + r;
-}
-
-// Product columns of a row tile in the second pass: its rows, to a multiple of 16.
-__device__ __forceinline__ int tile_rows(const PromptParams &p, const Unit &u, int rt) {
-  return min(u.tq, u.q.R - rt * u.tq) << p.group_shift;
-}
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  // The tile (row tile, or key tile) ends with this step.
+  __device__ __forceinline__ bool tile_done() const {
+    return PASS == 1 ? kt + 1 == tiles_seen(p, q, rt) : rt + 1 == q.nrt;
+  }
+  // This step is the last of the tile here.
+  __device__ __forceinline__ bool last_here() const { return pos + 1 == end || tile_done(); }
+  // (sequence, head) ends with this step, here.
+  __device__ __forceinline__ bool head_done() const {
+    return pos + 1 == end || (PASS == 1 ? rt + 1 == q.nrt && tile_done() : kt + 1 == q.nkt && tile_done());
+  }
+  // The first and the last CTA of the current tile.
+  __device__ __forceinline__ void ctas(int &first, int &last) const {
+    const int f = PASS == 1 ? 0 : first_rt(p, q, kt);
+    const int64_t u0 = pos - (PASS == 1 ? kt : rt - f);
+    first = (int)(u0 / run);
+    last = (int)((u0 + (PASS == 1 ? tiles_seen(p, q, rt) : q.nrt - f) - 1) / run);
+  }
+  // Second pass: so few row tiles that they stay in their slots for the whole
+  // (sequence, head), else each step loads its own.
+  __device__ __forceinline__ bool keeps() const { return PASS == 2 && q.nrt <= kQSlots; }
+  __device__ __forceinline__ void next() {
+    const bool done = tile_done(), head = head_done();
+    ++pos;
+    if (!more()) return;
+    if (!done) {
+      if (PASS == 1) ++kt;
+      else ++rt;
+      return;
+    }
+    cut_left = false;
+    if (!head) {
+      if (PASS == 1) {
+        ++rt;
+        kt = 0;
+      } else {
+        ++kt;
+        rt = first_rt(p, q, kt);
+      }
+      return;
+    }
+    loaded = rt = kt = 0;
+    if (++j < p.num_kv_heads) return;  // (first_rt(0) is 0)
+    j = 0;
+    do ++s; while (!seq_at(p, s, q, false));
+  }
+  // The statistics' row of the tile's row-th product row.
+  __device__ __forceinline__ int64_t stat_at(int row) const {
+    const int r = rt * tq + (row >> p.group_shift);
+    const int64_t at = p.by_query ? (int64_t)q.q_first + r : (int64_t)s * p.rows + r;
+    return at * p.num_q_heads + (j << p.group_shift) + (row & (p.group - 1));
+  }
+  // Last key that product row `row` of row tile rt sees; -1: no such row.
+  __device__ __forceinline__ int sees(int row) const {
+    const int r = rt * tq + (row >> p.group_shift);
+    return r < q.R ? q.base + r : -1;
+  }
+  __device__ __forceinline__ int tile_rows() const { return min(tq, q.R - rt * tq) << p.group_shift; }
+};
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   const bool ok = mbar_wait_bounded(bar, parity, abort);
@@ -198,6 +298,53 @@ struct Ring {
   }
 };
 
+// All threads: the total number of steps, and where this CTA's run starts.
+__device__ void find_start(const PromptParams &p, Start *out, int64_t *warp_sums, bool tell) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int S = p.num_seqs;
+  const int per = (S + kThreads - 1) / kThreads;
+  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  int64_t local = 0;
+  for (int s = s0; s < s1; ++s) {
+    Seq q;
+    if (seq_at(p, s, q, tell)) local += steps_of(p, q) * p.num_kv_heads;
+  }
+  int64_t incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - local, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
+  const int64_t begin = min(run * blockIdx.x, total), end = min(begin + run, total);
+  if (tid == 0) {
+    out->begin = begin;
+    out->end = end;
+    out->run = run;
+  }
+  if (begin < end && before <= begin && begin < before + local) {
+    for (int s = s0; s < s1; ++s) {
+      Seq q;
+      if (!seq_at(p, s, q, false)) continue;
+      const int64_t n = steps_of(p, q) * p.num_kv_heads;
+      if (begin < before + n) {
+        out->s = s;
+        out->offset = begin - before;
+        break;
+      }
+      before += n;
+    }
+  }
+  __syncthreads();
+}
+
 template <int D, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -211,18 +358,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sQ = smem + L::q, *sK = smem + L::k;
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint64_t *q_empty = q_full + kQSlots;
-  uint64_t *k_full = q_empty + kQSlots;
+  uint64_t *st_full = q_empty + kQSlots;
+  uint64_t *st_empty = st_full + kQSlots;
+  uint64_t *k_full = st_empty + kQSlots;
   uint64_t *k_empty = k_full + kKSlots;
   uint64_t *s_full = k_empty + kKSlots;
   uint64_t *s_empty = s_full + kBufs;
-  uint64_t *st_full = s_empty + kBufs;
-  uint64_t *st_empty = st_full + kStatSlots;
-  uint64_t *drain = st_empty + kStatSlots;
+  uint64_t *drain = s_empty + kBufs;
   float *stat = reinterpret_cast<float *>(smem + L::stat);
   int *qpos = reinterpret_cast<int *>(smem + L::qpos);
   float *red = reinterpret_cast<float *>(smem + L::red);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  volatile int *last_flag = reinterpret_cast<volatile int *>(smem + L::misc + 8);
+  Start *start = reinterpret_cast<Start *>(smem + L::misc + 16);
+  int64_t *warp_sums = reinterpret_cast<int64_t *>(smem + L::misc + 64);
+  static_assert(sizeof(Start) <= 48 && 64 + kThreads / 32 * 8 <= 256, "");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -230,6 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+      mbar_init(&st_full[i], 64);
+      mbar_init(&st_empty[i], kEpilogue / 32);
     }
     for (int i = 0; i < kKSlots; ++i) {
       mbar_init(&k_full[i], 1);
@@ -239,43 +392,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kEpilogue / 32);
     }
-    for (int i = 0; i < kStatSlots; ++i) {
-      mbar_init(&st_full[i], 64);
-      mbar_init(&st_empty[i], kEpilogue / 32);
-    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_k);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kBufs * kTile);
     tmem_relinquish();
   }
+  find_start(p, start, warp_sums, PASS == 1 && blockIdx.x == 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // The second pass may be scheduled as SMs become free; it waits for this
-  // grid's end where it reads the statistics.
-  if (PASS == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PASS == 1) {
+    // This pass is alone on the stream until it lets the second one start: it
+    // clears that one's counters (and the second pass clears this one's).
+    if (threadIdx.x == 0) p.tickets[kMaxCtas + blockIdx.x] = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
 
-  // Every role walks the same units, and in them the same steps: key tile by
-  // key tile, its row tiles.  Q stays while the row tile does, K while the key
-  // tile does.
+  // Every role walks the same steps.  A K tile stays while the key tile does; a
+  // Q tile for its row tile (first pass), for one step, or, where all row tiles
+  // of a sequence fit the slots, for the whole (sequence, head).
   if (warp == 0) {
     // ---- loads ----
     if (lane == 0) {
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_k);
       Ring rq, rk;
       int q_loads = 0, k_loads = 0;
       bool ok = true;
-      Unit u;
-      for (int64_t idx = blockIdx.x; idx < p.units && ok; idx += gridDim.x) {
-        if (!unit_at<PASS>(p, idx, u)) continue;
-        const int64_t bt = (int64_t)u.s * p.max_blocks_per_seq;
-        int held = -1;  // row tile in the current Q slot
-        for (int kt = u.kt0; kt < u.kt1 && ok; ++kt) {
+      int kt_in = -1;
+      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+        const bool load_q = PASS == 1 ? kt_in < 0 : !(w.keeps() && (w.loaded >> w.rt & 1));
+        if (PASS == 1 || kt_in < 0) {
           ok = mbar_wait_bounded(&k_empty[rk.slot], rk.phase ^ 1, abort_flag);
           if (!ok) break;
           uint8_t *kd = sK + rk.slot * L::kTileBytes;
@@ -283,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             // (a tile's second half may lie past the keys: it reads the first half's block, unused)
-            int pos = kt * kTile + half * 64;
-            if (pos >= u.q.len_k) pos = kt * kTile;
-            int blk = p.block_tables[bt + (pos >> p.block_shift)];
+            int at = w.kt * kTile + half * 64;
+            if (at >= w.q.len_k) at = w.kt * kTile;
+            int blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (at >> p.block_shift)];
             if (blk < 0 || blk >= p.num_blocks) {
               flag_status(p.status, PKV_DEV_BAD_BLOCK);
               blk = 0;
@@ -293,25 +444,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < XR; ++x)
               tma_load_4d(kd + x * kTile * 128 + half * 64 * 128, &tm_k, &k_full[rk.slot], x * 64,
-                          u.j, pos & ((1 << p.block_shift) - 1), blk);
+                          w.j, at & ((1 << p.block_shift) - 1), blk);
           }
           ++k_loads;
           rk.next(kKSlots);
-          for (int rt = PASS == 1 ? u.rt0 : u.first_rt(kt); rt < u.rt1 && ok; ++rt) {
-            if (rt == held) continue;
-            held = rt;
-            ok = mbar_wait_bounded(&q_empty[rq.slot], rq.phase ^ 1, abort_flag);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&q_full[rq.slot], L::kTileBytes);
-#pragma unroll
-            for (int x = 0; x < XR; ++x)
-              tma_load_3d(sQ + rq.slot * L::kTileBytes + x * kTile * 128, &tm_q, &q_full[rq.slot],
-                          x * 64, u.j << p.group_shift,
-                          u.q.q_begin + u.q.n - u.q.R + rt * u.tq);
-            ++q_loads;
-            rq.next(kQSlots);
-          }
         }
+        if (load_q) {
+          ok = mbar_wait_bounded(&q_empty[rq.slot], rq.phase ^ 1, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[rq.slot], L::kTileBytes);
+#pragma unroll
+          for (int x = 0; x < XR; ++x)
+            tma_load_3d(sQ + rq.slot * L::kTileBytes + x * kTile * 128, &tm_q, &q_full[rq.slot],
+                        x * 64, w.j << p.group_shift, w.q.q_first + w.rt * w.tq);
+          ++q_loads;
+          rq.next(kQSlots);
+          if (w.keeps()) w.loaded |= 1 << w.rt;
+        }
+        kt_in = w.last_here() ? -1 : w.kt;  // (>= 0: the tile goes on)
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
       for (int i = max(0, k_loads - kKSlots); i < k_loads; ++i)
@@ -327,47 +477,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring rq, rk, rs;
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
-      bool ok = true;
-      Unit u;
-      for (int64_t idx = blockIdx.x; idx < p.units && ok; idx += gridDim.x) {
-        if (!unit_at<PASS>(p, idx, u)) continue;
-        int held = -1;
-        for (int kt = u.kt0; kt < u.kt1 && ok; ++kt) {
+      bool ok = true, fresh = true;
+      int qslot = 0, kslot = 0, slot_of[kQSlots] = {0, 0};
+      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+        const bool keeps = w.keeps();
+        const bool load_q = PASS == 1 ? fresh : !(keeps && (w.loaded >> w.rt & 1));
+        if (PASS == 1 || fresh) {
           ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
-          const int rt0 = PASS == 1 ? u.rt0 : u.first_rt(kt);
-          for (int rt = rt0; rt < u.rt1 && ok; ++rt) {
-            if (rt != held) {
-              ok = mbar_wait_bounded(&q_full[rq.slot], rq.phase, abort_flag);
-              held = rt;
-            }
-            if (ok) ok = mbar_wait_bounded(&s_empty[rs.slot], rs.phase ^ 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t a = dq + (uint64_t)((rq.slot * L::kTileBytes) >> 4);
-            const uint64_t b = dk + (uint64_t)((rk.slot * L::kTileBytes) >> 4);
-            const uint32_t idesc =
-                PASS == 1 ? umma_idesc_bf16(kTile, kTile, false, false)
-                          : umma_idesc_bf16(kTile, (tile_rows(p, u, rt) + 15) & ~15, false, false);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk / 4) * kTile * 128 + (kk & 3) * 32) >> 4);
-              umma_bf16(tmem + rs.slot * kTile, PASS == 1 ? a + off : b + off,
-                        PASS == 1 ? b + off : a + off, idesc, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&s_full[rs.slot]);
-            rs.next(kBufs);
-            // Q is done with when the next step of the unit has another row
-            // tile, or there is none.
-            const bool next_same = kt + 1 < u.kt1 && rt + 1 == u.rt1 &&
-                                   (PASS == 1 ? u.rt0 : u.first_rt(kt + 1)) == rt;
-            if (!next_same) {
-              umma_commit(&q_empty[rq.slot]);
-              rq.next(kQSlots);
-              held = -1;
-            }
-          }
-          if (ok) umma_commit(&k_empty[rk.slot]);
+          kslot = rk.slot;
           rk.next(kKSlots);
+        }
+        if (ok && load_q) {
+          ok = mbar_wait_bounded(&q_full[rq.slot], rq.phase, abort_flag);
+          qslot = rq.slot;
+          rq.next(kQSlots);
+          if (keeps) {
+            w.loaded |= 1 << w.rt;
+            slot_of[w.rt & 1] = qslot;
+          }
+        } else if (keeps) {
+          qslot = slot_of[w.rt & 1];
+        }
+        if (ok) ok = mbar_wait_bounded(&s_empty[rs.slot], rs.phase ^ 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t a = dq + (uint64_t)((qslot * L::kTileBytes) >> 4);
+        const uint64_t b = dk + (uint64_t)((kslot * L::kTileBytes) >> 4);
+        // (second pass: no more columns than the row tile has rows, to 16)
+        const uint32_t idesc = PASS == 1
+                                   ? umma_idesc_bf16(kTile, kTile, false, false)
+                                   : umma_idesc_bf16(kTile, (w.tile_rows() + 15) & ~15, false, false);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk / 4) * kTile * 128 + (kk & 3) * 32) >> 4);
+          umma_bf16(tmem + rs.slot * kTile, PASS == 1 ? a + off : b + off,
+                    PASS == 1 ? b + off : a + off, idesc, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[rs.slot]);
+        rs.next(kBufs);
+        fresh = w.last_here();
+        if (PASS == 1 || fresh) umma_commit(&k_empty[kslot]);
+        if (PASS == 1 ? fresh : !keeps) umma_commit(&q_empty[qslot]);
+        if (keeps && w.head_done()) {
+          for (int x = 0; x < kQSlots; ++x)
+            if (w.loaded >> x & 1) umma_commit(&q_empty[slot_of[x]]);
         }
       }
       // Wait for the products before tensor memory is freed.
@@ -375,90 +528,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else if (warp < 4) {
-    // ---- second pass: the rows' denominators, one slot per Q load ----
+    // ---- second pass: the rows' denominators, beside their Q tiles ----
     if (PASS == 2) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      Ring rt_ring;
-      bool ok = true;
-      Unit u;
-      for (int64_t idx = blockIdx.x; idx < p.units && ok; idx += gridDim.x) {
-        if (!unit_at<PASS>(p, idx, u)) continue;
-        int held = -1;
-        for (int kt = u.kt0; kt < u.kt1 && ok; ++kt) {
-          for (int rt = u.first_rt(kt); rt < u.rt1; ++rt) {
-            if (rt == held) continue;
-            held = rt;
-            ok = warp_wait(&st_empty[rt_ring.slot], rt_ring.phase ^ 1, abort_flag);
-            if (!ok) break;
-            const int splits = u.last_pos(rt) / (kTile * p.split_tiles) + 1;
+      if (threadIdx.x == 64) p.tickets[blockIdx.x] = 0;
+      Ring r;
+      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+        const bool keeps = w.keeps();
+        if (keeps && (w.loaded >> w.rt & 1)) continue;
+        if (!warp_wait(&st_empty[r.slot], r.phase ^ 1, abort_flag)) break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int row = (warp - 2) * 64 + x * 32 + lane;
-              const int r = rt * u.tq + (row >> p.group_shift);
-              float neg = 0.f;
-              int pos = -1;
-              if (r < u.q.R) {
-                pos = u.q.c + u.q.n - u.q.R + r;
-                const float2 *part = p.part + stat_row(p, u, r) * p.num_q_heads +
-                                     (u.j << p.group_shift) + (row & (p.group - 1));
-                float m = -INFINITY, l = 0.f;
-                for (int i = 0; i < splits; ++i) {
-                  const float2 ml = __ldcg(part + (int64_t)i * p.stat_rows * p.num_q_heads);
-                  const float mn = fmaxf(m, ml.x);
-                  const float ref = mn == -INFINITY ? 0.f : mn;
-                  l = l * exp2f(m - ref) + ml.y * exp2f(ml.x - ref);
-                  m = mn;
-                }
-                neg = -(m + log2f(l));
-              }
-              stat[rt_ring.slot * kTile + row] = neg;
-              qpos[rt_ring.slot * kTile + row] = pos;
-            }
-            mbar_arrive(&st_full[rt_ring.slot]);
-            rt_ring.next(kStatSlots);
-          }
+        for (int x = 0; x < 2; ++x) {
+          const int row = (warp - 2) * 64 + x * 32 + lane;
+          const int last = w.sees(row);
+          stat[r.slot * kTile + row] = last >= 0 ? __ldcg(p.neg_lse + w.stat_at(row)) : 0.f;
+          qpos[r.slot * kTile + row] = last;
         }
+        mbar_arrive(&st_full[r.slot]);
+        r.next(kQSlots);
+        if (keeps) w.loaded |= 1 << w.rt;
       }
     }
   } else {
     // ---- exponentials and sums: two warps per lane quarter, which share the columns ----
     const int quarter = warp & 3;
     const int half = (warp - 4) >> 2;
-    const int row = quarter * 32 + lane;
+    const int row = quarter * 32 + lane;  // the thread's lane of tensor memory
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const float qs = p.qscale;
     Ring rs, rst;
     bool ok = true;
     int parity = 0;  // of the exchange buffers
-    Unit u;
-    for (int64_t idx = blockIdx.x; idx < p.units && ok; idx += gridDim.x) {
-      if (!unit_at<PASS>(p, idx, u)) continue;
-      if (PASS == 1) {
-        const int r = u.rt0 * u.tq + (row >> p.group_shift);
-        const int pos = r < u.q.R ? u.q.c + u.q.n - u.q.R + r : -1;  // last visible key
-        const bool any = __any_sync(0xffffffffu, pos >= 0);
-        float m = -INFINITY, l = 0.f;
-        for (int kt = u.kt0; kt < u.kt1; ++kt) {
-          ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (any) {
+    float m = -INFINITY, l = 0.f;           // first pass: the row's maximum and sum here
+    float2 acc = make_float2(0.f, 0.f);     // second pass: the key's sum here
+    int sslot = 0, slot_of[kQSlots] = {0, 0};
+    for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+      const bool keeps = w.keeps();
+      if (PASS == 2) {
+        if (!(keeps && (w.loaded >> w.rt & 1))) {
+          ok = warp_wait(&st_full[rst.slot], rst.phase, abort_flag);
+          sslot = rst.slot;
+          rst.next(kQSlots);
+          if (keeps) {
+            w.loaded |= 1 << w.rt;
+            slot_of[w.rt & 1] = sslot;
+          }
+        } else {
+          sslot = slot_of[w.rt & 1];
+        }
+      }
+      if (ok) ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
+      if (ok) {
+        tc_fence_after_sync();
+        if (PASS == 1) {
+          const int last = w.sees(row);
+          if (__any_sync(0xffffffffu, last >= 0)) {
             float v[64];
             float top;
             tmem_load64_max(tmem + lane_base + rs.slot * kTile + half * 64, v, top);
-            const int key0 = kt * kTile + half * 64;
+            const int key0 = w.kt * kTile + half * 64;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
             // Keys past the row's position are hidden; a negative scale makes
             // the smallest product the largest logit.
-            if (qs < 0.f || !__all_sync(0xffffffffu, key0 + 63 <= pos)) {
+            if (qs < 0.f || !__all_sync(0xffffffffu, key0 + 63 <= last)) {
               top = -INFINITY;
 #pragma unroll
               for (int i = 0; i < 64; ++i) {
-                v[i] = key0 + i <= pos ? v[i] * qs : -INFINITY;
+                v[i] = key0 + i <= last ? v[i] * qs : -INFINITY;
                 top = fmaxf(top, v[i]);
               }
               const float mn = fmaxf(m, top);
               const float ref = mn == -INFINITY ? 0.f : mn;
-              float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(v[i] - ref);
               l = l * fast_exp2(m - ref) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -466,101 +606,120 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               const float mn = fmaxf(m, top * qs);
               const float ref = mn == -INFINITY ? 0.f : mn;
-              float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(fmaf(v[i], qs, -ref));
               l = l * fast_exp2(m - ref) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
               m = mn;
             }
           }
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[rs.slot]);
-          rs.next(kBufs);
-        }
-        // The two halves of a row's keys, joined by the first half's thread.
-        float *ex = red + parity * 2 * kTile;
-        if (half == 1) {
-          ex[row] = m;
-          ex[kTile + row] = l;
-        }
-        if (epilogue_sync_any(!ok)) break;
-        if (half == 0 && pos >= 0) {
-          const float m2 = ex[row], l2 = ex[kTile + row];
-          const float mn = fmaxf(m, m2);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
-          p.part[((int64_t)(u.kt0 / p.split_tiles) * p.stat_rows + stat_row(p, u, r)) *
-                     p.num_q_heads +
-                 (u.j << p.group_shift) + (row & (p.group - 1))] = make_float2(mn, l);
-        }
-        parity ^= 1;
-      } else {
-        int held = -1;
-        for (int kt = u.kt0; kt < u.kt1 && ok; ++kt) {
-          const int key = kt * kTile + row;
-          float2 acc = make_float2(0.f, 0.f);
-          for (int rt = u.first_rt(kt); rt < u.rt1; ++rt) {
-            if (rt != held) {
-              ok = warp_wait(&st_full[rst.slot], rst.phase, abort_flag);
-              held = rt;
-            }
-            if (ok) ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const int rows = tile_rows(p, u, rt);
-            const bool open = kt * kTile + kTile - 1 <= u.first_pos(rt);  // every row sees the tile
-            for (int c0 = half * 32; c0 < rows; c0 += 64) {
-              float v[32];
-              tmem_load32(tmem + lane_base + rs.slot * kTile + c0, v);
-              const float4 *ns = reinterpret_cast<const float4 *>(stat + rst.slot * kTile + c0);
-              if (open && c0 + 32 <= rows) {
+        } else {
+          const int key = w.kt * kTile + row;
+          const int rows = w.tile_rows();
+          // Every row of the tile sees every key of the tile.
+          const bool open = w.kt * kTile + kTile - 1 <= w.q.base + w.rt * w.tq;
+          for (int c0 = half * 32; c0 < rows; c0 += 64) {
+            float v[32];
+            tmem_load32(tmem + lane_base + rs.slot * kTile + c0, v);
+            const float4 *ns = reinterpret_cast<const float4 *>(stat + sslot * kTile + c0);
+            if (open && c0 + 32 <= rows) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 n = ns[i / 4];
-                  acc.x += fast_exp2(fmaf(v[i], qs, n.x));
-                  acc.y += fast_exp2(fmaf(v[i + 1], qs, n.y));
-                  acc.x += fast_exp2(fmaf(v[i + 2], qs, n.z));
-                  acc.y += fast_exp2(fmaf(v[i + 3], qs, n.w));
-                }
-              } else {
-                const int4 *qp = reinterpret_cast<const int4 *>(qpos + rst.slot * kTile + c0);
+              for (int i = 0; i < 32; i += 4) {
+                const float4 n = ns[i / 4];
+                acc.x += fast_exp2(fmaf(v[i], qs, n.x));
+                acc.y += fast_exp2(fmaf(v[i + 1], qs, n.y));
+                acc.x += fast_exp2(fmaf(v[i + 2], qs, n.z));
+                acc.y += fast_exp2(fmaf(v[i + 3], qs, n.w));
+              }
+            } else {
+              const int4 *qp = reinterpret_cast<const int4 *>(qpos + sslot * kTile + c0);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 n = ns[i / 4];
-                  const int4 last = qp[i / 4];
-                  acc.x += key <= last.x ? fast_exp2(fmaf(v[i], qs, n.x)) : 0.f;
-                  acc.y += key <= last.y ? fast_exp2(fmaf(v[i + 1], qs, n.y)) : 0.f;
-                  acc.x += key <= last.z ? fast_exp2(fmaf(v[i + 2], qs, n.z)) : 0.f;
-                  acc.y += key <= last.w ? fast_exp2(fmaf(v[i + 3], qs, n.w)) : 0.f;
-                }
+              for (int i = 0; i < 32; i += 4) {
+                const float4 n = ns[i / 4];
+                const int4 last = qp[i / 4];
+                acc.x += key <= last.x ? fast_exp2(fmaf(v[i], qs, n.x)) : 0.f;
+                acc.y += key <= last.y ? fast_exp2(fmaf(v[i + 1], qs, n.y)) : 0.f;
+                acc.x += key <= last.z ? fast_exp2(fmaf(v[i + 2], qs, n.z)) : 0.f;
+                acc.y += key <= last.w ? fast_exp2(fmaf(v[i + 3], qs, n.w)) : 0.f;
               }
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[rs.slot]);
-            rs.next(kBufs);
-            const bool next_same = kt + 1 < u.kt1 && rt + 1 == u.rt1 && u.first_rt(kt + 1) == rt;
-            if (!next_same) {
-              if (lane == 0) mbar_arrive(&st_empty[rst.slot]);
-              rst.next(kStatSlots);
-              held = -1;
-            }
           }
-          float *ex = red + parity * kTile;
-          if (half == 1) ex[row] = acc.x + acc.y;
-          ok = !epilogue_sync_any(!ok);
-          if (half == 0 && ok && key < u.q.len_k) {
-            const float a = (acc.x + acc.y) + ex[row];
-            const int blk = p.block_tables[(int64_t)u.s * p.max_blocks_per_seq + (key >> p.block_shift)];
-            if (blk >= 0 && blk < p.num_blocks) {
-              float *w = p.key_weights + ((((int64_t)blk * p.num_kv_heads + u.j) << p.block_shift) +
-                                          (key & ((1 << p.block_shift) - 1)));
-              if (key >= u.q.c) *w = a;
-              else atomicAdd(w, a);
-            }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[rs.slot]);
+        if (PASS == 2 && lane == 0) {
+          if (!keeps) mbar_arrive(&st_empty[sslot]);
+          else if (w.head_done())
+            for (int x = 0; x < kQSlots; ++x)
+              if (w.loaded >> x & 1) mbar_arrive(&st_empty[slot_of[x]]);
+        }
+        rs.next(kBufs);
+      }
+      if (ok && !w.last_here()) continue;
+
+      // The tile ends here (or a wait ran out: then all eight warps meet and
+      // leave).  The halves' sums are joined by the first half's threads.
+      float *ex = red + parity * 2 * kTile;
+      parity ^= 1;
+      if (half == 1) {
+        ex[row] = PASS == 1 ? m : acc.x + acc.y;
+        if (PASS == 1) ex[kTile + row] = l;
+      }
+      if (epilogue_sync_any(!ok)) break;
+      float2 mine = make_float2(0.f, 0.f);  // (maximum, sum), or (-, sum)
+      auto join = [&](float2 x) {
+        if (PASS == 1) {
+          const float mn = fmaxf(mine.x, x.x);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          mine.y = mine.y * fast_exp2(mine.x - ref) + x.y * fast_exp2(x.x - ref);
+          mine.x = mn;
+        } else {
+          mine.y += x.y;
+        }
+      };
+      if (half == 0) {
+        mine = PASS == 1 ? make_float2(m, l) : make_float2(0.f, acc.x + acc.y);
+        join(PASS == 1 ? make_float2(ex[row], ex[kTile + row]) : make_float2(0.f, ex[row]));
+      }
+      m = -INFINITY;
+      l = 0.f;
+      acc = make_float2(0.f, 0.f);
+      bool finish = true;
+      if (w.cut_left || !w.tile_done()) {
+        // A part of a tile that several CTAs share: filed by CTA, place 0 if
+        // the tile began before it, place 1 if it begins here.
+        int c0, c1;
+        w.ctas(c0, c1);
+        if (half == 0) {
+          __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (w.cut_left ? 0 : 1)) * kTile + row, mine);
+          __threadfence();
+        }
+        if (epilogue_sync_any(false)) break;
+        if (threadIdx.x == 128) {
+          const unsigned int done = atomicAdd(&p.tickets[(PASS - 1) * kMaxCtas + c0], 1u);
+          *last_flag = done == (unsigned int)(c1 - c0) ? 1 : 0;
+          __threadfence();
+        }
+        if (epilogue_sync_any(false)) break;
+        finish = *last_flag != 0;
+        if (finish && half == 0) {
+          mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
+          for (int c = c0 + 1; c <= c1; ++c) join(__ldcg(p.parts + (int64_t)c * 2 * kTile + row));
+        }
+      }
+      if (!finish || half != 0) continue;
+      if (PASS == 1) {
+        if (w.sees(row) >= 0) p.neg_lse[w.stat_at(row)] = -(mine.x + log2f(mine.y));
+      } else {
+        const int key = w.kt * kTile + row;
+        if (key < w.q.len_k) {
+          const int blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
+          if (blk >= 0 && blk < p.num_blocks) {
+            float *to = p.key_weights + ((((int64_t)blk * p.num_kv_heads + w.j) << p.block_shift) +
+                                         (key & ((1 << p.block_shift) - 1)));
+            if (key >= w.q.c) *to = mine.y;
+            else atomicAdd(to, mine.y);
           }
-          parity ^= 1;
         }
       }
     }
@@ -574,39 +733,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// How a call is cut into units (host), from its arguments alone.
+// The workspace: counters, parts of cut tiles, the rows' denominators.
 struct Plan {
-  int64_t rows, row_tiles, key_tiles, stat_rows, splits, split_tiles, groups, group_tiles;
-  bool by_query, fits;
-  Plan(int64_t num_seqs, int64_t total_q, int64_t max_seqlen_q, int64_t window, int64_t group,
-       int64_t num_kv_heads, int64_t max_tokens) {
+  int64_t rows, stat_rows;
+  bool by_query;
+  size_t parts, neg_lse, total;
+  Plan(int64_t num_seqs, int64_t total_q, int64_t max_seqlen_q, int64_t window, int64_t Hq) {
     rows = window < max_seqlen_q ? window : max_seqlen_q;
-    const int64_t tq = kTile / group;
-    row_tiles = (rows + tq - 1) / tq;
-    key_tiles = (max_tokens + kTile - 1) / kTile;
-    by_query = num_seqs * rows > total_q;
+    // Rows are filed under (sequence, rank) or, where that is more, under their query.
+    by_query = rows > total_q / num_seqs;
     stat_rows = by_query ? total_q : num_seqs * rows;
-    // First pass: a row's keys in splits of up to 8 tiles (1024 keys), fewer
-    // while there are not two units for every SM.
-    split_tiles = kMaxSplitTiles;
-    const double heads = (double)num_seqs * num_kv_heads;  // (a product of arguments may pass 64 bits)
-    while (split_tiles > 1 &&
-           heads * row_tiles * ((key_tiles + split_tiles - 1) / split_tiles) < kUnitsWanted)
-      split_tiles /= 2;
-    splits = (key_tiles + split_tiles - 1) / split_tiles;
-    // Second pass: key tiles in groups of about 8 steps.
-    group_tiles = kMaxSplitTiles / row_tiles;
-    if (group_tiles < 1) group_tiles = 1;
-    while (group_tiles > 1 && heads * ((key_tiles + group_tiles - 1) / group_tiles) < kUnitsWanted)
-      group_tiles /= 2;
-    groups = (key_tiles + group_tiles - 1) / group_tiles;
-    fits = heads * row_tiles * splits < 4e18 && heads * groups < 4e18;
+    parts = 2 * kMaxCtas * sizeof(unsigned int);
+    neg_lse = parts + (size_t)kMaxCtas * 2 * kTile * sizeof(float2);
+    total = neg_lse + (size_t)(stat_rows * Hq) * sizeof(float);
   }
 };
 
 template <int D>
-pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, PromptParams prm, const Plan &plan,
-                  cudaStream_t stream) {
+pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const PromptParams &prm,
+                  int64_t most_steps, cudaStream_t stream) {
   const int smem = Layout<D>::total + 1024;
   const int sms = device_sm_count();
   int ctas = 0;
@@ -614,12 +759,10 @@ pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, PromptParams prm
       !kernel_smem_setup((const void *)prompt_weights_kernel<D, 1>, kThreads, smem, &ctas) ||
       !kernel_smem_setup((const void *)prompt_weights_kernel<D, 2>, kThreads, smem, &ctas))
     return PKV_ERR_CUDA;
-  prm.units = (int64_t)prm.num_seqs * plan.splits * plan.row_tiles * prm.num_kv_heads;
-  int64_t grid = prm.units < sms ? prm.units : sms;
+  int64_t grid = sms < kMaxCtas ? sms : kMaxCtas;
+  if (grid > most_steps) grid = most_steps;
   prompt_weights_kernel<D, 1><<<(unsigned)grid, kThreads, smem, stream>>>(tq, tk, prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  prm.units = (int64_t)prm.num_seqs * plan.groups * prm.num_kv_heads;
-  grid = prm.units < sms ? prm.units : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
@@ -648,13 +791,10 @@ extern "C" size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total
     return 0;
   // (bounded so that no product below can wrap)
   const int64_t group = num_q_heads / num_kv_heads;
-  if (group < 1 || group > kTile || num_q_heads > (1 << 16) || total_q > 0x7FFFFFFFLL ||
+  if (group < 1 || num_q_heads > (1 << 16) || total_q > 0x7FFFFFFFLL ||
       (int64_t)max_blocks_per_seq * block_size > 0x7FFFFFFFLL)
     return 0;
-  const Plan plan(num_seqs, total_q, max_seqlen_q, window, group, num_kv_heads,
-                  (int64_t)max_blocks_per_seq * block_size);
-  if (plan.splits * num_q_heads > (INT64_MAX / 16) / plan.stat_rows) return 0;
-  return 256 + (size_t)(plan.splits * num_q_heads * plan.stat_rows) * sizeof(float2);
+  return Plan(num_seqs, total_q, max_seqlen_q, window, num_q_heads).total;
 }
 
 extern "C" pkv_status pkv_paged_prefill_weights(
@@ -688,19 +828,19 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   if (workspace == nullptr || workspace_bytes < need ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_WORKSPACE;
-  const Plan plan(num_seqs, total_q, max_seqlen_q, window, G, num_kv_heads,
-                  (int64_t)max_blocks_per_seq * block_size);
-  if (!plan.fits) return PKV_ERR_UNSUPPORTED;  // more units than 64 bits number
+  const Plan plan(num_seqs, total_q, max_seqlen_q, window, num_q_heads);
   PromptParams prm;
   prm.key_weights = key_weights;
   prm.block_tables = block_tables;
   prm.cu_q = cu_seqlens_q;
   prm.cu_k = cu_seqlens_k;
-  prm.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + 256);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  prm.tickets = reinterpret_cast<unsigned int *>(ws);
+  prm.parts = reinterpret_cast<float2 *>(ws + plan.parts);
+  prm.neg_lse = reinterpret_cast<float *>(ws + plan.neg_lse);
   prm.status = dev_status;
   prm.num_blocks = num_blocks;
   prm.total_q = total_q;
-  prm.stat_rows = plan.stat_rows;
   prm.num_seqs = num_seqs;
   prm.num_q_heads = num_q_heads;
   prm.num_kv_heads = num_kv_heads;
@@ -712,12 +852,6 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   prm.window = window;
   prm.rows = (int)plan.rows;
   prm.by_query = plan.by_query ? 1 : 0;
-  prm.row_tiles = (int)plan.row_tiles;
-  prm.splits = (int)plan.splits;
-  prm.split_tiles = (int)plan.split_tiles;
-  prm.groups = (int)plan.groups;
-  prm.group_tiles = (int)plan.group_tiles;
-  prm.units = 0;
   prm.qscale = scale * kLog2e;
 
   // q as {D, Hq, T}: a box is 64 dims x the G heads of a kv head x 128 / G
@@ -736,5 +870,11 @@ extern "C" pkv_status pkv_paged_prefill_weights(
       !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true))
     return PKV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? launch<128>(tq, tk, prm, plan, st) : launch<64>(tq, tk, prm, plan, st);
+  // Steps that the batch can have at most (a small one needs fewer CTAs).
+  const int64_t row_tiles = ((int64_t)plan.rows * G + kTile - 1) / kTile;
+  const int64_t key_tiles = ((int64_t)max_blocks_per_seq * block_size + kTile - 1) / kTile;
+  const double most = (double)num_seqs * num_kv_heads * row_tiles * key_tiles;
+  const int64_t most_steps = most < kMaxCtas ? (int64_t)most : kMaxCtas;
+  return head_dim == 128 ? launch<128>(tq, tk, prm, most_steps, st)
+                         : launch<64>(tq, tk, prm, most_steps, st);
 }
