@@ -12,8 +12,8 @@
 // bytes; computing it again is 2 D operations on operands that are in L2):
 //  1. Rows: S = Q K^T with the rows in the lanes of tensor memory (M = 128 rows:
 //     128 / G queries of the G heads that share the keys; N = 128 keys).  A
-//     thread owns a row (for half of a tile's keys) and keeps its running maximum
-//     and sum over the row's key tiles.
+//     thread owns a row and keeps its running maximum and sum over the row's key
+//     tiles (two groups of four warps take the tiles in turn).
 //  2. Keys: S^T = K Q^T with the keys in the lanes, so that summing a key's
 //     weights over the rows is a sum inside one thread.
 // A step is one 128 x 128 product of a key tile and a row tile that sees any of
@@ -40,7 +40,7 @@ constexpr int kTile = 128;       // rows and keys per tile
 constexpr int kThreads = 384;
 constexpr int kEpilogue = 256;   // threads of warps 4-11
 constexpr int kBufs = 4;         // S buffers of 128 columns: all of tensor memory
-constexpr int kQSlots = 2;       // row tiles, with their denominators
+constexpr int kQSlots = 2;       // row tiles, with their denominators (a kept pair is slot0, slot1)
 constexpr int kMaxCtas = 512;    // places for cut tiles in the workspace (CTAs of a grid at most)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -118,14 +118,17 @@ __device__ __forceinline__ bool seq_at(const PromptParams &p, int s, Seq &q, boo
   return true;
 }
 
+// (128 / G is a power of two: divisions by it, and by a tile, are shifts)
+__device__ __forceinline__ int tq_shift(const PromptParams &p) { return 7 - p.group_shift; }
+static_assert(kTile == 128, "shifts by 7");
+
 // Key tiles that row tile rt sees: up to its last query's position.
 __device__ __forceinline__ int tiles_seen(const PromptParams &p, const Seq &q, int rt) {
-  return (q.base + min((rt + 1) * (kTile >> p.group_shift), q.R) - 1) / kTile + 1;
+  return ((q.base + min((rt + 1) << tq_shift(p), q.R) - 1) >> 7) + 1;
 }
 // The first row tile that sees any of key tile kt.
 __device__ __forceinline__ int first_rt(const PromptParams &p, const Seq &q, int kt) {
-  const int over = kt * kTile - q.base;  // queries before this one see none of it
-  return over <= 0 ? 0 : over / (kTile >> p.group_shift);
+  return max(kt * kTile - q.base, 0) >> tq_shift(p);  // (queries before that one see none of it)
 }
 // Steps of the first m row tiles.  Row tile rt + G starts 128 positions later
 // than rt, so it sees one tile more: whole turns of G row tiles sum in closed form.
@@ -174,6 +177,8 @@ struct Walk {
   int64_t pos, end, run;
   Seq q;
   int s, j, rt, kt, tq;
+  int tile_left;   // steps of the tile from this one on, here or not
+  bool last_tile;  // of the (sequence, head)
   int loaded;     // second pass, few row tiles: those in their slots for this (sequence, head)
   bool cut_left;  // the current tile's first steps are another CTA's
 
@@ -182,7 +187,8 @@ struct Walk {
     end = st.end;
     run = st.run;
     s = st.s;
-    j = rt = kt = loaded = 0;
+    j = rt = kt = loaded = tile_left = 0;
+    last_tile = false;
     cut_left = false;
     tq = kTile >> p.group_shift;
     if (pos >= end) return;
@@ -205,39 +211,46 @@ struct Walk {
       kt = lo;
       rt = first_rt(p, q, kt) + in;
     }
+    enter_tile();
+    if (PASS == 1) tile_left -= in;
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
-  // The tile (row tile, or key tile) ends with this step.
-  __device__ __forceinline__ bool tile_done() const {
-    return PASS == 1 ? kt + 1 == tiles_seen(p, q, rt) : rt + 1 == q.nrt;
+  __device__ __forceinline__ void enter_tile() {
+    if (PASS == 1) {
+      tile_left = tiles_seen(p, q, rt);
+      last_tile = rt + 1 == q.nrt;
+    } else {
+      tile_left = q.nrt - rt;
+      last_tile = kt + 1 == q.nkt;
+    }
   }
+  // The tile (row tile, or key tile) ends with this step.
+  __device__ __forceinline__ bool tile_done() const { return tile_left == 1; }
   // This step is the last of the tile here.
-  __device__ __forceinline__ bool last_here() const { return pos + 1 == end || tile_done(); }
+  __device__ __forceinline__ bool last_here() const { return tile_left == 1 || pos + 1 == end; }
   // (sequence, head) ends with this step, here.
   __device__ __forceinline__ bool head_done() const {
-    return pos + 1 == end || (PASS == 1 ? rt + 1 == q.nrt && tile_done() : kt + 1 == q.nkt && tile_done());
+    return (last_tile && tile_left == 1) || pos + 1 == end;
   }
   // The first and the last CTA of the current tile.
   __device__ __forceinline__ void ctas(int &first, int &last) const {
-    const int f = PASS == 1 ? 0 : first_rt(p, q, kt);
-    const int64_t u0 = pos - (PASS == 1 ? kt : rt - f);
-    first = (int)(u0 / run);
-    last = (int)((u0 + (PASS == 1 ? tiles_seen(p, q, rt) : q.nrt - f) - 1) / run);
+    const int done = PASS == 1 ? kt : rt - first_rt(p, q, kt);  // steps of the tile before this one
+    first = (int)((pos - done) / run);
+    last = (int)((pos + tile_left - 1) / run);
   }
   // Second pass: so few row tiles that they stay in their slots for the whole
   // (sequence, head), else each step loads its own.
   __device__ __forceinline__ bool keeps() const { return PASS == 2 && q.nrt <= kQSlots; }
   __device__ __forceinline__ void next() {
-    const bool done = tile_done(), head = head_done();
     ++pos;
-    if (!more()) return;
-    if (!done) {
+    if (--tile_left > 0) {
       if (PASS == 1) ++kt;
       else ++rt;
       return;
     }
+    if (!more()) return;
     cut_left = false;
-    if (!head) {
+    if (!last_tile) {
       if (PASS == 1) {
         ++rt;
         kt = 0;
@@ -245,12 +258,14 @@ struct Walk {
         ++kt;
         rt = first_rt(p, q, kt);
       }
-      return;
+    } else {
+      loaded = rt = kt = 0;
+      if (++j == p.num_kv_heads) {
+        j = 0;
+        do ++s; while (!seq_at(p, s, q, false));
+      }
     }
-    loaded = rt = kt = 0;
-    if (++j < p.num_kv_heads) return;  // (first_rt(0) is 0)
-    j = 0;
-    do ++s; while (!seq_at(p, s, q, false));
+    enter_tile();
   }
   // The statistics' row of the tile's row-th product row.
   __device__ __forceinline__ int64_t stat_at(int row) const {
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], kEpilogue / 32);
+      mbar_init(&s_empty[i], 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
       bool ok = true, fresh = true;
-      int qslot = 0, kslot = 0, slot_of[kQSlots] = {0, 0};
+      int qslot = 0, kslot = 0, slot0 = 0, slot1 = 0;
       for (Walk<PASS> w(p, *start); w.more(); w.next()) {
         const bool keeps = w.keeps();
         const bool load_q = PASS == 1 ? fresh : !(keeps && (w.loaded >> w.rt & 1));
@@ -493,10 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           rq.next(kQSlots);
           if (keeps) {
             w.loaded |= 1 << w.rt;
-            slot_of[w.rt & 1] = qslot;
+            if (w.rt == 0) slot0 = qslot;
+            else slot1 = qslot;
           }
         } else if (keeps) {
-          qslot = slot_of[w.rt & 1];
+          qslot = w.rt == 0 ? slot0 : slot1;
         }
         if (ok) ok = mbar_wait_bounded(&s_empty[rs.slot], rs.phase ^ 1, abort_flag);
         if (!ok) break;
@@ -519,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (PASS == 1 || fresh) umma_commit(&k_empty[kslot]);
         if (PASS == 1 ? fresh : !keeps) umma_commit(&q_empty[qslot]);
         if (keeps && w.head_done()) {
-          for (int x = 0; x < kQSlots; ++x)
-            if (w.loaded >> x & 1) umma_commit(&q_empty[slot_of[x]]);
+          if (w.loaded & 1) umma_commit(&q_empty[slot0]);
+          if (w.loaded & 2) umma_commit(&q_empty[slot1]);
         }
       }
       // Wait for the products before tensor memory is freed.
@@ -550,19 +566,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- exponentials and sums: two warps per lane quarter, which share the columns ----
+    // ---- exponentials and sums: two groups of four warps take the steps in turn ----
     const int quarter = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int side = (warp - 4) >> 2;     // the group
     const int row = quarter * 32 + lane;  // the thread's lane of tensor memory
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const float qs = p.qscale;
+    const float2 qs2 = make_float2(qs, qs);
     Ring rs, rst;
     bool ok = true;
     int parity = 0;  // of the exchange buffers
-    float m = -INFINITY, l = 0.f;           // first pass: the row's maximum and sum here
-    float2 acc = make_float2(0.f, 0.f);     // second pass: the key's sum here
-    int sslot = 0, slot_of[kQSlots] = {0, 0};
+    int turn = 0;    // the group whose step it is
+    float m = -INFINITY, l = 0.f;        // first pass: the row's maximum and sum, of this group's steps
+    float2 acc = make_float2(0.f, 0.f);  // second pass: the key's sum, of this group's steps
+    int sslot = 0, slot0 = 0, slot1 = 0;
     for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+      const bool mine_now = turn == side;
+      turn ^= 1;
       const bool keeps = w.keeps();
       if (PASS == 2) {
         if (!(keeps && (w.loaded >> w.rt & 1))) {
@@ -571,44 +591,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           rst.next(kQSlots);
           if (keeps) {
             w.loaded |= 1 << w.rt;
-            slot_of[w.rt & 1] = sslot;
+            if (w.rt == 0) slot0 = sslot;
+            else slot1 = sslot;
           }
         } else {
-          sslot = slot_of[w.rt & 1];
+          sslot = w.rt == 0 ? slot0 : slot1;
         }
       }
-      if (ok) ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
-      if (ok) {
+      if (ok && mine_now) ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
+      if (ok && mine_now) {
         tc_fence_after_sync();
+        const uint32_t ta = tmem + lane_base + rs.slot * kTile;
         if (PASS == 1) {
           const int last = w.sees(row);
           if (__any_sync(0xffffffffu, last >= 0)) {
-            float v[64];
-            float top;
-            tmem_load64_max(tmem + lane_base + rs.slot * kTile + half * 64, v, top);
-            const int key0 = w.kt * kTile + half * 64;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            // Keys past the row's position are hidden; a negative scale makes
-            // the smallest product the largest logit.
-            if (qs < 0.f || !__all_sync(0xffffffffu, key0 + 63 <= last)) {
-              top = -INFINITY;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kTile; c0 += 64) {
+              float v[64];
+              float top;
+              tmem_load64_max(ta + c0, v, top);
+              const int key0 = w.kt * kTile + c0;
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              float mn, ref;
+              // Keys past the row's position are hidden; a negative scale makes
+              // the smallest product the largest logit.
+              if (qs < 0.f || !__all_sync(0xffffffffu, key0 + 63 <= last)) {
+                top = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                v[i] = key0 + i <= last ? v[i] * qs : -INFINITY;
-                top = fmaxf(top, v[i]);
+                for (int i = 0; i < 64; ++i) {
+                  v[i] = key0 + i <= last ? v[i] * qs : -INFINITY;
+                  top = fmaxf(top, v[i]);
+                }
+                mn = fmaxf(m, top);
+                ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+                for (int i = 0; i < 64; i += 2)
+                  sum[(i >> 1) & 1] = __fadd2_rn(
+                      sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
+              } else {
+                mn = fmaxf(m, top * qs);
+                ref = mn == -INFINITY ? 0.f : mn;
+                const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                  const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
+                  sum[(i >> 1) & 1] =
+                      __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
+                }
               }
-              const float mn = fmaxf(m, top);
-              const float ref = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-              for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(v[i] - ref);
-              l = l * fast_exp2(m - ref) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-              m = mn;
-            } else {
-              const float mn = fmaxf(m, top * qs);
-              const float ref = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-              for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(fmaf(v[i], qs, -ref));
-              l = l * fast_exp2(m - ref) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+              l = l * fast_exp2(m - ref) + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
               m = mn;
             }
           }
@@ -617,19 +648,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rows = w.tile_rows();
           // Every row of the tile sees every key of the tile.
           const bool open = w.kt * kTile + kTile - 1 <= w.q.base + w.rt * w.tq;
-          for (int c0 = half * 32; c0 < rows; c0 += 64) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < rows; c0 += 32) {
             float v[32];
-            tmem_load32(tmem + lane_base + rs.slot * kTile + c0, v);
+            tmem_load32(ta + c0, v);
             const float4 *ns = reinterpret_cast<const float4 *>(stat + sslot * kTile + c0);
             if (open && c0 + 32 <= rows) {
+              float2 more = make_float2(0.f, 0.f);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 n = ns[i / 4];
-                acc.x += fast_exp2(fmaf(v[i], qs, n.x));
-                acc.y += fast_exp2(fmaf(v[i + 1], qs, n.y));
-                acc.x += fast_exp2(fmaf(v[i + 2], qs, n.z));
-                acc.y += fast_exp2(fmaf(v[i + 3], qs, n.w));
+                const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
+                const float2 z1 = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
+                acc = __fadd2_rn(acc, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+                more = __fadd2_rn(more, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
               }
+              acc = __fadd2_rn(acc, more);
             } else {
               const int4 *qp = reinterpret_cast<const int4 *>(qpos + sslot * kTile + c0);
 #pragma unroll
@@ -647,21 +681,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[rs.slot]);
-        if (PASS == 2 && lane == 0) {
-          if (!keeps) mbar_arrive(&st_empty[sslot]);
-          else if (w.head_done())
-            for (int x = 0; x < kQSlots; ++x)
-              if (w.loaded >> x & 1) mbar_arrive(&st_empty[slot_of[x]]);
+      }
+      rs.next(kBufs);
+      // (both groups release a row tile's denominators, each after its last use)
+      if (PASS == 2 && ok) {
+        __syncwarp();
+        if (lane == 0) {
+          if (!keeps) {
+            mbar_arrive(&st_empty[sslot]);
+          } else if (w.head_done()) {
+            if (w.loaded & 1) mbar_arrive(&st_empty[slot0]);
+            if (w.loaded & 2) mbar_arrive(&st_empty[slot1]);
+          }
         }
-        rs.next(kBufs);
       }
       if (ok && !w.last_here()) continue;
 
       // The tile ends here (or a wait ran out: then all eight warps meet and
-      // leave).  The halves' sums are joined by the first half's threads.
+      // leave).  The groups' sums are joined by the first group's threads.
       float *ex = red + parity * 2 * kTile;
       parity ^= 1;
-      if (half == 1) {
+      if (side == 1) {
         ex[row] = PASS == 1 ? m : acc.x + acc.y;
         if (PASS == 1) ex[kTile + row] = l;
       }
@@ -677,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mine.y += x.y;
         }
       };
-      if (half == 0) {
+      if (side == 0) {
         mine = PASS == 1 ? make_float2(m, l) : make_float2(0.f, acc.x + acc.y);
         join(PASS == 1 ? make_float2(ex[row], ex[kTile + row]) : make_float2(0.f, ex[row]));
       }
@@ -690,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile began before it, place 1 if it begins here.
         int c0, c1;
         w.ctas(c0, c1);
-        if (half == 0) {
+        if (side == 0) {
           __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (w.cut_left ? 0 : 1)) * kTile + row, mine);
           __threadfence();
         }
@@ -702,12 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (epilogue_sync_any(false)) break;
         finish = *last_flag != 0;
-        if (finish && half == 0) {
+        if (finish && side == 0) {
           mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
           for (int c = c0 + 1; c <= c1; ++c) join(__ldcg(p.parts + (int64_t)c * 2 * kTile + row));
         }
       }
-      if (!finish || half != 0) continue;
+      if (!finish || side != 0) continue;
       if (PASS == 1) {
         if (w.sees(row) >= 0) p.neg_lse[w.stat_at(row)] = -(mine.x + log2f(mine.y));
       } else {
