@@ -366,7 +366,7 @@ size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max
  * overlap on the device must not share a workspace.
  *
  * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in
- * {64, 128, 256, 512}.
+ * {64, 128, 256, 512}; max_blocks_per_seq * block_size at most 2^20.
  */
 pkv_status pkv_paged_prefill_weights(
     float *key_weights, const uint16_t *q, const uint16_t *k_cache, const int32_t *block_tables,

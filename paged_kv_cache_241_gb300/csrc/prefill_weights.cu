@@ -13,7 +13,7 @@
 //  1. Rows: S = Q K^T with the rows in the lanes of tensor memory (M = 128 rows:
 //     128 / G queries of the G heads that share the keys; N = 128 keys).  A
 //     thread owns a row and keeps its running maximum and sum over the row's key
-//     tiles (two groups of four warps take the tiles in turn).
+//     tiles.
 //  2. Keys: S^T = K Q^T with the keys in the lanes, so that summing a key's
 //     weights over the rows is a sum inside one thread.
 // A step is one 128 x 128 product of a key tile and a row tile that sees any of
@@ -38,9 +38,9 @@ namespace {
 
 constexpr int kTile = 128;       // rows and keys per tile
 constexpr int kThreads = 384;
-constexpr int kEpilogue = 256;   // threads of warps 4-11
 constexpr int kBufs = 4;         // S buffers of 128 columns: all of tensor memory
-constexpr int kQSlots = 2;       // row tiles, with their denominators (a kept pair is slot0, slot1)
+constexpr int kQSlots = 2;       // row tiles, with their denominators
+constexpr int kMaxTokens = 1 << 20;  // of a sequence (a head's steps are counted in 32 bits)
 constexpr int kMaxCtas = 512;    // places for cut tiles in the workspace (CTAs of a grid at most)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -51,12 +51,12 @@ struct Layout {
   static constexpr int q = 0;
   static constexpr int k = q + kQSlots * kTileBytes;
   static constexpr int bars = k + kKSlots * kTileBytes;
-  // q_full/q_empty[Q], k_full/k_empty[K], s_full/s_empty[B], st_full/st_empty[Q], drain
-  static constexpr int kNumBars = 4 * kQSlots + 2 * kKSlots + 2 * kBufs + 1;
+  // q_full/q_empty/st_full/st_empty[Q], k_full/k_empty[K], s_full/s_empty[B],
+  // x_full/x_empty[quarter][2], drain
+  static constexpr int kNumBars = 4 * kQSlots + 2 * kKSlots + 2 * kBufs + 16 + 1;
   static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [Q][128] -log2 denominators
-  static constexpr int qpos = stat + kQSlots * kTile * 4;        // [Q][128] last visible key, -1: no row
-  static constexpr int red = qpos + kQSlots * kTile * 4;         // [2][2][128] exchange between halves
-  static constexpr int misc = red + 4 * kTile * 4;  // tensor memory address, abort, last, start, scan
+  static constexpr int ex = stat + kQSlots * kTile * 4;          // [2][128] (maximum, sum), between the groups
+  static constexpr int misc = ex + 2 * kTile * 8;  // tensor memory address, abort flag, run, scan
   static constexpr int total = misc + 256;
   // One CTA per SM (it takes all of tensor memory): more than half of an SM's
   // shared memory, so that a second one never waits for tensor memory.
@@ -70,7 +70,7 @@ struct PromptParams {
   const int32_t *cu_k;
   float *neg_lse;           // [stat rows, Hq]: -log2 of a row's softmax denominator
   float2 *parts;            // [CTA][2][128]: parts of tiles cut between CTAs
-  unsigned int *tickets;    // [2][kMaxCtas]: parts of a cut tile that are done, by its first CTA
+  unsigned int *tickets;    // [2][kMaxCtas][4]: parts of a cut tile that are done, by its first CTA and lane quarter
   int32_t *status;
   int64_t num_blocks;
   int64_t total_q;
@@ -112,9 +112,8 @@ __device__ __forceinline__ bool seq_at(const PromptParams &p, int s, Seq &q, boo
   q.R = min(n, p.window);
   q.q_first = q_begin + n - q.R;
   q.base = q.len_k - q.R;
-  const int tq = kTile >> p.group_shift;
-  q.nrt = (q.R + tq - 1) / tq;
-  q.nkt = (q.len_k + kTile - 1) / kTile;
+  q.nrt = (q.R + (kTile >> p.group_shift) - 1) >> (7 - p.group_shift);
+  q.nkt = (q.len_k + kTile - 1) >> 7;
   return true;
 }
 
@@ -130,175 +129,120 @@ __device__ __forceinline__ int tiles_seen(const PromptParams &p, const Seq &q, i
 __device__ __forceinline__ int first_rt(const PromptParams &p, const Seq &q, int kt) {
   return max(kt * kTile - q.base, 0) >> tq_shift(p);  // (queries before that one see none of it)
 }
-// Steps of the first m row tiles.  Row tile rt + G starts 128 positions later
-// than rt, so it sees one tile more: whole turns of G row tiles sum in closed form.
-__device__ __forceinline__ int64_t steps_of_rows(const PromptParams &p, const Seq &q, int m) {
-  int64_t extra = 0;
-  if (m == q.nrt) {  // (the last row tile can be short)
-    extra = q.nkt;
-    --m;
-  }
-  const int G = p.group;
-  const int64_t turns = m >> p.group_shift;
-  const int rest = m & (G - 1);
-  int64_t sum = (int64_t)G * (turns * (turns - 1) / 2) + turns * rest;
-  for (int r = 0; r < G; ++r) {
-    const int64_t seen = (q.base + (r + 1) * (kTile >> p.group_shift) - 1) / kTile + 1;
-    sum += seen * (turns + (r < rest ? 1 : 0));
-  }
-  return sum + extra;
+// Steps of one head's first m row tiles (at most 2^30: kMaxTokens).  Row tile
+// rt + G starts 128 positions later than rt, so it sees one tile more: whole
+// turns of G row tiles sum in closed form.
+__device__ __forceinline__ int steps_of_rows(const PromptParams &p, const Seq &q, int m) {
+  const int turns = m >> p.group_shift, rest = m & (p.group - 1);
+  int sum = p.group * (turns * (turns - 1) / 2) + turns * rest;
+  for (int r = 0; r < p.group; ++r)
+    sum += (((q.base + ((r + 1) << tq_shift(p)) - 1) >> 7) + 1) * (turns + (r < rest ? 1 : 0));
+  return sum;
 }
-// Steps of the first k key tiles (second pass): row tiles from first_rt on, which
-// grows by G with every key tile once it is past zero.
-__device__ __forceinline__ int64_t steps_of_keys(const PromptParams &p, const Seq &q, int k) {
-  const int tq = kTile >> p.group_shift;
-  const int64_t e = (q.base + tq - 1) / tq;                 // first_rt(kt) = max(0, G kt - e)
-  const int64_t k1 = min((e + p.group - 1) >> p.group_shift, (int64_t)k);
-  const int64_t n = k - k1;
-  const int64_t skipped = p.group * (k1 * n + n * (n - 1) / 2) - e * n;
-  return (int64_t)k * q.nrt - skipped;
-}
-__device__ __forceinline__ int64_t steps_of(const PromptParams &p, const Seq &q) {
-  return steps_of_rows(p, q, q.nrt);
+// Steps of one head's first k key tiles: row tiles from first_rt on, which grows
+// by G with every key tile once it is past zero.  With k = nkt: all steps.
+__device__ __forceinline__ int steps_of_keys(const PromptParams &p, const Seq &q, int k) {
+  const int e = (q.base + (1 << tq_shift(p)) - 1) >> tq_shift(p);  // first_rt(kt) = max(0, G kt - e)
+  const int k1 = min((e + p.group - 1) >> p.group_shift, k);
+  const int n = k - k1;
+  return k * q.nrt - (p.group * (k1 * n + n * (n - 1) / 2) - e * n);
 }
 
-// Where a CTA's run of steps starts (found once, by all threads).
-struct Start {
-  int64_t begin, end;  // steps of the call
-  int64_t run;         // steps per CTA
-  int64_t offset;      // of `begin` within its sequence
-  int s;
+// Where a CTA's run of steps starts.
+struct Run {
+  int64_t begin, steps;  // first step of the call's, steps per CTA
+  int64_t left;          // steps to do
+  int s, j, tile, in;    // sequence, head, tile, and steps of that tile before `begin`
 };
 
-// A role's walk over its CTA's steps.
+// A role's walk over its CTA's run, tile by tile: row tiles in the first pass,
+// whose steps are key tiles, key tiles in the second, whose steps are row tiles.
 template <int PASS>
 struct Walk {
   const PromptParams &p;
-  int64_t pos, end, run;
   Seq q;
-  int s, j, rt, kt, tq;
-  int tile_left;   // steps of the tile from this one on, here or not
+  int s, j, tile;
+  int b0, b1;      // the tile's steps
+  int x0, x1;      // those of them that are here
+  int64_t k, left; // number of step x0 in the CTA's run; steps to do from x0 on
   bool last_tile;  // of the (sequence, head)
-  int loaded;     // second pass, few row tiles: those in their slots for this (sequence, head)
-  bool cut_left;  // the current tile's first steps are another CTA's
 
-  __device__ Walk(const PromptParams &prm, const Start &st) : p(prm) {
-    pos = st.begin;
-    end = st.end;
-    run = st.run;
-    s = st.s;
-    j = rt = kt = loaded = tile_left = 0;
-    last_tile = false;
-    cut_left = false;
-    tq = kTile >> p.group_shift;
-    if (pos >= end) return;
+  __device__ __forceinline__ Walk(const PromptParams &prm, const Run &run) : p(prm) {
+    left = run.left;
+    k = 0;
+    if (left <= 0) return;
+    s = run.s;
+    j = run.j;
+    tile = run.tile;
     seq_at(p, s, q, false);
-    const int64_t each = steps_of(p, q);
-    j = (int)(st.offset / each);
-    const int64_t at = st.offset - j * each;
-    int lo = 0, hi = (PASS == 1 ? q.nrt : q.nkt) - 1;  // the last tile that starts at or before `at`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((PASS == 1 ? steps_of_rows(p, q, mid) : steps_of_keys(p, q, mid)) <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    const int in = (int)(at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo)));
-    cut_left = in > 0;
+    enter(run.in);
+  }
+  __device__ __forceinline__ void enter(int in) {
     if (PASS == 1) {
-      rt = lo;
-      kt = in;
+      b0 = 0;
+      b1 = tiles_seen(p, q, tile);
+      last_tile = tile + 1 == q.nrt;
     } else {
-      kt = lo;
-      rt = first_rt(p, q, kt) + in;
+      b0 = first_rt(p, q, tile);
+      b1 = q.nrt;
+      last_tile = tile + 1 == q.nkt;
     }
-    enter_tile();
-    if (PASS == 1) tile_left -= in;
+    x0 = b0 + in;
+    x1 = (int)min((int64_t)b1, x0 + left);
   }
-  __device__ __forceinline__ bool more() const { return pos < end; }
-  __device__ __forceinline__ void enter_tile() {
-    if (PASS == 1) {
-      tile_left = tiles_seen(p, q, rt);
-      last_tile = rt + 1 == q.nrt;
-    } else {
-      tile_left = q.nrt - rt;
-      last_tile = kt + 1 == q.nkt;
-    }
-  }
-  // The tile (row tile, or key tile) ends with this step.
-  __device__ __forceinline__ bool tile_done() const { return tile_left == 1; }
-  // This step is the last of the tile here.
-  __device__ __forceinline__ bool last_here() const { return tile_left == 1 || pos + 1 == end; }
-  // (sequence, head) ends with this step, here.
-  __device__ __forceinline__ bool head_done() const {
-    return (last_tile && tile_left == 1) || pos + 1 == end;
-  }
-  // The first and the last CTA of the current tile.
-  __device__ __forceinline__ void ctas(int &first, int &last) const {
-    const int done = PASS == 1 ? kt : rt - first_rt(p, q, kt);  // steps of the tile before this one
-    first = (int)((pos - done) / run);
-    last = (int)((pos + tile_left - 1) / run);
-  }
-  // Second pass: so few row tiles that they stay in their slots for the whole
-  // (sequence, head), else each step loads its own.
-  __device__ __forceinline__ bool keeps() const { return PASS == 2 && q.nrt <= kQSlots; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next() {
-    ++pos;
-    if (--tile_left > 0) {
-      if (PASS == 1) ++kt;
-      else ++rt;
-      return;
-    }
-    if (!more()) return;
-    cut_left = false;
+    left -= x1 - x0;
+    k += x1 - x0;
+    if (left <= 0) return;
     if (!last_tile) {
-      if (PASS == 1) {
-        ++rt;
-        kt = 0;
-      } else {
-        ++kt;
-        rt = first_rt(p, q, kt);
-      }
+      ++tile;
     } else {
-      loaded = rt = kt = 0;
+      tile = 0;
       if (++j == p.num_kv_heads) {
         j = 0;
         do ++s; while (!seq_at(p, s, q, false));
       }
     }
-    enter_tile();
+    enter(0);
   }
-  // The statistics' row of the tile's row-th product row.
-  __device__ __forceinline__ int64_t stat_at(int row) const {
-    const int r = rt * tq + (row >> p.group_shift);
+  // The (sequence, head) has no further tile here.
+  __device__ __forceinline__ bool head_done() const { return last_tile || left == x1 - x0; }
+  // Second pass: so few row tiles that they stay in their slots for the whole
+  // (sequence, head), else each step loads its own.
+  __device__ __forceinline__ bool keeps() const { return PASS == 2 && q.nrt <= kQSlots; }
+  // The statistics' row of row `row` of row tile rt.
+  __device__ __forceinline__ int64_t stat_at(int rt, int row) const {
+    const int r = (rt << tq_shift(p)) + (row >> p.group_shift);
     const int64_t at = p.by_query ? (int64_t)q.q_first + r : (int64_t)s * p.rows + r;
     return at * p.num_q_heads + (j << p.group_shift) + (row & (p.group - 1));
   }
-  // Last key that product row `row` of row tile rt sees; -1: no such row.
-  __device__ __forceinline__ int sees(int row) const {
-    const int r = rt * tq + (row >> p.group_shift);
+  // Last key that row `row` of row tile rt sees; -1: no such row.
+  __device__ __forceinline__ int sees(int rt, int row) const {
+    const int r = (rt << tq_shift(p)) + (row >> p.group_shift);
     return r < q.R ? q.base + r : -1;
   }
-  __device__ __forceinline__ int tile_rows() const { return min(tq, q.R - rt * tq) << p.group_shift; }
+  __device__ __forceinline__ int tile_rows(int rt) const {
+    return min(1 << tq_shift(p), q.R - (rt << tq_shift(p))) << p.group_shift;
+  }
+};
+
+// Row tiles of a (sequence, head) that have a slot (second pass, keeps()): the
+// number of the load that brought each.
+struct Kept {
+  int mask = 0, load0 = 0, load1 = 0;
+  __device__ __forceinline__ bool has(int rt) const { return mask >> rt & 1; }
+  __device__ __forceinline__ int load_of(int rt) const { return rt == 0 ? load0 : load1; }
+  __device__ __forceinline__ void put(int rt, int load) {
+    mask |= 1 << rt;
+    if (rt == 0) load0 = load;
+    else load1 = load;
+  }
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   const bool ok = mbar_wait_bounded(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
-}
-
-// Barrier of the epilogue warps; true when any thread brought pred, so that all
-// of them leave together when a wait has run out.
-__device__ __forceinline__ bool epilogue_sync_any(bool pred) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.s32 p, %2, 0;\n\t"
-      "bar.red.or.pred q, 1, %1, p;\n\t"
-      "selp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(kEpilogue), "r"(pred ? 1 : 0)
-      : "memory");
-  return r != 0;
 }
 
 // Position in a ring of n slots whose barriers alternate phases.
@@ -313,8 +257,9 @@ struct Ring {
   }
 };
 
-// All threads: the total number of steps, and where this CTA's run starts.
-__device__ void find_start(const PromptParams &p, Start *out, int64_t *warp_sums, bool tell) {
+// All threads: the CTA's run of steps.
+template <int PASS>
+__device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
   const int per = (S + kThreads - 1) / kThreads;
@@ -322,7 +267,7 @@ __device__ void find_start(const PromptParams &p, Start *out, int64_t *warp_sums
   int64_t local = 0;
   for (int s = s0; s < s1; ++s) {
     Seq q;
-    if (seq_at(p, s, q, tell)) local += steps_of(p, q) * p.num_kv_heads;
+    if (seq_at(p, s, q, tell)) local += (int64_t)steps_of_keys(p, q, q.nkt) * p.num_kv_heads;
   }
   int64_t incl = local;
 #pragma unroll
@@ -330,34 +275,62 @@ __device__ void find_start(const PromptParams &p, Start *out, int64_t *warp_sums
     const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) warp_sums[warp] = incl;
+  if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int64_t before = incl - local, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
   }
-  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
-  const int64_t begin = min(run * blockIdx.x, total), end = min(begin + run, total);
+  const int64_t most = total + gridDim.x - 1;
+  const int64_t steps = most <= 0xFFFFFFFFll ? (int64_t)((uint32_t)most / gridDim.x)
+                                             : most / gridDim.x;
+  const int64_t begin = steps * blockIdx.x;
   if (tid == 0) {
     out->begin = begin;
-    out->end = end;
-    out->run = run;
+    out->steps = steps;
+    out->left = begin < total ? min(steps, total - begin) : 0;
   }
-  if (begin < end && before <= begin && begin < before + local) {
+  if (begin < total && before <= begin && begin < before + local) {
     for (int s = s0; s < s1; ++s) {
       Seq q;
       if (!seq_at(p, s, q, false)) continue;
-      const int64_t n = steps_of(p, q) * p.num_kv_heads;
+      const int64_t n = (int64_t)steps_of_keys(p, q, q.nkt) * p.num_kv_heads;
       if (begin < before + n) {
         out->s = s;
-        out->offset = begin - before;
+        scratch[kThreads / 32] = begin - before;
         break;
       }
       before += n;
     }
   }
   __syncthreads();
+  if (warp == 0 && begin < total) {
+    // The head, and in it the last tile that starts at or before the run's
+    // first step: 32 candidates at a time.
+    Seq q;
+    seq_at(p, out->s, q, false);
+    const int64_t offset = scratch[kThreads / 32];
+    const int each = steps_of_keys(p, q, q.nkt);
+    const int j = offset <= 0xFFFFFFFFll ? (int)((uint32_t)offset / (uint32_t)each)
+                                         : (int)(offset / each);
+    const int at = (int)(offset - (int64_t)j * each);
+    int lo = 0, hi = PASS == 1 ? q.nrt : q.nkt;  // in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5;
+      const int x = lo + lane * step;
+      const bool starts =
+          x < hi && (PASS == 1 ? steps_of_rows(p, q, x) : steps_of_keys(p, q, x)) <= at;
+      const int n = __popc(__ballot_sync(0xffffffffu, starts));  // (lane 0 always does)
+      hi = min(hi, lo + n * step);
+      lo += (n - 1) * step;
+    }
+    if (lane == 0) {
+      out->j = j;
+      out->tile = lo;
+      out->in = at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo));
+    }
+  }
 }
 
 template <int D, int PASS>
@@ -367,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<D>;
   constexpr int XR = D / 64;  // 128-byte regions across D
   constexpr int kKSlots = L::kKSlots;
+  static_assert(kQSlots == 2 && kBufs == 4, "slots by the low bits of a count");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -379,25 +353,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *k_empty = k_full + kKSlots;
   uint64_t *s_full = k_empty + kKSlots;
   uint64_t *s_empty = s_full + kBufs;
-  uint64_t *drain = s_empty + kBufs;
+  uint64_t *x_full = s_empty + kBufs;
+  uint64_t *x_empty = x_full + 8;
+  uint64_t *drain = x_empty + 8;
   float *stat = reinterpret_cast<float *>(smem + L::stat);
-  int *qpos = reinterpret_cast<int *>(smem + L::qpos);
-  float *red = reinterpret_cast<float *>(smem + L::red);
+  float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
-  volatile int *last_flag = reinterpret_cast<volatile int *>(smem + L::misc + 8);
-  Start *start = reinterpret_cast<Start *>(smem + L::misc + 16);
-  int64_t *warp_sums = reinterpret_cast<int64_t *>(smem + L::misc + 64);
-  static_assert(sizeof(Start) <= 48 && 64 + kThreads / 32 * 8 <= 256, "");
+  Run *run = reinterpret_cast<Run *>(smem + L::misc + 16);
+  int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 64);
+  static_assert(sizeof(Run) <= 48 && 64 + (kThreads / 32 + 1) * 8 <= 256, "");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&st_full[i], 64);
-      mbar_init(&st_empty[i], kEpilogue / 32);
+      mbar_init(&st_empty[i], 8);
     }
     for (int i = 0; i < kKSlots; ++i) {
       mbar_init(&k_full[i], 1);
@@ -407,17 +381,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_empty[i], 1);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_k);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(tmem_slot, kBufs * kTile);
     tmem_relinquish();
   }
-  find_start(p, start, warp_sums, PASS == 1 && blockIdx.x == 0);
+  find_run<PASS>(p, run, scratch, PASS == 1 && blockIdx.x == 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -425,118 +404,143 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (PASS == 1) {
     // This pass is alone on the stream until it lets the second one start: it
     // clears that one's counters (and the second pass clears this one's).
-    if (threadIdx.x == 0) p.tickets[kMaxCtas + blockIdx.x] = 0;
+    if (threadIdx.x < 4) p.tickets[(kMaxCtas + blockIdx.x) * 4 + threadIdx.x] = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 
-  // Every role walks the same steps.  A K tile stays while the key tile does; a
-  // Q tile for its row tile (first pass), for one step, or, where all row tiles
-  // of a sequence fit the slots, for the whole (sequence, head).
+  // Every role walks the same run.  First pass: a Q tile per tile, a K tile per
+  // step.  Second pass: a K tile per tile, a Q tile per step or, where all row
+  // tiles of a sequence fit the slots, one load of each per (sequence, head).
+  // Slots, buffers and their phases follow from counts: the n-th Q load is in
+  // slot n & 1, step k of the run in buffer k & 3.
   if (warp == 0) {
     // ---- loads ----
     if (lane == 0) {
-      Ring rq, rk;
-      int q_loads = 0, k_loads = 0;
+      Ring rk;
+      int k_loads = 0, q_loads = 0;
       bool ok = true;
-      int kt_in = -1;
-      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
-        const bool load_q = PASS == 1 ? kt_in < 0 : !(w.keeps() && (w.loaded >> w.rt & 1));
-        if (PASS == 1 || kt_in < 0) {
-          ok = mbar_wait_bounded(&k_empty[rk.slot], rk.phase ^ 1, abort_flag);
-          if (!ok) break;
+      const uint32_t in_block = (1u << p.block_shift) - 1;
+      Kept kept;
+      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
+        const int32_t *bt = p.block_tables + (int64_t)w.s * p.max_blocks_per_seq;
+        auto load_k = [&](int kt) -> bool {
+          // (a tile's second half may lie past the keys: it reads the first half's block, unused)
+          const int at0 = kt * kTile, at1 = at0 + 64 < w.q.len_k ? at0 + 64 : at0;
+          int blk0 = bt[at0 >> p.block_shift], blk1 = bt[at1 >> p.block_shift];
+          if (blk0 < 0 || blk0 >= p.num_blocks || blk1 < 0 || blk1 >= p.num_blocks) {
+            flag_status(p.status, PKV_DEV_BAD_BLOCK);
+            if (blk0 < 0 || blk0 >= p.num_blocks) blk0 = 0;
+            if (blk1 < 0 || blk1 >= p.num_blocks) blk1 = 0;
+          }
+          if (!mbar_wait_bounded(&k_empty[rk.slot], rk.phase ^ 1, abort_flag)) return false;
           uint8_t *kd = sK + rk.slot * L::kTileBytes;
           mbar_arrive_expect_tx(&k_full[rk.slot], L::kTileBytes);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // (a tile's second half may lie past the keys: it reads the first half's block, unused)
-            int at = w.kt * kTile + half * 64;
-            if (at >= w.q.len_k) at = w.kt * kTile;
-            int blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (at >> p.block_shift)];
-            if (blk < 0 || blk >= p.num_blocks) {
-              flag_status(p.status, PKV_DEV_BAD_BLOCK);
-              blk = 0;
-            }
-#pragma unroll
-            for (int x = 0; x < XR; ++x)
-              tma_load_4d(kd + x * kTile * 128 + half * 64 * 128, &tm_k, &k_full[rk.slot], x * 64,
-                          w.j, at & ((1 << p.block_shift) - 1), blk);
+          for (int x = 0; x < XR; ++x) {
+            tma_load_4d(kd + x * kTile * 128, &tm_k, &k_full[rk.slot], x * 64, w.j, at0 & in_block,
+                        blk0);
+            tma_load_4d(kd + x * kTile * 128 + 64 * 128, &tm_k, &k_full[rk.slot], x * 64, w.j,
+                        at1 & in_block, blk1);
           }
           ++k_loads;
           rk.next(kKSlots);
-        }
-        if (load_q) {
-          ok = mbar_wait_bounded(&q_empty[rq.slot], rq.phase ^ 1, abort_flag);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&q_full[rq.slot], L::kTileBytes);
+          return true;
+        };
+        auto load_q = [&](int rt) -> bool {
+          const int slot = q_loads & 1;
+          if (!mbar_wait_bounded(&q_empty[slot], ((q_loads >> 1) & 1) ^ 1, abort_flag)) return false;
+          mbar_arrive_expect_tx(&q_full[slot], L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < XR; ++x)
-            tma_load_3d(sQ + rq.slot * L::kTileBytes + x * kTile * 128, &tm_q, &q_full[rq.slot],
-                        x * 64, w.j << p.group_shift, w.q.q_first + w.rt * w.tq);
+            tma_load_3d(sQ + slot * L::kTileBytes + x * kTile * 128, &tm_q, &q_full[slot], x * 64,
+                        w.j << p.group_shift, w.q.q_first + (rt << tq_shift(p)));
           ++q_loads;
-          rq.next(kQSlots);
-          if (w.keeps()) w.loaded |= 1 << w.rt;
+          return true;
+        };
+        if (PASS == 1) {
+          ok = load_q(w.tile);
+          for (int x = w.x0; ok && x < w.x1; ++x) ok = load_k(x);
+        } else {
+          ok = load_k(w.tile);
+          const bool keeps = w.keeps();
+          for (int x = w.x0; ok && x < w.x1; ++x) {
+            if (keeps && kept.has(x)) continue;
+            if (keeps) kept.put(x, q_loads);
+            ok = load_q(x);
+          }
+          if (w.head_done()) kept.mask = 0;
         }
-        kt_in = w.last_here() ? -1 : w.kt;  // (>= 0: the tile goes on)
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
       for (int i = max(0, k_loads - kKSlots); i < k_loads; ++i)
         if (!mbar_wait_bounded(&k_full[i % kKSlots], (i / kKSlots) & 1, nullptr))
           flag_status(p.status, PKV_DEV_TIMEOUT);
       for (int i = max(0, q_loads - kQSlots); i < q_loads; ++i)
-        if (!mbar_wait_bounded(&q_full[i % kQSlots], (i / kQSlots) & 1, nullptr))
+        if (!mbar_wait_bounded(&q_full[i & 1], (i >> 1) & 1, nullptr))
           flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else if (warp == 1) {
     // ---- products ----
     if (lane == 0) {
-      Ring rq, rk, rs;
+      Ring rk;
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
-      bool ok = true, fresh = true;
-      int qslot = 0, kslot = 0, slot0 = 0, slot1 = 0;
-      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
-        const bool keeps = w.keeps();
-        const bool load_q = PASS == 1 ? fresh : !(keeps && (w.loaded >> w.rt & 1));
-        if (PASS == 1 || fresh) {
-          ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
-          kslot = rk.slot;
-          rk.next(kKSlots);
-        }
-        if (ok && load_q) {
-          ok = mbar_wait_bounded(&q_full[rq.slot], rq.phase, abort_flag);
-          qslot = rq.slot;
-          rq.next(kQSlots);
-          if (keeps) {
-            w.loaded |= 1 << w.rt;
-            if (w.rt == 0) slot0 = qslot;
-            else slot1 = qslot;
-          }
-        } else if (keeps) {
-          qslot = w.rt == 0 ? slot0 : slot1;
-        }
-        if (ok) ok = mbar_wait_bounded(&s_empty[rs.slot], rs.phase ^ 1, abort_flag);
-        if (!ok) break;
+      bool ok = true;
+      int q_loads = 0;
+      Kept kept;
+      // The product of a Q slot and a K slot into the buffer of step k.
+      auto product = [&](int qslot, int kslot, int k, uint32_t idesc) -> bool {
+        if (!mbar_wait_bounded(&s_empty[k & 3], ((k >> 2) & 1) ^ 1, abort_flag)) return false;
         tc_fence_after_sync();
         const uint64_t a = dq + (uint64_t)((qslot * L::kTileBytes) >> 4);
         const uint64_t b = dk + (uint64_t)((kslot * L::kTileBytes) >> 4);
-        // (second pass: no more columns than the row tile has rows, to 16)
-        const uint32_t idesc = PASS == 1
-                                   ? umma_idesc_bf16(kTile, kTile, false, false)
-                                   : umma_idesc_bf16(kTile, (w.tile_rows() + 15) & ~15, false, false);
+        const uint32_t d = tmem + (k & 3) * kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk / 4) * kTile * 128 + (kk & 3) * 32) >> 4);
-          umma_bf16(tmem + rs.slot * kTile, PASS == 1 ? a + off : b + off,
-                    PASS == 1 ? b + off : a + off, idesc, kk > 0 ? 1u : 0u);
+          umma_bf16(d, PASS == 1 ? a + off : b + off, PASS == 1 ? b + off : a + off, idesc,
+                    kk > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[rs.slot]);
-        rs.next(kBufs);
-        fresh = w.last_here();
-        if (PASS == 1 || fresh) umma_commit(&k_empty[kslot]);
-        if (PASS == 1 ? fresh : !keeps) umma_commit(&q_empty[qslot]);
-        if (keeps && w.head_done()) {
-          if (w.loaded & 1) umma_commit(&q_empty[slot0]);
-          if (w.loaded & 2) umma_commit(&q_empty[slot1]);
+        umma_commit(&s_full[k & 3]);
+        return true;
+      };
+      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
+        if (PASS == 1) {
+          ok = mbar_wait_bounded(&q_full[q_loads & 1], (q_loads >> 1) & 1, abort_flag);
+          int k = (int)w.k;  // (its low bits count)
+          for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
+            ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
+                 product(q_loads & 1, rk.slot, k, umma_idesc_bf16(kTile, kTile, false, false));
+            if (ok) umma_commit(&k_empty[rk.slot]);
+            rk.next(kKSlots);
+          }
+          if (ok) umma_commit(&q_empty[q_loads & 1]);
+          ++q_loads;
+        } else {
+          const bool keeps = w.keeps();
+          ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
+          int k = (int)w.k;  // (its low bits count)
+          for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
+            int load = q_loads;
+            if (keeps && kept.has(x)) {
+              load = kept.load_of(x);
+            } else {
+              ok = mbar_wait_bounded(&q_full[load & 1], (load >> 1) & 1, abort_flag);
+              if (keeps) kept.put(x, load);
+              ++q_loads;
+            }
+            // (no more columns than the row tile has rows, to 16)
+            ok = ok && product(load & 1, rk.slot, k,
+                               umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false));
+            if (ok && !keeps) umma_commit(&q_empty[load & 1]);
+          }
+          if (ok) umma_commit(&k_empty[rk.slot]);
+          rk.next(kKSlots);
+          if (w.head_done()) {
+            if (ok && keeps && kept.has(0)) umma_commit(&q_empty[kept.load0 & 1]);
+            if (ok && keeps && kept.has(1)) umma_commit(&q_empty[kept.load1 & 1]);
+            kept.mask = 0;
+          }
         }
       }
       // Wait for the products before tensor memory is freed.
@@ -547,211 +551,233 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- second pass: the rows' denominators, beside their Q tiles ----
     if (PASS == 2) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (threadIdx.x == 64) p.tickets[blockIdx.x] = 0;
-      Ring r;
-      for (Walk<PASS> w(p, *start); w.more(); w.next()) {
+      if (threadIdx.x >= 64 && threadIdx.x < 68)
+        p.tickets[blockIdx.x * 4 + (threadIdx.x - 64)] = 0;
+      int q_loads = 0;
+      bool ok = true;
+      Kept kept;
+      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
         const bool keeps = w.keeps();
-        if (keeps && (w.loaded >> w.rt & 1)) continue;
-        if (!warp_wait(&st_empty[r.slot], r.phase ^ 1, abort_flag)) break;
+        for (int x = w.x0; x < w.x1; ++x) {
+          if (keeps && kept.has(x)) continue;
+          if (keeps) kept.put(x, q_loads);
+          float neg[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int row = (warp - 2) * 64 + x * 32 + lane;
-          const int last = w.sees(row);
-          stat[r.slot * kTile + row] = last >= 0 ? __ldcg(p.neg_lse + w.stat_at(row)) : 0.f;
-          qpos[r.slot * kTile + row] = last;
+          for (int i = 0; i < 2; ++i) {
+            const int row = (warp - 2) * 64 + i * 32 + lane;
+            neg[i] = w.sees(x, row) >= 0 ? __ldcg(p.neg_lse + w.stat_at(x, row)) : -INFINITY;
+          }
+          const int slot = q_loads & 1;
+          ok = warp_wait(&st_empty[slot], ((q_loads >> 1) & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          stat[slot * kTile + (warp - 2) * 64 + lane] = neg[0];
+          stat[slot * kTile + (warp - 2) * 64 + 32 + lane] = neg[1];
+          mbar_arrive(&st_full[slot]);
+          ++q_loads;
         }
-        mbar_arrive(&st_full[r.slot]);
-        r.next(kQSlots);
-        if (keeps) w.loaded |= 1 << w.rt;
+        if (w.head_done()) kept.mask = 0;
       }
     }
   } else {
-    // ---- exponentials and sums: two groups of four warps take the steps in turn ----
+    // ---- exponentials and sums: two groups of four warps ----
+    // They take the steps in turn or, where a tile has few (second pass, row
+    // tiles that stay in their slots), the tiles.
     const int quarter = warp & 3;
-    const int side = (warp - 4) >> 2;     // the group
+    const int side = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;  // the thread's lane of tensor memory
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16);
     const float qs = p.qscale;
     const float2 qs2 = make_float2(qs, qs);
-    Ring rs, rst;
     bool ok = true;
-    int parity = 0;  // of the exchange buffers
-    int turn = 0;    // the group whose step it is
-    float m = -INFINITY, l = 0.f;        // first pass: the row's maximum and sum, of this group's steps
-    float2 acc = make_float2(0.f, 0.f);  // second pass: the key's sum, of this group's steps
-    int sslot = 0, slot0 = 0, slot1 = 0;
-    for (Walk<PASS> w(p, *start); w.more(); w.next()) {
-      const bool mine_now = turn == side;
-      turn ^= 1;
+    int q_loads = 0, swaps = 0;
+    Kept kept;
+    auto wait_product = [&](int k) -> bool {
+      if (!warp_wait(&s_full[k & 3], (k >> 2) & 1, abort_flag)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    auto release_product = [&](int k) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[k & 3]);
+    };
+    auto join = [&](float2 a, float2 b) -> float2 {
+      if (PASS == 2) return make_float2(0.f, a.y + b.y);
+      const float mn = fmaxf(a.x, b.x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      return make_float2(mn, a.y * fast_exp2(a.x - ref) + b.y * fast_exp2(b.x - ref));
+    };
+    for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
+      // (maximum, sum) of the row, or (-, sum) of the key, over this thread's steps.
+      float2 mine = make_float2(PASS == 1 ? -INFINITY : 0.f, 0.f);
       const bool keeps = w.keeps();
-      if (PASS == 2) {
-        if (!(keeps && (w.loaded >> w.rt & 1))) {
-          ok = warp_wait(&st_full[rst.slot], rst.phase, abort_flag);
-          sslot = rst.slot;
-          rst.next(kQSlots);
-          if (keeps) {
-            w.loaded |= 1 << w.rt;
-            if (w.rt == 0) slot0 = sslot;
-            else slot1 = sslot;
-          }
-        } else {
-          sslot = w.rt == 0 ? slot0 : slot1;
-        }
-      }
-      if (ok && mine_now) ok = warp_wait(&s_full[rs.slot], rs.phase, abort_flag);
-      if (ok && mine_now) {
-        tc_fence_after_sync();
-        const uint32_t ta = tmem + lane_base + rs.slot * kTile;
-        if (PASS == 1) {
-          const int last = w.sees(row);
-          if (__any_sync(0xffffffffu, last >= 0)) {
+      bool owner = true;  // of the tile, alone
+      if (PASS == 1) {
+        const int last = w.sees(w.tile, row);
+        const int odd = ((int)w.k ^ side) & 1;
+        int k = (int)w.k + odd;
+        for (int x = w.x0 + odd; x < w.x1; x += 2, k += 2) {
+          ok = wait_product(k);
+          if (!ok) break;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kTile; c0 += 64) {
-              float v[64];
-              float top;
-              tmem_load64_max(ta + c0, v, top);
-              const int key0 = w.kt * kTile + c0;
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-              float mn, ref;
-              // Keys past the row's position are hidden; a negative scale makes
-              // the smallest product the largest logit.
-              if (qs < 0.f || !__all_sync(0xffffffffu, key0 + 63 <= last)) {
-                top = -INFINITY;
+          for (int c0 = 0; c0 < kTile; c0 += 64) {
+            const int key0 = x * kTile + c0;
+            if (!__any_sync(0xffffffffu, key0 <= last)) break;  // (hidden from all 32 rows)
+            float v[64];
+            float top;
+            tmem_load64_max(ta + (k & 3) * kTile + c0, v, top);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float mn, ref;
+            if (qs > 0.f && __all_sync(0xffffffffu, key0 + 63 <= last)) {
+              mn = fmaxf(mine.x, top * qs);
+              ref = mn == -INFINITY ? 0.f : mn;
+              const float2 nref = make_float2(-ref, -ref);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                  v[i] = key0 + i <= last ? v[i] * qs : -INFINITY;
-                  top = fmaxf(top, v[i]);
-                }
-                mn = fmaxf(m, top);
-                ref = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-                for (int i = 0; i < 64; i += 2)
-                  sum[(i >> 1) & 1] = __fadd2_rn(
-                      sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
-              } else {
-                mn = fmaxf(m, top * qs);
-                ref = mn == -INFINITY ? 0.f : mn;
-                const float2 nref = make_float2(-ref, -ref);
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                  const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
-                  sum[(i >> 1) & 1] =
-                      __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
-                }
+              for (int i = 0; i < 64; i += 2) {
+                const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
+                sum[(i >> 1) & 1] =
+                    __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
               }
-              l = l * fast_exp2(m - ref) + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-              m = mn;
+            } else {
+              // Keys past the row's position are hidden; a scale that is not
+              // positive puts the largest logit elsewhere.
+              top = -INFINITY;
+              const int shown = last - key0;
+#pragma unroll
+              for (int i = 0; i < 64; ++i) {
+                v[i] = i <= shown ? v[i] * qs : -INFINITY;
+                top = fmaxf(top, v[i]);
+              }
+              mn = fmaxf(mine.x, top);
+              ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+              for (int i = 0; i < 64; i += 2)
+                sum[(i >> 1) & 1] = __fadd2_rn(
+                    sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
             }
+            mine.y = mine.y * fast_exp2(mine.x - ref) +
+                     ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+            mine.x = mn;
           }
-        } else {
-          const int key = w.kt * kTile + row;
-          const int rows = w.tile_rows();
+          release_product(k);
+        }
+      } else {
+        const int key = w.tile * kTile + row;
+        const bool by_tile = keeps;
+        owner = !by_tile || (w.tile & 1) == side;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        const int odd = by_tile ? 0 : ((int)w.k ^ side) & 1;
+        if (by_tile) {
+          for (int x = w.x0; x < w.x1; ++x)
+            if (!kept.has(x)) kept.put(x, q_loads++);
+        }
+        int k = (int)w.k + odd;
+        for (int x = w.x0 + odd; owner && x < w.x1; x += by_tile ? 1 : 2, k += by_tile ? 1 : 2) {
+          const int load = by_tile ? kept.load_of(x) : q_loads + (x - w.x0);
+          ok = warp_wait(&st_full[load & 1], (load >> 1) & 1, abort_flag) && wait_product(k);
+          if (!ok) break;
+          const int rows = w.tile_rows(x);
+          // Columns of this key's weights: from its first row that sees it on.
+          const int first = (key - w.q.base - (x << tq_shift(p))) * p.group;
           // Every row of the tile sees every key of the tile.
-          const bool open = w.kt * kTile + kTile - 1 <= w.q.base + w.rt * w.tq;
+          const bool open = w.tile * kTile + kTile - 1 <= w.q.base + (x << tq_shift(p));
 #pragma unroll 1
           for (int c0 = 0; c0 < rows; c0 += 32) {
             float v[32];
-            tmem_load32(ta + c0, v);
-            const float4 *ns = reinterpret_cast<const float4 *>(stat + sslot * kTile + c0);
+            tmem_load32(ta + (k & 3) * kTile + c0, v);
+            const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 1) * kTile + c0);
             if (open && c0 + 32 <= rows) {
-              float2 more = make_float2(0.f, 0.f);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 n = ns[i / 4];
                 const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
-                const float2 z1 = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
-                acc = __fadd2_rn(acc, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
-                more = __fadd2_rn(more, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+                const float2 z1 =
+                    __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
+                acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+                acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
               }
-              acc = __fadd2_rn(acc, more);
             } else {
-              const int4 *qp = reinterpret_cast<const int4 *>(qpos + sslot * kTile + c0);
+              const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 n = ns[i / 4];
-                const int4 last = qp[i / 4];
-                acc.x += key <= last.x ? fast_exp2(fmaf(v[i], qs, n.x)) : 0.f;
-                acc.y += key <= last.y ? fast_exp2(fmaf(v[i + 1], qs, n.y)) : 0.f;
-                acc.x += key <= last.z ? fast_exp2(fmaf(v[i + 2], qs, n.z)) : 0.f;
-                acc.y += key <= last.w ? fast_exp2(fmaf(v[i + 3], qs, n.w)) : 0.f;
+                const float e0 = fast_exp2(fmaf(v[i], qs, n.x)), e1 = fast_exp2(fmaf(v[i + 1], qs, n.y));
+                const float e2 = fast_exp2(fmaf(v[i + 2], qs, n.z)), e3 = fast_exp2(fmaf(v[i + 3], qs, n.w));
+                acc0.x += (unsigned)(i - lo) < (unsigned)n_in ? e0 : 0.f;
+                acc0.y += (unsigned)(i + 1 - lo) < (unsigned)n_in ? e1 : 0.f;
+                acc1.x += (unsigned)(i + 2 - lo) < (unsigned)n_in ? e2 : 0.f;
+                acc1.y += (unsigned)(i + 3 - lo) < (unsigned)n_in ? e3 : 0.f;
               }
             }
           }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[rs.slot]);
-      }
-      rs.next(kBufs);
-      // (both groups release a row tile's denominators, each after its last use)
-      if (PASS == 2 && ok) {
-        __syncwarp();
-        if (lane == 0) {
-          if (!keeps) {
-            mbar_arrive(&st_empty[sslot]);
-          } else if (w.head_done()) {
-            if (w.loaded & 1) mbar_arrive(&st_empty[slot0]);
-            if (w.loaded & 2) mbar_arrive(&st_empty[slot1]);
+          release_product(k);
+          // (this group alone used the step's denominators: both groups' arrivals are its own)
+          if (!by_tile && lane == 0) {
+            mbar_arrive(&st_empty[load & 1]);
+            mbar_arrive(&st_empty[load & 1]);
           }
         }
+        mine.y = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        if (!by_tile) {
+          q_loads += w.x1 - w.x0;
+        } else if (w.head_done()) {
+          // Both groups release the kept rows, once they are there at all.
+          for (int x = 0; ok && x < kQSlots; ++x) {
+            if (!kept.has(x)) continue;
+            const int load = kept.load_of(x);
+            ok = warp_wait(&st_full[load & 1], (load >> 1) & 1, abort_flag);
+            if (ok && lane == 0) mbar_arrive(&st_empty[load & 1]);
+          }
+          kept.mask = 0;
+        }
+        if (ok && !owner) continue;
       }
-      if (ok && !w.last_here()) continue;
+      if (!ok) break;
 
-      // The tile ends here (or a wait ran out: then all eight warps meet and
-      // leave).  The groups' sums are joined by the first group's threads.
-      float *ex = red + parity * 2 * kTile;
-      parity ^= 1;
-      if (side == 1) {
-        ex[row] = PASS == 1 ? m : acc.x + acc.y;
-        if (PASS == 1) ex[kTile + row] = l;
-      }
-      if (epilogue_sync_any(!ok)) break;
-      float2 mine = make_float2(0.f, 0.f);  // (maximum, sum), or (-, sum)
-      auto join = [&](float2 x) {
-        if (PASS == 1) {
-          const float mn = fmaxf(mine.x, x.x);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          mine.y = mine.y * fast_exp2(mine.x - ref) + x.y * fast_exp2(x.x - ref);
-          mine.x = mn;
-        } else {
-          mine.y += x.y;
+      // The tile ends here.  Steps taken in turn: the first group gets the
+      // second one's part, warp from warp.
+      if (!keeps) {
+        const int buf = swaps & 1, bar = quarter * 2 + buf;
+        const uint32_t phase = (swaps >> 1) & 1;
+        ++swaps;
+        if (side == 1) {
+          ok = warp_wait(&x_empty[bar], phase ^ 1, abort_flag);
+          if (!ok) break;
+          ex[buf * kTile + row] = mine;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&x_full[bar]);
+          continue;
         }
-      };
-      if (side == 0) {
-        mine = PASS == 1 ? make_float2(m, l) : make_float2(0.f, acc.x + acc.y);
-        join(PASS == 1 ? make_float2(ex[row], ex[kTile + row]) : make_float2(0.f, ex[row]));
+        ok = warp_wait(&x_full[bar], phase, abort_flag);
+        if (!ok) break;
+        mine = join(mine, ex[buf * kTile + row]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_empty[bar]);
       }
-      m = -INFINITY;
-      l = 0.f;
-      acc = make_float2(0.f, 0.f);
-      bool finish = true;
-      if (w.cut_left || !w.tile_done()) {
+      if (w.x0 != w.b0 || w.x1 != w.b1) {
         // A part of a tile that several CTAs share: filed by CTA, place 0 if
-        // the tile began before it, place 1 if it begins here.
-        int c0, c1;
-        w.ctas(c0, c1);
-        if (side == 0) {
-          __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (w.cut_left ? 0 : 1)) * kTile + row, mine);
+        // the tile began before it, place 1 if it begins here.  The warp that
+        // is the last to file its 32 rows joins all of them, in order.
+        const int64_t at = run->begin + w.k;
+        const int c0 = (int)((at - (w.x0 - w.b0)) / run->steps);
+        const int c1 = (int)((at + (w.b1 - w.x0) - 1) / run->steps);
+        __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (w.x0 != w.b0 ? 0 : 1)) * kTile + row, mine);
+        __threadfence();
+        __syncwarp();
+        unsigned int done = 0;
+        if (lane == 0) {
+          done = atomicAdd(&p.tickets[((PASS - 1) * kMaxCtas + c0) * 4 + quarter], 1u);
           __threadfence();
         }
-        if (epilogue_sync_any(false)) break;
-        if (threadIdx.x == 128) {
-          const unsigned int done = atomicAdd(&p.tickets[(PASS - 1) * kMaxCtas + c0], 1u);
-          *last_flag = done == (unsigned int)(c1 - c0) ? 1 : 0;
-          __threadfence();
-        }
-        if (epilogue_sync_any(false)) break;
-        finish = *last_flag != 0;
-        if (finish && side == 0) {
-          mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
-          for (int c = c0 + 1; c <= c1; ++c) join(__ldcg(p.parts + (int64_t)c * 2 * kTile + row));
-        }
+        done = __shfl_sync(0xffffffffu, done, 0);
+        if (done != (unsigned int)(c1 - c0)) continue;
+        mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
+        for (int c = c0 + 1; c <= c1; ++c) mine = join(mine, __ldcg(p.parts + (int64_t)c * 2 * kTile + row));
       }
-      if (!finish || side != 0) continue;
       if (PASS == 1) {
-        if (w.sees(row) >= 0) p.neg_lse[w.stat_at(row)] = -(mine.x + log2f(mine.y));
+        if (w.sees(w.tile, row) >= 0) p.neg_lse[w.stat_at(w.tile, row)] = -(mine.x + log2f(mine.y));
       } else {
-        const int key = w.kt * kTile + row;
+        const int key = w.tile * kTile + row;
         if (key < w.q.len_k) {
           const int blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
           if (blk >= 0 && blk < p.num_blocks) {
@@ -783,7 +809,7 @@ struct Plan {
     // Rows are filed under (sequence, rank) or, where that is more, under their query.
     by_query = rows > total_q / num_seqs;
     stat_rows = by_query ? total_q : num_seqs * rows;
-    parts = 2 * kMaxCtas * sizeof(unsigned int);
+    parts = 2 * kMaxCtas * 4 * sizeof(unsigned int);
     neg_lse = parts + (size_t)kMaxCtas * 2 * kTile * sizeof(float2);
     total = neg_lse + (size_t)(stat_rows * Hq) * sizeof(float);
   }
@@ -854,6 +880,7 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   if (G != 1 && G != 2 && G != 4 && G != 8) return PKV_ERR_UNSUPPORTED;
   if (block_size != 64 && block_size != 128 && block_size != 256 && block_size != 512)
     return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * block_size > kMaxTokens) return PKV_ERR_UNSUPPORTED;
   if (!isfinite(scale)) return PKV_ERR_INVALID_ARG;  // NaN or infinite
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (total_q > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
