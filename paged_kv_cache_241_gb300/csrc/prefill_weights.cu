@@ -24,10 +24,11 @@
 // to finish (a counter; nothing waits), from the parts in their order, so the
 // result does not depend on which one that is.
 // Both passes are the same persistent kernel: warp 0 loads tiles (TMA, 128-byte
-// swizzle, through the block table), warp 1 issues tcgen05.mma into four
-// 128-column buffers of tensor memory, warps 2 and 3 fetch the rows'
-// denominators (second pass), warps 4-11 exponentiate and sum.  Loads, products
-// and exponentials of different steps overlap.
+// swizzle, through the block table), warps 1 and 2 issue tcgen05.mma in turn (one
+// fills the queue while the other waits for its operands) into four 128-column
+// buffers of tensor memory, warp 3 fetches the rows' denominators (second pass),
+// warps 4-19 exponentiate and sum, a group of four for each buffer.  Loads,
+// products and exponentials of different steps overlap.
 #include <math.h>
 
 #include "host_common.h"
@@ -37,9 +38,12 @@ namespace pkv {
 namespace {
 
 constexpr int kTile = 128;       // rows and keys per tile
-constexpr int kThreads = 384;
-constexpr int kBufs = 4;         // S buffers of 128 columns: all of tensor memory
-constexpr int kQSlots = 2;       // row tiles, with their denominators
+constexpr int kGroups = 4;       // of four warps: exponentials and sums
+constexpr int kIssuers = 2;
+constexpr int kThreads = 128 + kGroups * 128;
+constexpr int kBufs = kGroups;   // S buffers of 128 columns: all of tensor memory
+constexpr int kQSlots = 2;       // row tiles
+constexpr int kStatSlots = 4;    // row tiles' denominators (second pass)
 constexpr int kMaxTokens = 1 << 20;  // of a sequence (a head's steps are counted in 32 bits)
 constexpr int kMaxCtas = 512;    // places for cut tiles in the workspace (CTAs of a grid at most)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,13 +55,14 @@ struct Layout {
   static constexpr int q = 0;
   static constexpr int k = q + kQSlots * kTileBytes;
   static constexpr int bars = k + kKSlots * kTileBytes;
-  // q_full/q_empty/st_full/st_empty[Q], k_full/k_empty[K], s_full/s_empty[B],
+  // q_full/q_empty[Q], st_empty[T], k_full/k_empty[K], s_full/s_empty[B],
   // x_full/x_empty[quarter][2], drain
-  static constexpr int kNumBars = 4 * kQSlots + 2 * kKSlots + 2 * kBufs + 16 + 1;
-  static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [Q][128] -log2 denominators
-  static constexpr int ex = stat + kQSlots * kTile * 4;          // [2][128] (maximum, sum), between the groups
-  static constexpr int misc = ex + 2 * kTile * 8;  // tensor memory address, abort flag, run, scan
-  static constexpr int total = misc + 256;
+  static constexpr int kNumBars =
+      2 * kQSlots + kStatSlots + 2 * kKSlots + 2 * kBufs + 16 + 1;
+  static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [T][128] -log2 denominators
+  static constexpr int ex = stat + kStatSlots * kTile * 4;       // [2][groups - 1][128] (maximum, sum)
+  static constexpr int misc = ex + 2 * (kGroups - 1) * kTile * 8;  // tensor memory address, abort, run, scan
+  static constexpr int total = misc + 512;
   // One CTA per SM (it takes all of tensor memory): more than half of an SM's
   // shared memory, so that a second one never waits for tensor memory.
   static_assert(total + 1024 <= 232448 && total > 114 * 1024, "shared memory");
@@ -151,8 +156,9 @@ __device__ __forceinline__ int steps_of_keys(const PromptParams &p, const Seq &q
 // Where a CTA's run of steps starts.
 struct Run {
   int64_t begin, steps;  // first step of the call's, steps per CTA
-  int64_t left;          // steps to do
+  int left;              // steps to do
   int s, j, tile, in;    // sequence, head, tile, and steps of that tile before `begin`
+  Seq q;                 // that sequence
 };
 
 // A role's walk over its CTA's run, tile by tile: row tiles in the first pass,
@@ -164,7 +170,7 @@ struct Walk {
   int s, j, tile;
   int b0, b1;      // the tile's steps
   int x0, x1;      // those of them that are here
-  int64_t k, left; // number of step x0 in the CTA's run; steps to do from x0 on
+  int k, left;     // number of step x0 in the CTA's run; steps to do from x0 on
   bool last_tile;  // of the (sequence, head)
 
   __device__ __forceinline__ Walk(const PromptParams &prm, const Run &run) : p(prm) {
@@ -174,7 +180,7 @@ struct Walk {
     s = run.s;
     j = run.j;
     tile = run.tile;
-    seq_at(p, s, q, false);
+    q = run.q;
     enter(run.in);
   }
   __device__ __forceinline__ void enter(int in) {
@@ -188,7 +194,7 @@ struct Walk {
       last_tile = tile + 1 == q.nkt;
     }
     x0 = b0 + in;
-    x1 = (int)min((int64_t)b1, x0 + left);
+    x1 = min(b1, x0 + left);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next() {
@@ -245,6 +251,56 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// Arrive n times at once.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
+}
+
+// Load 32 consecutive fp32 columns of this thread's lane of tensor memory with
+// their maximum (NaN ignored), and wait for them.
+__device__ __forceinline__ void tmem_load32_max(uint32_t taddr, float (&v)[32], float &vmax) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(vmax)
+      : "r"(taddr)
+      : "memory");
+}
+
+// A count in shared memory that one warp raises and others wait for.
+__device__ __forceinline__ void count_set(int *count, int n) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
+}
+__device__ __forceinline__ int count_get(const int *count) {
+  int n;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
+  return n;
+}
+// Whole warp: wait until the count has passed n, as long as a barrier's wait may last.
+__device__ __forceinline__ bool count_wait(const int *count, int n, volatile int *abort) {
+  bool ok = true;
+  if (count_get(count) - n <= 0) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; ok && count_get(count) - n <= 0; ++i) {
+      if ((i & 15u) == 0) {
+        if (*abort) ok = false;
+        else if (global_timer_ns() - t0 > g_wait_limit_ns) {
+          *abort = 1;
+          ok = false;
+        }
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Position in a ring of n slots whose barriers alternate phases.
 struct Ring {
   int slot = 0;
@@ -262,12 +318,17 @@ template <int PASS>
 __device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
-  const int per = (S + kThreads - 1) / kThreads;
+  const int per = (S + kThreads - 1) / kThreads;  // (one, for batches up to kThreads)
   const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
   int64_t local = 0;
+  int each = 0;
+  Seq q;
   for (int s = s0; s < s1; ++s) {
-    Seq q;
-    if (seq_at(p, s, q, tell)) local += (int64_t)steps_of_keys(p, q, q.nkt) * p.num_kv_heads;
+    each = 0;
+    if (seq_at(p, s, q, tell)) {
+      each = steps_of_keys(p, q, q.nkt);
+      local += (int64_t)each * p.num_kv_heads;
+    }
   }
   int64_t incl = local;
 #pragma unroll
@@ -278,43 +339,48 @@ __device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int64_t before = incl - local, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+    const int64_t x = scratch[w];
+    if (w < warp) before += x;
+    total += x;
   }
   const int64_t most = total + gridDim.x - 1;
   const int64_t steps = most <= 0xFFFFFFFFll ? (int64_t)((uint32_t)most / gridDim.x)
                                              : most / gridDim.x;
   const int64_t begin = steps * blockIdx.x;
+  // (2^31 steps of one CTA, tens of minutes, are no batch: refused)
+  const bool some = begin < total && steps <= 0x7FFFFFFFll;
   if (tid == 0) {
     out->begin = begin;
     out->steps = steps;
-    out->left = begin < total ? min(steps, total - begin) : 0;
+    out->left = some ? (int)min(steps, total - begin) : 0;
+    if (steps > 0x7FFFFFFFll) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
   }
-  if (begin < total && before <= begin && begin < before + local) {
-    for (int s = s0; s < s1; ++s) {
-      Seq q;
-      if (!seq_at(p, s, q, false)) continue;
-      const int64_t n = (int64_t)steps_of_keys(p, q, q.nkt) * p.num_kv_heads;
-      if (begin < before + n) {
-        out->s = s;
-        scratch[kThreads / 32] = begin - before;
-        break;
+  if (some && before <= begin && begin < before + local) {
+    int s = s0;
+    if (per > 1) {
+      for (; s < s1; ++s) {
+        if (!seq_at(p, s, q, false)) continue;
+        each = steps_of_keys(p, q, q.nkt);
+        if (begin < before + (int64_t)each * p.num_kv_heads) break;
+        before += (int64_t)each * p.num_kv_heads;
       }
-      before += n;
     }
-  }
-  __syncthreads();
-  if (warp == 0 && begin < total) {
-    // The head, and in it the last tile that starts at or before the run's
-    // first step: 32 candidates at a time.
-    Seq q;
-    seq_at(p, out->s, q, false);
-    const int64_t offset = scratch[kThreads / 32];
-    const int each = steps_of_keys(p, q, q.nkt);
+    const int64_t offset = begin - before;
     const int j = offset <= 0xFFFFFFFFll ? (int)((uint32_t)offset / (uint32_t)each)
                                          : (int)(offset / each);
-    const int at = (int)(offset - (int64_t)j * each);
+    out->s = s;
+    out->j = j;
+    out->in = (int)(offset - (int64_t)j * each);  // (steps of the head, until the tile is found)
+    out->q = q;
+  }
+  __syncthreads();
+  if (warp == 0 && some) {
+    // The last tile that starts at or before the run's first step: 32
+    // candidates at a time.
+    q = out->q;
+    const int at = out->in;
     int lo = 0, hi = PASS == 1 ? q.nrt : q.nkt;  // in [lo, hi)
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) >> 5;
@@ -326,7 +392,6 @@ __device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool
       lo += (n - 1) * step;
     }
     if (lane == 0) {
-      out->j = j;
       out->tile = lo;
       out->in = at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo));
     }
@@ -340,16 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<D>;
   constexpr int XR = D / 64;  // 128-byte regions across D
   constexpr int kKSlots = L::kKSlots;
-  static_assert(kQSlots == 2 && kBufs == 4, "slots by the low bits of a count");
+  static_assert(kQSlots == 2 && kStatSlots == 4 && kBufs == 4 && kIssuers == 2, "by the low bits of a count");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sQ = smem + L::q, *sK = smem + L::k;
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint64_t *q_empty = q_full + kQSlots;
-  uint64_t *st_full = q_empty + kQSlots;
-  uint64_t *st_empty = st_full + kQSlots;
-  uint64_t *k_full = st_empty + kQSlots;
+  uint64_t *st_empty = q_empty + kQSlots;
+  uint64_t *k_full = st_empty + kStatSlots;
   uint64_t *k_empty = k_full + kKSlots;
   uint64_t *s_full = k_empty + kKSlots;
   uint64_t *s_empty = s_full + kBufs;
@@ -360,33 +424,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  int *stats_in = reinterpret_cast<int *>(smem + L::misc + 8);  // row tiles whose denominators are in
   Run *run = reinterpret_cast<Run *>(smem + L::misc + 16);
-  int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 64);
-  static_assert(sizeof(Run) <= 48 && 64 + (kThreads / 32 + 1) * 8 <= 256, "");
+  int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 128);
+  static_assert(sizeof(Run) <= 112 && 128 + kThreads / 32 * 8 <= 512, "");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 32) {
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&st_full[i], 64);
-      mbar_init(&st_empty[i], 8);
+      mbar_init(&q_empty[i], kIssuers);
     }
+    for (int i = 0; i < kStatSlots; ++i) mbar_init(&st_empty[i], kGroups * 4);
     for (int i = 0; i < kKSlots; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], PASS == 1 ? 1 : kIssuers);  // (a step's own, or all of a tile's)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&x_full[i], 1);
+      mbar_init(&x_full[i], kGroups - 1);
       mbar_init(&x_empty[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, kIssuers);
     *abort_flag = 0;
+    *stats_in = 0;
     fence_barrier_init();
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_k);
@@ -411,8 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Every role walks the same run.  First pass: a Q tile per tile, a K tile per
   // step.  Second pass: a K tile per tile, a Q tile per step or, where all row
   // tiles of a sequence fit the slots, one load of each per (sequence, head).
-  // Slots, buffers and their phases follow from counts: the n-th Q load is in
-  // slot n & 1, step k of the run in buffer k & 3.
+  // A wait on a barrier tells only two phases apart, so whoever waits for a slot
+  // must see every use of it: S buffer g belongs to group g and to issuer g & 1;
+  // both issuers wait for, and release, every Q tile, and every K tile of the
+  // second pass; the denominators, which a group may skip many of, are counted.
   if (warp == 0) {
     // ---- loads ----
     if (lane == 0) {
@@ -479,39 +546,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(&q_full[i & 1], (i >> 1) & 1, nullptr))
           flag_status(p.status, PKV_DEV_TIMEOUT);
     }
-  } else if (warp == 1) {
-    // ---- products ----
+  } else if (warp <= kIssuers) {
+    // ---- products: the two warps take the steps in turn ----
     if (lane == 0) {
+      const int me = warp - 1;
       Ring rk;
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
       bool ok = true;
       int q_loads = 0;
       Kept kept;
-      // The product of a Q slot and a K slot into the buffer of step k.
-      auto product = [&](int qslot, int kslot, int k, uint32_t idesc) -> bool {
-        if (!mbar_wait_bounded(&s_empty[k & 3], ((k >> 2) & 1) ^ 1, abort_flag)) return false;
+      uint32_t uses = 0;  // bit g: parity of the uses of buffer g
+      // The product of a Q slot and a K slot into buffer g.
+      auto product = [&](int qslot, int kslot, int g, uint32_t idesc) -> bool {
+        if (!mbar_wait_bounded(&s_empty[g], ((uses >> g) & 1) ^ 1, abort_flag)) return false;
+        uses ^= 1u << g;
         tc_fence_after_sync();
         const uint64_t a = dq + (uint64_t)((qslot * L::kTileBytes) >> 4);
         const uint64_t b = dk + (uint64_t)((kslot * L::kTileBytes) >> 4);
-        const uint32_t d = tmem + (k & 3) * kTile;
+        const uint32_t d = tmem + g * kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk / 4) * kTile * 128 + (kk & 3) * 32) >> 4);
           umma_bf16(d, PASS == 1 ? a + off : b + off, PASS == 1 ? b + off : a + off, idesc,
                     kk > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[k & 3]);
+        umma_commit(&s_full[g]);
         return true;
       };
       for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
         if (PASS == 1) {
           ok = mbar_wait_bounded(&q_full[q_loads & 1], (q_loads >> 1) & 1, abort_flag);
-          int k = (int)w.k;  // (its low bits count)
+          int k = w.k;
           for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
-            ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
-                 product(q_loads & 1, rk.slot, k, umma_idesc_bf16(kTile, kTile, false, false));
-            if (ok) umma_commit(&k_empty[rk.slot]);
+            if ((k & 1) == me) {
+              ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
+                   product(q_loads & 1, rk.slot, k & 3, umma_idesc_bf16(kTile, kTile, false, false));
+              if (ok) umma_commit(&k_empty[rk.slot]);
+            }
             rk.next(kKSlots);
           }
           if (ok) umma_commit(&q_empty[q_loads & 1]);
@@ -519,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const bool keeps = w.keeps();
           ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
-          int k = (int)w.k;  // (its low bits count)
+          int k = w.k;
           for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
             int load = q_loads;
             if (keeps && kept.has(x)) {
@@ -529,30 +601,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (keeps) kept.put(x, load);
               ++q_loads;
             }
-            // (no more columns than the row tile has rows, to 16)
-            ok = ok && product(load & 1, rk.slot, k,
-                               umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false));
-            if (ok && !keeps) umma_commit(&q_empty[load & 1]);
+            const int g = (keeps ? w.tile : k) & 3;
+            if ((g & 1) == me) {
+              // (no more columns than the row tile has rows, to 16)
+              ok = ok && product(load & 1, rk.slot, g,
+                                 umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false));
+              if (ok && !keeps) umma_commit(&q_empty[load & 1]);
+            } else if (ok && !keeps) {
+              mbar_arrive(&q_empty[load & 1]);
+            }
           }
           if (ok) umma_commit(&k_empty[rk.slot]);
           rk.next(kKSlots);
           if (w.head_done()) {
-            if (ok && keeps && kept.has(0)) umma_commit(&q_empty[kept.load0 & 1]);
-            if (ok && keeps && kept.has(1)) umma_commit(&q_empty[kept.load1 & 1]);
+            if (ok && kept.has(0)) umma_commit(&q_empty[kept.load0 & 1]);
+            if (ok && kept.has(1)) umma_commit(&q_empty[kept.load1 & 1]);
             kept.mask = 0;
           }
         }
       }
-      // Wait for the products before tensor memory is freed.
+      // Wait for the products of both before tensor memory is freed.
       umma_commit(drain);
       if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
     }
-  } else if (warp < 4) {
-    // ---- second pass: the rows' denominators, beside their Q tiles ----
+  } else if (warp == 3) {
+    // ---- second pass: the rows' denominators ----
     if (PASS == 2) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (threadIdx.x >= 64 && threadIdx.x < 68)
-        p.tickets[blockIdx.x * 4 + (threadIdx.x - 64)] = 0;
+      if (lane < 4) p.tickets[blockIdx.x * 4 + lane] = 0;
       int q_loads = 0;
       bool ok = true;
       Kept kept;
@@ -561,45 +637,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = w.x0; x < w.x1; ++x) {
           if (keeps && kept.has(x)) continue;
           if (keeps) kept.put(x, q_loads);
-          float neg[2];
+          float neg[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = (warp - 2) * 64 + i * 32 + lane;
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 32 + lane;
             neg[i] = w.sees(x, row) >= 0 ? __ldcg(p.neg_lse + w.stat_at(x, row)) : -INFINITY;
           }
-          const int slot = q_loads & 1;
-          ok = warp_wait(&st_empty[slot], ((q_loads >> 1) & 1) ^ 1, abort_flag);
+          const int slot = q_loads & 3;
+          ok = warp_wait(&st_empty[slot], ((q_loads >> 2) & 1) ^ 1, abort_flag);
           if (!ok) break;
-          stat[slot * kTile + (warp - 2) * 64 + lane] = neg[0];
-          stat[slot * kTile + (warp - 2) * 64 + 32 + lane] = neg[1];
-          mbar_arrive(&st_full[slot]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) stat[slot * kTile + i * 32 + lane] = neg[i];
+          __syncwarp();
+          if (lane == 0) count_set(stats_in, q_loads + 1);
           ++q_loads;
         }
         if (w.head_done()) kept.mask = 0;
       }
     }
   } else {
-    // ---- exponentials and sums: two groups of four warps ----
+    // ---- exponentials and sums: a group of four warps for each S buffer ----
     // They take the steps in turn or, where a tile has few (second pass, row
     // tiles that stay in their slots), the tiles.
     const int quarter = warp & 3;
-    const int side = (warp - 4) >> 2;
+    const int side = (warp - 4) >> 2;     // the group
     const int row = quarter * 32 + lane;  // the thread's lane of tensor memory
-    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + side * kTile;
     const float qs = p.qscale;
     const float2 qs2 = make_float2(qs, qs);
     bool ok = true;
     int q_loads = 0, swaps = 0;
     Kept kept;
-    auto wait_product = [&](int k) -> bool {
-      if (!warp_wait(&s_full[k & 3], (k >> 2) & 1, abort_flag)) return false;
+    uint32_t phase_s = 0;  // of this group's buffer
+    auto wait_product = [&]() -> bool {
+      if (!warp_wait(&s_full[side], phase_s, abort_flag)) return false;
+      phase_s ^= 1;
       tc_fence_after_sync();
       return true;
     };
-    auto release_product = [&](int k) {
+    auto release_product = [&]() {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[k & 3]);
+      if (lane == 0) mbar_arrive(&s_empty[side]);
     };
     auto join = [&](float2 a, float2 b) -> float2 {
       if (PASS == 2) return make_float2(0.f, a.y + b.y);
@@ -611,29 +690,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (maximum, sum) of the row, or (-, sum) of the key, over this thread's steps.
       float2 mine = make_float2(PASS == 1 ? -INFINITY : 0.f, 0.f);
       const bool keeps = w.keeps();
-      bool owner = true;  // of the tile, alone
       if (PASS == 1) {
         const int last = w.sees(w.tile, row);
-        const int odd = ((int)w.k ^ side) & 1;
-        int k = (int)w.k + odd;
-        for (int x = w.x0 + odd; x < w.x1; x += 2, k += 2) {
-          ok = wait_product(k);
+        const int skip = (side - w.k) & 3;
+        for (int x = w.x0 + skip; x < w.x1; x += kGroups) {
+          ok = wait_product();
           if (!ok) break;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 64) {
-            const int key0 = x * kTile + c0;
-            if (!__any_sync(0xffffffffu, key0 <= last)) break;  // (hidden from all 32 rows)
-            float v[64];
+          for (int c0 = 0; c0 < kTile; c0 += 32) {
+            const int shown = last - (x * kTile + c0);  // of these 32 keys, the last that the row sees
+            if (!__any_sync(0xffffffffu, shown >= 0)) break;  // (hidden from all 32 rows)
+            float v[32];
             float top;
-            tmem_load64_max(ta + (k & 3) * kTile + c0, v, top);
+            tmem_load32_max(ta + c0, v, top);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             float mn, ref;
-            if (qs > 0.f && __all_sync(0xffffffffu, key0 + 63 <= last)) {
+            if (qs > 0.f && __all_sync(0xffffffffu, shown >= 31)) {
               mn = fmaxf(mine.x, top * qs);
               ref = mn == -INFINITY ? 0.f : mn;
               const float2 nref = make_float2(-ref, -ref);
 #pragma unroll
-              for (int i = 0; i < 64; i += 2) {
+              for (int i = 0; i < 32; i += 2) {
                 const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
                 sum[(i >> 1) & 1] =
                     __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
@@ -642,16 +719,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               // Keys past the row's position are hidden; a scale that is not
               // positive puts the largest logit elsewhere.
               top = -INFINITY;
-              const int shown = last - key0;
 #pragma unroll
-              for (int i = 0; i < 64; ++i) {
+              for (int i = 0; i < 32; ++i) {
                 v[i] = i <= shown ? v[i] * qs : -INFINITY;
                 top = fmaxf(top, v[i]);
               }
               mn = fmaxf(mine.x, top);
               ref = mn == -INFINITY ? 0.f : mn;
 #pragma unroll
-              for (int i = 0; i < 64; i += 2)
+              for (int i = 0; i < 32; i += 2)
                 sum[(i >> 1) & 1] = __fadd2_rn(
                     sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
             }
@@ -659,22 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                      ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
             mine.x = mn;
           }
-          release_product(k);
+          release_product();
         }
       } else {
         const int key = w.tile * kTile + row;
-        const bool by_tile = keeps;
-        owner = !by_tile || (w.tile & 1) == side;
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        const int odd = by_tile ? 0 : ((int)w.k ^ side) & 1;
-        if (by_tile) {
+        if (keeps) {
           for (int x = w.x0; x < w.x1; ++x)
             if (!kept.has(x)) kept.put(x, q_loads++);
         }
-        int k = (int)w.k + odd;
-        for (int x = w.x0 + odd; owner && x < w.x1; x += by_tile ? 1 : 2, k += by_tile ? 1 : 2) {
-          const int load = by_tile ? kept.load_of(x) : q_loads + (x - w.x0);
-          ok = warp_wait(&st_full[load & 1], (load >> 1) & 1, abort_flag) && wait_product(k);
+        const bool owner = !keeps || (w.tile & 3) == side;  // of the tile, alone if it keeps
+        const int skip = keeps ? 0 : (side - w.k) & 3, by = keeps ? 1 : kGroups;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        for (int x = w.x0 + skip; owner && x < w.x1; x += by) {
+          const int load = keeps ? kept.load_of(x) : q_loads + (x - w.x0);
+          ok = count_wait(stats_in, load, abort_flag) && wait_product();
           if (!ok) break;
           const int rows = w.tile_rows(x);
           // Columns of this key's weights: from its first row that sees it on.
@@ -684,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c0 = 0; c0 < rows; c0 += 32) {
             float v[32];
-            tmem_load32(ta + (k & 3) * kTile + c0, v);
-            const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 1) * kTile + c0);
+            tmem_load32(ta + c0, v);
+            const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 3) * kTile + c0);
             if (open && c0 + 32 <= rows) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
@@ -698,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
+              if (!__any_sync(0xffffffffu, n_in > 0)) continue;
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 n = ns[i / 4];
@@ -710,23 +785,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          release_product(k);
-          // (this group alone used the step's denominators: both groups' arrivals are its own)
-          if (!by_tile && lane == 0) {
-            mbar_arrive(&st_empty[load & 1]);
-            mbar_arrive(&st_empty[load & 1]);
-          }
+          release_product();
+          // (this group alone used the step's denominators: it releases them for all)
+          if (!keeps && lane == 0) mbar_arrive_n(&st_empty[load & 3], kGroups);
         }
         mine.y = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-        if (!by_tile) {
+        if (!keeps) {
           q_loads += w.x1 - w.x0;
         } else if (w.head_done()) {
-          // Both groups release the kept rows, once they are there at all.
-          for (int x = 0; ok && x < kQSlots; ++x) {
+          // Every group releases the kept rows, once they are there at all.
+#pragma unroll
+          for (int x = 0; x < kQSlots; ++x) {
             if (!kept.has(x)) continue;
             const int load = kept.load_of(x);
-            ok = warp_wait(&st_full[load & 1], (load >> 1) & 1, abort_flag);
-            if (ok && lane == 0) mbar_arrive(&st_empty[load & 1]);
+            ok = ok && count_wait(stats_in, load, abort_flag);
+            if (ok && lane == 0) mbar_arrive(&st_empty[load & 3]);
           }
           kept.mask = 0;
         }
@@ -735,22 +808,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // The tile ends here.  Steps taken in turn: the first group gets the
-      // second one's part, warp from warp.
+      // others' parts, warp from warp.
       if (!keeps) {
         const int buf = swaps & 1, bar = quarter * 2 + buf;
         const uint32_t phase = (swaps >> 1) & 1;
         ++swaps;
-        if (side == 1) {
+        float2 *part = ex + buf * (kGroups - 1) * kTile + row;
+        if (side != 0) {
           ok = warp_wait(&x_empty[bar], phase ^ 1, abort_flag);
           if (!ok) break;
-          ex[buf * kTile + row] = mine;
+          part[(side - 1) * kTile] = mine;
           __syncwarp();
           if (lane == 0) mbar_arrive(&x_full[bar]);
           continue;
         }
         ok = warp_wait(&x_full[bar], phase, abort_flag);
         if (!ok) break;
-        mine = join(mine, ex[buf * kTile + row]);
+#pragma unroll
+        for (int x = 0; x < kGroups - 1; ++x) mine = join(mine, part[x * kTile]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_empty[bar]);
       }
