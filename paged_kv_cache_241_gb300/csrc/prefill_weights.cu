@@ -153,69 +153,66 @@ __device__ __forceinline__ int steps_of_keys(const PromptParams &p, const Seq &q
   return k * q.nrt - (p.group * (k1 * n + n * (n - 1) / 2) - e * n);
 }
 
-// Where a CTA's run of steps starts.
+// A CTA's run of steps: from step `in` of tile `tile` of head j of sequence s on,
+// to step `out` (exclusive) of tile `end_tile` of head end_j of sequence end_s.
+// First pass: tiles are row tiles, their steps key tiles; second pass: the other
+// way round.
 struct Run {
   int64_t begin, steps;  // first step of the call's, steps per CTA
   int left;              // steps to do
-  int s, j, tile, in;    // sequence, head, tile, and steps of that tile before `begin`
-  Seq q;                 // that sequence
+  int s, j, tile, in;
+  int end_s, end_j, end_tile, out;
+  Seq q;                 // sequence s
 };
 
-// A role's walk over its CTA's run, tile by tile: row tiles in the first pass,
-// whose steps are key tiles, key tiles in the second, whose steps are row tiles.
+// A role's walk over its CTA's run, head by head: of head (s, j) the tiles
+// [t0, t1], of which the first may have lost its first steps to the CTA before
+// and the last its last ones to the next.
 template <int PASS>
 struct Walk {
   const PromptParams &p;
+  const Run *run;
   Seq q;
-  int s, j, tile;
-  int b0, b1;      // the tile's steps
-  int x0, x1;      // those of them that are here
-  int k, left;     // number of step x0 in the CTA's run; steps to do from x0 on
-  bool last_tile;  // of the (sequence, head)
+  int s, j, t0, t1;
+  int in, out;
+  bool some;
 
-  __device__ __forceinline__ Walk(const PromptParams &prm, const Run &run) : p(prm) {
-    left = run.left;
-    k = 0;
-    if (left <= 0) return;
-    s = run.s;
-    j = run.j;
-    tile = run.tile;
-    q = run.q;
-    enter(run.in);
+  __device__ __forceinline__ Walk(const PromptParams &prm, const Run *r) : p(prm), run(r) {
+    some = r->left > 0;
+    q = r->q;
+    s = r->s;
+    j = r->j;
+    t0 = r->tile;
+    in = r->in;
+    set_end();
   }
-  __device__ __forceinline__ void enter(int in) {
-    if (PASS == 1) {
-      b0 = 0;
-      b1 = tiles_seen(p, q, tile);
-      last_tile = tile + 1 == q.nrt;
-    } else {
-      b0 = first_rt(p, q, tile);
-      b1 = q.nrt;
-      last_tile = tile + 1 == q.nkt;
-    }
-    x0 = b0 + in;
-    x1 = min(b1, x0 + left);
+  __device__ __forceinline__ void set_end() {
+    const bool last = s == run->end_s && j == run->end_j;
+    t1 = last ? run->end_tile : (PASS == 1 ? q.nrt : q.nkt) - 1;
+    out = last ? run->out : 0x7FFFFFFF;
   }
-  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool more() const { return some; }
   __device__ __forceinline__ void next() {
-    left -= x1 - x0;
-    k += x1 - x0;
-    if (left <= 0) return;
-    if (!last_tile) {
-      ++tile;
-    } else {
-      tile = 0;
-      if (++j == p.num_kv_heads) {
-        j = 0;
-        do ++s; while (!seq_at(p, s, q, false));
-      }
+    if (s == run->end_s && j == run->end_j) {
+      some = false;
+      return;
     }
-    enter(0);
+    t0 = in = 0;
+    if (++j == p.num_kv_heads) {
+      j = 0;
+      do ++s; while (!seq_at(p, s, q, false));
+    }
+    set_end();
   }
-  // The (sequence, head) has no further tile here.
-  __device__ __forceinline__ bool head_done() const { return last_tile || left == x1 - x0; }
+  // Steps [b0, b1) of tile t, of which [x0, x1) are here.
+  __device__ __forceinline__ void steps(int t, int &b0, int &b1, int &x0, int &x1) const {
+    b0 = PASS == 1 ? 0 : first_rt(p, q, t);
+    b1 = PASS == 1 ? tiles_seen(p, q, t) : q.nrt;
+    x0 = b0 + (t == t0 ? in : 0);
+    x1 = t == t1 ? min(b1 - b0, out) + b0 : b1;
+  }
   // Second pass: so few row tiles that they stay in their slots for the whole
-  // (sequence, head), else each step loads its own.
+  // head, else each step loads its own.
   __device__ __forceinline__ bool keeps() const { return PASS == 2 && q.nrt <= kQSlots; }
   // The statistics' row of row `row` of row tile rt.
   __device__ __forceinline__ int64_t stat_at(int rt, int row) const {
@@ -230,19 +227,6 @@ struct Walk {
   }
   __device__ __forceinline__ int tile_rows(int rt) const {
     return min(1 << tq_shift(p), q.R - (rt << tq_shift(p))) << p.group_shift;
-  }
-};
-
-// Row tiles of a (sequence, head) that have a slot (second pass, keeps()): the
-// number of the load that brought each.
-struct Kept {
-  int mask = 0, load0 = 0, load1 = 0;
-  __device__ __forceinline__ bool has(int rt) const { return mask >> rt & 1; }
-  __device__ __forceinline__ int load_of(int rt) const { return rt == 0 ? load0 : load1; }
-  __device__ __forceinline__ void put(int rt, int load) {
-    mask |= 1 << rt;
-    if (rt == 0) load0 = load;
-    else load1 = load;
   }
 };
 
@@ -313,9 +297,28 @@ struct Ring {
   }
 };
 
+// Warp: the last tile of a head that starts at or before its step `at`, and how
+// many steps before; 32 candidates at a time.
+template <int PASS>
+__device__ __forceinline__ int find_tile(const PromptParams &p, const Seq &q, int at, int &in) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = PASS == 1 ? q.nrt : q.nkt;  // in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int x = lo + lane * step;
+    const bool starts =
+        x < hi && (PASS == 1 ? steps_of_rows(p, q, x) : steps_of_keys(p, q, x)) <= at;
+    const int n = __popc(__ballot_sync(0xffffffffu, starts));  // (lane 0 always does)
+    hi = min(hi, lo + n * step);
+    lo += (n - 1) * step;
+  }
+  in = at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo));
+  return lo;
+}
+
 // All threads: the CTA's run of steps.
 template <int PASS>
-__device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool tell) {
+__device__ void find_run(const PromptParams &p, Run *run, int64_t *scratch, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
   const int per = (S + kThreads - 1) / kThreads;  // (one, for batches up to kThreads)
@@ -351,49 +354,58 @@ __device__ void find_run(const PromptParams &p, Run *out, int64_t *scratch, bool
   const int64_t begin = steps * blockIdx.x;
   // (2^31 steps of one CTA, tens of minutes, are no batch: refused)
   const bool some = begin < total && steps <= 0x7FFFFFFFll;
+  const int64_t last = min(begin + steps, total) - 1;
   if (tid == 0) {
-    out->begin = begin;
-    out->steps = steps;
-    out->left = some ? (int)min(steps, total - begin) : 0;
+    run->begin = begin;
+    run->steps = steps;
+    run->left = some ? (int)(last + 1 - begin) : 0;
     if (steps > 0x7FFFFFFFll) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
   }
-  if (some && before <= begin && begin < before + local) {
+  // The sequence and head of the run's first step, then of its last one.
+  Seq *qs = reinterpret_cast<Seq *>(scratch + kThreads / 32);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int64_t at = x == 0 ? begin : last;
+    if (!some || at < before || at >= before + local) continue;
+    int64_t b = before;
     int s = s0;
     if (per > 1) {
       for (; s < s1; ++s) {
         if (!seq_at(p, s, q, false)) continue;
         each = steps_of_keys(p, q, q.nkt);
-        if (begin < before + (int64_t)each * p.num_kv_heads) break;
-        before += (int64_t)each * p.num_kv_heads;
+        if (at < b + (int64_t)each * p.num_kv_heads) break;
+        b += (int64_t)each * p.num_kv_heads;
       }
     }
-    const int64_t offset = begin - before;
+    const int64_t offset = at - b;
     const int j = offset <= 0xFFFFFFFFll ? (int)((uint32_t)offset / (uint32_t)each)
                                          : (int)(offset / each);
-    out->s = s;
-    out->j = j;
-    out->in = (int)(offset - (int64_t)j * each);  // (steps of the head, until the tile is found)
-    out->q = q;
+    const int in = (int)(offset - (int64_t)j * each);  // (steps of the head, until the tile is found)
+    if (x == 0) {
+      run->s = s;
+      run->j = j;
+      run->in = in;
+      run->q = q;
+    } else {
+      run->end_s = s;
+      run->end_j = j;
+      run->out = in;
+      *qs = q;
+    }
   }
   __syncthreads();
-  if (warp == 0 && some) {
-    // The last tile that starts at or before the run's first step: 32
-    // candidates at a time.
-    q = out->q;
-    const int at = out->in;
-    int lo = 0, hi = PASS == 1 ? q.nrt : q.nkt;  // in [lo, hi)
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5;
-      const int x = lo + lane * step;
-      const bool starts =
-          x < hi && (PASS == 1 ? steps_of_rows(p, q, x) : steps_of_keys(p, q, x)) <= at;
-      const int n = __popc(__ballot_sync(0xffffffffu, starts));  // (lane 0 always does)
-      hi = min(hi, lo + n * step);
-      lo += (n - 1) * step;
-    }
+  if (warp < 2 && some) {
+    int in;
+    const int tile = find_tile<PASS>(p, warp == 0 ? run->q : *qs, warp == 0 ? run->in : run->out, in);
+    __syncwarp();
     if (lane == 0) {
-      out->tile = lo;
-      out->in = at - (PASS == 1 ? steps_of_rows(p, q, lo) : steps_of_keys(p, q, lo));
+      if (warp == 0) {
+        run->tile = tile;
+        run->in = in;
+      } else {
+        run->end_tile = tile;
+        run->out = in + 1;
+      }
     }
   }
 }
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *stats_in = reinterpret_cast<int *>(smem + L::misc + 8);  // row tiles whose denominators are in
   Run *run = reinterpret_cast<Run *>(smem + L::misc + 16);
   int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 128);
-  static_assert(sizeof(Run) <= 112 && 128 + kThreads / 32 * 8 <= 512, "");
+  static_assert(sizeof(Run) <= 112 && 128 + kThreads / 32 * 8 + sizeof(Seq) <= 512, "");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -487,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_loads = 0, q_loads = 0;
       bool ok = true;
       const uint32_t in_block = (1u << p.block_shift) - 1;
-      Kept kept;
-      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
+      for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
         const int32_t *bt = p.block_tables + (int64_t)w.s * p.max_blocks_per_seq;
         auto load_k = [&](int kt) -> bool {
           // (a tile's second half may lie past the keys: it reads the first half's block, unused)
@@ -524,18 +535,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++q_loads;
           return true;
         };
-        if (PASS == 1) {
-          ok = load_q(w.tile);
-          for (int x = w.x0; ok && x < w.x1; ++x) ok = load_k(x);
-        } else {
-          ok = load_k(w.tile);
-          const bool keeps = w.keeps();
-          for (int x = w.x0; ok && x < w.x1; ++x) {
-            if (keeps && kept.has(x)) continue;
-            if (keeps) kept.put(x, q_loads);
-            ok = load_q(x);
+        const bool keeps = w.keeps();
+        for (int t = w.t0; ok && t <= w.t1; ++t) {
+          int b0, b1, x0, x1;
+          w.steps(t, b0, b1, x0, x1);
+          if (PASS == 1) {
+            ok = load_q(t);
+            for (int x = x0; ok && x < x1; ++x) ok = load_k(x);
+          } else {
+            ok = load_k(t);
+            if (keeps) {
+              for (int x = 0; ok && t == w.t0 && x < w.q.nrt; ++x) ok = load_q(x);
+            } else {
+              for (int x = x0; ok && x < x1; ++x) ok = load_q(x);
+            }
           }
-          if (w.head_done()) kept.mask = 0;
         }
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
@@ -554,8 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
       bool ok = true;
-      int q_loads = 0;
-      Kept kept;
+      int q_loads = 0, k = 0;  // (k: steps taken in turn)
       uint32_t uses = 0;  // bit g: parity of the uses of buffer g
       // The product of a Q slot and a K slot into buffer g.
       auto product = [&](int qslot, int kslot, int g, uint32_t idesc) -> bool {
@@ -574,50 +587,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&s_full[g]);
         return true;
       };
-      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
-        if (PASS == 1) {
-          ok = mbar_wait_bounded(&q_full[q_loads & 1], (q_loads >> 1) & 1, abort_flag);
-          int k = w.k;
-          for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
-            if ((k & 1) == me) {
-              ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
-                   product(q_loads & 1, rk.slot, k & 3, umma_idesc_bf16(kTile, kTile, false, false));
-              if (ok) umma_commit(&k_empty[rk.slot]);
-            }
-            rk.next(kKSlots);
+      for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
+        const bool keeps = w.keeps();
+        if (keeps) {
+          for (int x = 0; ok && x < w.q.nrt; ++x) {
+            const int load = q_loads + x;
+            ok = mbar_wait_bounded(&q_full[load & 1], (load >> 1) & 1, abort_flag);
           }
-          if (ok) umma_commit(&q_empty[q_loads & 1]);
-          ++q_loads;
-        } else {
-          const bool keeps = w.keeps();
+        }
+        for (int t = w.t0; ok && t <= w.t1; ++t) {
+          int b0, b1, x0, x1;
+          w.steps(t, b0, b1, x0, x1);
+          if (PASS == 1) {
+            ok = mbar_wait_bounded(&q_full[q_loads & 1], (q_loads >> 1) & 1, abort_flag);
+            for (int x = x0; ok && x < x1; ++x, ++k) {
+              if ((k & 1) == me) {
+                ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
+                     product(q_loads & 1, rk.slot, k & 3,
+                             umma_idesc_bf16(kTile, kTile, false, false));
+                if (ok) umma_commit(&k_empty[rk.slot]);
+              }
+              rk.next(kKSlots);
+            }
+            if (ok) umma_commit(&q_empty[q_loads & 1]);
+            ++q_loads;
+            continue;
+          }
           ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
-          int k = w.k;
-          for (int x = w.x0; ok && x < w.x1; ++x, ++k) {
-            int load = q_loads;
-            if (keeps && kept.has(x)) {
-              load = kept.load_of(x);
-            } else {
-              ok = mbar_wait_bounded(&q_full[load & 1], (load >> 1) & 1, abort_flag);
-              if (keeps) kept.put(x, load);
-              ++q_loads;
+          for (int x = x0; ok && x < x1; ++x) {
+            // (no more columns than the row tile has rows, to 16)
+            const uint32_t idesc = umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false);
+            if (keeps) {
+              if ((t & 1) == me) ok = product((q_loads + x) & 1, rk.slot, t & 3, idesc);
+              continue;
             }
-            const int g = (keeps ? w.tile : k) & 3;
-            if ((g & 1) == me) {
-              // (no more columns than the row tile has rows, to 16)
-              ok = ok && product(load & 1, rk.slot, g,
-                                 umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false));
-              if (ok && !keeps) umma_commit(&q_empty[load & 1]);
-            } else if (ok && !keeps) {
-              mbar_arrive(&q_empty[load & 1]);
+            ok = mbar_wait_bounded(&q_full[q_loads & 1], (q_loads >> 1) & 1, abort_flag);
+            if ((k & 1) != me) {
+              if (ok) mbar_arrive(&q_empty[q_loads & 1]);
+            } else if (ok) {
+              ok = product(q_loads & 1, rk.slot, k & 3, idesc);
+              if (ok) umma_commit(&q_empty[q_loads & 1]);
             }
+            ++q_loads;
+            ++k;
           }
           if (ok) umma_commit(&k_empty[rk.slot]);
           rk.next(kKSlots);
-          if (w.head_done()) {
-            if (ok && kept.has(0)) umma_commit(&q_empty[kept.load0 & 1]);
-            if (ok && kept.has(1)) umma_commit(&q_empty[kept.load1 & 1]);
-            kept.mask = 0;
-          }
+        }
+        if (keeps) {
+          for (int x = 0; ok && x < w.q.nrt; ++x) umma_commit(&q_empty[(q_loads + x) & 1]);
+          q_loads += w.q.nrt;
         }
       }
       // Wait for the products of both before tensor memory is freed.
@@ -631,28 +650,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < 4) p.tickets[blockIdx.x * 4 + lane] = 0;
       int q_loads = 0;
       bool ok = true;
-      Kept kept;
-      for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
-        const bool keeps = w.keeps();
-        for (int x = w.x0; x < w.x1; ++x) {
-          if (keeps && kept.has(x)) continue;
-          if (keeps) kept.put(x, q_loads);
+      for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
+        auto fill = [&](int rt) -> bool {
           float neg[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = i * 32 + lane;
-            neg[i] = w.sees(x, row) >= 0 ? __ldcg(p.neg_lse + w.stat_at(x, row)) : -INFINITY;
+            neg[i] = w.sees(rt, row) >= 0 ? __ldcg(p.neg_lse + w.stat_at(rt, row)) : -INFINITY;
           }
           const int slot = q_loads & 3;
-          ok = warp_wait(&st_empty[slot], ((q_loads >> 2) & 1) ^ 1, abort_flag);
-          if (!ok) break;
+          if (!warp_wait(&st_empty[slot], ((q_loads >> 2) & 1) ^ 1, abort_flag)) return false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) stat[slot * kTile + i * 32 + lane] = neg[i];
           __syncwarp();
-          if (lane == 0) count_set(stats_in, q_loads + 1);
           ++q_loads;
+          if (lane == 0) count_set(stats_in, q_loads);
+          return true;
+        };
+        if (w.keeps()) {
+          for (int x = 0; ok && x < w.q.nrt; ++x) ok = fill(x);
+          continue;
         }
-        if (w.head_done()) kept.mask = 0;
+        for (int t = w.t0; ok && t <= w.t1; ++t) {
+          int b0, b1, x0, x1;
+          w.steps(t, b0, b1, x0, x1);
+          for (int x = x0; ok && x < x1; ++x) ok = fill(x);
+        }
       }
     }
   } else {
@@ -666,8 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float qs = p.qscale;
     const float2 qs2 = make_float2(qs, qs);
     bool ok = true;
-    int q_loads = 0, swaps = 0;
-    Kept kept;
+    int q_loads = 0, swaps = 0, k = 0;  // (k: steps taken in turn)
     uint32_t phase_s = 0;  // of this group's buffer
     auto wait_product = [&]() -> bool {
       if (!warp_wait(&s_full[side], phase_s, abort_flag)) return false;
@@ -686,182 +708,183 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ref = mn == -INFINITY ? 0.f : mn;
       return make_float2(mn, a.y * fast_exp2(a.x - ref) + b.y * fast_exp2(b.x - ref));
     };
-    for (Walk<PASS> w(p, *run); ok && w.more(); w.next()) {
-      // (maximum, sum) of the row, or (-, sum) of the key, over this thread's steps.
-      float2 mine = make_float2(PASS == 1 ? -INFINITY : 0.f, 0.f);
+    for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
       const bool keeps = w.keeps();
-      if (PASS == 1) {
-        const int last = w.sees(w.tile, row);
-        const int skip = (side - w.k) & 3;
-        for (int x = w.x0 + skip; x < w.x1; x += kGroups) {
-          ok = wait_product();
-          if (!ok) break;
+      if (keeps) ok = count_wait(stats_in, q_loads + w.q.nrt - 1, abort_flag);
+      // (keeps: a group's tiles are those of its number, modulo the groups)
+      for (int t = keeps ? w.t0 + ((side - w.t0) & 3) : w.t0; ok && t <= w.t1; t += keeps ? kGroups : 1) {
+        int b0, b1, x0, x1;
+        w.steps(t, b0, b1, x0, x1);
+        // (maximum, sum) of the row, or (-, sum) of the key, over this thread's steps.
+        float2 mine = make_float2(PASS == 1 ? -INFINITY : 0.f, 0.f);
+        int blk = -1;
+        if (PASS == 1) {
+          const int last = w.sees(t, row);
+          const int most = __reduce_max_sync(0xffffffffu, last);
+          for (int x = x0 + ((side - k) & 3); x < x1; x += kGroups) {
+            ok = wait_product();
+            if (!ok) break;
+            // Runs of 32 keys, up to the last that any of the warp's rows sees.
+            const int runs = min((most - x * kTile + 32) >> 5, kTile / 32);
+            if (runs <= 0) release_product();
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 32) {
-            const int shown = last - (x * kTile + c0);  // of these 32 keys, the last that the row sees
-            if (!__any_sync(0xffffffffu, shown >= 0)) break;  // (hidden from all 32 rows)
-            float v[32];
-            float top;
-            tmem_load32_max(ta + c0, v, top);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            float mn, ref;
-            if (qs > 0.f && __all_sync(0xffffffffu, shown >= 31)) {
-              mn = fmaxf(mine.x, top * qs);
-              ref = mn == -INFINITY ? 0.f : mn;
-              const float2 nref = make_float2(-ref, -ref);
+            for (int c = 0; c < runs; ++c) {
+              const int shown = last - (x * kTile + c * 32);  // of these keys, the last that the row sees
+              float v[32];
+              float top;
+              tmem_load32_max(ta + c * 32, v, top);
+              if (c + 1 == runs) release_product();  // (the product is read: the next one may come)
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              float mn, ref;
+              if (qs > 0.f && __all_sync(0xffffffffu, shown >= 31)) {
+                mn = fmaxf(mine.x, top * qs);
+                ref = mn == -INFINITY ? 0.f : mn;
+                const float2 nref = make_float2(-ref, -ref);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
-                sum[(i >> 1) & 1] =
-                    __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
+                for (int i = 0; i < 32; i += 2) {
+                  const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
+                  sum[(i >> 1) & 1] =
+                      __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
+                }
+              } else {
+                // Keys past the row's position are hidden; a scale that is not
+                // positive puts the largest logit elsewhere.
+                top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  v[i] = i <= shown ? v[i] * qs : -INFINITY;
+                  top = fmaxf(top, v[i]);
+                }
+                mn = fmaxf(mine.x, top);
+                ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                  sum[(i >> 1) & 1] = __fadd2_rn(
+                      sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
               }
-            } else {
-              // Keys past the row's position are hidden; a scale that is not
-              // positive puts the largest logit elsewhere.
-              top = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                v[i] = i <= shown ? v[i] * qs : -INFINITY;
-                top = fmaxf(top, v[i]);
-              }
-              mn = fmaxf(mine.x, top);
-              ref = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                sum[(i >> 1) & 1] = __fadd2_rn(
-                    sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
-            }
-            mine.y = mine.y * fast_exp2(mine.x - ref) +
-                     ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-            mine.x = mn;
-          }
-          release_product();
-        }
-      } else {
-        const int key = w.tile * kTile + row;
-        if (keeps) {
-          for (int x = w.x0; x < w.x1; ++x)
-            if (!kept.has(x)) kept.put(x, q_loads++);
-        }
-        const bool owner = !keeps || (w.tile & 3) == side;  // of the tile, alone if it keeps
-        const int skip = keeps ? 0 : (side - w.k) & 3, by = keeps ? 1 : kGroups;
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        for (int x = w.x0 + skip; owner && x < w.x1; x += by) {
-          const int load = keeps ? kept.load_of(x) : q_loads + (x - w.x0);
-          ok = count_wait(stats_in, load, abort_flag) && wait_product();
-          if (!ok) break;
-          const int rows = w.tile_rows(x);
-          // Columns of this key's weights: from its first row that sees it on.
-          const int first = (key - w.q.base - (x << tq_shift(p))) * p.group;
-          // Every row of the tile sees every key of the tile.
-          const bool open = w.tile * kTile + kTile - 1 <= w.q.base + (x << tq_shift(p));
-#pragma unroll 1
-          for (int c0 = 0; c0 < rows; c0 += 32) {
-            float v[32];
-            tmem_load32(ta + c0, v);
-            const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 3) * kTile + c0);
-            if (open && c0 + 32 <= rows) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 n = ns[i / 4];
-                const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
-                const float2 z1 =
-                    __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
-                acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
-                acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
-              }
-            } else {
-              const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
-              if (!__any_sync(0xffffffffu, n_in > 0)) continue;
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 n = ns[i / 4];
-                const float e0 = fast_exp2(fmaf(v[i], qs, n.x)), e1 = fast_exp2(fmaf(v[i + 1], qs, n.y));
-                const float e2 = fast_exp2(fmaf(v[i + 2], qs, n.z)), e3 = fast_exp2(fmaf(v[i + 3], qs, n.w));
-                acc0.x += (unsigned)(i - lo) < (unsigned)n_in ? e0 : 0.f;
-                acc0.y += (unsigned)(i + 1 - lo) < (unsigned)n_in ? e1 : 0.f;
-                acc1.x += (unsigned)(i + 2 - lo) < (unsigned)n_in ? e2 : 0.f;
-                acc1.y += (unsigned)(i + 3 - lo) < (unsigned)n_in ? e3 : 0.f;
-              }
+              mine.y = mine.y * fast_exp2(mine.x - ref) +
+                       ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+              mine.x = mn;
             }
           }
-          release_product();
-          // (this group alone used the step's denominators: it releases them for all)
-          if (!keeps && lane == 0) mbar_arrive_n(&st_empty[load & 3], kGroups);
-        }
-        mine.y = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-        if (!keeps) {
-          q_loads += w.x1 - w.x0;
-        } else if (w.head_done()) {
-          // Every group releases the kept rows, once they are there at all.
+          k += x1 - x0;
+        } else {
+          const int key = t * kTile + row;
+          if ((keeps || side == 0) && key < w.q.len_k)
+            blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
+          const int skip = keeps ? 0 : (side - k) & 3, by = keeps ? 1 : kGroups;
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+          for (int x = x0 + skip; x < x1; x += by) {
+            const int load = q_loads + (keeps ? x : x - x0);
+            ok = (keeps || count_wait(stats_in, load, abort_flag)) && wait_product();
+            if (!ok) break;
+            const int rows = w.tile_rows(x);
+            // Columns of this key's weights: from its first row that sees it on.
+            const int first = (key - w.q.base - (x << tq_shift(p))) * p.group;
+            // Every row of the tile sees every key of the tile.
+            const bool open = t * kTile + kTile - 1 <= w.q.base + (x << tq_shift(p));
+#pragma unroll 1
+            for (int c0 = 0; c0 < rows; c0 += 32) {
+              float v[32];
+              tmem_load32(ta + c0, v);
+              if (c0 + 32 >= rows) release_product();  // (the product is read: the next one may come)
+              const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 3) * kTile + c0);
+              if (open && c0 + 32 <= rows) {
 #pragma unroll
-          for (int x = 0; x < kQSlots; ++x) {
-            if (!kept.has(x)) continue;
-            const int load = kept.load_of(x);
-            ok = ok && count_wait(stats_in, load, abort_flag);
-            if (ok && lane == 0) mbar_arrive(&st_empty[load & 3]);
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 n = ns[i / 4];
+                  const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
+                  const float2 z1 =
+                      __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
+                  acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+                  acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+                }
+              } else {
+                const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
+                if (!__any_sync(0xffffffffu, n_in > 0)) continue;
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 n = ns[i / 4];
+                  const float e0 = fast_exp2(fmaf(v[i], qs, n.x)), e1 = fast_exp2(fmaf(v[i + 1], qs, n.y));
+                  const float e2 = fast_exp2(fmaf(v[i + 2], qs, n.z)), e3 = fast_exp2(fmaf(v[i + 3], qs, n.w));
+                  acc0.x += (unsigned)(i - lo) < (unsigned)n_in ? e0 : 0.f;
+                  acc0.y += (unsigned)(i + 1 - lo) < (unsigned)n_in ? e1 : 0.f;
+                  acc1.x += (unsigned)(i + 2 - lo) < (unsigned)n_in ? e2 : 0.f;
+                  acc1.y += (unsigned)(i + 3 - lo) < (unsigned)n_in ? e3 : 0.f;
+                }
+              }
+            }
+            // (this group alone used the step's denominators: it releases them for all)
+            if (!keeps) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive_n(&st_empty[load & 3], kGroups);
+            }
           }
-          kept.mask = 0;
+          mine.y = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+          if (!keeps) {
+            k += x1 - x0;
+            q_loads += x1 - x0;
+          }
         }
-        if (ok && !owner) continue;
-      }
-      if (!ok) break;
-
-      // The tile ends here.  Steps taken in turn: the first group gets the
-      // others' parts, warp from warp.
-      if (!keeps) {
-        const int buf = swaps & 1, bar = quarter * 2 + buf;
-        const uint32_t phase = (swaps >> 1) & 1;
-        ++swaps;
-        float2 *part = ex + buf * (kGroups - 1) * kTile + row;
-        if (side != 0) {
-          ok = warp_wait(&x_empty[bar], phase ^ 1, abort_flag);
-          if (!ok) break;
-          part[(side - 1) * kTile] = mine;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&x_full[bar]);
-          continue;
-        }
-        ok = warp_wait(&x_full[bar], phase, abort_flag);
         if (!ok) break;
-#pragma unroll
-        for (int x = 0; x < kGroups - 1; ++x) mine = join(mine, part[x * kTile]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_empty[bar]);
-      }
-      if (w.x0 != w.b0 || w.x1 != w.b1) {
-        // A part of a tile that several CTAs share: filed by CTA, place 0 if
-        // the tile began before it, place 1 if it begins here.  The warp that
-        // is the last to file its 32 rows joins all of them, in order.
-        const int64_t at = run->begin + w.k;
-        const int c0 = (int)((at - (w.x0 - w.b0)) / run->steps);
-        const int c1 = (int)((at + (w.b1 - w.x0) - 1) / run->steps);
-        __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (w.x0 != w.b0 ? 0 : 1)) * kTile + row, mine);
-        __threadfence();
-        __syncwarp();
-        unsigned int done = 0;
-        if (lane == 0) {
-          done = atomicAdd(&p.tickets[((PASS - 1) * kMaxCtas + c0) * 4 + quarter], 1u);
-          __threadfence();
-        }
-        done = __shfl_sync(0xffffffffu, done, 0);
-        if (done != (unsigned int)(c1 - c0)) continue;
-        mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
-        for (int c = c0 + 1; c <= c1; ++c) mine = join(mine, __ldcg(p.parts + (int64_t)c * 2 * kTile + row));
-      }
-      if (PASS == 1) {
-        if (w.sees(w.tile, row) >= 0) p.neg_lse[w.stat_at(w.tile, row)] = -(mine.x + log2f(mine.y));
-      } else {
-        const int key = w.tile * kTile + row;
-        if (key < w.q.len_k) {
-          const int blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
-          if (blk >= 0 && blk < p.num_blocks) {
-            float *to = p.key_weights + ((((int64_t)blk * p.num_kv_heads + w.j) << p.block_shift) +
-                                         (key & ((1 << p.block_shift) - 1)));
-            if (key >= w.q.c) *to = mine.y;
-            else atomicAdd(to, mine.y);
+
+        // The tile ends here.  Steps taken in turn: the first group gets the
+        // others' parts, warp from warp.
+        if (!keeps) {
+          const int buf = swaps & 1, bar = quarter * 2 + buf;
+          const uint32_t phase = (swaps >> 1) & 1;
+          ++swaps;
+          float2 *part = ex + buf * (kGroups - 1) * kTile + row;
+          if (side != 0) {
+            ok = warp_wait(&x_empty[bar], phase ^ 1, abort_flag);
+            if (!ok) break;
+            part[(side - 1) * kTile] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x_full[bar]);
+            continue;
           }
+          ok = warp_wait(&x_full[bar], phase, abort_flag);
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < kGroups - 1; ++x) mine = join(mine, part[x * kTile]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&x_empty[bar]);
         }
+        if (x0 != b0 || x1 != b1) {
+          // A part of a tile that several CTAs share: filed by CTA, place 0 if
+          // the tile began before it, place 1 if it begins here.  The warp that
+          // is the last to file its 32 rows joins all of them, in order.
+          const int64_t at = x1 != b1 ? run->begin + run->left - (x1 - x0) : run->begin;  // of step x0
+          const int c0 = (int)((at - (x0 - b0)) / run->steps);
+          const int c1 = (int)((at + (b1 - x0) - 1) / run->steps);
+          __stcg(p.parts + ((int64_t)blockIdx.x * 2 + (x0 != b0 ? 0 : 1)) * kTile + row, mine);
+          __threadfence();
+          __syncwarp();
+          unsigned int done = 0;
+          if (lane == 0) {
+            done = atomicAdd(&p.tickets[((PASS - 1) * kMaxCtas + c0) * 4 + quarter], 1u);
+            __threadfence();
+          }
+          done = __shfl_sync(0xffffffffu, done, 0);
+          if (done != (unsigned int)(c1 - c0)) continue;
+          mine = __ldcg(p.parts + ((int64_t)c0 * 2 + 1) * kTile + row);
+          for (int c = c0 + 1; c <= c1; ++c)
+            mine = join(mine, __ldcg(p.parts + (int64_t)c * 2 * kTile + row));
+        }
+        if (PASS == 1) {
+          if (w.sees(t, row) >= 0) p.neg_lse[w.stat_at(t, row)] = -(mine.x + log2f(mine.y));
+        } else if (blk >= 0 && blk < p.num_blocks) {
+          const int key = t * kTile + row;
+          float *to = p.key_weights + ((((int64_t)blk * p.num_kv_heads + w.j) << p.block_shift) +
+                                       (key & ((1 << p.block_shift) - 1)));
+          if (key >= w.q.c) *to = mine.y;
+          else atomicAdd(to, mine.y);
+        }
+      }
+      if (keeps) {  // every group releases the head's denominators
+        __syncwarp();
+        for (int x = 0; ok && lane == 0 && x < w.q.nrt; ++x) mbar_arrive(&st_empty[(q_loads + x) & 3]);
+        q_loads += w.q.nrt;
       }
     }
   }
