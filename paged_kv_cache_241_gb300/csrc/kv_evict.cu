@@ -11,8 +11,8 @@
 // the next eviction.
 //
 // Two launches: one CTA per (sequence, kv head) selects and writes `kept` (the
-// old position of what is to sit at each place), then one per (sequence, kv
-// head, K or V) moves the rows that `kept` says.
+// old position of what is to sit at each place), then CTAs per (sequence, kv
+// head, K or V, run of places) move the rows that `kept` says.
 #include "host_common.h"
 #include "pkv_common.cuh"
 
@@ -22,9 +22,12 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;             // selection by digits of 11, 11 and 10 bits
-constexpr int kSuper = 1024;            // positions per entry of the rank table
+constexpr int kRankWords = 4;           // bitmap words per entry of the rank table
 constexpr int kMaxContext = 1 << 20;    // the bitmap of kept positions is in shared memory
+constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory
 constexpr int kMoveThreads = 256;
+constexpr int kMovePlaces = 512;        // places per CTA of the second launch
+constexpr int kMoveDepth = 8;           // 16-byte vectors that a thread has in flight
 
 struct EvictParams {
   uint16_t *k_cache;
@@ -95,8 +98,19 @@ __device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) 
   return found[0];
 }
 
+// Shared memory of the selection: keys, bitmap, rank table.
+struct SelectSmem {
+  int keys, words, ranks;  // entries
+  __host__ __device__ SelectSmem(int room) {
+    keys = room < kKeyCache ? room : kKeyCache;
+    words = (room + 31) / 32 + kRankWords;
+    ranks = words / kRankWords + 2;
+  }
+  __host__ __device__ int bytes() const { return (keys + words + ranks) * 4; }
+};
+
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t bits[];  // bit i: position i is kept; then the rank table
+  extern __shared__ uint32_t dyn[];
   __shared__ int hist[kBins];
   __shared__ int warp_sums[kSelWarps];
   __shared__ int found[2];
@@ -108,6 +122,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int L = p.context_lens[s];
   const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
   const int shift = p.block_shift;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const SelectSmem lay((int)room);
+  uint32_t *keys = dyn;
+  uint32_t *bits = dyn + lay.keys;  // bit i: position i is kept
+  int *ranks = reinterpret_cast<int *>(bits + lay.words);  // kept positions before each 128
 
   bool bad = false;
   if (L < 0 || L > room) {
@@ -131,21 +150,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   for (int i = tid; i < p.recent; i += kSelThreads) kept[H + i] = N + i;
   if (H == 0) return;
 
-  auto key_at = [&](int i) { return order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]); };
+  auto read_key = [&](int i) {
+    return order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
+  };
+  const int cached = min(N, lay.keys);
+#pragma unroll 4
+  for (int i = tid; i < cached; i += kSelThreads) keys[i] = read_key(i);
+  auto key_at = [&](int i) { return i < cached ? keys[i] : read_key(i); };
 
-  // The H-th largest key T, digit by digit; `need` of the keys equal to T are kept.
+  // The H-th largest key T, digit by digit; `need` of the keys equal to T are
+  // kept.  (A thread reads back the keys that it stored.)
   uint32_t T = 0;
   int need = H;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int lo = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const int above = pass == 0 ? 31 : (pass == 1 ? 21 : 10);  // the digits known so far
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
     for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
     __syncthreads();
-    for (int i = tid; i < N; i += kSelThreads) {
-      const uint32_t u = key_at(i);
-      const bool in = pass == 0 || (u >> (lo + (pass == 1 ? 11 : 10))) == (T >> (lo + (pass == 1 ? 11 : 10)));
-      if (in) atomicAdd(&hist[(u >> lo) & mask], 1);
+    for (int i0 = 0; i0 < N; i0 += kSelThreads) {
+      const int i = i0 + tid;
+      const uint32_t u = i < N ? key_at(i) : 0u;
+      const bool in = i < N && (pass == 0 || (u >> above) == (T >> above));
+      // Equal digits throughout a warp (weights that are all zero) count at
+      // once; others collide little.
+      int same;
+      const uint32_t digit = in ? (u >> lo) & mask : kBins;
+      __match_all_sync(0xffffffffu, digit, &same);
+      if (same) {
+        if (in && lane == 0) atomicAdd(&hist[digit], 32);
+      } else if (in) {
+        atomicAdd(&hist[digit], 1);
+      }
     }
     __syncthreads();
     T |= (uint32_t)pick_bin(hist, warp_sums, found, need) << lo;
@@ -160,129 +197,197 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   for (int w = w0; w < w1; ++w) {
     const int i = w * 32 + lane;
     const uint32_t u = i < N ? key_at(i) : 0u;
-    equal += __popc(__ballot_sync(0xffffffffu, i < N && u == T));
+    const uint32_t above = __ballot_sync(0xffffffffu, i < N && u > T);
+    const uint32_t eqs = __ballot_sync(0xffffffffu, i < N && u == T);
+    if (lane == 0) bits[w] = above;
+    equal += __popc(eqs);
   }
   if (lane == 0) warp_sums[warp] = equal;
   __syncthreads();
   int rank = 0;
   for (int w = 0; w < warp; ++w) rank += warp_sums[w];
-  __syncthreads();
-  for (int w = w0; w < w1; ++w) {
-    const int i = w * 32 + lane;
-    const uint32_t u = i < N ? key_at(i) : 0u;
-    const bool eq = i < N && u == T;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-    const bool keep = (i < N && u > T) || (eq && rank + __popc(eqs & ((1u << lane) - 1)) < need);
-    const uint32_t word = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) bits[w] = word;
-    rank += __popc(eqs);
+  if (rank < need && equal > 0) {  // some of this warp's equal keys are kept
+    for (int w = w0; w < w1 && rank < need; ++w) {
+      const int i = w * 32 + lane;
+      const bool eq = i < N && key_at(i) == T;
+      const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
+      const uint32_t take =
+          __ballot_sync(0xffffffffu, eq && rank + __popc(eqs & ((1u << lane) - 1)) < need);
+      if (lane == 0) bits[w] |= take;
+      rank += __popc(eqs);
+    }
   }
+  if (tid < kRankWords) bits[words + tid] = 0;  // (the last entry's words)
   __syncthreads();
 
-  // Kept positions before each group of kSuper: the rank table.
-  int *table = reinterpret_cast<int *>(bits + words);
-  const int supers = (N + kSuper - 1) / kSuper;
-  for (int x = warp; x < supers; x += kSelWarps) {
-    const int w = x * (kSuper / 32) + lane;
-    int c = w < words ? __popc(bits[w]) : 0;
+  // The rank table: an exclusive scan of the entries' counts, block-wide runs.
+  const int entries = (words + kRankWords - 1) / kRankWords;
+  const int per = (entries + kSelThreads - 1) / kSelThreads;
+  const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+  int local = 0;
+  for (int e = e0; e < e1; ++e)
+    for (int x = 0; x < kRankWords; ++x) local += __popc(bits[e * kRankWords + x]);
+  int incl = local;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    if (lane == 0) table[x + 1] = c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
+  if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  if (tid == 0) {
-    table[0] = 0;
-    for (int x = 0; x < supers; ++x) table[x + 1] += table[x];
+  int run = incl - local;
+  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  for (int e = e0; e < e1; ++e) {
+    ranks[e] = run;
+    for (int x = 0; x < kRankWords; ++x) run += __popc(bits[e * kRankWords + x]);
   }
   __syncthreads();
   auto kept_before = [&](int i) {  // kept positions in [0, i)
-    int c = table[i / kSuper];
     const int w = i >> 5;
-    for (int x = (i / kSuper) * (kSuper / 32); x < w; ++x) c += __popc(bits[x]);
-    if (i & 31) c += __popc(bits[w] & ((1u << (i & 31)) - 1));
-    return c;
+    int c = ranks[w / kRankWords];
+    for (int x = w & ~(kRankWords - 1); x < w; ++x) c += __popc(bits[x]);
+    return c + __popc(bits[w] & ((1u << (i & 31)) - 1));
   };
   const int inside = kept_before(H);  // kept tokens that need not move
-  for (int w = tid; w < words; w += kSelThreads) {
-    uint32_t word = bits[w];
-    if (word == 0) continue;
-    int r = w * 32 + 31 >= H ? kept_before(w * 32) : 0;
-    while (word != 0) {
-      const int i = w * 32 + __ffs(word) - 1;
-      word &= word - 1;
-      if (i < H) {
-        kept[i] = i;
-        ++r;
-        continue;
-      }
-      // The (r - inside)-th place in [0, H) that is not kept.
-      const int hole_rank = r - inside;
-      ++r;
-      int lo = 0, hi = (H - 1) / kSuper;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (mid * kSuper - table[mid] <= hole_rank) lo = mid;
-        else hi = mid - 1;
-      }
-      int left = hole_rank - (lo * kSuper - table[lo]);
-      int x = lo * (kSuper / 32);
-      for (;; ++x) {
-        const int holes = 32 - __popc(bits[x]);
-        if (left < holes) break;
-        left -= holes;
-      }
-      uint32_t free_bits = ~bits[x];
-      for (; left > 0; --left) free_bits &= free_bits - 1;
-      kept[x * 32 + __ffs(free_bits) - 1] = i;
+  for (int i = tid; i < H; i += kSelThreads) {
+    if ((bits[i >> 5] >> (i & 31)) & 1) {
+      kept[i] = i;
+      continue;
     }
+    // The free place's number among the free ones gives the mover's among the
+    // kept positions: the entry, the word, then the bit.
+    const int want = inside + (i - kept_before(i));
+    int lo = 0, hi = entries - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (ranks[mid] <= want) lo = mid;
+      else hi = mid - 1;
+    }
+    int left = want - ranks[lo];
+    int w = lo * kRankWords;
+    for (int c = __popc(bits[w]); left >= c; c = __popc(bits[w])) {
+      left -= c;
+      ++w;
+    }
+    uint32_t word = bits[w];
+    int base = 0;
+#pragma unroll
+    for (int width = 16; width > 0; width >>= 1) {
+      const int c = __popc(word & ((1u << width) - 1));
+      if (left >= c) {
+        left -= c;
+        word >>= width;
+        base += width;
+      } else {
+        word &= (1u << width) - 1;
+      }
+    }
+    kept[i] = w * 32 + base;
   }
 }
 
-// Rows move from kept[i] to i.  Places in [0, H) only take from positions at or
-// behind H, so their copies are independent; after them the recent rows move
-// down in order, each step reading its rows before any of them is written (a
-// place is written only after the row that was there has been read: a row's
-// new place is never behind its old one).
+// Rows move from kept[i] to i, for the places of this CTA.  Places in [0, H) take
+// rows from positions at or behind H; after them the recent rows move down to
+// [H, budget).  The rows that the recent ones overwrite are read before: the
+// ones that move to places in [0, H), all by the CTA that moves the recent rows
+// and ahead of them; and of the recent rows themselves each step reads before
+// any of its rows is written (a row's new place is never behind its old one).
+// Every other row is read by its CTA and written by none.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+  __shared__ longlong2 moves[kMovePlaces];  // (from, to): rows of the cache, by (slot, kv head)
+  __shared__ int64_t wmoves[kMovePlaces][2];
+  __shared__ int count;
   const int unit = blockIdx.x >> 1;
   const int s = unit / p.num_kv_heads;
   const int j = unit - s * p.num_kv_heads;
+  const int L = p.context_lens[s];
+  if (L <= p.budget) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
   const int32_t *kept = p.kept + (int64_t)unit * p.budget;
+  if (kept[p.budget - 1] < 0) return;  // (a sequence that was refused)
+  const int tid = threadIdx.x, lane = tid & 31;
   const int H = p.budget - p.recent;
-  const int L = p.context_lens[s];
-  if (L <= p.budget || kept[p.budget - 1] < 0) return;  // (-1 in the last place: a bad sequence)
-  uint4 *cache = reinterpret_cast<uint4 *>((blockIdx.x & 1) ? p.v_cache : p.k_cache);
-  const bool sums = (blockIdx.x & 1) == 0;  // the K unit moves the weights too
-  const int shift = p.block_shift;
-  const int V = p.row_vecs;
-  auto row = [&](int i) { return cache + (slot_at(bt, i, shift) * p.num_kv_heads + j) * V; };
+  const bool sums = (blockIdx.x & 1) == 0;  // the K units move the weights too
+  uint4 *cache = reinterpret_cast<uint4 *>(sums ? p.k_cache : p.v_cache);
+  const int shift = p.block_shift, Hkv = p.num_kv_heads;
+  const int V = p.row_vecs, vshift = V == 16 ? 4 : 3;
+  auto row_of = [&](int i) { return slot_at(bt, i, shift) * Hkv + j; };
 
-  for (int x = threadIdx.x; x < H * V; x += kMoveThreads) {
-    const int i = x / V, v = x - i * V;
-    const int src = kept[i];
-    if (src != i) {
-      row(i)[v] = row(src)[v];
-      if (sums && v == 0)
-        p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)] =
-            p.key_weights[weight_at(bt, src, shift, p.num_kv_heads, j)];
+  // With `recent`, CTA 0 of the unit takes the movers that recent rows are to
+  // overwrite, whatever their new place; the others leave those out.
+  const int first = blockIdx.y * kMovePlaces;
+  auto move_listed = [&]() {  // the rows in `moves`: no two touch the same one
+    __syncthreads();
+    const int n = count, total = n << vshift;
+    for (int base = tid; base < total; base += kMoveThreads * kMoveDepth) {
+      uint4 a[kMoveDepth];
+#pragma unroll
+      for (int u = 0; u < kMoveDepth; ++u) {
+        const int x = base + u * kMoveThreads;
+        if (x < total) a[u] = cache[(moves[x >> vshift].x << vshift) + (x & (V - 1))];
+      }
+#pragma unroll
+      for (int u = 0; u < kMoveDepth; ++u) {
+        const int x = base + u * kMoveThreads;
+        if (x < total) cache[(moves[x >> vshift].y << vshift) + (x & (V - 1))] = a[u];
+      }
     }
-  }
-  __syncthreads();
-  const int total = p.recent * V;
-  for (int base = 0; base < total; base += kMoveThreads) {
-    const int x = base + threadIdx.x;
-    const int i = x / V, v = x - i * V;
-    uint4 a = make_uint4(0, 0, 0, 0);
-    float w = 0.f;
-    if (x < total) {
-      a = row(L - p.recent + i)[v];
-      if (sums && v == 0) w = p.key_weights[weight_at(bt, L - p.recent + i, shift, p.num_kv_heads, j)];
+    if (sums)
+      for (int x = tid; x < n; x += kMoveThreads) p.key_weights[wmoves[x][1]] = p.key_weights[wmoves[x][0]];
+    __syncthreads();
+  };
+  auto list = [&](int src, int dst, bool take) {  // whole warps
+    const uint32_t all = __ballot_sync(0xffffffffu, take);
+    int at = 0;
+    if (lane == 0 && all) at = atomicAdd(&count, __popc(all));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1));
+    if (take) {
+      moves[at] = make_longlong2(row_of(src), row_of(dst));
+      if (sums) {
+        wmoves[at][0] = weight_at(bt, src, shift, Hkv, j);
+        wmoves[at][1] = weight_at(bt, dst, shift, Hkv, j);
+      }
+    }
+  };
+  auto take_places = [&](int begin, bool overwritten) {
+    if (tid == 0) count = 0;
+    __syncthreads();
+    for (int x = tid; x < kMovePlaces; x += kMoveThreads) {
+      const int i = begin + x;
+      const int src = i < H ? kept[i] : 0;
+      list(src, i, i < H && src != i && (src < p.budget) == overwritten);
+    }
+    move_listed();
+  };
+  if (first < H) take_places(first, false);
+  if (blockIdx.y != 0) return;
+  // (a mover below `budget` can go to any free place below H)
+  if (p.recent == 0) return;
+  for (int begin = 0; begin < H; begin += kMovePlaces) take_places(begin, true);
+
+  const int total = p.recent << vshift;
+  for (int base = 0; base < total; base += kMoveThreads * kMoveDepth) {
+    uint4 a[kMoveDepth];
+    int64_t to[kMoveDepth];
+    float w[kMoveDepth];
+#pragma unroll
+    for (int u = 0; u < kMoveDepth; ++u) {
+      const int x = base + u * kMoveThreads + tid;
+      if (x >= total) continue;
+      const int i = x >> vshift, v = x & (V - 1);
+      a[u] = cache[(row_of(L - p.recent + i) << vshift) + v];
+      to[u] = (row_of(H + i) << vshift) + v;
+      if (sums && v == 0) w[u] = p.key_weights[weight_at(bt, L - p.recent + i, shift, Hkv, j)];
     }
     __syncthreads();
-    if (x < total) {
-      row(H + i)[v] = a;
-      if (sums && v == 0) p.key_weights[weight_at(bt, H + i, shift, p.num_kv_heads, j)] = w;
+#pragma unroll
+    for (int u = 0; u < kMoveDepth; ++u) {
+      const int x = base + u * kMoveThreads + tid;
+      if (x >= total) continue;
+      cache[to[u]] = a[u];
+      if (sums && (x & (V - 1)) == 0)
+        p.key_weights[weight_at(bt, H + (x >> vshift), shift, Hkv, j)] = w[u];
     }
   }
 }
@@ -333,13 +438,24 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   prm.budget = budget;
   prm.recent = recent;
   const int room = max_blocks_per_seq * block_size;
-  const int smem = (room / 32 + room / kSuper + 4) * 4;
+  const int smem = SelectSmem(room).bytes();
   int ctas = 0;
   if (!kernel_smem_setup((const void *)evict_select_kernel, kSelThreads, smem, &ctas))
     return PKV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   evict_select_kernel<<<(unsigned)units, kSelThreads, smem, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  evict_move_kernel<<<(unsigned)(2 * units), kMoveThreads, 0, st>>>(prm);
+  const int heavy = budget - recent;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * units),
+                     (unsigned)(heavy > 0 ? (heavy + kMovePlaces - 1) / kMovePlaces : 1));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, prm) != cudaSuccess) return PKV_ERR_CUDA;
   return launch_status();
 }
