@@ -19,12 +19,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;             // selection by digits of 11, 11 and 10 bits
 constexpr int kRankWords = 4;           // bitmap words per entry of the rank table
 constexpr int kMaxContext = 1 << 20;    // the bitmap of kept positions is in shared memory
 constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory
+constexpr int kLongContext = 4096;      // from here on a selecting CTA has 1024 threads, not 256
 constexpr int kMoveThreads = 256;
 constexpr int kMovePlaces = 512;        // places per CTA of the second launch
 constexpr int kMoveDepth = 8;           // 16-byte vectors that a thread has in flight
@@ -67,6 +66,7 @@ __device__ __forceinline__ int64_t weight_at(const int32_t *bt, int i, int shift
 
 // The digit bin of the `need`-th largest among the counted keys; *need becomes
 // the rank inside that bin.  All threads call it and get the same answer.
+template <int kSelThreads>
 __device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int per = kBins / kSelThreads;
@@ -109,7 +109,10 @@ struct SelectSmem {
   __host__ __device__ int bytes() const { return (keys + words + ranks) * 4; }
 };
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
+    evict_select_kernel(const EvictParams p) {
+  constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t dyn[];
   __shared__ int hist[kBins];
   __shared__ int warp_sums[kSelWarps];
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     return order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
   };
   const int cached = min(N, lay.keys);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid; i < cached; i += kSelThreads) keys[i] = read_key(i);
   auto key_at = [&](int i) { return i < cached ? keys[i] : read_key(i); };
 
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       }
     }
     __syncthreads();
-    T |= (uint32_t)pick_bin(hist, warp_sums, found, need) << lo;
+    T |= (uint32_t)pick_bin<kSelThreads>(hist, warp_sums, found, need) << lo;
   }
 
   // Kept: keys above T, and the first `need` of those equal to it.  Each warp
@@ -287,109 +290,102 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 }
 
 // Rows move from kept[i] to i, for the places of this CTA.  Places in [0, H) take
-// rows from positions at or behind H; after them the recent rows move down to
-// [H, budget).  The rows that the recent ones overwrite are read before: the
-// ones that move to places in [0, H), all by the CTA that moves the recent rows
-// and ahead of them; and of the recent rows themselves each step reads before
-// any of its rows is written (a row's new place is never behind its old one).
-// Every other row is read by its CTA and written by none.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
-  __shared__ longlong2 moves[kMovePlaces];  // (from, to): rows of the cache, by (slot, kv head)
-  __shared__ int64_t wmoves[kMovePlaces][2];
+// rows from positions at or behind H, and the recent rows move down to
+// [H, budget).  A CTA lists its moves and does them in batches, each of which
+// reads all of its rows before it writes any.  Rows that some move overwrites
+// are read by the CTA that does, and in time: CTA 0 of a unit moves the recent
+// rows in ascending order (a row's new place is never behind its old one) and,
+// listed before them, every row that they overwrite.  Rows at or behind
+// `budget` that move below H are written by none: the CTAs of a unit share them
+// by place.
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
+  __shared__ int2 moves[kMovePlaces];  // (from, to)
   __shared__ int count;
   const int unit = blockIdx.x >> 1;
   const int s = unit / p.num_kv_heads;
   const int j = unit - s * p.num_kv_heads;
   const int L = p.context_lens[s];
   if (L <= p.budget) return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) count = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
   const int32_t *kept = p.kept + (int64_t)unit * p.budget;
   if (kept[p.budget - 1] < 0) return;  // (a sequence that was refused)
-  const int tid = threadIdx.x, lane = tid & 31;
   const int H = p.budget - p.recent;
   const bool sums = (blockIdx.x & 1) == 0;  // the K units move the weights too
   uint4 *cache = reinterpret_cast<uint4 *>(sums ? p.k_cache : p.v_cache);
   const int shift = p.block_shift, Hkv = p.num_kv_heads;
   const int V = p.row_vecs, vshift = V == 16 ? 4 : 3;
-  auto row_of = [&](int i) { return slot_at(bt, i, shift) * Hkv + j; };
+  auto at = [&](int i, int v) { return ((slot_at(bt, i, shift) * Hkv + j) << vshift) + v; };
+  __syncthreads();
 
-  // With `recent`, CTA 0 of the unit takes the movers that recent rows are to
-  // overwrite, whatever their new place; the others leave those out.
-  const int first = blockIdx.y * kMovePlaces;
-  auto move_listed = [&]() {  // the rows in `moves`: no two touch the same one
-    __syncthreads();
-    const int n = count, total = n << vshift;
-    for (int base = tid; base < total; base += kMoveThreads * kMoveDepth) {
+  auto do_moves = [&](int n) {  // the first n listed
+    const int total = n << vshift;
+    for (int base = 0; base < total; base += kMoveThreads * kMoveDepth) {
       uint4 a[kMoveDepth];
+      float w[kMoveDepth];
 #pragma unroll
       for (int u = 0; u < kMoveDepth; ++u) {
-        const int x = base + u * kMoveThreads;
-        if (x < total) a[u] = cache[(moves[x >> vshift].x << vshift) + (x & (V - 1))];
+        const int x = base + u * kMoveThreads + tid;
+        if (x >= total) break;
+        const int from = moves[x >> vshift].x, v = x & (V - 1);
+        a[u] = cache[at(from, v)];
+        if (sums && v == 0) w[u] = p.key_weights[weight_at(bt, from, shift, Hkv, j)];
       }
+      __syncthreads();
 #pragma unroll
       for (int u = 0; u < kMoveDepth; ++u) {
-        const int x = base + u * kMoveThreads;
-        if (x < total) cache[(moves[x >> vshift].y << vshift) + (x & (V - 1))] = a[u];
-      }
-    }
-    if (sums)
-      for (int x = tid; x < n; x += kMoveThreads) p.key_weights[wmoves[x][1]] = p.key_weights[wmoves[x][0]];
-    __syncthreads();
-  };
-  auto list = [&](int src, int dst, bool take) {  // whole warps
-    const uint32_t all = __ballot_sync(0xffffffffu, take);
-    int at = 0;
-    if (lane == 0 && all) at = atomicAdd(&count, __popc(all));
-    at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1));
-    if (take) {
-      moves[at] = make_longlong2(row_of(src), row_of(dst));
-      if (sums) {
-        wmoves[at][0] = weight_at(bt, src, shift, Hkv, j);
-        wmoves[at][1] = weight_at(bt, dst, shift, Hkv, j);
+        const int x = base + u * kMoveThreads + tid;
+        if (x >= total) break;
+        const int to = moves[x >> vshift].y, v = x & (V - 1);
+        cache[at(to, v)] = a[u];
+        if (sums && v == 0) p.key_weights[weight_at(bt, to, shift, Hkv, j)] = w[u];
       }
     }
   };
-  auto take_places = [&](int begin, bool overwritten) {
-    if (tid == 0) count = 0;
-    __syncthreads();
+  // Lists the moves to places [begin, begin + kMovePlaces): CTA 0 those of rows
+  // that recent ones overwrite, and in a CTA's own run of places the others.
+  auto list_places = [&](int begin, bool own, bool overwritten) {
     for (int x = tid; x < kMovePlaces; x += kMoveThreads) {
       const int i = begin + x;
-      const int src = i < H ? kept[i] : 0;
-      list(src, i, i < H && src != i && (src < p.budget) == overwritten);
-    }
-    move_listed();
-  };
-  if (first < H) take_places(first, false);
-  if (blockIdx.y != 0) return;
-  // (a mover below `budget` can go to any free place below H)
-  if (p.recent == 0) return;
-  for (int begin = 0; begin < H; begin += kMovePlaces) take_places(begin, true);
-
-  const int total = p.recent << vshift;
-  for (int base = 0; base < total; base += kMoveThreads * kMoveDepth) {
-    uint4 a[kMoveDepth];
-    int64_t to[kMoveDepth];
-    float w[kMoveDepth];
-#pragma unroll
-    for (int u = 0; u < kMoveDepth; ++u) {
-      const int x = base + u * kMoveThreads + tid;
-      if (x >= total) continue;
-      const int i = x >> vshift, v = x & (V - 1);
-      a[u] = cache[(row_of(L - p.recent + i) << vshift) + v];
-      to[u] = (row_of(H + i) << vshift) + v;
-      if (sums && v == 0) w[u] = p.key_weights[weight_at(bt, L - p.recent + i, shift, Hkv, j)];
+      const int src = i < H ? kept[i] : i;
+      const bool take = src != i && (src < p.budget ? overwritten : own);
+      const uint32_t all = __ballot_sync(0xffffffffu, take);
+      int first = 0;
+      if (lane == 0 && all) first = atomicAdd(&count, __popc(all));
+      first = __shfl_sync(0xffffffffu, first, 0) + __popc(all & ((1u << lane) - 1));
+      if (take) moves[first] = make_int2(src, i);
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveDepth; ++u) {
-      const int x = base + u * kMoveThreads + tid;
-      if (x >= total) continue;
-      cache[to[u]] = a[u];
-      if (sums && (x & (V - 1)) == 0)
-        p.key_weights[weight_at(bt, H + (x >> vshift), shift, Hkv, j)] = w[u];
+  };
+  const bool lead = blockIdx.y == 0;
+  // (without recent rows nothing is overwritten: no mover is below the budget)
+  const int places = lead && p.recent > 0 ? H : min(H, (int)(blockIdx.y + 1) * kMovePlaces);
+  for (int begin = blockIdx.y * kMovePlaces; begin < places; begin += kMovePlaces) {
+    list_places(begin, begin == (int)blockIdx.y * kMovePlaces, lead);
+    if (begin + kMovePlaces < places) {  // more to list
+      do_moves(count);
+      __syncthreads();
+      if (tid == 0) count = 0;
+      __syncthreads();
     }
   }
+  int n = count;
+  int done = 0;  // recent rows listed so far
+  while (lead && done < p.recent) {
+    const int more = min(p.recent - done, kMovePlaces - n);
+    for (int x = tid; x < more; x += kMoveThreads)
+      moves[n + x] = make_int2(L - p.recent + done + x, H + done + x);
+    n += more;
+    done += more;
+    __syncthreads();
+    if (done == p.recent) break;
+    do_moves(n);
+    __syncthreads();
+    n = 0;
+  }
+  do_moves(n);
 }
 
 }  // namespace
@@ -439,11 +435,18 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   prm.recent = recent;
   const int room = max_blocks_per_seq * block_size;
   const int smem = SelectSmem(room).bytes();
-  int ctas = 0;
-  if (!kernel_smem_setup((const void *)evict_select_kernel, kSelThreads, smem, &ctas))
-    return PKV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<(unsigned)units, kSelThreads, smem, st>>>(prm);
+  // Short contexts: many small CTAs per SM hide one another's barriers; long
+  // ones: more threads for a sequence's keys.  Measured (us): 512 units of 1024
+  // to 1280 tokens SHORT; 128 units of 2000 to 16384 tokens LONG.
+  const bool is_long = room > kLongContext;
+  int ctas = 0;
+  if (!kernel_smem_setup(is_long ? (const void *)evict_select_kernel<1024>
+                                 : (const void *)evict_select_kernel<256>,
+                         is_long ? 1024 : 256, smem, &ctas))
+    return PKV_ERR_CUDA;
+  if (is_long) evict_select_kernel<1024><<<(unsigned)units, 1024, smem, st>>>(prm);
+  else evict_select_kernel<256><<<(unsigned)units, 256, smem, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   const int heavy = budget - recent;
   cudaLaunchConfig_t cfg = {};
