@@ -316,7 +316,9 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  *   key_weights(slot of p, j)  = a[s,j,p]  for p = context_lens[s] - 1
  * (the newest token is this call's own: its slot's old sum was another's).
  * fp32 logits and statistics; the weights are rounded to bf16 for the product
- * with V alone (as the tensor cores take them).
+ * with V alone (as the tensor cores take them).  The batch's tokens are cut
+ * into runs of equal length, so the last bits of a sequence's results can
+ * change with the other sequences' lengths; the same call gives the same bits.
  *
  * workspace: device memory of at least pkv_decode_weights_workspace_size(...)
  * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that

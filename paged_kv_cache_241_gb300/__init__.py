@@ -317,30 +317,38 @@ def paged_prefill_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_
     _check(st, "pkv_paged_prefill_attn")
 
 
-def _need_key_weights(key_weights, k_cache):
+def _check_args(what, key_weights, k_cache, args, dev_status):
+    """The checks of the key-weight calls: every tensor's dtype, rank, layout
+    and device (all on the current one: the library launches there), and
+    key_weights' shape.  args: (name, tensor or None, dtype, rank).  One pass
+    without exceptions or objects: these calls take a few microseconds."""
     import torch
 
+    dev = torch.cuda.current_device() if k_cache.is_cuda else -1
+    for name, t, dtype, ndim in args:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or dev < 0 or
+                              t.dim() != ndim or not t.is_contiguous()):
+            _need(t, dtype, name, ndim)
+            raise ValueError(f"{what}: {name} is not on the current CUDA device")
+    if dev_status is not None and (dev_status.dtype is not torch.int32 or
+                                   dev_status.get_device() != dev or dev_status.numel() < 1):
+        raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
     NB, BS, Hkv, _ = k_cache.shape
-    _need(key_weights, torch.float32, "key_weights", 3)
-    if tuple(key_weights.shape) != (NB, Hkv, BS):
+    if key_weights.shape != (NB, Hkv, BS):
         raise ValueError(f"key_weights: expected [num_blocks, Hkv, block_size] = {(NB, Hkv, BS)}")
+    return dev
 
 
-def _need_status(dev_status):
+def _raw_stream(stream, dev) -> int:
     import torch
 
-    if dev_status is not None:
-        _need(dev_status, torch.int32, "dev_status")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(getattr(stream, "cuda_stream", stream))
 
 
-def _same_device(what, *tensors):
-    """Every tensor on the first one's device, which must be the current one
-    (the library launches on the current device)."""
-    import torch
-
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or devices.pop().index != torch.cuda.current_device():
-        raise ValueError(f"{what}: all tensors must be on the current CUDA device")
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _workspace(n, what, device):
@@ -368,36 +376,29 @@ def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_table
     import torch
 
     lib = load()
-    store = (k, v, slot_mapping)
-    if any(t is None for t in store) and any(t is not None for t in store):
+    if not (k is None) == (v is None) == (slot_mapping is None):
         raise ValueError("paged_decode_weights_attn: k, v and slot_mapping go together")
-    for name, t, dt, nd in (("out", out, torch.bfloat16, 3), ("q", q, torch.bfloat16, 3),
-                            ("k", k, torch.bfloat16, 3), ("v", v, torch.bfloat16, 3),
-                            ("slot_mapping", slot_mapping, torch.int32, 1),
-                            ("k_cache", k_cache, torch.bfloat16, 4),
-                            ("v_cache", v_cache, torch.bfloat16, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("context_lens", context_lens, torch.int32, 1),
-                            ("workspace", workspace, torch.uint8, 1)):
-        if t is not None:
-            _need(t, dt, name, nd)
-    _need_key_weights(key_weights, k_cache)
-    _need_status(dev_status)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _check_args("paged_decode_weights_attn", key_weights, k_cache, (
+        ("out", out, bf16, 3), ("q", q, bf16, 3), ("k", k, bf16, 3), ("v", v, bf16, 3),
+        ("slot_mapping", slot_mapping, i32, 1), ("k_cache", k_cache, bf16, 4),
+        ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
+        ("context_lens", context_lens, i32, 1), ("workspace", workspace, torch.uint8, 1),
+        ("key_weights", key_weights, torch.float32, 3)), dev_status)
     S, Hq, D = q.shape
     NB, BS, Hkv, Dc = k_cache.shape
-    if Dc != D or tuple(out.shape) != (S, Hq, D) or block_tables.shape[0] != S or \
-            context_lens.shape[0] != S or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if Dc != D or out.shape != q.shape or block_tables.shape[0] != S or \
+            context_lens.shape[0] != S or v_cache.shape != k_cache.shape:
         raise ValueError("paged_decode_weights_attn: inconsistent shapes")
-    if k is not None and (tuple(k.shape) != (S, Hkv, D) or tuple(v.shape) != (S, Hkv, D) or
+    if k is not None and (k.shape != (S, Hkv, D) or v.shape != (S, Hkv, D) or
                           slot_mapping.shape[0] != S):
         raise ValueError("paged_decode_weights_attn: inconsistent shapes of the new tokens")
-    _same_device("paged_decode_weights_attn", out, key_weights, q, k_cache, v_cache, block_tables,
-                 context_lens, workspace, k, v, slot_mapping, dev_status)
     st = lib.pkv_paged_decode_weights_attn(
-        _ptr(out), _ptr(key_weights), _ptr(q), _ptr(k), _ptr(v), _ptr(slot_mapping),
-        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Hq, Hkv, D, BS,
-        block_tables.shape[1], NB, int(max_total_blocks), float(scale), _ptr(workspace),
-        workspace.numel(), _ptr(dev_status), _stream(stream))
+        out.data_ptr(), key_weights.data_ptr(), q.data_ptr(), _addr(k), _addr(v),
+        _addr(slot_mapping), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), S, Hq, Hkv, D, BS, block_tables.shape[1], NB,
+        int(max_total_blocks), float(scale), workspace.data_ptr(), workspace.numel(),
+        _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_decode_weights_attn")
 
 
@@ -424,26 +425,22 @@ def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, c
     import torch
 
     lib = load()
-    for name, t, dt, nd in (("q", q, torch.bfloat16, 3), ("k_cache", k_cache, torch.bfloat16, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("cu_seqlens_q", cu_seqlens_q, torch.int32, 1),
-                            ("cu_seqlens_k", cu_seqlens_k, torch.int32, 1),
-                            ("workspace", workspace, torch.uint8, 1)):
-        _need(t, dt, name, nd)
-    _need_key_weights(key_weights, k_cache)
-    _need_status(dev_status)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _check_args("paged_prefill_weights", key_weights, k_cache, (
+        ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
+        ("cu_seqlens_q", cu_seqlens_q, i32, 1), ("cu_seqlens_k", cu_seqlens_k, i32, 1),
+        ("workspace", workspace, torch.uint8, 1),
+        ("key_weights", key_weights, torch.float32, 3)), dev_status)
     T, Hq, D = q.shape
     NB, BS, Hkv, Dc = k_cache.shape
     S = cu_seqlens_q.shape[0] - 1
     if Dc != D or block_tables.shape[0] != S or cu_seqlens_k.shape[0] != S + 1:
         raise ValueError("paged_prefill_weights: inconsistent shapes")
-    _same_device("paged_prefill_weights", key_weights, q, k_cache, block_tables, cu_seqlens_q,
-                 cu_seqlens_k, workspace, dev_status)
     st = lib.pkv_paged_prefill_weights(
-        _ptr(key_weights), _ptr(q), _ptr(k_cache), _ptr(block_tables), _ptr(cu_seqlens_q),
-        _ptr(cu_seqlens_k), S, T, int(max_seqlen_q), _window(window), Hq, Hkv, D, BS,
-        block_tables.shape[1], NB, float(scale), _ptr(workspace), workspace.numel(),
-        _ptr(dev_status), _stream(stream))
+        key_weights.data_ptr(), q.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, T, int(max_seqlen_q),
+        _window(window), Hq, Hkv, D, BS, block_tables.shape[1], NB, float(scale),
+        workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_prefill_weights")
 
 
@@ -456,25 +453,21 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
     import torch
 
     lib = load()
-    for name, t, dt, nd in (("k_cache", k_cache, torch.bfloat16, 4),
-                            ("v_cache", v_cache, torch.bfloat16, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("context_lens", context_lens, torch.int32, 1),
-                            ("kept", kept, torch.int32, 3), ("new_lens", new_lens, torch.int32, 1)):
-        _need(t, dt, name, nd)
-    _need_key_weights(key_weights, k_cache)
-    _need_status(dev_status)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _check_args("kv_evict", key_weights, k_cache, (
+        ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
+        ("block_tables", block_tables, i32, 2), ("context_lens", context_lens, i32, 1),
+        ("kept", kept, i32, 3), ("new_lens", new_lens, i32, 1),
+        ("key_weights", key_weights, torch.float32, 3)), dev_status)
     NB, BS, Hkv, D = k_cache.shape
     S = block_tables.shape[0]
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or context_lens.shape[0] != S or \
-            new_lens.shape[0] != S or tuple(kept.shape) != (S, Hkv, int(budget)):
+    if v_cache.shape != k_cache.shape or context_lens.shape[0] != S or \
+            new_lens.shape[0] != S or kept.shape != (S, Hkv, int(budget)):
         raise ValueError("kv_evict: inconsistent shapes")
-    _same_device("kv_evict", k_cache, v_cache, key_weights, block_tables, context_lens, kept,
-                 new_lens, dev_status)
-    st = lib.pkv_kv_evict(_ptr(k_cache), _ptr(v_cache), _ptr(key_weights), _ptr(block_tables),
-                          _ptr(context_lens), S, Hkv, D, BS, block_tables.shape[1], NB,
-                          int(budget), int(recent), _ptr(kept), _ptr(new_lens), _ptr(dev_status),
-                          _stream(stream))
+    st = lib.pkv_kv_evict(k_cache.data_ptr(), v_cache.data_ptr(), key_weights.data_ptr(),
+                          block_tables.data_ptr(), context_lens.data_ptr(), S, Hkv, D, BS,
+                          block_tables.shape[1], NB, int(budget), int(recent), kept.data_ptr(),
+                          new_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_kv_evict")
 
 

@@ -7,12 +7,14 @@
 // when the whole context has been read, so the logits (4 G bytes a key and kv
 // head, beside the 4 D bytes of its K and V) go through the workspace:
 //
-//  1. Split-K attention.  An item is (chunk of a sequence's tokens, kv head).
-//     It writes its logits (log2 units), its maximum and sum, and its
+//  1. Split-K attention.  All tokens of the batch, sequence after sequence in
+//     tiles, are cut into runs of equal length whatever the sequences' lengths;
+//     a warp takes one run for one kv head.  Of every sequence in its run it
+//     writes the logits (log2 units), and a part: their maximum and sum, and the
 //     unnormalised output.
-//  2. Join, a programmatic dependent launch over the same items: every CTA
-//     joins the maxima and sums of its sequence's chunks, writes its share of
-//     the output, and adds its chunk's weights to the sums.
+//  2. Join, a programmatic dependent launch: every CTA joins the maxima and sums
+//     of a sequence's parts, then adds the weights of its own tokens to the sums
+//     and writes its share of the output.
 #include <math.h>
 
 #include "host_common.h"
@@ -24,10 +26,11 @@ namespace {
 constexpr int kWarpsMost = 8;        // warps per CTA (one CTA per SM)
 constexpr int kStages = 3;           // ring of tiles per warp
 constexpr int kMaxSeqs = 16384;
-constexpr int kMaxChunk = 256;
+constexpr int kMaxWarps = 4096;      // warps of a grid at most (places for parts)
+constexpr int kMinTiles = 4;         // tiles per run at least (parts cost a join)
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 constexpr int kJoinThreads = 256;
-constexpr int kJoinTokens = 2048;    // tokens per CTA of the second launch
+constexpr int kJoinTokens = 1024;    // tokens per CTA of the second launch
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightsParams {
@@ -45,17 +48,17 @@ struct WeightsParams {
   const int32_t *new_slots;
   uint16_t *k_cache_w;
   uint16_t *v_cache_w;
-  int32_t *chunk_prefix;  // [num_seqs + 1]: first chunk of each sequence
-  float *part_ml;         // [chunks, Hkv, G, 2]   (max in log2 units, sum)
-  float *part_o;          // [chunks, Hkv, D, G]
-  float *logits;          // [chunks, Hkv, chunk, G]
+  int32_t *tile_prefix;   // [num_seqs + 1]: first tile of each sequence
+  float *part_ml;         // [num_seqs + runs, Hkv, G, 2]   (max in log2 units, sum)
+  float *part_o;          // [num_seqs + runs, Hkv, D, G]
+  float *logits;          // [tiles, Hkv, tile, G]
   int32_t *status;
   int64_t num_blocks;
-  int64_t max_chunks;
+  int64_t max_tiles;
   int num_seqs;
   int num_kv_heads;
   int block_shift;
-  int chunk;  // tokens per item: 64 << n
+  int runs;   // runs of the batch's tiles at most
   int max_blocks_per_seq;
   float qscale;  // scale * log2(e)
 };
@@ -67,15 +70,16 @@ __device__ __forceinline__ int visible(const WeightsParams &p, int s) {
   return L <= 0 ? 0 : (int)min((int64_t)L, room);
 }
 
-// First chunk of every sequence into prefix[0 .. S] (shared memory), by all
-// threads; returns the number of chunks.
-__device__ int scan_chunks(const WeightsParams &p, int *prefix, int *warp_sums) {
+// First tile of every sequence into prefix[0 .. S] (shared memory), by all
+// threads; returns the number of tiles.
+template <int kRows>
+__device__ int scan_tiles(const WeightsParams &p, int *prefix, int *warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
   const int per = (S + blockDim.x - 1) / blockDim.x;
   const int begin = min(tid * per, S), end = min(begin + per, S);
   int local = 0;
-  for (int s = begin; s < end; ++s) local += (visible(p, s) + p.chunk - 1) / p.chunk;
+  for (int s = begin; s < end; ++s) local += (visible(p, s) + kRows - 1) / kRows;
   int incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -91,22 +95,29 @@ __device__ int scan_chunks(const WeightsParams &p, int *prefix, int *warp_sums) 
   }
   for (int s = begin; s < end; ++s) {
     prefix[s] = run;
-    run += (visible(p, s) + p.chunk - 1) / p.chunk;
+    run += (visible(p, s) + kRows - 1) / kRows;
   }
   if (tid == 0) prefix[S] = total;
   __syncthreads();
   return total;
 }
 
-// The sequence that chunk c belongs to (the last s with prefix[s] <= c).
-__device__ __forceinline__ int seq_of(const int *prefix, int S, int c) {
+// The sequence that tile t belongs to (the last s with prefix[s] <= t).
+__device__ __forceinline__ int seq_of(const int *prefix, int S, int t) {
   int lo = 0, hi = S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= c) lo = mid;
+    if (prefix[mid] <= t) lo = mid;
     else hi = mid - 1;
   }
   return lo;
+}
+
+// Tiles per run.  Run r has tiles [r * n, (r + 1) * n) of the batch; its part of
+// sequence s is filed under s + r: every part begins where a sequence or a run
+// does, so no two have the same number.
+__device__ __forceinline__ int run_tiles(const WeightsParams &p, int tiles) {
+  return max((tiles + p.runs - 1) / p.runs, kMinTiles);
 }
 
 // 16-byte asynchronous copy; zeros instead when !take.
@@ -143,7 +154,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // Shared memory of one warp: a ring of tiles (kRows tokens of K, then of V),
-// and as many places for the query rows of the items in flight.
+// and as many places for the query rows of the sequences in flight.
 template <int D, int G>
 struct WarpSmem {
   static constexpr int kRows = 2048 / D;          // 16 tokens of 128 dims, 32 of 64
@@ -159,10 +170,11 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// First launch.  A warp is by itself: it takes items (a chunk of a sequence's
-// tokens, one kv head) and streams their K and V through its own ring with
-// cp.async, up to two tiles ahead and across items, so nothing in the loop
-// waits for another warp.  Per 16 tokens the products are m16n8k16: S = K q^T
+// First launch.  A warp is by itself: it streams the K and V of its run, for its
+// kv head, through its own ring with cp.async, up to two tiles ahead and across
+// sequences, so nothing in the loop waits for another warp; the warps of the
+// other kv heads of the same tokens run beside it (whole rows of the cache are
+// read at about the same time).  Per 16 tokens the products are m16n8k16: S = K q^T
 // (tokens x dims x heads; the G heads of the group are the columns, of 8) and
 // O^T += V^T P (dims x tokens x heads), in which a lane's two heads are the
 // same in S, in P and in O, so maximum and rescaling need no exchange of O.
@@ -171,9 +183,10 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 template <int D, int G>
 __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(const WeightsParams p) {
   using W = WarpSmem<D, G>;
+  constexpr int kRows = W::kRows;
   constexpr int kCols = D / 8;              // 16-byte columns per row
   constexpr int kRowsPer = 32 / kCols;      // rows per warp-wide copy
-  constexpr int kSlices = W::kRows / 16;
+  constexpr int kSlices = kRows / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ int warp_sums[kWarpsMost];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -182,126 +195,131 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   int *prefix = reinterpret_cast<int *>(smem_raw + warps * W::bytes);  // [S + 1]
   const uint32_t tiles = smem_u32(mine);
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
-  const int S = p.num_seqs, Hkv = p.num_kv_heads, C = p.chunk, shift = p.block_shift;
+  const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
 
-  const int total = scan_chunks(p, prefix, warp_sums);
-  const bool over = total > p.max_chunks;
+  const int total = scan_tiles<kRows>(p, prefix, warp_sums);
+  const bool over = total > p.max_tiles;
   if (blockIdx.x == 0) {
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
       const int L = p.context_lens[s];
       if (L <= 0 || L != visible(p, s)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
     }
     if (over && threadIdx.x == 0) flag_status(p.status, PKV_DEV_WORKSPACE);
-    for (int s = threadIdx.x; s <= S; s += blockDim.x) p.chunk_prefix[s] = over ? 0 : prefix[s];
+    for (int s = threadIdx.x; s <= S; s += blockDim.x) p.tile_prefix[s] = over ? 0 : prefix[s];
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (over) return;
 
-  const int64_t items = (int64_t)total * Hkv;
-  const int64_t stride = (int64_t)gridDim.x * warps;
+  const int per_run = run_tiles(p, total);
+  const int runs = (total + per_run - 1) / per_run;
+  const int64_t jobs = (int64_t)runs * Hkv;  // (run, head), heads innermost
   const uint64_t policy = l2_policy_evict_first();
-
-  // Where an item's tokens are; lane l holds the l-th block id of the chunk.
-  struct Item {
-    int64_t id;
-    int s, j, first, valid, newest, blk;
-  };
-  auto locate = [&](int64_t id, Item &x) {
-    x.id = id;
-    if (id >= items) return;
-    const int c = (int)(id / Hkv);
-    x.j = (int)(id - (int64_t)c * Hkv);
-    x.s = seq_of(prefix, S, c);
-    x.first = (c - prefix[x.s]) * C;
-    const int L = visible(p, x.s);
-    x.valid = min(C, L - x.first);
-    // (a chunk's newest token, as an index into the chunk; only with a store to do)
-    x.newest = p.new_k != nullptr && L == p.context_lens[x.s] ? L - 1 - x.first : -1;
-  };
-  auto fetch_blocks = [&](Item &x) {
-    x.blk = 0;
-    if (x.id < items && lane * 64 < C) {
-      const int i = x.first + (lane << 6);  // (64 tokens are always in one block)
-      if (lane * 64 < x.valid) {
-        x.blk = p.block_tables[(int64_t)x.s * p.max_blocks_per_seq + (i >> shift)];
-        if (x.blk < 0 || x.blk >= p.num_blocks) {
-          flag_status(p.status, PKV_DEV_BAD_BLOCK);
-          x.blk = 0;
-        }
-      }
-    }
-  };
-
-  // The loading side, ahead of the consuming side by up to two tiles.
-  Item in, in_next;
-  int in_tok = 0, in_slot = 0, in_q = 0;
-  locate((int64_t)blockIdx.x * warps + warp, in);
-  fetch_blocks(in);
-  locate(in.id + stride, in_next);
-  fetch_blocks(in_next);
   const int col = lane % kCols, row0 = lane / kCols;
+  for (int64_t job = (int64_t)blockIdx.x * warps + warp; job < jobs;
+       job += (int64_t)gridDim.x * warps) {
+  const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
+  const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
+
+  // The loading side, ahead of the consuming side by up to two tiles: tile in_t
+  // of the batch, at token in_tok of sequence in_s (in_L tokens), in block
+  // blk; blk_next is the block after it, of this sequence or the next one.
+  int in_t = t_begin, in_s = seq_of(prefix, S, t_begin);
+  int in_tok = (t_begin - prefix[in_s]) * kRows;
+  int in_L = visible(p, in_s);
+  int in_slot = 0, in_q = 0;
+  bool in_first = true;  // the sequence's first tile of this run
+  auto block_of = [&](int s, int tok) {
+    int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
+    if (blk < 0 || blk >= p.num_blocks) {
+      if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+      blk = 0;
+    }
+    return blk;
+  };
+  auto next_seq = [&](int s) {  // the next sequence with tokens
+    do ++s; while (s < S && prefix[s + 1] == prefix[s]);
+    return s;
+  };
+  auto block_after = [&]() {
+    const int tok = ((in_tok >> shift) + 1) << shift;
+    if (tok < in_L) return block_of(in_s, tok);
+    const int s = next_seq(in_s);
+    return s < S ? block_of(s, 0) : 0;
+  };
+  int blk = block_of(in_s, in_tok), blk_next = block_after();
   auto issue = [&]() {
-    if (in.id < items) {
-      if (in_tok == 0) {
-        const uint16_t *q = p.q + ((int64_t)in.s * Hkv + in.j) * G * D;
+    if (in_t < t_end) {
+      if (in_first) {
+        const uint16_t *q = p.q + ((int64_t)in_s * Hkv + j) * G * D;
         for (int x = lane; x < G * kCols; x += 32)
           copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
         in_q = in_q + 1 == kStages ? 0 : in_q + 1;
+        in_first = false;
       }
-      const int blk = __shfl_sync(0xffffffffu, in.blk, in_tok >> 6);
-      const int64_t slot = ((int64_t)blk << shift) + ((in.first + in_tok) & ((1 << shift) - 1));
-      const int64_t at = ((slot + row0) * Hkv + in.j) * D + col * 8;
+      const int64_t slot = ((int64_t)blk << shift) + (in_tok & ((1 << shift) - 1));
+      const int64_t at = ((slot + row0) * Hkv + j) * D + col * 8;
       const int64_t step = (int64_t)kRowsPer * Hkv * D;
-      const int64_t fresh = ((int64_t)in.s * Hkv + in.j) * D + col * 8;
+      const int64_t fresh = ((int64_t)in_s * Hkv + j) * D + col * 8;
+      // (the newest token comes from the inputs when the call stores it)
+      const int newest = p.new_k != nullptr && in_L == p.context_lens[in_s] ? in_L - 1 : -1;
       const uint32_t dst = tiles + in_slot * 2 * W::kHalf;
 #pragma unroll
-      for (int i = 0; i < W::kRows / kRowsPer; ++i) {
+      for (int i = 0; i < kRows / kRowsPer; ++i) {
         const int t = in_tok + row0 + i * kRowsPer;
         const uint32_t to = dst + tile_at<D>(row0 + i * kRowsPer, col);
-        const bool is_new = t == in.newest;
-        copy16(to, is_new ? p.new_k + fresh : p.k_cache + at + i * step, t < in.valid, policy);
-        copy16(to + W::kHalf, is_new ? p.new_v + fresh : p.v_cache + at + i * step, t < in.valid, policy);
+        const bool is_new = t == newest;
+        copy16(to, is_new ? p.new_k + fresh : p.k_cache + at + i * step, t < in_L, policy);
+        copy16(to + W::kHalf, is_new ? p.new_v + fresh : p.v_cache + at + i * step, t < in_L, policy);
       }
-      in_tok += W::kRows;
-      if (in_tok >= in.valid) {
-        in_tok = 0;
-        in = in_next;
-        locate(in.id + stride, in_next);
-        fetch_blocks(in_next);
-      }
+      ++in_t;
       in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+      if (in_t < t_end) {
+        in_tok += kRows;
+        const bool ends = in_tok >= in_L;
+        if (ends || (in_tok & ((1 << shift) - 1)) == 0) {
+          if (ends) {
+            in_s = next_seq(in_s);
+            in_tok = 0;
+            in_L = visible(p, in_s);
+            in_first = true;
+          }
+          blk = blk_next;
+          blk_next = block_after();
+        }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue();
 
-  // The consuming side.
+  // The consuming side: sequence after sequence of the run.
   const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
   const bool owner = h0 < G;      // (of the 8 columns only G are heads)
   int slot = 0, qslot = 0;
-  Item x;
-  for (int64_t id = (int64_t)blockIdx.x * warps + warp; id < items; id += stride) {
-    locate(id, x);
+  for (int s = seq_of(prefix, S, t_begin), tile = t_begin; tile < t_end; s = next_seq(s)) {
+    const int L = visible(p, s);
+    const int first = (tile - prefix[s]) * kRows;                  // tokens [first, last) are here
+    const int last = min(L, first + (t_end - tile) * kRows);
     uint32_t qf[D / 16][2];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[D / 16][4];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float *lg = p.logits + id * C * G;
-    for (int tok = 0; tok < x.valid; tok += W::kRows) {
+    for (int tok = first; tok < last; tok += kRows, ++tile) {
+      float *lg = p.logits + ((int64_t)tile * Hkv + j) * kRows * G;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // every lane's copies are in, and the slot filled next is read out
       issue();
-      if (tok == 0) {
+      if (tok == first) {
         // q as the second operand: lane (head, dim pair) per 8 dims.  Rows past
         // G repeat the last one (their columns are not used).
         const uint32_t qa = qslots + qslot * W::kQ;
-        const int r = min(lane & 7, G - 1);
+        const int row = min(lane & 7, G - 1);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t f[4];
-          ldmatrix4(f, qa + tile_at<D>(r, i * 4 + (lane >> 3)));
+          ldmatrix4(f, qa + tile_at<D>(row, i * 4 + (lane >> 3)));
           qf[2 * i][0] = f[0];
           qf[2 * i][1] = f[1];
           qf[2 * i + 1][0] = f[2];
@@ -314,29 +332,30 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
       for (int sl = 0; sl < kSlices; ++sl) {
         // S: rows are tokens (lane / 4 and + 8), columns the lane's two heads.
         float s_even[4] = {0.f, 0.f, 0.f, 0.f}, s_odd[4] = {0.f, 0.f, 0.f, 0.f};
-        const int r = sl * 16 + (lane & 15);
+        const int kr = sl * 16 + (lane & 15);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t a[4];
-          ldmatrix4(a, ka + tile_at<D>(r, 2 * i + (lane >> 4)));
+          ldmatrix4(a, ka + tile_at<D>(kr, 2 * i + (lane >> 4)));
           if (i & 1) mma16816(s_odd, a, qf[i][0], qf[i][1]);
           else mma16816(s_even, a, qf[i][0], qf[i][1]);
         }
-        const int t0 = tok + sl * 16 + (lane >> 2), t1 = t0 + 8;
+        const int i0 = sl * 16 + (lane >> 2), i1 = i0 + 8;  // rows of the tile
+        const bool in0 = tok + i0 < L, in1 = tok + i1 < L;
         float z[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = (s_even[i] + s_odd[i]) * p.qscale;
         if (owner) {
           if (G == 1) {
-            if (t0 < x.valid) lg[t0] = z[0];
-            if (t1 < x.valid) lg[t1] = z[2];
+            if (in0) lg[i0] = z[0];
+            if (in1) lg[i1] = z[2];
           } else {
-            if (t0 < x.valid) *reinterpret_cast<float2 *>(lg + t0 * G + h0) = make_float2(z[0], z[1]);
-            if (t1 < x.valid) *reinterpret_cast<float2 *>(lg + t1 * G + h0) = make_float2(z[2], z[3]);
+            if (in0) *reinterpret_cast<float2 *>(lg + i0 * G + h0) = make_float2(z[0], z[1]);
+            if (in1) *reinterpret_cast<float2 *>(lg + i1 * G + h0) = make_float2(z[2], z[3]);
           }
         }
-        if (t0 >= x.valid) z[0] = z[1] = -INFINITY;
-        if (t1 >= x.valid) z[2] = z[3] = -INFINITY;
+        if (!in0) z[0] = z[1] = -INFINITY;
+        if (!in1) z[2] = z[3] = -INFINITY;
         float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) {
@@ -381,8 +400,9 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
       l0 += __shfl_xor_sync(0xffffffffu, l0, k);
       l1 += __shfl_xor_sync(0xffffffffu, l1, k);
     }
+    const int64_t part = (int64_t)(s + r) * Hkv + j;
     if (owner) {
-      float *po = p.part_o + id * G * D;
+      float *po = p.part_o + part * G * D;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const int d = i * 16 + (lane >> 2);
@@ -395,7 +415,7 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
         }
       }
       if (lane < 4) {
-        float *ml = p.part_ml + (id * G + h0) * 2;
+        float *ml = p.part_ml + (part * G + h0) * 2;
         ml[0] = m0;
         ml[1] = l0;
         if (G > 1) {
@@ -404,13 +424,13 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
         }
       }
     }
-    // The chunk with the newest token stores it (no item of the call reads its slot).
-    if (x.newest >= 0 && x.newest < x.valid) {
-      const int64_t to = p.new_slots[x.s];
+    // The run with the newest token stores it (no run of the call reads its slot).
+    if (p.new_k != nullptr && last == L && L == p.context_lens[s]) {
+      const int64_t to = p.new_slots[s];
       if (to >= 0 && to < p.num_blocks << shift) {
         if (lane < kCols) {
-          const int64_t from = ((int64_t)x.s * Hkv + x.j) * kCols + lane;
-          const int64_t at = (to * Hkv + x.j) * kCols + lane;
+          const int64_t from = ((int64_t)s * Hkv + j) * kCols + lane;
+          const int64_t at = (to * Hkv + j) * kCols + lane;
           reinterpret_cast<uint4 *>(p.k_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_k)[from];
           reinterpret_cast<uint4 *>(p.v_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_v)[from];
         }
@@ -420,10 +440,12 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  }
 }
 
 // Second launch: one CTA per (sequence, kv head, kJoinTokens tokens).  It joins
-// the maxima and sums of all of its sequence's chunks, then adds the weights of
+// the maxima and sums of all of its sequence's parts, then adds the weights of
 // its own tokens and writes its share of the output.
 template <int D, int G>
 __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const WeightsParams p) {
@@ -432,19 +454,24 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
   __shared__ float stat[2][G];   // maximum, 1 / sum
   __shared__ float4 acc_s[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int Hkv = p.num_kv_heads, C = p.chunk, shift = p.block_shift;
+  constexpr int kRows = WarpSmem<D, G>::kRows;
+  const int Hkv = p.num_kv_heads, shift = p.block_shift;
   const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
   const int L = visible(p, s);  // an input of the call: the first launch does not write it
   const int begin = blockIdx.y * kJoinTokens;
   if (begin >= L) return;
   const int newest = p.context_lens[s] - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.chunk_prefix[p.num_seqs] == 0) return;  // the call was refused for want of workspace
-  const int c0 = p.chunk_prefix[s];
-  const int n = (L + C - 1) / C;
-  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + ((int64_t)c0 * Hkv + j) * G;
+  const int tiles = p.tile_prefix[p.num_seqs];
+  const int tile0 = p.tile_prefix[s];
+  if (tiles == 0) return;  // the call was refused for want of workspace
+  const int per_run = run_tiles(p, tiles);
+  const int r0 = tile0 / per_run;                                        // the sequence's runs
+  const int n = (tile0 + (L + kRows - 1) / kRows - 1) / per_run - r0 + 1;
+  const int64_t part0 = (int64_t)(s + r0) * Hkv + j;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + part0 * G;
   const int64_t ml_step = (int64_t)Hkv * G;
-  // Thread (chunk, head): running maximum and sum over its chunks.
+  // Thread (part, head): running maximum and sum over its parts.
   {
     const int g = tid % G;
     float m = -INFINITY, l = 0.f;
@@ -489,59 +516,66 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
   }
   const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
   const int end = min(L, begin + kJoinTokens);
-#pragma unroll 2
-  for (int i = begin + tid; i < end; i += kJoinThreads) {
-    const int c = i / C;
-    const float *lg = p.logits + (((int64_t)(c0 + c) * Hkv + j) * C + (i - c * C)) * G;
-    float z[G];
+  constexpr int kEach = kJoinTokens / kJoinThreads;
+  float z[kEach][G];
+  int blk[kEach];
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) {
+    const int i = begin + tid + x * kJoinThreads;
+    blk[x] = -1;
+    if (i >= end) continue;
+    blk[x] = bt[i >> shift];
+    const float *lg = p.logits + (((int64_t)(tile0 + i / kRows) * Hkv + j) * kRows + i % kRows) * G;
     if constexpr (G >= 4) {
 #pragma unroll
       for (int g = 0; g < G; g += 4) {
         const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
-        z[g] = y.x;
-        z[g + 1] = y.y;
-        z[g + 2] = y.z;
-        z[g + 3] = y.w;
+        z[x][g] = y.x;
+        z[x][g + 1] = y.y;
+        z[x][g + 2] = y.z;
+        z[x][g + 3] = y.w;
       }
     } else if constexpr (G == 2) {
       const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
-      z[0] = y.x;
-      z[1] = y.y;
+      z[x][0] = y.x;
+      z[x][1] = y.y;
     } else {
-      z[0] = __ldcg(lg);
-    }
-    const int blk = bt[i >> shift];
-    float a = 0.f;
-#pragma unroll
-    for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[g] - M[g]), inv[g], a);
-    if (blk >= 0 && blk < p.num_blocks) {
-      float *w = p.key_weights + ((((int64_t)blk * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
-      if (i == newest) *w = a;
-      else atomicAdd(w, a);
+      z[x][0] = __ldcg(lg);
     }
   }
-  // Output: the sequence's CTAs share the D * G values in runs of four; the
-  // threads of a CTA share the chunks.
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) {
+    const int i = begin + tid + x * kJoinThreads;
+    if (blk[x] < 0 || blk[x] >= p.num_blocks) continue;  // (also: past the end)
+    float a = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[x][g] - M[g]), inv[g], a);
+    float *w = p.key_weights + ((((int64_t)blk[x] * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
+    if (i == newest) *w = a;
+    else atomicAdd(w, a);
+  }
+  // Output: the sequence's CTAs share the D * G values, four at a time; the
+  // threads of a CTA share the parts.
   constexpr int kQuads = D * G / 4;
   const int parts = (L + kJoinTokens - 1) / kJoinTokens;
   const int per = (kQuads + parts - 1) / parts;
   const int q0 = min((int)blockIdx.y * per, kQuads), q1 = min(q0 + per, kQuads);
-  const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + ((int64_t)c0 * Hkv + j) * kQuads;
+  const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + part0 * kQuads;
   for (int qb = q0; qb < q1; qb += kJoinThreads) {
     const int width = min(q1 - qb, kJoinThreads);
     const int lanes = kJoinThreads / width;  // threads per quad
-    const int q = qb + tid % width, r0 = tid / width;
+    const int q = qb + tid % width, mine = tid / width;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int e = q * 4;  // value e is dim e / G of head e % G
-    if (r0 < lanes) {
+    if (mine < lanes) {
 #pragma unroll 4
-      for (int r = r0; r < n; r += lanes) {
+      for (int r = mine; r < n; r += lanes) {
         const float4 y = __ldcg(po + (int64_t)r * Hkv * kQuads + q);
         const float *mr = reinterpret_cast<const float *>(ml + r * ml_step);
-        acc.x = fmaf(fast_exp2(__ldcg(mr + 2 * (e % G)) - M[e % G]), y.x, acc.x);
-        acc.y = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 1) % G)) - M[(e + 1) % G]), y.y, acc.y);
-        acc.z = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 2) % G)) - M[(e + 2) % G]), y.z, acc.z);
-        acc.w = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 3) % G)) - M[(e + 3) % G]), y.w, acc.w);
+        acc.x = fmaf(fast_exp2(__ldcg(mr + 2 * (e % G)) - stat[0][e % G]), y.x, acc.x);
+        acc.y = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 1) % G)) - stat[0][(e + 1) % G]), y.y, acc.y);
+        acc.z = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 2) % G)) - stat[0][(e + 2) % G]), y.z, acc.z);
+        acc.w = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 3) % G)) - stat[0][(e + 3) % G]), y.w, acc.w);
       }
     }
     __syncthreads();
@@ -566,34 +600,24 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
   }
 }
 
-// Tokens per item: the largest chunk that still leaves some 4000 items (a GPU runs 1216 warps), for
-// which a batch's context lengths count as long as its block bound allows.
-int chunk_for(int64_t max_total_blocks, int block_size, int num_kv_heads) {
-  int c = kMaxChunk;
-  while (c > 64 && max_total_blocks * block_size / c * num_kv_heads < 4096) c >>= 1;
-  return c;
-}
-
-// Chunks that sequences of at most max_total_blocks blocks in all can have.
-int64_t chunks_for(int64_t max_total_blocks, int block_size, int chunk) {
-  return chunk >= block_size ? max_total_blocks : max_total_blocks * (block_size / chunk);
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Workspace {
   size_t prefix, ml, o, logits, total;
-  Workspace(int64_t S, int64_t Hq, int64_t D, int64_t chunks, int64_t chunk) {
+  // Tokens: all that max_total_blocks blocks hold, in whole tiles.
+  Workspace(int64_t S, int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens) {
+    const int64_t parts = (S + 1) * Hkv + kMaxWarps;  // of a head: num_seqs + runs
+    const int64_t G = Hq / Hkv;
     prefix = 256;
     ml = prefix + align256((size_t)(S + 1) * 4);
-    o = ml + align256((size_t)(chunks * Hq) * 8);
-    logits = o + align256((size_t)(chunks * Hq * D) * 4);
-    total = logits + align256((size_t)(chunks * Hq * chunk) * 4);
+    o = ml + align256((size_t)(parts * G) * 8);
+    logits = o + align256((size_t)(parts * G * D) * 4);
+    total = logits + align256((size_t)(tokens * Hq) * 4);
   }
 };
 
 template <int D, int G>
-pkv_status launch(const WeightsParams &prm, cudaStream_t stream) {
+pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
   const int prefix = (prm.num_seqs + 1) * 4;
@@ -605,12 +629,20 @@ pkv_status launch(const WeightsParams &prm, cudaStream_t stream) {
   if (!kernel_smem_setup((const void *)decode_weights_kernel<D, G>, warps * 32, smem, &ctas))
     return PKV_ERR_CUDA;
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
-  int64_t items = (int64_t)prm.num_seqs * ((room + prm.chunk - 1) / prm.chunk);
-  if (items > prm.max_chunks) items = prm.max_chunks;
-  items *= prm.num_kv_heads;
-  int64_t grid = (items + warps - 1) / warps;
+  const int kRows = WarpSmem<D, G>::kRows;
+  // As many runs as give every warp of the GPU one of a kv head, and no more
+  // than the longest possible batch has.
+  int64_t all = (int64_t)sms * warps;
+  if (all > kMaxWarps) all = kMaxWarps;
+  int64_t runs = all / prm.num_kv_heads;
+  int64_t tiles = (int64_t)prm.num_seqs * ((room + kRows - 1) / kRows);
+  if (tiles > prm.max_tiles) tiles = prm.max_tiles;
+  const int64_t most = (tiles + kMinTiles - 1) / kMinTiles;
+  if (runs > most) runs = most;
+  if (runs < 1) runs = 1;
+  prm.runs = (int)runs;
+  int64_t grid = (runs * prm.num_kv_heads + warps - 1) / warps;
   if (grid > sms) grid = sms;
-  if (grid < 1) grid = 1;
   decode_weights_kernel<D, G><<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -642,11 +674,11 @@ extern "C" size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_head
       block_size > (1 << 16))
     return 0;
   // (bounded so that no product below can wrap)
-  if (max_total_blocks > (int64_t)1 << 40) return 0;
-  const int64_t per_block = (int64_t)num_q_heads * (head_dim + 2 + block_size) * 4 * ((block_size + 63) / 64 + 8);
-  if (max_total_blocks > (INT64_MAX / 2) / per_block) return 0;
-  const int c = chunk_for(max_total_blocks, block_size, num_kv_heads);
-  return Workspace(num_seqs, num_q_heads, head_dim, chunks_for(max_total_blocks, block_size, c), c)
+  if (num_q_heads < num_kv_heads) return 0;
+  if ((double)num_seqs * num_q_heads * head_dim > 1e17) return 0;
+  const int64_t per_token = (int64_t)num_q_heads * 4;
+  if (max_total_blocks > (INT64_MAX / 4) / (per_token * block_size)) return 0;
+  return Workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, max_total_blocks * block_size)
       .total;
 }
 
@@ -690,9 +722,11 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
     return PKV_ERR_WORKSPACE;
 
   WeightsParams prm;
-  prm.chunk = chunk_for(max_total_blocks, block_size, num_kv_heads);
-  prm.max_chunks = chunks_for(max_total_blocks, block_size, prm.chunk);
-  const Workspace lay(num_seqs, num_q_heads, head_dim, prm.max_chunks, prm.chunk);
+  // (32-bit tile numbers; a longer bound admits what they can number)
+  const int rows = 2048 / head_dim;
+  prm.max_tiles = max_total_blocks * block_size / rows;
+  if (prm.max_tiles > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
+  const Workspace lay(num_seqs, num_q_heads, num_kv_heads, head_dim, max_total_blocks * block_size);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   prm.out = out;
   prm.key_weights = key_weights;
@@ -706,7 +740,7 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
   prm.new_slots = slot_mapping;
   prm.k_cache_w = k_cache;
   prm.v_cache_w = v_cache;
-  prm.chunk_prefix = reinterpret_cast<int32_t *>(ws + lay.prefix);
+  prm.tile_prefix = reinterpret_cast<int32_t *>(ws + lay.prefix);
   prm.part_ml = reinterpret_cast<float *>(ws + lay.ml);
   prm.part_o = reinterpret_cast<float *>(ws + lay.o);
   prm.logits = reinterpret_cast<float *>(ws + lay.logits);
@@ -717,6 +751,7 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
   prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.qscale = scale * kLog2e;
+  prm.runs = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define PKV_CASE(DD, GG) \
   if (head_dim == DD && G == GG) return launch<DD, GG>(prm, st);

@@ -84,9 +84,9 @@ def test_weights_workspace_sizes(lib):  # noqa: F811
     f = lib.pkv_decode_weights_workspace_size
     assert f(0, 16, 8, 128, 256, 8) == 0 and f(4, 16, 8, 128, 256, -1) == 0
     assert f(4, 16, 8, 128, 256, 1 << 62) == 0 and f(4, 1 << 20, 8, 128, 256, 8) == 0
-    # it holds at least every block's logits and a partial for each
+    # it holds at least every block's logits
     for mtb in (0, 1, 7, 4000, 1 << 20):
-        assert f(4, 16, 8, 128, 256, mtb) >= mtb * 16 * (256 + 128 + 2) * 4
+        assert f(4, 16, 8, 128, 256, mtb) >= mtb * 16 * 256 * 4
     g = lib.pkv_prefill_weights_workspace_size
     assert g(0, 10, 10, 5, 16, 8, 4, 256) == 0 and g(2, 10, 10, 0, 16, 8, 4, 256) == 0
     assert g(2, 20, 10, 5, 16, 8, 4, 256) >= 2 * 5 * 16 * 4
