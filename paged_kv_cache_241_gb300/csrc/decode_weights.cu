@@ -471,6 +471,36 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
   const int64_t part0 = (int64_t)(s + r0) * Hkv + j;
   const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + part0 * G;
   const int64_t ml_step = (int64_t)Hkv * G;
+  // A thread's tokens: their logits and blocks, asked for before the statistics.
+  const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+  const int end = min(L, begin + kJoinTokens);
+  constexpr int kEach = kJoinTokens / kJoinThreads;
+  float z[kEach][G];
+  int blk[kEach];
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) {
+    const int i = begin + tid + x * kJoinThreads;
+    blk[x] = -1;
+    if (i >= end) continue;
+    blk[x] = bt[i >> shift];
+    const float *lg = p.logits + (((int64_t)(tile0 + i / kRows) * Hkv + j) * kRows + i % kRows) * G;
+    if constexpr (G >= 4) {
+#pragma unroll
+      for (int g = 0; g < G; g += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
+        z[x][g] = y.x;
+        z[x][g + 1] = y.y;
+        z[x][g + 2] = y.z;
+        z[x][g + 3] = y.w;
+      }
+    } else if constexpr (G == 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
+      z[x][0] = y.x;
+      z[x][1] = y.y;
+    } else {
+      z[x][0] = __ldcg(lg);
+    }
+  }
   // Thread (part, head): running maximum and sum over its parts.
   {
     const int g = tid % G;
@@ -507,42 +537,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
     }
     __syncthreads();
   }
-  // Weights: a thread takes a token.
   float M[G], inv[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     M[g] = stat[0][g];
     inv[g] = stat[1][g];
   }
-  const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-  const int end = min(L, begin + kJoinTokens);
-  constexpr int kEach = kJoinTokens / kJoinThreads;
-  float z[kEach][G];
-  int blk[kEach];
-#pragma unroll
-  for (int x = 0; x < kEach; ++x) {
-    const int i = begin + tid + x * kJoinThreads;
-    blk[x] = -1;
-    if (i >= end) continue;
-    blk[x] = bt[i >> shift];
-    const float *lg = p.logits + (((int64_t)(tile0 + i / kRows) * Hkv + j) * kRows + i % kRows) * G;
-    if constexpr (G >= 4) {
-#pragma unroll
-      for (int g = 0; g < G; g += 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
-        z[x][g] = y.x;
-        z[x][g + 1] = y.y;
-        z[x][g + 2] = y.z;
-        z[x][g + 3] = y.w;
-      }
-    } else if constexpr (G == 2) {
-      const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
-      z[x][0] = y.x;
-      z[x][1] = y.y;
-    } else {
-      z[x][0] = __ldcg(lg);
-    }
-  }
+  // Their weights.
 #pragma unroll
   for (int x = 0; x < kEach; ++x) {
     const int i = begin + tid + x * kJoinThreads;

@@ -19,13 +19,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kBins = 2048;             // selection by digits of 11, 11 and 10 bits
+constexpr int kBins = 256;              // selection by digits of 8 bits
+constexpr int kCopies = 8;              // of a bin, side by side: lanes with equal digits collide less
 constexpr int kRankWords = 4;           // bitmap words per entry of the rank table
 constexpr int kMaxContext = 1 << 20;    // the bitmap of kept positions is in shared memory
 constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory
 constexpr int kLongContext = 4096;      // from here on a selecting CTA has 1024 threads, not 256
 constexpr int kMoveThreads = 256;
-constexpr int kMovePlaces = 512;        // places per CTA of the second launch
+constexpr int kMoveList = 1024;         // moves that a CTA can list
+constexpr int kMoveCtas = 2048;         // of the second launch, about
+constexpr int kMinPlaces = 128;         // places per CTA of the second launch at least
 constexpr int kMoveDepth = 8;           // 16-byte vectors that a thread has in flight
 
 struct EvictParams {
@@ -45,6 +48,7 @@ struct EvictParams {
   int max_blocks_per_seq;
   int budget;
   int recent;
+  int places;  // per CTA of the second launch
 };
 
 // Weights as integers of the same order: NaN counts as -inf, -0 as +0.
@@ -66,36 +70,51 @@ __device__ __forceinline__ int64_t weight_at(const int32_t *bt, int i, int shift
 
 // The digit bin of the `need`-th largest among the counted keys; *need becomes
 // the rank inside that bin.  All threads call it and get the same answer.
-template <int kSelThreads>
 __device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int per = kBins / kSelThreads;
-  // Thread t owns bins in descending order: bins kBins - 1 - (t * per + x).
-  int local = 0;
+  int count = 0, incl = 0;
+  if (warp < kBins / 32) {  // thread t has the t-th bin from the top
+    const int4 *bin = reinterpret_cast<const int4 *>(hist + (kBins - 1 - tid) * kCopies);
+    const int4 a = bin[0], b = bin[1];
+    count = (a.x + a.y) + (a.z + a.w) + (b.x + b.y) + (b.z + b.w);
+    incl = count;
 #pragma unroll
-  for (int x = 0; x < per; ++x) local += hist[kBins - 1 - (tid * per + x)];
-  int incl = local;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
   }
-  if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int before = incl - local;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  if (warp < kBins / 32) {
+    int before = incl - count;
 #pragma unroll
-  for (int x = 0; x < per; ++x) {
-    const int c = hist[kBins - 1 - (tid * per + x)];
-    if (before < need && need <= before + c) {
-      found[0] = kBins - 1 - (tid * per + x);
+    for (int w = 0; w < kBins / 32; ++w) before += w < warp ? warp_sums[w] : 0;
+    if (before < need && need <= before + count) {
+      found[0] = kBins - 1 - tid;
       found[1] = need - before;
     }
-    before += c;
   }
   __syncthreads();
   need = found[1];
   return found[0];
+}
+
+// Position of the n-th (from 0) set bit of a word that has more than n.
+__device__ __forceinline__ int nth_bit(uint32_t word, int n) {
+  int base = 0;
+#pragma unroll
+  for (int width = 16; width > 0; width >>= 1) {
+    const int c = __popc(word & ((1u << width) - 1));
+    if (n >= c) {
+      n -= c;
+      word >>= width;
+      base += width;
+    } else {
+      word &= (1u << width) - 1;
+    }
+  }
+  return base;
 }
 
 // Shared memory of the selection: keys, bitmap, rank table.
@@ -106,7 +125,7 @@ struct SelectSmem {
     words = (room + 31) / 32 + kRankWords;
     ranks = words / kRankWords + 2;
   }
-  __host__ __device__ int bytes() const { return (keys + words + ranks) * 4; }
+  __host__ __device__ int bytes() const { return (keys + 2 * words + ranks) * 4; }
 };
 
 template <int kSelThreads>
@@ -114,8 +133,8 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
     evict_select_kernel(const EvictParams p) {
   constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t dyn[];
-  __shared__ int hist[kBins];
-  __shared__ int warp_sums[kSelWarps];
+  __shared__ __align__(16) int hist[kBins * kCopies];
+  __shared__ int warp_sums[2][32];
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / p.num_kv_heads;
@@ -129,120 +148,113 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
   const SelectSmem lay((int)room);
   uint32_t *keys = dyn;
   uint32_t *bits = dyn + lay.keys;  // bit i: position i is kept
-  int *ranks = reinterpret_cast<int *>(bits + lay.words);  // kept positions before each 128
+  uint32_t *equals = bits + lay.words;                      // its key equals the last kept one
+  int *ranks = reinterpret_cast<int *>(equals + lay.words);  // kept positions before each 128
 
-  bool bad = false;
-  if (L < 0 || L > room) {
-    bad = true;
-    if (j == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
-  } else {
-    const int nb = (int)(((int64_t)L + (1 << shift) - 1) >> shift);
+  // Candidates [0, N), of which H are kept; their keys are read as the blocks are checked.
+  const int N = L - p.recent;
+  const int H = p.budget - p.recent;
+  const bool cuts = L > p.budget && L <= room;  // (H < N then)
+  bool bad = L < 0 || L > room;
+  if (bad && j == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+  const int cached = cuts && H > 0 ? min(N, lay.keys) : 0;
+  if (!bad) {
     int wrong = 0;
+    const int nb = (int)(((int64_t)L + (1 << shift) - 1) >> shift);
     for (int b = tid; b < nb; b += kSelThreads) wrong |= bt[b] < 0 || bt[b] >= p.num_blocks;
+#pragma unroll 8
+    for (int i = tid; i < cached; i += kSelThreads) {
+      const int blk = bt[i >> shift];
+      if (blk >= 0 && blk < p.num_blocks)
+        keys[i] = order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
+    }
     bad = __syncthreads_or(wrong) != 0;
     if (bad && j == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
   }
-  if (j == 0 && tid == 0) p.new_lens[s] = (bad || L <= p.budget) ? L : p.budget;
-  if (bad || L <= p.budget) {  // nothing moves
+  if (j == 0 && tid == 0) p.new_lens[s] = cuts && !bad ? p.budget : L;
+  if (bad || !cuts) {  // nothing moves
     for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = (!bad && i < L) ? i : -1;
     return;
   }
-
-  const int N = L - p.recent;            // candidates: positions [0, N)
-  const int H = p.budget - p.recent;     // of which H are kept (H < N)
   for (int i = tid; i < p.recent; i += kSelThreads) kept[H + i] = N + i;
   if (H == 0) return;
-
-  auto read_key = [&](int i) {
-    return order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
+  auto key_at = [&](int i) {
+    return i < cached ? keys[i]
+                      : order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
   };
-  const int cached = min(N, lay.keys);
-#pragma unroll 8
-  for (int i = tid; i < cached; i += kSelThreads) keys[i] = read_key(i);
-  auto key_at = [&](int i) { return i < cached ? keys[i] : read_key(i); };
 
   // The H-th largest key T, digit by digit; `need` of the keys equal to T are
   // kept.  (A thread reads back the keys that it stored.)
   uint32_t T = 0;
   int need = H;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int lo = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const int above = pass == 0 ? 31 : (pass == 1 ? 21 : 10);  // the digits known so far
-    const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+  for (int lo = 24; lo >= 0; lo -= 8) {
+    for (int b = tid; b < kBins * kCopies / 4; b += kSelThreads)
+      reinterpret_cast<int4 *>(hist)[b] = make_int4(0, 0, 0, 0);
     __syncthreads();
     for (int i0 = 0; i0 < N; i0 += kSelThreads) {
       const int i = i0 + tid;
       const uint32_t u = i < N ? key_at(i) : 0u;
-      const bool in = i < N && (pass == 0 || (u >> above) == (T >> above));
+      const bool in = i < N && (lo == 24 || (u >> (lo + 8)) == (T >> (lo + 8)));  // (the digits known so far)
       // Equal digits throughout a warp (weights that are all zero) count at
       // once; others collide little.
       int same;
-      const uint32_t digit = in ? (u >> lo) & mask : kBins;
+      const uint32_t digit = in ? (u >> lo) & (kBins - 1) : kBins;
       __match_all_sync(0xffffffffu, digit, &same);
       if (same) {
-        if (in && lane == 0) atomicAdd(&hist[digit], 32);
+        if (in && lane == 0) atomicAdd(&hist[digit * kCopies], 32);
       } else if (in) {
-        atomicAdd(&hist[digit], 1);
+        atomicAdd(&hist[digit * kCopies + (lane & (kCopies - 1))], 1);
       }
     }
     __syncthreads();
-    T |= (uint32_t)pick_bin<kSelThreads>(hist, warp_sums, found, need) << lo;
+    T |= (uint32_t)pick_bin(hist, warp_sums[0], found, need) << lo;
   }
 
   // Kept: keys above T, and the first `need` of those equal to it.  Each warp
-  // takes a run of whole words of the bitmap, in order.
+  // takes a run of whole entries of the rank table, in order.
   const int words = (N + 31) >> 5;
-  const int per_warp = (words + kSelWarps - 1) / kSelWarps;
-  const int w0 = min(warp * per_warp, words), w1 = min(w0 + per_warp, words);
-  int equal = 0;
+  const int entries = (words + kRankWords - 1) / kRankWords;
+  const int per_warp = ((entries + kSelWarps - 1) / kSelWarps) * kRankWords;
+  const int w0 = min(warp * per_warp, entries * kRankWords);
+  const int w1 = min(w0 + per_warp, entries * kRankWords);
+  int above = 0, equal = 0;
   for (int w = w0; w < w1; ++w) {
     const int i = w * 32 + lane;
     const uint32_t u = i < N ? key_at(i) : 0u;
-    const uint32_t above = __ballot_sync(0xffffffffu, i < N && u > T);
-    const uint32_t eqs = __ballot_sync(0xffffffffu, i < N && u == T);
-    if (lane == 0) bits[w] = above;
-    equal += __popc(eqs);
-  }
-  if (lane == 0) warp_sums[warp] = equal;
-  __syncthreads();
-  int rank = 0;
-  for (int w = 0; w < warp; ++w) rank += warp_sums[w];
-  if (rank < need && equal > 0) {  // some of this warp's equal keys are kept
-    for (int w = w0; w < w1 && rank < need; ++w) {
-      const int i = w * 32 + lane;
-      const bool eq = i < N && key_at(i) == T;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-      const uint32_t take =
-          __ballot_sync(0xffffffffu, eq && rank + __popc(eqs & ((1u << lane) - 1)) < need);
-      if (lane == 0) bits[w] |= take;
-      rank += __popc(eqs);
+    const uint32_t more = __ballot_sync(0xffffffffu, i < N && u > T);
+    const uint32_t same = __ballot_sync(0xffffffffu, i < N && u == T);
+    if (lane == 0) {
+      bits[w] = more;
+      equals[w] = same;
     }
+    above += __popc(more);
+    equal += __popc(same);
   }
-  if (tid < kRankWords) bits[words + tid] = 0;  // (the last entry's words)
+  if (lane == 0) {
+    warp_sums[0][warp] = above;
+    warp_sums[1][warp] = equal;
+  }
   __syncthreads();
-
-  // The rank table: an exclusive scan of the entries' counts, block-wide runs.
-  const int entries = (words + kRankWords - 1) / kRankWords;
-  const int per = (entries + kSelThreads - 1) / kSelThreads;
-  const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
-  int local = 0;
-  for (int e = e0; e < e1; ++e)
-    for (int x = 0; x < kRankWords; ++x) local += __popc(bits[e * kRankWords + x]);
-  int incl = local;
+  int run = 0, rank = 0;  // above T, and equal to it, before this warp's positions
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+  for (int w = 0; w < kSelWarps; ++w) {
+    run += w < warp ? warp_sums[0][w] : 0;
+    rank += w < warp ? warp_sums[1][w] : 0;
   }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  int run = incl - local;
-  for (int w = 0; w < warp; ++w) run += warp_sums[w];
-  for (int e = e0; e < e1; ++e) {
-    ranks[e] = run;
-    for (int x = 0; x < kRankWords; ++x) run += __popc(bits[e * kRankWords + x]);
+  run += min(rank, need);
+  for (int w = w0; w < w1; ++w) {
+    if (lane == 0 && w % kRankWords == 0) ranks[w / kRankWords] = run;
+    const uint32_t same = equals[w];
+    uint32_t word = bits[w];
+    if (same != 0 && rank < need) {
+      const bool take = (same >> lane & 1) && rank + __popc(same & ((1u << lane) - 1)) < need;
+      word |= __ballot_sync(0xffffffffu, take);
+      __syncwarp();
+      if (lane == 0) bits[w] = word;
+    }
+    rank += __popc(same);
+    run += __popc(word);
   }
   __syncthreads();
   auto kept_before = [&](int i) {  // kept positions in [0, i)
@@ -251,41 +263,30 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
     for (int x = w & ~(kRankWords - 1); x < w; ++x) c += __popc(bits[x]);
     return c + __popc(bits[w] & ((1u << (i & 31)) - 1));
   };
-  const int inside = kept_before(H);  // kept tokens that need not move
-  for (int i = tid; i < H; i += kSelThreads) {
-    if ((bits[i >> 5] >> (i & 31)) & 1) {
-      kept[i] = i;
-      continue;
-    }
-    // The free place's number among the free ones gives the mover's among the
-    // kept positions: the entry, the word, then the bit.
-    const int want = inside + (i - kept_before(i));
-    int lo = 0, hi = entries - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (ranks[mid] <= want) lo = mid;
-      else hi = mid - 1;
-    }
-    int left = want - ranks[lo];
-    int w = lo * kRankWords;
-    for (int c = __popc(bits[w]); left >= c; c = __popc(bits[w])) {
-      left -= c;
-      ++w;
-    }
-    uint32_t word = bits[w];
-    int base = 0;
-#pragma unroll
-    for (int width = 16; width > 0; width >>= 1) {
-      const int c = __popc(word & ((1u << width) - 1));
-      if (left >= c) {
-        left -= c;
-        word >>= width;
-        base += width;
-      } else {
-        word &= (1u << width) - 1;
+  for (int i = tid; i < H; i += kSelThreads)
+    if ((bits[i >> 5] >> (i & 31)) & 1) kept[i] = i;
+  // The r-th free place below H takes the r-th kept position behind: each is
+  // looked up by its number, among the free ones or the kept ones before it.
+  const int inside = kept_before(H);
+  for (int r = tid; r < H - inside; r += kSelThreads) {
+    auto find = [&](int want, int free) {  // (free: 1 to count the positions that are not kept)
+      auto before = [&](int e) { return free ? e * kRankWords * 32 - ranks[e] : ranks[e]; };
+      int lo = 0, hi = entries - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before(mid) <= want) lo = mid;
+        else hi = mid - 1;
       }
-    }
-    kept[i] = w * 32 + base;
+      int left = want - before(lo);
+      int w = lo * kRankWords;
+      const uint32_t flip = free ? 0xFFFFFFFFu : 0u;
+      for (int c = __popc(bits[w] ^ flip); left >= c; c = __popc(bits[w] ^ flip)) {
+        left -= c;
+        ++w;
+      }
+      return w * 32 + nth_bit(bits[w] ^ flip, left);
+    };
+    kept[find(r, 1)] = find(inside + r, 0);
   }
 }
 
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
 // `budget` that move below H are written by none: the CTAs of a unit share them
 // by place.
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
-  __shared__ int2 moves[kMovePlaces];  // (from, to)
+  __shared__ int2 moves[kMoveList];  // (from, to)
   __shared__ int count;
   const int unit = blockIdx.x >> 1;
   const int s = unit / p.num_kv_heads;
@@ -344,12 +345,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
       }
     }
   };
-  // Lists the moves to places [begin, begin + kMovePlaces): CTA 0 those of rows
-  // that recent ones overwrite, and in a CTA's own run of places the others.
-  auto list_places = [&](int begin, bool own, bool overwritten) {
-    for (int x = tid; x < kMovePlaces; x += kMoveThreads) {
-      const int i = begin + x;
-      const int src = i < H ? kept[i] : i;
+  // Lists the moves to places [begin, end): CTA 0 those of rows that recent ones
+  // overwrite, and in a CTA's own run of places the others.
+  auto list_places = [&](int begin, int end, bool own, bool overwritten) {
+    for (int x = begin; x < end; x += kMoveThreads) {
+      const int i = x + tid;
+      const int src = i < end ? kept[i] : i;
       const bool take = src != i && (src < p.budget ? overwritten : own);
       const uint32_t all = __ballot_sync(0xffffffffu, take);
       int first = 0;
@@ -360,21 +361,24 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     __syncthreads();
   };
   const bool lead = blockIdx.y == 0;
+  const int first = min(H, (int)blockIdx.y * p.places), end = min(H, first + p.places);
+  list_places(first, end, true, lead);
   // (without recent rows nothing is overwritten: no mover is below the budget)
-  const int places = lead && p.recent > 0 ? H : min(H, (int)(blockIdx.y + 1) * kMovePlaces);
-  for (int begin = blockIdx.y * kMovePlaces; begin < places; begin += kMovePlaces) {
-    list_places(begin, begin == (int)blockIdx.y * kMovePlaces, lead);
-    if (begin + kMovePlaces < places) {  // more to list
-      do_moves(count);
+  for (int begin = end; lead && p.recent > 0 && begin < H; begin += kMoveThreads) {
+    const int listed = count;
+    __syncthreads();  // (all have read it: the next places add to it)
+    if (listed + kMoveThreads > kMoveList) {
+      do_moves(listed);
       __syncthreads();
       if (tid == 0) count = 0;
       __syncthreads();
     }
+    list_places(begin, min(H, begin + kMoveThreads), false, true);
   }
   int n = count;
   int done = 0;  // recent rows listed so far
   while (lead && done < p.recent) {
-    const int more = min(p.recent - done, kMovePlaces - n);
+    const int more = min(p.recent - done, kMoveList - n);
     for (int x = tid; x < more; x += kMoveThreads)
       moves[n + x] = make_int2(L - p.recent + done + x, H + done + x);
     n += more;
@@ -433,6 +437,7 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.budget = budget;
   prm.recent = recent;
+  prm.places = 0;
   const int room = max_blocks_per_seq * block_size;
   const int smem = SelectSmem(room).bytes();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -448,10 +453,17 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   if (is_long) evict_select_kernel<1024><<<(unsigned)units, 1024, smem, st>>>(prm);
   else evict_select_kernel<256><<<(unsigned)units, 256, smem, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  const int heavy = budget - recent;
+  // Enough CTAs to fill the GPU: a unit's places in several parts when there are
+  // few units.
+  const int64_t heavy = budget - recent;
+  const int64_t wanted = (kMoveCtas + 2 * units - 1) / (2 * units);
+  int64_t places = (heavy + wanted - 1) / wanted;
+  if (places < kMinPlaces) places = kMinPlaces;
+  if (places > kMoveList) places = kMoveList;
+  prm.places = (int)places;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * units),
-                     (unsigned)(heavy > 0 ? (heavy + kMovePlaces - 1) / kMovePlaces : 1));
+                     (unsigned)(heavy > 0 ? (heavy + places - 1) / places : 1));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -438,6 +438,12 @@ def test_evict_long_context(lib):
     check_evict(lib, b, 39990, 20000, sums_for(b, 7))
 
 
+@pytest.mark.parametrize("kind", ["few", "zeros"])
+def test_evict_more_candidates_than_the_key_cache_holds(lib, kind):
+    b = batch([70000, 45001], 1, 1, 64, 66, block_size=512)
+    check_evict(lib, b, 30011, 77, special(kind, b))
+
+
 def test_evict_bad_sequences_are_left_as_they_were(lib):
     b = batch([300, 600, 700, 40, 500], 2, 2, 64, 65)
     st = Step(lib, b)
