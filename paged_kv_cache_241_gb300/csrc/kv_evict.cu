@@ -198,11 +198,10 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
       const bool in = i < N && (lo == 24 || (u >> (lo + 8)) == (T >> (lo + 8)));  // (the digits known so far)
       // Equal digits throughout a warp (weights that are all zero) count at
       // once; others collide little.
-      int same;
-      const uint32_t digit = in ? (u >> lo) & (kBins - 1) : kBins;
-      __match_all_sync(0xffffffffu, digit, &same);
-      if (same) {
-        if (in && lane == 0) atomicAdd(&hist[digit * kCopies], 32);
+      const uint32_t digit = (u >> lo) & (kBins - 1);
+      const uint32_t first = __shfl_sync(0xffffffffu, digit, 0);
+      if (__all_sync(0xffffffffu, in && digit == first)) {
+        if (lane == 0) atomicAdd(&hist[digit * kCopies], 32);
       } else if (in) {
         atomicAdd(&hist[digit * kCopies + (lane & (kCopies - 1))], 1);
       }
@@ -348,9 +347,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
   // Lists the moves to places [begin, end): CTA 0 those of rows that recent ones
   // overwrite, and in a CTA's own run of places the others.
   auto list_places = [&](int begin, int end, bool own, bool overwritten) {
-    for (int x = begin; x < end; x += kMoveThreads) {
-      const int i = x + tid;
-      const int src = i < end ? kept[i] : i;
+    int srcs[kMoveList / kMoveThreads];  // (all asked for at once; no run is longer than the list)
+#pragma unroll
+    for (int u = 0; u < kMoveList / kMoveThreads; ++u) {
+      const int i = begin + u * kMoveThreads + tid;
+      srcs[u] = i < end ? kept[i] : i;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveList / kMoveThreads; ++u) {
+      if (begin + u * kMoveThreads >= end) break;
+      const int i = begin + u * kMoveThreads + tid, src = srcs[u];
       const bool take = src != i && (src < p.budget ? overwritten : own);
       const uint32_t all = __ballot_sync(0xffffffffu, take);
       int first = 0;
@@ -364,16 +370,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
   const int first = min(H, (int)blockIdx.y * p.places), end = min(H, first + p.places);
   list_places(first, end, true, lead);
   // (without recent rows nothing is overwritten: no mover is below the budget)
-  for (int begin = end; lead && p.recent > 0 && begin < H; begin += kMoveThreads) {
+  for (int begin = end; lead && p.recent > 0 && begin < H; begin += kMoveList / 2) {
     const int listed = count;
     __syncthreads();  // (all have read it: the next places add to it)
-    if (listed + kMoveThreads > kMoveList) {
+    if (listed > kMoveList / 2) {
       do_moves(listed);
       __syncthreads();
       if (tid == 0) count = 0;
       __syncthreads();
     }
-    list_places(begin, min(H, begin + kMoveThreads), false, true);
+    list_places(begin, min(H, begin + kMoveList / 2), false, true);
   }
   int n = count;
   int done = 0;  // recent rows listed so far
