@@ -29,7 +29,10 @@ constexpr int kMaxSeqs = 16384;
 constexpr int kMaxWarps = 4096;      // warps of a grid at most (places for parts)
 constexpr int kMinTiles = 4;         // tiles per run at least (parts cost a join)
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
-constexpr int kJoinThreads = 256;
+// Threads of the second launch's CTAs: fewer tokens each where a token has eight
+// logits (registers; two long sequences 55.3 -> 54.1 us), more where it has few
+// (a CTA's fixed work counts more; 64 skewed sequences 114 -> 109 us).
+__host__ __device__ constexpr int join_threads(int G) { return G == 8 ? 256 : 128; }
 constexpr int kJoinTokens = 1024;    // tokens per CTA of the second launch
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -448,12 +451,10 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
 // the maxima and sums of all of its sequence's parts, then adds the weights of
 // its own tokens and writes its share of the output.
 template <int D, int G>
-__global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const WeightsParams p) {
-  constexpr int kJoinWarps = kJoinThreads / 32;
-  __shared__ float red[2][kJoinWarps][G];
-  __shared__ float stat[2][G];   // maximum, 1 / sum
+__global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(const WeightsParams p) {
+  constexpr int kJoinThreads = join_threads(G);
   __shared__ float4 acc_s[kJoinThreads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   constexpr int kRows = WarpSmem<D, G>::kRows;
   const int Hkv = p.num_kv_heads, shift = p.block_shift;
   const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
@@ -501,15 +502,27 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
       z[x][0] = __ldcg(lg);
     }
   }
-  // Thread (part, head): running maximum and sum over its parts.
+  // Lane (part, head) of every warp: running maximum and sum over its parts;
+  // then over the parts of all lanes.  (No barrier: a CTA's warps do this alike.)
+  float M[G], inv[G];
   {
-    const int g = tid % G;
+    const int g = lane % G;
     float m = -INFINITY, l = 0.f;
-    for (int r = tid / G; r < n; r += kJoinThreads / G) {
-      const float2 x = __ldcg(ml + r * ml_step + g);
-      const float mn = fmaxf(m, x.x);
+    constexpr int kStep = 32 / G, kBatch = 8;  // (a batch's loads are asked for at once)
+    for (int first = lane / G; first < n; first += kStep * kBatch) {
+      float2 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int r = first + u * kStep;
+        x[u] = r < n ? __ldcg(ml + r * ml_step + g) : make_float2(-INFINITY, 0.f);
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, x[u].x);
       const float ref = mn == -INFINITY ? 0.f : mn;
-      l = l * fast_exp2(m - ref) + x.y * fast_exp2(x.x - ref);
+      l *= fast_exp2(m - ref);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) l = fmaf(x[u].y, fast_exp2(x[u].x - ref), l);
       m = mn;
     }
 #pragma unroll
@@ -521,27 +534,12 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
       l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
       m = mn;
     }
-    if (lane < G) {
-      red[0][warp][lane] = m;
-      red[1][warp][lane] = l;
-    }
-    __syncthreads();
-    if (tid < G) {
-      m = -INFINITY;
-      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[0][w][tid]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      l = 0.f;
-      for (int w = 0; w < kJoinWarps; ++w) l += red[1][w][tid] * fast_exp2(red[0][w][tid] - ref);
-      stat[0][tid] = m;
-      stat[1][tid] = 1.f / l;
-    }
-    __syncthreads();
-  }
-  float M[G], inv[G];
+    l = 1.f / l;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    M[g] = stat[0][g];
-    inv[g] = stat[1][g];
+    for (int x = 0; x < G; ++x) {
+      M[x] = __shfl_sync(0xffffffffu, m, x);
+      inv[x] = __shfl_sync(0xffffffffu, l, x);
+    }
   }
   // Their weights.
 #pragma unroll
@@ -568,15 +566,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
     const int q = qb + tid % width, mine = tid / width;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int e = q * 4;  // value e is dim e / G of head e % G
+    // The value of head (e + x) % G, x < 4.
+    auto of_head = [&](const float (&of)[G], int x) {
+      if constexpr (G == 8) return (e & 4) ? of[4 + x] : of[x];
+      else return of[x % G];
+    };
     if (mine < lanes) {
 #pragma unroll 4
       for (int r = mine; r < n; r += lanes) {
         const float4 y = __ldcg(po + (int64_t)r * Hkv * kQuads + q);
         const float *mr = reinterpret_cast<const float *>(ml + r * ml_step);
-        acc.x = fmaf(fast_exp2(__ldcg(mr + 2 * (e % G)) - stat[0][e % G]), y.x, acc.x);
-        acc.y = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 1) % G)) - stat[0][(e + 1) % G]), y.y, acc.y);
-        acc.z = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 2) % G)) - stat[0][(e + 2) % G]), y.z, acc.z);
-        acc.w = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 3) % G)) - stat[0][(e + 3) % G]), y.w, acc.w);
+        acc.x = fmaf(fast_exp2(__ldcg(mr + 2 * (e % G)) - of_head(M, 0)), y.x, acc.x);
+        acc.y = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 1) % G)) - of_head(M, 1)), y.y, acc.y);
+        acc.z = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 2) % G)) - of_head(M, 2)), y.z, acc.z);
+        acc.w = fmaf(fast_exp2(__ldcg(mr + 2 * ((e + 3) % G)) - of_head(M, 3)), y.w, acc.w);
       }
     }
     __syncthreads();
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_weights_join_kernel(const
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int g = (e + k) % G, d = (e + k) / G;
-        out[g * D + d] = (uint16_t)pack_bf16x2(v[k] * stat[1][g], 0.f);
+        out[g * D + d] = (uint16_t)pack_bf16x2(v[k] * of_head(inv, k), 0.f);
       }
     }
   }
@@ -649,7 +652,7 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(prm.num_seqs * prm.num_kv_heads),
                      (unsigned)((room + kJoinTokens - 1) / kJoinTokens));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(join_threads(G));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
