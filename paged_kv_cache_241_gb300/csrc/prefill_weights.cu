@@ -540,12 +540,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_loads = 0, q_loads = 0;
       bool ok = true;
       const uint32_t in_block = (1u << p.block_shift) - 1;
+      const bool two = in_block < kTile - 1;  // blocks of 64: two per tile
       for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
         const int32_t *bt = p.block_tables + (int64_t)w.s * p.max_blocks_per_seq;
+        // A tile's block ids: one, or of blocks of 64 two, the second of which
+        // may lie past the keys (it is then the first again, unused).  The next
+        // tile's are asked for as a tile is loaded.
+        int near = -1, blk0 = 0, blk1 = 0;  // of tile `near`
+        auto ask_blocks = [&](int kt) {
+          near = kt;
+          const int at1 = kt * kTile + 64;
+          blk0 = bt[(kt * kTile) >> p.block_shift];
+          blk1 = two && at1 < w.q.len_k ? bt[at1 >> p.block_shift] : blk0;
+        };
         auto load_k = [&](int kt) -> bool {
-          // (a tile's second half may lie past the keys: it reads the first half's block, unused)
-          const int at0 = kt * kTile, at1 = at0 + 64 < w.q.len_k ? at0 + 64 : at0;
-          int blk0 = bt[at0 >> p.block_shift], blk1 = bt[at1 >> p.block_shift];
+          if (near != kt) ask_blocks(kt);
           if (blk0 < 0 || blk0 >= p.num_blocks || blk1 < 0 || blk1 >= p.num_blocks) {
             flag_status(p.status, PKV_DEV_BAD_BLOCK);
             if (blk0 < 0 || blk0 >= p.num_blocks) blk0 = 0;
@@ -556,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&k_full[rk.slot], L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < XR; ++x) {
-            tma_load_4d(kd + x * kTile * 128, &tm_k, &k_full[rk.slot], x * 64, w.j, at0 & in_block,
-                        blk0);
-            tma_load_4d(kd + x * kTile * 128 + 64 * 128, &tm_k, &k_full[rk.slot], x * 64, w.j,
-                        at1 & in_block, blk1);
+            uint8_t *region = kd + x * kTile * 128;
+            tma_load_4d(region, &tm_k, &k_full[rk.slot], x * 64, w.j, (kt * kTile) & in_block, blk0);
+            if (two) tma_load_4d(region + 64 * 128, &tm_k, &k_full[rk.slot], x * 64, w.j, 0, blk1);
           }
+          if (kt + 1 < w.q.nkt) ask_blocks(kt + 1);
           ++k_loads;
           rk.next(kKSlots);
           return true;
@@ -1067,12 +1076,13 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   const uint64_t qdims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)total_q};
   const uint64_t qstr[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
   const uint32_t qbox[3] = {64u, (uint32_t)G, (uint32_t)(kTile / G)};
-  // cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
+  // cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 128 tokens (64
+  // of blocks that have no more) x 1 block.
   const uint64_t kdims[4] = {(uint64_t)head_dim, (uint64_t)num_kv_heads, (uint64_t)block_size,
                              (uint64_t)num_blocks};
   const uint64_t kstr[3] = {(uint64_t)head_dim * 2, (uint64_t)num_kv_heads * head_dim * 2,
                             (uint64_t)block_size * num_kv_heads * head_dim * 2};
-  const uint32_t kbox[4] = {64u, 1u, 64u, 1u};
+  const uint32_t kbox[4] = {64u, 1u, (uint32_t)(block_size < kTile ? 64 : kTile), 1u};
   CUtensorMap tq, tk;
   if (!encode_bf16_map(&tq, q, 3, qdims, qstr, qbox, true) ||
       !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true))
