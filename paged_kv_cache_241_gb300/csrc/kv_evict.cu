@@ -49,6 +49,7 @@ struct EvictParams {
   int budget;
   int recent;
   int places;  // per CTA of the second launch
+  int aligned;  // key_weights to 16 bytes
 };
 
 // Weights as integers of the same order: NaN counts as -inf, -0 as +0.
@@ -129,10 +130,10 @@ struct SelectSmem {
 };
 
 template <int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
     evict_select_kernel(const EvictParams p) {
   constexpr int kSelWarps = kSelThreads / 32;
-  extern __shared__ uint32_t dyn[];
+  extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ __align__(16) int hist[kBins * kCopies];
   __shared__ int warp_sums[2][32];
   __shared__ int found[2];
@@ -162,11 +163,17 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
     int wrong = 0;
     const int nb = (int)(((int64_t)L + (1 << shift) - 1) >> shift);
     for (int b = tid; b < nb; b += kSelThreads) wrong |= bt[b] < 0 || bt[b] >= p.num_blocks;
-#pragma unroll 8
-    for (int i = tid; i < cached; i += kSelThreads) {
+    // Four neighbours at a time: they share a block, which has room behind N too.
+#pragma unroll 4
+    for (int i = tid * 4; i < cached; i += kSelThreads * 4) {
       const int blk = bt[i >> shift];
-      if (blk >= 0 && blk < p.num_blocks)
-        keys[i] = order_key(p.key_weights[weight_at(bt, i, shift, p.num_kv_heads, j)]);
+      if (blk < 0 || blk >= p.num_blocks) continue;
+      const float *from = p.key_weights + weight_at(bt, i, shift, p.num_kv_heads, j);
+      float4 w;
+      if (p.aligned) w = *reinterpret_cast<const float4 *>(from);
+      else w = make_float4(from[0], from[1], from[2], from[3]);
+      *reinterpret_cast<uint4 *>(keys + i) =
+          make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
     }
     bad = __syncthreads_or(wrong) != 0;
     if (bad && j == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
@@ -192,20 +199,20 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
     for (int b = tid; b < kBins * kCopies / 4; b += kSelThreads)
       reinterpret_cast<int4 *>(hist)[b] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i0 = 0; i0 < N; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint32_t u = i < N ? key_at(i) : 0u;
-      const bool in = i < N && (lo == 24 || (u >> (lo + 8)) == (T >> (lo + 8)));  // (the digits known so far)
-      // Equal digits throughout a warp (weights that are all zero) count at
-      // once; others collide little.
-      const uint32_t digit = (u >> lo) & (kBins - 1);
-      const uint32_t first = __shfl_sync(0xffffffffu, digit, 0);
-      if (__all_sync(0xffffffffu, in && digit == first)) {
-        if (lane == 0) atomicAdd(&hist[digit * kCopies], 32);
-      } else if (in) {
-        atomicAdd(&hist[digit * kCopies + (lane & (kCopies - 1))], 1);
-      }
+    int *mine = hist + (lane & (kCopies - 1));
+    auto count = [&](uint32_t u) {
+      if (lo == 24 || (u >> (lo + 8)) == (T >> (lo + 8)))  // (the digits known so far)
+        atomicAdd(mine + ((u >> lo) & (kBins - 1)) * kCopies, 1);
+    };
+#pragma unroll 2
+    for (int i = tid * 4; i < cached; i += kSelThreads * 4) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(keys + i);
+      count(u.x);
+      if (i + 1 < N) count(u.y);
+      if (i + 2 < N) count(u.z);
+      if (i + 3 < N) count(u.w);
     }
+    for (int i = cached + tid; i < N; i += kSelThreads) count(key_at(i));
     __syncthreads();
     T |= (uint32_t)pick_bin(hist, warp_sums[0], found, need) << lo;
   }
@@ -242,18 +249,32 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads)
     rank += w < warp ? warp_sums[1][w] : 0;
   }
   run += min(rank, need);
-  for (int w = w0; w < w1; ++w) {
-    if (lane == 0 && w % kRankWords == 0) ranks[w / kRankWords] = run;
-    const uint32_t same = equals[w];
-    uint32_t word = bits[w];
-    if (same != 0 && rank < need) {
-      const bool take = (same >> lane & 1) && rank + __popc(same & ((1u << lane) - 1)) < need;
-      word |= __ballot_sync(0xffffffffu, take);
-      __syncwarp();
-      if (lane == 0) bits[w] = word;
+  for (int base = w0; base < w1; base += 32) {  // a word per lane
+    const int w = base + lane;
+    const uint32_t same = w < w1 ? equals[w] : 0u;
+    uint32_t word = w < w1 ? bits[w] : 0u;
+    int before = __popc(same);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
     }
-    rank += __popc(same);
-    run += __popc(word);
+    const int all_same = __shfl_sync(0xffffffffu, before, 31);
+    const int left = need - (rank + before - __popc(same));  // of this word's, so many are kept
+    if (left >= __popc(same)) word |= same;
+    else if (left > 0) word |= same & ((1u << nth_bit(same, left)) - 1);
+    int kept_to = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, kept_to, o);
+      if (lane >= o) kept_to += y;
+    }
+    if (w < w1) {
+      bits[w] = word;
+      if (w % kRankWords == 0) ranks[w / kRankWords] = run + kept_to - __popc(word);
+    }
+    rank += all_same;
+    run += __shfl_sync(0xffffffffu, kept_to, 31);
   }
   __syncthreads();
   auto kept_before = [&](int i) {  // kept positions in [0, i)
@@ -444,6 +465,7 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   prm.budget = budget;
   prm.recent = recent;
   prm.places = 0;
+  prm.aligned = aligned16(key_weights) ? 1 : 0;
   const int room = max_blocks_per_seq * block_size;
   const int smem = SelectSmem(room).bytes();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
