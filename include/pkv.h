@@ -327,11 +327,13 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its
  * row of out is left as it was; one that is longer than its table is flagged
  * and clamped, and all of its weights are added.  A block id out of range is
- * flagged, its weights are dropped and the sequence's output is undefined.
- * More blocks than max_total_blocks: PKV_DEV_WORKSPACE, nothing is written.
+ * flagged, its weights are dropped and what else the sequence gets is undefined.
+ * More tokens than max_total_blocks blocks hold: PKV_DEV_WORKSPACE, nothing is
+ * written.
  *
- * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in
- * {64, 128, 256, 512}; num_seqs <= 16384.
+ * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
+ * block_size in {64, 128, 256, 512}; num_seqs <= 16384; max_blocks_per_seq *
+ * block_size at most 65535 * 1024.
  */
 pkv_status pkv_paged_decode_weights_attn(
     uint16_t *out, float *key_weights, const uint16_t *q, const uint16_t *new_k,
@@ -361,14 +363,17 @@ size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max
  * window >= max_seqlen_q counts every query.  A sequence with n = 0 changes
  * nothing.  One whose lengths do not fit (n > max_seqlen_q, n > len_k, more
  * keys than its table holds) is flagged, PKV_DEV_BAD_SEQLEN, and left out; a
- * block id out of range is flagged and its keys' sums are left as they were.
+ * block id out of range is flagged, its keys' sums are left as they were, and
+ * the sequence's others are undefined.
  *
  * workspace: device memory of at least pkv_prefill_weights_workspace_size(...)
  * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that
- * overlap on the device must not share a workspace.
+ * overlap on the device must not share a workspace.  How the work is split
+ * depends on the batch, and with it the last bits; the same call gives the same
+ * bits (keys in shared blocks apart).
  *
- * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in
- * {64, 128, 256, 512}; max_blocks_per_seq * block_size at most 2^20.
+ * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
+ * block_size in {64, 128, 256, 512}; max_blocks_per_seq * block_size at most 2^20.
  */
 pkv_status pkv_paged_prefill_weights(
     float *key_weights, const uint16_t *q, const uint16_t *k_cache, const int32_t *block_tables,

@@ -406,13 +406,15 @@ def prefill_weights_workspace(num_seqs, total_q, max_seqlen_q, window, num_q_hea
                               max_blocks_per_seq, block_size, device="cuda"):
     """Allocate a zero-filled workspace for paged_prefill_weights."""
     n = int(load().pkv_prefill_weights_workspace_size(
-        num_seqs, total_q, max_seqlen_q, _window(window), num_q_heads, num_kv_heads,
+        num_seqs, total_q, max_seqlen_q, _c_int32(window), num_q_heads, num_kv_heads,
         max_blocks_per_seq, block_size))
     return _workspace(n, "prefill_weights_workspace", device)
 
 
-def _window(window) -> int:
-    return min(int(window), 0x7FFFFFFF)
+def _c_int32(x) -> int:
+    """An int argument as the library sees it: what does not fit stays too large
+    or becomes -1 (refused there), instead of wrapping around."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
 
 
 def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, cu_seqlens_k,
@@ -438,8 +440,8 @@ def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, c
         raise ValueError("paged_prefill_weights: inconsistent shapes")
     st = lib.pkv_paged_prefill_weights(
         key_weights.data_ptr(), q.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
-        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, T, int(max_seqlen_q),
-        _window(window), Hq, Hkv, D, BS, block_tables.shape[1], NB, float(scale),
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, T, _c_int32(max_seqlen_q),
+        _c_int32(window), Hq, Hkv, D, BS, block_tables.shape[1], NB, float(scale),
         workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_prefill_weights")
 
@@ -466,7 +468,8 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
         raise ValueError("kv_evict: inconsistent shapes")
     st = lib.pkv_kv_evict(k_cache.data_ptr(), v_cache.data_ptr(), key_weights.data_ptr(),
                           block_tables.data_ptr(), context_lens.data_ptr(), S, Hkv, D, BS,
-                          block_tables.shape[1], NB, int(budget), int(recent), kept.data_ptr(),
+                          block_tables.shape[1], NB, _c_int32(budget), _c_int32(recent),
+                          kept.data_ptr(),
                           new_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_kv_evict")
 

@@ -469,9 +469,10 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   const int room = max_blocks_per_seq * block_size;
   const int smem = SelectSmem(room).bytes();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Short contexts: many small CTAs per SM hide one another's barriers; long
-  // ones: more threads for a sequence's keys.  Measured (us): 512 units of 1024
-  // to 1280 tokens SHORT; 128 units of 2000 to 16384 tokens LONG.
+  // Short contexts: small CTAs, several per SM, hide one another's barriers; long
+  // ones: more threads for a sequence's keys.  Measured, both sides: 512 units of
+  // 1025 to 1280 tokens 42.4 us with 256 threads and 58.2 with 1024; 128 units of
+  // 2000 to 16384 tokens 66.0 and 51.2.
   const bool is_long = room > kLongContext;
   int ctas = 0;
   if (!kernel_smem_setup(is_long ? (const void *)evict_select_kernel<1024>

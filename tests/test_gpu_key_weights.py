@@ -464,6 +464,69 @@ def test_evict_bad_sequences_are_left_as_they_were(lib):
         assert torch.equal(a[other].view(torch.uint8), c[other].view(torch.uint8))
 
 
+def off_by_one(t):
+    """The same values 4 bytes past a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 1, device=t.device, dtype=t.dtype)
+    moved = flat[1:].view(t.shape)
+    moved.copy_(t)
+    return moved
+
+
+def test_sums_that_are_aligned_to_their_values_alone(lib):
+    b = batch([300, 1100, 64], 4, 2, 64, 67)
+    ref, st = Step(lib, b), Step(lib, b)
+    st.kw = off_by_one(st.kw)
+    outs = []
+    for x in (ref, st):
+        kept = torch.empty((3, 2, 200), dtype=torch.int32, device="cuda")
+        new_lens = torch.empty((3,), dtype=torch.int32, device="cuda")
+        x.decode_weights()
+        x.prefill_weights(4)
+        lib.kv_evict(x.k_cache, x.v_cache, x.kw, x.block_tables, x.context_lens, 200, 30, kept, new_lens, x.status)
+        assert x.status_value() == 0
+        outs.append((x.out, x.kw, x.k_cache, x.v_cache, kept))
+    for a, c in zip(*outs):
+        assert torch.equal(a, c)
+
+
+def test_prefill_is_the_same_every_time(lib):
+    # Tiles cut between CTAs are joined by whichever finishes last, in one order.
+    b = prompts([900, 300, 64, 1200], [100, 0, 700, 0], 2, 2, 128, 68)
+    st = Step(lib, b)
+    ws = lib.prefill_weights_workspace(4, b.q.shape[0], 1200, 1 << 20, 4, 2, b.block_tables.shape[1], 256)
+    want = None
+    for window in (1 << 20, 48) * 10:
+        st.kw.copy_(torch.from_numpy(st.sums0))
+        st.prefill_weights(window, ws=ws)
+        if want is None:
+            want = {}
+        if window not in want:
+            want[window] = st.kw.clone()
+        assert torch.equal(st.kw, want[window])
+    assert st.status_value() == 0
+
+
+def test_workspaces_serve_calls_of_other_sizes(lib):
+    # One workspace of each kind, as large as any call needs, for a mix of calls.
+    dws = lib.decode_weights_workspace(8, 16, 2, 128, 64, 400)
+    pws = lib.prefill_weights_workspace(8, 2000, 2000, 1 << 20, 16, 2, 64, 512)
+    for seed in range(6):
+        rng = np.random.default_rng(seed)
+        G, D, bs = int(rng.choice([1, 2, 4, 8])), int(rng.choice([64, 128])), int(rng.choice([64, 256]))
+        lens = rng.integers(1, 700, size=int(rng.integers(1, 8))).tolist()
+        b = batch(lens, G, 2, D, seed, block_size=bs)
+        st, ref = Step(lib, b), Step(lib, b)
+        st.decode_weights(ws=dws)
+        ref.decode_weights()
+        assert torch.equal(st.out, ref.out) and torch.equal(st.kw, ref.kw)
+        b = prompts(lens, rng.integers(0, 300, size=len(lens)).tolist(), G, 2, D, seed, block_size=bs)
+        st, ref = Step(lib, b), Step(lib, b)
+        window = int(rng.choice([3, 40, 1 << 20]))
+        st.prefill_weights(window, ws=pws)
+        ref.prefill_weights(window)
+        assert torch.equal(st.kw, ref.kw)
+
+
 # ------------------------------------------------- streams, graphs, calls together
 
 def test_two_streams_with_workspaces_of_their_own(lib):

@@ -221,3 +221,9 @@ def test_manager_evict_may_release_shared_tail_blocks(lib):  # noqa: F811
     with pytest.raises(pkv.PkvError):
         bm.evict(2, 4)
     assert [bm.ref_count(int(b)) for b in bm.block_table(2, 5)] == [2, 2, 2, 2, 1]
+
+
+def test_int_arguments_do_not_wrap():
+    # 2**32 + 5 must not reach the library as 5
+    assert pkv._c_int32((1 << 32) + 5) == 0x7FFFFFFF and pkv._c_int32(-(1 << 32) + 5) == -1
+    assert pkv._c_int32(7) == 7 and pkv._c_int32(0) == 0
