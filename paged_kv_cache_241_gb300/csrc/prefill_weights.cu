@@ -773,9 +773,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (PASS == 1) {
           const int last = w.sees(t, row);
           const int most = __reduce_max_sync(0xffffffffu, last);
+          const int least = __reduce_min_sync(0xffffffffu, last);
           for (int x = x0 + ((side - k) & 3); x < x1; x += kGroups) {
             ok = wait_product();
             if (!ok) break;
+            if (qs > 0.f && x * kTile + kTile - 1 <= least) {  // every key, by every row of the warp
+#pragma unroll 2
+              for (int c = 0; c < kTile / 32; ++c) {
+                float v[32];
+                float top;
+                tmem_load32_max(ta + c * 32, v, top);
+                if (c + 1 == kTile / 32) release_product();
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+                const float mn = fmaxf(mine.x, top * qs);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
+                  const float2 z1 = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, nref);
+                  sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+                  sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+                }
+                sum0 = __fadd2_rn(sum0, sum1);
+                mine.y = fmaf(mine.y, fast_exp2(mine.x - ref), sum0.x + sum0.y);
+                mine.x = mn;
+              }
+              continue;
+            }
             // Runs of 32 keys, up to the last that any of the warp's rows sees.
             const int runs = min((most - x * kTile + 32) >> 5, kTile / 32);
             if (runs <= 0) release_product();
@@ -788,32 +813,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c + 1 == runs) release_product();  // (the product is read: the next one may come)
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               float mn, ref;
-              if (qs > 0.f && __all_sync(0xffffffffu, shown >= 31)) {
-                mn = fmaxf(mine.x, top * qs);
-                ref = mn == -INFINITY ? 0.f : mn;
-                const float2 nref = make_float2(-ref, -ref);
+              // Keys past the row's position are hidden; a scale that is not
+              // positive puts the largest logit elsewhere.
+              top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float2 z = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, nref);
-                  sum[(i >> 1) & 1] =
-                      __fadd2_rn(sum[(i >> 1) & 1], make_float2(fast_exp2(z.x), fast_exp2(z.y)));
-                }
-              } else {
-                // Keys past the row's position are hidden; a scale that is not
-                // positive puts the largest logit elsewhere.
-                top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  v[i] = i <= shown ? v[i] * qs : -INFINITY;
-                  top = fmaxf(top, v[i]);
-                }
-                mn = fmaxf(mine.x, top);
-                ref = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                  sum[(i >> 1) & 1] = __fadd2_rn(
-                      sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
+              for (int i = 0; i < 32; ++i) {
+                v[i] = i <= shown ? v[i] * qs : -INFINITY;
+                top = fmaxf(top, v[i]);
               }
+              mn = fmaxf(mine.x, top);
+              ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                sum[(i >> 1) & 1] = __fadd2_rn(
+                    sum[(i >> 1) & 1], make_float2(fast_exp2(v[i] - ref), fast_exp2(v[i + 1] - ref)));
               mine.y = mine.y * fast_exp2(mine.x - ref) +
                        ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
               mine.x = mn;
