@@ -31,6 +31,8 @@
 // products and exponentials of different steps overlap.
 #include <math.h>
 
+#include <type_traits>
+
 #include "host_common.h"
 #include "pkv_common.cuh"
 
@@ -43,26 +45,30 @@ constexpr int kIssuers = 2;
 constexpr int kThreads = 128 + kGroups * 128;
 constexpr int kBufs = kGroups;   // S buffers of 128 columns: all of tensor memory
 constexpr int kKeep = 2;         // row tiles that stay in their slots for a whole head
-constexpr int kStatSlots = 4;    // row tiles' denominators (second pass)
+constexpr int kStatSlots = 8;    // row tiles' denominators (second pass)
+constexpr int kStatAhead = 4;    // of them on their way at a time
 constexpr int kMaxTokens = 1 << 20;  // of a sequence (a head's steps are counted in 32 bits)
 constexpr int kMaxCtas = 512;    // places for cut tiles in the workspace (CTAs of a grid at most)
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+template <int D, int PASS>
 struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kQSlots = 2;  // (3 and 3 K slots, D = 128: no faster either way)
-  static constexpr int kKSlots = D == 128 ? 4 : 6;
+  // Row tiles stream in the second pass (8 whole prompts: 58 us with 2 and 4 slots,
+  // 55 with 3 and 3 or 4 and 2; a window of 32, where keys stream there too, 21, 21
+  // and 23), keys in the first.
+  static constexpr int kQSlots = PASS == 1 ? 2 : 3;
+  static constexpr int kKSlots = (D == 128 ? 6 : 8) - kQSlots;
   static constexpr int q = 0;
   static constexpr int k = q + kQSlots * kTileBytes;
   static constexpr int bars = k + kKSlots * kTileBytes;
   // q_full/q_empty[Q], st_empty[T], k_full/k_empty[K], s_full/s_empty[B],
-  // x_full/x_empty[quarter][2], drain
+  // x_empty[quarter][2], drain
   static constexpr int kNumBars =
-      2 * kQSlots + kStatSlots + 2 * kKSlots + 2 * kBufs + 16 + 1;
+      2 * kQSlots + kStatSlots + 2 * kKSlots + 2 * kBufs + 8 + 1;
   static constexpr int stat = (bars + kNumBars * 8 + 15) & ~15;  // [T][128] -log2 denominators
-  static constexpr int ex = stat + kStatSlots * kTile * 4;       // [2][groups - 1][128] (maximum, sum)
-  static constexpr int misc = ex + 2 * (kGroups - 1) * kTile * 8;  // tensor memory address, abort, run, scan
+  static constexpr int ex = stat + kStatSlots * kTile * 4;       // [2][groups][128] (maximum, sum)
+  static constexpr int misc = ex + 2 * kGroups * kTile * 8;  // tensor memory address, abort, run, scan
   static constexpr int total = misc + 512;
   // One CTA per SM (it takes all of tensor memory): more than half of an SM's
   // shared memory, so that a second one never waits for tensor memory.
@@ -159,14 +165,16 @@ __device__ __forceinline__ int steps_of_keys(const PromptParams &p, const Seq &q
 // A run's length counts a tile's beginning and end too, and a head's, as so many
 // steps ahead of it: with one row tile per head and a key tile or two, they are
 // most of the work.  Measured: window of 32 queries, 16 prompts of 64 to 4096
-// tokens, 47.7 us without and 40.4 us with them; 8 whole prompts 110.7 and 99.5.
+// tokens, 47.7 us without and 40.4 us with them; 8 whole prompts 110.7 and 99.5,
+// and 93.3 with a second pass's tile (joined between the groups, filed and added)
+// counted as two steps.
 template <int PASS>
 struct Order {
   // Second pass: so few row tiles that they stay in their slots for the whole
   // head, else each step loads its own.
   static __device__ __forceinline__ bool keeps(const Seq &q) { return PASS == 2 && q.nrt <= kKeep; }
   static __device__ __forceinline__ int tiles(const Seq &q) { return PASS == 1 ? q.nrt : q.nkt; }
-  static __device__ __forceinline__ int per_tile(const Seq &q) { return keeps(q) ? 0 : 1; }
+  static __device__ __forceinline__ int per_tile(const Seq &q) { return keeps(q) ? 0 : PASS; }
   static __device__ __forceinline__ int per_head(const Seq &q) { return keeps(q) ? 2 : 0; }
   // Where tile m of a head starts.
   static __device__ __forceinline__ int start(const PromptParams &p, const Seq &q, int m) {
@@ -289,6 +297,11 @@ __device__ __forceinline__ void tmem_load32_max(uint32_t taddr, float (&v)[32], 
       : "memory");
 }
 
+// Copy 4 bytes to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async4(float *dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A count in shared memory that one warp raises and others wait for.
 __device__ __forceinline__ void count_set(int *count, int n) {
   asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
@@ -296,6 +309,15 @@ __device__ __forceinline__ void count_set(int *count, int n) {
 __device__ __forceinline__ int count_get(const int *count) {
   int n;
   asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
+  return n;
+}
+// Raise it by one and return what it was.
+__device__ __forceinline__ int count_add(int *count) {
+  int n;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+               : "=r"(n)
+               : "r"(smem_u32(count))
+               : "memory");
   return n;
 }
 // Whole warp: wait until the count has passed n, as long as a barrier's wait may last.
@@ -455,10 +477,11 @@ template <int D, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k, const PromptParams p) {
-  using L = Layout<D>;
+  using L = Layout<D, PASS>;
   constexpr int XR = D / 64;  // 128-byte regions across D
   constexpr int kKSlots = L::kKSlots, kQSlots = L::kQSlots;
-  static_assert(kStatSlots == 4 && kBufs == 4 && kIssuers == 2, "by the low bits of a count");
+  static_assert((kStatSlots & (kStatSlots - 1)) == 0 && kBufs == 4 && kIssuers == 2,
+                "by the low bits of a count");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -470,17 +493,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *k_empty = k_full + kKSlots;
   uint64_t *s_full = k_empty + kKSlots;
   uint64_t *s_empty = s_full + kBufs;
-  uint64_t *x_full = s_empty + kBufs;
-  uint64_t *x_empty = x_full + 8;
+  uint64_t *x_empty = s_empty + kBufs;
   uint64_t *drain = x_empty + 8;
   float *stat = reinterpret_cast<float *>(smem + L::stat);
   float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
   int *stats_in = reinterpret_cast<int *>(smem + L::misc + 8);  // row tiles whose denominators are in
-  Run *run = reinterpret_cast<Run *>(smem + L::misc + 16);
-  int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 128);
-  static_assert(sizeof(Run) <= 112 && 128 + kThreads / 32 * 8 + sizeof(Seq) <= 512, "");
+  int *parts_in = reinterpret_cast<int *>(smem + L::misc + 16);  // groups that are through with a tile, [quarter][2]
+  Run *run = reinterpret_cast<Run *>(smem + L::misc + 48);
+  int64_t *scratch = reinterpret_cast<int64_t *>(smem + L::misc + 160);
+  static_assert(sizeof(Run) <= 112 && 160 + kThreads / 32 * 8 + sizeof(Seq) <= 512, "");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -499,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_empty[i], 4);
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&x_full[i], kGroups - 1);
       mbar_init(&x_empty[i], 1);
+      parts_in[i] = 0;
     }
     mbar_init(drain, kIssuers);
     *abort_flag = 0;
@@ -702,21 +725,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < 4) p.tickets[blockIdx.x * 4 + lane] = 0;
       int q_loads = 0;
       bool ok = true;
+      const int apart = 32 >> p.group_shift;  // queries from a lane's row to its next
+      // All but the last `ahead` row tiles asked for are in.
+      auto tell = [&](auto ahead) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(decltype(ahead)::value) : "memory");
+        __syncwarp();
+        if (lane == 0) count_set(stats_in, q_loads - (int)decltype(ahead)::value);
+      };
       for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
+        // (asynchronous copies, kStatAhead row tiles in flight: one row tile every
+        // 500 cycles instead of 1200, a step's products taking about 900)
+        const float *mine = p.neg_lse + w.stat_at(0, lane);  // this lane's of row tile 0
         auto fill = [&](int rt) -> bool {
-          float neg[4];
+          const int slot = q_loads & (kStatSlots - 1);
+          if (!warp_wait(&st_empty[slot], ((q_loads / kStatSlots) & 1) ^ 1, abort_flag)) return false;
+          float *to = stat + slot * kTile + lane;
+          const float *from = mine + (int64_t)(rt << tq_shift(p)) * p.num_q_heads;
+          const int left = w.q.R - (rt << tq_shift(p)) - (lane >> p.group_shift);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int row = i * 32 + lane;
-            neg[i] = w.sees(rt, row) >= 0 ? __ldcg(p.neg_lse + w.stat_at(rt, row)) : -INFINITY;
+            if (i * apart < left) cp_async4(to + i * 32, from + (int64_t)i * apart * p.num_q_heads);
+            else to[i * 32] = -INFINITY;
           }
-          const int slot = q_loads & 3;
-          if (!warp_wait(&st_empty[slot], ((q_loads >> 2) & 1) ^ 1, abort_flag)) return false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) stat[slot * kTile + i * 32 + lane] = neg[i];
-          __syncwarp();
+          asm volatile("cp.async.commit_group;" ::: "memory");
           ++q_loads;
-          if (lane == 0) count_set(stats_in, q_loads);
+          tell(std::integral_constant<int, kStatAhead - 1>());
           return true;
         };
         if (w.keeps()) {
@@ -729,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = x0; ok && x < x1; ++x) ok = fill(x);
         }
       }
+      tell(std::integral_constant<int, 0>());
     }
   } else {
     // ---- exponentials and sums: a group of four warps for each S buffer ----
@@ -835,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           k += x1 - x0;
         } else {
           const int key = t * kTile + row;
-          if ((keeps || side == 0) && key < w.q.len_k)
+          if (key < w.q.len_k)
             blk = p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
           const int skip = keeps ? 0 : (side - k) & 3, by = keeps ? 1 : kGroups;
           float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
@@ -853,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float v[32];
               tmem_load32(ta + c0, v);
               if (c0 + 32 >= rows) release_product();  // (the product is read: the next one may come)
-              const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & 3) * kTile + c0);
+              const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & (kStatSlots - 1)) * kTile + c0);
               if (open && c0 + 32 <= rows) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
@@ -882,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (this group alone used the step's denominators: it releases them for all)
             if (!keeps) {
               __syncwarp();
-              if (lane == 0) mbar_arrive_n(&st_empty[load & 3], kGroups);
+              if (lane == 0) mbar_arrive_n(&st_empty[load & (kStatSlots - 1)], kGroups);
             }
           }
           mine.y = (acc0.x + acc0.y) + (acc1.x + acc1.y);
@@ -893,27 +927,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
 
-        // The tile ends here.  Steps taken in turn: the first group gets the
-        // others' parts, warp from warp.
+        // The tile ends here.  Steps taken in turn: the last of the groups to
+        // arrive, warp by warp, joins the parts of all, in order; none waits for
+        // the others (8 whole prompts 94.8 -> 93.2 us).
         if (!keeps) {
           const int buf = swaps & 1, bar = quarter * 2 + buf;
-          const uint32_t phase = (swaps >> 1) & 1;
-          ++swaps;
-          float2 *part = ex + buf * (kGroups - 1) * kTile + row;
-          if (side != 0) {
-            ok = warp_wait(&x_empty[bar], phase ^ 1, abort_flag);
-            if (!ok) break;
-            part[(side - 1) * kTile] = mine;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&x_full[bar]);
-            continue;
-          }
-          ok = warp_wait(&x_full[bar], phase, abort_flag);
+          ok = warp_wait(&x_empty[bar], ((swaps >> 1) & 1) ^ 1, abort_flag);
           if (!ok) break;
-#pragma unroll
-          for (int x = 0; x < kGroups - 1; ++x) mine = join(mine, part[x * kTile]);
+          ++swaps;
+          float2 *part = ex + buf * kGroups * kTile + row;
+          part[side * kTile] = mine;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&x_empty[bar]);
+          int in = 0;
+          if (lane == 0) in = count_add(&parts_in[bar]);
+          in = __shfl_sync(0xffffffffu, in, 0);
+          __syncwarp();
+          if (in != kGroups - 1) continue;
+          mine = part[0];
+#pragma unroll
+          for (int x = 1; x < kGroups; ++x) mine = join(mine, part[x * kTile]);
+          __syncwarp();
+          if (lane == 0) {
+            parts_in[bar] = 0;
+            mbar_arrive(&x_empty[bar]);
+          }
         }
         if (x0 != b0 || x1 != b1) {
           // A part of a tile that several CTAs share: filed by CTA, place 0 if
@@ -948,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (keeps) {  // every group releases the head's denominators
         __syncwarp();
-        for (int x = 0; ok && lane == 0 && x < w.q.nrt; ++x) mbar_arrive(&st_empty[(q_loads + x) & 3]);
+        for (int x = 0; ok && lane == 0 && x < w.q.nrt; ++x) mbar_arrive(&st_empty[(q_loads + x) & (kStatSlots - 1)]);
         q_loads += w.q.nrt;
       }
     }
@@ -981,7 +1018,7 @@ struct Plan {
 template <int D>
 pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const PromptParams &prm,
                   int64_t most_steps, cudaStream_t stream) {
-  constexpr int smem = Layout<D>::total + 1024;
+  constexpr int smem = Layout<D, 1>::total + 1024;
   const int sms = device_sm_count();
   int ctas = 0;
   if (sms <= 0 ||
