@@ -23,7 +23,9 @@ constexpr int kBins = 256;              // selection by digits of 8 bits
 constexpr int kCopies = 8;              // of a bin, side by side: lanes with equal digits collide less
 constexpr int kRankWords = 4;           // bitmap words per entry of the rank table
 constexpr int kMaxContext = 1 << 20;    // the bitmap of kept positions is in shared memory
-constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory
+constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory, at most
+constexpr int kKeepEquals = 1 << 18;    // tables up to here also keep a bitmap of the equal keys
+constexpr int kSelectBytes = 216 << 10; // shared memory of the selection, beside its counters
 constexpr int kLongContext = 4096;      // from here on a selecting CTA has 1024 threads, not 256
 constexpr int kMoveThreads = 256;
 constexpr int kMoveList = 1024;         // moves that a CTA can list
@@ -118,15 +120,20 @@ __device__ __forceinline__ int nth_bit(uint32_t word, int n) {
   return base;
 }
 
-// Shared memory of the selection: keys, bitmap, rank table.
+// Shared memory of the selection: keys, bitmaps, rank table.  The table's length
+// sizes the bitmaps; past kKeepEquals positions (32 KB a bitmap) the second one
+// is counted again instead, and the keys take what is left (14 K of them at 2^20).
 struct SelectSmem {
-  int keys, words, ranks;  // entries
+  int keys, words, equals, ranks;  // entries
   __host__ __device__ SelectSmem(int room) {
-    keys = room < kKeyCache ? room : kKeyCache;
     words = (room + 31) / 32 + kRankWords;
+    equals = room <= kKeepEquals ? words : 0;
     ranks = words / kRankWords + 2;
+    const int left = (kSelectBytes / 4 - words - equals - ranks) & ~3;
+    keys = left < kKeyCache ? left : kKeyCache;
+    if (room < keys) keys = room;
   }
-  __host__ __device__ int bytes() const { return (keys + 2 * words + ranks) * 4; }
+  __host__ __device__ int bytes() const { return (keys + words + equals + ranks) * 4; }
 };
 
 template <int kSelThreads>
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
   uint32_t *keys = dyn;
   uint32_t *bits = dyn + lay.keys;  // bit i: position i is kept
   uint32_t *equals = bits + lay.words;                      // its key equals the last kept one
-  int *ranks = reinterpret_cast<int *>(equals + lay.words);  // kept positions before each 128
+  int *ranks = reinterpret_cast<int *>(equals + lay.equals);  // kept positions before each 128
 
   // Candidates [0, N), of which H are kept; their keys are read as the blocks are checked.
   const int N = L - p.recent;
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
     const uint32_t same = __ballot_sync(0xffffffffu, i < N && u == T);
     if (lane == 0) {
       bits[w] = more;
-      equals[w] = same;
+      if (lay.equals > 0) equals[w] = same;
     }
     above += __popc(more);
     equal += __popc(same);
@@ -251,7 +258,16 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
   run += min(rank, need);
   for (int base = w0; base < w1; base += 32) {  // a word per lane
     const int w = base + lane;
-    const uint32_t same = w < w1 ? equals[w] : 0u;
+    uint32_t same = 0;
+    if (lay.equals > 0) {
+      same = w < w1 ? equals[w] : 0u;
+    } else {
+      for (int x = base; x < min(base + 32, w1); ++x) {
+        const int i = x * 32 + lane;
+        const uint32_t all = __ballot_sync(0xffffffffu, i < N && key_at(i) == T);
+        if (w == x) same = all;
+      }
+    }
     uint32_t word = w < w1 ? bits[w] : 0u;
     int before = __popc(same);
 #pragma unroll

@@ -444,6 +444,15 @@ def test_evict_more_candidates_than_the_key_cache_holds(lib, kind):
     check_evict(lib, b, 30011, 77, special(kind, b))
 
 
+@pytest.mark.parametrize("pad,lens", [(384, [70000, 300]), (512, [140000]), (1978, [35333]), (876, [600000])])
+@pytest.mark.parametrize("kind", ["few", "random"])
+def test_evict_with_a_long_table(lib, pad, lens, kind):
+    """Tables up to the 2^20 tokens that a call may have, of contexts shorter and as long."""
+    b = batch(lens, 1, 1, 64, 68, block_size=512, max_blocks_pad=pad)
+    assert b.block_tables.shape[1] * 512 <= 1 << 20
+    check_evict(lib, b, 5003, 77, sums_for(b, 8) if kind == "random" else special(kind, b))
+
+
 def test_evict_bad_sequences_are_left_as_they_were(lib):
     b = batch([300, 600, 700, 40, 500], 2, 2, 64, 65)
     st = Step(lib, b)
