@@ -460,9 +460,12 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
   const int L = visible(p, s);  // an input of the call: the first launch does not write it
   const int begin = blockIdx.y * kJoinTokens;
-  if (begin >= L) return;
+  // (The launch must not end before the first one has, or a next call on the
+  // stream could share the workspace with it: one CTA always waits.)
+  if (begin >= L && (blockIdx.x | blockIdx.y) != 0) return;
   const int newest = p.context_lens[s] - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (begin >= L) return;
   const int tiles = p.tile_prefix[p.num_seqs];
   const int tile0 = p.tile_prefix[s];
   if (tiles == 0) return;  // the call was refused for want of workspace

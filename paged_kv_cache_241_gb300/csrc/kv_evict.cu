@@ -24,9 +24,11 @@ constexpr int kCopies = 8;              // of a bin, side by side: lanes with eq
 constexpr int kRankWords = 4;           // bitmap words per entry of the rank table
 constexpr int kMaxContext = 1 << 20;    // the bitmap of kept positions is in shared memory
 constexpr int kKeyCache = 40 << 10;     // candidates whose keys stay in shared memory, at most
-constexpr int kKeepEquals = 1 << 18;    // tables up to here also keep a bitmap of the equal keys
+constexpr int kKeepEquals = 1 << 18;    // tables up to here also keep a bitmap of the equal keys (the
+                                        // selections of 256 threads always: kLongContext)
 constexpr int kSelectBytes = 216 << 10; // shared memory of the selection, beside its counters
 constexpr int kLongContext = 4096;      // from here on a selecting CTA has 1024 threads, not 256
+static_assert(kLongContext <= kKeepEquals, "");
 constexpr int kMoveThreads = 256;
 constexpr int kMoveList = 1024;         // moves that a CTA can list
 constexpr int kMoveCtas = 2048;         // of the second launch, about
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
     const uint32_t same = __ballot_sync(0xffffffffu, i < N && u == T);
     if (lane == 0) {
       bits[w] = more;
-      if (lay.equals > 0) equals[w] = same;
+      if (kSelThreads == 256 || lay.equals > 0) equals[w] = same;
     }
     above += __popc(more);
     equal += __popc(same);
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
   for (int base = w0; base < w1; base += 32) {  // a word per lane
     const int w = base + lane;
     uint32_t same = 0;
-    if (lay.equals > 0) {
+    if (kSelThreads == 256 || lay.equals > 0) {
       same = w < w1 ? equals[w] : 0u;
     } else {
       for (int x = base; x < min(base + 32, w1); ++x) {
@@ -342,10 +344,13 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
   const int s = unit / p.num_kv_heads;
   const int j = unit - s * p.num_kv_heads;
   const int L = p.context_lens[s];
-  if (L <= p.budget) return;
+  // (The launch must not end before the first one has: what follows on the stream
+  // reads that one's outputs.  One CTA waits for it whatever there is to move.)
+  if (L <= p.budget && (blockIdx.x | blockIdx.y) != 0) return;
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) count = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (L <= p.budget) return;
   const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
   const int32_t *kept = p.kept + (int64_t)unit * p.budget;
   if (kept[p.budget - 1] < 0) return;  // (a sequence that was refused)

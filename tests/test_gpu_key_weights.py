@@ -473,6 +473,28 @@ def test_evict_bad_sequences_are_left_as_they_were(lib):
         assert torch.equal(a[other].view(torch.uint8), c[other].view(torch.uint8))
 
 
+def test_evict_outputs_are_there_for_the_next_kernel_when_nothing_moves(lib):
+    """All sequences within the budget: the second launch has nothing to do, and must
+    not let the stream go on before the first one has written its outputs."""
+    S, Hkv, budget = 512, 8, 8192
+    kc, vc = (torch.zeros((S, 64, Hkv, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    kw = torch.zeros((S, Hkv, 64), device="cuda")
+    tables = torch.arange(S, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    lens = (torch.arange(S, device="cuda") % 64 + 1).int()
+    kept = torch.empty((S, Hkv, budget), dtype=torch.int32, device="cuda")
+    new_lens = torch.empty((S,), dtype=torch.int32, device="cuda")
+    at = torch.arange(budget, dtype=torch.int32, device="cuda")
+    want = torch.where(at < lens[:, None], at, -1)[:, None, :]
+    seen = torch.empty_like(kept)
+    for _ in range(20):
+        kept.fill_(99)
+        new_lens.fill_(99)
+        lib.kv_evict(kc, vc, kw, tables, lens, budget, 16, kept, new_lens)
+        lens_seen = new_lens.clone()
+        seen.copy_(kept)
+        assert torch.equal(lens_seen, lens) and (seen == want).all()
+
+
 def off_by_one(t):
     """The same values 4 bytes past a 16-byte boundary."""
     flat = torch.empty(t.numel() + 1, device=t.device, dtype=t.dtype)
