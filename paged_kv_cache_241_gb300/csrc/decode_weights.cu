@@ -74,33 +74,34 @@ __device__ __forceinline__ int visible(const WeightsParams &p, int s) {
 }
 
 // First tile of every sequence into prefix[0 .. S] (shared memory), by all
-// threads; returns the number of tiles.
+// threads; returns the number of tiles.  (Summed in 64 bits: lengths that the
+// workspace has no room for may be any; the prefix holds for those that fit.)
 template <int kRows>
-__device__ int scan_tiles(const WeightsParams &p, int *prefix, int *warp_sums) {
+__device__ int64_t scan_tiles(const WeightsParams &p, int *prefix, int64_t *warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_seqs;
   const int per = (S + blockDim.x - 1) / blockDim.x;
   const int begin = min(tid * per, S), end = min(begin + per, S);
-  int local = 0;
+  int64_t local = 0;
   for (int s = begin; s < end; ++s) local += (visible(p, s) + kRows - 1) / kRows;
-  int incl = local;
+  int64_t incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int run = incl - local, total = 0;
+  int64_t run = incl - local, total = 0;
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
     if (w < warp) run += warp_sums[w];
     total += warp_sums[w];
   }
   for (int s = begin; s < end; ++s) {
-    prefix[s] = run;
+    prefix[s] = (int)run;
     run += (visible(p, s) + kRows - 1) / kRows;
   }
-  if (tid == 0) prefix[S] = total;
+  if (tid == 0) prefix[S] = (int)total;
   __syncthreads();
   return total;
 }
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   constexpr int kRowsPer = 32 / kCols;      // rows per warp-wide copy
   constexpr int kSlices = kRows / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ int warp_sums[kWarpsMost];
+  __shared__ int64_t warp_sums[kWarpsMost];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5;
   uint8_t *mine = smem_raw + warp * W::bytes;
@@ -200,8 +201,9 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
   const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
 
-  const int total = scan_tiles<kRows>(p, prefix, warp_sums);
-  const bool over = total > p.max_tiles;
+  const int64_t all = scan_tiles<kRows>(p, prefix, warp_sums);
+  const bool over = all > p.max_tiles;
+  const int total = (int)all;
   if (blockIdx.x == 0) {
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
       const int L = p.context_lens[s];

@@ -200,6 +200,24 @@ def test_decode_context_longer_than_the_table(lib):
     assert_weights(st.kw, st.sums0 + brought, brought, weight_rtol(b, ekc), "clamped: all added")
 
 
+def test_decode_stops_at_lengths_that_add_up_past_32_bits(lib):
+    """The sum of the tiles of all sequences is 2^32 less a few: far more than the
+    workspace has room for, and negative in 32 bits."""
+    S, blocks = 1024, 131070
+    b = batch([5], 1, 1, 128, 19, block_size=512)
+    st = Step(lib, b)
+    q = torch.zeros((S, 1, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    tables = torch.zeros((S, blocks), dtype=torch.int32, device="cuda")
+    lens = torch.full((S,), blocks * 512, dtype=torch.int32, device="cuda")
+    assert S * (blocks * 512 // 16) > 2**31 and (S * (blocks * 512 // 16)) % 2**32 > 2**31
+    ws = lib.decode_weights_workspace(S, 1, 1, 128, 512, 4)
+    before = st.kw.clone()
+    lib.paged_decode_weights_attn(out, st.kw, q, st.k_cache, st.v_cache, tables, lens, 1.0, ws, 4, dev_status=st.status)
+    assert st.status_value() == lib.DEV_WORKSPACE
+    assert (out == 7.0).all() and torch.equal(before, st.kw)
+
+
 def test_decode_nan_stays_in_its_sequence(lib):
     b = batch([40, 300], 2, 2, 64, 25)
     st = Step(lib, b)
