@@ -33,7 +33,11 @@ constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_1
 // logits (registers; two long sequences 55.3 -> 54.1 us), more where it has few
 // (a CTA's fixed work counts more; 64 skewed sequences 114 -> 109 us).
 __host__ __device__ constexpr int join_threads(int G) { return G == 8 ? 256 : 128; }
-constexpr int kJoinTokens = 1024;    // tokens per CTA of the second launch
+constexpr int kJoinTokens = 1024;    // tokens that a CTA of the second launch takes at a time
+// CTAs of the second launch, about: the table may be far longer than the contexts,
+// and past this many a CTA takes several parts of its sequence rather than the
+// launch having one for every part that the table has room for.
+constexpr int kJoinCtas = 16384;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightsParams {
@@ -449,9 +453,9 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   }
 }
 
-// Second launch: one CTA per (sequence, kv head, kJoinTokens tokens).  It joins
-// the maxima and sums of all of its sequence's parts, then adds the weights of
-// its own tokens and writes its share of the output.
+// Second launch: one CTA per (sequence, kv head, kJoinTokens tokens), or several
+// such parts of a sequence.  It joins the maxima and sums of all of its sequence's
+// runs, then adds the weights of its own tokens and writes its share of the output.
 template <int D, int G>
 __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(const WeightsParams p) {
   constexpr int kJoinThreads = join_threads(G);
@@ -479,34 +483,37 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   const int64_t ml_step = (int64_t)Hkv * G;
   // A thread's tokens: their logits and blocks, asked for before the statistics.
   const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-  const int end = min(L, begin + kJoinTokens);
   constexpr int kEach = kJoinTokens / kJoinThreads;
   float z[kEach][G];
   int blk[kEach];
+  auto ask = [&](int begin) {
+    const int end = min(L, begin + kJoinTokens);
 #pragma unroll
-  for (int x = 0; x < kEach; ++x) {
-    const int i = begin + tid + x * kJoinThreads;
-    blk[x] = -1;
-    if (i >= end) continue;
-    blk[x] = bt[i >> shift];
-    const float *lg = p.logits + (((int64_t)(tile0 + i / kRows) * Hkv + j) * kRows + i % kRows) * G;
-    if constexpr (G >= 4) {
+    for (int x = 0; x < kEach; ++x) {
+      const int i = begin + tid + x * kJoinThreads;
+      blk[x] = -1;
+      if (i >= end) continue;
+      blk[x] = bt[i >> shift];
+      const float *lg = p.logits + (((int64_t)(tile0 + i / kRows) * Hkv + j) * kRows + i % kRows) * G;
+      if constexpr (G >= 4) {
 #pragma unroll
-      for (int g = 0; g < G; g += 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
-        z[x][g] = y.x;
-        z[x][g + 1] = y.y;
-        z[x][g + 2] = y.z;
-        z[x][g + 3] = y.w;
+        for (int g = 0; g < G; g += 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(lg + g));
+          z[x][g] = y.x;
+          z[x][g + 1] = y.y;
+          z[x][g + 2] = y.z;
+          z[x][g + 3] = y.w;
+        }
+      } else if constexpr (G == 2) {
+        const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
+        z[x][0] = y.x;
+        z[x][1] = y.y;
+      } else {
+        z[x][0] = __ldcg(lg);
       }
-    } else if constexpr (G == 2) {
-      const float2 y = __ldcg(reinterpret_cast<const float2 *>(lg));
-      z[x][0] = y.x;
-      z[x][1] = y.y;
-    } else {
-      z[x][0] = __ldcg(lg);
     }
-  }
+  };
+  ask(begin);
   // Lane (part, head) of every warp: running maximum and sum over its parts;
   // then over the parts of all lanes.  (No barrier: a CTA's warps do this alike.)
   float M[G], inv[G];
@@ -546,22 +553,30 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
       inv[x] = __shfl_sync(0xffffffffu, l, x);
     }
   }
-  // Their weights.
+  // Their weights, and those of the CTA's further parts.
+  auto add = [&](int begin) {
 #pragma unroll
-  for (int x = 0; x < kEach; ++x) {
-    const int i = begin + tid + x * kJoinThreads;
-    if (blk[x] < 0 || blk[x] >= p.num_blocks) continue;  // (also: past the end)
-    float a = 0.f;
+    for (int x = 0; x < kEach; ++x) {
+      const int i = begin + tid + x * kJoinThreads;
+      if (blk[x] < 0 || blk[x] >= p.num_blocks) continue;  // (also: past the end)
+      float a = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[x][g] - M[g]), inv[g], a);
-    float *w = p.key_weights + ((((int64_t)blk[x] * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
-    if (i == newest) *w = a;
-    else atomicAdd(w, a);
+      for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[x][g] - M[g]), inv[g], a);
+      float *w = p.key_weights + ((((int64_t)blk[x] * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
+      if (i == newest) *w = a;
+      else atomicAdd(w, a);
+    }
+  };
+  add(begin);
+  const int stride = gridDim.y * kJoinTokens;
+  for (int more = begin + stride; more < L; more += stride) {
+    ask(more);
+    add(more);
   }
   // Output: the sequence's CTAs share the D * G values, four at a time; the
   // threads of a CTA share the parts.
   constexpr int kQuads = D * G / 4;
-  const int parts = (L + kJoinTokens - 1) / kJoinTokens;
+  const int parts = min((L + kJoinTokens - 1) / kJoinTokens, (int)gridDim.y);
   const int per = (kQuads + parts - 1) / parts;
   const int q0 = min((int)blockIdx.y * per, kQuads), q1 = min(q0 + per, kQuads);
   const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + part0 * kQuads;
@@ -655,8 +670,10 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   decode_weights_kernel<D, G><<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(prm.num_seqs * prm.num_kv_heads),
-                     (unsigned)((room + kJoinTokens - 1) / kJoinTokens));
+  const int64_t units = (int64_t)prm.num_seqs * prm.num_kv_heads;
+  int64_t parts = (room + kJoinTokens - 1) / kJoinTokens;
+  if (parts * units > kJoinCtas) parts = units < kJoinCtas ? kJoinCtas / units : 1;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)parts);
   cfg.blockDim = dim3(join_threads(G));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

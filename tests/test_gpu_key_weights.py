@@ -218,6 +218,12 @@ def test_decode_stops_at_lengths_that_add_up_past_32_bits(lib):
     assert (out == 7.0).all() and torch.equal(before, st.kw)
 
 
+def test_decode_join_with_more_parts_than_ctas(lib):
+    """512 sequences of eight kv heads: the second launch has four CTAs for each,
+    the longest takes five parts and a bit."""
+    check_decode(lib, batch([1] * 300 + [5400] + [70] * 210 + [4097], 1, 8, 64, 20, block_size=64))
+
+
 def test_decode_nan_stays_in_its_sequence(lib):
     b = batch([40, 300], 2, 2, 64, 25)
     st = Step(lib, b)
