@@ -27,17 +27,18 @@ constexpr int kWarpsMost = 8;        // warps per CTA (one CTA per SM)
 constexpr int kStages = 3;           // ring of tiles per warp
 constexpr int kMaxSeqs = 16384;
 constexpr int kMaxWarps = 4096;      // warps of a grid at most (places for parts)
-constexpr int kMinTiles = 4;         // tiles per run at least (parts cost a join)
+constexpr int kShortTiles = 64;      // a sequence of so many tiles may have a run for each
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 // Threads of the second launch's CTAs: fewer tokens each where a token has eight
 // logits (registers; two long sequences 55.3 -> 54.1 us), more where it has few
 // (a CTA's fixed work counts more; 64 skewed sequences 114 -> 109 us).
 __host__ __device__ constexpr int join_threads(int G) { return G == 8 ? 256 : 128; }
-constexpr int kJoinTokens = 1024;    // tokens that a CTA of the second launch takes at a time
+constexpr int kJoinTokens = 1024;    // tokens that a CTA of the second launch takes at a time, at most
 // CTAs of the second launch, about: the table may be far longer than the contexts,
 // and past this many a CTA takes several parts of its sequence rather than the
 // launch having one for every part that the table has room for.
 constexpr int kJoinCtas = 16384;
+constexpr int kJoinFill = 2;         // CTAs per SM that make smaller parts unnecessary
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightsParams {
@@ -66,6 +67,7 @@ struct WeightsParams {
   int num_kv_heads;
   int block_shift;
   int runs;   // runs of the batch's tiles at most
+  int join_tokens;  // tokens that a CTA of the second launch takes at a time
   int max_blocks_per_seq;
   float qscale;  // scale * log2(e)
 };
@@ -123,9 +125,13 @@ __device__ __forceinline__ int seq_of(const int *prefix, int S, int t) {
 
 // Tiles per run.  Run r has tiles [r * n, (r + 1) * n) of the batch; its part of
 // sequence s is filed under s + r: every part begins where a sequence or a run
-// does, so no two have the same number.
+// does, so no two have the same number.  A run of one tile is the shortest way
+// through the first launch, but the join reads a part for each: 2 sequences under
+// 300 tokens 13.0 us with runs of four tiles and 10.9 with one; 4 sequences of 1000
+// to 2000 tokens, two kv heads, 16.4 with two and 19.5 with one.
 __device__ __forceinline__ int run_tiles(const WeightsParams &p, int tiles) {
-  return max((tiles + p.runs - 1) / p.runs, kMinTiles);
+  const int least = tiles > (int64_t)kShortTiles * p.num_seqs ? 2 : 1;
+  return max((tiles + p.runs - 1) / p.runs, least);
 }
 
 // 16-byte asynchronous copy; zeros instead when !take.
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   const int Hkv = p.num_kv_heads, shift = p.block_shift;
   const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
   const int L = visible(p, s);  // an input of the call: the first launch does not write it
-  const int begin = blockIdx.y * kJoinTokens;
+  const int begin = blockIdx.y * p.join_tokens;
   // (The launch must not end before the first one has, or a next call on the
   // stream could share the workspace with it: one CTA always waits.)
   if (begin >= L && (blockIdx.x | blockIdx.y) != 0) return;
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   float z[kEach][G];
   int blk[kEach];
   auto ask = [&](int begin) {
-    const int end = min(L, begin + kJoinTokens);
+    const int end = min(L, begin + p.join_tokens);
 #pragma unroll
     for (int x = 0; x < kEach; ++x) {
       const int i = begin + tid + x * kJoinThreads;
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
     }
   };
   add(begin);
-  const int stride = gridDim.y * kJoinTokens;
+  const int stride = gridDim.y * p.join_tokens;
   for (int more = begin + stride; more < L; more += stride) {
     ask(more);
     add(more);
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   // Output: the sequence's CTAs share the D * G values, four at a time; the
   // threads of a CTA share the parts.
   constexpr int kQuads = D * G / 4;
-  const int parts = min((L + kJoinTokens - 1) / kJoinTokens, (int)gridDim.y);
+  const int parts = min((L + p.join_tokens - 1) / p.join_tokens, (int)gridDim.y);
   const int per = (kQuads + parts - 1) / parts;
   const int q0 = min((int)blockIdx.y * per, kQuads), q1 = min(q0 + per, kQuads);
   const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + part0 * kQuads;
@@ -655,23 +661,29 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
   const int kRows = WarpSmem<D, G>::kRows;
   // As many runs as give every warp of the GPU one of a kv head, and no more
-  // than the longest possible batch has.
+  // than the longest possible batch has tiles.
   int64_t all = (int64_t)sms * warps;
   if (all > kMaxWarps) all = kMaxWarps;
   int64_t runs = all / prm.num_kv_heads;
   int64_t tiles = (int64_t)prm.num_seqs * ((room + kRows - 1) / kRows);
   if (tiles > prm.max_tiles) tiles = prm.max_tiles;
-  const int64_t most = (tiles + kMinTiles - 1) / kMinTiles;
-  if (runs > most) runs = most;
+  if (runs > tiles) runs = tiles;
   if (runs < 1) runs = 1;
   prm.runs = (int)runs;
   int64_t grid = (runs * prm.num_kv_heads + warps - 1) / warps;
   if (grid > sms) grid = sms;
+  // Few sequences: parts down to a token per thread, so that the join has CTAs for
+  // the GPU too (one sequence of 1000 tokens, eight kv heads: 18.5 us with 1024
+  // tokens per CTA, 14.4 with 128; with four query heads each of 16 sequences of
+  // 100 to 900 tokens 21.9 and 18.5).
+  const int64_t units = (int64_t)prm.num_seqs * prm.num_kv_heads;
+  prm.join_tokens = kJoinTokens;
+  while (prm.join_tokens > join_threads(G) && units * room < (int64_t)prm.join_tokens * kJoinFill * sms)
+    prm.join_tokens /= 2;
   decode_weights_kernel<D, G><<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  const int64_t units = (int64_t)prm.num_seqs * prm.num_kv_heads;
-  int64_t parts = (room + kJoinTokens - 1) / kJoinTokens;
+  int64_t parts = (room + prm.join_tokens - 1) / prm.join_tokens;
   if (parts * units > kJoinCtas) parts = units < kJoinCtas ? kJoinCtas / units : 1;
   cfg.gridDim = dim3((unsigned)units, (unsigned)parts);
   cfg.blockDim = dim3(join_threads(G));
@@ -778,6 +790,7 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.qscale = scale * kLog2e;
   prm.runs = 0;
+  prm.join_tokens = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define PKV_CASE(DD, GG) \
   if (head_dim == DD && G == GG) return launch<DD, GG>(prm, st);
