@@ -92,9 +92,8 @@ __device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) 
   }
   __syncthreads();
   if (warp < kBins / 32) {
-    int before = incl - count;
-#pragma unroll
-    for (int w = 0; w < kBins / 32; ++w) before += w < warp ? warp_sums[w] : 0;
+    const int before =
+        incl - count + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
     if (before < need && need <= before + count) {
       found[0] = kBins - 1 - tid;
       found[1] = need - before;
@@ -251,12 +250,9 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
     warp_sums[1][warp] = equal;
   }
   __syncthreads();
-  int run = 0, rank = 0;  // above T, and equal to it, before this warp's positions
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    run += w < warp ? warp_sums[0][w] : 0;
-    rank += w < warp ? warp_sums[1][w] : 0;
-  }
+  // Above T, and equal to it, before this warp's positions.
+  int run = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[0][lane] : 0);
+  int rank = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[1][lane] : 0);
   run += min(rank, need);
   for (int base = w0; base < w1; base += 32) {  // a word per lane
     const int w = base + lane;

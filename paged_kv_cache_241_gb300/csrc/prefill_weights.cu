@@ -131,7 +131,7 @@ __device__ __forceinline__ bool seq_at(const PromptParams &p, int s, Seq &q, boo
 
 // (128 / G is a power of two: divisions by it, and by a tile, are shifts)
 __device__ __forceinline__ int tq_shift(const PromptParams &p) { return 7 - p.group_shift; }
-static_assert(kTile == 128, "shifts by 7");
+static_assert(kTile == 128 && kThreads / 32 <= 32, "shifts by 7; a lane per warp");
 
 // Key tiles that row tile rt sees: up to its last query's position.
 __device__ __forceinline__ int tiles_seen(const PromptParams &p, const Seq &q, int rt) {
@@ -388,6 +388,7 @@ __device__ void find_run(const PromptParams &p, Run *run, int64_t *scratch, bool
   int64_t local = 0;
   int each = 0;
   Seq q;
+  Seq *qs = reinterpret_cast<Seq *>(scratch + kThreads / 32);  // that of the next run's first place
   for (int s = s0; s < s1; ++s) {
     each = 0;
     if (seq_at(p, s, q, tell)) {
@@ -403,60 +404,65 @@ __device__ void find_run(const PromptParams &p, Run *run, int64_t *scratch, bool
   }
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  int64_t before = incl - local, total = 0;
+  // The warps that have sequences go on (for most batches one; all of them, each
+  // adding up the warps' sums one by one, took 2000 of the prologue's 5700 cycles).
+  if (warp * 32 * per < S) {
+    const int64_t own = lane < kThreads / 32 ? scratch[lane] : 0;
+    int64_t upto = own;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t x = scratch[w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  const int64_t most = total + gridDim.x - 1;
-  const int64_t length = most <= 0xFFFFFFFFll ? (int64_t)((uint32_t)most / gridDim.x)
-                                              : most / gridDim.x;
-  const int64_t begin = min(length * blockIdx.x, total), end = min(begin + length, total);
-  if (tid == 0) {
-    run->begin = begin;
-    run->end = end;
-    run->length = length;
-    if (end == total) {  // the end of the batch
-      run->end_s = S;
-      run->end_j = run->end_tile = run->end_in = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-  }
-  // The sequence and head of the run's first place, then of the next run's.
-  Seq *qs = reinterpret_cast<Seq *>(scratch + kThreads / 32);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int64_t at = x == 0 ? begin : end;
-    if (at >= total || at < before || at >= before + local) continue;
-    int64_t b = before;
-    int s = s0;
-    if (per > 1) {
-      for (; s < s1; ++s) {
-        if (!seq_at(p, s, q, false)) continue;
-        each = Order<PASS>::length(p, q);
-        if (at < b + (int64_t)each * p.num_kv_heads) break;
-        b += (int64_t)each * p.num_kv_heads;
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int64_t before = incl - local + __shfl_sync(0xffffffffu, upto - own, warp);
+    const int64_t most = total + gridDim.x - 1;
+    const int64_t length = most <= 0xFFFFFFFFll ? (int64_t)((uint32_t)most / gridDim.x)
+                                                : most / gridDim.x;
+    const int64_t begin = min(length * blockIdx.x, total), end = min(begin + length, total);
+    if (tid == 0) {
+      run->begin = begin;
+      run->end = end;
+      run->length = length;
+      if (end == total) {  // the end of the batch
+        run->end_s = S;
+        run->end_j = run->end_tile = run->end_in = 0;
       }
     }
-    const int64_t offset = at - b;
-    const int j = offset <= 0xFFFFFFFFll ? (int)((uint32_t)offset / (uint32_t)each)
-                                         : (int)(offset / each);
-    const int in = (int)(offset - (int64_t)j * each);  // (place in the head, until the tile is found)
-    if (x == 0) {
-      run->s = s;
-      run->j = j;
-      run->in = in;
-      run->q = q;
-    } else {
-      run->end_s = s;
-      run->end_j = j;
-      run->end_in = in;
-      *qs = q;
+    // The sequence and head of the run's first place, then of the next run's.
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t at = x == 0 ? begin : end;
+      if (at >= total || at < before || at >= before + local) continue;
+      int64_t b = before;
+      int s = s0;
+      if (per > 1) {
+        for (; s < s1; ++s) {
+          if (!seq_at(p, s, q, false)) continue;
+          each = Order<PASS>::length(p, q);
+          if (at < b + (int64_t)each * p.num_kv_heads) break;
+          b += (int64_t)each * p.num_kv_heads;
+        }
+      }
+      const int64_t offset = at - b;
+      const int j = offset <= 0xFFFFFFFFll ? (int)((uint32_t)offset / (uint32_t)each)
+                                           : (int)(offset / each);
+      const int in = (int)(offset - (int64_t)j * each);  // (place in the head, until the tile is found)
+      if (x == 0) {
+        run->s = s;
+        run->j = j;
+        run->in = in;
+        run->q = q;
+      } else {
+        run->end_s = s;
+        run->end_j = j;
+        run->end_in = in;
+        *qs = q;
+      }
     }
   }
   __syncthreads();
-  if (warp < 2 && (warp == 0 ? begin : end) < total) {
+  if (warp == 0 ? run->begin < run->end : warp == 1 && run->end_s < S) {
     int in;
     const int tile =
         find_tile<PASS>(p, warp == 0 ? run->q : *qs, warp == 0 ? run->in : run->end_in, in);
