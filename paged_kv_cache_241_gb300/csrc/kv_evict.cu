@@ -73,9 +73,11 @@ __device__ __forceinline__ int64_t weight_at(const int32_t *bt, int i, int shift
   return (((int64_t)bt[i >> shift] * Hkv + j) << shift) + (i & ((1 << shift) - 1));
 }
 
-// The digit bin of the `need`-th largest among the counted keys; *need becomes
-// the rank inside that bin.  All threads call it and get the same answer.
-__device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) {
+// The digit bin of the `need`-th largest among the counted keys; `need` becomes
+// the rank inside that bin, `all` says whether it is the bin's last.  All threads
+// call it and get the same answer.
+__device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need,
+                        bool &all) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int count = 0, incl = 0;
   if (warp < kBins / 32) {  // thread t has the t-th bin from the top
@@ -97,10 +99,12 @@ __device__ int pick_bin(const int *hist, int *warp_sums, int *found, int &need) 
     if (before < need && need <= before + count) {
       found[0] = kBins - 1 - tid;
       found[1] = need - before;
+      found[2] = count;
     }
   }
   __syncthreads();
   need = found[1];
+  all = need == found[2];
   return found[0];
 }
 
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
   extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ __align__(16) int hist[kBins * kCopies];
   __shared__ int warp_sums[2][32];
-  __shared__ int found[2];
+  __shared__ int found[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / p.num_kv_heads;
   const int j = blockIdx.x - s * p.num_kv_heads;
@@ -222,7 +226,16 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 1)
     }
     for (int i = cached + tid; i < N; i += kSelThreads) count(key_at(i));
     __syncthreads();
-    T |= (uint32_t)pick_bin(hist, warp_sums[0], found, need) << lo;
+    bool all;
+    T |= (uint32_t)pick_bin(hist, warp_sums[0], found, need, all) << lo;
+    // All keys with these digits are kept: the digits behind do not matter (of
+    // keys that differ the third pass is mostly the last, of few the second).
+    // (Not all keys are kept, so a smaller one exists and T is not 0.)
+    if (all) {
+      T -= 1;
+      need = 0;
+      break;
+    }
   }
 
   // Kept: keys above T, and the first `need` of those equal to it.  Each warp
