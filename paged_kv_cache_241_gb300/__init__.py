@@ -320,11 +320,11 @@ def paged_prefill_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_
 def _check_args(what, key_weights, k_cache, args, dev_status):
     """The checks of the key-weight calls: every tensor's dtype, rank, layout
     and device (all on the current one: the library launches there), and
-    key_weights' shape.  args: (name, tensor or None, dtype, rank).  One pass
-    without exceptions or objects: these calls take a few microseconds."""
+    key_weights' shape.  args: (name, tensor or None, dtype, rank).  Says what is
+    wrong, if anything is; the calls ask _plain first."""
     import torch
 
-    dev = torch.cuda.current_device() if k_cache.is_cuda else -1
+    dev = _device_of(k_cache)
     for name, t, dtype, ndim in args:
         if t is not None and (t.dtype is not dtype or t.get_device() != dev or dev < 0 or
                               t.dim() != ndim or not t.is_contiguous()):
@@ -336,7 +336,27 @@ def _check_args(what, key_weights, k_cache, args, dev_status):
     NB, BS, Hkv, _ = k_cache.shape
     if key_weights.shape != (NB, Hkv, BS):
         raise ValueError(f"key_weights: expected [num_blocks, Hkv, block_size] = {(NB, Hkv, BS)}")
-    return dev
+
+
+def _plain(dev, dtype, *tensors) -> bool:
+    """Whether all are contiguous, of dtype and on device dev (a few microseconds a
+    call are mostly such checks: no names, no objects)."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return dev >= 0
+
+
+def _plain_status(dev, dev_status) -> bool:
+    import torch
+
+    return dev_status is None or _plain(dev, torch.int32, dev_status) and dev_status.numel() > 0
+
+
+def _device_of(k_cache) -> int:
+    import torch
+
+    return torch.cuda.current_device() if k_cache.is_cuda else -1
 
 
 def _raw_stream(stream, dev) -> int:
@@ -378,25 +398,32 @@ def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_table
     lib = load()
     if not (k is None) == (v is None) == (slot_mapping is None):
         raise ValueError("paged_decode_weights_attn: k, v and slot_mapping go together")
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = _check_args("paged_decode_weights_attn", key_weights, k_cache, (
-        ("out", out, bf16, 3), ("q", q, bf16, 3), ("k", k, bf16, 3), ("v", v, bf16, 3),
-        ("slot_mapping", slot_mapping, i32, 1), ("k_cache", k_cache, bf16, 4),
-        ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
-        ("context_lens", context_lens, i32, 1), ("workspace", workspace, torch.uint8, 1),
-        ("key_weights", key_weights, torch.float32, 3)), dev_status)
-    S, Hq, D = q.shape
-    NB, BS, Hkv, Dc = k_cache.shape
-    if Dc != D or out.shape != q.shape or block_tables.shape[0] != S or \
-            context_lens.shape[0] != S or v_cache.shape != k_cache.shape:
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev = _device_of(k_cache)
+    q_shape, cache_shape, table_shape = q.shape, k_cache.shape, block_tables.shape
+    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, out, q, k_cache, v_cache) and
+            _plain(dev, i32, block_tables, context_lens) and _plain(dev, f32, key_weights) and
+            _plain(dev, torch.uint8, workspace) and
+            (k is None or _plain(dev, bf16, k, v) and _plain(dev, i32, slot_mapping)) and
+            len(q_shape) == 3 and len(cache_shape) == 4 and len(table_shape) == 2):
+        _check_args("paged_decode_weights_attn", key_weights, k_cache, (
+            ("out", out, bf16, 3), ("q", q, bf16, 3), ("k", k, bf16, 3), ("v", v, bf16, 3),
+            ("slot_mapping", slot_mapping, i32, 1), ("k_cache", k_cache, bf16, 4),
+            ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
+            ("context_lens", context_lens, i32, 1), ("workspace", workspace, torch.uint8, 1),
+            ("key_weights", key_weights, f32, 3)), dev_status)
+    S, Hq, D = q_shape
+    NB, BS, Hkv, Dc = cache_shape
+    if Dc != D or out.shape != q_shape or table_shape[0] != S or context_lens.shape != (S,) or \
+            v_cache.shape != cache_shape or key_weights.shape != (NB, Hkv, BS):
         raise ValueError("paged_decode_weights_attn: inconsistent shapes")
     if k is not None and (k.shape != (S, Hkv, D) or v.shape != (S, Hkv, D) or
-                          slot_mapping.shape[0] != S):
+                          slot_mapping.shape != (S,)):
         raise ValueError("paged_decode_weights_attn: inconsistent shapes of the new tokens")
     st = lib.pkv_paged_decode_weights_attn(
         out.data_ptr(), key_weights.data_ptr(), q.data_ptr(), _addr(k), _addr(v),
         _addr(slot_mapping), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        context_lens.data_ptr(), S, Hq, Hkv, D, BS, block_tables.shape[1], NB,
+        context_lens.data_ptr(), S, Hq, Hkv, D, BS, table_shape[1], NB,
         int(max_total_blocks), float(scale), workspace.data_ptr(), workspace.numel(),
         _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_decode_weights_attn")
@@ -427,21 +454,28 @@ def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, c
     import torch
 
     lib = load()
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = _check_args("paged_prefill_weights", key_weights, k_cache, (
-        ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
-        ("cu_seqlens_q", cu_seqlens_q, i32, 1), ("cu_seqlens_k", cu_seqlens_k, i32, 1),
-        ("workspace", workspace, torch.uint8, 1),
-        ("key_weights", key_weights, torch.float32, 3)), dev_status)
-    T, Hq, D = q.shape
-    NB, BS, Hkv, Dc = k_cache.shape
-    S = cu_seqlens_q.shape[0] - 1
-    if Dc != D or block_tables.shape[0] != S or cu_seqlens_k.shape[0] != S + 1:
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev = _device_of(k_cache)
+    q_shape, cache_shape, table_shape = q.shape, k_cache.shape, block_tables.shape
+    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, q, k_cache) and
+            _plain(dev, i32, block_tables, cu_seqlens_q, cu_seqlens_k) and
+            _plain(dev, f32, key_weights) and _plain(dev, torch.uint8, workspace) and
+            len(q_shape) == 3 and len(cache_shape) == 4 and len(table_shape) == 2):
+        _check_args("paged_prefill_weights", key_weights, k_cache, (
+            ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4),
+            ("block_tables", block_tables, i32, 2), ("cu_seqlens_q", cu_seqlens_q, i32, 1),
+            ("cu_seqlens_k", cu_seqlens_k, i32, 1), ("workspace", workspace, torch.uint8, 1),
+            ("key_weights", key_weights, f32, 3)), dev_status)
+    T, Hq, D = q_shape
+    NB, BS, Hkv, Dc = cache_shape
+    S = table_shape[0]
+    if Dc != D or cu_seqlens_q.shape != (S + 1,) or cu_seqlens_k.shape != (S + 1,) or \
+            key_weights.shape != (NB, Hkv, BS):
         raise ValueError("paged_prefill_weights: inconsistent shapes")
     st = lib.pkv_paged_prefill_weights(
         key_weights.data_ptr(), q.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, T, _c_int32(max_seqlen_q),
-        _c_int32(window), Hq, Hkv, D, BS, block_tables.shape[1], NB, float(scale),
+        _c_int32(window), Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
         workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_prefill_weights")
 
@@ -455,22 +489,26 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
     import torch
 
     lib = load()
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = _check_args("kv_evict", key_weights, k_cache, (
-        ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
-        ("block_tables", block_tables, i32, 2), ("context_lens", context_lens, i32, 1),
-        ("kept", kept, i32, 3), ("new_lens", new_lens, i32, 1),
-        ("key_weights", key_weights, torch.float32, 3)), dev_status)
-    NB, BS, Hkv, D = k_cache.shape
-    S = block_tables.shape[0]
-    if v_cache.shape != k_cache.shape or context_lens.shape[0] != S or \
-            new_lens.shape[0] != S or kept.shape != (S, Hkv, int(budget)):
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev = _device_of(k_cache)
+    cache_shape, table_shape = k_cache.shape, block_tables.shape
+    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, k_cache, v_cache) and
+            _plain(dev, i32, block_tables, context_lens, kept, new_lens) and
+            _plain(dev, f32, key_weights) and len(cache_shape) == 4 and len(table_shape) == 2):
+        _check_args("kv_evict", key_weights, k_cache, (
+            ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
+            ("block_tables", block_tables, i32, 2), ("context_lens", context_lens, i32, 1),
+            ("kept", kept, i32, 3), ("new_lens", new_lens, i32, 1),
+            ("key_weights", key_weights, f32, 3)), dev_status)
+    NB, BS, Hkv, D = cache_shape
+    S = table_shape[0]
+    if v_cache.shape != cache_shape or context_lens.shape != (S,) or new_lens.shape != (S,) or \
+            kept.shape != (S, Hkv, int(budget)) or key_weights.shape != (NB, Hkv, BS):
         raise ValueError("kv_evict: inconsistent shapes")
     st = lib.pkv_kv_evict(k_cache.data_ptr(), v_cache.data_ptr(), key_weights.data_ptr(),
                           block_tables.data_ptr(), context_lens.data_ptr(), S, Hkv, D, BS,
-                          block_tables.shape[1], NB, _c_int32(budget), _c_int32(recent),
-                          kept.data_ptr(),
-                          new_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
+                          table_shape[1], NB, _c_int32(budget), _c_int32(recent),
+                          kept.data_ptr(), new_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_kv_evict")
 
 

@@ -15,6 +15,13 @@
 //  2. Join, a programmatic dependent launch: every CTA joins the maxima and sums
 //     of a sequence's parts, then adds the weights of its own tokens to the sums
 //     and writes its share of the output.
+//
+// Bound by HBM.  Measured: 64 sequences of 128 to 2048 tokens with their store
+// (16 heads on 8, D = 128: 283 MB) 59 us, of which the first launch 50 us at 5.6 TB/s
+// (83 % of a copy); 64 skewed ones to 8192 tokens (594 MB) 112 us, 96 at 6.1 TB/s;
+// two of 24 K to 33 K tokens (64 heads on 8: 236 MB) 55 us, 44 at 5.3 TB/s.  What is
+// above the reading is the second launch (10, 15 and 13.5 us, partly under the
+// first's tail): it starts when the last maximum is known.
 #include <math.h>
 
 #include "host_common.h"

@@ -29,6 +29,16 @@
 // buffers of tensor memory, warp 3 fetches the rows' denominators (second pass),
 // warps 4-19 exponentiate and sum, a group of four for each buffer.  Loads,
 // products and exponentials of different steps overlap.
+//
+// Measured (first and second pass alone, us; the call):
+//   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  24 + 21, 37
+//   12 chunks of 100 to 512 on up to 7800 cached, window 64, 32 heads on 8,
+//   D = 64:                                                           39 + 53, 86
+//   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           47 + 52, 91
+// A window's first pass is the reading of K (73 MB) and the two prologues; the
+// others are bound by the exponentials and the arithmetic around them: a step takes
+// 0.40 to 0.50 us, its 16384 exponentials alone 0.26 (62 a nanosecond and SM), with
+// scaling and sum 0.33; its product 0.17 (D = 64) or 0.33.
 #include <math.h>
 
 #include <type_traits>
