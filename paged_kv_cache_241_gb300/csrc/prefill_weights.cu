@@ -33,7 +33,7 @@
 // Measured (first and second pass alone, us; the call):
 //   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  24 + 21, 37
 //   12 chunks of 100 to 512 on up to 7800 cached, window 64, 32 heads on 8,
-//   D = 64:                                                           39 + 53, 86
+//   D = 64:                                                           39 + 50, 83
 //   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           47 + 52, 91
 // A window's first pass is the reading of K (73 MB) and the two prologues; the
 // others are bound by the exponentials and the arithmetic around them: a step takes
@@ -898,35 +898,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first = (key - w.q.base - (x << tq_shift(p))) * p.group;
             // Every row of the tile sees every key of the tile.
             const bool open = t * kTile + kTile - 1 <= w.q.base + (x << tq_shift(p));
-#pragma unroll 1
-            for (int c0 = 0; c0 < rows; c0 += 32) {
+            const float4 *ns =
+                reinterpret_cast<const float4 *>(stat + (load & (kStatSlots - 1)) * kTile);
+            // No row or key is hidden: all four runs unrolled, where the exponentials
+            // are the bound (D = 64, the chunks: 86.3 us without and 83.4 with it;
+            // D = 128, where the products take as long, window 39.7 and 41.0, whole
+            // prompts 93.3 and 94.2).
+            auto open_run = [&](int c0) {
               float v[32];
               tmem_load32(ta + c0, v);
               if (c0 + 32 >= rows) release_product();  // (the product is read: the next one may come)
-              const float4 *ns = reinterpret_cast<const float4 *>(stat + (load & (kStatSlots - 1)) * kTile + c0);
-              if (open && c0 + 32 <= rows) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 n = ns[i / 4];
-                  const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
-                  const float2 z1 =
-                      __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
-                  acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
-                  acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
-                }
-              } else {
-                const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
-                if (!__any_sync(0xffffffffu, n_in > 0)) continue;
+              for (int i = 0; i < 32; i += 4) {
+                const float4 n = ns[(c0 + i) / 4];
+                const float2 z0 = __ffma2_rn(make_float2(v[i], v[i + 1]), qs2, make_float2(n.x, n.y));
+                const float2 z1 =
+                    __ffma2_rn(make_float2(v[i + 2], v[i + 3]), qs2, make_float2(n.z, n.w));
+                acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+                acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+              }
+            };
+            auto any_run = [&](int c0) {
+              float v[32];
+              tmem_load32(ta + c0, v);
+              if (c0 + 32 >= rows) release_product();
+              const int lo = max(first - c0, 0), n_in = max(min(rows - c0, 32) - lo, 0);
+              if (!__any_sync(0xffffffffu, n_in > 0)) return;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 n = ns[i / 4];
-                  const float e0 = fast_exp2(fmaf(v[i], qs, n.x)), e1 = fast_exp2(fmaf(v[i + 1], qs, n.y));
-                  const float e2 = fast_exp2(fmaf(v[i + 2], qs, n.z)), e3 = fast_exp2(fmaf(v[i + 3], qs, n.w));
-                  acc0.x += (unsigned)(i - lo) < (unsigned)n_in ? e0 : 0.f;
-                  acc0.y += (unsigned)(i + 1 - lo) < (unsigned)n_in ? e1 : 0.f;
-                  acc1.x += (unsigned)(i + 2 - lo) < (unsigned)n_in ? e2 : 0.f;
-                  acc1.y += (unsigned)(i + 3 - lo) < (unsigned)n_in ? e3 : 0.f;
-                }
+              for (int i = 0; i < 32; i += 4) {
+                const float4 n = ns[(c0 + i) / 4];
+                const float e0 = fast_exp2(fmaf(v[i], qs, n.x)), e1 = fast_exp2(fmaf(v[i + 1], qs, n.y));
+                const float e2 = fast_exp2(fmaf(v[i + 2], qs, n.z)), e3 = fast_exp2(fmaf(v[i + 3], qs, n.w));
+                acc0.x += (unsigned)(i - lo) < (unsigned)n_in ? e0 : 0.f;
+                acc0.y += (unsigned)(i + 1 - lo) < (unsigned)n_in ? e1 : 0.f;
+                acc1.x += (unsigned)(i + 2 - lo) < (unsigned)n_in ? e2 : 0.f;
+                acc1.y += (unsigned)(i + 3 - lo) < (unsigned)n_in ? e3 : 0.f;
+              }
+            };
+            if (D == 64 && open && rows == kTile) {
+#pragma unroll
+              for (int c0 = 0; c0 < kTile; c0 += 32) open_run(c0);
+            } else if (D == 64) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < rows; c0 += 32) any_run(c0);
+            } else {
+#pragma unroll 1
+              for (int c0 = 0; c0 < rows; c0 += 32) {
+                if (open && c0 + 32 <= rows) open_run(c0);
+                else any_run(c0);
               }
             }
             // (this group alone used the step's denominators: it releases them for all)

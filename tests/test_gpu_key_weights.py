@@ -301,6 +301,14 @@ def test_prefill_longer_prompts(lib, window):
     check_prefill(lib, prompts([700, 300], [1500, 0], 2, 1, 128, 50), window)
 
 
+@pytest.mark.parametrize("G,Hkv,cached", [(1, 4, 0), (2, 2, 300), (8, 1, 0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_rows_of_many_tiles(lib, D, G, Hkv, cached):
+    """More row tiles than any ring of the kernel has slots, most of whose products
+    no row or key is hidden from, in heads of unlike lengths."""
+    check_prefill(lib, prompts([1700, 129, 960, 1301], [cached, 0, cached, 7], G, Hkv, D, 36), 1 << 20)
+
+
 def test_prefill_long_cache_few_queries(lib):
     check_prefill(lib, prompts([5, 40], [9000, 4090], 8, 1, 64, 51, block_size=64), 8)
 
