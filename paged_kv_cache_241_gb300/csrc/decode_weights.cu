@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
   const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the kernel before the call)
   const int64_t all = scan_tiles<kRows>(p, prefix, warp_sums);
   const bool over = all > p.max_tiles;
   const int total = (int)all;
@@ -687,19 +688,25 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   prm.join_tokens = kJoinTokens;
   while (prm.join_tokens > join_threads(G) && units * room < (int64_t)prm.join_tokens * kJoinFill * sms)
     prm.join_tokens /= 2;
-  decode_weights_kernel<D, G><<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
-  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  // Both launches are programmatic dependents of what precedes them, the first one
+  // of the kernel before the call: 2.0 to 2.6 us less from call to call (64 sequences
+  // with their store 58.5 -> 56.0).
   cudaLaunchConfig_t cfg = {};
-  int64_t parts = (room + prm.join_tokens - 1) / prm.join_tokens;
-  if (parts * units > kJoinCtas) parts = units < kJoinCtas ? kJoinCtas / units : 1;
-  cfg.gridDim = dim3((unsigned)units, (unsigned)parts);
-  cfg.blockDim = dim3(join_threads(G));
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_weights_kernel<D, G>, prm) != cudaSuccess) return PKV_ERR_CUDA;
+  int64_t parts = (room + prm.join_tokens - 1) / prm.join_tokens;
+  if (parts * units > kJoinCtas) parts = units < kJoinCtas ? kJoinCtas / units : 1;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)parts);
+  cfg.blockDim = dim3(join_threads(G));
+  cfg.dynamicSmemBytes = 0;
   if (cudaLaunchKernelEx(&cfg, decode_weights_join_kernel<D, G>, prm) != cudaSuccess)
     return PKV_ERR_CUDA;
   return launch_status();

@@ -652,6 +652,91 @@ def test_captured_and_replayed(lib):
     assert st.status_value() == 0
 
 
+@pytest.mark.parametrize("before", ["kernel", "copy", "memset", "two streams", "nothing"])
+@pytest.mark.parametrize("op", ["decode", "prompt", "evict"])
+def test_calls_wait_for_what_is_before_them(lib, op, before):
+    """The first launch of a call may start under the tail of what precedes it on the
+    stream, whatever that is, and must see all of its results: inputs that slow work
+    has just written, eagerly and in a captured graph."""
+    b = batch([900, 1300, 64], 4, 2, 128, 73, num_blocks=16)
+    st = Step(lib, b)
+    ws = st.workspace(20)
+    pws = lib.prefill_weights_workspace(3, 3, 1, 4, 8, 2, b.block_tables.shape[1], 256)
+    kept = torch.empty((3, 2, 256), dtype=torch.int32, device="cuda")
+    new_lens = torch.empty((3,), dtype=torch.int32, device="cuda")
+    inputs = st.context_lens, st.cu_k, st.q, st.kw, st.k_cache, st.v_cache
+    true = [x.clone() for x in inputs]
+    slow, other = torch.rand((2048, 2048), device="cuda"), torch.empty((2048, 2048), device="cuda")
+    side = torch.cuda.Stream()
+
+    def spoil():
+        for x in inputs:
+            x.zero_()
+        for x in (st.out, kept, new_lens):
+            x.fill_(7)
+        torch.cuda.synchronize()
+
+    def feed():
+        for _ in range(10):
+            torch.mm(slow, slow, out=other)
+        for x, y in zip(inputs, true):
+            torch.add(y, 0, out=x) if before == "kernel" else x.copy_(y)
+
+    def go():
+        if before == "two streams":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                feed()
+            other.add_(1.0)
+            torch.cuda.current_stream().wait_stream(side)
+        elif before != "nothing":
+            feed()
+        if before == "memset":
+            st.out.zero_()
+        if op == "decode":
+            st.decode_weights(mtb=20, ws=ws)
+        elif op == "prompt":
+            lib.paged_prefill_weights(st.kw, st.q, st.k_cache, st.block_tables, st.cu_q, st.cu_k, 1, 4, b.scale, pws, st.status)
+        else:
+            lib.kv_evict(st.k_cache, st.v_cache, st.kw, st.block_tables, st.context_lens, 256, 32, kept, new_lens, st.status)
+
+    def outputs():
+        torch.cuda.synchronize()
+        return [x.clone() for x in (st.out, st.kw, st.k_cache, st.v_cache, kept, new_lens)]
+
+    def start():
+        spoil()
+        if before == "nothing":
+            for x, y in zip(inputs, true):
+                x.copy_(y)
+            torch.cuda.synchronize()
+
+    spoil()
+    feed()
+    torch.cuda.synchronize()
+    if before == "memset":
+        st.out.zero_()
+    before, kind = "nothing", before
+    go()
+    want = outputs()
+    before = kind
+    for _ in range(3):
+        start()
+        go()
+        for x, y in zip(outputs(), want):
+            assert torch.equal(x, y)
+    g = torch.cuda.CUDAGraph()
+    start()
+    with torch.cuda.graph(g):
+        go()
+    for _ in range(3):
+        start()
+        g.replay()
+        for x, y in zip(outputs(), want):
+            assert torch.equal(x, y)
+    assert st.status_value() == 0
+
+
 def test_a_sequence_goes_on_in_a_bounded_cache(lib):
     """Prompts, their weights, eviction, decode steps that store and collect, and
     eviction again whenever a budget's worth and a block has filled up; the block
