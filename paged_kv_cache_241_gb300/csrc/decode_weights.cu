@@ -17,11 +17,11 @@
 //     and writes its share of the output.
 //
 // Bound by HBM.  Measured: 64 sequences of 128 to 2048 tokens with their store
-// (16 heads on 8, D = 128: 283 MB) 59 us, of which the first launch 50 us at 5.6 TB/s
-// (83 % of a copy); 64 skewed ones to 8192 tokens (594 MB) 112 us, 96 at 6.1 TB/s;
-// two of 24 K to 33 K tokens (64 heads on 8: 236 MB) 55 us, 44 at 5.3 TB/s.  What is
-// above the reading is the second launch (10, 15 and 13.5 us, partly under the
-// first's tail): it starts when the last maximum is known.
+// (16 heads on 8, D = 128: 283 MB) 56 us, of which the first launch alone 50 to 53 at
+// 5.3 to 5.6 TB/s (about 80 % of a copy); 64 skewed ones to 8192 tokens (594 MB) 110 us,
+// 96 at 6.1 TB/s; two of 24 K to 33 K tokens (64 heads on 8: 236 MB) 52 us, 44 at 5.3
+// TB/s.  What is above the reading is the second launch (10, 15 and 14 us alone, its
+// caches cold): it starts when the last maximum is known.
 #include <math.h>
 
 #include "host_common.h"
@@ -240,230 +240,230 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
   const int col = lane % kCols, row0 = lane / kCols;
   for (int64_t job = (int64_t)blockIdx.x * warps + warp; job < jobs;
        job += (int64_t)gridDim.x * warps) {
-  const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
-  const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
+    const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
+    const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
 
-  // The loading side, ahead of the consuming side by up to two tiles: tile in_t
-  // of the batch, at token in_tok of sequence in_s (in_L tokens), in block
-  // blk; blk_next is the block after it, of this sequence or the next one.
-  int in_t = t_begin, in_s = seq_of(prefix, S, t_begin);
-  int in_tok = (t_begin - prefix[in_s]) * kRows;
-  int in_L = visible(p, in_s);
-  int in_slot = 0, in_q = 0;
-  bool in_first = true;  // the sequence's first tile of this run
-  auto block_of = [&](int s, int tok) {
-    int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
-      blk = 0;
-    }
-    return blk;
-  };
-  auto next_seq = [&](int s) {  // the next sequence with tokens
-    do ++s; while (s < S && prefix[s + 1] == prefix[s]);
-    return s;
-  };
-  auto block_after = [&]() {
-    const int tok = ((in_tok >> shift) + 1) << shift;
-    if (tok < in_L) return block_of(in_s, tok);
-    const int s = next_seq(in_s);
-    return s < S ? block_of(s, 0) : 0;
-  };
-  int blk = block_of(in_s, in_tok), blk_next = block_after();
-  auto issue = [&]() {
-    if (in_t < t_end) {
-      if (in_first) {
-        const uint16_t *q = p.q + ((int64_t)in_s * Hkv + j) * G * D;
-        for (int x = lane; x < G * kCols; x += 32)
-          copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
-        in_q = in_q + 1 == kStages ? 0 : in_q + 1;
-        in_first = false;
+    // The loading side, ahead of the consuming side by up to two tiles: tile in_t
+    // of the batch, at token in_tok of sequence in_s (in_L tokens), in block
+    // blk; blk_next is the block after it, of this sequence or the next one.
+    int in_t = t_begin, in_s = seq_of(prefix, S, t_begin);
+    int in_tok = (t_begin - prefix[in_s]) * kRows;
+    int in_L = visible(p, in_s);
+    int in_slot = 0, in_q = 0;
+    bool in_first = true;  // the sequence's first tile of this run
+    auto block_of = [&](int s, int tok) {
+      int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+        blk = 0;
       }
-      const int64_t slot = ((int64_t)blk << shift) + (in_tok & ((1 << shift) - 1));
-      const int64_t at = ((slot + row0) * Hkv + j) * D + col * 8;
-      const int64_t step = (int64_t)kRowsPer * Hkv * D;
-      const int64_t fresh = ((int64_t)in_s * Hkv + j) * D + col * 8;
-      // (the newest token comes from the inputs when the call stores it)
-      const int newest = p.new_k != nullptr && in_L == p.context_lens[in_s] ? in_L - 1 : -1;
-      const uint32_t dst = tiles + in_slot * 2 * W::kHalf;
-#pragma unroll
-      for (int i = 0; i < kRows / kRowsPer; ++i) {
-        const int t = in_tok + row0 + i * kRowsPer;
-        const uint32_t to = dst + tile_at<D>(row0 + i * kRowsPer, col);
-        const bool is_new = t == newest;
-        copy16(to, is_new ? p.new_k + fresh : p.k_cache + at + i * step, t < in_L, policy);
-        copy16(to + W::kHalf, is_new ? p.new_v + fresh : p.v_cache + at + i * step, t < in_L, policy);
-      }
-      ++in_t;
-      in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+      return blk;
+    };
+    auto next_seq = [&](int s) {  // the next sequence with tokens
+      do ++s; while (s < S && prefix[s + 1] == prefix[s]);
+      return s;
+    };
+    auto block_after = [&]() {
+      const int tok = ((in_tok >> shift) + 1) << shift;
+      if (tok < in_L) return block_of(in_s, tok);
+      const int s = next_seq(in_s);
+      return s < S ? block_of(s, 0) : 0;
+    };
+    int blk = block_of(in_s, in_tok), blk_next = block_after();
+    auto issue = [&]() {
       if (in_t < t_end) {
-        in_tok += kRows;
-        const bool ends = in_tok >= in_L;
-        if (ends || (in_tok & ((1 << shift) - 1)) == 0) {
-          if (ends) {
-            in_s = next_seq(in_s);
-            in_tok = 0;
-            in_L = visible(p, in_s);
-            in_first = true;
+        if (in_first) {
+          const uint16_t *q = p.q + ((int64_t)in_s * Hkv + j) * G * D;
+          for (int x = lane; x < G * kCols; x += 32)
+            copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
+          in_q = in_q + 1 == kStages ? 0 : in_q + 1;
+          in_first = false;
+        }
+        const int64_t slot = ((int64_t)blk << shift) + (in_tok & ((1 << shift) - 1));
+        const int64_t at = ((slot + row0) * Hkv + j) * D + col * 8;
+        const int64_t step = (int64_t)kRowsPer * Hkv * D;
+        const int64_t fresh = ((int64_t)in_s * Hkv + j) * D + col * 8;
+        // (the newest token comes from the inputs when the call stores it)
+        const int newest = p.new_k != nullptr && in_L == p.context_lens[in_s] ? in_L - 1 : -1;
+        const uint32_t dst = tiles + in_slot * 2 * W::kHalf;
+#pragma unroll
+        for (int i = 0; i < kRows / kRowsPer; ++i) {
+          const int t = in_tok + row0 + i * kRowsPer;
+          const uint32_t to = dst + tile_at<D>(row0 + i * kRowsPer, col);
+          const bool is_new = t == newest;
+          copy16(to, is_new ? p.new_k + fresh : p.k_cache + at + i * step, t < in_L, policy);
+          copy16(to + W::kHalf, is_new ? p.new_v + fresh : p.v_cache + at + i * step, t < in_L, policy);
+        }
+        ++in_t;
+        in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+        if (in_t < t_end) {
+          in_tok += kRows;
+          const bool ends = in_tok >= in_L;
+          if (ends || (in_tok & ((1 << shift) - 1)) == 0) {
+            if (ends) {
+              in_s = next_seq(in_s);
+              in_tok = 0;
+              in_L = visible(p, in_s);
+              in_first = true;
+            }
+            blk = blk_next;
+            blk_next = block_after();
           }
-          blk = blk_next;
-          blk_next = block_after();
         }
       }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
-  // The consuming side: sequence after sequence of the run.
-  const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
-  const bool owner = h0 < G;      // (of the 8 columns only G are heads)
-  int slot = 0, qslot = 0;
-  for (int s = seq_of(prefix, S, t_begin), tile = t_begin; tile < t_end; s = next_seq(s)) {
-    const int L = visible(p, s);
-    const int first = (tile - prefix[s]) * kRows;                  // tokens [first, last) are here
-    const int last = min(L, first + (t_end - tile) * kRows);
-    uint32_t qf[D / 16][2];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float o[D / 16][4];
+    // The consuming side: sequence after sequence of the run.
+    const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
+    const bool owner = h0 < G;      // (of the 8 columns only G are heads)
+    int slot = 0, qslot = 0;
+    for (int s = seq_of(prefix, S, t_begin), tile = t_begin; tile < t_end; s = next_seq(s)) {
+      const int L = visible(p, s);
+      const int first = (tile - prefix[s]) * kRows;                  // tokens [first, last) are here
+      const int last = min(L, first + (t_end - tile) * kRows);
+      uint32_t qf[D / 16][2];
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float o[D / 16][4];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    for (int tok = first; tok < last; tok += kRows, ++tile) {
-      float *lg = p.logits + ((int64_t)tile * Hkv + j) * kRows * G;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();  // every lane's copies are in, and the slot filled next is read out
-      issue();
-      if (tok == first) {
-        // q as the second operand: lane (head, dim pair) per 8 dims.  Rows past
-        // G repeat the last one (their columns are not used).
-        const uint32_t qa = qslots + qslot * W::kQ;
-        const int row = min(lane & 7, G - 1);
+      for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int tok = first; tok < last; tok += kRows, ++tile) {
+        float *lg = p.logits + ((int64_t)tile * Hkv + j) * kRows * G;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // every lane's copies are in, and the slot filled next is read out
+        issue();
+        if (tok == first) {
+          // q as the second operand: lane (head, dim pair) per 8 dims.  Rows past
+          // G repeat the last one (their columns are not used).
+          const uint32_t qa = qslots + qslot * W::kQ;
+          const int row = min(lane & 7, G - 1);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t f[4];
-          ldmatrix4(f, qa + tile_at<D>(row, i * 4 + (lane >> 3)));
-          qf[2 * i][0] = f[0];
-          qf[2 * i][1] = f[1];
-          qf[2 * i + 1][0] = f[2];
-          qf[2 * i + 1][1] = f[3];
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t f[4];
+            ldmatrix4(f, qa + tile_at<D>(row, i * 4 + (lane >> 3)));
+            qf[2 * i][0] = f[0];
+            qf[2 * i][1] = f[1];
+            qf[2 * i + 1][0] = f[2];
+            qf[2 * i + 1][1] = f[3];
+          }
+          qslot = qslot + 1 == kStages ? 0 : qslot + 1;
         }
-        qslot = qslot + 1 == kStages ? 0 : qslot + 1;
-      }
-      const uint32_t ka = tiles + slot * 2 * W::kHalf, va = ka + W::kHalf;
+        const uint32_t ka = tiles + slot * 2 * W::kHalf, va = ka + W::kHalf;
 #pragma unroll
-      for (int sl = 0; sl < kSlices; ++sl) {
-        // S: rows are tokens (lane / 4 and + 8), columns the lane's two heads.
-        float s_even[4] = {0.f, 0.f, 0.f, 0.f}, s_odd[4] = {0.f, 0.f, 0.f, 0.f};
-        const int kr = sl * 16 + (lane & 15);
+        for (int sl = 0; sl < kSlices; ++sl) {
+          // S: rows are tokens (lane / 4 and + 8), columns the lane's two heads.
+          float s_even[4] = {0.f, 0.f, 0.f, 0.f}, s_odd[4] = {0.f, 0.f, 0.f, 0.f};
+          const int kr = sl * 16 + (lane & 15);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t a[4];
-          ldmatrix4(a, ka + tile_at<D>(kr, 2 * i + (lane >> 4)));
-          if (i & 1) mma16816(s_odd, a, qf[i][0], qf[i][1]);
-          else mma16816(s_even, a, qf[i][0], qf[i][1]);
-        }
-        const int i0 = sl * 16 + (lane >> 2), i1 = i0 + 8;  // rows of the tile
-        const bool in0 = tok + i0 < L, in1 = tok + i1 < L;
-        float z[4];
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldmatrix4(a, ka + tile_at<D>(kr, 2 * i + (lane >> 4)));
+            if (i & 1) mma16816(s_odd, a, qf[i][0], qf[i][1]);
+            else mma16816(s_even, a, qf[i][0], qf[i][1]);
+          }
+          const int i0 = sl * 16 + (lane >> 2), i1 = i0 + 8;  // rows of the tile
+          const bool in0 = tok + i0 < L, in1 = tok + i1 < L;
+          float z[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = (s_even[i] + s_odd[i]) * p.qscale;
-        if (owner) {
-          if (G == 1) {
-            if (in0) lg[i0] = z[0];
-            if (in1) lg[i1] = z[2];
-          } else {
-            if (in0) *reinterpret_cast<float2 *>(lg + i0 * G + h0) = make_float2(z[0], z[1]);
-            if (in1) *reinterpret_cast<float2 *>(lg + i1 * G + h0) = make_float2(z[2], z[3]);
+          for (int i = 0; i < 4; ++i) z[i] = (s_even[i] + s_odd[i]) * p.qscale;
+          if (owner) {
+            if (G == 1) {
+              if (in0) lg[i0] = z[0];
+              if (in1) lg[i1] = z[2];
+            } else {
+              if (in0) *reinterpret_cast<float2 *>(lg + i0 * G + h0) = make_float2(z[0], z[1]);
+              if (in1) *reinterpret_cast<float2 *>(lg + i1 * G + h0) = make_float2(z[2], z[3]);
+            }
+          }
+          if (!in0) z[0] = z[1] = -INFINITY;
+          if (!in1) z[2] = z[3] = -INFINITY;
+          float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, k));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, k));
+          }
+          n0 = fmaxf(n0, m0);
+          n1 = fmaxf(n1, m1);
+          // (a maximum of -inf: every weight so far is zero, whatever the reference)
+          const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+          const float a0 = fast_exp2(m0 - r0), a1 = fast_exp2(m1 - r1);
+          m0 = n0;
+          m1 = n1;
+          const float p0 = fast_exp2(z[0] - r0), p1 = fast_exp2(z[1] - r1);
+          const float p2 = fast_exp2(z[2] - r0), p3 = fast_exp2(z[3] - r1);
+          l0 = fmaf(l0, a0, p0 + p2);
+          l1 = fmaf(l1, a1, p1 + p3);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][0] *= a0;
+            o[i][1] *= a1;
+            o[i][2] *= a0;
+            o[i][3] *= a1;
+          }
+          // P as the second operand of the next product: rounded to bf16 there,
+          // as the tensor cores take it; the sums keep the fp32 weights.
+          const uint32_t b0 = transpose8x8(pack_bf16x2(p0, p1));
+          const uint32_t b1 = transpose8x8(pack_bf16x2(p2, p3));
+          // V^T: two 8-token halves by two 8-dim columns, transposed on the way.
+          const int vr = sl * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldmatrix4_trans(a, va + tile_at<D>(vr, 2 * i + ((lane >> 3) & 1)));
+            mma16816(o[i], a, b0, b1);
           }
         }
-        if (!in0) z[0] = z[1] = -INFINITY;
-        if (!in1) z[2] = z[3] = -INFINITY;
-        float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+      }
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) {
-          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, k));
-          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, k));
-        }
-        n0 = fmaxf(n0, m0);
-        n1 = fmaxf(n1, m1);
-        // (a maximum of -inf: every weight so far is zero, whatever the reference)
-        const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
-        const float a0 = fast_exp2(m0 - r0), a1 = fast_exp2(m1 - r1);
-        m0 = n0;
-        m1 = n1;
-        const float p0 = fast_exp2(z[0] - r0), p1 = fast_exp2(z[1] - r1);
-        const float p2 = fast_exp2(z[2] - r0), p3 = fast_exp2(z[3] - r1);
-        l0 = fmaf(l0, a0, p0 + p2);
-        l1 = fmaf(l1, a1, p1 + p3);
+      for (int k = 4; k < 32; k <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, k);
+      }
+      const int64_t part = (int64_t)(s + r) * Hkv + j;
+      if (owner) {
+        float *po = p.part_o + part * G * D;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a1;
-          o[i][2] *= a0;
-          o[i][3] *= a1;
+          const int d = i * 16 + (lane >> 2);
+          if (G == 1) {
+            po[d] = o[i][0];
+            po[d + 8] = o[i][2];
+          } else {
+            *reinterpret_cast<float2 *>(po + d * G + h0) = make_float2(o[i][0], o[i][1]);
+            *reinterpret_cast<float2 *>(po + (d + 8) * G + h0) = make_float2(o[i][2], o[i][3]);
+          }
         }
-        // P as the second operand of the next product: rounded to bf16 there,
-        // as the tensor cores take it; the sums keep the fp32 weights.
-        const uint32_t b0 = transpose8x8(pack_bf16x2(p0, p1));
-        const uint32_t b1 = transpose8x8(pack_bf16x2(p2, p3));
-        // V^T: two 8-token halves by two 8-dim columns, transposed on the way.
-        const int vr = sl * 16 + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t a[4];
-          ldmatrix4_trans(a, va + tile_at<D>(vr, 2 * i + ((lane >> 3) & 1)));
-          mma16816(o[i], a, b0, b1);
-        }
-      }
-      slot = slot + 1 == kStages ? 0 : slot + 1;
-    }
-#pragma unroll
-    for (int k = 4; k < 32; k <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, k);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, k);
-    }
-    const int64_t part = (int64_t)(s + r) * Hkv + j;
-    if (owner) {
-      float *po = p.part_o + part * G * D;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int d = i * 16 + (lane >> 2);
-        if (G == 1) {
-          po[d] = o[i][0];
-          po[d + 8] = o[i][2];
-        } else {
-          *reinterpret_cast<float2 *>(po + d * G + h0) = make_float2(o[i][0], o[i][1]);
-          *reinterpret_cast<float2 *>(po + (d + 8) * G + h0) = make_float2(o[i][2], o[i][3]);
+        if (lane < 4) {
+          float *ml = p.part_ml + (part * G + h0) * 2;
+          ml[0] = m0;
+          ml[1] = l0;
+          if (G > 1) {
+            ml[2] = m1;
+            ml[3] = l1;
+          }
         }
       }
-      if (lane < 4) {
-        float *ml = p.part_ml + (part * G + h0) * 2;
-        ml[0] = m0;
-        ml[1] = l0;
-        if (G > 1) {
-          ml[2] = m1;
-          ml[3] = l1;
+      // The run with the newest token stores it (no run of the call reads its slot).
+      if (p.new_k != nullptr && last == L && L == p.context_lens[s]) {
+        const int64_t to = p.new_slots[s];
+        if (to >= 0 && to < p.num_blocks << shift) {
+          if (lane < kCols) {
+            const int64_t from = ((int64_t)s * Hkv + j) * kCols + lane;
+            const int64_t at = (to * Hkv + j) * kCols + lane;
+            reinterpret_cast<uint4 *>(p.k_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_k)[from];
+            reinterpret_cast<uint4 *>(p.v_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_v)[from];
+          }
+        } else if (to != -1 && lane == 0) {
+          flag_status(p.status, PKV_DEV_BAD_SLOT);
         }
       }
     }
-    // The run with the newest token stores it (no run of the call reads its slot).
-    if (p.new_k != nullptr && last == L && L == p.context_lens[s]) {
-      const int64_t to = p.new_slots[s];
-      if (to >= 0 && to < p.num_blocks << shift) {
-        if (lane < kCols) {
-          const int64_t from = ((int64_t)s * Hkv + j) * kCols + lane;
-          const int64_t at = (to * Hkv + j) * kCols + lane;
-          reinterpret_cast<uint4 *>(p.k_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_k)[from];
-          reinterpret_cast<uint4 *>(p.v_cache_w)[at] = reinterpret_cast<const uint4 *>(p.new_v)[from];
-        }
-      } else if (to != -1 && lane == 0) {
-        flag_status(p.status, PKV_DEV_BAD_SLOT);
-      }
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
   }
 }
 
@@ -701,15 +701,14 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, decode_weights_kernel<D, G>, prm) != cudaSuccess) return PKV_ERR_CUDA;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, decode_weights_kernel<D, G>, prm);
   int64_t parts = (room + prm.join_tokens - 1) / prm.join_tokens;
   if (parts * units > kJoinCtas) parts = units < kJoinCtas ? kJoinCtas / units : 1;
   cfg.gridDim = dim3((unsigned)units, (unsigned)parts);
   cfg.blockDim = dim3(join_threads(G));
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, decode_weights_join_kernel<D, G>, prm) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  return launch_status();
+  if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, decode_weights_join_kernel<D, G>, prm);
+  return launch_status();  // (either launch's error, which it clears)
 }
 
 }  // namespace

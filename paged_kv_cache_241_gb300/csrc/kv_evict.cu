@@ -17,8 +17,8 @@
 // The moves are bound by HBM, in rows of 128 or 256 bytes, the selection by its
 // barriers and by shared memory's atomics (a pass over a unit's keys is short).
 // Measured: 64 sequences of 1025 to 1280 tokens down to 1024 (8 kv heads, D = 128:
-// 131 MB) 40 us, the selection 12 and the moves 26 (5 TB/s); 16 prompts of 2000 to
-// 16384 tokens down to 2048 (149 MB) 49 us, 20 and 28 (5.2 TB/s).
+// 131 MB) 39 us, the selection 12 and the moves 26 (5 TB/s); 16 prompts of 2000 to
+// 16384 tokens down to 2048 (149 MB) 48 us, 20 and 28 (5.2 TB/s).
 #include "host_common.h"
 #include "pkv_common.cuh"
 
@@ -528,9 +528,8 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, is_long ? evict_select_kernel<1024> : evict_select_kernel<256>, prm) !=
-      cudaSuccess)
-    return PKV_ERR_CUDA;
+  cudaError_t err =
+      cudaLaunchKernelEx(&cfg, is_long ? evict_select_kernel<1024> : evict_select_kernel<256>, prm);
   // Enough CTAs to fill the GPU: a unit's places in several parts when there are
   // few units.
   const int64_t heavy = budget - recent;
@@ -543,6 +542,6 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
                      (unsigned)(heavy > 0 ? (heavy + places - 1) / places : 1));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, prm) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_status();
+  if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, evict_move_kernel, prm);
+  return launch_status();  // (either launch's error, which it clears)
 }

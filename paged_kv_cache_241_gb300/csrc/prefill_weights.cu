@@ -31,10 +31,10 @@
 // products and exponentials of different steps overlap.
 //
 // Measured (first and second pass alone, us; the call):
-//   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  24 + 21, 37
+//   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  24 + 21, 34
 //   12 chunks of 100 to 512 on up to 7800 cached, window 64, 32 heads on 8,
-//   D = 64:                                                           39 + 50, 83
-//   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           47 + 52, 91
+//   D = 64:                                                           40 + 49, 80
+//   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           47 + 53, 89
 // A window's first pass is the reading of K (73 MB) and the two prologues; the
 // others are bound by the exponentials and the arithmetic around them: a step takes
 // 0.40 to 0.50 us, its 16384 exponentials alone 0.26 (62 a nanosecond and SM), with
@@ -1077,10 +1077,9 @@ pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const PromptPara
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, prompt_weights_kernel<D, 1>, tq, tk, prm) != cudaSuccess ||
-      cudaLaunchKernelEx(&cfg, prompt_weights_kernel<D, 2>, tq, tk, prm) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  return launch_status();
+  if (cudaLaunchKernelEx(&cfg, prompt_weights_kernel<D, 1>, tq, tk, prm) == cudaSuccess)
+    cudaLaunchKernelEx(&cfg, prompt_weights_kernel<D, 2>, tq, tk, prm);
+  return launch_status();  // (either launch's error, which it clears)
 }
 
 }  // namespace
