@@ -652,6 +652,33 @@ def test_captured_and_replayed(lib):
     assert st.status_value() == 0
 
 
+def test_blocks_past_32_bits_of_elements(lib):
+    """The same batch in the last blocks of caches of more than 2^32 values each."""
+    b = batch([900, 1300, 64], 2, 8, 128, 74, block_size=512)
+    ref, st = Step(lib, b), Step(lib, b)
+    NB, per = b.num_blocks, 512 * 8 * 128
+    big = (1 << 32) // per + 2 * NB
+    assert (big - NB) * per > 1 << 32
+    for name in ("k_cache", "v_cache", "kw"):
+        small = getattr(st, name)
+        pool = torch.empty((big, *small.shape[1:]), dtype=small.dtype, device="cuda")
+        pool[big - NB:].copy_(small)
+        setattr(st, name, pool)
+    st.block_tables = torch.where(st.block_tables >= 0, st.block_tables + (big - NB), -1).int()
+    st.slot_mapping = (st.slot_mapping + (big - NB) * 512).int()
+    outs = []
+    for x in (ref, st):
+        kept = torch.empty((3, 8, 256), dtype=torch.int32, device="cuda")
+        new_lens = torch.empty((3,), dtype=torch.int32, device="cuda")
+        x.decode_weights(fused=True)
+        x.prefill_weights(1)
+        lib.kv_evict(x.k_cache, x.v_cache, x.kw, x.block_tables, x.context_lens, 256, 32, kept, new_lens, x.status)
+        assert x.status_value() == 0
+        outs.append((x.out, x.kw[-NB:], x.k_cache[-NB:], x.v_cache[-NB:], kept, new_lens))
+    for a, c in zip(*outs):
+        assert torch.equal(a, c)
+
+
 @pytest.mark.parametrize("before", ["kernel", "copy", "memset", "two streams", "nothing"])
 @pytest.mark.parametrize("op", ["decode", "prompt", "evict"])
 def test_calls_wait_for_what_is_before_them(lib, op, before):
