@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_product();
             if (!ok) break;
             if (qs > 0.f && x * kTile + kTile - 1 <= least) {  // every key, by every row of the warp
-#pragma unroll 2
+#pragma unroll 4
               for (int c = 0; c < kTile / 32; ++c) {
                 float v[32];
                 float top;
