@@ -988,7 +988,13 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     }
     // Nothing to merge: one block, or the split-K grid refused the call for
     // want of workspace (it then leaves every partial unwritten).
-    if (nblk <= 1 || (int64_t)total > p.max_total_blocks) return;
+    if (nblk <= 1 || (int64_t)total > p.max_total_blocks) {
+      // (This launch must not end before the split-K grid has: a programmatic
+      // dependent that follows on the stream waits for this one alone.  One CTA
+      // waits, whatever there is to merge.)
+      if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
     pb0 = before;
   }
   // Partials are complete once the split-K grid has finished.
