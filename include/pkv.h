@@ -294,7 +294,11 @@ size_t pkv_prefill_workspace_size(void);
  * block changes hands.  Sums are fp32; a slot held by one sequence gets one
  * addition per call, so its sum does not depend on the order of anything.  A
  * block that several sequences of the batch share collects the weights of all
- * of them, by atomic additions whose order (hence last bit) can differ.
+ * of them, by atomic additions whose order (hence last bit) can differ; a slot
+ * that any of them brings is cleared before anything is added to it.  So the
+ * owner of a prefix and those that find it cached may be in one call, in any
+ * order.  A call that brings a token again (the last token of a prompt whose
+ * blocks were all found, stored once more) starts its sum again.
  */
 
 /*

@@ -7,7 +7,9 @@ queries, heads and positions, from the definitions:
   head's key collects the sum over the query heads of its group;
 * a call adds to the sums of keys that were there before it and sets the sums
   of the tokens that it brings (decode: the newest token; a prompt chunk: its
-  own tokens);
+  own tokens): those start at zero before any sequence of the call adds to them,
+  so that a slot which one sequence brings and another has cached, or several
+  bring, gets the weights of all;
 * eviction keeps the last `recent` positions and, of the others, the
   budget - recent with the largest sums (NaN as -inf, lowest position first
   among equals); kept positions below budget - recent stay, the kept ones
@@ -40,6 +42,9 @@ def decode_weights(key_weights, q, k_cache, block_tables, context_lens, scale):
     Hq = q.shape[1]
     qf = bf16_bits_to_f64(q)
     for s, L in enumerate(context_lens):
+        b, o = place_of(block_tables[s], int(L) - 1, BS)
+        after[b, :, o] = 0.0
+    for s, L in enumerate(context_lens):
         L = int(L)
         keys = bf16_bits_to_f64(gather_sequence(k_cache, block_tables[s], L))
         a = np.zeros((Hkv, L))
@@ -48,8 +53,6 @@ def decode_weights(key_weights, q, k_cache, block_tables, context_lens, scale):
             a[j] += softmax_weights(qf[s, h], keys[:, j], scale)
         for p in range(L):
             b, o = place_of(block_tables[s], p, BS)
-            if p == L - 1:
-                after[b, :, o] = 0.0
             after[b, :, o] += a[:, p]
             brought[b, :, o] += a[:, p]
     return after, brought
@@ -62,6 +65,11 @@ def prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, cu_seql
     NB, BS, Hkv, D = k_cache.shape
     Hq = q.shape[1]
     qf = bf16_bits_to_f64(q)
+    for s in range(len(cu_seqlens_q) - 1):
+        L = int(cu_seqlens_k[s + 1] - cu_seqlens_k[s])
+        for p in range(L - int(cu_seqlens_q[s + 1] - cu_seqlens_q[s]), L):
+            b, o = place_of(block_tables[s], p, BS)
+            after[b, :, o] = 0.0
     for s in range(len(cu_seqlens_q) - 1):
         q0, n = int(cu_seqlens_q[s]), int(cu_seqlens_q[s + 1] - cu_seqlens_q[s])
         L = int(cu_seqlens_k[s + 1] - cu_seqlens_k[s])
@@ -76,8 +84,6 @@ def prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, cu_seql
                 a[j, : c + i + 1] += softmax_weights(qf[q0 + i, h], keys[: c + i + 1, j], scale)
         for p in range(L):
             b, o = place_of(block_tables[s], p, BS)
-            if p >= c:
-                after[b, :, o] = 0.0
             after[b, :, o] += a[:, p]
             brought[b, :, o] += a[:, p]
     return after, brought

@@ -2,7 +2,7 @@
 //
 // One new token per sequence attends over its paged context, and the weight
 // that each key receives, summed over the query heads of its kv head, is added
-// to the key's running sum (the newest key's sum is set: its slot held another
+// to the key's running sum (the newest key's starts anew: its slot held another
 // token's).  The weights need the softmax's denominator, which is known only
 // when the whole context has been read, so the logits (4 G bytes a key and kv
 // head, beside the 4 D bytes of its K and V) go through the workspace:
@@ -11,7 +11,7 @@
 //     tiles, are cut into runs of equal length whatever the sequences' lengths;
 //     a warp takes one run for one kv head.  Of every sequence in its run it
 //     writes the logits (log2 units), and a part: their maximum and sum, and the
-//     unnormalised output.
+//     unnormalised output.  The run with a sequence's newest key clears its sum.
 //  2. Join, a programmatic dependent launch: every CTA joins the maxima and sums
 //     of a sequence's parts, then adds the weights of its own tokens to the sums
 //     and writes its share of the output.
@@ -447,8 +447,17 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
           }
         }
       }
-      // The run with the newest token stores it (no run of the call reads its slot).
-      if (p.new_k != nullptr && last == L && L == p.context_lens[s]) {
+      if (last != L || L != p.context_lens[s]) continue;
+      // The run with the newest token: its sum starts at zero.  (Here, and not by
+      // a store beside the second launch's additions: the slot may be in a block
+      // that another sequence of the call holds, too, as one of its older keys.)
+      if (lane == 0) {
+        const int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + ((L - 1) >> shift)];
+        if (blk >= 0 && blk < p.num_blocks)
+          p.key_weights[(((int64_t)blk * Hkv + j) << shift) + ((L - 1) & ((1 << shift) - 1))] = 0.f;
+      }
+      // And it is stored (no run of the call reads its slot).
+      if (p.new_k != nullptr) {
         const int64_t to = p.new_slots[s];
         if (to >= 0 && to < p.num_blocks << shift) {
           if (lane < kCols) {
@@ -483,7 +492,6 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
   // (The launch must not end before the first one has, or a next call on the
   // stream could share the workspace with it: one CTA always waits.)
   if (begin >= L && (blockIdx.x | blockIdx.y) != 0) return;
-  const int newest = p.context_lens[s] - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (begin >= L) return;
   const int tiles = p.tile_prefix[p.num_seqs];
@@ -576,9 +584,7 @@ __global__ void __launch_bounds__(join_threads(G)) decode_weights_join_kernel(co
       float a = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) a = fmaf(fast_exp2(z[x][g] - M[g]), inv[g], a);
-      float *w = p.key_weights + ((((int64_t)blk[x] * Hkv + j) << shift) + (i & ((1 << shift) - 1)));
-      if (i == newest) *w = a;
-      else atomicAdd(w, a);
+      atomicAdd(p.key_weights + ((((int64_t)blk[x] * Hkv + j) << shift) + (i & ((1 << shift) - 1))), a);
     }
   };
   add(begin);

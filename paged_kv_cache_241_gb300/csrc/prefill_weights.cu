@@ -5,7 +5,11 @@
 // the sum of key p (kv head j) receives
 //   a[p] = sum over queries i in [n - R, n) with c + i >= p, and over the query
 //          heads h of j's group, of softmax_p(scale <q[i,h], K[p,j]>):
-// added for keys cached before the chunk, set for the chunk's own.
+// added for keys cached before the chunk, set for the chunk's own: the first pass
+// clears the sums of those, and the second one, which runs when all of the first
+// has ended, adds to every key's.  (A sequence's own key may be another one's
+// cached key, where both hold a block and are in the same call: cleared before
+// anything is added, its sum has the weights of both whichever comes first.)
 //
 // A weight needs its row's softmax denominator, which needs the whole row, so
 // the product Q K^T is computed twice rather than kept (a pair's logit is 4
@@ -26,8 +30,8 @@
 // Both passes are the same persistent kernel: warp 0 loads tiles (TMA, 128-byte
 // swizzle, through the block table), warps 1 and 2 issue tcgen05.mma in turn (one
 // fills the queue while the other waits for its operands) into four 128-column
-// buffers of tensor memory, warp 3 fetches the rows' denominators (second pass),
-// warps 4-19 exponentiate and sum, a group of four for each buffer.  Loads,
+// buffers of tensor memory, warp 3 clears the sums of the chunks' keys (first pass)
+// or fetches the rows' denominators (second pass), warps 4-19 exponentiate and sum, a group of four for each buffer.  Loads,
 // products and exponentials of different steps overlap.
 //
 // Measured (first and second pass alone, us; the call):
@@ -273,6 +277,11 @@ struct Walk {
   __device__ __forceinline__ int sees(int rt, int row) const {
     const int r = (rt << tq_shift(p)) + (row >> p.group_shift);
     return r < q.R ? q.base + r : -1;
+  }
+  // The sum of a key in block blk.
+  __device__ __forceinline__ float *sum_of(int blk, int key) const {
+    return p.key_weights + ((((int64_t)blk * p.num_kv_heads + j) << p.block_shift) +
+                            (key & ((1 << p.block_shift) - 1)));
   }
   __device__ __forceinline__ int tile_rows(int rt) const {
     return min(1 << tq_shift(p), q.R - (rt << tq_shift(p))) << p.group_shift;
@@ -738,8 +747,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else if (warp == 3) {
-    // ---- second pass: the rows' denominators ----
-    if (PASS == 2) {
+    if (PASS == 1) {
+      // ---- first pass: the sums of the chunks' own keys start at zero ----
+      // (The last row tile of a head sees all of its keys, so each key tile is a
+      // step of it once.)
+      for (Walk<PASS> w(p, run); w.more(); w.next()) {
+        if (w.t1 != w.q.nrt - 1) continue;
+        int b0, b1, x0, x1;
+        w.steps(w.t1, b0, b1, x0, x1);
+        for (int x = max(x0, w.q.c >> 7); x < x1; ++x) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = x * kTile + i * 32 + lane;
+            if (key < w.q.c || key >= w.q.len_k) continue;
+            const int blk =
+                p.block_tables[(int64_t)w.s * p.max_blocks_per_seq + (key >> p.block_shift)];
+            if (blk >= 0 && blk < p.num_blocks) *w.sum_of(blk, key) = 0.f;
+          }
+        }
+      }
+    } else {
+      // ---- second pass: the rows' denominators ----
       asm volatile("griddepcontrol.wait;" ::: "memory");
       if (lane < 4) p.tickets[blockIdx.x * 4 + lane] = 0;
       int q_loads = 0;
@@ -1014,11 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (PASS == 1) {
           if (w.sees(t, row) >= 0) p.neg_lse[w.stat_at(t, row)] = -(mine.x + log2f(mine.y));
         } else if (blk >= 0 && blk < p.num_blocks) {
-          const int key = t * kTile + row;
-          float *to = p.key_weights + ((((int64_t)blk * p.num_kv_heads + w.j) << p.block_shift) +
-                                       (key & ((1 << p.block_shift) - 1)));
-          if (key >= w.q.c) *to = mine.y;
-          else atomicAdd(to, mine.y);
+          atomicAdd(w.sum_of(blk, t * kTile + row), mine.y);
         }
       }
       if (keeps) {  // every group releases the head's denominators

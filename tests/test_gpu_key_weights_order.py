@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import i32
-from test_gpu_key_weights import Step, batch
+import oracle
+from gpu_util import i32, oracle_caches
+from test_gpu_key_weights import Step, batch, prompts, weight_rtol
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,84 @@ def test_calls_wait_for_the_decode_before_them(lib, op, first):
         for a, c in zip(both(lambda: None), want):
             assert torch.equal(a, c)
     assert st.status_value() == 0
+
+
+# ------------------------------------- one sequence's own key, another's cached one
+
+def check_shared(st, tables, call, oracle_call):
+    """`call` ten times on stale sums (NaN where a token arrives), against the oracle.
+    A slot has an addition for each sequence at most, each off by 2^-24 of its result,
+    which is no more than the last one's."""
+    b = st.b
+    ekc, _ = oracle_caches(b)
+    kw, brought = oracle_call(st.sums0, ekc, tables)
+    assert np.isfinite(kw[np.unique(tables[tables >= 0])][:, :, :1]).all()
+    st.block_tables.copy_(i32(tables))
+    for _ in range(10):
+        st.kw.copy_(torch.from_numpy(st.sums0))
+        call()
+        assert st.status_value() == 0
+        got = st.kw.double().cpu().numpy()
+        bound = weight_rtol(b, ekc) * brought + b.num_seqs * 2.0**-24 * np.abs(kw)
+        bad = ~(np.abs(got - kw) <= bound) & ~(np.isnan(got) & np.isnan(kw))
+        assert not bad.any(), f"{int(bad.sum())} of {bad.size} outside; the first at {np.argwhere(bad)[0]}"
+
+
+def stale_sums(b, tables, first_own):
+    """Running sums, NaN in the slots of tokens that the call brings."""
+    sums = np.random.default_rng(5).random((b.num_blocks, b.num_kv_heads, b.block_size), dtype=np.float32)
+    for s, (c, L) in enumerate(zip(first_own, b.context_lens)):
+        p = np.arange(c, int(L))
+        sums[tables[s, p // b.block_size], :, p % b.block_size] = np.nan
+    return sums
+
+
+@pytest.mark.parametrize("owner", ["first", "last"])
+@pytest.mark.parametrize("window", [1, 40, 1 << 20])
+@pytest.mark.parametrize("G,D,bs", [(2, 64, 64), (1, 128, 128), (8, 64, 256)])
+def test_prompt_owner_of_a_prefix_and_those_that_find_it_in_one_call(lib, G, D, bs, window, owner):
+    """Full blocks get their keys when a prompt is admitted, so the prompts admitted
+    behind it hold its blocks before the call that fills them."""
+    new = [3 * bs + 70, 5, bs + 9, 1, 200, 33]
+    cached = [0] + [2 * bs] * 5
+    at = 0
+    if owner == "last":
+        new, cached, at = new[::-1], cached[::-1], 5
+    b = prompts(new, cached, G, 4, D, 91, block_size=bs)
+    tables = np.array(b.block_tables)
+    tables[:, :2] = tables[at, :2]
+    st = Step(lib, b, sums=stale_sums(b, tables, cached))
+    check_shared(st, tables, lambda: st.prefill_weights(window),
+                 lambda sums, kc, t: oracle.prefill_weights(sums, b.q, kc, t, b.cu_seqlens_q, b.cu_seqlens_k, window, b.scale))
+
+
+@pytest.mark.parametrize("owner", ["first", "last"])
+def test_prompt_found_whole_computes_its_last_token_again(lib, owner):
+    """The last token of a prompt whose blocks were all found is another sequence's
+    key (here still its own): the slot collects from both."""
+    new, cached = [512, 1, 1], [0, 255, 511]
+    at = 0
+    if owner == "last":
+        new, cached, at = new[::-1], cached[::-1], 2
+    b = prompts(new, cached, 2, 4, 64, 92)
+    tables = np.array(b.block_tables)
+    for s in range(3):
+        n = (new[s] + cached[s]) // 256
+        tables[s, :n] = tables[at, :n]
+    st = Step(lib, b, sums=stale_sums(b, tables, cached))
+    check_shared(st, tables, lambda: st.prefill_weights(1 << 20),
+                 lambda sums, kc, t: oracle.prefill_weights(sums, b.q, kc, t, b.cu_seqlens_q, b.cu_seqlens_k, 1 << 20, b.scale))
+
+
+@pytest.mark.parametrize("newest", ["first", "last"])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_decode_whose_newest_slot_is_in_a_shared_block(lib, G, newest):
+    lens = [256, 300, 256, 900]
+    if newest == "last":
+        lens = lens[::-1]
+    b = batch(lens, G, 4, 64, 93)
+    tables = np.array(b.block_tables)
+    tables[:, 0] = tables[0, 0]
+    st = Step(lib, b, sums=stale_sums(b, tables, [L - 1 for L in lens]))
+    check_shared(st, tables, st.decode_weights,
+                 lambda sums, kc, t: oracle.decode_weights(sums, b.q, kc, t, b.context_lens, b.scale))
