@@ -558,13 +558,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&tm_k);
   }
   __syncwarp();
+  // (the first pass may start under the tail of the kernel before the call; the
+  // second one starts when all of the first pass is past this point)
+  if (PASS == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Tensor memory after that wait only: the kernel before the call may still have
+  // to take its own, and would wait for this CTA's as this CTA for its end.  (The
+  // second pass's CTAs wait for first-pass ones, which have theirs and end.)
   if (warp == 1) {
     tmem_alloc(tmem_slot, kBufs * kTile);
     tmem_relinquish();
   }
-  // (the first pass may start under the tail of the kernel before the call; the
-  // second one starts when all of the first pass is past this point)
-  if (PASS == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   find_run<PASS>(p, run, scratch, PASS == 1 && blockIdx.x == 0);
   tc_fence_before_sync();
   __syncthreads();
