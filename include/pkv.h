@@ -376,6 +376,10 @@ size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max
  * depends on the batch, and with it the last bits; the same call gives the same
  * bits (keys in shared blocks apart).
  *
+ * A wait that runs out (PKV_DEV_TIMEOUT) while the rows' denominators are
+ * computed leaves rows out: the sums are then short of some queries' weights.
+ * One that runs out later leaves the sums of the call's sequences undefined.
+ *
  * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
  * block_size in {64, 128, 256, 512}; max_blocks_per_seq * block_size at most 2^20.
  */
@@ -385,6 +389,18 @@ pkv_status pkv_paged_prefill_weights(
     int max_seqlen_q, int window, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
     int max_blocks_per_seq, int64_t num_blocks, float scale, void *workspace,
     size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * test_prompt_fault -- TEST-ONLY fault injection for the bounded waits of
+ * paged_prefill_weights, as pkv_test_decode_fault is for decode's: sets, for
+ * the current device, the wall-clock limit of every wait (default 1 s) and,
+ * for the process, how many CTAs of a pass (1: denominators, 2: sums) load
+ * their tiles; the others wait for theirs in vain (-1: all load, the default).
+ * Restore with pkv_test_prompt_fault(1000000000, 1, -1).  Synchronous.  Returns
+ * PKV_ERR_INVALID_ARG for wait_limit_ns <= 0, a pass that is neither, or
+ * loading_ctas < -1.
+ */
+pkv_status pkv_test_prompt_fault(int64_t wait_limit_ns, int pass, int loading_ctas);
 
 /*
  * kv_evict -- shorten sequences to `budget` tokens, in place.

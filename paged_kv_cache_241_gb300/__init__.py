@@ -70,6 +70,7 @@ SIGNATURES = {
     "pkv_paged_prefill_weights": (_c_int, [_p, _p, _p, _p, _p, _p, _c_int, _c_i64, _c_int, _c_int,
                                            _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f,
                                            _p, _c_sz, _p, _p]),
+    "pkv_test_prompt_fault": (_c_int, [_c_i64, _c_int, _c_int]),
     "pkv_kv_evict": (_c_int, [_p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
                               _c_int, _c_int, _p, _p, _p, _p]),
     "pkv_w4a16_dequant": (_c_int, [_p, _p, _p, _c_i64, _c_i64, _c_int, _p]),
@@ -478,6 +479,14 @@ def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, c
         _c_int32(window), Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
         workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_prefill_weights")
+
+
+def test_prompt_fault(wait_limit_ns: int, which_pass: int, loading_ctas: int) -> None:
+    """TEST ONLY: shorten the wait limit of paged_prefill_weights on the current
+    device and let only the first `loading_ctas` CTAs of its first or second pass load
+    their tiles (-1: all).  Restore with test_prompt_fault(10**9, 1, -1)."""
+    _check(load().pkv_test_prompt_fault(int(wait_limit_ns), int(which_pass), int(loading_ctas)),
+           "test_prompt_fault")
 
 
 def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, recent, kept,

@@ -19,7 +19,7 @@ namespace pkv {
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // The limit the waits use.  Each translation unit has its own copy, fixed at
-// kWaitLimitNs except where a test hook shortens it (decode only).
+// kWaitLimitNs except where a test hook shortens it (decode, prompt key weights).
 static __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

@@ -45,6 +45,7 @@
 // scaling and sum 0.33; its product 0.17 (D = 64) or 0.33.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "host_common.h"
@@ -111,6 +112,7 @@ struct PromptParams {
   int window;
   int rows;          // min(window, max_seqlen_q): counted queries per sequence at most
   int by_query;      // a row's statistics are filed under its query (else sequence and rank)
+  int loading[2];    // CTAs of each pass that load their tiles: all, but in a test
   float qscale;
 };
 
@@ -498,10 +500,23 @@ __device__ void find_run(const PromptParams &p, Run *run, int64_t *scratch, bool
   }
 }
 
+// All threads of a first-pass CTA whose waits ran out: the row tiles of its run may
+// hold no denominators, or an earlier call's.  They are set to weigh nothing, so that
+// the second pass leaves their rows out.  (Another CTA may have finished a tile that
+// they share, or be about to: such a row counts or does not.  A call of its own: the
+// kernel has no registers to spare.)
+__device__ __noinline__ void leave_out(const PromptParams &p, const Run *run) {
+  const int row = threadIdx.x;
+  if (row >= kTile) return;
+  for (Walk<1> w(p, run); w.more(); w.next())
+    for (int t = w.t0; t <= w.t1; ++t)
+      if (w.sees(t, row) >= 0) p.neg_lse[w.stat_at(t, row)] = -INFINITY;
+}
+
 template <int D, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_k, const PromptParams p) {
+                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ PromptParams p) {
   using L = Layout<D, PASS>;
   constexpr int XR = D / 64;  // 128-byte regions across D
   constexpr int kKSlots = L::kKSlots, kQSlots = L::kQSlots;
@@ -561,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the first pass may start under the tail of the kernel before the call; the
   // second one starts when all of the first pass is past this point)
   if (PASS == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  find_run<PASS>(p, run, scratch, PASS == 1 && blockIdx.x == 0);
   // Tensor memory after that wait only: the kernel before the call may still have
   // to take its own, and would wait for this CTA's as this CTA for its end.  (The
   // second pass's CTAs wait for first-pass ones, which have theirs and end.)
@@ -568,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, kBufs * kTile);
     tmem_relinquish();
   }
-  find_run<PASS>(p, run, scratch, PASS == 1 && blockIdx.x == 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -592,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring rk, rq;
       int k_loads = 0, q_loads = 0;
-      bool ok = true;
+      bool ok = (int)blockIdx.x < p.loading[PASS - 1];
       const uint32_t in_block = (1u << p.block_shift) - 1;
       const bool two = in_block < kTile - 1;  // blocks of 64: two per tile
       for (Walk<PASS> w(p, run); ok && w.more(); w.next()) {
@@ -1057,7 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, PKV_DEV_TIMEOUT);
+  if (*abort_flag) {
+    if (threadIdx.x == 0) flag_status(p.status, PKV_DEV_TIMEOUT);
+    if (PASS == 1) leave_out(p, run);
+  }
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kBufs * kTile);
@@ -1079,6 +1097,10 @@ struct Plan {
     total = neg_lse + (size_t)(stat_rows * Hq) * sizeof(float);
   }
 };
+
+// Test-only fault injection, set by pkv_test_prompt_fault: PromptParams::loading of
+// the calls that follow.
+std::atomic<int> g_loading[2] = {{kMaxCtas}, {kMaxCtas}};
 
 template <int D>
 pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const PromptParams &prm,
@@ -1184,6 +1206,8 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   prm.window = window;
   prm.rows = (int)plan.rows;
   prm.by_query = plan.by_query ? 1 : 0;
+  prm.loading[0] = g_loading[0];
+  prm.loading[1] = g_loading[1];
   prm.qscale = scale * kLog2e;
 
   // q as {D, Hq, T}: a box is 64 dims x the G heads of a kv head x 128 / G
@@ -1211,4 +1235,19 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   const int64_t most_steps = most < kMaxCtas ? (int64_t)most : kMaxCtas;
   return head_dim == 128 ? launch<128>(tq, tk, prm, most_steps, st)
                          : launch<64>(tq, tk, prm, most_steps, st);
+}
+
+// ---------------------------------------------------------------------------
+// Test-only fault injection for the bounded waits of the prompt kernel.
+// ---------------------------------------------------------------------------
+
+extern "C" pkv_status pkv_test_prompt_fault(int64_t wait_limit_ns, int pass, int loading_ctas) {
+  if (wait_limit_ns <= 0 || (pass != 1 && pass != 2) || loading_ctas < -1)
+    return PKV_ERR_INVALID_ARG;
+  const unsigned long long limit = (unsigned long long)wait_limit_ns;
+  if (cudaMemcpyToSymbol(pkv::g_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  for (int x = 0; x < 2; ++x)
+    pkv::g_loading[x] = pass == x + 1 && loading_ctas >= 0 ? loading_ctas : pkv::kMaxCtas;
+  return PKV_OK;
 }
