@@ -290,8 +290,19 @@ struct Walk {
   }
 };
 
+// Wait on a barrier of the pass.  What the second pass's roles wait for can depend
+// on denominators, hence on the first pass, which may have long to go when a CTA
+// that shares the GPU with its tail begins (runs are equal by steps, not by time: up
+// to a fifth of the pass).  So the limit counts from the first pass's end on.
+template <int PASS>
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (PASS == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+  return mbar_wait_slow(bar, parity, abort);
+}
+template <int PASS>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  const bool ok = mbar_wait_bounded(bar, parity, abort);
+  const bool ok = wait_bar<PASS>(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -341,10 +352,12 @@ __device__ __forceinline__ int count_add(int *count) {
                : "memory");
   return n;
 }
-// Whole warp: wait until the count has passed n, as long as a barrier's wait may last.
+// Whole warp, second pass: wait until the count has passed n, as long as a barrier's
+// wait may last.
 __device__ __forceinline__ bool count_wait(const int *count, int n, volatile int *abort) {
   bool ok = true;
   if (count_get(count) - n <= 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1; ok && count_get(count) - n <= 0; ++i) {
       if ((i & 15u) == 0) {
@@ -629,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (blk0 < 0 || blk0 >= p.num_blocks) blk0 = 0;
             if (blk1 < 0 || blk1 >= p.num_blocks) blk1 = 0;
           }
-          if (!mbar_wait_bounded(&k_empty[rk.slot], rk.phase ^ 1, abort_flag)) return false;
+          if (!wait_bar<PASS>(&k_empty[rk.slot], rk.phase ^ 1, abort_flag)) return false;
           uint8_t *kd = sK + rk.slot * L::kTileBytes;
           mbar_arrive_expect_tx(&k_full[rk.slot], L::kTileBytes);
 #pragma unroll
@@ -645,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto load_q = [&](int rt) -> bool {
           const int slot = rq.slot;
-          if (!mbar_wait_bounded(&q_empty[slot], rq.phase ^ 1, abort_flag)) return false;
+          if (!wait_bar<PASS>(&q_empty[slot], rq.phase ^ 1, abort_flag)) return false;
           mbar_arrive_expect_tx(&q_full[slot], L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < XR; ++x)
@@ -692,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t uses = 0;  // bit g: parity of the uses of buffer g
       // The product of a Q slot and a K slot into buffer g.
       auto product = [&](int qslot, int kslot, int g, uint32_t idesc) -> bool {
-        if (!mbar_wait_bounded(&s_empty[g], ((uses >> g) & 1) ^ 1, abort_flag)) return false;
+        if (!wait_bar<PASS>(&s_empty[g], ((uses >> g) & 1) ^ 1, abort_flag)) return false;
         uses ^= 1u << g;
         tc_fence_after_sync();
         const uint64_t a = dq + (uint64_t)((qslot * L::kTileBytes) >> 4);
@@ -712,17 +725,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keeps) {
           for (int x = 0; ok && x < w.q.nrt; ++x) {
             const Ring at = ring_at(rq, x, kQSlots);
-            ok = mbar_wait_bounded(&q_full[at.slot], at.phase, abort_flag);
+            ok = wait_bar<PASS>(&q_full[at.slot], at.phase, abort_flag);
           }
         }
         for (int t = w.t0; ok && t <= w.t1; ++t) {
           int b0, b1, x0, x1;
           w.steps(t, b0, b1, x0, x1);
           if (PASS == 1) {
-            ok = mbar_wait_bounded(&q_full[rq.slot], rq.phase, abort_flag);
+            ok = wait_bar<PASS>(&q_full[rq.slot], rq.phase, abort_flag);
             for (int x = x0; ok && x < x1; ++x, ++k) {
               if ((k & 1) == me) {
-                ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag) &&
+                ok = wait_bar<PASS>(&k_full[rk.slot], rk.phase, abort_flag) &&
                      product(rq.slot, rk.slot, k & 3,
                              umma_idesc_bf16(kTile, kTile, false, false));
                 if (ok) umma_commit(&k_empty[rk.slot]);
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rq.next(kQSlots);
             continue;
           }
-          ok = mbar_wait_bounded(&k_full[rk.slot], rk.phase, abort_flag);
+          ok = wait_bar<PASS>(&k_full[rk.slot], rk.phase, abort_flag);
           for (int x = x0; ok && x < x1; ++x) {
             // (no more columns than the row tile has rows, to 16)
             const uint32_t idesc = umma_idesc_bf16(kTile, (w.tile_rows(x) + 15) & ~15, false, false);
@@ -741,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((t & 1) == me) ok = product(ring_at(rq, x, kQSlots).slot, rk.slot, t & 3, idesc);
               continue;
             }
-            ok = mbar_wait_bounded(&q_full[rq.slot], rq.phase, abort_flag);
+            ok = wait_bar<PASS>(&q_full[rq.slot], rq.phase, abort_flag);
             if ((k & 1) != me) {
               if (ok) mbar_arrive(&q_empty[rq.slot]);
             } else if (ok) {
@@ -762,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Wait for the products of both before tensor memory is freed.
       umma_commit(drain);
-      if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
+      if (!wait_bar<PASS>(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else if (warp == 3) {
     if (PASS == 1) {
@@ -803,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float *mine = p.neg_lse + w.stat_at(0, lane);  // this lane's of row tile 0
         auto fill = [&](int rt) -> bool {
           const int slot = q_loads & (kStatSlots - 1);
-          if (!warp_wait(&st_empty[slot], ((q_loads / kStatSlots) & 1) ^ 1, abort_flag)) return false;
+          if (!warp_wait<PASS>(&st_empty[slot], ((q_loads / kStatSlots) & 1) ^ 1, abort_flag)) return false;
           float *to = stat + slot * kTile + lane;
           const float *from = mine + (int64_t)(rt << tq_shift(p)) * p.num_q_heads;
           const int left = w.q.R - (rt << tq_shift(p)) - (lane >> p.group_shift);
@@ -843,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int q_loads = 0, swaps = 0, k = 0;  // (k: steps taken in turn)
     uint32_t phase_s = 0;  // of this group's buffer
     auto wait_product = [&]() -> bool {
-      if (!warp_wait(&s_full[side], phase_s, abort_flag)) return false;
+      if (!warp_wait<PASS>(&s_full[side], phase_s, abort_flag)) return false;
       phase_s ^= 1;
       tc_fence_after_sync();
       return true;
@@ -1016,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the others (8 whole prompts 94.8 -> 93.2 us).
         if (!keeps) {
           const int buf = swaps & 1, bar = quarter * 2 + buf;
-          ok = warp_wait(&x_empty[bar], ((swaps >> 1) & 1) ^ 1, abort_flag);
+          ok = warp_wait<PASS>(&x_empty[bar], ((swaps >> 1) & 1) ^ 1, abort_flag);
           if (!ok) break;
           ++swaps;
           float2 *part = ex + buf * kGroups * kTile + row;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from gpu_util import oracle_caches
+from gpu_util import i32, oracle_caches
 from test_gpu_key_weights import Step, assert_weights, prompts, weight_rtol
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +59,37 @@ def test_prompt_wait_runs_out_then_next_call_is_correct(lib, which, loading, D, 
     st.prefill_weights(window, ws=ws)
     assert st.status_value() == 0
     assert_weights(st.kw, kw, brought, rtol, "prompt weights after a timed-out call")
+
+
+def test_prompt_limit_does_not_count_the_first_pass(lib):
+    """Runs of the first pass take the same steps but not the same time (here 8 ms, up
+    to a fifth less): the second pass's CTAs that begin on the SMs that end first must
+    not take the others' remaining time for their own waits'."""
+    D, H, BS, new = 64, 16, 512, 40960
+    seqs = [(1, 639)] * 3000 + [(new, 0)]
+    need = [-(-(n + c) // BS) for n, c in seqs]
+    tables = np.full((len(seqs), max(need)), -1, np.int32)
+    ends = np.cumsum(need)
+    for s, (n, end) in enumerate(zip(need, ends)):
+        tables[s, :n] = np.arange(end - n, end)
+    cu_q, cu_k = (i32(np.concatenate([[0], np.cumsum(x)])) for x in ([n for n, _ in seqs], [n + c for n, c in seqs]))
+    gen = torch.Generator(device="cuda").manual_seed(97)
+    kc = torch.randn(int(ends[-1]), BS, H, D, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(new + 3000, H, D, generator=gen, device="cuda").bfloat16()
+    tables = i32(tables)
+    ws = lib.prefill_weights_workspace(len(seqs), q.shape[0], new, 1 << 20, H, H, tables.shape[1], BS)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        kw = torch.zeros((kc.shape[0], H, BS), device="cuda")
+        lib.paged_prefill_weights(kw, q, kc, tables, cu_q, cu_k, new, 1 << 20, D**-0.5, ws, status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return kw
+
+    want = call()
+    try:
+        lib.test_prompt_fault(500_000, 1, -1)  # healthy waits last microseconds
+        assert torch.equal(call(), want)
+    finally:
+        lib.test_prompt_fault(1_000_000_000, 1, -1)
