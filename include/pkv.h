@@ -319,8 +319,8 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  *   key_weights(slot of p, j) += a[s,j,p]  for p < context_lens[s] - 1
  *   key_weights(slot of p, j)  = a[s,j,p]  for p = context_lens[s] - 1
  * (the newest token is this call's own: its slot's old sum was another's).
- * fp32 logits and statistics; the weights are rounded to bf16 for the product
- * with V alone (as the tensor cores take them).  The batch's tokens are cut
+ * fp32 logits and statistics; for the product with V alone the weights are
+ * taken as the sum of two bf16 (off by 2^-18 of a weight).  The batch's tokens are cut
  * into runs of equal length, so the last bits of a sequence's results can
  * change with the other sequences' lengths; the same call gives the same bits.
  *

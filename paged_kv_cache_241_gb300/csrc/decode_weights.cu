@@ -201,6 +201,13 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // same in S, in P and in O, so maximum and rescaling need no exchange of O.
 // Decode moves D * 4 bytes for 4 G D operations, far below what these products
 // run at: the loop is there to keep loads in flight (128 KB per SM).
+//
+// P is an operand in bf16: it goes in as the sum of two, its rounding and what
+// that leaves, so that a weight is off by 2^-18 of itself and not by 2^-9 (the
+// attention of paged_decode_attn keeps it in fp32; the outputs of the two then
+// differ by their own rounding alone).  A group of at most four heads has columns
+// to spare: columns 4 to 7 repeat the heads of 0 to 3 and take the second parts,
+// and the two halves of O are added at the end.  Eight heads need a second product.
 template <int D, int G>
 __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(const WeightsParams p) {
   using W = WarpSmem<D, G>;
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
 
     // The consuming side: sequence after sequence of the run.
     const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
-    const bool owner = h0 < G;      // (of the 8 columns only G are heads)
+    const bool owner = h0 < G;      // (of the 8 columns only G are heads of their own)
     int slot = 0, qslot = 0;
     for (int s = seq_of(prefix, S, t_begin), tile = t_begin; tile < t_end; s = next_seq(s)) {
       const int L = visible(p, s);
@@ -335,10 +342,10 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
         __syncwarp();  // every lane's copies are in, and the slot filled next is read out
         issue();
         if (tok == first) {
-          // q as the second operand: lane (head, dim pair) per 8 dims.  Rows past
-          // G repeat the last one (their columns are not used).
+          // q as the second operand: lane (head, dim pair) per 8 dims.  With fewer than
+          // eight heads, rows 4 to 7 are 0 to 3 again, those past G the last one.
           const uint32_t qa = qslots + qslot * W::kQ;
-          const int row = min(lane & 7, G - 1);
+          const int row = G == 8 ? lane & 7 : min(lane & 3, G - 1);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t f[4];
@@ -403,10 +410,21 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
             o[i][2] *= a0;
             o[i][3] *= a1;
           }
-          // P as the second operand of the next product: rounded to bf16 there,
-          // as the tensor cores take it; the sums keep the fp32 weights.
-          const uint32_t b0 = transpose8x8(pack_bf16x2(p0, p1));
-          const uint32_t b1 = transpose8x8(pack_bf16x2(p2, p3));
+          // P as the second operand of the next product, in two parts (see above);
+          // the sums keep the fp32 weights.
+          uint32_t first0 = pack_bf16x2(p0, p1), first1 = pack_bf16x2(p2, p3);
+          const uint32_t rest0 = pack_bf16x2(p0 - bf16lo(first0), p1 - bf16hi(first0));
+          const uint32_t rest1 = pack_bf16x2(p2 - bf16lo(first1), p3 - bf16hi(first1));
+          if (G < 8 && (lane & 2)) {
+            first0 = rest0;
+            first1 = rest1;
+          }
+          const uint32_t b0 = transpose8x8(first0), b1 = transpose8x8(first1);
+          uint32_t c0 = 0, c1 = 0;
+          if (G == 8) {
+            c0 = transpose8x8(rest0);
+            c1 = transpose8x8(rest1);
+          }
           // V^T: two 8-token halves by two 8-dim columns, transposed on the way.
           const int vr = sl * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
@@ -414,6 +432,7 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
             uint32_t a[4];
             ldmatrix4_trans(a, va + tile_at<D>(vr, 2 * i + ((lane >> 3) & 1)));
             mma16816(o[i], a, b0, b1);
+            if (G == 8) mma16816(o[i], a, c0, c1);
           }
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
@@ -422,6 +441,12 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) decode_weights_kernel(cons
       for (int k = 4; k < 32; k <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, k);
         l1 += __shfl_xor_sync(0xffffffffu, l1, k);
+      }
+      if (G < 8) {  // the two halves of O
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[i][x] += __shfl_xor_sync(0xffffffffu, o[i][x], 2);
       }
       const int64_t part = (int64_t)(s + r) * Hkv + j;
       if (owner) {
