@@ -383,8 +383,8 @@ def _workspace(n, what, device):
 def decode_weights_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                              max_total_blocks, device="cuda"):
     """Allocate a zero-filled workspace for paged_decode_weights_attn."""
-    n = int(load().pkv_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads,
-                                                     head_dim, block_size, max_total_blocks))
+    ints = map(_c_int32, (num_seqs, num_q_heads, num_kv_heads, head_dim, block_size))
+    n = int(load().pkv_decode_weights_workspace_size(*ints, _c_int64(max_total_blocks)))
     return _workspace(n, "decode_weights_workspace", device)
 
 
@@ -425,7 +425,7 @@ def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_table
         out.data_ptr(), key_weights.data_ptr(), q.data_ptr(), _addr(k), _addr(v),
         _addr(slot_mapping), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), S, Hq, Hkv, D, BS, table_shape[1], NB,
-        int(max_total_blocks), float(scale), workspace.data_ptr(), workspace.numel(),
+        _c_int64(max_total_blocks), float(scale), workspace.data_ptr(), workspace.numel(),
         _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_decode_weights_attn")
 
@@ -433,9 +433,10 @@ def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_table
 def prefill_weights_workspace(num_seqs, total_q, max_seqlen_q, window, num_q_heads, num_kv_heads,
                               max_blocks_per_seq, block_size, device="cuda"):
     """Allocate a zero-filled workspace for paged_prefill_weights."""
-    n = int(load().pkv_prefill_weights_workspace_size(
-        num_seqs, total_q, max_seqlen_q, _c_int32(window), num_q_heads, num_kv_heads,
-        max_blocks_per_seq, block_size))
+    ints = map(_c_int32, (max_seqlen_q, window, num_q_heads, num_kv_heads, max_blocks_per_seq,
+                          block_size))
+    n = int(load().pkv_prefill_weights_workspace_size(_c_int32(num_seqs), _c_int64(total_q),
+                                                      *ints))
     return _workspace(n, "prefill_weights_workspace", device)
 
 
@@ -443,6 +444,11 @@ def _c_int32(x) -> int:
     """An int argument as the library sees it: what does not fit stays too large
     or becomes -1 (refused there), instead of wrapping around."""
     return max(-1, min(int(x), 0x7FFFFFFF))
+
+
+def _c_int64(x) -> int:
+    """The same for an int64 argument."""
+    return max(-1, min(int(x), 0x7FFFFFFFFFFFFFFF))
 
 
 def paged_prefill_weights(key_weights, q, k_cache, block_tables, cu_seqlens_q, cu_seqlens_k,
@@ -587,7 +593,7 @@ class BlockManager:
         """The sequence is cut to its first keep_tokens places by kv_evict on
         its table as it was before this call; raises, changing nothing, when
         another sequence shares one of the blocks that eviction would rewrite."""
-        _check(self._lib.pkv_bm_evict(self._h, int(seq_id), int(keep_tokens)), "pkv_bm_evict")
+        _check(self._lib.pkv_bm_evict(self._h, int(seq_id), _c_int32(keep_tokens)), "pkv_bm_evict")
 
     def num_tokens(self, seq_id: int) -> int:
         return int(self._lib.pkv_bm_num_tokens(self._h, int(seq_id)))
