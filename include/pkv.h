@@ -416,7 +416,8 @@ pkv_status pkv_test_prompt_fault(int64_t wait_limit_ns, int pass, int loading_ct
  * left as they were and are the caller's to reuse (pkv_bm_evict).
  *   kept      int32 [num_seqs, Hkv, budget]: the position, before the call,
  *             of the token now at each place (-1 past a shorter sequence's end)
- *   new_lens  int32 [num_seqs]: min(L, budget); must not be context_lens itself
+ *   new_lens  int32 [num_seqs]: min(L, budget); must not overlap context_lens,
+ *             nor k_cache v_cache (PKV_ERR_INVALID_ARG)
  * Sequences of at most `budget` tokens are not touched.  Decode does not
  * depend on the order of the keys, so attention goes on with new_lens as the
  * context length; the positions that the model encodes count on from the old

@@ -482,7 +482,15 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   if (!aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(key_weights) & 3u) != 0)
     return PKV_ERR_INVALID_ARG;
-  if (new_lens == context_lens) return PKV_ERR_INVALID_ARG;  // every kv head reads the old length
+  // Buffers that share memory: K and V rows are moved by CTAs of their own, and every
+  // kv head reads the old lengths.
+  auto overlap = [](const void *a, const void *b, int64_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x < y ? y - x : x - y) < (uint64_t)bytes;
+  };
+  if (overlap(k_cache, v_cache, num_blocks * block_size * num_kv_heads * head_dim * 2) ||
+      overlap(context_lens, new_lens, (int64_t)num_seqs * 4))
+    return PKV_ERR_INVALID_ARG;
 
   EvictParams prm;
   prm.k_cache = k_cache;

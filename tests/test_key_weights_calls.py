@@ -46,3 +46,15 @@ def test_workspaces_do_not_wrap(lib):  # noqa: F811
         with pytest.raises(ValueError, match="no workspace"):
             pkv.decode_weights_workspace(**dict(sizes, **{name: (1 << 64) + sizes[name]}), device="meta")
     assert pkv.decode_weights_workspace(**dict(sizes, num_seqs=big + 4), device="meta").numel() > 1 << 40
+
+
+# ------------------------------------------------------------------ buffers that overlap
+
+def test_evict_rejects_buffers_that_overlap(lib):  # noqa: F811
+    base = dict(kc=1 << 40, vc=1 << 41, kw=1 << 42, bt=1 << 43, cl=1 << 44, S=4, Hkv=8, D=128, BS=256, maxb=8, NB=64,
+                budget=1024, recent=32, kept=1 << 45, nl=1 << 46, st=None, stream=None)
+    cache = 64 * 256 * 8 * 128 * 2
+    # (refused before any launch: there is no GPU here, and what is not refused fails to launch)
+    for kw in (dict(vc=base["kc"]), dict(vc=base["kc"] + cache - 16), dict(vc=base["kc"] - cache + 16),
+               dict(nl=base["cl"]), dict(nl=base["cl"] + 12), dict(nl=base["cl"] - 12)):
+        assert lib.pkv_kv_evict(*dict(base, **kw).values()) == 1, kw
