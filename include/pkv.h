@@ -335,6 +335,8 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  * More tokens than max_total_blocks blocks hold: PKV_DEV_WORKSPACE, nothing is
  * written.
  *
+ * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
+ *
  * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
  * block_size in {64, 128, 256, 512}; num_seqs <= 16384; max_blocks_per_seq *
  * block_size at most 65535 * 1024.
@@ -379,6 +381,8 @@ size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max
  * A wait that runs out (PKV_DEV_TIMEOUT) while the rows' denominators are
  * computed leaves rows out: the sums are then short of some queries' weights.
  * One that runs out later leaves the sums of the call's sequences undefined.
+ *
+ * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
  *
  * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
  * block_size in {64, 128, 256, 512}; max_blocks_per_seq * block_size at most 2^20.

@@ -786,7 +786,8 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
   if ((int64_t)num_seqs * num_kv_heads > 0x7FFFFFFFLL ||
       (int64_t)max_blocks_per_seq * block_size > (int64_t)65535 * kJoinTokens)
     return PKV_ERR_UNSUPPORTED;
-  if (!isfinite(scale)) return PKV_ERR_INVALID_ARG;  // NaN or infinite
+  // NaN or infinite, itself or in the exponentials' base 2 (a logit of zero would be NaN)
+  if (!isfinite(scale * kLog2e)) return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
   if (!out || !key_weights || !q || !k_cache || !v_cache || !block_tables || !context_lens)
     return PKV_ERR_INVALID_ARG;

@@ -1181,7 +1181,8 @@ extern "C" pkv_status pkv_paged_prefill_weights(
   if (block_size != 64 && block_size != 128 && block_size != 256 && block_size != 512)
     return PKV_ERR_UNSUPPORTED;
   if ((int64_t)max_blocks_per_seq * block_size > kMaxTokens) return PKV_ERR_UNSUPPORTED;
-  if (!isfinite(scale)) return PKV_ERR_INVALID_ARG;  // NaN or infinite
+  // NaN or infinite, itself or in the exponentials' base 2 (a logit of zero would be NaN)
+  if (!isfinite(scale * kLog2e)) return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (total_q > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
   if (!key_weights || !q || !k_cache || !block_tables || !cu_seqlens_q || !cu_seqlens_k)

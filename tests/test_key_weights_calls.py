@@ -4,6 +4,7 @@ import pytest
 
 import paged_kv_cache_241_gb300 as pkv
 from test_abi import lib  # noqa: F401  (fixture: the built library, no GPU)
+from test_key_weights_host import decode_call, prompt_call
 
 
 def test_prompt_fault_hook_rejects_bad_arguments(lib):  # noqa: F811
@@ -58,3 +59,15 @@ def test_evict_rejects_buffers_that_overlap(lib):  # noqa: F811
     for kw in (dict(vc=base["kc"]), dict(vc=base["kc"] + cache - 16), dict(vc=base["kc"] - cache + 16),
                dict(nl=base["cl"]), dict(nl=base["cl"] + 12), dict(nl=base["cl"] - 12)):
         assert lib.pkv_kv_evict(*dict(base, **kw).values()) == 1, kw
+
+
+# ----------------------------------------------------------------------- the scale
+
+def test_scales_that_overflow_in_base_two_are_refused(lib):  # noqa: F811
+    # (checked before the batch's size: S = 0 and T = 0 launch nothing)
+    for scale in (3.0e38, -3.0e38, 2.4e38):                 # times log2(e): past 3.4e38
+        assert decode_call(lib, S=0, scale=scale) == 1
+        assert prompt_call(lib, T=0, scale=scale) == 1
+    for scale in (2.3e38, -2.3e38, 0.0):
+        assert decode_call(lib, S=0, scale=scale) == 0
+        assert prompt_call(lib, T=0, scale=scale) == 0
