@@ -43,6 +43,9 @@ uint64_t block_key(uint64_t parent, const int32_t *tokens, int n) {
 struct Seq {
   std::vector<int32_t> table;   // physical block of each logical block
   std::vector<int32_t> tokens;  // all tokens so far (keys of blocks that fill up)
+  // Key of the last full block, whether that block answers for it or another one with
+  // the same tokens does: the next block's key hangs on it.
+  uint64_t chain = 0;
   bool cut = false;             // evicted: places no longer hold the tokens in order
 };
 
@@ -110,9 +113,6 @@ struct pkv_block_manager {
   void release(int b) {
     if (--ref[b] == 0) push_free(b);
   }
-  uint64_t key_of_block(const Seq &s, int i) const {
-    return i < 0 ? 0 : key[s.table[i]];
-  }
 };
 
 extern "C" pkv_block_manager *pkv_bm_create(int num_blocks, int block_size) {
@@ -176,10 +176,11 @@ extern "C" pkv_status pkv_bm_allocate(pkv_block_manager *m, int64_t seq_id, cons
     const int b = m->take_fresh();
     s.table.push_back(b);
     if (i < full) {  // a full block gets its key now, for later sequences
-      const uint64_t k = block_key(m->key_of_block(s, i - 1), tokens + (size_t)i * bs, bs);
-      m->set_key(b, k, tokens + (size_t)i * bs);
+      parent = block_key(parent, tokens + (size_t)i * bs, bs);
+      m->set_key(b, parent, tokens + (size_t)i * bs);
     }
   }
+  s.chain = parent;
   // At least the last prompt token is computed even when every block was found.
   int cached = (int)hits.size() * bs;
   if (cached >= num_tokens) cached = num_tokens - 1;
@@ -203,10 +204,9 @@ extern "C" pkv_status pkv_bm_append(pkv_block_manager *m, int64_t seq_id, int32_
   if ((len + 1) % bs == 0 && !s.cut) {  // a block just filled up: key it for later sequences
     const int i = (len + 1) / bs - 1;
     const int b = s.table[i];
-    if (m->key[b] == 0) {
-      const uint64_t k = block_key(m->key_of_block(s, i - 1), &s.tokens[(size_t)i * bs], bs);
-      if (m->lookup(k, &s.tokens[(size_t)i * bs]) < 0) m->set_key(b, k, &s.tokens[(size_t)i * bs]);
-    }
+    s.chain = block_key(s.chain, &s.tokens[(size_t)i * bs], bs);
+    if (m->key[b] == 0 && m->lookup(s.chain, &s.tokens[(size_t)i * bs]) < 0)
+      m->set_key(b, s.chain, &s.tokens[(size_t)i * bs]);
   }
   return PKV_OK;
 }
