@@ -694,8 +694,7 @@ pkv_status launch(WeightsParams prm, cudaStream_t stream) {
   if (warps > kWarpsMost) warps = kWarpsMost;
   static_assert((kMaxDynamicSmem - 1024 - (kMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
   const int smem = warps * WarpSmem<D, G>::bytes + prefix;
-  int ctas = 0;
-  if (!kernel_smem_setup((const void *)decode_weights_kernel<D, G>, warps * 32, smem, &ctas))
+  if (!kernel_smem_setup((const void *)decode_weights_kernel<D, G>, warps * 32, smem, nullptr))
     return PKV_ERR_CUDA;
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
   const int kRows = WarpSmem<D, G>::kRows;

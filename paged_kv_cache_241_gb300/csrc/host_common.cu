@@ -41,6 +41,7 @@ bool kernel_smem_setup(const void *func, int threads, int bytes, int *ctas_per_s
       return false;
     st.configured = bytes;
   }
+  if (ctas_per_sm == nullptr) return true;
   if (st.occ_bytes != bytes) {
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, (size_t)bytes) !=

@@ -15,7 +15,9 @@ int device_sm_count();
 // Let `func` (a __global__ function) use `bytes` of dynamic shared memory on
 // the current device (the attribute is per device; it is only ever raised)
 // and store in *ctas_per_sm how many of its CTAs of `threads` threads fit on
-// an SM with that much.  Cached per (kernel, device) and thread-safe.
+// an SM with that much (null: not asked for; the answer is kept for one size at a
+// time, so that calls of alternating sizes would ask anew).  Cached per (kernel,
+// device) and thread-safe.
 // Returns false on a CUDA error.
 bool kernel_smem_setup(const void *func, int threads, int bytes, int *ctas_per_sm);
 

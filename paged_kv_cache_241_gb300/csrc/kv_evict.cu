@@ -519,10 +519,9 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
   // 1025 to 1280 tokens 42.4 us with 256 threads and 58.2 with 1024; 128 units of
   // 2000 to 16384 tokens 66.0 and 51.2.
   const bool is_long = room > kLongContext;
-  int ctas = 0;
   if (!kernel_smem_setup(is_long ? (const void *)evict_select_kernel<1024>
                                  : (const void *)evict_select_kernel<256>,
-                         is_long ? 1024 : 256, smem, &ctas))
+                         is_long ? 1024 : 256, smem, nullptr))
     return PKV_ERR_CUDA;
   // Both programmatic dependents, the first one of the kernel before the call (16
   // prompts 50.5 -> 48.0 us from call to call, the copy of their sums included).

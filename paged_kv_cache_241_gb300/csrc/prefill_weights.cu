@@ -1120,10 +1120,9 @@ pkv_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const PromptPara
                   int64_t most_steps, cudaStream_t stream) {
   constexpr int smem = Layout<D, 1>::total + 1024;
   const int sms = device_sm_count();
-  int ctas = 0;
   if (sms <= 0 ||
-      !kernel_smem_setup((const void *)prompt_weights_kernel<D, 1>, kThreads, smem, &ctas) ||
-      !kernel_smem_setup((const void *)prompt_weights_kernel<D, 2>, kThreads, smem, &ctas))
+      !kernel_smem_setup((const void *)prompt_weights_kernel<D, 1>, kThreads, smem, nullptr) ||
+      !kernel_smem_setup((const void *)prompt_weights_kernel<D, 2>, kThreads, smem, nullptr))
     return PKV_ERR_CUDA;
   int64_t grid = sms < kMaxCtas ? sms : kMaxCtas;
   if (grid > most_steps) grid = most_steps;
