@@ -484,12 +484,13 @@ extern "C" pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *
     return PKV_ERR_INVALID_ARG;
   // Buffers that share memory: K and V rows are moved by CTAs of their own, and every
   // kv head reads the old lengths.
-  auto overlap = [](const void *a, const void *b, int64_t bytes) {
+  // (in double: any number of blocks, and distances below 2^53 exactly)
+  auto overlap = [](const void *a, const void *b, double bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return (x < y ? y - x : x - y) < (uint64_t)bytes;
+    return (double)(x < y ? y - x : x - y) < bytes;
   };
-  if (overlap(k_cache, v_cache, num_blocks * block_size * num_kv_heads * head_dim * 2) ||
-      overlap(context_lens, new_lens, (int64_t)num_seqs * 4))
+  if (overlap(k_cache, v_cache, (double)num_blocks * block_size * num_kv_heads * head_dim * 2) ||
+      overlap(context_lens, new_lens, num_seqs * 4.0))
     return PKV_ERR_INVALID_ARG;
 
   EvictParams prm;

@@ -57,6 +57,7 @@ def test_evict_rejects_buffers_that_overlap(lib):  # noqa: F811
     cache = 64 * 256 * 8 * 128 * 2
     # (refused before any launch: there is no GPU here, and what is not refused fails to launch)
     for kw in (dict(vc=base["kc"]), dict(vc=base["kc"] + cache - 16), dict(vc=base["kc"] - cache + 16),
+               dict(vc=base["kc"] + 16, NB=1 << 62), dict(vc=base["kc"] + 16, NB=(1 << 63) - 1),
                dict(nl=base["cl"]), dict(nl=base["cl"] + 12), dict(nl=base["cl"] - 12)):
         assert lib.pkv_kv_evict(*dict(base, **kw).values()) == 1, kw
 
