@@ -142,3 +142,29 @@ def test_decode_whose_newest_slot_is_in_a_shared_block(lib, G, newest):
     st = Step(lib, b, sums=stale_sums(b, tables, [L - 1 for L in lens]))
     check_shared(st, tables, st.decode_weights,
                  lambda sums, kc, t: oracle.decode_weights(sums, b.q, kc, t, b.context_lens, b.scale))
+
+
+# ---------------------------------------------------------------- two calls at a time
+
+def test_prompts_on_two_streams(lib):
+    """Each pass takes all of an SM's tensor memory; calls on two streams take turns."""
+    shapes = [([900, 300, 64, 1200], [100, 0, 700, 0]), ([33, 1500, 257], [2000, 0, 31])]
+    steps = [Step(lib, prompts(new, cached, 2, 2, 128, 94 + i)) for i, (new, cached) in enumerate(shapes)]
+    windows = (1 << 20, 48)
+    want, spaces = [], []
+    for st, window in zip(steps, windows):
+        b = st.b
+        spaces.append(lib.prefill_weights_workspace(b.num_seqs, b.q.shape[0], int(b.new_lens.max()), window, b.num_q_heads,
+                                                    b.num_kv_heads, b.block_tables.shape[1], b.block_size))
+        st.prefill_weights(window, ws=spaces[-1])
+        want.append(st.kw.clone())
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(10):
+        for st in steps:
+            st.kw.copy_(torch.from_numpy(st.sums0))
+        torch.cuda.synchronize()
+        for st, window, ws, stream in zip(steps, windows, spaces, streams):
+            st.prefill_weights(window, ws=ws, stream=stream)
+        torch.cuda.synchronize()
+        for st, kw in zip(steps, want):
+            assert torch.equal(st.kw, kw) and st.status_value() == 0
