@@ -325,8 +325,8 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  * change with the other sequences' lengths; the same call gives the same bits.
  *
  * workspace: device memory of at least pkv_decode_weights_workspace_size(...)
- * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that
- * overlap on the device must not share a workspace.
+ * bytes, 256-byte aligned; it needs no initialisation (a call reads what it has
+ * written itself).  Calls that overlap on the device must not share a workspace.
  *
  * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its
  * row of out is left as it was; one that is longer than its table is flagged
@@ -339,7 +339,8 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  *
  * Two launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
  * block_size in {64, 128, 256, 512}; num_seqs <= 16384; max_blocks_per_seq *
- * block_size at most 65535 * 1024.
+ * block_size at most 65535 * 1024; max_total_blocks * block_size at most
+ * (2^31 - 1) * 2048 / head_dim.
  */
 pkv_status pkv_paged_decode_weights_attn(
     uint16_t *out, float *key_weights, const uint16_t *q, const uint16_t *new_k,
@@ -376,7 +377,8 @@ size_t pkv_prefill_weights_workspace_size(int num_seqs, int64_t total_q, int max
  * bytes, 256-byte aligned, zero-filled once before its first use.  Calls that
  * overlap on the device must not share a workspace.  How the work is split
  * depends on the batch, and with it the last bits; the same call gives the same
- * bits (keys in shared blocks apart).
+ * bits (keys in shared blocks apart).  A row's denominator is kept as one fp32
+ * logarithm, so a weight is off by 2^-24 of that logarithm too.
  *
  * A wait that runs out (PKV_DEV_TIMEOUT) while the rows' denominators are
  * computed leaves rows out: the sums are then short of some queries' weights.

@@ -382,7 +382,7 @@ def _workspace(n, what, device):
 
 def decode_weights_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                              max_total_blocks, device="cuda"):
-    """Allocate a zero-filled workspace for paged_decode_weights_attn."""
+    """Allocate a workspace for paged_decode_weights_attn."""
     ints = map(_c_int32, (num_seqs, num_q_heads, num_kv_heads, head_dim, block_size))
     n = int(load().pkv_decode_weights_workspace_size(*ints, _c_int64(max_total_blocks)))
     return _workspace(n, "decode_weights_workspace", device)
@@ -432,7 +432,8 @@ def paged_decode_weights_attn(out, key_weights, q, k_cache, v_cache, block_table
 
 def prefill_weights_workspace(num_seqs, total_q, max_seqlen_q, window, num_q_heads, num_kv_heads,
                               max_blocks_per_seq, block_size, device="cuda"):
-    """Allocate a zero-filled workspace for paged_prefill_weights."""
+    """Allocate a zero-filled workspace for paged_prefill_weights (filled on the
+    current stream: calls on another one wait for it)."""
     ints = map(_c_int32, (max_seqlen_q, window, num_q_heads, num_kv_heads, max_blocks_per_seq,
                           block_size))
     n = int(load().pkv_prefill_weights_workspace_size(_c_int32(num_seqs), _c_int64(total_q),

@@ -17,10 +17,10 @@
 //     and writes its share of the output.
 //
 // Bound by HBM.  Measured: 64 sequences of 128 to 2048 tokens with their store
-// (16 heads on 8, D = 128: 283 MB) 56 us, of which the first launch alone 50 to 53 at
-// 5.3 to 5.6 TB/s (about 80 % of a copy); 64 skewed ones to 8192 tokens (594 MB) 110 us,
-// 96 at 6.1 TB/s; two of 24 K to 33 K tokens (64 heads on 8: 236 MB) 52 us, 44 at 5.3
-// TB/s.  What is above the reading is the second launch (10, 15 and 14 us alone, its
+// (16 heads on 8, D = 128: 283 MB) 56 us, of which the first launch alone 50 to 55 at
+// 5.2 to 5.6 TB/s (about 80 % of a copy); 64 skewed ones to 8192 tokens (594 MB) 110 us,
+// 98 at 6.0 TB/s; two of 24 K to 33 K tokens (64 heads on 8: 236 MB) 52 us, 45 at 5.2
+// TB/s.  What is above the reading is the second launch (11, 16 and 13 us alone, its
 // caches cold): it starts when the last maximum is known.
 #include <math.h>
 
@@ -804,7 +804,7 @@ extern "C" pkv_status pkv_paged_decode_weights_attn(
     return PKV_ERR_WORKSPACE;
 
   WeightsParams prm;
-  // (32-bit tile numbers; a longer bound admits what they can number)
+  // (32-bit tile numbers: a bound of more tiles is refused)
   const int rows = 2048 / head_dim;
   prm.max_tiles = max_total_blocks * block_size / rows;
   if (prm.max_tiles > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;

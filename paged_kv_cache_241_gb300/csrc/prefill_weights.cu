@@ -34,15 +34,24 @@
 // or fetches the rows' denominators (second pass), warps 4-19 exponentiate and sum, a group of four for each buffer.  Loads,
 // products and exponentials of different steps overlap.
 //
+// A row's denominator is kept as one fp32, its -log2 (the maximum included): an error
+// of 2^-24 of that number, so for every weight of the row 2^-24 ln 2 times it, below
+// 1e-6 while the logits are below 16.  Maximum and sum apart would be exact to the
+// sum, and a second read of shared memory for every exponential of the second pass,
+// where the one there is costs 6 of 80 us.
+//
 // Measured (first and second pass alone, us; the call):
-//   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  24 + 21, 34
+//   window of 32, 16 prompts to 4096 tokens, 16 heads on 8, D = 128:  26 + 23, 35
 //   12 chunks of 100 to 512 on up to 7800 cached, window 64, 32 heads on 8,
-//   D = 64:                                                           40 + 49, 80
-//   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           47 + 53, 89
-// A window's first pass is the reading of K (73 MB) and the two prologues; the
-// others are bound by the exponentials and the arithmetic around them: a step takes
-// 0.40 to 0.50 us, its 16384 exponentials alone 0.26 (62 a nanosecond and SM), with
-// scaling and sum 0.33; its product 0.17 (D = 64) or 0.33.
+//   D = 64:                                                           41 + 51, 80
+//   8 whole prompts of 300 to 2048, 16 heads on 8, D = 128:           49 + 54, 90
+// A window's first pass is the reading of K (73 MB) and the two prologues.  In the
+// others no single stage is the bound: a step takes 0.40 to 0.50 us, its 16384
+// exponentials alone 0.26 (62 a nanosecond and SM), with scaling and sum 0.33; its
+// product 0.17 (D = 64) or 0.33; and copies without exponentials, tensor-memory loads
+// and three quarters of each product were only 9 to 17 % faster.  What is left is the
+// hand-over between steps: a group has one S buffer, and from its last load of it
+// until the next product has arrived it has the last 32 columns' exponentials to do.
 #include <math.h>
 
 #include <atomic>
