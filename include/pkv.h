@@ -298,7 +298,9 @@ size_t pkv_prefill_workspace_size(void);
  * that any of them brings is cleared before anything is added to it.  So the
  * owner of a prefix and those that find it cached may be in one call, in any
  * order.  A call that brings a token again (the last token of a prompt whose
- * blocks were all found, stored once more) starts its sum again.
+ * blocks were all found, stored once more) starts its sum again; its row should
+ * be the one that is there, since others of the call may read it before or
+ * after a fused store.
  */
 
 /*
