@@ -6,7 +6,7 @@ import torch
 
 import oracle
 from gpu_util import i32, oracle_caches
-from test_gpu_key_weights import Step, batch, prompts, weight_rtol
+from test_gpu_key_weights import Step, assert_weights, batch, prompts, weight_rtol
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,16 @@ def test_prompts_on_two_streams(lib):
         torch.cuda.synchronize()
         for st, kw in zip(steps, want):
             assert torch.equal(st.kw, kw) and st.status_value() == 0
+
+
+@pytest.mark.parametrize("S", [639, 641, 1300])
+def test_prompts_of_more_sequences_than_a_cta_has_threads(lib, S):
+    """Every thread of a CTA counts the work of one sequence, of two or three."""
+    rng = np.random.default_rng(S)
+    b = prompts(rng.integers(1, 40, S).tolist(), rng.integers(0, 60, S).tolist(), 2, 2, 64, 98, block_size=64)
+    st = Step(lib, b)
+    st.prefill_weights(16)
+    assert st.status_value() == 0
+    ekc, _ = oracle_caches(b)
+    kw, brought = oracle.prefill_weights(st.sums0, b.q, ekc, b.block_tables, b.cu_seqlens_q, b.cu_seqlens_k, 16, b.scale)
+    assert_weights(st.kw, kw, brought, weight_rtol(b, ekc), f"{S} sequences")
