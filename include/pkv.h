@@ -75,6 +75,7 @@ typedef enum pkv_status {
 #define PKV_DEV_TIMEOUT 0x8     /* a bounded wait ran out */
 #define PKV_DEV_WORKSPACE 0x10  /* decode: more blocks than max_total_blocks */
 #define PKV_DEV_BAD_SEQLEN 0x20 /* prefill: bad cu_seqlens (n > len_k, n > max_seqlen_q) */
+#define PKV_DEV_NO_BLOCKS 0x40  /* plan_step: too few free blocks, sequences were refused */
 
 /* Human-readable name of a pkv_status value (static string). */
 const char *pkv_status_string(int status);
@@ -446,6 +447,109 @@ pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *key_weights
                         int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                         int64_t num_blocks, int budget, int recent, int32_t *kept,
                         int32_t *new_lens, int32_t *dev_status, void *stream);
+
+/*
+ * plan_step -- block tables, slots and positions of a step, on the device.
+ *
+ * The device's counterpart of pkv_bm_append, pkv_bm_free, pkv_bm_block_table and
+ * pkv_bm_slots, for a batch at a time: a captured loop of steps needs no host between
+ * them.  What a row of the tables begins with may come from the block manager (a
+ * shared prefix); the blocks behind come from a stack of free ones, free_blocks
+ * [free_capacity] int32, of which the first *num_free are on it, the last one on top.
+ *
+ * For every sequence s that holds L = context_lens[s] tokens, new_lens[s] says:
+ *   n > 0   n tokens arrive, at positions L .. L + n - 1.  They take n rows of the
+ *           step, behind those of the sequences before s, and if they need blocks,
+ *           need = ceil((L + n) / block_size) - ceil(L / block_size), these come off
+ *           the top of the stack in order into block_tables[s]
+ *   0       it pauses: no rows, nothing changes
+ *   -1      it ends: its blocks go back onto the stack in order, but for the first
+ *           borrowed_blocks[s] (NULL: none), which are somebody else's.  Its row of
+ *           block_tables stays as it was
+ * All sequences that end come first, in order of s, then those that need blocks: what
+ * one gives back another one takes in the same step.
+ * Written, for the step's num_rows rows of which cu_seqlens_q[num_seqs] are in use:
+ *   slot_mapping[r], positions[r]   (-1 and 0 behind the last row in use)
+ *   cu_seqlens_q, cu_seqlens_k      sums of n, and of the lengths after the step
+ *   new_context_lens, *new_num_free (may be the same arrays as context_lens and
+ *                                   num_free; otherwise a call can be repeated)
+ *
+ * A sequence whose blocks the stack does not hold is refused, PKV_DEV_NO_BLOCKS, and
+ * with it all later ones that need any: those keep what they have, their rows have
+ * slots of -1, and cu_seqlens_k counts no keys for them (so prefill leaves them out).
+ * One that needs no block goes on.  Refused and flagged the same way are sequences
+ * whose rows end behind num_rows (PKV_DEV_BAD_SEQLEN), and those with a negative
+ * length or one that its table has no room for (PKV_DEV_BAD_CONTEXT; positions count
+ * from 0 where L itself is bad).  new_lens < -1 counts as 0 and borrowed_blocks
+ * outside [0, ceil(L / block_size)] as the nearer end, flagged BAD_SEQLEN and
+ * BAD_CONTEXT.  A block id out of range gives slots of -1 (PKV_DEV_BAD_BLOCK); so is
+ * flagged a *num_free outside [0, free_capacity], taken as the nearer end, and a stack
+ * with no room for what comes back, which is then dropped.  No block may be held
+ * twice, nor held and free, but in borrowed places.  Sums saturate at 2^31 - 1
+ * (flagged BAD_SEQLEN).
+ *
+ * One launch.  Supported: block_size in {64, 128, 256, 512}; num_seqs <= 16384;
+ * max_blocks_per_seq * block_size at most 2^30; num_blocks * block_size and
+ * free_capacity below 2^31, num_rows below 2^31 - 1.
+ */
+pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *context_lens,
+                         const int32_t *borrowed_blocks, int32_t *block_tables,
+                         int32_t *free_blocks, const int32_t *num_free,
+                         int32_t *new_context_lens, int32_t *new_num_free, int32_t *slot_mapping,
+                         int32_t *positions, int32_t *cu_seqlens_q, int32_t *cu_seqlens_k,
+                         int num_seqs, int64_t num_rows, int max_blocks_per_seq, int block_size,
+                         int64_t num_blocks, int64_t free_capacity, int32_t *dev_status,
+                         void *stream);
+
+/*
+ * rope_turns -- frequencies as pkv_norm_rope_store reads them (host, no GPU work).
+ *
+ * turns[i] = the fraction of a turn that inv_freq[i] radians per position are, in units
+ * of 2^-64 of a turn, rounded to nearest; inv_freq finite, at most 10^6 in magnitude
+ * (PKV_ERR_INVALID_ARG, nothing is written).  Angles are as exact as inv_freq is: a
+ * double's last bit is 2^-33 of a turn at position 2^20 where a pair turns at 1 radian
+ * per position.  Any scaling for long contexts is one of inv_freq (and of amplitude).
+ */
+pkv_status pkv_rope_turns(const double *inv_freq, int num_pairs, uint64_t *turns);
+
+/*
+ * norm_rope_store -- norm of each query and key head, rotation by position, and
+ * kv_store, in one pass over a step's projections.
+ *
+ * For each token t and each of the Hq heads x of q and Hkv heads of k:
+ *   y  = x / sqrt(mean(x^2) + eps) * weight   (q_weight, k_weight [D] bf16; both NULL:
+ *                                              y = x)
+ *   y' = y with the pairs of its first rotary_dim values turned: pair i, (y[i],
+ *        y[i + rotary_dim / 2]) or, interleaved, (y[2i], y[2i + 1]), by the angle
+ *        positions[t] * turns[i] / 2^64 turns: (a, b) -> amplitude * (a cos - b sin,
+ *        b cos + a sin)
+ * y' of q goes to q_out [T, Hq, D], that of k to slot slot_mapping[t] of k_cache and, if
+ * k_out is not NULL, to k_out [T, Hkv, D]; v goes to v_cache as it is, to the bit.
+ * k_cache, v_cache and slot_mapping all NULL: nothing is stored, v is not read and
+ * k_out is required.  All arithmetic in fp32, rounded once, to bf16.  positions may be
+ * any int32 (negative ones turn backwards).
+ *
+ * q, k, v: as in kv_store, values between tokens given by their strides (0 =
+ * contiguous), so that all three may be parts of one projection.  q_out may be q, and
+ * k_out k, where those are contiguous; other overlaps of outputs and inputs return
+ * PKV_ERR_INVALID_ARG (caches are not checked).  slot_mapping as for kv_store: -1
+ * skips (q_out and k_out are written all the same), other slots out of range are
+ * flagged (PKV_DEV_BAD_SLOT) and skipped, slots >= 0 must be unique.
+ *
+ * One launch.  Supported: head_dim in {64, 128}; rotary_dim a multiple of 16 from 0
+ * (then turns and positions may be NULL) to head_dim; at most 65536 heads of a kind.
+ * eps >= 0 and amplitude finite.
+ */
+pkv_status pkv_norm_rope_store(uint16_t *q_out, uint16_t *k_out, const uint16_t *q,
+                               const uint16_t *k, const uint16_t *v, uint16_t *k_cache,
+                               uint16_t *v_cache, const int32_t *slot_mapping,
+                               const int32_t *positions, const uint64_t *turns,
+                               const uint16_t *q_weight, const uint16_t *k_weight,
+                               int64_t num_tokens, int num_q_heads, int num_kv_heads,
+                               int head_dim, int64_t q_token_stride, int64_t k_token_stride,
+                               int64_t v_token_stride, int rotary_dim, int interleaved, float eps,
+                               float amplitude, int64_t num_blocks, int block_size,
+                               int32_t *dev_status, void *stream);
 
 /*
  * w4a16_dequant -- W4A16-G128 weight dequantisation (s1nh.org post on

@@ -19,6 +19,14 @@ has not been built, `load()` raises.
                                   context_lens, scale, workspace, max_total_blocks)
     pkv.kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget,
                  recent, kept, new_lens)
+    # a step without the host: blocks and slots, projections into the cache, attention
+    # over prefixes that sequences share
+    pkv.plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, context_lens,
+                  num_free, slot_mapping, positions, cu_q, cu_k, num_blocks, block_size)
+    pkv.norm_rope_store(q_out, q, k, v, positions, pkv.rope_turns(inv_freq), k_cache, v_cache,
+                        slot_mapping, q_weight=q_weight, k_weight=k_weight)
+    pkv.paged_decode_shared_attn(out, q_out, k_cache, v_cache, block_tables, context_lens,
+                                 group_starts, shared_blocks, scale, shared_workspace)
 """
 from __future__ import annotations
 
@@ -38,6 +46,7 @@ DEV_BAD_CONTEXT = 0x4
 DEV_TIMEOUT = 0x8
 DEV_WORKSPACE = 0x10
 DEV_BAD_SEQLEN = 0x20
+DEV_NO_BLOCKS = 0x40
 
 # Exported symbols and their ctypes signatures (must match include/pkv.h).
 _c_int, _c_i64, _c_sz, _c_f, _p = (ctypes.c_int, ctypes.c_int64, ctypes.c_size_t,
@@ -73,6 +82,11 @@ SIGNATURES = {
     "pkv_test_prompt_fault": (_c_int, [_c_i64, _c_int, _c_int]),
     "pkv_kv_evict": (_c_int, [_p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
                               _c_int, _c_int, _p, _p, _p, _p]),
+    "pkv_plan_step": (_c_int, [_p] * 12 + [_c_int, _c_i64, _c_int, _c_int, _c_i64, _c_i64, _p, _p]),
+    "pkv_rope_turns": (_c_int, [_p, _c_int, _p]),
+    "pkv_norm_rope_store": (_c_int, [_p] * 12 + [_c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64,
+                                                 _c_i64, _c_int, _c_int, _c_f, _c_f, _c_i64,
+                                                 _c_int, _p, _p]),
     "pkv_w4a16_dequant": (_c_int, [_p, _p, _p, _c_i64, _c_i64, _c_int, _p]),
     "pkv_bm_create": (_p, [_c_int, _c_int]),
     "pkv_bm_destroy": (None, [_p]),
@@ -526,6 +540,153 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
                           table_shape[1], NB, _c_int32(budget), _c_int32(recent),
                           kept.data_ptr(), new_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_kv_evict")
+
+
+def _refuse(what, dev, args, dev_status=None):
+    """Says what is wrong with a call's tensors: dtype, rank, layout or device (the
+    library launches on the current one).  args: (name, tensor or None, dtype, rank)."""
+    import torch
+
+    for name, t, dtype, ndim in args:
+        if t is None:
+            continue
+        _need(t, dtype, name, ndim)
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is not on the current CUDA device")
+    if not _plain_status(dev, dev_status):
+        raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
+
+
+def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_context_lens,
+              new_num_free, slot_mapping, positions, cu_seqlens_q, cu_seqlens_k, num_blocks,
+              block_size, borrowed_blocks=None, dev_status=None, stream=None) -> None:
+    """Blocks, slots and positions of a step from its sequences' lengths, on the
+    device (see include/pkv.h).  All int32: new_lens, context_lens, new_context_lens,
+    borrowed_blocks [S]; block_tables [S, max_blocks]; free_blocks [any], num_free and
+    new_num_free [1]; slot_mapping, positions [rows]; cu_seqlens_q, cu_seqlens_k [S + 1].
+    new_context_lens may be context_lens, and new_num_free num_free."""
+    import torch
+
+    lib = load()
+    i32 = torch.int32
+    dev = torch.cuda.current_device() if block_tables.is_cuda else -1
+    table_shape = block_tables.shape
+    if not (_plain_status(dev, dev_status) and
+            _plain(dev, i32, new_lens, context_lens, block_tables, free_blocks, num_free,
+                   new_context_lens, new_num_free, slot_mapping, positions, cu_seqlens_q,
+                   cu_seqlens_k) and
+            (borrowed_blocks is None or _plain(dev, i32, borrowed_blocks)) and
+            len(table_shape) == 2):
+        _refuse("plan_step", dev, (
+            ("new_lens", new_lens, i32, 1), ("context_lens", context_lens, i32, 1),
+            ("block_tables", block_tables, i32, 2), ("free_blocks", free_blocks, i32, 1),
+            ("num_free", num_free, i32, 1), ("new_context_lens", new_context_lens, i32, 1),
+            ("new_num_free", new_num_free, i32, 1), ("slot_mapping", slot_mapping, i32, 1),
+            ("positions", positions, i32, 1), ("cu_seqlens_q", cu_seqlens_q, i32, 1),
+            ("cu_seqlens_k", cu_seqlens_k, i32, 1),
+            ("borrowed_blocks", borrowed_blocks, i32, 1)), dev_status)
+    S, wide = table_shape
+    if not (new_lens.shape == context_lens.shape == new_context_lens.shape == (S,) and
+            cu_seqlens_q.shape == cu_seqlens_k.shape == (S + 1,) and
+            num_free.shape == new_num_free.shape == (1,) and free_blocks.dim() == 1 and
+            slot_mapping.dim() == 1 and slot_mapping.shape == positions.shape and
+            (borrowed_blocks is None or borrowed_blocks.shape == (S,))):
+        raise ValueError("plan_step: inconsistent shapes")
+    st = lib.pkv_plan_step(
+        new_lens.data_ptr(), context_lens.data_ptr(), _addr(borrowed_blocks),
+        block_tables.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+        new_context_lens.data_ptr(), new_num_free.data_ptr(), slot_mapping.data_ptr(),
+        positions.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S,
+        slot_mapping.numel(), wide, _c_int32(block_size), _c_int64(num_blocks),
+        free_blocks.numel(), _addr(dev_status), _raw_stream(stream, dev))
+    _check(st, "pkv_plan_step")
+
+
+def rope_turns(inv_freq, device="cuda"):
+    """What norm_rope_store takes for the frequencies inv_freq (radians per
+    position of each pair, in 64 bits, already scaled for long contexts where they
+    are to be): int64 [rotary_dim / 2] on `device`."""
+    import numpy as np
+    import torch
+
+    f = np.ascontiguousarray(torch.as_tensor(inv_freq, dtype=torch.float64).cpu().numpy())
+    if f.ndim != 1:
+        raise ValueError("rope_turns: inv_freq must have one dim")
+    turns = np.empty(f.shape, dtype=np.int64)
+    _check(load().pkv_rope_turns(f.ctypes.data, f.size, turns.ctypes.data), "pkv_rope_turns")
+    return torch.from_numpy(turns).to(device)
+
+
+def _rows_of(t, name, shape, dev):
+    """Values between the tokens of t [T, heads, D], whose rows must be contiguous."""
+    import torch
+
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: is not on the current CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
+    # (strides of dims of size one, and of tokens of which there is one, say nothing)
+    step, head, value = t.stride()
+    T, H, D = shape
+    if (value != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError(f"{name}: rows must be contiguous [heads, D]")
+    return step if T > 1 else H * D
+
+
+def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None,
+                    slot_mapping=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, amplitude=1.0, dev_status=None, stream=None) -> None:
+    """The norm of each head of q [T, Hq, D] and k [T, Hkv, D] (with q_weight and
+    k_weight [D]), their rotation by positions [T] (int32) and turns [R / 2] (of
+    rope_turns: the first R dims turn), and the store of k and v at slot_mapping [T] of
+    the caches, in one pass.  q, k and v may be strided by token (parts of one
+    projection).  Without caches k goes to k_out [T, Hkv, D] alone.  bf16."""
+    import torch
+
+    lib = load()
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = torch.cuda.current_device() if q.is_cuda else -1
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("norm_rope_store: q and k must be [T, heads, D]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    q_step = _rows_of(q, "q", q.shape, dev)
+    k_step = _rows_of(k, "k", (T, Hkv, D), dev)
+    store = k_cache is not None
+    if not (store == (v_cache is not None) == (slot_mapping is not None)):
+        raise ValueError("norm_rope_store: k_cache, v_cache and slot_mapping go together")
+    v_step = _rows_of(v, "v", (T, Hkv, D), dev) if store else 0
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("norm_rope_store: q_weight and k_weight go together")
+    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, q_out) and
+            _plain(dev, i32, positions) and _plain(dev, torch.int64, turns) and
+            (k_out is None or _plain(dev, bf16, k_out)) and
+            (q_weight is None or _plain(dev, bf16, q_weight, k_weight)) and
+            (not store or _plain(dev, bf16, k_cache, v_cache) and _plain(dev, i32, slot_mapping))):
+        _refuse("norm_rope_store", dev, (
+            ("q_out", q_out, bf16, 3), ("positions", positions, i32, 1),
+            ("turns", turns, torch.int64, 1), ("k_out", k_out, bf16, 3),
+            ("q_weight", q_weight, bf16, 1), ("k_weight", k_weight, bf16, 1),
+            ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
+            ("slot_mapping", slot_mapping, i32, 1)), dev_status)
+    NB, BS = (k_cache.shape[0], k_cache.shape[1]) if store else (0, 0)
+    if q_out.shape != q.shape or positions.shape != (T,) or turns.dim() != 1 or \
+            (k_out is not None and k_out.shape != k.shape) or \
+            (q_weight is not None and not q_weight.shape == k_weight.shape == (D,)) or \
+            (store and not (k_cache.shape == v_cache.shape == (NB, BS, Hkv, D) and
+                            slot_mapping.shape == (T,))):
+        raise ValueError("norm_rope_store: inconsistent shapes")
+    st = lib.pkv_norm_rope_store(
+        q_out.data_ptr(), _addr(k_out), q.data_ptr(), k.data_ptr(), v.data_ptr() if store else None,
+        _addr(k_cache), _addr(v_cache), _addr(slot_mapping), positions.data_ptr(),
+        turns.data_ptr(), _addr(q_weight), _addr(k_weight), T, Hq, Hkv, D, q_step, k_step, v_step,
+        2 * turns.numel(), 1 if interleaved else 0, float(eps), float(amplitude), NB, BS,
+        _addr(dev_status), _raw_stream(stream, dev))
+    _check(st, "pkv_norm_rope_store")
 
 
 def w4a16_dequant(out, packed, scales, group_size=128, stream=None) -> None:

@@ -1,0 +1,371 @@
+// plan_step.cu -- a step's blocks, slots and positions from the sequences' lengths.
+//
+// What the host block manager does for one sequence at a time (a new block when the
+// length reaches a multiple of the block size plus one: CSDN essay "from nanoVLLM to
+// vLLM", Mountain 1), done for a batch on the device, so that a captured step can go
+// on without the host.  With L[s] tokens held, n[s] new ones, BS tokens to a block:
+//   have = ceil(L / BS), need = ceil((L + n) / BS) - have  (n > 0),
+//   give = have - borrowed  (n = -1: the sequence ends)
+// and the exclusive prefix sums of need, give and n over the sequences say where in
+// the stack of free blocks a sequence's blocks go to or come from, and which rows of
+// the step are its own.
+//
+// One launch of one CTA, or of one cluster of eight.  Every CTA scans the lengths by
+// itself (12 bytes a sequence); the sequences that end push their blocks; after a
+// cluster barrier all CTAs share the tables and the rows.  So lengths and counters
+// can be updated in place: nothing is written before everybody has read.
+#include <cooperative_groups.h>
+
+#include "host_common.h"
+#include "pkv_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxSeqs = 16384;
+constexpr int kPlanCluster = 8;     // portable cluster size
+// Up to so many rows and sequences one CTA of kPlanSmallSeqs threads does the step.
+constexpr int kPlanSmallRows = 2048;
+constexpr int kPlanSmallSeqs = 256;
+
+struct PlanParams {
+  const int32_t *new_lens;
+  const int32_t *context_lens;
+  const int32_t *borrowed;   // may be null
+  int32_t *block_tables;
+  int32_t *free_blocks;
+  const int32_t *num_free;
+  int32_t *new_context_lens;
+  int32_t *new_num_free;
+  int32_t *slots;
+  int32_t *positions;
+  int32_t *cu_q;
+  int32_t *cu_k;
+  int32_t *status;
+  int64_t num_rows;
+  int64_t num_blocks;
+  int capacity;      // of free_blocks
+  int num_seqs;
+  int max_blocks_per_seq;
+  int block_shift;
+};
+
+__device__ __forceinline__ int saturated(int64_t x) {
+  return x > 0x7FFFFFFF ? 0x7FFFFFFF : (int)x;
+}
+
+// Exclusive prefix sums of N values per thread over the CTA, and their totals.
+template <int N>
+__device__ __forceinline__ void scan_cta(int64_t (&x)[N], int64_t (&total)[N],
+                                         int64_t (*warp_sums)[N]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int64_t incl[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    incl[i] = x[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += y;
+    }
+    if (lane == 31) warp_sums[warp][i] = incl[i];
+  }
+  __syncthreads();
+  // Every warp adds up the warps' sums by itself.
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int64_t y = lane < warps ? warp_sums[lane][i] : 0;
+    int64_t mine = lane < warp ? y : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    }
+    total[i] = y;
+    x[i] = mine + incl[i] - x[i];
+  }
+  __syncthreads();
+}
+
+// A sequence's lengths, checked.
+struct PlanSeq {
+  int L;       // tokens held (0 if the length given does not fit the table)
+  int n;       // rows of the step (0: none)
+  int have, need, give, borrowed;
+  bool ends, out;  // out: its lengths do not fit, it takes no part but for its rows
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s, bool tell) {
+  PlanSeq q;
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  const int L = p.context_lens[s], n = p.new_lens[s];
+  int borrowed = p.borrowed != nullptr ? p.borrowed[s] : 0;
+  int bad = 0;
+  q.out = L < 0 || L > room;
+  q.L = q.out ? 0 : L;
+  q.n = n > 0 ? n : 0;
+  q.ends = n == -1 && !q.out;
+  if (n < -1) bad |= PKV_DEV_BAD_SEQLEN;
+  if (q.L + (int64_t)q.n > room) q.out = true;
+  if (q.out) bad |= PKV_DEV_BAD_CONTEXT;
+  const int bs1 = (1 << p.block_shift) - 1;
+  q.have = (int)(((int64_t)q.L + bs1) >> p.block_shift);
+  if (borrowed < 0 || borrowed > q.have) {
+    bad |= PKV_DEV_BAD_CONTEXT;
+    borrowed = borrowed < 0 ? 0 : q.have;
+  }
+  q.borrowed = borrowed;
+  q.give = q.ends ? q.have - borrowed : 0;
+  q.need = q.out || q.n == 0 ? 0 : (int)(((int64_t)q.L + q.n + bs1) >> p.block_shift) - q.have;
+  if (tell && bad) flag_status(p.status, bad);
+  return q;
+}
+
+// The sequence of row t: the last s with first[s] <= t (t < first[S]).
+__device__ __forceinline__ int seq_of_row(const int *first, int S, int t) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
+  namespace cg = cooperative_groups;
+  extern __shared__ int plan_smem[];
+  __shared__ int64_t sums3[32][3];
+  __shared__ int64_t sums1[32][1];
+  const int S = p.num_seqs, shift = p.block_shift;
+  int *first_row = plan_smem;           // [S + 1]
+  int *held = first_row + S + 1;        // [S]: L, or -1 - L when the sequence gets no slots
+  int *base = held + S;                 // [S]: blocks needed before it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the grid is one cluster)
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int free_given = *p.num_free;
+  const int free0 = min(max(free_given, 0), p.capacity);
+  if (free0 != free_given && rank == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+
+  const int per = (S + blockDim.x - 1) / (int)blockDim.x;
+  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  int64_t at[3] = {0, 0, 0}, total[3];  // give, need, rows
+  for (int s = s0; s < s1; ++s) {
+    const PlanSeq q = plan_seq(p, s, rank == 0);
+    at[0] += q.give;
+    at[1] += q.need;
+    at[2] += q.n;
+  }
+  scan_cta<3>(at, total, sums3);
+  const int left = (int)min((int64_t)free0 + total[0], (int64_t)p.capacity);
+  if (free0 + total[0] > p.capacity && rank == 0 && tid == 0)
+    flag_status(p.status, PKV_DEV_BAD_BLOCK);
+  int64_t keys[1] = {0}, all_keys[1], taken = 0;
+  {
+    int64_t need = at[1], row = at[2];
+    for (int s = s0; s < s1; ++s) {
+      const PlanSeq q = plan_seq(p, s, false);
+      const bool no_blocks = q.need > 0 && need + q.need > left;
+      const bool no_rows = q.n > 0 && row + q.n > p.num_rows;
+      if (rank == 0 && (no_blocks || no_rows))
+        flag_status(p.status, (no_blocks ? PKV_DEV_NO_BLOCKS : 0) | (no_rows ? PKV_DEV_BAD_SEQLEN : 0));
+      const bool refused = no_blocks || no_rows || q.out;
+      first_row[s] = saturated(row);
+      held[s] = refused ? -1 - q.L : q.L;
+      base[s] = saturated(need);
+      if (!refused && q.need > 0) taken = need + q.need;
+      if (!refused && !q.ends) keys[0] += q.L + q.n;
+      need += q.need;
+      row += q.n;
+    }
+  }
+  // Blocks taken: those up to the last sequence that takes any.
+  int64_t most = taken;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const int64_t y = __shfl_xor_sync(0xffffffffu, most, o);
+    most = y > most ? y : most;
+  }
+  if (lane == 0) sums3[warp][0] = most;
+  if (tid == 0) first_row[S] = saturated(total[2]);
+  scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
+  // Sequences that end give their blocks back, the first one's first: at[0] of the
+  // thread's sequences are before its own.
+  {
+    int64_t give = at[0];
+    for (int s = s0; s < s1; ++s) {
+      const PlanSeq q = plan_seq(p, s, false);
+      if (!q.ends) continue;
+      // (base of a sequence that ends: where its blocks go)
+      base[s] = saturated(give);
+      give += q.give;
+    }
+  }
+  __syncthreads();
+  const int W = ctas * warps, w = rank * warps + warp;
+  for (int s = w; s < S; s += W) {
+    if (p.new_lens[s] != -1) continue;
+    const PlanSeq q = plan_seq(p, s, false);
+    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq + q.borrowed;
+    for (int i = lane; i < q.give; i += 32) {
+      const int64_t to = (int64_t)free0 + base[s] + i;
+      if (to < p.capacity) p.free_blocks[to] = row[i];
+    }
+  }
+  // What comes back is on the stack, and nobody reads lengths or counters any more.
+  if (ctas > 1) cg::this_cluster().sync();
+  else __syncthreads();
+
+  // Block number b of the blocks needed, from the top of the stack.
+  auto block_at = [&](int64_t b) -> int {
+    const int64_t i = (int64_t)left - 1 - b;
+    return i >= 0 ? __ldcg(p.free_blocks + i) : -1;
+  };
+  // Tables, lengths and sums: a warp per sequence; the first CTA writes the rest.
+  for (int s = w; s < S; s += W) {
+    const int L = held[s], n = first_row[s + 1] - first_row[s];
+    if (L < 0 || n == 0) continue;
+    const int bs1 = (1 << shift) - 1;
+    const int have = (L + bs1) >> shift;
+    const int need = (int)(((int64_t)L + n + bs1) >> shift) - have;
+    int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq + have;
+    for (int i = lane; i < need; i += 32) row[i] = block_at((int64_t)base[s] + i);
+  }
+  if (rank == ctas - 1) {
+    int64_t key = keys[0];
+    for (int s = s0; s < s1; ++s) {
+      const int h = held[s], n = first_row[s + 1] - first_row[s];
+      const bool ends = p.new_lens[s] == -1 && h >= 0;
+      const int after = ends ? 0 : h < 0 ? -1 : h + n;
+      p.cu_q[s] = first_row[s];
+      p.cu_k[s] = saturated(key);
+      if (after > 0) key += after;
+      if (after >= 0) p.new_context_lens[s] = after;
+      else p.new_context_lens[s] = p.context_lens[s];  // as it was
+    }
+    if (tid == 0) {
+      int64_t got = 0;
+      for (int i = 0; i < warps; ++i) got = sums3[i][0] > got ? sums3[i][0] : got;
+      *p.new_num_free = left - (int)got;
+      p.cu_q[S] = first_row[S];
+      p.cu_k[S] = saturated(all_keys[0]);
+      if (all_keys[0] > 0x7FFFFFFF || total[2] > 0x7FFFFFFF)
+        flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+    }
+  }
+  // Rows: four neighbours a thread.
+  const int rows = first_row[S];
+  const int64_t step = (int64_t)ctas * blockDim.x * 4;
+  for (int64_t t0 = ((int64_t)rank * blockDim.x + tid) * 4; t0 < p.num_rows; t0 += step) {
+    int slot[4], pos[4];
+    int s = -1, blk = -1, lb = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + i;
+      slot[i] = -1;
+      pos[i] = 0;
+      if (t >= rows || t >= p.num_rows) continue;
+      if (s < 0) s = seq_of_row(first_row, S, (int)t);
+      else while (first_row[s + 1] <= t) ++s, lb = -1;
+      const int h = held[s];
+      const int L = h < 0 ? -1 - h : h;
+      pos[i] = (int)((uint32_t)L + (uint32_t)(t - first_row[s]));
+      if (h < 0) continue;
+      const int b = pos[i] >> shift;
+      if (b != lb) {
+        lb = b;
+        const int have = (L + (1 << shift) - 1) >> shift;
+        blk = b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
+                       : block_at((int64_t)base[s] + b - have);
+        if (blk < 0 || blk >= p.num_blocks) {
+          flag_status(p.status, PKV_DEV_BAD_BLOCK);
+          blk = -1;
+        }
+      }
+      if (blk >= 0) slot[i] = (blk << shift) + (pos[i] & ((1 << shift) - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t0 + i < p.num_rows) {
+        p.slots[t0 + i] = slot[i];
+        p.positions[t0 + i] = pos[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *context_lens,
+                                    const int32_t *borrowed_blocks, int32_t *block_tables,
+                                    int32_t *free_blocks, const int32_t *num_free,
+                                    int32_t *new_context_lens, int32_t *new_num_free,
+                                    int32_t *slot_mapping, int32_t *positions,
+                                    int32_t *cu_seqlens_q, int32_t *cu_seqlens_k, int num_seqs,
+                                    int64_t num_rows, int max_blocks_per_seq, int block_size,
+                                    int64_t num_blocks, int64_t free_capacity,
+                                    int32_t *dev_status, void *stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || num_rows < 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
+      num_blocks <= 0 || free_capacity < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (block_size != 64 && block_size != 128 && block_size != 256 && block_size != 512)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > kPlanMaxSeqs || num_rows > 0x7FFFFFFELL || free_capacity > 0x7FFFFFFFLL ||
+      num_blocks > 0x7FFFFFFFLL / block_size ||
+      (int64_t)max_blocks_per_seq * block_size > (1 << 30))
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 && num_rows > 0) return PKV_ERR_INVALID_ARG;
+  if (!num_free || !new_num_free || !cu_seqlens_q || !cu_seqlens_k) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!new_lens || !context_lens || !block_tables || !new_context_lens))
+    return PKV_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!slot_mapping || !positions)) return PKV_ERR_INVALID_ARG;
+  if (free_capacity > 0 && !free_blocks) return PKV_ERR_INVALID_ARG;
+
+  PlanParams prm;
+  prm.new_lens = new_lens;
+  prm.context_lens = context_lens;
+  prm.borrowed = borrowed_blocks;
+  prm.block_tables = block_tables;
+  prm.free_blocks = free_blocks;
+  prm.num_free = num_free;
+  prm.new_context_lens = new_context_lens;
+  prm.new_num_free = new_num_free;
+  prm.slots = slot_mapping;
+  prm.positions = positions;
+  prm.cu_q = cu_seqlens_q;
+  prm.cu_k = cu_seqlens_k;
+  prm.status = dev_status;
+  prm.num_rows = num_rows;
+  prm.num_blocks = num_blocks;
+  prm.capacity = (int)free_capacity;
+  prm.num_seqs = num_seqs;
+  prm.max_blocks_per_seq = max_blocks_per_seq;
+  prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
+
+  const bool small = num_rows <= kPlanSmallRows && num_seqs <= kPlanSmallSeqs;
+  const int threads = small ? kPlanSmallSeqs : kPlanThreads;
+  const int smem = (3 * num_seqs + 1) * 4;
+  if (!kernel_smem_setup((const void *)plan_step_kernel, threads, smem, nullptr))
+    return PKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(small ? 1 : kPlanCluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cfg.gridDim.x;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+  return launch_status();
+}
