@@ -552,6 +552,55 @@ pkv_status pkv_norm_rope_store(uint16_t *q_out, uint16_t *k_out, const uint16_t 
                                int32_t *dev_status, void *stream);
 
 /*
+ * Bytes of device workspace paged_decode_shared_attn needs: the plan of the batch and
+ * the parts of its rows.  Returns 0 for invalid sizes.
+ */
+size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                        int num_kv_heads, int head_dim);
+
+/*
+ * paged_decode_shared_attn -- paged_decode_attn for a batch in which groups of
+ * sequences begin with the same blocks (a system prompt, samples of one answer), whose
+ * keys and values are then read once for a group.
+ *
+ * out, q, caches, block_tables and context_lens as for paged_decode_attn, and the same
+ * result up to rounding.  Group g is the neighbouring sequences group_starts[g] ..
+ * group_starts[g + 1] - 1 (group_starts int32 [num_groups + 1], from 0 to num_seqs);
+ * the first shared_blocks[g] (int32 [num_groups]) entries of their rows of block_tables
+ * are the same, and only those of its first sequence with a context are read there.  A
+ * group uses no more of them than its shortest context fills; a group of one, or one
+ * with shared_blocks of 0, is attended like any other sequence.  pkv_bm_prefix_groups
+ * finds groups.
+ * fp32 logits and statistics; for the product with V alone the weights are taken as the
+ * sum of two bf16 (off by 2^-18 of a weight).  How the work is split depends on the
+ * batch, and with it the last bits; the same call gives the same bits.
+ *
+ * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its row of out
+ * is left as it was; one that is longer than its table is flagged and clamped.
+ * shared_blocks outside [0, max_blocks_per_seq] is flagged the same way and taken as the
+ * nearer end.  group_starts that do not begin at 0, end at num_seqs or ever go back are
+ * flagged (PKV_DEV_BAD_SEQLEN); every sequence is then attended by itself.  A block id
+ * out of range is flagged and what its sequences get is undefined.
+ *
+ * workspace: device memory of at least pkv_decode_shared_workspace_size(...) bytes,
+ * 256-byte aligned; it needs no initialisation.  Calls that overlap on the device must
+ * not share a workspace.
+ *
+ * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
+ *
+ * Four launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
+ * block_size in {64, 128, 256, 512}; num_seqs <= 8192, 1 <= num_groups <= num_seqs
+ * (else PKV_ERR_INVALID_ARG); at most 4096 kv heads; max_blocks_per_seq * block_size at
+ * most 2^20.
+ */
+pkv_status pkv_paged_decode_shared_attn(
+    uint16_t *out, const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+    const int32_t *block_tables, const int32_t *context_lens, const int32_t *group_starts,
+    const int32_t *shared_blocks, int num_seqs, int num_groups, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * w4a16_dequant -- W4A16-G128 weight dequantisation (s1nh.org post on
  * upgrading nano-vllm to big-vLLM, section on quantisation: every int32 of
  * weight_packed holds eight 4-bit values; int32 -> u4 unpack -> s4
@@ -630,6 +679,19 @@ int pkv_bm_block_table(const pkv_block_manager *m, int64_t seq_id, int32_t *out,
 /* slots[i] = block_table[p / bs] * bs + p % bs for p = first .. first+count-1. */
 pkv_status pkv_bm_slots(const pkv_block_manager *m, int64_t seq_id, int first, int count,
                         int32_t *slots);
+/* An order of sequences, and groups of neighbours in it, for
+ * pkv_paged_decode_shared_attn: group g is the seq_ids[order[i]] for i = group_starts[g]
+ * .. group_starts[g + 1] - 1, which begin with the same shared_blocks[g] blocks.  Groups
+ * are chosen so that the blocks that need not be read again, sum of (members - 1) *
+ * shared_blocks, are many: where some sequences share more among themselves than with
+ * the rest, they become a group of their own if that saves more.  Sequences that share
+ * nothing are groups of one with shared_blocks 0.  order and shared_blocks have room
+ * for num_seqs values, group_starts for num_seqs + 1; *num_groups are written.  An
+ * unknown sequence, or one that is listed twice: PKV_ERR_INVALID_ARG; no host memory:
+ * PKV_ERR_WORKSPACE. */
+pkv_status pkv_bm_prefix_groups(const pkv_block_manager *m, const int64_t *seq_ids, int num_seqs,
+                                int32_t *order, int32_t *group_starts, int32_t *shared_blocks,
+                                int *num_groups);
 /* Reference count of a block (0 = free), -1 on a bad index. */
 int pkv_bm_ref_count(const pkv_block_manager *m, int block);
 

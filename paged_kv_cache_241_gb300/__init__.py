@@ -87,6 +87,9 @@ SIGNATURES = {
     "pkv_norm_rope_store": (_c_int, [_p] * 12 + [_c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64,
                                                  _c_i64, _c_int, _c_int, _c_f, _c_f, _c_i64,
                                                  _c_int, _p, _p]),
+    "pkv_decode_shared_workspace_size": (_c_sz, [_c_int] * 5),
+    "pkv_paged_decode_shared_attn": (_c_int, [_p] * 8 + [_c_int] * 7 + [_c_i64, _c_f, _p, _c_sz,
+                                                                        _p, _p]),
     "pkv_w4a16_dequant": (_c_int, [_p, _p, _p, _c_i64, _c_i64, _c_int, _p]),
     "pkv_bm_create": (_p, [_c_int, _c_int]),
     "pkv_bm_destroy": (None, [_p]),
@@ -98,6 +101,7 @@ SIGNATURES = {
     "pkv_bm_num_tokens": (_c_int, [_p, _c_i64]),
     "pkv_bm_block_table": (_c_int, [_p, _c_i64, _p, _c_int]),
     "pkv_bm_slots": (_c_int, [_p, _c_i64, _c_int, _c_int, _p]),
+    "pkv_bm_prefix_groups": (_c_int, [_p, _p, _c_int, _p, _p, _p, ctypes.POINTER(_c_int)]),
     "pkv_bm_ref_count": (_c_int, [_p, _c_int]),
 }
 
@@ -689,6 +693,52 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
     _check(st, "pkv_norm_rope_store")
 
 
+def decode_shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                            device="cuda"):
+    """Allocate a workspace for paged_decode_shared_attn."""
+    n = int(load().pkv_decode_shared_workspace_size(*map(_c_int32, (
+        num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim))))
+    return _workspace(n, "decode_shared_workspace", device)
+
+
+def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
+                             shared_blocks, scale, workspace, dev_status=None,
+                             stream=None) -> None:
+    """paged_decode_attn for a batch of groups of neighbouring sequences: group g is
+    group_starts[g] .. group_starts[g + 1] - 1 (int32 [groups + 1]), and the first
+    shared_blocks[g] (int32 [groups]) blocks of its sequences are the same ones, read
+    once (see include/pkv.h; BlockManager.prefix_groups finds groups)."""
+    import torch
+
+    lib = load()
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _device_of(k_cache)
+    q_shape, cache_shape, table_shape = q.shape, k_cache.shape, block_tables.shape
+    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, out, q, k_cache, v_cache) and
+            _plain(dev, i32, block_tables, context_lens, group_starts, shared_blocks) and
+            _plain(dev, torch.uint8, workspace) and
+            len(q_shape) == 3 and len(cache_shape) == 4 and len(table_shape) == 2):
+        _refuse("paged_decode_shared_attn", dev, (
+            ("out", out, bf16, 3), ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4),
+            ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
+            ("context_lens", context_lens, i32, 1), ("group_starts", group_starts, i32, 1),
+            ("shared_blocks", shared_blocks, i32, 1), ("workspace", workspace, torch.uint8, 1)),
+            dev_status)
+    S, Hq, D = q_shape
+    NB, BS, Hkv, Dc = cache_shape
+    groups = shared_blocks.numel()
+    if Dc != D or out.shape != q_shape or table_shape[0] != S or context_lens.shape != (S,) or \
+            v_cache.shape != cache_shape or shared_blocks.dim() != 1 or \
+            group_starts.shape != (groups + 1,):
+        raise ValueError("paged_decode_shared_attn: inconsistent shapes")
+    st = lib.pkv_paged_decode_shared_attn(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), group_starts.data_ptr(),
+        shared_blocks.data_ptr(), S, groups, Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
+        workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
+    _check(st, "pkv_paged_decode_shared_attn")
+
+
 def w4a16_dequant(out, packed, scales, group_size=128, stream=None) -> None:
     """out [N, K] bf16 <- packed [N, K/8] int32 (eight 4-bit values per word,
     lowest nibble first, value = nibble - 8) times scales [N, K/128] bf16."""
@@ -776,6 +826,23 @@ class BlockManager:
         _check(self._lib.pkv_bm_slots(self._h, int(seq_id), int(first), int(count),
                                       out.ctypes.data), "pkv_bm_slots")
         return out
+
+    def prefix_groups(self, seq_ids):
+        """(order, group_starts, shared_blocks), int32 arrays, for paged_decode_shared_attn
+        on a batch of seq_ids[order[0]], seq_ids[order[1]], ...: neighbours in that order
+        that begin with the same blocks are a group."""
+        import numpy as np
+
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        if ids.ndim != 1:
+            raise ValueError("prefix_groups: seq_ids must have one dim")
+        n = int(ids.size)
+        order, starts, shared = (np.empty(n + x, dtype=np.int32) for x in (0, 1, 0))
+        groups = ctypes.c_int(0)
+        _check(self._lib.pkv_bm_prefix_groups(self._h, ids.ctypes.data, n, order.ctypes.data,
+                                              starts.ctypes.data, shared.ctypes.data,
+                                              ctypes.byref(groups)), "pkv_bm_prefix_groups")
+        return order, starts[:groups.value + 1], shared[:groups.value]
 
     def ref_count(self, block: int) -> int:
         return int(self._lib.pkv_bm_ref_count(self._h, int(block)))

@@ -15,8 +15,10 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <new>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pkv.h"
@@ -267,6 +269,138 @@ extern "C" pkv_status pkv_bm_slots(const pkv_block_manager *m, int64_t seq_id, i
   for (int i = 0; i < count; ++i) {
     const int p = first + i;
     slots[i] = s.table[p / bs] * bs + p % bs;
+  }
+  return PKV_OK;
+}
+
+namespace {
+
+// Groups of sequences by their common first blocks.  With the tables sorted, sequences
+// that share a prefix are neighbours, and the ranges of them are a tree: a range whose
+// members share `depth` blocks falls into ranges by the block behind.  A sequence is in
+// the group of the innermost range around it that is one; a group of k sequences saves
+// (k - 1) * depth readings of a block.  The most that can be saved inside a range depends
+// on which of the ranges around it is the next group (sequences left over count its depth
+// each), so it is worked out for each of them, innermost ranges first.
+struct PrefixGroups {
+  struct Range {
+    int first, last;   // of the sorted sequences, [first, last)
+    int depth;         // blocks that they share
+    int parent;
+    bool apart = false;
+  };
+  const std::vector<const std::vector<int32_t> *> &tables;  // by the sorted place
+  std::vector<Range> ranges;                                // parents before children
+
+  explicit PrefixGroups(const std::vector<const std::vector<int32_t> *> &t) : tables(t) {
+    const int n = (int)tables.size();
+    ranges.push_back({0, n, 0, -1});
+    for (size_t r = 0; r < ranges.size(); ++r) {
+      const int first = ranges[r].first, last = ranges[r].last, depth = ranges[r].depth;
+      for (int i = first; i < last;) {  // children: runs with the same block at `depth`
+        int e = i + 1;
+        const auto &a = *tables[i];
+        if ((int)a.size() > depth)
+          while (e < last && (int)tables[e]->size() > depth && (*tables[e])[depth] == a[depth]) ++e;
+        if (e - i >= 2) {
+          const auto &b = *tables[e - 1];  // (sorted: the ends share the least)
+          int d = depth;
+          while (d < (int)a.size() && d < (int)b.size() && a[d] == b[d]) ++d;
+          ranges.push_back({i, e, d, (int)r});
+        }
+        i = e;
+      }
+    }
+    const size_t n_ranges = ranges.size();
+    std::vector<int> level(n_ranges, 0), direct(n_ranges);
+    for (size_t r = 0; r < n_ranges; ++r) {
+      direct[r] = ranges[r].last - ranges[r].first;
+      if (r > 0) {
+        level[r] = level[ranges[r].parent] + 1;
+        direct[ranges[r].parent] -= direct[r];
+      }
+    }
+    // inside[r][i]: saved by r's ranges when the group around them is the range around r
+    // at level i (i = level[r]: r itself); better[r][i]: r is a group when that one is.
+    std::vector<std::vector<int64_t>> inside(n_ranges);
+    std::vector<std::vector<bool>> better(n_ranges);
+    for (size_t r = 0; r < n_ranges; ++r) inside[r].assign(level[r] + 1, 0);
+    for (size_t r = n_ranges; r-- > 1;) {
+      const Range &x = ranges[r];
+      const int64_t own = inside[r][level[r]] + (int64_t)(direct[r] - 1) * x.depth;
+      better[r].assign(level[r], false);
+      int up = x.parent;
+      for (int i = level[r] - 1; i >= 0; --i, up = ranges[up].parent) {
+        const int64_t joins = inside[r][i] + (int64_t)direct[r] * ranges[up].depth;
+        better[r][i] = own > joins;
+        inside[x.parent][i] += better[r][i] ? own : joins;
+      }
+      std::vector<int64_t>().swap(inside[r]);
+    }
+    std::vector<int> around(n_ranges, 0);  // level of the group that a range's sequences are in
+    for (size_t r = 1; r < n_ranges; ++r) {
+      const int i = around[ranges[r].parent];
+      ranges[r].apart = better[r][i];
+      around[r] = ranges[r].apart ? level[r] : i;
+    }
+  }
+  // Blocks that the sequences at two places share.
+  int common(int i, int j) const {
+    const auto &a = *tables[i], &b = *tables[j];
+    int d = 0;
+    while (d < (int)a.size() && d < (int)b.size() && a[d] == b[d]) ++d;
+    return d;
+  }
+};
+
+}  // namespace
+
+extern "C" pkv_status pkv_bm_prefix_groups(const pkv_block_manager *m, const int64_t *seq_ids,
+                                           int num_seqs, int32_t *order, int32_t *group_starts,
+                                           int32_t *shared_blocks, int *num_groups) {
+  if (m == nullptr || num_seqs < 0 || group_starts == nullptr || num_groups == nullptr ||
+      (num_seqs > 0 && (seq_ids == nullptr || order == nullptr || shared_blocks == nullptr)))
+    return PKV_ERR_INVALID_ARG;
+  try {
+    std::vector<const std::vector<int32_t> *> given(num_seqs);
+    std::unordered_map<int64_t, int> seen;
+    for (int i = 0; i < num_seqs; ++i) {
+      auto it = m->seqs.find(seq_ids[i]);
+      if (it == m->seqs.end() || !seen.emplace(seq_ids[i], i).second) return PKV_ERR_INVALID_ARG;
+      given[i] = &it->second.table;
+    }
+    std::vector<int> sorted(num_seqs);
+    for (int i = 0; i < num_seqs; ++i) sorted[i] = i;
+    std::stable_sort(sorted.begin(), sorted.end(), [&](int a, int b) { return *given[a] < *given[b]; });
+    std::vector<const std::vector<int32_t> *> tables(num_seqs);
+    for (int i = 0; i < num_seqs; ++i) tables[i] = given[sorted[i]];
+    const PrefixGroups g(tables);
+    // The range whose group a sequence is in: the innermost that is taken out (or the
+    // root, which shares nothing: a group of one for each).
+    std::vector<int> of(num_seqs, 0);
+    for (size_t r = 1; r < g.ranges.size(); ++r)  // (parents come first, so inner ones win)
+      if (g.ranges[r].apart)
+        for (int i = g.ranges[r].first; i < g.ranges[r].last; ++i) of[i] = (int)r;
+    std::vector<std::vector<int>> members(g.ranges.size());
+    for (int i = 0; i < num_seqs; ++i) members[of[i]].push_back(i);
+    int at = 0, n = 0;
+    for (size_t r = 1; r < g.ranges.size(); ++r) {
+      if (members[r].empty()) continue;
+      group_starts[n] = at;
+      // (of what is left of a range: the places are in order, so its ends share the least)
+      shared_blocks[n++] =
+          members[r].size() >= 2 ? g.common(members[r].front(), members[r].back()) : 0;
+      for (int i : members[r]) order[at++] = sorted[i];
+    }
+    for (int i : members[0]) {
+      group_starts[n] = at;
+      shared_blocks[n++] = 0;
+      order[at++] = sorted[i];
+    }
+    group_starts[n] = at;
+    *num_groups = n;
+  } catch (...) {
+    return PKV_ERR_WORKSPACE;
   }
   return PKV_OK;
 }

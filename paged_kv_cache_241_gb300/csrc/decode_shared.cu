@@ -1,0 +1,1316 @@
+// decode_shared.cu -- decode attention for a batch whose sequences share prefixes.
+//
+// The block manager lets sequences with the same beginning hold the same blocks (CSDN
+// essay "from nanoVLLM to vLLM", Mountain 1; nano-vllm hub page, "core tech 4").  Plain
+// decode reads those blocks once for every sequence.  Here a group of neighbouring
+// sequences with the same first blocks reads them once: for a kv head, the query rows
+// of all (sequence, head of its group) are one matrix Q [m G, D], and over the prefix's
+// keys, which every row sees whole,
+//   M = max_p z,  l = sum_p exp(z_p - M),  o = sum_p exp(z_p - M) V_p,  z = scale Q K^T
+// is a product on the tensor cores.  What a sequence has behind the prefix is split-K
+// decode.  All parts (M, l, o) of a row are then joined:
+//   out = sum_i exp(M_i - M) o_i / sum_i exp(M_i - M) l_i.
+//
+// Four launches, each a programmatic dependent of the one before:
+//  1. plan: one CTA.  A group's prefix ends where its shortest sequence does; prefix
+//     sums of the work of groups (steps of 64 keys) and of sequences (tiles of 4 KiB
+//     of K) go to the workspace.
+//  2. tails: all sequences' own tokens, cut into runs of equal length, a warp for each
+//     run and kv head (m16n8k16, cp.async; bound by HBM).
+//  3. prefixes: units of (group, kv head, 256 rows) by steps, cut into runs of equal
+//     length, a CTA for each (tcgen05, TMA).
+//  4. join.
+#include <math.h>
+
+#include "cta_scan.cuh"
+#include "host_common.h"
+#include "pkv_common.cuh"
+#include "warp_mma.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kSharedMaxSeqs = 8192;
+constexpr int kMaxTokens = 1 << 20;      // of a sequence
+constexpr int kPlanThreads = 1024;
+constexpr int kWarpsMost = 8;            // warps per CTA of the tails (one CTA per SM)
+constexpr int kStages = 3;               // ring of tiles per warp
+constexpr int kMaxWarps = 4096;          // warps of the tails' grid at most (places for parts)
+constexpr int kMaxCtas = 512;            // CTAs of the prefixes' grid at most (places for parts)
+constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
+constexpr int BM = 128;                  // rows of a product
+constexpr int BN = 64;                   // keys of a step
+constexpr int kPairRows = 2 * BM;        // rows of a unit: two products share its keys
+constexpr int kUnitSlots = 4;
+constexpr int kJoinThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The prefix of a group, in the workspace.
+struct GroupPlan {
+  int64_t step0;  // steps of the groups before it
+  int start;      // its first sequence
+  int lead;       // the sequence whose row of the block tables is read
+  int members;
+  int tiles;      // steps of 64 keys (0: nothing is shared)
+  int pairs;      // units of one kv head
+  int pad;
+};
+
+struct Totals {
+  int64_t steps;  // of all prefixes
+  int64_t tiles;  // of all tails
+};
+
+struct SharedParams {
+  uint16_t *out;
+  const uint16_t *q;
+  const uint16_t *k_cache;
+  const uint16_t *v_cache;
+  const int32_t *block_tables;
+  const int32_t *context_lens;
+  const int32_t *group_starts;
+  const int32_t *shared_blocks;
+  Totals *totals;
+  GroupPlan *groups;   // [num_groups + 1] (the last one: step0 alone)
+  int32_t *tile0;      // [num_seqs + 1]: first tile of each sequence's tail
+  int32_t *begin;      // [num_seqs]: first token of it
+  int32_t *len;        // [num_seqs]: tokens of the sequence (0: no output)
+  int32_t *group_of;   // [num_seqs]
+  float *tail_ml;      // [num_seqs + runs, Hkv, G, 2]   (max in log2 units, sum)
+  float *tail_o;       // [num_seqs + runs, Hkv, G, D]
+  float *first_ml;     // [num_seqs, Hq, 2]: a unit's first part
+  float *first_o;      // [num_seqs, Hq, D]
+  float *run_ml;       // [CTAs, 256, 2]: the part with which a run begins inside a unit
+  float *run_o;        // [CTAs, 256, D]
+  int32_t *status;
+  int64_t num_blocks;
+  int num_seqs;
+  int num_groups;
+  int num_kv_heads;
+  int group_size;      // G
+  int block_shift;
+  int max_blocks_per_seq;
+  int runs;            // runs of the tails' tiles at most
+  int ctas;            // runs of the prefixes' steps at most
+  float qscale;        // scale * log2(e)
+};
+
+// Tokens of K in a tile of a tail: 4 KiB.
+__host__ __device__ constexpr int tail_rows(int D) { return 2048 / D; }
+
+// Tiles per run of the tails; run r's part of sequence s is filed under s + r (a part
+// begins where a sequence or a run does, so no two have the same number).
+__device__ __forceinline__ int run_tiles(const SharedParams &p, int64_t tiles) {
+  const int64_t n = (tiles + p.runs - 1) / p.runs;
+  return n < 1 ? 1 : (int)n;
+}
+// Steps per run of the prefixes.
+__device__ __forceinline__ int64_t run_steps(const SharedParams &p, int64_t steps) {
+  const int64_t n = (steps + p.ctas - 1) / p.ctas;
+  return n < 1 ? 1 : n;
+}
+
+// ----------------------------------------------------------------------- 1. plan
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, int D) {
+  extern __shared__ int plan_smem[];
+  __shared__ int64_t sums[32][1];
+  const int S = p.num_seqs, N = p.num_groups, tid = threadIdx.x;
+  int *starts = plan_smem;       // [N + 1]
+  int *eff = starts + N + 1;     // [N]: blocks that the group shares
+  int *lead = eff + N;           // [N]: its first sequence with tokens
+  int *count = lead + N;         // [N]: its sequences with tokens
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  bool ok = true;
+  for (int g = tid; g <= N; g += blockDim.x) {
+    const int x = p.group_starts[g];
+    starts[g] = x;
+    ok = ok && (g > 0 || x == 0) && (g < N || x == S);
+    if (g < N) {
+      const int b = p.shared_blocks[g];
+      if (b < 0 || b > p.max_blocks_per_seq) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+      eff[g] = min(max(b, 0), p.max_blocks_per_seq);
+      lead[g] = 0x7FFFFFFF;
+      count[g] = 0;
+    }
+  }
+  __syncthreads();
+  for (int g = tid; g < N; g += blockDim.x) ok = ok && starts[g] <= starts[g + 1];
+  ok = __syncthreads_and(ok) != 0;
+  // (no groups then: every sequence by itself)
+  if (!ok && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  auto tokens = [&](int s) {
+    const int L = p.context_lens[s];
+    return L <= 0 ? 0 : (int)min((int64_t)L, room);
+  };
+  if (ok) {
+    for (int s0 = tid & ~31; s0 < S; s0 += blockDim.x) {
+      const int s = s0 + (tid & 31);
+      const int L = s < S ? tokens(s) : 0;
+      const int g = s < S ? seq_of(starts, N, s) : -1;
+      // (a warp's sequences are neighbours: mostly one group)
+      const unsigned peers = __match_any_sync(0xffffffffu, L > 0 ? g : -1 - (tid & 31));
+      if (L > 0) {
+        const int least = __reduce_min_sync(peers, L >> p.block_shift);
+        if ((tid & 31) == __ffs(peers) - 1) {
+          atomicMin(&eff[g], least);
+          atomicMin(&lead[g], s);
+          atomicAdd(&count[g], __popc(peers));
+        }
+      }
+    }
+  }
+  __syncthreads();
+  {
+    const int per = (N + blockDim.x - 1) / (int)blockDim.x;
+    const int g0 = min(tid * per, N), g1 = min(g0 + per, N);
+    auto plan = [&](int g) {
+      GroupPlan x;
+      const int blocks = ok && count[g] >= 2 ? eff[g] : 0;
+      x.start = starts[g];
+      x.members = blocks > 0 ? starts[g + 1] - starts[g] : 0;
+      x.lead = blocks > 0 ? lead[g] : 0;
+      x.tiles = (int)(((int64_t)blocks << p.block_shift) / BN);
+      x.pairs = (x.members * p.group_size + kPairRows - 1) / kPairRows;
+      x.pad = 0;
+      x.step0 = 0;
+      return x;
+    };
+    int64_t at[1] = {0}, total[1];
+    for (int g = g0; g < g1; ++g) {
+      const GroupPlan x = plan(g);
+      at[0] += (int64_t)x.tiles * x.pairs * p.num_kv_heads;
+    }
+    scan_cta<1>(at, total, sums);
+    for (int g = g0; g < g1; ++g) {
+      GroupPlan x = plan(g);
+      x.step0 = at[0];
+      p.groups[g] = x;
+      at[0] += (int64_t)x.tiles * x.pairs * p.num_kv_heads;
+    }
+    if (tid == 0) {
+      p.groups[N].step0 = total[0];
+      p.totals->steps = total[0];
+    }
+  }
+  {
+    const int rows = tail_rows(D);
+    const int per = (S + blockDim.x - 1) / (int)blockDim.x;
+    const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+    auto first = [&](int s, int L, int &g) {
+      g = ok ? seq_of(starts, N, s) : 0;
+      return L > 0 && ok && count[g] >= 2 ? eff[g] << p.block_shift : 0;
+    };
+    int64_t at[1] = {0}, total[1];
+    for (int s = s0; s < s1; ++s) {
+      int g;
+      const int L = tokens(s);
+      at[0] += (L - first(s, L, g) + rows - 1) / rows;
+      if (L != p.context_lens[s] || L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+    }
+    scan_cta<1>(at, total, sums);
+    for (int s = s0; s < s1; ++s) {
+      int g;
+      const int L = tokens(s), b = first(s, L, g);
+      p.tile0[s] = (int)at[0];
+      p.begin[s] = b;
+      p.len[s] = L;
+      p.group_of[s] = g;
+      at[0] += (L - b + rows - 1) / rows;
+    }
+    if (tid == 0) {
+      p.tile0[S] = (int)total[0];
+      p.totals->tiles = total[0];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- 2. tails
+
+// Shared memory of one warp: a ring of tiles (tail_rows tokens of K, then of V), and
+// as many places for the query rows of the sequences in flight.
+template <int D, int G>
+struct WarpSmem {
+  static constexpr int kRows = tail_rows(D);
+  static constexpr int kHalf = kRows * D * 2;     // 4 KiB of K or V
+  static constexpr int kQ = G * D * 2;
+  static constexpr int bytes = kStages * (2 * kHalf + kQ);
+};
+
+// A warp streams the K and V of its run, for its kv head, through its own ring, up to
+// two tiles ahead and across sequences; nothing in the loop waits for another warp, and
+// the warps of the other kv heads of the same tokens run beside it.  Per 16 tokens:
+// S = K q^T (tokens x dims x heads) and O^T += V^T P (dims x tokens x heads).  P is an
+// operand in bf16: it goes in as the sum of two, its rounding and what that leaves, so
+// that a weight is off by 2^-18 of itself and not by 2^-9 (paged_decode_attn keeps it in
+// fp32).  With at most four heads columns 4 to 7 repeat the heads of 0 to 3 and take the
+// second parts; eight heads need a second product.
+template <int D, int G>
+__global__ void __launch_bounds__(kWarpsMost * 32, 1) shared_tails_kernel(const SharedParams p) {
+  using W = WarpSmem<D, G>;
+  constexpr int kRows = W::kRows;
+  constexpr int kCols = D / 8;              // 16-byte columns per row
+  constexpr int kRowsPer = 32 / kCols;      // rows per warp-wide copy
+  constexpr int kSlices = kRows / 16;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
+  uint8_t *mine = smem_raw + warp * W::bytes;
+  const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
+  int *tile0 = reinterpret_cast<int *>(smem_raw + warps * W::bytes);  // [S + 1]
+  int *begin = tile0 + S + 1;                                         // [S]
+  int *len = begin + S;                                               // [S]
+  const uint32_t tiles = smem_u32(mine);
+  const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int s = threadIdx.x; s <= S; s += blockDim.x) {
+    tile0[s] = __ldcg(p.tile0 + s);
+    if (s < S) {
+      begin[s] = __ldcg(p.begin + s);
+      len[s] = __ldcg(p.len + s);
+    }
+  }
+  __syncthreads();
+  const int total = tile0[S];
+  const int per_run = run_tiles(p, total);
+  const int runs = (total + per_run - 1) / per_run;
+  const int64_t jobs = (int64_t)runs * Hkv;  // (run, head), heads innermost
+  const uint64_t policy = l2_policy_evict_first();
+  const int col = lane % kCols, row0 = lane / kCols;
+  for (int64_t job = (int64_t)blockIdx.x * warps + warp; job < jobs;
+       job += (int64_t)gridDim.x * warps) {
+    const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
+    const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
+
+    // The loading side: tile in_t of the batch, at token in_tok of sequence in_s (in_L
+    // tokens), in block blk; blk_next is the block after it, of this sequence or the next.
+    int in_t = t_begin, in_s = seq_of(tile0, S, t_begin);
+    int in_tok = begin[in_s] + (t_begin - tile0[in_s]) * kRows;
+    int in_L = len[in_s];
+    int in_slot = 0, in_q = 0;
+    bool in_first = true;  // the sequence's first tile of this run
+    auto block_of = [&](int s, int tok) {
+      int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+        blk = 0;
+      }
+      return blk;
+    };
+    auto next_seq = [&](int s) {  // the next sequence with a tail
+      do ++s; while (s < S && tile0[s + 1] == tile0[s]);
+      return s;
+    };
+    auto block_after = [&]() {
+      const int tok = ((in_tok >> shift) + 1) << shift;
+      if (tok < in_L) return block_of(in_s, tok);
+      const int s = next_seq(in_s);
+      return s < S ? block_of(s, begin[s]) : 0;
+    };
+    int blk = block_of(in_s, in_tok), blk_next = block_after();
+    auto issue = [&]() {
+      if (in_t < t_end) {
+        if (in_first) {
+          const uint16_t *q = p.q + ((int64_t)in_s * Hkv + j) * G * D;
+          for (int x = lane; x < G * kCols; x += 32)
+            copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
+          in_q = in_q + 1 == kStages ? 0 : in_q + 1;
+          in_first = false;
+        }
+        const int64_t slot = ((int64_t)blk << shift) + (in_tok & ((1 << shift) - 1));
+        const int64_t at = ((slot + row0) * Hkv + j) * D + col * 8;
+        const int64_t step = (int64_t)kRowsPer * Hkv * D;
+        const uint32_t dst = tiles + in_slot * 2 * W::kHalf;
+#pragma unroll
+        for (int i = 0; i < kRows / kRowsPer; ++i) {
+          const int t = in_tok + row0 + i * kRowsPer;
+          const uint32_t to = dst + tile_at<D>(row0 + i * kRowsPer, col);
+          copy16(to, p.k_cache + at + i * step, t < in_L, policy);
+          copy16(to + W::kHalf, p.v_cache + at + i * step, t < in_L, policy);
+        }
+        ++in_t;
+        in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+        if (in_t < t_end) {
+          in_tok += kRows;
+          const bool ends = in_tok >= in_L;
+          if (ends || (in_tok & ((1 << shift) - 1)) == 0) {
+            if (ends) {
+              in_s = next_seq(in_s);
+              in_tok = begin[in_s];
+              in_L = len[in_s];
+              in_first = true;
+            }
+            blk = blk_next;
+            blk_next = block_after();
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    // The consuming side: sequence after sequence of the run.
+    const int h0 = 2 * (lane & 3);  // this lane's heads: columns h0, h0 + 1 of the group
+    const bool owner = h0 < G;      // (of the 8 columns only G are heads of their own)
+    int slot = 0, qslot = 0;
+    for (int s = seq_of(tile0, S, t_begin), tile = t_begin; tile < t_end; s = next_seq(s)) {
+      const int L = len[s];
+      const int first = begin[s] + (tile - tile0[s]) * kRows;       // tokens [first, last) are here
+      const int last = min(L, first + (t_end - tile) * kRows);
+      uint32_t qf[D / 16][2];
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float o[D / 16][4];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int tok = first; tok < last; tok += kRows, ++tile) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // every lane's copies are in, and the slot filled next is read out
+        issue();
+        if (tok == first) {
+          // q as the second operand: lane (head, dim pair) per 8 dims.  With fewer than
+          // eight heads, rows 4 to 7 are 0 to 3 again, those past G the last one.
+          const uint32_t qa = qslots + qslot * W::kQ;
+          const int row = G == 8 ? lane & 7 : min(lane & 3, G - 1);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t f[4];
+            ldmatrix4(f, qa + tile_at<D>(row, i * 4 + (lane >> 3)));
+            qf[2 * i][0] = f[0];
+            qf[2 * i][1] = f[1];
+            qf[2 * i + 1][0] = f[2];
+            qf[2 * i + 1][1] = f[3];
+          }
+          qslot = qslot + 1 == kStages ? 0 : qslot + 1;
+        }
+        const uint32_t ka = tiles + slot * 2 * W::kHalf, va = ka + W::kHalf;
+#pragma unroll
+        for (int sl = 0; sl < kSlices; ++sl) {
+          // S: rows are tokens (lane / 4 and + 8), columns the lane's two heads.
+          float s_even[4] = {0.f, 0.f, 0.f, 0.f}, s_odd[4] = {0.f, 0.f, 0.f, 0.f};
+          const int kr = sl * 16 + (lane & 15);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldmatrix4(a, ka + tile_at<D>(kr, 2 * i + (lane >> 4)));
+            if (i & 1) mma16816(s_odd, a, qf[i][0], qf[i][1]);
+            else mma16816(s_even, a, qf[i][0], qf[i][1]);
+          }
+          const int i0 = sl * 16 + (lane >> 2), i1 = i0 + 8;  // rows of the tile
+          float z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = (s_even[i] + s_odd[i]) * p.qscale;
+          if (tok + i0 >= L) z[0] = z[1] = -INFINITY;
+          if (tok + i1 >= L) z[2] = z[3] = -INFINITY;
+          float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, k));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, k));
+          }
+          n0 = fmaxf(n0, m0);
+          n1 = fmaxf(n1, m1);
+          // (a maximum of -inf: every weight so far is zero, whatever the reference)
+          const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+          const float a0 = fast_exp2(m0 - r0), a1 = fast_exp2(m1 - r1);
+          m0 = n0;
+          m1 = n1;
+          const float p0 = fast_exp2(z[0] - r0), p1 = fast_exp2(z[1] - r1);
+          const float p2 = fast_exp2(z[2] - r0), p3 = fast_exp2(z[3] - r1);
+          l0 = fmaf(l0, a0, p0 + p2);
+          l1 = fmaf(l1, a1, p1 + p3);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][0] *= a0;
+            o[i][1] *= a1;
+            o[i][2] *= a0;
+            o[i][3] *= a1;
+          }
+          // P as the second operand of the next product, in two parts (see above);
+          // the sums keep the fp32 weights.
+          uint32_t first0 = pack_bf16x2(p0, p1), first1 = pack_bf16x2(p2, p3);
+          const uint32_t rest0 = pack_bf16x2(p0 - bf16lo(first0), p1 - bf16hi(first0));
+          const uint32_t rest1 = pack_bf16x2(p2 - bf16lo(first1), p3 - bf16hi(first1));
+          if (G < 8 && (lane & 2)) {
+            first0 = rest0;
+            first1 = rest1;
+          }
+          const uint32_t b0 = transpose8x8(first0), b1 = transpose8x8(first1);
+          uint32_t c0 = 0, c1 = 0;
+          if (G == 8) {
+            c0 = transpose8x8(rest0);
+            c1 = transpose8x8(rest1);
+          }
+          // V^T: two 8-token halves by two 8-dim columns, transposed on the way.
+          const int vr = sl * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldmatrix4_trans(a, va + tile_at<D>(vr, 2 * i + ((lane >> 3) & 1)));
+            mma16816(o[i], a, b0, b1);
+            if (G == 8) mma16816(o[i], a, c0, c1);
+          }
+        }
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+      }
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, k);
+      }
+      if (G < 8) {  // the two halves of O
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[i][x] += __shfl_xor_sync(0xffffffffu, o[i][x], 2);
+      }
+      if (owner) {
+        const int64_t part = ((int64_t)(s + r) * Hkv + j) * G + h0;
+        float *po = p.tail_o + part * D;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int d = i * 16 + (lane >> 2);
+          po[d] = o[i][0];
+          po[d + 8] = o[i][2];
+          if (G > 1) {
+            po[D + d] = o[i][1];
+            po[D + d + 8] = o[i][3];
+          }
+        }
+        if (lane < 4) {
+          float2 *ml = reinterpret_cast<float2 *>(p.tail_ml) + part;
+          ml[0] = make_float2(m0, l0);
+          if (G > 1) ml[1] = make_float2(m1, l1);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------- 3. prefixes
+
+// A piece of a unit: steps [tile, tile + n) of rows [256 pair, 256 pair + rows) of the
+// group that begins at sequence start, for kv head kvh.
+struct Piece {
+  int start, lead, kvh, pair, rows, tile, n;
+  int first;  // it begins where the unit does: its parts are filed by row, else by run
+};
+
+template <int D>
+struct PrefixLayout {
+  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kKVBytes = BN * D * 2;
+  static constexpr int kSlots0 = (kMaxDynamicSmem - 3072 - 2 * kQBytes) / kKVBytes;
+  static constexpr int kSlots = kSlots0 < 16 ? kSlots0 : 16;
+  static constexpr int kKStages = kSlots * 2 / 5;  // (a V slot is held longer)
+  static constexpr int kVStages = kSlots - kKStages;
+  static constexpr int q = 0;
+  static constexpr int k = q + 2 * kQBytes;
+  static constexpr int v = k + kKStages * kKVBytes;
+  static constexpr int bars = v + kVStages * kKVBytes;
+  // q_full, q_empty, k_full[SK], v_full[SV], k_empty[SK], v_empty[SV], s_full[2][2],
+  // p_full[2][2], p_free[2][2], o_free[2], unit_full[U], unit_empty[U], drain
+  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 14 + 2 * kUnitSlots + 1;
+  static constexpr int misc = bars + kNumBars * 8;  // tensor memory address, abort flag
+  static constexpr int ring = misc + 8;
+  static constexpr int total = ring + (int)sizeof(Piece) * kUnitSlots;
+  // One CTA per SM (it takes all of tensor memory): more than half of an SM's shared
+  // memory, so that a second one never waits for tensor memory.
+  static_assert(total + 1024 <= kMaxDynamicSmem && total > 114 * 1024, "shared memory");
+};
+
+// Tensor memory columns (lane = row): O of the two row tiles at 0 and D, then two S
+// buffers of 64 columns for each.  A buffer holds S (fp32), then over it P as two bf16
+// terms, 32 columns each: the weights' roundings and what those leave.
+template <int D>
+struct PrefixCols {
+  static constexpr uint32_t kS = 2 * D;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  const bool ok = mbar_wait_bounded(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void store32(float *ptr, const float (&v)[64], int i) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(ptr), "f"(v[i]),
+               "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]),
+               "f"(v[i + 6]), "f"(v[i + 7])
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
+  using L = PrefixLayout<D>;
+  constexpr int XR = D / 64;  // 128-byte swizzle regions across D
+  constexpr int kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr uint32_t kSCol = PrefixCols<D>::kS;
+  constexpr int kKWarp = 0, kSWarp = 1, kVWarp = 2, kPVWarp = 3;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sQ = smem + L::q, *sK = smem + L::k, *sV = smem + L::v;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  uint64_t *q_full = bars;
+  uint64_t *q_empty = bars + 1;             // the piece's S products no longer read Q
+  uint64_t *k_full = bars + 2;
+  uint64_t *v_full = k_full + kKStages;
+  uint64_t *k_empty = v_full + kVStages;
+  uint64_t *v_empty = k_empty + kKStages;
+  uint64_t *s_full = v_empty + kVStages;    // [row tile][buffer]: S is in
+  uint64_t *p_full = s_full + 4;            // P is written over it
+  uint64_t *p_free = p_full + 4;            // that P.V is done (O updated, buffer free)
+  uint64_t *o_free = p_free + 4;            // [row tile]: O has been read
+  uint64_t *unit_full = o_free + 2;
+  uint64_t *unit_empty = unit_full + kUnitSlots;
+  uint64_t *drain = unit_empty + kUnitSlots;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  Piece *ring = reinterpret_cast<Piece *>(smem + L::ring);  // start < 0 ends
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The plan is there: the kernel before began after it, and this one after that.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t steps = __ldcg(&p.totals->steps);
+  const int64_t len = run_steps(p, steps);
+  const int64_t x0 = (int64_t)blockIdx.x * len;
+  if (x0 >= steps) {
+    // (The launch must not end before the one before it has: the join waits for this one.)
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int64_t x1 = x0 + len < steps ? x0 + len : steps;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&p_free[i], 1);
+    }
+    mbar_init(&o_free[0], 4);
+    mbar_init(&o_free[1], 4);
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], 1 + 2 + 8);  // V loader, issuers, softmax warps
+    }
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  auto next_piece = [&](int &iu, Piece &u) -> bool {
+    const int slot = iu % kUnitSlots;
+    if (!warp_wait(&unit_full[slot], (iu / kUnitSlots) & 1, abort_flag)) return false;
+    u = ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&unit_empty[slot]);
+    ++iu;
+    return u.start >= 0;
+  };
+
+  if (warp == kKWarp || warp == kVWarp) {
+    // Loaders: warp 0 walks the run (handing its pieces to the other roles) and loads Q
+    // and K, warp 2 loads V.
+    const bool is_k = warp == kKWarp;
+    uint64_t *full = is_k ? k_full : v_full;
+    uint64_t *empty = is_k ? k_empty : v_empty;
+    uint8_t *slots = is_k ? sK : sV;
+    const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+    const int nst = is_k ? kKStages : kVStages;
+    int iu = 0, g = 0, q_loads = 0;
+    bool ok = true;
+    if (lane == 0) {
+      if (is_k) tma_prefetch_map(&tm_q);
+      tma_prefetch_map(map);
+    }
+    int64_t x = x0;
+    int grp = 0;
+    GroupPlan gp = {};
+    int64_t gp_end = -1;  // steps up to the end of the group in gp
+    for (;;) {
+      Piece u;
+      bool have;
+      if (is_k) {
+        have = x < x1;
+        if (have) {
+          if (x >= gp_end) {
+            // The group of step x: the last one that begins at it or before.
+            int lo = grp, hi = p.num_groups;
+            while (hi - lo > 1) {
+              const int stride = (hi - lo + 31) / 32;
+              const int at = lo + lane * stride;
+              const bool before = at < hi && __ldcg(&p.groups[at].step0) <= x;
+              const int k = __popc(__ballot_sync(0xffffffffu, before));
+              const int from = lo + (k - 1) * stride;
+              hi = min(hi, from + stride);
+              lo = from;
+            }
+            grp = lo;
+            const int4 *src = reinterpret_cast<const int4 *>(p.groups + grp);
+            const int4 a = __ldcg(src), b = __ldcg(src + 1);
+            gp.step0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
+            gp.start = a.z;
+            gp.lead = a.w;
+            gp.members = b.x;
+            gp.tiles = b.y;
+            gp.pairs = b.z;
+            gp_end = gp.step0 + (int64_t)gp.tiles * gp.pairs * p.num_kv_heads;
+          }
+          const int64_t in = x - gp.step0;
+          const int unit = (int)(in / gp.tiles);
+          u.tile = (int)(in - (int64_t)unit * gp.tiles);
+          u.n = (int)min((int64_t)(gp.tiles - u.tile), x1 - x);
+          u.kvh = unit / gp.pairs;
+          u.pair = unit - u.kvh * gp.pairs;
+          u.rows = min(kPairRows, gp.members * p.group_size - u.pair * kPairRows);
+          u.start = gp.start;
+          u.lead = gp.lead;
+          u.first = u.tile == 0;
+          x += u.n;
+        } else {
+          u.start = -1;
+        }
+        const int slot = iu % kUnitSlots;
+        if (iu >= kUnitSlots)
+          ok = warp_wait(&unit_empty[slot], ((iu / kUnitSlots) - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          ring[slot] = u;
+          mbar_arrive(&unit_full[slot]);  // (release: orders the stores above)
+        }
+        ++iu;
+      } else {
+        have = next_piece(iu, u);
+      }
+      if (!have) break;
+      if (lane == 0) {
+        if (is_k) {
+          // Q of this piece once the last one's S products are done with it.
+          if (iu >= 2) ok = mbar_wait_bounded(q_empty, (iu - 2) & 1, abort_flag);
+          if (ok) {
+            ++q_loads;
+            const int tiles = u.rows > BM ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, tiles * L::kQBytes);
+            for (int h = 0; h < tiles; ++h)
+              for (int xr = 0; xr < XR; ++xr)
+                tma_load_3d(sQ + h * L::kQBytes + xr * BM * 128, &tm_q, q_full, xr * 64,
+                            u.kvh * p.group_size,
+                            u.start + (u.pair * kPairRows + h * BM) / p.group_size);
+          }
+        }
+        const int32_t *row = p.block_tables + (int64_t)u.lead * p.max_blocks_per_seq;
+        for (int i = 0; i < u.n && ok; ++i, ++g) {
+          const int st = g % nst;
+          if (g >= nst && !mbar_wait_bounded(&empty[st], ((g / nst) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int key0 = (u.tile + i) * BN;
+          int blk = row[key0 >> p.block_shift];
+          if (blk < 0 || (int64_t)blk >= p.num_blocks) {
+            flag_status(p.status, PKV_DEV_BAD_BLOCK);
+            blk = 0;
+          }
+          mbar_arrive_expect_tx(&full[st], L::kKVBytes);
+          for (int xr = 0; xr < XR; ++xr)
+            tma_load_4d(slots + st * L::kKVBytes + xr * BN * 128, map, &full[st], xr * 64, u.kvh,
+                        key0 & ((1 << p.block_shift) - 1), blk);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      g = __shfl_sync(0xffffffffu, g, 0);
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      // Do not leave while copies into this CTA's shared memory are in flight.
+      if (is_k && q_loads > 0 && !mbar_wait_bounded(q_full, (q_loads - 1) & 1, nullptr))
+        flag_status(p.status, PKV_DEV_TIMEOUT);
+      for (int i = max(0, g - nst); i < g; ++i)
+        if (!mbar_wait_bounded(&full[i % nst], (i / nst) & 1, nullptr))
+          flag_status(p.status, PKV_DEV_TIMEOUT);
+    }
+  } else if (warp == kSWarp || warp == kPVWarp) {
+    // Issuers: warp 1 S = Q K^T, warp 3 O += P V.  gh[h]: steps of row tile h so far,
+    // uh[h]: pieces (the second row tile takes no part in pieces of up to 128 rows).
+    int iu = 0, g = 0;
+    int gh[2] = {0, 0}, uh[2] = {0, 0};
+    bool ok = true;
+    Piece u;
+    if (warp == kSWarp) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(BM, BN, false, false);
+      const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
+      while (ok && next_piece(iu, u)) {
+        const int nh = u.rows > BM ? 2 : 1;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(q_full, (iu - 1) & 1, abort_flag);
+          for (int i = 0; i < u.n && ok; ++i, ++g) {
+            const int st = g % kKStages;
+            ok = mbar_wait_bounded(&k_full[st], (g / kKStages) & 1, abort_flag);
+            const uint64_t dk_st = dk + (uint64_t)((st * L::kKVBytes) >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h >= nh || !ok) break;
+              const int gt = gh[h] + i, b = gt & 1;
+              if (gt >= 2)
+                ok = mbar_wait_bounded(&p_free[2 * h + b], ((gt - 2) >> 1) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint32_t d = tmem + kSCol + (2 * h + b) * BN;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk & 3) * 32;
+                umma_bf16(d, dq + (uint64_t)((h * L::kQBytes + (kk / 4) * BM * 128 + off) >> 4),
+                          dk_st + (uint64_t)(((kk / 4) * BN * 128 + off) >> 4), idesc_s,
+                          kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[2 * h + b]);
+            }
+            if (ok) umma_commit(&k_empty[st]);
+          }
+          if (ok) umma_commit(q_empty);
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        g = __shfl_sync(0xffffffffu, g, 0);
+        gh[0] += u.n;
+        if (nh == 2) gh[1] += u.n;
+      }
+    } else {
+      constexpr uint32_t idesc_o = umma_idesc_bf16(BM, D, false, true);
+      const uint64_t dv = umma_desc_sw128(smem_u32(sV), BN * 128, 1024);
+      while (ok && next_piece(iu, u)) {
+        const int nh = u.rows > BM ? 2 : 1;
+        if (lane == 0) {
+          for (int i = 0; i < u.n && ok; ++i, ++g) {
+            const int st = g % kVStages;
+            ok = mbar_wait_bounded(&v_full[st], (g / kVStages) & 1, abort_flag);
+            const uint64_t dv_st = dv + (uint64_t)((st * L::kKVBytes) >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h >= nh || !ok) break;
+              const int gt = gh[h] + i, b = gt & 1;
+              ok = mbar_wait_bounded(&p_full[2 * h + b], (gt >> 1) & 1, abort_flag);
+              if (ok && i == 0 && uh[h] >= 1)
+                ok = mbar_wait_bounded(&o_free[h], (uh[h] - 1) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint32_t pa = tmem + kSCol + (2 * h + b) * BN;
+              // Both terms of P: columns 0-31 and 32-63 of the buffer.
+#pragma unroll
+              for (int kk = 0; kk < BN / 8; ++kk)
+                umma_bf16_tmem_a(tmem + h * D, pa + kk * 8,
+                                 dv_st + (uint64_t)(((kk % (BN / 16)) * 16 * 128) >> 4), idesc_o,
+                                 (i > 0 || kk > 0) ? 1u : 0u);
+              umma_commit(&p_free[2 * h + b]);
+            }
+            if (ok) umma_commit(&v_empty[st]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        g = __shfl_sync(0xffffffffu, g, 0);
+        for (int h = 0; h < nh; ++h) {
+          gh[h] += u.n;
+          ++uh[h];
+        }
+      }
+    }
+    if (lane == 0) {
+      // Wait for the products of both issuers before tensor memory is freed.
+      umma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
+    }
+  } else {
+    // Softmax: four warps per row tile, a thread per row (tile 0: warps 4, 5, 10, 11).
+    const int h = (((warp - 4) >> 1) ^ ((warp - 4) >> 2)) & 1;
+    const int quarter = warp & 3;   // tensor memory lanes this warp may access
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const float qs = p.qscale;
+    int iu = 0, gt = 0;
+    bool ok = true;
+    Piece u;
+    // A piece's (max, sum, O) as a part, once its last P.V (step g_last) is in O; run
+    // after the next piece's first P is published, which that wait then overlaps.
+    auto write_part = [&](const Piece &e, float m_e, float l_e, int g_last) -> bool {
+      if (!warp_wait(&p_free[2 * h + (g_last & 1)], (g_last >> 1) & 1, abort_flag)) return false;
+      tc_fence_after_sync();
+      const int r = h * BM + row;
+      const int Hq = p.num_kv_heads * p.group_size;
+      const int idx = e.pair * kPairRows + r;  // of the group's rows
+      const int64_t at = e.first ? (int64_t)(e.start + idx / p.group_size) * Hq +
+                                       e.kvh * p.group_size + idx % p.group_size
+                                 : (int64_t)blockIdx.x * kPairRows + r;
+      float *o = (e.first ? p.first_o : p.run_o) + at * D;
+#pragma unroll 1
+      for (int half = 0; half < D / 64; ++half) {
+        float ov[64];
+        tmem_load64(tmem + lane_base + h * D + half * 64, ov);
+        if (r < e.rows) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 8) store32(o + half * 64 + i, ov, i);
+        }
+      }
+      if (r < e.rows)
+        reinterpret_cast<float2 *>(e.first ? p.first_ml : p.run_ml)[at] = make_float2(m_e, l_e);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[h]);
+      return true;
+    };
+    bool pending = false;
+    Piece e;
+    float e_m = 0.f, e_l = 0.f;
+    int e_g = 0;
+    while (ok && next_piece(iu, u)) {
+      if (h == 1 && u.rows <= BM) continue;
+      // A warp whose rows all lie behind the piece's skips the arithmetic.
+      const bool live = h * BM + quarter * 32 < u.rows;
+      // Running max in log2 units, raised (and O rescaled) only when a step's exceeds it
+      // by more than 8: P stays <= 2^8, and l and O share the reference.
+      float m_ref = -INFINITY, l_run = 0.f;
+      for (int i = 0; i < u.n && ok; ++i, ++gt) {
+        const int b = gt & 1;
+        const uint32_t sp = tmem + lane_base + kSCol + (2 * h + b) * BN;
+        ok = warp_wait(&s_full[2 * h + b], (gt >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after_sync();
+        float alpha = 1.f, rs = 0.f;
+        if (live) {
+          float sv[BN], mt;
+          if (qs > 0.f) {
+            tmem_load64_max(sp, sv, mt);
+          } else {
+            tmem_load64(sp, sv);
+            mt = sv[0];
+#pragma unroll
+            for (int c = 1; c < BN; ++c) mt = fminf(mt, sv[c]);
+          }
+          mt *= qs;
+          if (i == 0 || mt > m_ref + 8.f) {
+            const float m_new = fmaxf(m_ref, mt);
+            alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+            m_ref = m_new;
+          }
+          // (a maximum of -inf: every weight so far is zero, whatever the reference)
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 q2 = make_float2(qs, qs), nm2 = make_float2(-ref, -ref);
+          float2 r01 = make_float2(0.f, 0.f), r23 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float hi[16], lo[16];
+#pragma unroll
+            for (int c = hf * 32; c < hf * 32 + 32; c += 4) {
+              const float2 x01 = __ffma2_rn(make_float2(sv[c], sv[c + 1]), q2, nm2);
+              const float2 x23 = __ffma2_rn(make_float2(sv[c + 2], sv[c + 3]), q2, nm2);
+              const float2 p01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+              const float2 p23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+              r01 = __fadd2_rn(r01, p01);
+              r23 = __fadd2_rn(r23, p23);
+              const uint32_t h01 = pack_bf16x2(p01.x, p01.y), h23 = pack_bf16x2(p23.x, p23.y);
+              const int w = (c - hf * 32) / 2;
+              hi[w] = __uint_as_float(h01);
+              hi[w + 1] = __uint_as_float(h23);
+              lo[w] = __uint_as_float(pack_bf16x2(p01.x - bf16lo(h01), p01.y - bf16hi(h01)));
+              lo[w + 1] = __uint_as_float(pack_bf16x2(p23.x - bf16lo(h23), p23.y - bf16hi(h23)));
+            }
+            tmem_store16_async(sp + hf * 16, hi);
+            tmem_store16_async(sp + 32 + hf * 16, lo);
+          }
+          tmem_wait_st();
+          rs = (r01.x + r01.y) + (r23.x + r23.y);
+        }
+        if (live && i > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
+          // O is rescaled once the last P.V has landed in it (the next waits for this
+          // step's P).
+          ok = warp_wait(&p_free[2 * h + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            float ov[32];
+            const uint32_t oa = tmem + lane_base + h * D + cc * 32;
+            tmem_load32(oa, ov);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] *= alpha;
+            tmem_store32(oa, ov);
+          }
+        }
+        l_run = l_run * alpha + rs;
+        tc_fence_before_sync();
+        mbar_arrive(&p_full[2 * h + b]);
+        if (pending) {
+          pending = false;
+          ok = write_part(e, e_m, e_l, e_g);
+        }
+      }
+      if (!ok) break;
+      pending = true;
+      e = u;
+      e_m = m_ref;
+      e_l = l_run;
+      e_g = gt - 1;
+    }
+    if (ok && pending) ok = write_part(e, e_m, e_l, e_g);
+    tc_fence_before_sync();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, PKV_DEV_TIMEOUT);
+  if (warp == kSWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ----------------------------------------------------------------------- 4. join
+
+// A CTA per (sequence, kv head).
+template <int D, int G>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
+  __shared__ float4 acc_s[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int Hkv = p.num_kv_heads, Hq = Hkv * G;
+  const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int L = __ldcg(p.len + s);
+  if (L <= 0) return;
+  // The parts of the tail: of runs r0, r0 + 1, ...
+  const int t0 = __ldcg(p.tile0 + s), t1 = __ldcg(p.tile0 + s + 1);
+  const GroupPlan gp = p.groups[__ldcg(p.group_of + s)];
+  const int64_t tiles = __ldcg(&p.totals->tiles), steps = __ldcg(&p.totals->steps);
+  int n_tail = 0;
+  int64_t tail_row = 0;
+  if (t1 > t0) {
+    const int per_run = run_tiles(p, tiles);
+    const int r0 = t0 / per_run;
+    n_tail = (t1 - 1) / per_run - r0 + 1;
+    tail_row = ((int64_t)(s + r0) * Hkv + j) * G;
+  }
+  // Those of the prefix: of the unit that has the sequence's rows.
+  int n_pre = 0;
+  int64_t first_row = 0, run_row = 0;
+  if (gp.tiles > 0) {
+    const int64_t len = run_steps(p, steps);
+    const int idx = (s - gp.start) * G;
+    const int64_t u0 = gp.step0 + (int64_t)(j * gp.pairs + idx / kPairRows) * gp.tiles;
+    const int64_t c0 = u0 / len;
+    n_pre = (int)((u0 + gp.tiles - 1) / len - c0 + 1);
+    first_row = (int64_t)s * Hq + j * G;
+    run_row = c0 * kPairRows + idx % kPairRows;
+  }
+  const int n = n_tail + n_pre;
+  // Row (of its kind's arrays) of part i, head 0.
+  auto row_of = [&](int i, const float *&ml, const float *&o) -> int64_t {
+    if (i < n_tail) {
+      ml = p.tail_ml;
+      o = p.tail_o;
+      return tail_row + (int64_t)i * Hkv * G;
+    }
+    i -= n_tail;
+    ml = i == 0 ? p.first_ml : p.run_ml;
+    o = i == 0 ? p.first_o : p.run_o;
+    return i == 0 ? first_row : run_row + (int64_t)i * kPairRows;
+  };
+  // Maximum and sum of every head: lane (part, head) of every warp alike.
+  float M[G], inv[G];
+  {
+    const int g = lane % G;
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane / G; i < n; i += 32 / G) {
+      const float *ml, *o;
+      const int64_t at = row_of(i, ml, o) + g;
+      const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml) + at);
+      const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - ref) + x.y * fast_exp2(x.x - ref);
+      m = mn;
+    }
+#pragma unroll
+    for (int k = G; k < 32; k <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, k);
+      const float l2 = __shfl_xor_sync(0xffffffffu, l, k);
+      const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
+      m = mn;
+    }
+    l = 1.f / l;
+#pragma unroll
+    for (int x = 0; x < G; ++x) {
+      M[x] = __shfl_sync(0xffffffffu, m, x);
+      inv[x] = __shfl_sync(0xffffffffu, l, x);
+    }
+  }
+  // The D * G values, four at a time; several threads of a CTA share the parts of each.
+  constexpr int kQuads = D * G / 4;
+  for (int qb = 0; qb < kQuads; qb += kJoinThreads) {
+    const int width = min(kQuads - qb, kJoinThreads);
+    const int lanes = kJoinThreads / width;
+    const int quad = qb + tid % width, mine = tid / width;
+    const int g = quad / (D / 4), d = quad % (D / 4);
+    float Mg = M[0], ig = inv[0];
+#pragma unroll
+    for (int x = 1; x < G; ++x)
+      if (g == x) {
+        Mg = M[x];
+        ig = inv[x];
+      }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = mine; i < n; i += lanes) {
+      const float *ml, *o;
+      const int64_t at = row_of(i, ml, o) + g;
+      const float4 y = __ldcg(reinterpret_cast<const float4 *>(o) + at * (D / 4) + d);
+      const float m = __ldcg(ml + 2 * at);
+      // (a part without weight: its maximum is -inf, and the joined one may be, too)
+      const float w = m == -INFINITY ? 0.f : fast_exp2(m - Mg);
+      acc.x = fmaf(w, y.x, acc.x);
+      acc.y = fmaf(w, y.y, acc.y);
+      acc.z = fmaf(w, y.z, acc.z);
+      acc.w = fmaf(w, y.w, acc.w);
+    }
+    __syncthreads();
+    acc_s[tid] = acc;
+    __syncthreads();
+    if (tid < width) {
+      for (int k = 1; k < lanes; ++k) {
+        const float4 y = acc_s[k * width + tid];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      uint2 w;
+      w.x = pack_bf16x2(acc.x * ig, acc.y * ig);
+      w.y = pack_bf16x2(acc.z * ig, acc.w * ig);
+      *reinterpret_cast<uint2 *>(p.out + (((int64_t)s * Hq + j * G + g) * D + d * 4)) = w;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- host
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Workspace {
+  size_t totals, groups, tile0, begin, len, group_of, tail_ml, tail_o, first_ml, first_o, run_ml,
+      run_o, total;
+  Workspace(int64_t S, int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
+    const int64_t parts = S * Hq + (kMaxWarps + Hkv) * (Hq / Hkv);  // (num_seqs + runs) of each head
+    totals = 0;
+    groups = 256;
+    tile0 = groups + align256((size_t)(N + 1) * sizeof(GroupPlan));
+    begin = tile0 + align256((size_t)(S + 1) * 4);
+    len = begin + align256((size_t)S * 4);
+    group_of = len + align256((size_t)S * 4);
+    tail_ml = group_of + align256((size_t)S * 4);
+    tail_o = tail_ml + align256((size_t)parts * 8);
+    first_ml = tail_o + align256((size_t)(parts * D) * 4);
+    first_o = first_ml + align256((size_t)(S * Hq) * 8);
+    run_ml = first_o + align256((size_t)(S * Hq * D) * 4);
+    run_o = run_ml + align256((size_t)kMaxCtas * kPairRows * 8);
+    total = run_o + align256((size_t)(kMaxCtas * kPairRows * D) * 4);
+  }
+};
+
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, int smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int G>
+pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk,
+                  const CUtensorMap &tv, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return PKV_ERR_CUDA;
+  const int S = prm.num_seqs;
+  const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
+  const int plan_smem = (4 * prm.num_groups + 1) * 4;
+  const int seq_smem = (3 * S + 1) * 4;
+  int warps = (kMaxDynamicSmem - 1024 - seq_smem) / WarpSmem<D, G>::bytes;
+  if (warps > kWarpsMost) warps = kWarpsMost;
+  static_assert((kMaxDynamicSmem - 1024 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
+  const int tails_smem = warps * WarpSmem<D, G>::bytes + seq_smem;
+  const int prefix_smem = PrefixLayout<D>::total + 1024;
+  if (!kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr) ||
+      !kernel_smem_setup((const void *)shared_tails_kernel<D, G>, warps * 32, tails_smem, nullptr) ||
+      !kernel_smem_setup((const void *)shared_prefix_kernel<D>, 384, prefix_smem, nullptr))
+    return PKV_ERR_CUDA;
+  // As many runs as give every warp of the GPU one of a kv head, and no more than the
+  // longest possible batch has tiles.
+  int64_t all = (int64_t)sms * warps;
+  if (all > kMaxWarps) all = kMaxWarps;
+  int64_t runs = all / prm.num_kv_heads;
+  const int rows = tail_rows(D);
+  const int64_t tiles = (int64_t)S * ((room + rows - 1) / rows);
+  if (runs > tiles) runs = tiles;
+  if (runs < 1) runs = 1;
+  prm.runs = (int)runs;
+  int64_t grid = (runs * prm.num_kv_heads + warps - 1) / warps;
+  if (grid > sms) grid = sms;
+  const int64_t pairs = (int64_t)S * G / kPairRows + (S + 1) / 2;  // of a kv head, at most
+  int64_t steps = pairs * prm.num_kv_heads * (room / BN);
+  int64_t ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (ctas > steps) ctas = steps;
+  prm.ctas = (int)ctas;
+  cudaError_t err = launch_dependent<SharedParams, int>(shared_plan_kernel, 1, kPlanThreads,
+                                                        plan_smem, stream, prm, D);
+  if (err == cudaSuccess)
+    err = launch_dependent<SharedParams>(shared_tails_kernel<D, G>, (unsigned)grid, warps * 32,
+                                         tails_smem, stream, prm);
+  if (err == cudaSuccess)
+    err = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, SharedParams>(
+        shared_prefix_kernel<D>, (unsigned)ctas, 384, prefix_smem, stream, tq, tk, tv, prm);
+  if (err == cudaSuccess)
+    err = launch_dependent<SharedParams>(shared_join_kernel<D, G>, (unsigned)(S * prm.num_kv_heads),
+                                         kJoinThreads, 0, stream, prm);
+  return launch_status();  // (any launch's error, which it clears)
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                                   int num_kv_heads, int head_dim) {
+  using namespace pkv;
+  if (num_seqs <= 0 || num_groups <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+    return 0;
+  if (num_q_heads > (1 << 16) || head_dim > (1 << 16) || num_q_heads < num_kv_heads) return 0;
+  return Workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim).total;
+}
+
+extern "C" pkv_status pkv_paged_decode_shared_attn(
+    uint16_t *out, const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+    const int32_t *block_tables, const int32_t *context_lens, const int32_t *group_starts,
+    const int32_t *shared_blocks, int num_seqs, int num_groups, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || num_groups < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+  const int G = num_q_heads / num_kv_heads;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PKV_ERR_UNSUPPORTED;
+  if (block_size != 64 && block_size != 128 && block_size != 256 && block_size != 512)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > kSharedMaxSeqs || num_kv_heads > 4096 ||
+      (int64_t)max_blocks_per_seq * block_size > kMaxTokens)
+    return PKV_ERR_UNSUPPORTED;
+  // NaN or infinite, itself or in the exponentials' base 2 (a logit of zero would be NaN)
+  if (!isfinite(scale * kLog2e)) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_groups == 0 || num_groups > num_seqs) return PKV_ERR_INVALID_ARG;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !group_starts ||
+      !shared_blocks)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_INVALID_ARG;
+  const size_t need = pkv_decode_shared_workspace_size(num_seqs, num_groups, num_q_heads,
+                                                       num_kv_heads, head_dim);
+  if (workspace == nullptr || workspace_bytes < need ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PKV_ERR_WORKSPACE;
+
+  const Workspace lay(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  SharedParams prm;
+  prm.out = out;
+  prm.q = q;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.block_tables = block_tables;
+  prm.context_lens = context_lens;
+  prm.group_starts = group_starts;
+  prm.shared_blocks = shared_blocks;
+  prm.totals = reinterpret_cast<Totals *>(ws + lay.totals);
+  prm.groups = reinterpret_cast<GroupPlan *>(ws + lay.groups);
+  prm.tile0 = reinterpret_cast<int32_t *>(ws + lay.tile0);
+  prm.begin = reinterpret_cast<int32_t *>(ws + lay.begin);
+  prm.len = reinterpret_cast<int32_t *>(ws + lay.len);
+  prm.group_of = reinterpret_cast<int32_t *>(ws + lay.group_of);
+  prm.tail_ml = reinterpret_cast<float *>(ws + lay.tail_ml);
+  prm.tail_o = reinterpret_cast<float *>(ws + lay.tail_o);
+  prm.first_ml = reinterpret_cast<float *>(ws + lay.first_ml);
+  prm.first_o = reinterpret_cast<float *>(ws + lay.first_o);
+  prm.run_ml = reinterpret_cast<float *>(ws + lay.run_ml);
+  prm.run_o = reinterpret_cast<float *>(ws + lay.run_o);
+  prm.status = dev_status;
+  prm.num_blocks = num_blocks;
+  prm.num_seqs = num_seqs;
+  prm.num_groups = num_groups;
+  prm.num_kv_heads = num_kv_heads;
+  prm.group_size = G;
+  prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
+  prm.max_blocks_per_seq = max_blocks_per_seq;
+  prm.runs = 0;
+  prm.ctas = 0;
+  prm.qscale = scale * kLog2e;
+
+  // q as {D, Hq, S}: a box is 64 dims x the G heads of a kv head x 128 / G sequences.
+  const uint64_t qdims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)num_seqs};
+  const uint64_t qstr[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
+  const uint32_t qbox[3] = {64u, (uint32_t)G, (uint32_t)(BM / G)};
+  // cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
+  const uint64_t kdims[4] = {(uint64_t)head_dim, (uint64_t)num_kv_heads, (uint64_t)block_size,
+                             (uint64_t)num_blocks};
+  const uint64_t kstr[3] = {(uint64_t)head_dim * 2, (uint64_t)num_kv_heads * head_dim * 2,
+                            (uint64_t)block_size * num_kv_heads * head_dim * 2};
+  const uint32_t kbox[4] = {64u, 1u, (uint32_t)BN, 1u};
+  CUtensorMap tq, tk, tv;
+  if (!encode_bf16_map(&tq, q, 3, qdims, qstr, qbox, true) ||
+      !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true) ||
+      !encode_bf16_map(&tv, v_cache, 4, kdims, kstr, kbox, true))
+    return PKV_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define PKV_CASE(DD, GG) \
+  if (head_dim == DD && G == GG) return launch<DD, GG>(prm, tq, tk, tv, st);
+  PKV_CASE(64, 1)
+  PKV_CASE(64, 2)
+  PKV_CASE(64, 4)
+  PKV_CASE(64, 8)
+  PKV_CASE(128, 1)
+  PKV_CASE(128, 2)
+  PKV_CASE(128, 4)
+  PKV_CASE(128, 8)
+#undef PKV_CASE
+  return PKV_ERR_UNSUPPORTED;
+}

@@ -26,6 +26,7 @@
 
 #include "host_common.h"
 #include "pkv_common.cuh"
+#include "warp_mma.cuh"
 
 namespace pkv {
 namespace {
@@ -119,17 +120,6 @@ __device__ int64_t scan_tiles(const WeightsParams &p, int *prefix, int64_t *warp
   return total;
 }
 
-// The sequence that tile t belongs to (the last s with prefix[s] <= t).
-__device__ __forceinline__ int seq_of(const int *prefix, int S, int t) {
-  int lo = 0, hi = S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // Tiles per run.  Run r has tiles [r * n, (r + 1) * n) of the batch; its part of
 // sequence s is filed under s + r: every part begins where a sequence or a run
 // does, so no two have the same number.  A run of one tile is the shortest way
@@ -141,39 +131,6 @@ __device__ __forceinline__ int run_tiles(const WeightsParams &p, int tiles) {
   return max((tiles + p.runs - 1) / p.runs, least);
 }
 
-// 16-byte asynchronous copy; zeros instead when !take.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool take, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
-               "l"(src), "r"(take ? 16 : 0), "l"(policy)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// d (16 x 8, fp32) += a (16 x 16, bf16) * b (16 x 8, bf16)
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Shared memory of one warp: a ring of tiles (kRows tokens of K, then of V),
 // and as many places for the query rows of the sequences in flight.
 template <int D, int G>
@@ -183,13 +140,6 @@ struct WarpSmem {
   static constexpr int kQ = G * D * 2;
   static constexpr int bytes = kStages * (2 * kHalf + kQ);
 };
-
-// Byte offset of 16-byte column c of row r in a tile of rows of D values: the
-// columns of eight consecutive rows are spread over the banks.
-template <int D>
-__device__ __forceinline__ uint32_t tile_at(int r, int c) {
-  return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
-}
 
 // First launch.  A warp is by itself: it streams the K and V of its run, for its
 // kv head, through its own ring with cp.async, up to two tiles ahead and across

@@ -16,8 +16,10 @@
 // can be updated in place: nothing is written before everybody has read.
 #include <cooperative_groups.h>
 
+#include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
+#include "warp_mma.cuh"
 
 namespace pkv {
 namespace {
@@ -55,39 +57,6 @@ __device__ __forceinline__ int saturated(int64_t x) {
   return x > 0x7FFFFFFF ? 0x7FFFFFFF : (int)x;
 }
 
-// Exclusive prefix sums of N values per thread over the CTA, and their totals.
-template <int N>
-__device__ __forceinline__ void scan_cta(int64_t (&x)[N], int64_t (&total)[N],
-                                         int64_t (*warp_sums)[N]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int64_t incl[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    incl[i] = x[i];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl[i], o);
-      if (lane >= o) incl[i] += y;
-    }
-    if (lane == 31) warp_sums[warp][i] = incl[i];
-  }
-  __syncthreads();
-  // Every warp adds up the warps' sums by itself.
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    int64_t y = lane < warps ? warp_sums[lane][i] : 0;
-    int64_t mine = lane < warp ? y : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      y += __shfl_xor_sync(0xffffffffu, y, o);
-      mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    }
-    total[i] = y;
-    x[i] = mine + incl[i] - x[i];
-  }
-  __syncthreads();
-}
-
 // A sequence's lengths, checked.
 struct PlanSeq {
   int L;       // tokens held (0 if the length given does not fit the table)
@@ -120,17 +89,6 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s, bool tel
   q.need = q.out || q.n == 0 ? 0 : (int)(((int64_t)q.L + q.n + bs1) >> p.block_shift) - q.have;
   if (tell && bad) flag_status(p.status, bad);
   return q;
-}
-
-// The sequence of row t: the last s with first[s] <= t (t < first[S]).
-__device__ __forceinline__ int seq_of_row(const int *first, int S, int t) {
-  int lo = 0, hi = S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
@@ -269,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
       slot[i] = -1;
       pos[i] = 0;
       if (t >= rows || t >= p.num_rows) continue;
-      if (s < 0) s = seq_of_row(first_row, S, (int)t);
+      if (s < 0) s = seq_of(first_row, S, (int)t);
       else while (first_row[s + 1] <= t) ++s, lb = -1;
       const int h = held[s];
       const int L = h < 0 ? -1 - h : h;
