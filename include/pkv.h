@@ -572,7 +572,7 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  * with shared_blocks of 0, is attended like any other sequence.  pkv_bm_prefix_groups
  * finds groups.
  * fp32 logits and statistics; for the product with V alone the weights are taken as the
- * sum of two bf16 (off by 2^-18 of a weight).  How the work is split depends on the
+ * sum of two bf16 (off by 2^-17 of a weight).  How the work is split depends on the
  * batch, and with it the last bits; the same call gives the same bits.
  *
  * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its row of out
@@ -588,7 +588,7 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  *
  * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
  *
- * Four launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
+ * Three launches.  Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8};
  * block_size in {64, 128, 256, 512}; num_seqs <= 8192, 1 <= num_groups <= num_seqs
  * (else PKV_ERR_INVALID_ARG); at most 4096 kv heads; max_blocks_per_seq * block_size at
  * most 2^20.

@@ -11,15 +11,15 @@
 // decode.  All parts (M, l, o) of a row are then joined:
 //   out = sum_i exp(M_i - M) o_i / sum_i exp(M_i - M) l_i.
 //
-// Four launches, each a programmatic dependent of the one before:
+// Three launches, each a programmatic dependent of the one before:
 //  1. plan: one CTA.  A group's prefix ends where its shortest sequence does; prefix
 //     sums of the work of groups (steps of 64 keys) and of sequences (tiles of 4 KiB
-//     of K) go to the workspace.
-//  2. tails: all sequences' own tokens, cut into runs of equal length, a warp for each
-//     run and kv head (m16n8k16, cp.async; bound by HBM).
-//  3. prefixes: units of (group, kv head, 256 rows) by steps, cut into runs of equal
-//     length, a CTA for each (tcgen05, TMA).
-//  4. join.
+//     of K) go to the workspace, and how many CTAs work on prefixes.
+//  2. attention: one CTA per SM.  Some of them take the prefixes, units of (group, kv
+//     head, 256 rows) by steps, cut into runs of equal cost, a CTA for each (tcgen05,
+//     TMA); the others the tails, all sequences' own tokens, cut into runs of equal
+//     length, a warp for each run and kv head (m16n8k16, cp.async; bound by HBM).
+//  3. join.
 #include <math.h>
 
 #include "cta_scan.cuh"
@@ -36,18 +36,18 @@ constexpr int kPlanThreads = 1024;
 constexpr int kWarpsMost = 8;            // warps per CTA of the tails (one CTA per SM)
 constexpr int kStages = 3;               // ring of tiles per warp
 constexpr int kMaxWarps = 4096;          // warps of the tails' grid at most (places for parts)
-constexpr int kMaxCtas = 512;            // CTAs of the prefixes' grid at most (places for parts)
+constexpr int kMaxCtas = 512;            // CTAs of the attention's grid at most (places for parts)
+constexpr int kThreads = 384;            // of the attention's CTAs
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 constexpr int BM = 128;                  // rows of a product
 constexpr int BN = 64;                   // keys of a step
 constexpr int kPairRows = 2 * BM;        // rows of a unit: two products share its keys
 constexpr int kUnitSlots = 4;
-constexpr int kJoinThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The prefix of a group, in the workspace.
 struct GroupPlan {
-  int64_t step0;  // steps of the groups before it
+  int64_t cost0;  // cost of the groups before it
   int start;      // its first sequence
   int lead;       // the sequence whose row of the block tables is read
   int members;
@@ -55,10 +55,27 @@ struct GroupPlan {
   int pairs;      // units of one kv head
   int pad;
 };
+// The cost of a step, in kCostNs: of a unit with two row tiles 4 (its products), of one
+// with a single row tile 3 (its loads).  A kv head's units follow one another.
+__device__ __forceinline__ int step_cost(int rows) { return rows > BM ? 4 : 3; }
+__device__ __forceinline__ int head_cost(const GroupPlan &g, int group_size) {  // of all its units' steps
+  const int rows = g.members * group_size, last = rows % kPairRows;
+  return rows / kPairRows * 4 + (last == 0 ? 0 : step_cost(last));
+}
+
+// A sequence's tail, in the workspace.
+struct SeqPlan {
+  int tile0;  // tiles of the tails before it
+  int begin;  // its first token
+  int len;    // tokens of the sequence (0: no output)
+  int group;
+};
 
 struct Totals {
-  int64_t steps;  // of all prefixes
-  int64_t tiles;  // of all tails
+  int64_t cost;     // of all prefixes
+  int64_t tiles;    // of all tails
+  int prefix_ctas;  // CTAs that take the prefixes; the others take the tails
+  int pad;
 };
 
 struct SharedParams {
@@ -71,11 +88,8 @@ struct SharedParams {
   const int32_t *group_starts;
   const int32_t *shared_blocks;
   Totals *totals;
-  GroupPlan *groups;   // [num_groups + 1] (the last one: step0 alone)
-  int32_t *tile0;      // [num_seqs + 1]: first tile of each sequence's tail
-  int32_t *begin;      // [num_seqs]: first token of it
-  int32_t *len;        // [num_seqs]: tokens of the sequence (0: no output)
-  int32_t *group_of;   // [num_seqs]
+  GroupPlan *groups;   // [num_groups]
+  SeqPlan *seqs;       // [num_seqs]
   float *tail_ml;      // [num_seqs + runs, Hkv, G, 2]   (max in log2 units, sum)
   float *tail_o;       // [num_seqs + runs, Hkv, G, D]
   float *first_ml;     // [num_seqs, Hq, 2]: a unit's first part
@@ -90,8 +104,8 @@ struct SharedParams {
   int group_size;      // G
   int block_shift;
   int max_blocks_per_seq;
-  int runs;            // runs of the tails' tiles at most
-  int ctas;            // runs of the prefixes' steps at most
+  int ctas;            // of the attention's grid
+  int tail_warps;      // warps of a CTA that takes tails
   float qscale;        // scale * log2(e)
 };
 
@@ -100,21 +114,36 @@ __host__ __device__ constexpr int tail_rows(int D) { return 2048 / D; }
 
 // Tiles per run of the tails; run r's part of sequence s is filed under s + r (a part
 // begins where a sequence or a run does, so no two have the same number).
-__device__ __forceinline__ int run_tiles(const SharedParams &p, int64_t tiles) {
-  const int64_t n = (tiles + p.runs - 1) / p.runs;
-  return n < 1 ? 1 : (int)n;
+__device__ __forceinline__ int run_tiles(const SharedParams &p, const Totals &t) {
+  const int runs = max((p.ctas - t.prefix_ctas) * p.tail_warps / p.num_kv_heads, 1);
+  return max((int)((t.tiles + runs - 1) / runs), 1);
 }
-// Steps per run of the prefixes.
-__device__ __forceinline__ int64_t run_steps(const SharedParams &p, int64_t steps) {
-  const int64_t n = (steps + p.ctas - 1) / p.ctas;
-  return n < 1 ? 1 : n;
+// Cost per run of the prefixes (at least that of the dearest step).
+__device__ __forceinline__ int64_t run_cost(const Totals &t) {
+  const int n = max(t.prefix_ctas, 1);
+  return max((t.cost + n - 1) / n, (int64_t)4);
 }
 
 // ----------------------------------------------------------------------- 1. plan
 
+// How many of the CTAs take the prefixes: what lets both kinds end together.  Times in
+// nanoseconds, as measured: of a unit of cost, and the beginning and end of a run; of a
+// tile of a tail (K and V of tail_rows tokens, a kv head) for all of a CTA's warps, and
+// of their beginning.
+constexpr int kCostNs = 310, kPrefixNs = 6000, kTileNs = 140, kTailNs = 2500;
+
+__device__ __forceinline__ int64_t time_with(const SharedParams &p, int64_t cost, int64_t tiles, int n) {
+  const int64_t prefix = cost == 0 ? 0 : n == 0 ? INT64_MAX : (cost + n - 1) / n * kCostNs + kPrefixNs;
+  const int rest = p.ctas - n;
+  const int64_t work = tiles * p.num_kv_heads * kTileNs;
+  const int64_t tails = tiles == 0 ? 0 : rest == 0 ? INT64_MAX : work / rest + kTailNs;
+  return prefix > tails ? prefix : tails;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, int D) {
   extern __shared__ int plan_smem[];
-  __shared__ int64_t sums[32][1];
+  __shared__ int64_t sums[32][2];
+  __shared__ unsigned long long best;
   const int S = p.num_seqs, N = p.num_groups, tid = threadIdx.x;
   int *starts = plan_smem;       // [N + 1]
   int *eff = starts + N + 1;     // [N]: blocks that the group shares
@@ -122,6 +151,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   int *count = lead + N;         // [N]: its sequences with tokens
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  auto tokens = [&](int L) { return L <= 0 ? 0 : (int)min((int64_t)L, room); };
+  const int first_L = tid < S ? p.context_lens[tid] : 0;  // (asked for ahead)
   bool ok = true;
   for (int g = tid; g <= N; g += blockDim.x) {
     const int x = p.group_starts[g];
@@ -135,20 +167,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       count[g] = 0;
     }
   }
+  if (tid == 0) best = ~0ull;
   __syncthreads();
   for (int g = tid; g < N; g += blockDim.x) ok = ok && starts[g] <= starts[g + 1];
   ok = __syncthreads_and(ok) != 0;
   // (no groups then: every sequence by itself)
   if (!ok && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
-  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
-  auto tokens = [&](int s) {
-    const int L = p.context_lens[s];
-    return L <= 0 ? 0 : (int)min((int64_t)L, room);
-  };
   if (ok) {
     for (int s0 = tid & ~31; s0 < S; s0 += blockDim.x) {
       const int s = s0 + (tid & 31);
-      const int L = s < S ? tokens(s) : 0;
+      const int L = s < S ? tokens(s == tid ? first_L : p.context_lens[s]) : 0;
       const int g = s < S ? seq_of(starts, N, s) : -1;
       // (a warp's sequences are neighbours: mostly one group)
       const unsigned peers = __match_any_sync(0xffffffffu, L > 0 ? g : -1 - (tid & 31));
@@ -163,67 +191,62 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     }
   }
   __syncthreads();
-  {
-    const int per = (N + blockDim.x - 1) / (int)blockDim.x;
-    const int g0 = min(tid * per, N), g1 = min(g0 + per, N);
-    auto plan = [&](int g) {
-      GroupPlan x;
-      const int blocks = ok && count[g] >= 2 ? eff[g] : 0;
-      x.start = starts[g];
-      x.members = blocks > 0 ? starts[g + 1] - starts[g] : 0;
-      x.lead = blocks > 0 ? lead[g] : 0;
-      x.tiles = (int)(((int64_t)blocks << p.block_shift) / BN);
-      x.pairs = (x.members * p.group_size + kPairRows - 1) / kPairRows;
-      x.pad = 0;
-      x.step0 = 0;
-      return x;
-    };
-    int64_t at[1] = {0}, total[1];
-    for (int g = g0; g < g1; ++g) {
-      const GroupPlan x = plan(g);
-      at[0] += (int64_t)x.tiles * x.pairs * p.num_kv_heads;
-    }
-    scan_cta<1>(at, total, sums);
-    for (int g = g0; g < g1; ++g) {
-      GroupPlan x = plan(g);
-      x.step0 = at[0];
-      p.groups[g] = x;
-      at[0] += (int64_t)x.tiles * x.pairs * p.num_kv_heads;
-    }
-    if (tid == 0) {
-      p.groups[N].step0 = total[0];
-      p.totals->steps = total[0];
-    }
+  const int per_g = (N + blockDim.x - 1) / (int)blockDim.x;
+  const int g0 = min(tid * per_g, N), g1 = min(g0 + per_g, N);
+  auto plan = [&](int g) {
+    GroupPlan x;
+    const int blocks = ok && count[g] >= 2 ? eff[g] : 0;
+    x.start = starts[g];
+    x.members = blocks > 0 ? starts[g + 1] - starts[g] : 0;
+    x.lead = blocks > 0 ? lead[g] : 0;
+    x.tiles = (int)(((int64_t)blocks << p.block_shift) / BN);
+    x.pairs = (x.members * p.group_size + kPairRows - 1) / kPairRows;
+    x.pad = 0;
+    x.cost0 = 0;
+    return x;
+  };
+  auto cost_of = [&](const GroupPlan &x) {
+    return (int64_t)x.tiles * head_cost(x, p.group_size) * p.num_kv_heads;
+  };
+  const int rows = tail_rows(D);
+  const int per = (S + blockDim.x - 1) / (int)blockDim.x;
+  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  auto first = [&](int s, int L, int &g) {
+    g = ok ? seq_of(starts, N, s) : 0;
+    return L > 0 && ok && count[g] >= 2 ? eff[g] << p.block_shift : 0;
+  };
+  int64_t at[2] = {0, 0}, total[2];
+  for (int g = g0; g < g1; ++g) at[0] += cost_of(plan(g));
+  for (int s = s0; s < s1; ++s) {
+    int g;
+    const int L0 = per == 1 ? first_L : p.context_lens[s], L = tokens(L0);
+    at[1] += (L - first(s, L, g) + rows - 1) / rows;
+    if (L != L0 || L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
   }
-  {
-    const int rows = tail_rows(D);
-    const int per = (S + blockDim.x - 1) / (int)blockDim.x;
-    const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
-    auto first = [&](int s, int L, int &g) {
-      g = ok ? seq_of(starts, N, s) : 0;
-      return L > 0 && ok && count[g] >= 2 ? eff[g] << p.block_shift : 0;
-    };
-    int64_t at[1] = {0}, total[1];
-    for (int s = s0; s < s1; ++s) {
-      int g;
-      const int L = tokens(s);
-      at[0] += (L - first(s, L, g) + rows - 1) / rows;
-      if (L != p.context_lens[s] || L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
-    }
-    scan_cta<1>(at, total, sums);
-    for (int s = s0; s < s1; ++s) {
-      int g;
-      const int L = tokens(s), b = first(s, L, g);
-      p.tile0[s] = (int)at[0];
-      p.begin[s] = b;
-      p.len[s] = L;
-      p.group_of[s] = g;
-      at[0] += (L - b + rows - 1) / rows;
-    }
-    if (tid == 0) {
-      p.tile0[S] = (int)total[0];
-      p.totals->tiles = total[0];
-    }
+  scan_cta<2>(at, total, sums);
+  for (int g = g0; g < g1; ++g) {
+    GroupPlan x = plan(g);
+    x.cost0 = at[0];
+    p.groups[g] = x;
+    at[0] += cost_of(x);
+  }
+  for (int s = s0; s < s1; ++s) {
+    int g;
+    const int L = tokens(per == 1 ? first_L : p.context_lens[s]), b = first(s, L, g);
+    *reinterpret_cast<int4 *>(p.seqs + s) = make_int4((int)at[1], b, L, g);
+    at[1] += (L - b + rows - 1) / rows;
+  }
+  // The best of all splits, the one with the fewest CTAs on prefixes among equals.
+  for (int n = tid; n <= p.ctas; n += blockDim.x) {
+    const int64_t t = time_with(p, total[0], total[1], n);
+    const unsigned long long key = (unsigned long long)min(t, (int64_t)1 << 50) << 12 | (unsigned)n;
+    atomicMin(&best, key);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.totals->cost = total[0];
+    p.totals->tiles = total[1];
+    p.totals->prefix_ctas = (int)(best & 0xFFF);
   }
 }
 
@@ -248,15 +271,14 @@ struct WarpSmem {
 // fp32).  With at most four heads columns 4 to 7 repeat the heads of 0 to 3 and take the
 // second parts; eight heads need a second product.
 template <int D, int G>
-__global__ void __launch_bounds__(kWarpsMost * 32, 1) shared_tails_kernel(const SharedParams p) {
+__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, uint8_t *smem_raw) {
   using W = WarpSmem<D, G>;
   constexpr int kRows = W::kRows;
   constexpr int kCols = D / 8;              // 16-byte columns per row
   constexpr int kRowsPer = 32 / kCols;      // rows per warp-wide copy
   constexpr int kSlices = kRows / 16;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = blockDim.x >> 5;
+  const int warps = p.tail_warps;
   uint8_t *mine = smem_raw + warp * W::bytes;
   const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
   int *tile0 = reinterpret_cast<int *>(smem_raw + warps * W::bytes);  // [S + 1]
@@ -265,24 +287,23 @@ __global__ void __launch_bounds__(kWarpsMost * 32, 1) shared_tails_kernel(const 
   const uint32_t tiles = smem_u32(mine);
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int s = threadIdx.x; s <= S; s += blockDim.x) {
-    tile0[s] = __ldcg(p.tile0 + s);
-    if (s < S) {
-      begin[s] = __ldcg(p.begin + s);
-      len[s] = __ldcg(p.len + s);
-    }
+  for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
+    tile0[s] = x.x;
+    begin[s] = x.y;
+    len[s] = x.z;
   }
+  if (threadIdx.x == 0) tile0[S] = (int)sum.tiles;
   __syncthreads();
+  if (warp >= warps) return;
   const int total = tile0[S];
-  const int per_run = run_tiles(p, total);
+  const int per_run = run_tiles(p, sum);
   const int runs = (total + per_run - 1) / per_run;
   const int64_t jobs = (int64_t)runs * Hkv;  // (run, head), heads innermost
   const uint64_t policy = l2_policy_evict_first();
   const int col = lane % kCols, row0 = lane / kCols;
-  for (int64_t job = (int64_t)blockIdx.x * warps + warp; job < jobs;
-       job += (int64_t)gridDim.x * warps) {
+  for (int64_t job = (int64_t)(blockIdx.x - sum.prefix_ctas) * warps + warp; job < jobs;
+       job += (int64_t)(p.ctas - sum.prefix_ctas) * warps) {
     const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
     const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
 
@@ -506,7 +527,7 @@ template <int D>
 struct PrefixLayout {
   static constexpr int kQBytes = BM * D * 2;
   static constexpr int kKVBytes = BN * D * 2;
-  static constexpr int kSlots0 = (kMaxDynamicSmem - 3072 - 2 * kQBytes) / kKVBytes;
+  static constexpr int kSlots0 = (kMaxDynamicSmem - 6144 - 2 * kQBytes) / kKVBytes;
   static constexpr int kSlots = kSlots0 < 16 ? kSlots0 : 16;
   static constexpr int kKStages = kSlots * 2 / 5;  // (a V slot is held longer)
   static constexpr int kVStages = kSlots - kKStages;
@@ -515,19 +536,23 @@ struct PrefixLayout {
   static constexpr int v = k + kKStages * kKVBytes;
   static constexpr int bars = v + kVStages * kKVBytes;
   // q_full, q_empty, k_full[SK], v_full[SV], k_empty[SK], v_empty[SV], s_full[2][2],
-  // p_full[2][2], p_free[2][2], o_free[2], unit_full[U], unit_empty[U], drain
-  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 14 + 2 * kUnitSlots + 1;
+  // p_full[2][2], p_free[2][2], o_free[2], unit_full[U], unit_empty[U], ex_full, drain
+  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 14 + 2 * kUnitSlots + 2;
   static constexpr int misc = bars + kNumBars * 8;  // tensor memory address, abort flag
   static constexpr int ring = misc + 8;
-  static constexpr int total = ring + (int)sizeof(Piece) * kUnitSlots;
+  static constexpr int ex = ring + (int)sizeof(Piece) * kUnitSlots;  // [2][2][128] (max, sum)
+  static constexpr int total = ex + 4 * BM * 8;
   // One CTA per SM (it takes all of tensor memory): more than half of an SM's shared
   // memory, so that a second one never waits for tensor memory.
   static_assert(total + 1024 <= kMaxDynamicSmem && total > 114 * 1024, "shared memory");
 };
 
-// Tensor memory columns (lane = row): O of the two row tiles at 0 and D, then two S
+// There are two chains of S, softmax and P.V.  A piece of more than 128 rows has a row
+// tile for each, and both see every step; of one row tile they take the steps in turn
+// and add up at its end, so that the softmax of two steps is in flight either way.
+// Tensor memory columns (lane = row): O of the two chains at 0 and D, then two S
 // buffers of 64 columns for each.  A buffer holds S (fp32), then over it P as two bf16
-// terms, 32 columns each: the weights' roundings and what those leave.
+// terms, 32 columns each: the weight cut to bf16, and what that leaves.
 template <int D>
 struct PrefixCols {
   static constexpr uint32_t kS = 2 * D;
@@ -538,25 +563,33 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void store32(float *ptr, const float (&v)[64], int i) {
+__device__ __forceinline__ void store32(float *ptr, const float (&v)[32], int i) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(ptr), "f"(v[i]),
                "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]),
                "f"(v[i + 6]), "f"(v[i + 7])
                : "memory");
 }
 
+// Steps [0, n) of a piece that chain h takes.
+__device__ __forceinline__ int chain_steps(const Piece &u, int h) {
+  return u.rows > BM ? u.n : (u.n + 1 - h) >> 1;
+}
+
+// Two bf16 cut (not rounded) from two floats, packed; the floats that they are.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 template <int D>
-__global__ void __launch_bounds__(384, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
-                         const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
+__device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                         const CUtensorMap &tm_v, const SharedParams &p,
+                                         const Totals &sum, uint8_t *smem_raw) {
   using L = PrefixLayout<D>;
   constexpr int XR = D / 64;  // 128-byte swizzle regions across D
   constexpr int kKStages = L::kKStages, kVStages = L::kVStages;
   constexpr uint32_t kSCol = PrefixCols<D>::kS;
   constexpr int kKWarp = 0, kSWarp = 1, kVWarp = 2, kPVWarp = 3;
 
-  extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sQ = smem + L::q, *sK = smem + L::k, *sV = smem + L::v;
@@ -573,23 +606,19 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t *o_free = p_free + 4;            // [row tile]: O has been read
   uint64_t *unit_full = o_free + 2;
   uint64_t *unit_empty = unit_full + kUnitSlots;
-  uint64_t *drain = unit_empty + kUnitSlots;
+  uint64_t *ex_full = unit_empty + kUnitSlots;  // every softmax warp's (max, sum) of a piece
+  uint64_t *drain = ex_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::misc + 4);
   Piece *ring = reinterpret_cast<Piece *>(smem + L::ring);  // start < 0 ends
 
+  float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The plan is there: the kernel before began after it, and this one after that.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t steps = __ldcg(&p.totals->steps);
-  const int64_t len = run_steps(p, steps);
+  const int64_t len = run_cost(sum);
   const int64_t x0 = (int64_t)blockIdx.x * len;
-  if (x0 >= steps) {
-    // (The launch must not end before the one before it has: the join waits for this one.)
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  const int64_t x1 = x0 + len < steps ? x0 + len : steps;
+  if (x0 >= sum.cost) return;
+  const int64_t x1 = x0 + len < sum.cost ? x0 + len : sum.cost;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -607,24 +636,33 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&p_full[i], 128);
       mbar_init(&p_free[i], 1);
     }
-    mbar_init(&o_free[0], 4);
-    mbar_init(&o_free[1], 4);
+    mbar_init(&o_free[0], 8);  // every softmax warp, or a chain's own four twice
+    mbar_init(&o_free[1], 8);
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
       mbar_init(&unit_empty[i], 1 + 2 + 8);  // V loader, issuers, softmax warps
     }
+    mbar_init(ex_full, 8);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
   }
-  if (warp == kSWarp) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
   __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  // (the loaders go ahead; the others wait for tensor memory)
+  uint32_t tmem = 0;
+  if (warp != kKWarp && warp != kVWarp) {
+    if (warp == kSWarp) {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    named_bar_sync(1, kThreads - 64);
+    tc_fence_after_sync();
+    tmem = *tmem_slot;
+  }
 
   auto next_piece = [&](int &iu, Piece &u) -> bool {
     const int slot = iu % kUnitSlots;
@@ -647,27 +685,25 @@ __global__ void __launch_bounds__(384, 1)
     const int nst = is_k ? kKStages : kVStages;
     int iu = 0, g = 0, q_loads = 0;
     bool ok = true;
-    if (lane == 0) {
-      if (is_k) tma_prefetch_map(&tm_q);
-      tma_prefetch_map(map);
-    }
     int64_t x = x0;
     int grp = 0;
     GroupPlan gp = {};
-    int64_t gp_end = -1;  // steps up to the end of the group in gp
+    int64_t per_head = 1;
+    int64_t gp_end = -1;  // cost up to the end of the group in gp
     for (;;) {
       Piece u;
       bool have;
       if (is_k) {
-        have = x < x1;
-        if (have) {
+        // The run has the steps that begin in [x0, x1).
+        have = false;
+        while (x < x1) {
           if (x >= gp_end) {
-            // The group of step x: the last one that begins at it or before.
+            // The group at x: the last one that begins there or before.
             int lo = grp, hi = p.num_groups;
             while (hi - lo > 1) {
               const int stride = (hi - lo + 31) / 32;
               const int at = lo + lane * stride;
-              const bool before = at < hi && __ldcg(&p.groups[at].step0) <= x;
+              const bool before = at < hi && __ldcg(&p.groups[at].cost0) <= x;
               const int k = __popc(__ballot_sync(0xffffffffu, before));
               const int from = lo + (k - 1) * stride;
               hi = min(hi, from + stride);
@@ -676,28 +712,33 @@ __global__ void __launch_bounds__(384, 1)
             grp = lo;
             const int4 *src = reinterpret_cast<const int4 *>(p.groups + grp);
             const int4 a = __ldcg(src), b = __ldcg(src + 1);
-            gp.step0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
+            gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
             gp.start = a.z;
             gp.lead = a.w;
             gp.members = b.x;
             gp.tiles = b.y;
-            gp.pairs = b.z;
-            gp_end = gp.step0 + (int64_t)gp.tiles * gp.pairs * p.num_kv_heads;
+            per_head = (int64_t)gp.tiles * head_cost(gp, p.group_size);
+            gp_end = gp.cost0 + per_head * p.num_kv_heads;
           }
-          const int64_t in = x - gp.step0;
-          const int unit = (int)(in / gp.tiles);
-          u.tile = (int)(in - (int64_t)unit * gp.tiles);
-          u.n = (int)min((int64_t)(gp.tiles - u.tile), x1 - x);
-          u.kvh = unit / gp.pairs;
-          u.pair = unit - u.kvh * gp.pairs;
+          u.kvh = (int)((x - gp.cost0) / per_head);
+          const int64_t head0 = gp.cost0 + u.kvh * per_head;
+          u.pair = (int)((x - head0) / (4 * (int64_t)gp.tiles));
+          const int64_t unit0 = head0 + (int64_t)u.pair * 4 * gp.tiles;
           u.rows = min(kPairRows, gp.members * p.group_size - u.pair * kPairRows);
+          const int each = step_cost(u.rows);
+          u.tile = (int)((x - unit0 + each - 1) / each);
+          const int end = (int)min((int64_t)gp.tiles, (x1 - unit0 + each - 1) / each);
+          u.n = end - u.tile;
           u.start = gp.start;
           u.lead = gp.lead;
           u.first = u.tile == 0;
-          x += u.n;
-        } else {
-          u.start = -1;
+          x = unit0 + (int64_t)end * each;
+          if (u.n > 0) {
+            have = true;
+            break;
+          }
         }
+        if (!have) u.start = -1;
         const int slot = iu % kUnitSlots;
         if (iu >= kUnitSlots)
           ok = warp_wait(&unit_empty[slot], ((iu / kUnitSlots) - 1) & 1, abort_flag);
@@ -717,9 +758,9 @@ __global__ void __launch_bounds__(384, 1)
           if (iu >= 2) ok = mbar_wait_bounded(q_empty, (iu - 2) & 1, abort_flag);
           if (ok) {
             ++q_loads;
-            const int tiles = u.rows > BM ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, tiles * L::kQBytes);
-            for (int h = 0; h < tiles; ++h)
+            const int each = u.rows > BM ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, each * L::kQBytes);
+            for (int h = 0; h < each; ++h)
               for (int xr = 0; xr < XR; ++xr)
                 tma_load_3d(sQ + h * L::kQBytes + xr * BM * 128, &tm_q, q_full, xr * 64,
                             u.kvh * p.group_size,
@@ -758,8 +799,8 @@ __global__ void __launch_bounds__(384, 1)
           flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else if (warp == kSWarp || warp == kPVWarp) {
-    // Issuers: warp 1 S = Q K^T, warp 3 O += P V.  gh[h]: steps of row tile h so far,
-    // uh[h]: pieces (the second row tile takes no part in pieces of up to 128 rows).
+    // Issuers: warp 1 S = Q K^T, warp 3 O += P V.  gh[h]: steps of chain h so far, uh[h]:
+    // pieces of which it had any.
     int iu = 0, g = 0;
     int gh[2] = {0, 0}, uh[2] = {0, 0};
     bool ok = true;
@@ -769,7 +810,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
       while (ok && next_piece(iu, u)) {
-        const int nh = u.rows > BM ? 2 : 1;
+        const bool both = u.rows > BM;
         if (lane == 0) {
           ok = mbar_wait_bounded(q_full, (iu - 1) & 1, abort_flag);
           for (int i = 0; i < u.n && ok; ++i, ++g) {
@@ -778,8 +819,9 @@ __global__ void __launch_bounds__(384, 1)
             const uint64_t dk_st = dk + (uint64_t)((st * L::kKVBytes) >> 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (h >= nh || !ok) break;
-              const int gt = gh[h] + i, b = gt & 1;
+              if (!ok) break;
+              if (!both && h != (i & 1)) continue;
+              const int gt = gh[h] + (both ? i : i >> 1), b = gt & 1;
               if (gt >= 2)
                 ok = mbar_wait_bounded(&p_free[2 * h + b], ((gt - 2) >> 1) & 1, abort_flag);
               if (!ok) break;
@@ -788,7 +830,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk & 3) * 32;
-                umma_bf16(d, dq + (uint64_t)((h * L::kQBytes + (kk / 4) * BM * 128 + off) >> 4),
+                umma_bf16(d, dq + (uint64_t)(((both ? h * L::kQBytes : 0) + (kk / 4) * BM * 128 + off) >> 4),
                           dk_st + (uint64_t)(((kk / 4) * BN * 128 + off) >> 4), idesc_s,
                           kk > 0 ? 1u : 0u);
               }
@@ -800,14 +842,14 @@ __global__ void __launch_bounds__(384, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         g = __shfl_sync(0xffffffffu, g, 0);
-        gh[0] += u.n;
-        if (nh == 2) gh[1] += u.n;
+        gh[0] += chain_steps(u, 0);
+        gh[1] += chain_steps(u, 1);
       }
     } else {
       constexpr uint32_t idesc_o = umma_idesc_bf16(BM, D, false, true);
       const uint64_t dv = umma_desc_sw128(smem_u32(sV), BN * 128, 1024);
       while (ok && next_piece(iu, u)) {
-        const int nh = u.rows > BM ? 2 : 1;
+        const bool both = u.rows > BM;
         if (lane == 0) {
           for (int i = 0; i < u.n && ok; ++i, ++g) {
             const int st = g % kVStages;
@@ -815,10 +857,12 @@ __global__ void __launch_bounds__(384, 1)
             const uint64_t dv_st = dv + (uint64_t)((st * L::kKVBytes) >> 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (h >= nh || !ok) break;
-              const int gt = gh[h] + i, b = gt & 1;
+              if (!ok) break;
+              if (!both && h != (i & 1)) continue;
+              const int ih = both ? i : i >> 1;  // the chain's own number of the step
+              const int gt = gh[h] + ih, b = gt & 1;
               ok = mbar_wait_bounded(&p_full[2 * h + b], (gt >> 1) & 1, abort_flag);
-              if (ok && i == 0 && uh[h] >= 1)
+              if (ok && ih == 0 && uh[h] >= 1)
                 ok = mbar_wait_bounded(&o_free[h], (uh[h] - 1) & 1, abort_flag);
               if (!ok) break;
               tc_fence_after_sync();
@@ -828,7 +872,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int kk = 0; kk < BN / 8; ++kk)
                 umma_bf16_tmem_a(tmem + h * D, pa + kk * 8,
                                  dv_st + (uint64_t)(((kk % (BN / 16)) * 16 * 128) >> 4), idesc_o,
-                                 (i > 0 || kk > 0) ? 1u : 0u);
+                                 (ih > 0 || kk > 0) ? 1u : 0u);
               umma_commit(&p_free[2 * h + b]);
             }
             if (ok) umma_commit(&v_empty[st]);
@@ -836,9 +880,10 @@ __global__ void __launch_bounds__(384, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         g = __shfl_sync(0xffffffffu, g, 0);
-        for (int h = 0; h < nh; ++h) {
-          gh[h] += u.n;
-          ++uh[h];
+        for (int h = 0; h < 2; ++h) {
+          const int n = chain_steps(u, h);
+          gh[h] += n;
+          uh[h] += n > 0 ? 1 : 0;
         }
       }
     }
@@ -848,56 +893,28 @@ __global__ void __launch_bounds__(384, 1)
       if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
     }
   } else {
-    // Softmax: four warps per row tile, a thread per row (tile 0: warps 4, 5, 10, 11).
+    // Softmax: four warps per chain, a thread per row (chain 0: warps 4, 5, 10, 11).
     const int h = (((warp - 4) >> 1) ^ ((warp - 4) >> 2)) & 1;
     const int quarter = warp & 3;   // tensor memory lanes this warp may access
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const float qs = p.qscale;
-    int iu = 0, gt = 0;
+    const int Hq = p.num_kv_heads * p.group_size;
+    int iu = 0, turn = 0;
+    int gh[2] = {0, 0};  // steps of the chains before this piece
     bool ok = true;
     Piece u;
-    // A piece's (max, sum, O) as a part, once its last P.V (step g_last) is in O; run
-    // after the next piece's first P is published, which that wait then overlaps.
-    auto write_part = [&](const Piece &e, float m_e, float l_e, int g_last) -> bool {
-      if (!warp_wait(&p_free[2 * h + (g_last & 1)], (g_last >> 1) & 1, abort_flag)) return false;
-      tc_fence_after_sync();
-      const int r = h * BM + row;
-      const int Hq = p.num_kv_heads * p.group_size;
-      const int idx = e.pair * kPairRows + r;  // of the group's rows
-      const int64_t at = e.first ? (int64_t)(e.start + idx / p.group_size) * Hq +
-                                       e.kvh * p.group_size + idx % p.group_size
-                                 : (int64_t)blockIdx.x * kPairRows + r;
-      float *o = (e.first ? p.first_o : p.run_o) + at * D;
-#pragma unroll 1
-      for (int half = 0; half < D / 64; ++half) {
-        float ov[64];
-        tmem_load64(tmem + lane_base + h * D + half * 64, ov);
-        if (r < e.rows) {
-#pragma unroll
-          for (int i = 0; i < 64; i += 8) store32(o + half * 64 + i, ov, i);
-        }
-      }
-      if (r < e.rows)
-        reinterpret_cast<float2 *>(e.first ? p.first_ml : p.run_ml)[at] = make_float2(m_e, l_e);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[h]);
-      return true;
-    };
-    bool pending = false;
-    Piece e;
-    float e_m = 0.f, e_l = 0.f;
-    int e_g = 0;
     while (ok && next_piece(iu, u)) {
-      if (h == 1 && u.rows <= BM) continue;
+      const bool both = u.rows > BM;
+      const int n = chain_steps(u, h);
       // A warp whose rows all lie behind the piece's skips the arithmetic.
-      const bool live = h * BM + quarter * 32 < u.rows;
+      const int row0 = both ? h * BM : 0;
+      const bool live = row0 + quarter * 32 < u.rows;
       // Running max in log2 units, raised (and O rescaled) only when a step's exceeds it
       // by more than 8: P stays <= 2^8, and l and O share the reference.
       float m_ref = -INFINITY, l_run = 0.f;
-      for (int i = 0; i < u.n && ok; ++i, ++gt) {
-        const int b = gt & 1;
+      for (int i = 0; i < n && ok; ++i) {
+        const int gt = gh[h] + i, b = gt & 1;
         const uint32_t sp = tmem + lane_base + kSCol + (2 * h + b) * BN;
         ok = warp_wait(&s_full[2 * h + b], (gt >> 1) & 1, abort_flag);
         if (!ok) break;
@@ -934,12 +951,15 @@ __global__ void __launch_bounds__(384, 1)
               const float2 p23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
               r01 = __fadd2_rn(r01, p01);
               r23 = __fadd2_rn(r23, p23);
-              const uint32_t h01 = pack_bf16x2(p01.x, p01.y), h23 = pack_bf16x2(p23.x, p23.y);
+              const uint32_t h01 = cut_bf16x2(p01.x, p01.y), h23 = cut_bf16x2(p23.x, p23.y);
               const int w = (c - hf * 32) / 2;
               hi[w] = __uint_as_float(h01);
               hi[w + 1] = __uint_as_float(h23);
-              lo[w] = __uint_as_float(pack_bf16x2(p01.x - bf16lo(h01), p01.y - bf16hi(h01)));
-              lo[w + 1] = __uint_as_float(pack_bf16x2(p23.x - bf16lo(h23), p23.y - bf16hi(h23)));
+              // (what the cut leaves, exact in fp32, is rounded: 2^-17 of the weight)
+              const float2 d01 = __fadd2_rn(p01, make_float2(-bf16lo(h01), -bf16hi(h01)));
+              const float2 d23 = __fadd2_rn(p23, make_float2(-bf16lo(h23), -bf16hi(h23)));
+              lo[w] = __uint_as_float(pack_bf16x2(d01.x, d01.y));
+              lo[w + 1] = __uint_as_float(pack_bf16x2(d23.x, d23.y));
             }
             tmem_store16_async(sp + hf * 16, hi);
             tmem_store16_async(sp + 32 + hf * 16, lo);
@@ -948,8 +968,8 @@ __global__ void __launch_bounds__(384, 1)
           rs = (r01.x + r01.y) + (r23.x + r23.y);
         }
         if (live && i > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
-          // O is rescaled once the last P.V has landed in it (the next waits for this
-          // step's P).
+          // O is rescaled once the chain's last P.V has landed in it (the next waits for
+          // this step's P).
           ok = warp_wait(&p_free[2 * h + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after_sync();
@@ -966,19 +986,81 @@ __global__ void __launch_bounds__(384, 1)
         l_run = l_run * alpha + rs;
         tc_fence_before_sync();
         mbar_arrive(&p_full[2 * h + b]);
-        if (pending) {
-          pending = false;
-          ok = write_part(e, e_m, e_l, e_g);
-        }
       }
       if (!ok) break;
-      pending = true;
-      e = u;
-      e_m = m_ref;
-      e_l = l_run;
-      e_g = gt - 1;
+
+      // The piece's (max, sum, O) as a part, once its last P.V are in O.  Their barriers
+      // cannot run ahead: a chain's next P.V waits until O has been read (o_free).
+      gh[0] += chain_steps(u, 0);
+      gh[1] += chain_steps(u, 1);
+      const int other = both ? 0 : chain_steps(u, 1 - h);
+      float a_mine = 1.f, a_other = 0.f;
+      if (n > 0) {
+        const int gl = gh[h] - 1;
+        ok = warp_wait(&p_free[2 * h + (gl & 1)], (gl >> 1) & 1, abort_flag);
+        if (!ok) break;
+      }
+      if (!both) {
+        // Chains that took the steps in turn: the joint maximum, and a half of the dims for
+        // each to add up and write.
+        // (two places in turn: a warp may be at the next piece's end when another reads)
+        float2 *mine = ex + ((turn & 1) * 2 + h) * BM, *its = ex + ((turn & 1) * 2 + 1 - h) * BM;
+        mine[row] = make_float2(m_ref, l_run);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ex_full);
+        ok = warp_wait(ex_full, turn & 1, abort_flag);
+        if (!ok) break;
+        ++turn;
+        const float2 x = its[row];
+        const float M = fmaxf(m_ref, x.x), ref = M == -INFINITY ? 0.f : M;
+        a_mine = fast_exp2(m_ref - ref);
+        a_other = fast_exp2(x.x - ref);
+        l_run = l_run * a_mine + x.y * a_other;
+        m_ref = M;
+      }
+      // (the other chain's last P.V is in, too: its warps have waited for it)
+      tc_fence_after_sync();
+      const int r = row0 + row;
+      if (live) {
+        const int idx = u.pair * kPairRows + r;  // of the group's rows
+        const int64_t at = u.first ? (int64_t)(u.start + idx / p.group_size) * Hq +
+                                         u.kvh * p.group_size + idx % p.group_size
+                                   : (int64_t)blockIdx.x * kPairRows + r;
+        float *o = (u.first ? p.first_o : p.run_o) + at * D;
+        const int c0 = both ? 0 : h * (D / 2), c1 = both ? D : c0 + D / 2;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          float ov[32], v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+          if (n > 0) tmem_load32(tmem + lane_base + h * D + c, ov);
+          if (!both) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] *= a_mine;
+            if (other > 0) {
+              tmem_load32(tmem + lane_base + (1 - h) * D + c, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = fmaf(v[e], a_other, ov[e]);
+            }
+          }
+          if (r < u.rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store32(o + c + e, ov, e);
+          }
+        }
+        if (r < u.rows && (both || h == 0))
+          reinterpret_cast<float2 *>(u.first ? p.first_ml : p.run_ml)[at] = make_float2(m_ref, l_run);
+      }
+      // O has been read: of its own chain, or of both that had steps.
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (both || n > 0) mbar_arrive(&o_free[h]);
+        if (both) mbar_arrive(&o_free[h]);
+        if (!both && other > 0) mbar_arrive(&o_free[1 - h]);
+      }
     }
-    if (ok && pending) ok = write_part(e, e_m, e_l, e_g);
     tc_fence_before_sync();
   }
 
@@ -988,129 +1070,169 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The launch of both.
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  // (before any of tensor memory is taken, too: a kernel before the call may need it)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Totals sum;
+  sum.cost = __ldcg(&p.totals->cost);
+  sum.tiles = __ldcg(&p.totals->tiles);
+  sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
+  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, tm_v, p, sum, smem_raw);
+  else tails<D, G>(p, sum, smem_raw);
 }
 
 // ----------------------------------------------------------------------- 4. join
 
-// A CTA per (sequence, kv head).
+// Warps that share the parts of a row: as many as fill a CTA of eight, two at least.
+__host__ __device__ constexpr int join_warps(int G) { return G >= 4 ? 2 : 8 / G; }
+
+// A CTA per (sequence, kv head); a row's warps take its parts in turn, a lane four
+// (D = 64: two) of the D values.
 template <int D, int G>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
-  __shared__ float4 acc_s[kJoinThreads];
-  const int tid = threadIdx.x, lane = tid & 31;
+__global__ void __launch_bounds__(join_warps(G) * G * 32) shared_join_kernel(const SharedParams p) {
+  constexpr int kEach = D / 32, kShare = join_warps(G), kWarps = kShare * G;
+  constexpr int kAhead = 8;  // parts asked for at a time
+  __shared__ float acc_s[kWarps][D];
+  __shared__ float2 ml_s[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = warp / kShare, share = warp - g * kShare;
   const int Hkv = p.num_kv_heads, Hq = Hkv * G;
   const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int L = __ldcg(p.len + s);
-  if (L <= 0) return;
+  // (The plan is there: the launch before began after it, and this one after that.)
+  const int4 seq = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
+  Totals sum;
+  sum.cost = __ldcg(&p.totals->cost);
+  sum.tiles = __ldcg(&p.totals->tiles);
+  sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
+  GroupPlan gp;
+  {
+    const int4 *src = reinterpret_cast<const int4 *>(p.groups + seq.w);
+    const int4 a = __ldcg(src), b = __ldcg(src + 1);
+    gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
+    gp.start = a.z;
+    gp.members = b.x;
+    gp.tiles = b.y;
+  }
   // The parts of the tail: of runs r0, r0 + 1, ...
-  const int t0 = __ldcg(p.tile0 + s), t1 = __ldcg(p.tile0 + s + 1);
-  const GroupPlan gp = p.groups[__ldcg(p.group_of + s)];
-  const int64_t tiles = __ldcg(&p.totals->tiles), steps = __ldcg(&p.totals->steps);
+  const int t0 = seq.x, tiles = (seq.z - seq.y + tail_rows(D) - 1) / tail_rows(D);
   int n_tail = 0;
   int64_t tail_row = 0;
-  if (t1 > t0) {
-    const int per_run = run_tiles(p, tiles);
+  if (tiles > 0) {
+    const int per_run = run_tiles(p, sum);
     const int r0 = t0 / per_run;
-    n_tail = (t1 - 1) / per_run - r0 + 1;
-    tail_row = ((int64_t)(s + r0) * Hkv + j) * G;
+    n_tail = (t0 + tiles - 1) / per_run - r0 + 1;
+    tail_row = ((int64_t)(s + r0) * Hkv + j) * G + g;
   }
-  // Those of the prefix: of the unit that has the sequence's rows.
+  // Those of the prefix: of the unit that has the row, its first step's and of the runs
+  // behind that one.
   int n_pre = 0;
-  int64_t first_row = 0, run_row = 0;
+  int64_t run_row = 0;
+  const int64_t first_row = (int64_t)s * Hq + j * G + g;
   if (gp.tiles > 0) {
-    const int64_t len = run_steps(p, steps);
-    const int idx = (s - gp.start) * G;
-    const int64_t u0 = gp.step0 + (int64_t)(j * gp.pairs + idx / kPairRows) * gp.tiles;
-    const int64_t c0 = u0 / len;
-    n_pre = (int)((u0 + gp.tiles - 1) / len - c0 + 1);
-    first_row = (int64_t)s * Hq + j * G;
+    const int64_t len = run_cost(sum);
+    const int idx = (s - gp.start) * G + g, pair = idx / kPairRows;
+    const int64_t unit0 = gp.cost0 + ((int64_t)j * head_cost(gp, G) + 4 * pair) * gp.tiles;
+    const int each = step_cost(gp.members * G - pair * kPairRows);
+    const int64_t c0 = unit0 / len;
+    n_pre = (int)((unit0 + (int64_t)(gp.tiles - 1) * each) / len - c0 + 1);
     run_row = c0 * kPairRows + idx % kPairRows;
   }
   const int n = n_tail + n_pre;
-  // Row (of its kind's arrays) of part i, head 0.
-  auto row_of = [&](int i, const float *&ml, const float *&o) -> int64_t {
-    if (i < n_tail) {
-      ml = p.tail_ml;
-      o = p.tail_o;
-      return tail_row + (int64_t)i * Hkv * G;
-    }
-    i -= n_tail;
-    ml = i == 0 ? p.first_ml : p.run_ml;
-    o = i == 0 ? p.first_o : p.run_o;
-    return i == 0 ? first_row : run_row + (int64_t)i * kPairRows;
-  };
-  // Maximum and sum of every head: lane (part, head) of every warp alike.
-  float M[G], inv[G];
-  {
-    const int g = lane % G;
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane / G; i < n; i += 32 / G) {
-      const float *ml, *o;
-      const int64_t at = row_of(i, ml, o) + g;
-      const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml) + at);
-      const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
-      l = l * fast_exp2(m - ref) + x.y * fast_exp2(x.x - ref);
-      m = mn;
-    }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (seq.z <= 0) return;
+  // A warp's parts: 32 of their maxima at a time, a lane each.
+  float m = -INFINITY, l = 0.f;
+  float acc[kEach];
 #pragma unroll
-    for (int k = G; k < 32; k <<= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, k);
-      const float l2 = __shfl_xor_sync(0xffffffffu, l, k);
-      const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
-      l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
-      m = mn;
+  for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+  for (int base = share; base < n; base += 32 * kShare) {
+    int i = base + lane * kShare;
+    const int count = min(32, (n - base + kShare - 1) / kShare);
+    float2 x = make_float2(-INFINITY, 0.f);
+    const float *o = p.tail_o;
+    if (i < n) {  // part i: its row of its kind's arrays
+      const float *ml = p.tail_ml;
+      int64_t at = tail_row + (int64_t)i * Hkv * G;
+      i -= n_tail;
+      if (i >= 0) {
+        ml = i == 0 ? p.first_ml : p.run_ml;
+        o = i == 0 ? p.first_o : p.run_o;
+        at = i == 0 ? first_row : run_row + (int64_t)i * kPairRows;
+      }
+      x = __ldcg(reinterpret_cast<const float2 *>(ml) + at);
+      o += at * D;
     }
-    l = 1.f / l;
+    float mn = x.x;
 #pragma unroll
-    for (int x = 0; x < G; ++x) {
-      M[x] = __shfl_sync(0xffffffffu, m, x);
-      inv[x] = __shfl_sync(0xffffffffu, l, x);
+    for (int k = 16; k > 0; k >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, k));
+    mn = fmaxf(mn, m);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float old = fast_exp2(m - ref), w = fast_exp2(x.x - ref);
+    float lw = x.y * w;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, k);
+    l = l * old + lw;
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] *= old;
+    for (int k0 = 0; k0 < count; k0 += kAhead) {
+      float y[kAhead][kEach];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float *from = reinterpret_cast<const float *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + u) & 31));
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) y[u][e] = 0.f;
+        if (k0 + u < count) {
+          if constexpr (kEach == 4)
+            *reinterpret_cast<float4 *>(y[u]) = __ldcg(reinterpret_cast<const float4 *>(from) + lane);
+          else
+            *reinterpret_cast<float2 *>(y[u]) = __ldcg(reinterpret_cast<const float2 *>(from) + lane);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + u) & 31);
+        if (k0 + u < count) {
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) acc[e] = fmaf(wk, y[u][e], acc[e]);
+        }
+      }
     }
   }
-  // The D * G values, four at a time; several threads of a CTA share the parts of each.
-  constexpr int kQuads = D * G / 4;
-  for (int qb = 0; qb < kQuads; qb += kJoinThreads) {
-    const int width = min(kQuads - qb, kJoinThreads);
-    const int lanes = kJoinThreads / width;
-    const int quad = qb + tid % width, mine = tid / width;
-    const int g = quad / (D / 4), d = quad % (D / 4);
-    float Mg = M[0], ig = inv[0];
+  // The sums of a row's warps.
+  if (lane == 0) ml_s[warp] = make_float2(m, l);
 #pragma unroll
-    for (int x = 1; x < G; ++x)
-      if (g == x) {
-        Mg = M[x];
-        ig = inv[x];
-      }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = mine; i < n; i += lanes) {
-      const float *ml, *o;
-      const int64_t at = row_of(i, ml, o) + g;
-      const float4 y = __ldcg(reinterpret_cast<const float4 *>(o) + at * (D / 4) + d);
-      const float m = __ldcg(ml + 2 * at);
-      // (a part without weight: its maximum is -inf, and the joined one may be, too)
-      const float w = m == -INFINITY ? 0.f : fast_exp2(m - Mg);
-      acc.x = fmaf(w, y.x, acc.x);
-      acc.y = fmaf(w, y.y, acc.y);
-      acc.z = fmaf(w, y.z, acc.z);
-      acc.w = fmaf(w, y.w, acc.w);
+  for (int e = 0; e < kEach; ++e) acc_s[warp][lane * kEach + e] = acc[e];
+  __syncthreads();
+  constexpr int kPairs = D / 2;  // of values, to a thread each
+  for (int x = threadIdx.x; x < G * kPairs; x += kWarps * 32) {
+    const int row = x / kPairs, d = (x - row * kPairs) * 2;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) M = fmaxf(M, ml_s[row * kShare + w].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float total = 0.f, v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) {
+      const float2 y = ml_s[row * kShare + w];
+      const float a = fast_exp2(y.x - ref);
+      total = fmaf(y.y, a, total);
+      v0 = fmaf(acc_s[row * kShare + w][d], a, v0);
+      v1 = fmaf(acc_s[row * kShare + w][d + 1], a, v1);
     }
-    __syncthreads();
-    acc_s[tid] = acc;
-    __syncthreads();
-    if (tid < width) {
-      for (int k = 1; k < lanes; ++k) {
-        const float4 y = acc_s[k * width + tid];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-      }
-      uint2 w;
-      w.x = pack_bf16x2(acc.x * ig, acc.y * ig);
-      w.y = pack_bf16x2(acc.z * ig, acc.w * ig);
-      *reinterpret_cast<uint2 *>(p.out + (((int64_t)s * Hq + j * G + g) * D + d * 4)) = w;
-    }
+    const float inv = 1.f / total;
+    *reinterpret_cast<uint32_t *>(p.out + ((int64_t)s * Hq + j * G + row) * D + d) =
+        pack_bf16x2(v0 * inv, v1 * inv);
   }
 }
 
@@ -1119,17 +1241,13 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Workspace {
-  size_t totals, groups, tile0, begin, len, group_of, tail_ml, tail_o, first_ml, first_o, run_ml,
-      run_o, total;
+  size_t totals, groups, seqs, tail_ml, tail_o, first_ml, first_o, run_ml, run_o, total;
   Workspace(int64_t S, int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
     const int64_t parts = S * Hq + (kMaxWarps + Hkv) * (Hq / Hkv);  // (num_seqs + runs) of each head
     totals = 0;
     groups = 256;
-    tile0 = groups + align256((size_t)(N + 1) * sizeof(GroupPlan));
-    begin = tile0 + align256((size_t)(S + 1) * 4);
-    len = begin + align256((size_t)S * 4);
-    group_of = len + align256((size_t)S * 4);
-    tail_ml = group_of + align256((size_t)S * 4);
+    seqs = groups + align256((size_t)N * sizeof(GroupPlan));
+    tail_ml = seqs + align256((size_t)S * sizeof(SeqPlan));
     tail_o = tail_ml + align256((size_t)parts * 8);
     first_ml = tail_o + align256((size_t)(parts * D) * 4);
     first_o = first_ml + align256((size_t)(S * Hq) * 8);
@@ -1167,40 +1285,32 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   int warps = (kMaxDynamicSmem - 1024 - seq_smem) / WarpSmem<D, G>::bytes;
   if (warps > kWarpsMost) warps = kWarpsMost;
   static_assert((kMaxDynamicSmem - 1024 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
-  const int tails_smem = warps * WarpSmem<D, G>::bytes + seq_smem;
-  const int prefix_smem = PrefixLayout<D>::total + 1024;
+  int smem = warps * WarpSmem<D, G>::bytes + seq_smem;
+  if (smem < PrefixLayout<D>::total + 1024) smem = PrefixLayout<D>::total + 1024;
   if (!kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr) ||
-      !kernel_smem_setup((const void *)shared_tails_kernel<D, G>, warps * 32, tails_smem, nullptr) ||
-      !kernel_smem_setup((const void *)shared_prefix_kernel<D>, 384, prefix_smem, nullptr))
+      !kernel_smem_setup((const void *)shared_attn_kernel<D, G>, kThreads, smem, nullptr))
     return PKV_ERR_CUDA;
-  // As many runs as give every warp of the GPU one of a kv head, and no more than the
-  // longest possible batch has tiles.
-  int64_t all = (int64_t)sms * warps;
-  if (all > kMaxWarps) all = kMaxWarps;
-  int64_t runs = all / prm.num_kv_heads;
+  // A CTA per SM, and no more than the longest possible batch has work for: a warp per
+  // tile and kv head, a CTA per step of the prefixes.  (Two at least: one of a kind.)
   const int rows = tail_rows(D);
-  const int64_t tiles = (int64_t)S * ((room + rows - 1) / rows);
-  if (runs > tiles) runs = tiles;
-  if (runs < 1) runs = 1;
-  prm.runs = (int)runs;
-  int64_t grid = (runs * prm.num_kv_heads + warps - 1) / warps;
-  if (grid > sms) grid = sms;
+  const int64_t tiles = (int64_t)S * ((room + rows - 1) / rows) * prm.num_kv_heads;
   const int64_t pairs = (int64_t)S * G / kPairRows + (S + 1) / 2;  // of a kv head, at most
-  int64_t steps = pairs * prm.num_kv_heads * (room / BN);
-  int64_t ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  if (ctas > steps) ctas = steps;
+  const int64_t steps = pairs * prm.num_kv_heads * (room / BN);
+  int64_t ctas = (tiles + warps - 1) / warps + steps;
+  if (ctas > sms) ctas = sms;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (ctas * warps > kMaxWarps) ctas = kMaxWarps / warps;
+  if (ctas < 2) ctas = 2;
   prm.ctas = (int)ctas;
+  prm.tail_warps = warps;
   cudaError_t err = launch_dependent<SharedParams, int>(shared_plan_kernel, 1, kPlanThreads,
                                                         plan_smem, stream, prm, D);
   if (err == cudaSuccess)
-    err = launch_dependent<SharedParams>(shared_tails_kernel<D, G>, (unsigned)grid, warps * 32,
-                                         tails_smem, stream, prm);
-  if (err == cudaSuccess)
     err = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, SharedParams>(
-        shared_prefix_kernel<D>, (unsigned)ctas, 384, prefix_smem, stream, tq, tk, tv, prm);
+        shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, tv, prm);
   if (err == cudaSuccess)
     err = launch_dependent<SharedParams>(shared_join_kernel<D, G>, (unsigned)(S * prm.num_kv_heads),
-                                         kJoinThreads, 0, stream, prm);
+                                         join_warps(G) * G * 32, 0, stream, prm);
   return launch_status();  // (any launch's error, which it clears)
 }
 
@@ -1263,10 +1373,7 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.shared_blocks = shared_blocks;
   prm.totals = reinterpret_cast<Totals *>(ws + lay.totals);
   prm.groups = reinterpret_cast<GroupPlan *>(ws + lay.groups);
-  prm.tile0 = reinterpret_cast<int32_t *>(ws + lay.tile0);
-  prm.begin = reinterpret_cast<int32_t *>(ws + lay.begin);
-  prm.len = reinterpret_cast<int32_t *>(ws + lay.len);
-  prm.group_of = reinterpret_cast<int32_t *>(ws + lay.group_of);
+  prm.seqs = reinterpret_cast<SeqPlan *>(ws + lay.seqs);
   prm.tail_ml = reinterpret_cast<float *>(ws + lay.tail_ml);
   prm.tail_o = reinterpret_cast<float *>(ws + lay.tail_o);
   prm.first_ml = reinterpret_cast<float *>(ws + lay.first_ml);
@@ -1281,8 +1388,8 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.group_size = G;
   prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
   prm.max_blocks_per_seq = max_blocks_per_seq;
-  prm.runs = 0;
   prm.ctas = 0;
+  prm.tail_warps = 0;
   prm.qscale = scale * kLog2e;
 
   // q as {D, Hq, S}: a box is 64 dims x the G heads of a kv head x 128 / G sequences.
