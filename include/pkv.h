@@ -567,10 +567,10 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  * result up to rounding.  Group g is the neighbouring sequences group_starts[g] ..
  * group_starts[g + 1] - 1 (group_starts int32 [num_groups + 1], from 0 to num_seqs);
  * the first shared_blocks[g] (int32 [num_groups]) entries of their rows of block_tables
- * are the same, and only those of its first sequence with a context are read there.  A
- * group uses no more of them than its shortest context fills; a group of one, or one
- * with shared_blocks of 0, is attended like any other sequence.  pkv_bm_prefix_groups
- * finds groups.
+ * are the same in all of them (any of the rows may be read).  A group uses no more of
+ * them than its shortest context fills; a group of one, or one with shared_blocks of 0,
+ * is attended like any other sequence, and so is every one where all contexts together
+ * are so short that reading them whole is faster.  pkv_bm_prefix_groups finds groups.
  * fp32 logits and statistics; for the product with V alone the weights are taken as the
  * sum of two bf16 (off by 2^-17 of a weight).  How the work is split depends on the
  * batch, and with it the last bits; the same call gives the same bits.
@@ -580,7 +580,8 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  * shared_blocks outside [0, max_blocks_per_seq] is flagged the same way and taken as the
  * nearer end.  group_starts that do not begin at 0, end at num_seqs or ever go back are
  * flagged (PKV_DEV_BAD_SEQLEN); every sequence is then attended by itself.  A block id
- * out of range is flagged and what its sequences get is undefined.
+ * out of range is flagged and what its sequences get is undefined.  A wait that runs out
+ * (PKV_DEV_TIMEOUT) leaves the rows of out undefined.
  *
  * workspace: device memory of at least pkv_decode_shared_workspace_size(...) bytes,
  * 256-byte aligned; it needs no initialisation.  Calls that overlap on the device must
@@ -599,6 +600,17 @@ pkv_status pkv_paged_decode_shared_attn(
     const int32_t *shared_blocks, int num_seqs, int num_groups, int num_q_heads,
     int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
     float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * test_shared_fault -- TEST-ONLY, for paged_decode_shared_attn: sets, for the current
+ * device, the wall-clock limit of every wait (default 1 s) and, for the process, how
+ * many CTAs load the prefixes that they work on (the others wait for theirs in vain,
+ * PKV_DEV_TIMEOUT; -1: all, the default), and whether prefixes are shared however
+ * little there is to read (0: where it pays, the default).  Restore with
+ * pkv_test_shared_fault(1000000000, -1, 0).  Synchronous.  Returns PKV_ERR_INVALID_ARG
+ * for wait_limit_ns <= 0 or loading_ctas < -1.
+ */
+pkv_status pkv_test_shared_fault(int64_t wait_limit_ns, int loading_ctas, int share_always);
 
 /*
  * w4a16_dequant -- W4A16-G128 weight dequantisation (s1nh.org post on

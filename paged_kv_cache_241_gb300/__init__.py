@@ -90,6 +90,7 @@ SIGNATURES = {
     "pkv_decode_shared_workspace_size": (_c_sz, [_c_int] * 5),
     "pkv_paged_decode_shared_attn": (_c_int, [_p] * 8 + [_c_int] * 7 + [_c_i64, _c_f, _p, _c_sz,
                                                                         _p, _p]),
+    "pkv_test_shared_fault": (_c_int, [_c_i64, _c_int, _c_int]),
     "pkv_w4a16_dequant": (_c_int, [_p, _p, _p, _c_i64, _c_i64, _c_int, _p]),
     "pkv_bm_create": (_p, [_c_int, _c_int]),
     "pkv_bm_destroy": (None, [_p]),
@@ -737,6 +738,14 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
         shared_blocks.data_ptr(), S, groups, Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
         workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     _check(st, "pkv_paged_decode_shared_attn")
+
+
+def test_shared_fault(wait_limit_ns: int, loading_ctas: int, share_always: int) -> None:
+    """TEST ONLY: shorten the wait limit of paged_decode_shared_attn on the current
+    device, let only the first `loading_ctas` CTAs load their prefixes (-1: all), and
+    share prefixes however short.  Restore with test_shared_fault(10**9, -1, 0)."""
+    _check(load().pkv_test_shared_fault(int(wait_limit_ns), int(loading_ctas), int(share_always)),
+           "test_shared_fault")
 
 
 def w4a16_dequant(out, packed, scales, group_size=128, stream=None) -> None:

@@ -22,6 +22,8 @@
 //  3. join.
 #include <math.h>
 
+#include <atomic>
+
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
@@ -43,6 +45,7 @@ constexpr int BM = 128;                  // rows of a product
 constexpr int BN = 64;                   // keys of a step
 constexpr int kPairRows = 2 * BM;        // rows of a unit: two products share its keys
 constexpr int kUnitSlots = 4;
+constexpr int kJoinWarps = 4;            // per CTA
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The prefix of a group, in the workspace.
@@ -56,11 +59,18 @@ struct GroupPlan {
   int pad;
 };
 // The cost of a step, in kCostNs: of a unit with two row tiles 4 (its products), of one
-// with a single row tile 3 (its loads).  A kv head's units follow one another.
+// with a single row tile 3 (its loads).  A unit's beginning costs kUnitCost ahead of its
+// steps (a run that goes through the end of one into the next drains its pipeline there);
+// a kv head's units follow one another.
+constexpr int kUnitCost = 14;
 __device__ __forceinline__ int step_cost(int rows) { return rows > BM ? 4 : 3; }
-__device__ __forceinline__ int head_cost(const GroupPlan &g, int group_size) {  // of all its units' steps
+__device__ __forceinline__ int64_t full_unit_cost(const GroupPlan &g) {  // of 256 rows
+  return kUnitCost + 4 * (int64_t)g.tiles;
+}
+__device__ __forceinline__ int64_t head_cost(const GroupPlan &g, int group_size) {
   const int rows = g.members * group_size, last = rows % kPairRows;
-  return rows / kPairRows * 4 + (last == 0 ? 0 : step_cost(last));
+  return rows / kPairRows * full_unit_cost(g) +
+         (last == 0 || g.tiles == 0 ? 0 : kUnitCost + (int64_t)step_cost(last) * g.tiles);
 }
 
 // A sequence's tail, in the workspace.
@@ -106,6 +116,8 @@ struct SharedParams {
   int max_blocks_per_seq;
   int ctas;            // of the attention's grid
   int tail_warps;      // warps of a CTA that takes tails
+  int loading;         // CTAs that load their prefixes: all, but in a test
+  int share_always;    // whatever it saves (test)
   float qscale;        // scale * log2(e)
 };
 
@@ -118,7 +130,8 @@ __device__ __forceinline__ int run_tiles(const SharedParams &p, const Totals &t)
   const int runs = max((p.ctas - t.prefix_ctas) * p.tail_warps / p.num_kv_heads, 1);
   return max((int)((t.tiles + runs - 1) / runs), 1);
 }
-// Cost per run of the prefixes (at least that of the dearest step).
+// Cost per run of the prefixes (at least that of the dearest step, so that every run
+// between a unit's first and last has a step of it).
 __device__ __forceinline__ int64_t run_cost(const Totals &t) {
   const int n = max(t.prefix_ctas, 1);
   return max((t.cost + n - 1) / n, (int64_t)4);
@@ -130,20 +143,21 @@ __device__ __forceinline__ int64_t run_cost(const Totals &t) {
 // nanoseconds, as measured: of a unit of cost, and the beginning and end of a run; of a
 // tile of a tail (K and V of tail_rows tokens, a kv head) for all of a CTA's warps, and
 // of their beginning.
-constexpr int kCostNs = 310, kPrefixNs = 6000, kTileNs = 140, kTailNs = 2500;
+constexpr int kCostNs = 320, kPrefixNs = 7000, kTailNs = 2500;
+// (eight heads take two products with V)
+__device__ __forceinline__ float tile_ns(int G) { return G == 8 ? 175.f : 145.f; }
 
-__device__ __forceinline__ int64_t time_with(const SharedParams &p, int64_t cost, int64_t tiles, int n) {
-  const int64_t prefix = cost == 0 ? 0 : n == 0 ? INT64_MAX : (cost + n - 1) / n * kCostNs + kPrefixNs;
+__device__ __forceinline__ float time_with(const SharedParams &p, float cost, float tiles, int n) {
   const int rest = p.ctas - n;
-  const int64_t work = tiles * p.num_kv_heads * kTileNs;
-  const int64_t tails = tiles == 0 ? 0 : rest == 0 ? INT64_MAX : work / rest + kTailNs;
-  return prefix > tails ? prefix : tails;
+  const float prefix = cost == 0.f ? 0.f : n == 0 ? INFINITY : __fdividef(cost * kCostNs, n) + kPrefixNs;
+  const float tails =
+      tiles == 0.f ? 0.f : rest == 0 ? INFINITY : __fdividef(tiles * p.num_kv_heads * tile_ns(p.group_size), rest) + kTailNs;
+  return fmaxf(prefix, tails);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, int D) {
   extern __shared__ int plan_smem[];
-  __shared__ int64_t sums[32][2];
-  __shared__ unsigned long long best;
+  __shared__ int64_t sums[32][3];
   const int S = p.num_seqs, N = p.num_groups, tid = threadIdx.x;
   int *starts = plan_smem;       // [N + 1]
   int *eff = starts + N + 1;     // [N]: blocks that the group shares
@@ -167,7 +181,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       count[g] = 0;
     }
   }
-  if (tid == 0) best = ~0ull;
   __syncthreads();
   for (int g = tid; g < N; g += blockDim.x) ok = ok && starts[g] <= starts[g + 1];
   ok = __syncthreads_and(ok) != 0;
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     return x;
   };
   auto cost_of = [&](const GroupPlan &x) {
-    return (int64_t)x.tiles * head_cost(x, p.group_size) * p.num_kv_heads;
+    return head_cost(x, p.group_size) * p.num_kv_heads;
   };
   const int rows = tail_rows(D);
   const int per = (S + blockDim.x - 1) / (int)blockDim.x;
@@ -215,15 +228,26 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     g = ok ? seq_of(starts, N, s) : 0;
     return L > 0 && ok && count[g] >= 2 ? eff[g] << p.block_shift : 0;
   };
-  int64_t at[2] = {0, 0}, total[2];
+  int64_t at[3] = {0, 0, 0}, total[3];  // cost, tiles of the tails; tiles without sharing
   for (int g = g0; g < g1; ++g) at[0] += cost_of(plan(g));
   for (int s = s0; s < s1; ++s) {
     int g;
     const int L0 = per == 1 ? first_L : p.context_lens[s], L = tokens(L0);
     at[1] += (L - first(s, L, g) + rows - 1) / rows;
+    at[2] += (L + rows - 1) / rows;
     if (L != L0 || L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
   }
-  scan_cta<2>(at, total, sums);
+  scan_cta<3>(at, total, sums);
+  // Little work: reading every context whole takes less than a run of a prefix at its
+  // best, and so nothing is shared.
+  if (!p.share_always &&
+      (float)total[2] * p.num_kv_heads * tile_ns(p.group_size) + (float)kTailNs * p.ctas <=
+          (float)total[0] * kCostNs + (float)kPrefixNs * p.ctas) {
+    ok = false;
+    at[0] = total[0] = 0;
+    at[1] = at[2];
+    total[1] = total[2];
+  }
   for (int g = g0; g < g1; ++g) {
     GroupPlan x = plan(g);
     x.cost0 = at[0];
@@ -236,17 +260,32 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     *reinterpret_cast<int4 *>(p.seqs + s) = make_int4((int)at[1], b, L, g);
     at[1] += (L - b + rows - 1) / rows;
   }
-  // The best of all splits, the one with the fewest CTAs on prefixes among equals.
-  for (int n = tid; n <= p.ctas; n += blockDim.x) {
-    const int64_t t = time_with(p, total[0], total[1], n);
-    const unsigned long long key = (unsigned long long)min(t, (int64_t)1 << 50) << 12 | (unsigned)n;
-    atomicMin(&best, key);
-  }
-  __syncthreads();
-  if (tid == 0) {
-    p.totals->cost = total[0];
-    p.totals->tiles = total[1];
-    p.totals->prefix_ctas = (int)(best & 0xFFF);
+  // The best of all splits, the one with the fewest CTAs on prefixes among equals.  (With
+  // work of both kinds there are two CTAs, so some split has a time.)
+  if (tid < 32) {
+    float best = INFINITY;
+    int best_n = 0;
+    for (int n = tid; n <= p.ctas; n += 32) {
+      const float t = time_with(p, (float)total[0], (float)total[1], n);
+      if (t < best) {
+        best = t;
+        best_n = n;
+      }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, best, k);
+      const int n = __shfl_xor_sync(0xffffffffu, best_n, k);
+      if (t < best || (t == best && n < best_n)) {
+        best = t;
+        best_n = n;
+      }
+    }
+    if (tid == 0) {
+      p.totals->cost = total[0];
+      p.totals->tiles = total[1];
+      p.totals->prefix_ctas = best_n;
+    }
   }
 }
 
@@ -529,7 +568,7 @@ struct PrefixLayout {
   static constexpr int kKVBytes = BN * D * 2;
   static constexpr int kSlots0 = (kMaxDynamicSmem - 6144 - 2 * kQBytes) / kKVBytes;
   static constexpr int kSlots = kSlots0 < 16 ? kSlots0 : 16;
-  static constexpr int kKStages = kSlots * 2 / 5;  // (a V slot is held longer)
+  static constexpr int kKStages = (kSlots * 2 + 2) / 5;  // (a V slot is held longer)
   static constexpr int kVStages = kSlots - kKStages;
   static constexpr int q = 0;
   static constexpr int k = q + 2 * kQBytes;
@@ -582,8 +621,8 @@ __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
 
 template <int D>
 __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                         const CUtensorMap &tm_v, const SharedParams &p,
-                                         const Totals &sum, uint8_t *smem_raw) {
+                                         const SharedParams &p, const Totals &sum,
+                                         const int4 (&near)[2], uint8_t *smem_raw) {
   using L = PrefixLayout<D>;
   constexpr int XR = D / 64;  // 128-byte swizzle regions across D
   constexpr int kKStages = L::kKStages, kVStages = L::kVStages;
@@ -648,7 +687,6 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     fence_barrier_init();
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_k);
-    tma_prefetch_map(&tm_v);
   }
   __syncthreads();
   // (the loaders go ahead; the others wait for tensor memory)
@@ -674,15 +712,9 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     return u.start >= 0;
   };
 
-  if (warp == kKWarp || warp == kVWarp) {
-    // Loaders: warp 0 walks the run (handing its pieces to the other roles) and loads Q
-    // and K, warp 2 loads V.
-    const bool is_k = warp == kKWarp;
-    uint64_t *full = is_k ? k_full : v_full;
-    uint64_t *empty = is_k ? k_empty : v_empty;
-    uint8_t *slots = is_k ? sK : sV;
-    const CUtensorMap *map = is_k ? &tm_k : &tm_v;
-    const int nst = is_k ? kKStages : kVStages;
+  if (warp == kKWarp) {
+    // Warp 0 walks the run (handing its pieces to the other roles) and loads Q and K.
+    const bool loads = (int)blockIdx.x < p.loading;
     int iu = 0, g = 0, q_loads = 0;
     bool ok = true;
     int64_t x = x0;
@@ -692,13 +724,23 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     int64_t gp_end = -1;  // cost up to the end of the group in gp
     for (;;) {
       Piece u;
-      bool have;
-      if (is_k) {
-        // The run has the steps that begin in [x0, x1).
-        have = false;
-        while (x < x1) {
-          if (x >= gp_end) {
-            // The group at x: the last one that begins there or before.
+      // The run has the steps that begin in [x0, x1).
+      bool have = false;
+      while (x < x1) {
+        if (x >= gp_end) {
+          // The group at x: the last one that begins there or before.
+          int4 a, b;
+          if (p.num_groups <= 32) {
+            const int64_t at = (int64_t)(uint32_t)near[0].x | ((int64_t)near[0].y << 32);
+            const unsigned before = __ballot_sync(0xffffffffu, lane < p.num_groups && at <= x);
+            const int from = 31 - __clz((int)before);
+            a.x = __shfl_sync(0xffffffffu, near[0].x, from);
+            a.y = __shfl_sync(0xffffffffu, near[0].y, from);
+            a.z = __shfl_sync(0xffffffffu, near[0].z, from);
+            a.w = __shfl_sync(0xffffffffu, near[0].w, from);
+            b.x = __shfl_sync(0xffffffffu, near[1].x, from);
+            b.y = __shfl_sync(0xffffffffu, near[1].y, from);
+          } else {
             int lo = grp, hi = p.num_groups;
             while (hi - lo > 1) {
               const int stride = (hi - lo + 31) / 32;
@@ -710,80 +752,79 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
               lo = from;
             }
             grp = lo;
-            const int4 *src = reinterpret_cast<const int4 *>(p.groups + grp);
-            const int4 a = __ldcg(src), b = __ldcg(src + 1);
-            gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
-            gp.start = a.z;
-            gp.lead = a.w;
-            gp.members = b.x;
-            gp.tiles = b.y;
-            per_head = (int64_t)gp.tiles * head_cost(gp, p.group_size);
-            gp_end = gp.cost0 + per_head * p.num_kv_heads;
+            a = __ldcg(reinterpret_cast<const int4 *>(p.groups + grp));
+            b = __ldcg(reinterpret_cast<const int4 *>(p.groups + grp) + 1);
           }
-          u.kvh = (int)((x - gp.cost0) / per_head);
-          const int64_t head0 = gp.cost0 + u.kvh * per_head;
-          u.pair = (int)((x - head0) / (4 * (int64_t)gp.tiles));
-          const int64_t unit0 = head0 + (int64_t)u.pair * 4 * gp.tiles;
-          u.rows = min(kPairRows, gp.members * p.group_size - u.pair * kPairRows);
-          const int each = step_cost(u.rows);
-          u.tile = (int)((x - unit0 + each - 1) / each);
-          const int end = (int)min((int64_t)gp.tiles, (x1 - unit0 + each - 1) / each);
-          u.n = end - u.tile;
-          u.start = gp.start;
-          u.lead = gp.lead;
-          u.first = u.tile == 0;
-          x = unit0 + (int64_t)end * each;
-          if (u.n > 0) {
-            have = true;
-            break;
-          }
+          gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
+          gp.start = a.z;
+          gp.lead = a.w;
+          gp.members = b.x;
+          gp.tiles = b.y;
+          per_head = head_cost(gp, p.group_size);
+          gp_end = gp.cost0 + per_head * p.num_kv_heads;
         }
-        if (!have) u.start = -1;
-        const int slot = iu % kUnitSlots;
-        if (iu >= kUnitSlots)
-          ok = warp_wait(&unit_empty[slot], ((iu / kUnitSlots) - 1) & 1, abort_flag);
-        if (!ok) break;
-        if (lane == 0) {
-          ring[slot] = u;
-          mbar_arrive(&unit_full[slot]);  // (release: orders the stores above)
+        u.kvh = (int)((x - gp.cost0) / per_head);
+        const int64_t head0 = gp.cost0 + u.kvh * per_head;
+        u.pair = (int)((x - head0) / full_unit_cost(gp));
+        const int64_t step0 = head0 + u.pair * full_unit_cost(gp) + kUnitCost;
+        u.rows = min(kPairRows, gp.members * p.group_size - u.pair * kPairRows);
+        const int each = step_cost(u.rows);
+        u.tile = x <= step0 ? 0 : (int)((x - step0 + each - 1) / each);
+        const int end = x1 <= step0 ? 0 : (int)min((int64_t)gp.tiles, (x1 - step0 + each - 1) / each);
+        u.n = end - u.tile;
+        u.start = gp.start;
+        u.lead = gp.lead;
+        u.first = u.tile == 0;
+        x = step0 + (int64_t)end * each;
+        if (u.n > 0) {
+          have = true;
+          break;
         }
-        ++iu;
-      } else {
-        have = next_piece(iu, u);
       }
-      if (!have) break;
+      if (!have) u.start = -1;
+      const int slot = iu % kUnitSlots;
+      if (iu >= kUnitSlots)
+        ok = warp_wait(&unit_empty[slot], ((iu / kUnitSlots) - 1) & 1, abort_flag);
+      if (!ok) break;
       if (lane == 0) {
-        if (is_k) {
-          // Q of this piece once the last one's S products are done with it.
-          if (iu >= 2) ok = mbar_wait_bounded(q_empty, (iu - 2) & 1, abort_flag);
-          if (ok) {
-            ++q_loads;
-            const int each = u.rows > BM ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, each * L::kQBytes);
-            for (int h = 0; h < each; ++h)
-              for (int xr = 0; xr < XR; ++xr)
-                tma_load_3d(sQ + h * L::kQBytes + xr * BM * 128, &tm_q, q_full, xr * 64,
-                            u.kvh * p.group_size,
-                            u.start + (u.pair * kPairRows + h * BM) / p.group_size);
-          }
-        }
+        ring[slot] = u;
+        mbar_arrive(&unit_full[slot]);  // (release: orders the stores above)
+      }
+      ++iu;
+      if (!have || !loads) break;
+      if (lane == 0) {
         const int32_t *row = p.block_tables + (int64_t)u.lead * p.max_blocks_per_seq;
+        int blk = row[u.tile * BN >> p.block_shift];  // (asked for ahead of Q)
+        // Q of this piece once the last one's S products are done with it.
+        if (iu >= 2) ok = mbar_wait_bounded(q_empty, (iu - 2) & 1, abort_flag);
+        if (ok) {
+          ++q_loads;
+          const int each = u.rows > BM ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, each * L::kQBytes);
+          for (int h = 0; h < each; ++h)
+            for (int xr = 0; xr < XR; ++xr)
+              tma_load_3d(sQ + h * L::kQBytes + xr * BM * 128, &tm_q, q_full, xr * 64,
+                          u.kvh * p.group_size,
+                          u.start + (u.pair * kPairRows + h * BM) / p.group_size);
+        }
         for (int i = 0; i < u.n && ok; ++i, ++g) {
-          const int st = g % nst;
-          if (g >= nst && !mbar_wait_bounded(&empty[st], ((g / nst) - 1) & 1, abort_flag)) {
+          const int st = g % kKStages;
+          if (g >= kKStages && !mbar_wait_bounded(&k_empty[st], ((g / kKStages) - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           const int key0 = (u.tile + i) * BN;
-          int blk = row[key0 >> p.block_shift];
-          if (blk < 0 || (int64_t)blk >= p.num_blocks) {
+          const int off = key0 & ((1 << p.block_shift) - 1);
+          if (i > 0 && off == 0) blk = row[key0 >> p.block_shift];
+          int from = blk;
+          if (from < 0 || (int64_t)from >= p.num_blocks) {
             flag_status(p.status, PKV_DEV_BAD_BLOCK);
-            blk = 0;
+            from = 0;
           }
-          mbar_arrive_expect_tx(&full[st], L::kKVBytes);
+          mbar_arrive_expect_tx(&k_full[st], L::kKVBytes);
           for (int xr = 0; xr < XR; ++xr)
-            tma_load_4d(slots + st * L::kKVBytes + xr * BN * 128, map, &full[st], xr * 64, u.kvh,
-                        key0 & ((1 << p.block_shift) - 1), blk);
+            tma_load_4d(sK + st * L::kKVBytes + xr * BN * 128, &tm_k, &k_full[st], xr * 64, u.kvh,
+                        off, from);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -792,12 +833,61 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     }
     if (lane == 0) {
       // Do not leave while copies into this CTA's shared memory are in flight.
-      if (is_k && q_loads > 0 && !mbar_wait_bounded(q_full, (q_loads - 1) & 1, nullptr))
+      if (q_loads > 0 && !mbar_wait_bounded(q_full, (q_loads - 1) & 1, nullptr))
         flag_status(p.status, PKV_DEV_TIMEOUT);
-      for (int i = max(0, g - nst); i < g; ++i)
-        if (!mbar_wait_bounded(&full[i % nst], (i / nst) & 1, nullptr))
+      for (int i = max(0, g - kKStages); i < g; ++i)
+        if (!mbar_wait_bounded(&k_full[i % kKStages], (i / kKStages) & 1, nullptr))
           flag_status(p.status, PKV_DEV_TIMEOUT);
     }
+  } else if (warp == kVWarp) {
+    // Warp 2 copies V with cp.async, a second load path beside the SM's TMA unit, in the
+    // swizzle that TMA would write.  Copies of up to kAhead steps are in flight; a step's
+    // are made visible to the tensor cores' proxy and published when they are in.
+    constexpr int kAhead = kVStages - 2;
+    constexpr int kChunks = D / 8;          // 16-byte chunks of a row
+    constexpr int kRowsPer = 32 / kChunks;  // rows per warp-wide copy
+    const int col = lane % kChunks, row0 = lane / kChunks;
+    const uint64_t policy = l2_policy_evict_normal();
+    int iu = 0, g = 0, published = 0;
+    bool ok = true;
+    Piece u;
+    auto publish = [&]() {  // the oldest step that is not, whose copies are in
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[published % kVStages]);
+      ++published;
+    };
+    while (ok && next_piece(iu, u)) {
+      const int32_t *row = p.block_tables + (int64_t)u.lead * p.max_blocks_per_seq;
+      int blk = row[u.tile * BN >> p.block_shift];
+      for (int i = 0; i < u.n; ++i, ++g) {
+        const int st = g % kVStages;
+        if (g >= kVStages) ok = warp_wait(&v_empty[st], ((g / kVStages) - 1) & 1, abort_flag);
+        if (!ok) break;
+        const int key0 = (u.tile + i) * BN;
+        const int off = key0 & ((1 << p.block_shift) - 1);
+        if (i > 0 && off == 0) blk = row[key0 >> p.block_shift];
+        const int64_t from = blk < 0 || (int64_t)blk >= p.num_blocks ? 0 : blk;  // (flagged by warp 0)
+        const uint16_t *src =
+            p.v_cache + ((((from << p.block_shift) + off + row0) * p.num_kv_heads + u.kvh) * D + col * 8);
+        const int64_t step = (int64_t)kRowsPer * p.num_kv_heads * D;
+        const uint32_t dst = smem_u32(sV) + st * L::kKVBytes + (col >> 3) * BN * 128;
+#pragma unroll 8
+        for (int r = 0; r < BN / kRowsPer; ++r) {
+          const int at = row0 + r * kRowsPer;
+          copy16(dst + at * 128 + (((col & 7) ^ (at & 7)) << 4), src + r * step, true, policy);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (g - published >= kAhead) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+          publish();
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok)
+        while (published < g) publish();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == kSWarp || warp == kPVWarp) {
     // Issuers: warp 1 S = Q K^T, warp 3 O += P V.  gh[h]: steps of chain h so far, uh[h]:
     // pieces of which it had any.
@@ -1027,6 +1117,8 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
         const int64_t at = u.first ? (int64_t)(u.start + idx / p.group_size) * Hq +
                                          u.kvh * p.group_size + idx % p.group_size
                                    : (int64_t)blockIdx.x * kPairRows + r;
+        // (eight dims of a row at a time: the same with eight dims of all rows together,
+        // whose stores fill whole lines, ended a piece 0.5 us sooner and the join 1.5 later)
         float *o = (u.first ? p.first_o : p.run_o) + at * D;
         const int c0 = both ? 0 : h * (D / 2), c1 = both ? D : c0 + D / 2;
 #pragma unroll 1
@@ -1076,37 +1168,42 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
-                       const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
+                       const __grid_constant__ CUtensorMap tm_k, const SharedParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   // (before any of tensor memory is taken, too: a kernel before the call may need it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (the first 32 groups' plans are asked for beside the totals)
+  const int lane = threadIdx.x & 31;
+  int4 near[2] = {};
+  if (threadIdx.x < 32 && lane < p.num_groups) {
+    near[0] = __ldcg(reinterpret_cast<const int4 *>(p.groups + lane));
+    near[1] = __ldcg(reinterpret_cast<const int4 *>(p.groups + lane) + 1);
+  }
   Totals sum;
   sum.cost = __ldcg(&p.totals->cost);
   sum.tiles = __ldcg(&p.totals->tiles);
   sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
-  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, tm_v, p, sum, smem_raw);
+  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, p, sum, near, smem_raw);
   else tails<D, G>(p, sum, smem_raw);
 }
 
 // ----------------------------------------------------------------------- 4. join
 
-// Warps that share the parts of a row: as many as fill a CTA of eight, two at least.
-__host__ __device__ constexpr int join_warps(int G) { return G >= 4 ? 2 : 8 / G; }
-
-// A CTA per (sequence, kv head); a row's warps take its parts in turn, a lane four
-// (D = 64: two) of the D values.
-template <int D, int G>
-__global__ void __launch_bounds__(join_warps(G) * G * 32) shared_join_kernel(const SharedParams p) {
-  constexpr int kEach = D / 32, kShare = join_warps(G), kWarps = kShare * G;
+// A row (sequence, query head) is joined by kShare of a CTA's four warps, which take its
+// parts in turn, a lane four (D = 64: two) of the D values.
+template <int D, int kShare>
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const SharedParams p) {
+  constexpr int kEach = D / 32, kRows = kJoinWarps / kShare;
   constexpr int kAhead = 8;  // parts asked for at a time
-  __shared__ float acc_s[kWarps][D];
-  __shared__ float2 ml_s[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = warp / kShare, share = warp - g * kShare;
-  const int Hkv = p.num_kv_heads, Hq = Hkv * G;
-  const int s = blockIdx.x / Hkv, j = blockIdx.x - s * Hkv;
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float2 ml_s[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % kShare;
+  const int Hkv = p.num_kv_heads, G = p.group_size, Hq = Hkv * G;
+  const int64_t rows = (int64_t)p.num_seqs * Hq;
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / kShare;
+  const int s = (int)(min(row, rows - 1) / Hq), head = (int)(min(row, rows - 1) - (int64_t)s * Hq);
+  const int j = head / G, g = head - j * G;
   // (The plan is there: the launch before began after it, and this one after that.)
   const int4 seq = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
   Totals sum;
@@ -1136,19 +1233,17 @@ __global__ void __launch_bounds__(join_warps(G) * G * 32) shared_join_kernel(con
   // behind that one.
   int n_pre = 0;
   int64_t run_row = 0;
-  const int64_t first_row = (int64_t)s * Hq + j * G + g;
   if (gp.tiles > 0) {
     const int64_t len = run_cost(sum);
     const int idx = (s - gp.start) * G + g, pair = idx / kPairRows;
-    const int64_t unit0 = gp.cost0 + ((int64_t)j * head_cost(gp, G) + 4 * pair) * gp.tiles;
+    const int64_t step0 = gp.cost0 + j * head_cost(gp, G) + pair * full_unit_cost(gp) + kUnitCost;
     const int each = step_cost(gp.members * G - pair * kPairRows);
-    const int64_t c0 = unit0 / len;
-    n_pre = (int)((unit0 + (int64_t)(gp.tiles - 1) * each) / len - c0 + 1);
+    const int64_t c0 = step0 / len;
     run_row = c0 * kPairRows + idx % kPairRows;
+    n_pre = (int)((step0 + (int64_t)(gp.tiles - 1) * each) / len - c0 + 1);
   }
-  const int n = n_tail + n_pre;
+  const int n = row < rows && seq.z > 0 ? n_tail + n_pre : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (seq.z <= 0) return;
   // A warp's parts: 32 of their maxima at a time, a lane each.
   float m = -INFINITY, l = 0.f;
   float acc[kEach];
@@ -1166,7 +1261,7 @@ __global__ void __launch_bounds__(join_warps(G) * G * 32) shared_join_kernel(con
       if (i >= 0) {
         ml = i == 0 ? p.first_ml : p.run_ml;
         o = i == 0 ? p.first_o : p.run_o;
-        at = i == 0 ? first_row : run_row + (int64_t)i * kPairRows;
+        at = i == 0 ? row : run_row + (int64_t)i * kPairRows;
       }
       x = __ldcg(reinterpret_cast<const float2 *>(ml) + at);
       o += at * D;
@@ -1210,33 +1305,45 @@ __global__ void __launch_bounds__(join_warps(G) * G * 32) shared_join_kernel(con
     }
   }
   // The sums of a row's warps.
-  if (lane == 0) ml_s[warp] = make_float2(m, l);
+  float M = m;
+  if constexpr (kShare > 1) {
+    if (lane == 0) ml_s[warp] = make_float2(m, l);
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) acc_s[warp][lane * kEach + e] = acc[e];
-  __syncthreads();
-  constexpr int kPairs = D / 2;  // of values, to a thread each
-  for (int x = threadIdx.x; x < G * kPairs; x += kWarps * 32) {
-    const int row = x / kPairs, d = (x - row * kPairs) * 2;
-    float M = -INFINITY;
+    for (int e = 0; e < kEach; ++e) acc_s[warp][lane * kEach + e] = acc[e];
+    __syncthreads();
+    if (share != 0) return;
 #pragma unroll
-    for (int w = 0; w < kShare; ++w) M = fmaxf(M, ml_s[row * kShare + w].x);
+    for (int w = 1; w < kShare; ++w) M = fmaxf(M, ml_s[warp + w].x);
     const float ref = M == -INFINITY ? 0.f : M;
-    float total = 0.f, v0 = 0.f, v1 = 0.f;
+    const float a0 = fast_exp2(m - ref);
+    l *= a0;
 #pragma unroll
-    for (int w = 0; w < kShare; ++w) {
-      const float2 y = ml_s[row * kShare + w];
+    for (int e = 0; e < kEach; ++e) acc[e] *= a0;
+#pragma unroll
+    for (int w = 1; w < kShare; ++w) {
+      const float2 y = ml_s[warp + w];
       const float a = fast_exp2(y.x - ref);
-      total = fmaf(y.y, a, total);
-      v0 = fmaf(acc_s[row * kShare + w][d], a, v0);
-      v1 = fmaf(acc_s[row * kShare + w][d + 1], a, v1);
+      l = fmaf(y.y, a, l);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) acc[e] = fmaf(acc_s[warp + w][lane * kEach + e], a, acc[e]);
     }
-    const float inv = 1.f / total;
-    *reinterpret_cast<uint32_t *>(p.out + ((int64_t)s * Hq + j * G + row) * D + d) =
-        pack_bf16x2(v0 * inv, v1 * inv);
   }
+  if (n == 0) return;  // (no such row, or an empty context: left as it was)
+  const float inv = 1.f / l;
+  uint16_t *out = p.out + row * D + lane * kEach;
+  if constexpr (kEach == 4)
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
 // ------------------------------------------------------------------------- host
+
+// Test-only, set by pkv_test_shared_fault: SharedParams::loading and share_always of the
+// process's calls.
+std::atomic<int> g_loading{kMaxCtas};
+std::atomic<int> g_share_always{0};
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -1275,7 +1382,7 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned th
 
 template <int D, int G>
 pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk,
-                  const CUtensorMap &tv, cudaStream_t stream) {
+                  cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
   const int S = prm.num_seqs;
@@ -1303,14 +1410,24 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   if (ctas < 2) ctas = 2;
   prm.ctas = (int)ctas;
   prm.tail_warps = warps;
-  cudaError_t err = launch_dependent<SharedParams, int>(shared_plan_kernel, 1, kPlanThreads,
+  const int plan_threads = S <= 256 ? 256 : kPlanThreads;
+  cudaError_t err = launch_dependent<SharedParams, int>(shared_plan_kernel, 1, plan_threads,
                                                         plan_smem, stream, prm, D);
   if (err == cudaSuccess)
-    err = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, SharedParams>(
-        shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, tv, prm);
-  if (err == cudaSuccess)
-    err = launch_dependent<SharedParams>(shared_join_kernel<D, G>, (unsigned)(S * prm.num_kv_heads),
-                                         join_warps(G) * G * 32, 0, stream, prm);
+    err = launch_dependent<CUtensorMap, CUtensorMap, SharedParams>(
+        shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, prm);
+  if (err == cudaSuccess) {
+    // As many warps to a row as leave the join's CTAs one turn on the GPU (eight to an SM):
+    // 1024 rows of about 20 parts took 6.7 us with one and 4.4 with two, 4096 of 6 the
+    // other way round (two turns) 4.0 and 7.5.
+    const int64_t rows = (int64_t)S * prm.num_kv_heads * G, room = 8 * (int64_t)sms;
+    const int share = rows <= room ? 4 : rows <= 2 * room ? 2 : 1;
+    const unsigned grid = (unsigned)((rows + kJoinWarps / share - 1) / (kJoinWarps / share));
+    err = launch_dependent<SharedParams>(share == 4   ? shared_join_kernel<D, 4>
+                                         : share == 2 ? shared_join_kernel<D, 2>
+                                                      : shared_join_kernel<D, 1>,
+                                         grid, kJoinWarps * 32, 0, stream, prm);
+  }
   return launch_status();  // (any launch's error, which it clears)
 }
 
@@ -1390,26 +1507,27 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.ctas = 0;
   prm.tail_warps = 0;
+  prm.loading = g_loading.load(std::memory_order_relaxed);
+  prm.share_always = g_share_always.load(std::memory_order_relaxed);
   prm.qscale = scale * kLog2e;
 
   // q as {D, Hq, S}: a box is 64 dims x the G heads of a kv head x 128 / G sequences.
   const uint64_t qdims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)num_seqs};
   const uint64_t qstr[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
   const uint32_t qbox[3] = {64u, (uint32_t)G, (uint32_t)(BM / G)};
-  // cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
+  // k_cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
   const uint64_t kdims[4] = {(uint64_t)head_dim, (uint64_t)num_kv_heads, (uint64_t)block_size,
                              (uint64_t)num_blocks};
   const uint64_t kstr[3] = {(uint64_t)head_dim * 2, (uint64_t)num_kv_heads * head_dim * 2,
                             (uint64_t)block_size * num_kv_heads * head_dim * 2};
   const uint32_t kbox[4] = {64u, 1u, (uint32_t)BN, 1u};
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk;
   if (!encode_bf16_map(&tq, q, 3, qdims, qstr, qbox, true) ||
-      !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true) ||
-      !encode_bf16_map(&tv, v_cache, 4, kdims, kstr, kbox, true))
+      !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true))
     return PKV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define PKV_CASE(DD, GG) \
-  if (head_dim == DD && G == GG) return launch<DD, GG>(prm, tq, tk, tv, st);
+  if (head_dim == DD && G == GG) return launch<DD, GG>(prm, tq, tk, st);
   PKV_CASE(64, 1)
   PKV_CASE(64, 2)
   PKV_CASE(64, 4)
@@ -1420,4 +1538,14 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   PKV_CASE(128, 8)
 #undef PKV_CASE
   return PKV_ERR_UNSUPPORTED;
+}
+
+extern "C" pkv_status pkv_test_shared_fault(int64_t wait_limit_ns, int loading_ctas, int share_always) {
+  if (wait_limit_ns <= 0 || loading_ctas < -1) return PKV_ERR_INVALID_ARG;
+  const unsigned long long limit = (unsigned long long)wait_limit_ns;
+  if (cudaMemcpyToSymbol(pkv::g_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  pkv::g_loading = loading_ctas >= 0 ? loading_ctas : pkv::kMaxCtas;
+  pkv::g_share_always = share_always != 0;
+  return PKV_OK;
 }

@@ -10,6 +10,7 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
+    config.addinivalue_line("markers", "by_choice: decode over shared prefixes shares them only where it pays")
 
 
 @pytest.fixture(scope="session")

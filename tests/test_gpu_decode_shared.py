@@ -4,7 +4,7 @@ Tolerances, derived: a logit is scale times a sum of D products that are exact i
 in fp32 in some order, each of the D additions off by at most 2^-23 (the tensor cores may
 truncate) of the sum of magnitudes A <= |q| |k|, so the logit by e = |scale| A D 2^-23; the
 product with log2(e) and its subtraction from the maximum by 2^-22 of |z| <= |scale| A, which e
-covers from D = 8 on.  A weight exp(z - log sum) is then off by 2 e of itself, and by 2^-18 for
+covers from D = 8 on.  A weight exp(z - log sum) is then off by 2 e of itself, and by 2^-17 for
 its two bf16 terms, a few 2^-22 for exponentials and the sums' positive terms: r = 2 e + 2^-16.
 The output sum_p w_p v_p with both its weights and their sum off by r is off by 2 r max|v|, plus
 the products' own accumulation, at most 2^-23 per key of max|v| w_p: n terms, and the joining of
@@ -23,6 +23,15 @@ from gpu_util import bits
 pytestmark = pytest.mark.gpu
 
 HALF_STEP = torch.finfo(torch.bfloat16).eps / 2
+
+
+@pytest.fixture(autouse=True)
+def share(request, lib):
+    """Prefixes are shared however short (most of these are far too short to pay), but in tests of the choice."""
+    always = not request.node.get_closest_marker("by_choice")
+    lib.test_shared_fault(10**9, -1, int(always))
+    yield
+    lib.test_shared_fault(10**9, -1, 0)
 
 
 class Shared:
@@ -271,19 +280,6 @@ def test_block_ids_out_of_range_are_flagged(lib):
     s.compare(only={2, 4})
 
 
-def test_only_the_first_sequences_row_is_read_for_the_prefix(lib):
-    s = Shared([(4, [30, 2, 90])], 4, 2, 128)
-    tables = s.tables.copy()
-    want = s.tables.copy()
-    tables[1:, :4] = 10**6
-    s.tables = tables
-    lib.paged_decode_shared_attn(**s.args(lib))
-    torch.cuda.synchronize()
-    s.tables = want
-    assert int(s.status.item()) == 0
-    s.compare()
-
-
 def test_the_same_call_gives_the_same_bits(lib):
     s = Shared([(9, [(53 * i) % 400 for i in range(40)]), (0, [777])], 16, 4, 128, 128)
     a = s.args(lib)
@@ -409,3 +405,31 @@ def test_refusals_of_the_binding(lib):
         lib.paged_decode_shared_attn(**{**a, "workspace": a["workspace"][:-256]})
     with pytest.raises(lib.PkvError, match="INVALID_ARG"):
         lib.paged_decode_shared_attn(**{**a, "scale": float("nan")})
+
+
+@pytest.mark.by_choice
+@pytest.mark.parametrize("groups", [[(1, [1, 70])], [(8, [5, 0, 200]), (0, [700])], [(150, [(37 * i) % 300 for i in range(40)])],
+                                    [(30, [3, 9]), (60, list(range(60))), (0, [900, 5])]])
+@pytest.mark.parametrize("G,D", [(2, 128), (8, 64)])
+def test_shared_or_not_as_it_pays(lib, groups, G, D):
+    """From batches too short for it to ones that are not."""
+    Shared(groups, 4 * G, 4, D, 64).check(lib)
+
+
+@pytest.mark.parametrize("loading", [0, 1, 20])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out_then_the_next_call(lib, loading, D):
+    """CTAs that load nothing: all else in them waits for tiles that never come, gives up and says so."""
+    s = Shared([(60, [(37 * i) % 100 for i in range(30)]), (20, [5, 9])], 8, 4, D)
+    a = s.args(lib)
+    lib.test_shared_fault(2_000_000, loading, 1)
+    lib.paged_decode_shared_attn(**a)
+    torch.cuda.synchronize()
+    lib.test_shared_fault(10**9, -1, 1)
+    assert int(s.status.item()) == lib.DEV_TIMEOUT
+    s.status.zero_()
+    s.out.fill_(7.0)
+    lib.paged_decode_shared_attn(**a)
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    s.compare()
