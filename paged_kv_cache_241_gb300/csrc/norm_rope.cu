@@ -26,6 +26,10 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeTokens = 8;  // tokens of a CTA, where there are many
+constexpr int kRopeAhead = 2;   // tokens that a warp has asked for at a time
+constexpr int kRopePlaces = 3;  // stream: tokens that a warp has in shared memory
+constexpr int kRopeSmem = 220 * 1024;
+constexpr int kRopeStreamTokens = 16;  // tokens per SM from which on they are streamed
 
 struct RopeParams {
   uint16_t *q_out;
@@ -48,6 +52,7 @@ struct RopeParams {
   int num_kv_heads;
   int rotary;           // R
   int tokens_per_cta;
+  int warp_bytes;       // shared memory of a warp (stream)
   float eps;
   float amplitude;
 };
@@ -78,19 +83,22 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 // A head is D / 16 lanes, each with two runs of eight dims: with the halves paired,
 // dims 8j and R/2 + 8j on (lane j < R/16), so that a lane has both of a pair; behind
-// the rotated part, and interleaved, 16 neighbouring dims.
+// the rotated part, and interleaved, 16 neighbouring dims.  A warp keeps its block of
+// heads (and with it their weights, in registers) over the CTA's tokens.
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;         // lanes of a head
-  constexpr int kHeads = 32 / kLanes;    // heads a warp takes at a time
-  extern __shared__ float rope_smem[];   // [tokens][cos: R/2, sin: R/2]
+  constexpr int kHeads = 32 / kLanes;    // heads of a warp's block
+  extern __shared__ float rope_smem[];   // [tokens][cos: R/2, sin: R/2], [tokens] slots
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int R = p.rotary, half = R >> 1;
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
-  const int heads = Hq + Hkv + (p.k_cache != nullptr ? Hkv : 0);
-  const int per_token = (heads + kHeads - 1) / kHeads;
+  const bool store = p.k_cache != nullptr;
+  const int heads = Hq + Hkv + (store ? Hkv : 0);
+  const int blocks = (heads + kHeads - 1) / kHeads;
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
   const int tokens = (int)min((int64_t)p.tokens_per_cta, p.num_tokens - t0);
+  int64_t *slots = reinterpret_cast<int64_t *>(rope_smem + p.tokens_per_cta * R);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -105,109 +113,341 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopePa
     rope_smem[t * R + a] = cs * p.amplitude;
     rope_smem[t * R + half + a] = sn * p.amplitude;
   }
+  for (int t = tid; t < tokens; t += blockDim.x) {
+    int64_t slot = store ? p.slots[t0 + t] : -1;
+    if (slot < -1 || slot >= p.num_slots) {
+      if (store) flag_status(p.status, PKV_DEV_BAD_SLOT);
+      slot = -1;
+    }
+    slots[t] = slot;
+  }
   __syncthreads();
 
   const int j = lane % kLanes, sub = lane / kLanes;
   const bool rotates = 16 * j < R;
   const int da = kInterleaved ? 16 * j : rotates ? 8 * j : 16 * j;
   const int db = kInterleaved ? da + 8 : rotates ? half + 8 * j : da + 8;
-  for (int item = warp; item < tokens * per_token; item += warps) {
-    const int ti = item / per_token;
-    const int64_t t = t0 + ti;
-    const int h = (item - ti * per_token) * kHeads + sub;
-    const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hkv;
+  const bool norm = p.q_weight != nullptr;
+  // More warps than blocks: those of one block share the tokens.
+  const int share = max(warps / blocks, 1), first = warp / blocks;
+  if (first >= share && blocks < warps) return;
+  for (int block = blocks < warps ? warp % blocks : warp; block < blocks; block += min(blocks, warps)) {
+    const int h = block * kHeads + sub;
+    const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hkv, live = h < heads;
     const int hk = is_k ? h - Hq : h - Hq - Hkv;  // head of k or v
-    int64_t slot = -1;
-    bool live = h < heads;
-    if (live && !is_q && p.k_cache != nullptr) {
-      slot = p.slots[t];
-      if (slot < -1 || slot >= p.num_slots) {
-        if (hk == 0 && is_k && j == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
-        slot = -1;
-      }
-      if (!is_k && slot < 0) live = false;
+    const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+    const uint16_t *src = (is_q ? p.q + h * D : (is_k ? p.k : p.v) + hk * D) + t0 * stride;
+    uint16_t *cache = (is_k ? p.k_cache : p.v_cache) + hk * D;
+    float ua[8], ub[8];
+    if (norm && live && (is_q || is_k)) {
+      const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
+      unpack8(*reinterpret_cast<const uint4 *>(weight + da), ua);
+      unpack8(*reinterpret_cast<const uint4 *>(weight + db), ub);
     }
-    const uint16_t *src = is_q   ? p.q + t * p.q_stride + (int64_t)h * D
-                          : is_k ? p.k + t * p.k_stride + (int64_t)hk * D
-                                 : p.v + t * p.v_stride + (int64_t)hk * D;
-    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (live) {
-      wa = load16(src + da);
-      wb = load16(src + db);
-    }
-    float a[8], b[8];
-    unpack8(wa, a);
-    unpack8(wb, b);
-    float sum = 0.f;
+    for (int ti0 = first; ti0 < tokens; ti0 += share * kRopeAhead) {
+      uint4 in[kRopeAhead][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-#pragma unroll
-    for (int k = 1; k < kLanes; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    if (is_q || is_k) {
-      if (p.q_weight != nullptr) {
-        const float inv = rsqrtf(sum * (1.f / D) + p.eps);
-        const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
-        float ua[8], ub[8];
-        unpack8(*reinterpret_cast<const uint4 *>(weight + da), ua);
-        unpack8(*reinterpret_cast<const uint4 *>(weight + db), ub);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] = a[i] * inv * ua[i];
-          b[i] = b[i] * inv * ub[i];
+      for (int x = 0; x < kRopeAhead; ++x) {
+        const int ti = ti0 + x * share;
+        in[x][0] = in[x][1] = make_uint4(0, 0, 0, 0);
+        if (ti < tokens && live) {
+          in[x][0] = load16(src + ti * stride + da);
+          in[x][1] = load16(src + ti * stride + db);
         }
       }
-      if (rotates) {
-        const float *cs = rope_smem + ti * R + 8 * j, *sn = cs + half;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // The lane's i-th pair.
-          float &x = kInterleaved ? (i < 4 ? a[2 * i & 7] : b[2 * i & 7]) : a[i];
-          float &y = kInterleaved ? (i < 4 ? a[(2 * i + 1) & 7] : b[(2 * i + 1) & 7]) : b[i];
-          const float x0 = x, y0 = y;
-          x = x0 * cs[i] - y0 * sn[i];
-          y = y0 * cs[i] + x0 * sn[i];
+      for (int x = 0; x < kRopeAhead; ++x) {
+        const int ti = ti0 + x * share;
+        if (ti >= tokens) break;
+        uint4 wa = in[x][0], wb = in[x][1];
+        float a[8], b[8];
+        unpack8(wa, a);
+        unpack8(wb, b);
+        if (norm) {  // (all lanes: a block may have heads of two kinds)
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
+#pragma unroll
+          for (int k = 1; k < kLanes; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+          const float inv = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            a[i] = a[i] * inv * ua[i];
+            b[i] = b[i] * inv * ub[i];
+          }
+        }
+        if (is_q || is_k) {
+          if (rotates) {
+            const float *cs = rope_smem + ti * R + 8 * j, *sn = cs + half;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              // The lane's i-th pair.
+              float &y0 = kInterleaved ? (i < 4 ? a[2 * i & 7] : b[2 * i & 7]) : a[i];
+              float &y1 = kInterleaved ? (i < 4 ? a[(2 * i + 1) & 7] : b[(2 * i + 1) & 7]) : b[i];
+              const float x0 = y0, x1 = y1;
+              y0 = x0 * cs[i] - x1 * sn[i];
+              y1 = x1 * cs[i] + x0 * sn[i];
+            }
+          }
+          // Without norm and rotation a value stays as it is, to the bit.
+          if (norm || rotates) {
+            wa = pack8(a);
+            wb = pack8(b);
+          }
+        }
+        if (!live) continue;
+        auto put = [&](uint16_t *dst) {
+          *reinterpret_cast<uint4 *>(dst + da) = wa;
+          *reinterpret_cast<uint4 *>(dst + db) = wb;
+        };
+        if (is_q) {
+          put(p.q_out + ((t0 + ti) * Hq + h) * D);
+        } else {
+          if (is_k && p.k_out != nullptr) put(p.k_out + ((t0 + ti) * Hkv + hk) * D);
+          const int64_t slot = slots[ti];
+          if (slot >= 0) put(cache + slot * Hkv * D);
         }
       }
-      // Without norm and rotation a value stays as it is, to the bit.
-      if (p.q_weight != nullptr || rotates) {
-        wa = pack8(a);
-        wb = pack8(b);
-      }
-    }
-    if (!live) continue;
-    auto put = [&](uint16_t *dst) {
-      *reinterpret_cast<uint4 *>(dst + da) = wa;
-      *reinterpret_cast<uint4 *>(dst + db) = wb;
-    };
-    if (is_q) {
-      put(p.q_out + (t * Hq + h) * D);
-    } else {
-      if (is_k && p.k_out != nullptr) put(p.k_out + (t * Hkv + hk) * D);
-      if (slot >= 0) put((is_k ? p.k_cache : p.v_cache) + (slot * Hkv + hk) * D);
     }
   }
 }
 
+// ------------------------------------------------------------------ many tokens
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {  // all but the last N groups are read out
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// A warp takes tokens by itself, every (number of warps)-th: the rows of q, k and v of
+// a token come as bulk copies into one of its places in shared memory, q and k are
+// normed and turned there, and all three leave as bulk copies, v without ever being in
+// a register.  Copies in of the next two tokens and out of the last one are under way
+// meanwhile; no warp waits for another.
 template <int D, bool kInterleaved>
-pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
-  const int sms = device_sm_count();
-  if (sms <= 0) return PKV_ERR_CUDA;
-  // Few tokens: one per CTA, so that the step is on as many SMs as it can be.
-  prm.tokens_per_cta = prm.num_tokens <= 8 * (int64_t)sms ? 1 : kRopeTokens;
-  const int64_t grid = (prm.num_tokens + prm.tokens_per_cta - 1) / prm.tokens_per_cta;
-  if (grid > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
+__global__ void __launch_bounds__(kRopeWarps * 32, 1) norm_rope_stream_kernel(const RopeParams p) {
+  constexpr int kLanes = D / 16;
+  constexpr int kHeads = 32 / kLanes;
+  extern __shared__ __align__(128) uint8_t stream_smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int R = p.rotary, half = R >> 1;
+  const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
+  const bool store = p.k_cache != nullptr, norm = p.q_weight != nullptr;
+  const uint32_t q_bytes = Hq * D * 2, kv_bytes = Hkv * D * 2;
+  const uint32_t row_bytes = q_bytes + kv_bytes * (store ? 2 : 1);
+  uint8_t *rows = stream_smem + (size_t)warp * p.warp_bytes;   // [kRopePlaces][row_bytes]
+  float *angles = reinterpret_cast<float *>(rows + kRopePlaces * row_bytes);  // [cos: R/2, sin: R/2]
+  uint64_t *full = reinterpret_cast<uint64_t *>(angles + R);
+  if (lane == 0) {
+    for (int i = 0; i < kRopePlaces; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  const int64_t first = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  const uint64_t policy = l2_policy_evict_first();
+  auto load = [&](int64_t t, int place) {  // (lane 0)
+    uint8_t *to = rows + place * row_bytes;
+    mbar_arrive_expect_tx(&full[place], row_bytes);
+    bulk_load(to, p.q + t * p.q_stride, q_bytes, &full[place], policy);
+    bulk_load(to + q_bytes, p.k + t * p.k_stride, kv_bytes, &full[place], policy);
+    if (store) bulk_load(to + q_bytes + kv_bytes, p.v + t * p.v_stride, kv_bytes, &full[place], policy);
+  };
+  if (lane == 0)
+    for (int i = 0; i < kRopePlaces - 1; ++i)
+      if (first + i * step < p.num_tokens) load(first + i * step, i);
+
+  const int j = lane % kLanes, sub = lane / kLanes;
+  const bool rotates = 16 * j < R;
+  const int da = kInterleaved ? 16 * j : rotates ? 8 * j : 16 * j;
+  const int db = kInterleaved ? da + 8 : rotates ? half + 8 * j : da + 8;
+  float wq[16], wk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) wq[i] = wk[i] = 1.f;
+  if (norm) {
+    auto weights = [&](const uint16_t *from, float (&w)[16]) {
+      float a[8], b[8];
+      unpack8(*reinterpret_cast<const uint4 *>(from + da), a);
+      unpack8(*reinterpret_cast<const uint4 *>(from + db), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = a[i];
+        w[8 + i] = b[i];
+      }
+    };
+    weights(p.q_weight, wq);
+    weights(p.k_weight, wk);
+  }
+  int position = 0, slot_next = -1;
+  if (first < p.num_tokens) {
+    if (R > 0) position = p.positions[first];
+    if (store) slot_next = p.slots[first];
+  }
+  int place = 0, phase = 0;
+  bool ok = true;
+  for (int64_t t = first; t < p.num_tokens; t += step) {
+    int64_t slot = slot_next;
+    if (slot < -1 || slot >= p.num_slots) {
+      if (store && lane == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
+      slot = -1;
+    }
+    for (int a = lane; a < half; a += 32) {
+      const uint64_t turn = (uint64_t)(int64_t)position * p.turns[a];
+      const float x = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // (see norm_rope_kernel)
+      float sn, cs;
+      sincospif(x, &sn, &cs);
+      angles[a] = cs * p.amplitude;
+      angles[half + a] = sn * p.amplitude;
+    }
+    if (t + step < p.num_tokens) {  // (the next token's, asked for ahead)
+      if (R > 0) position = p.positions[t + step];
+      if (store) slot_next = p.slots[t + step];
+    }
+    __syncwarp();
+    float cs[8], sn[8];
+    if (rotates) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = angles[8 * j + i];
+        sn[i] = angles[half + 8 * j + i];
+      }
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[place], phase, nullptr));
+    if (!ok) break;
+    uint8_t *at = rows + place * row_bytes;
+    auto turn_heads = [&](uint8_t *base, int heads, const float (&w)[16]) {
+#pragma unroll 2
+      for (int h0 = 0; h0 < heads; h0 += kHeads) {
+        const int h = h0 + sub;
+        const bool live = h < heads;
+        uint8_t *row = base + (live ? h : heads - 1) * (D * 2);
+        uint4 *pa = reinterpret_cast<uint4 *>(row + da * 2), *pb = reinterpret_cast<uint4 *>(row + db * 2);
+        float a[8], b[8];
+        unpack8(*pa, a);
+        unpack8(*pb, b);
+        if (norm) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
+#pragma unroll
+          for (int k = 1; k < kLanes; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+          const float inv = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            a[i] = a[i] * inv * w[i];
+            b[i] = b[i] * inv * w[8 + i];
+          }
+        }
+        if (rotates) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float &y0 = kInterleaved ? (i < 4 ? a[2 * i & 7] : b[2 * i & 7]) : a[i];
+            float &y1 = kInterleaved ? (i < 4 ? a[(2 * i + 1) & 7] : b[(2 * i + 1) & 7]) : b[i];
+            const float x0 = y0, x1 = y1;
+            y0 = x0 * cs[i] - x1 * sn[i];
+            y1 = x1 * cs[i] + x0 * sn[i];
+          }
+        }
+        // (what neither norm nor rotation touches stays as it is, to the bit)
+        if (live && (norm || rotates)) {
+          *pa = pack8(a);
+          *pb = pack8(b);
+        }
+      }
+    };
+    turn_heads(at, Hq, wq);
+    turn_heads(at + q_bytes, Hkv, wk);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      bulk_store(p.q_out + t * Hq * D, at, q_bytes);
+      if (p.k_out != nullptr) bulk_store(p.k_out + t * Hkv * D, at + q_bytes, kv_bytes);
+      if (slot >= 0) {
+        bulk_store(p.k_cache + slot * Hkv * D, at + q_bytes, kv_bytes);
+        bulk_store(p.v_cache + slot * Hkv * D, at + q_bytes + kv_bytes, kv_bytes);
+      }
+      bulk_commit();
+      // The place of the token before is read out: the next copies in go there.
+      const int64_t next = t + (kRopePlaces - 1) * step;
+      if (next < p.num_tokens) {
+        bulk_wait_read<1>();
+        load(next, place == 0 ? kRopePlaces - 1 : place - 1);
+      }
+    }
+    if (++place == kRopePlaces) {
+      place = 0;
+      phase ^= 1;
+    }
+  }
+  if (lane == 0) {
+    if (!ok) {  // (a wait ran out: the copies still under way end before the CTA does)
+      flag_status(p.status, PKV_DEV_TIMEOUT);
+      for (int i = 0; i < kRopePlaces; ++i) mbar_wait_bounded(&full[i], i < place ? phase ^ 1 : phase, nullptr);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+}
+
+pkv_status launch_dependent(void (*kernel)(RopeParams), unsigned grid, int threads, int smem,
+                            cudaStream_t stream, const RopeParams &prm) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kRopeWarps * 32);
-  cfg.dynamicSmemBytes = (size_t)prm.tokens_per_cta * prm.rotary * sizeof(float);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, kInterleaved>, prm);
+  cudaLaunchKernelEx(&cfg, kernel, prm);
   return launch_status();
+}
+
+template <int D, bool kInterleaved>
+pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return PKV_ERR_CUDA;
+  // Many tokens: streamed, if a token's rows leave room for enough warps.
+  const int64_t row = ((int64_t)prm.num_q_heads + prm.num_kv_heads * (prm.k_cache != nullptr ? 2 : 1)) * D * 2;
+  const int64_t warp_bytes = (kRopePlaces * row + prm.rotary * 4 + kRopePlaces * 8 + 127) & ~(int64_t)127;
+  int warps = warp_bytes <= kRopeSmem ? (int)(kRopeSmem / warp_bytes) : 0;
+  if (warps > kRopeWarps) warps = kRopeWarps;
+  if (prm.num_tokens > kRopeStreamTokens * (int64_t)sms && warps >= 4) {
+    const int smem = (int)(warps * warp_bytes);
+    int per_sm = 1;
+    prm.warp_bytes = (int)warp_bytes;
+    if (!kernel_smem_setup((const void *)norm_rope_stream_kernel<D, kInterleaved>, warps * 32, smem, &per_sm))
+      return PKV_ERR_CUDA;
+    int64_t grid = (int64_t)sms * per_sm;
+    if (grid > (prm.num_tokens + warps - 1) / warps) grid = (prm.num_tokens + warps - 1) / warps;
+    return launch_dependent(norm_rope_stream_kernel<D, kInterleaved>, (unsigned)grid, warps * 32, smem, stream, prm);
+  }
+  // Few tokens: one per CTA, so that the step is on as many SMs as it can be.
+  prm.tokens_per_cta = prm.num_tokens <= 8 * (int64_t)sms ? 1 : kRopeTokens;
+  const int64_t grid = (prm.num_tokens + prm.tokens_per_cta - 1) / prm.tokens_per_cta;
+  if (grid > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
+  return launch_dependent(norm_rope_kernel<D, kInterleaved>, (unsigned)grid, kRopeWarps * 32,
+                          (int)(prm.tokens_per_cta * (prm.rotary * sizeof(float) + sizeof(int64_t))), stream, prm);
 }
 
 // [a, a + n) and [b, b + m) values of 16 bits have any in common.
@@ -312,6 +552,7 @@ extern "C" pkv_status pkv_norm_rope_store(
   prm.num_kv_heads = num_kv_heads;
   prm.rotary = rotary_dim;
   prm.tokens_per_cta = 0;
+  prm.warp_bytes = 0;
   prm.eps = eps;
   prm.amplitude = amplitude;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -268,3 +268,71 @@ def test_offsets_past_32_bits(lib):
     r.call(lib, k_out=True)
     assert torch.equal(kc.view(-1, Hkv, D)[r.slots.long()], r.k_out)
     assert torch.equal(vc.view(-1, Hkv, D)[r.slots.long()], r.v)
+
+
+# More tokens than this per SM are streamed through shared memory, a token to a warp.
+MANY = 16 * 152
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,R", [(1, 1, 64, 64), (3, 1, 128, 48), (5, 2, 64, 16), (4, 4, 128, 32)])
+def test_streamed_rows(lib, Hq, Hkv, D, R, interleaved):
+    Rows(MANY + 117, Hq, Hkv, D, R, packed=interleaved).check(lib, norm=R != 16, interleaved=interleaved, amplitude=1.2)
+
+
+@pytest.mark.parametrize("store,k_out", [(True, True), (False, True)])
+def test_streamed_keys_as_a_tensor(lib, store, k_out):
+    Rows(MANY + 1, 2, 1, 64, 32, packed=store).check(lib, store=store, k_out=k_out)
+
+
+def test_streamed_rows_are_those_of_few(lib):
+    """The same tokens, streamed and a part of them at a time: the same bits (ordinary head counts, a whole head turned)."""
+    r = Rows(3 * MANY + 5, 16, 8, 128, 128)
+    r.call(lib, k_out=True)
+    q, k, kc, vc = r.q_out.clone(), r.k_out.clone(), r.kc.clone(), r.vc.clone()
+    r.q_out.zero_(), r.k_out.zero_(), r.kc.zero_(), r.vc.zero_()
+    turns, T = lib.rope_turns(r.inv_freq), r.q.shape[0]
+    for a in range(0, T, 1000):
+        b = min(a + 1000, T)
+        lib.norm_rope_store(r.q_out[a:b], r.q[a:b], r.k[a:b], r.v[a:b], r.positions[a:b], turns, r.kc, r.vc, r.slots[a:b], k_out=r.k_out[a:b],
+                            q_weight=r.qw, k_weight=r.kw)
+    torch.cuda.synchronize()
+    kept = r.slots[r.slots >= 0].long()
+    assert torch.equal(q, r.q_out) and torch.equal(k, r.k_out)
+    assert torch.equal(kc.flatten(0, 1)[kept], r.kc.flatten(0, 1)[kept]) and torch.equal(vc.flatten(0, 1)[kept], r.vc.flatten(0, 1)[kept])
+
+
+def test_streamed_in_place(lib):
+    r = Rows(MANY + 50, 6, 2, 128, 128, packed=False)
+    r.call(lib, k_out=True)
+    q, k = r.q.clone(), r.k.clone()
+    lib.norm_rope_store(q, q, k, r.v, r.positions, lib.rope_turns(r.inv_freq), k_out=k, q_weight=r.qw, k_weight=r.kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q.view(torch.int16), r.q_out.view(torch.int16))
+    assert torch.equal(k.view(torch.int16), r.k_out.view(torch.int16))
+
+
+def test_streamed_bits_that_do_not_turn_and_bad_slots(lib):
+    r = Rows(MANY + 7, 3, 2, 128, 32, packed=False, skip=0.0)
+    bits = torch.randint(-2**15, 2**15, r.q.shape, dtype=torch.int32).to(torch.int16).cuda()
+    r.q.view(torch.int16)[..., 32:] = bits[..., 32:]
+    r.v.view(torch.int16).copy_(bits[:, :2])
+    r.slots[5], r.slots[MANY] = r.kc.shape[0] * r.kc.shape[1], -9
+    r.call(lib, norm=False)
+    assert torch.equal(r.q_out.view(torch.int16)[..., 32:], bits[..., 32:])
+    kept = ((r.slots >= 0) & (r.slots < r.kc.shape[0] * r.kc.shape[1])).nonzero()[:, 0]
+    assert torch.equal(r.vc.flatten(0, 1)[r.slots[kept].long()].view(torch.int16), r.v[kept].view(torch.int16))
+    assert int(r.status.item()) == lib.DEV_BAD_SLOT
+
+
+def test_many_rows_too_wide_to_stream(lib):
+    """Rows of a token that leave shared memory room for fewer than four warps."""
+    r = Rows(MANY + 3, 64, 16, 128, 16, packed=False, block=256)
+    r.call(lib, norm=True)
+    T = r.q.shape[0]
+    q = r.q_out.clone()
+    turns = lib.rope_turns(r.inv_freq)
+    r.q_out.zero_()
+    lib.norm_rope_store(r.q_out[:700], r.q[:700], r.k[:700], r.v[:700], r.positions[:700], turns, r.kc, r.vc, r.slots[:700], q_weight=r.qw, k_weight=r.kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q[:700], r.q_out[:700])
