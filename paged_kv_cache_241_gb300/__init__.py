@@ -547,19 +547,23 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
     _check(st, "pkv_kv_evict")
 
 
-def _refuse(what, dev, args, dev_status=None):
-    """Says what is wrong with a call's tensors: dtype, rank, layout or device (the
-    library launches on the current one).  args: (name, tensor or None, dtype, rank)."""
+def _is_current(dev) -> bool:
+    """Whether a tensor's device is the current one (where the library launches)."""
     import torch
 
+    return dev >= 0 and torch._C._cuda_getDevice() == dev
+
+
+def _refuse(what, args, dev_status=None):
+    """Says what is wrong with a call's tensors: dtype, rank, layout or device.
+    args: (name, tensor or None, dtype, rank)."""
     for name, t, dtype, ndim in args:
         if t is None:
             continue
         _need(t, dtype, name, ndim)
-        if t.get_device() != dev:
+        if not _is_current(t.get_device()):
             raise ValueError(f"{what}: {name} is not on the current CUDA device")
-    if not _plain_status(dev, dev_status):
-        raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
+    raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
 
 
 def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_context_lens,
@@ -572,17 +576,15 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
     new_context_lens may be context_lens, and new_num_free num_free."""
     import torch
 
-    lib = load()
+    lib = _lib or load()
     i32 = torch.int32
-    dev = torch.cuda.current_device() if block_tables.is_cuda else -1
-    table_shape = block_tables.shape
-    if not (_plain_status(dev, dev_status) and
-            _plain(dev, i32, new_lens, context_lens, block_tables, free_blocks, num_free,
+    dev = block_tables.get_device()
+    if not (_plain(dev, i32, block_tables, new_lens, context_lens, free_blocks, num_free,
                    new_context_lens, new_num_free, slot_mapping, positions, cu_seqlens_q,
-                   cu_seqlens_k) and
+                   cu_seqlens_k) and _is_current(dev) and
             (borrowed_blocks is None or _plain(dev, i32, borrowed_blocks)) and
-            len(table_shape) == 2):
-        _refuse("plan_step", dev, (
+            (dev_status is None or _plain_status(dev, dev_status)) and block_tables.dim() == 2):
+        _refuse("plan_step", (
             ("new_lens", new_lens, i32, 1), ("context_lens", context_lens, i32, 1),
             ("block_tables", block_tables, i32, 2), ("free_blocks", free_blocks, i32, 1),
             ("num_free", num_free, i32, 1), ("new_context_lens", new_context_lens, i32, 1),
@@ -590,21 +592,23 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
             ("positions", positions, i32, 1), ("cu_seqlens_q", cu_seqlens_q, i32, 1),
             ("cu_seqlens_k", cu_seqlens_k, i32, 1),
             ("borrowed_blocks", borrowed_blocks, i32, 1)), dev_status)
-    S, wide = table_shape
-    if not (new_lens.shape == context_lens.shape == new_context_lens.shape == (S,) and
-            cu_seqlens_q.shape == cu_seqlens_k.shape == (S + 1,) and
-            num_free.shape == new_num_free.shape == (1,) and free_blocks.dim() == 1 and
-            slot_mapping.dim() == 1 and slot_mapping.shape == positions.shape and
-            (borrowed_blocks is None or borrowed_blocks.shape == (S,))):
+    S, wide = block_tables.shape
+    per_seq, sums, rows = (S,), (S + 1,), slot_mapping.shape
+    if new_lens.shape != per_seq or context_lens.shape != per_seq or \
+            new_context_lens.shape != per_seq or cu_seqlens_q.shape != sums or \
+            cu_seqlens_k.shape != sums or num_free.shape != (1,) or new_num_free.shape != (1,) or \
+            free_blocks.dim() != 1 or len(rows) != 1 or positions.shape != rows or \
+            (borrowed_blocks is not None and borrowed_blocks.shape != per_seq):
         raise ValueError("plan_step: inconsistent shapes")
     st = lib.pkv_plan_step(
-        new_lens.data_ptr(), context_lens.data_ptr(), _addr(borrowed_blocks),
-        block_tables.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
-        new_context_lens.data_ptr(), new_num_free.data_ptr(), slot_mapping.data_ptr(),
-        positions.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S,
-        slot_mapping.numel(), wide, _c_int32(block_size), _c_int64(num_blocks),
-        free_blocks.numel(), _addr(dev_status), _raw_stream(stream, dev))
-    _check(st, "pkv_plan_step")
+        new_lens.data_ptr(), context_lens.data_ptr(),
+        None if borrowed_blocks is None else borrowed_blocks.data_ptr(), block_tables.data_ptr(),
+        free_blocks.data_ptr(), num_free.data_ptr(), new_context_lens.data_ptr(),
+        new_num_free.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, rows[0], wide, _c_int32(block_size),
+        _c_int64(num_blocks), free_blocks.numel(), _addr(dev_status), _raw_stream(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_plan_step")
 
 
 def rope_turns(inv_freq, device="cuda"):
@@ -622,24 +626,31 @@ def rope_turns(inv_freq, device="cuda"):
     return torch.from_numpy(turns).to(device)
 
 
-def _rows_of(t, name, shape, dev):
-    """Values between the tokens of t [T, heads, D], whose rows must be contiguous."""
+def _refuse_rows(what, rows, D):
+    """Says what is wrong with q, k or v.  rows: (name, tensor, shape)."""
     import torch
 
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: is not on the current CUDA device")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-    # (strides of dims of size one, and of tokens of which there is one, say nothing)
+    for name, t, shape in rows:
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+        if not t.is_cuda or not _is_current(t.get_device()):
+            raise ValueError(f"{name}: must be a CUDA tensor on the current device")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
+        if _token_step(t, D) < 0:
+            raise ValueError(f"{name}: rows must be contiguous [heads, D]")
+
+
+def _token_step(t, D) -> int:
+    """Values between the tokens of t [T, heads, D] (0: contiguous); -1 when its rows are
+    not.  (Strides of dims of size one, and of tokens of which there is one, say nothing.)"""
     step, head, value = t.stride()
-    T, H, D = shape
+    if head == D and value == 1:
+        return step if t.shape[0] > 1 else 0
+    T, H, _ = t.shape
     if (value != 1 and D > 1) or (head != D and H > 1):
-        raise ValueError(f"{name}: rows must be contiguous [heads, D]")
-    return step if T > 1 else H * D
+        return -1
+    return step if T > 1 else 0
 
 
 def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None,
@@ -652,46 +663,62 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
     projection).  Without caches k goes to k_out [T, Hkv, D] alone.  bf16."""
     import torch
 
-    lib = load()
+    lib = _lib or load()
     bf16, i32 = torch.bfloat16, torch.int32
-    dev = torch.cuda.current_device() if q.is_cuda else -1
-    if q.dim() != 3 or k.dim() != 3:
+    dev = q.get_device()
+    q_shape, k_shape = q.shape, k.shape
+    if len(q_shape) != 3 or len(k_shape) != 3:
         raise ValueError("norm_rope_store: q and k must be [T, heads, D]")
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    q_step = _rows_of(q, "q", q.shape, dev)
-    k_step = _rows_of(k, "k", (T, Hkv, D), dev)
+    T, Hq, D = q_shape
+    Hkv = k_shape[1]
     store = k_cache is not None
-    if not (store == (v_cache is not None) == (slot_mapping is not None)):
+    if (v_cache is not None) is not store or (slot_mapping is not None) is not store:
         raise ValueError("norm_rope_store: k_cache, v_cache and slot_mapping go together")
-    v_step = _rows_of(v, "v", (T, Hkv, D), dev) if store else 0
-    if (q_weight is None) != (k_weight is None):
+    norm = q_weight is not None
+    if (k_weight is not None) is not norm:
         raise ValueError("norm_rope_store: q_weight and k_weight go together")
-    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, q_out) and
-            _plain(dev, i32, positions) and _plain(dev, torch.int64, turns) and
+    kv_shape = (T, Hkv, D)
+    rows = (("q", q, q_shape), ("k", k, kv_shape), ("v", v, kv_shape)) if store else \
+        (("q", q, q_shape), ("k", k, kv_shape))
+    steps = [0, 0, 0]
+    for i, (_, t, shape) in enumerate(rows):
+        if t.dtype is not bf16 or t.get_device() != dev or t.shape != shape:
+            _refuse_rows("norm_rope_store", rows, D)
+        steps[i] = _token_step(t, D)
+    if min(steps) < 0 or not _is_current(dev):
+        _refuse_rows("norm_rope_store", rows, D)
+    if not (_plain(dev, bf16, q_out) and _plain(dev, i32, positions) and
+            _plain(dev, torch.int64, turns) and
+            (not store or _plain(dev, bf16, k_cache, v_cache) and _plain(dev, i32, slot_mapping)) and
+            (not norm or _plain(dev, bf16, q_weight, k_weight)) and
             (k_out is None or _plain(dev, bf16, k_out)) and
-            (q_weight is None or _plain(dev, bf16, q_weight, k_weight)) and
-            (not store or _plain(dev, bf16, k_cache, v_cache) and _plain(dev, i32, slot_mapping))):
-        _refuse("norm_rope_store", dev, (
+            (dev_status is None or _plain_status(dev, dev_status))):
+        _refuse("norm_rope_store", (
             ("q_out", q_out, bf16, 3), ("positions", positions, i32, 1),
             ("turns", turns, torch.int64, 1), ("k_out", k_out, bf16, 3),
             ("q_weight", q_weight, bf16, 1), ("k_weight", k_weight, bf16, 1),
             ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
             ("slot_mapping", slot_mapping, i32, 1)), dev_status)
-    NB, BS = (k_cache.shape[0], k_cache.shape[1]) if store else (0, 0)
-    if q_out.shape != q.shape or positions.shape != (T,) or turns.dim() != 1 or \
-            (k_out is not None and k_out.shape != k.shape) or \
-            (q_weight is not None and not q_weight.shape == k_weight.shape == (D,)) or \
-            (store and not (k_cache.shape == v_cache.shape == (NB, BS, Hkv, D) and
-                            slot_mapping.shape == (T,))):
+    NB = BS = 0
+    per_token = (T,)
+    if store:
+        cache_shape = k_cache.shape
+        if len(cache_shape) != 4 or cache_shape[2] != Hkv or cache_shape[3] != D or \
+                v_cache.shape != cache_shape or slot_mapping.shape != per_token:
+            raise ValueError("norm_rope_store: inconsistent shapes of the caches or slots")
+        NB, BS = cache_shape[0], cache_shape[1]
+    if q_out.shape != q_shape or positions.shape != per_token or turns.dim() != 1 or \
+            (k_out is not None and k_out.shape != k_shape) or \
+            (norm and (q_weight.shape != (D,) or k_weight.shape != (D,))):
         raise ValueError("norm_rope_store: inconsistent shapes")
     st = lib.pkv_norm_rope_store(
         q_out.data_ptr(), _addr(k_out), q.data_ptr(), k.data_ptr(), v.data_ptr() if store else None,
         _addr(k_cache), _addr(v_cache), _addr(slot_mapping), positions.data_ptr(),
-        turns.data_ptr(), _addr(q_weight), _addr(k_weight), T, Hq, Hkv, D, q_step, k_step, v_step,
-        2 * turns.numel(), 1 if interleaved else 0, float(eps), float(amplitude), NB, BS,
+        turns.data_ptr(), _addr(q_weight), _addr(k_weight), T, Hq, Hkv, D, steps[0], steps[1],
+        steps[2], 2 * turns.numel(), 1 if interleaved else 0, float(eps), float(amplitude), NB, BS,
         _addr(dev_status), _raw_stream(stream, dev))
-    _check(st, "pkv_norm_rope_store")
+    if st:
+        raise PkvError(st, "pkv_norm_rope_store")
 
 
 def decode_shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
@@ -711,15 +738,16 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
     once (see include/pkv.h; BlockManager.prefix_groups finds groups)."""
     import torch
 
-    lib = load()
+    lib = _lib or load()
     bf16, i32 = torch.bfloat16, torch.int32
-    dev = _device_of(k_cache)
+    dev = q.get_device()
     q_shape, cache_shape, table_shape = q.shape, k_cache.shape, block_tables.shape
-    if not (_plain_status(dev, dev_status) and _plain(dev, bf16, out, q, k_cache, v_cache) and
+    if not (_plain(dev, bf16, q, out, k_cache, v_cache) and _is_current(dev) and
             _plain(dev, i32, block_tables, context_lens, group_starts, shared_blocks) and
             _plain(dev, torch.uint8, workspace) and
+            (dev_status is None or _plain_status(dev, dev_status)) and
             len(q_shape) == 3 and len(cache_shape) == 4 and len(table_shape) == 2):
-        _refuse("paged_decode_shared_attn", dev, (
+        _refuse("paged_decode_shared_attn", (
             ("out", out, bf16, 3), ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4),
             ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
             ("context_lens", context_lens, i32, 1), ("group_starts", group_starts, i32, 1),
@@ -737,7 +765,8 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
         block_tables.data_ptr(), context_lens.data_ptr(), group_starts.data_ptr(),
         shared_blocks.data_ptr(), S, groups, Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
         workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
-    _check(st, "pkv_paged_decode_shared_attn")
+    if st:
+        raise PkvError(st, "pkv_paged_decode_shared_attn")
 
 
 def test_shared_fault(wait_limit_ns: int, loading_ctas: int, share_always: int) -> None:

@@ -11,10 +11,11 @@
 // decode.  All parts (M, l, o) of a row are then joined:
 //   out = sum_i exp(M_i - M) o_i / sum_i exp(M_i - M) l_i.
 //
-// Three launches, each a programmatic dependent of the one before:
+// Three launches, each a programmatic dependent of the one before, or two:
 //  1. plan: one CTA.  A group's prefix ends where its shortest sequence does; prefix
 //     sums of the work of groups (steps of 64 keys) and of sequences (tiles of 4 KiB
-//     of K) go to the workspace, and how many CTAs work on prefixes.
+//     of K) go to the workspace, and how many CTAs work on prefixes.  A small batch has
+//     no such launch: every CTA of the next one plans for itself, in shared memory.
 //  2. attention: one CTA per SM.  Some of them take the prefixes, units of (group, kv
 //     head, 256 rows) by steps, cut into runs of equal cost, a CTA for each (tcgen05,
 //     TMA); the others the tails, all sequences' own tokens, cut into runs of equal
@@ -40,6 +41,13 @@ constexpr int kStages = 3;               // ring of tiles per warp
 constexpr int kMaxWarps = 4096;          // warps of the tails' grid at most (places for parts)
 constexpr int kMaxCtas = 512;            // CTAs of the attention's grid at most (places for parts)
 constexpr int kThreads = 384;            // of the attention's CTAs
+// A batch is planned by every CTA for itself where its tables have room for no more K and
+// V than kNearBytes, in at most so many sequences and groups: two short sequences 10.6 ->
+// 8.4 us and 2 us less on the host; 64 behind a system prompt 33.0 -> 34.9, as the join
+// can then not read the plan before it waits.
+constexpr int64_t kNearBytes = 16 << 20;
+constexpr int kNearSeqs = kThreads;
+constexpr int kNearGroups = 32;
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 constexpr int BM = 128;                  // rows of a product
 constexpr int BN = 64;                   // keys of a step
@@ -118,23 +126,35 @@ struct SharedParams {
   int tail_warps;      // warps of a CTA that takes tails
   int loading;         // CTAs that load their prefixes: all, but in a test
   int share_always;    // whatever it saves (test)
+  int near;            // the attention's CTAs plan
+  int plan_at;         // where their plan (or groups) is in shared memory
+  int head_dim;
   float qscale;        // scale * log2(e)
 };
 
 // Tokens of K in a tile of a tail: 4 KiB.
 __host__ __device__ constexpr int tail_rows(int D) { return 2048 / D; }
+__device__ __forceinline__ int tail_tiles(int tokens, int D) {
+  return D == 64 ? (tokens + 31) >> 5 : (tokens + 15) >> 4;
+}
+static_assert(tail_rows(64) == 32 && tail_rows(128) == 16, "shifts");
+
+// (Divisions of 64 bits take four times as long.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Tiles per run of the tails; run r's part of sequence s is filed under s + r (a part
 // begins where a sequence or a run does, so no two have the same number).
 __device__ __forceinline__ int run_tiles(const SharedParams &p, const Totals &t) {
   const int runs = max((p.ctas - t.prefix_ctas) * p.tail_warps / p.num_kv_heads, 1);
-  return max((int)((t.tiles + runs - 1) / runs), 1);
+  return max((int)quotient(t.tiles + runs - 1, runs), 1);
 }
 // Cost per run of the prefixes (at least that of the dearest step, so that every run
 // between a unit's first and last has a step of it).
 __device__ __forceinline__ int64_t run_cost(const Totals &t) {
   const int n = max(t.prefix_ctas, 1);
-  return max((t.cost + n - 1) / n, (int64_t)4);
+  return max(quotient(t.cost + n - 1, n), (int64_t)4);
 }
 
 // ----------------------------------------------------------------------- 1. plan
@@ -143,28 +163,36 @@ __device__ __forceinline__ int64_t run_cost(const Totals &t) {
 // nanoseconds, as measured: of a unit of cost, and the beginning and end of a run; of a
 // tile of a tail (K and V of tail_rows tokens, a kv head) for all of a CTA's warps, and
 // of their beginning.
-constexpr int kCostNs = 320, kPrefixNs = 7000, kTailNs = 2500;
+constexpr int kCostNs = 340, kPrefixNs = 6000, kTailNs = 2500;
 // (eight heads take two products with V)
 __device__ __forceinline__ float tile_ns(int G) { return G == 8 ? 175.f : 145.f; }
 
-__device__ __forceinline__ float time_with(const SharedParams &p, float cost, float tiles, int n) {
-  const int rest = p.ctas - n;
-  const float prefix = cost == 0.f ? 0.f : n == 0 ? INFINITY : __fdividef(cost * kCostNs, n) + kPrefixNs;
-  const float tails =
-      tiles == 0.f ? 0.f : rest == 0 ? INFINITY : __fdividef(tiles * p.num_kv_heads * tile_ns(p.group_size), rest) + kTailNs;
-  return fmaxf(prefix, tails);
+__device__ __forceinline__ int split_ctas(const SharedParams &p, float cost, float tiles) {
+  const float a = cost * kCostNs, b = tiles * p.num_kv_heads * tile_ns(p.group_size);
+  if (a == 0.f) return 0;
+  if (b == 0.f) return p.ctas;
+  // a / n + kPrefixNs = b / (ctas - n) + kTailNs, solved for n: the whole number beside
+  // it that ends sooner (one CTA of a kind at least).
+  const float N = p.ctas, d = kPrefixNs - kTailNs, e = d * N - a - b;
+  const float n = (e + sqrtf(e * e + 4.f * d * a * N)) / (2.f * d);
+  auto time = [&](float n) {
+    return fmaxf(__fdividef(a, n) + kPrefixNs, __fdividef(b, N - n) + kTailNs);
+  };
+  const float low = fminf(fmaxf(floorf(n), 1.f), N - 1.f), high = fminf(low + 1.f, N - 1.f);
+  return (int)(time(high) < time(low) ? high : low);
 }
+static_assert(kPrefixNs > kTailNs, "the equation's quadratic term");
 
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, int D) {
-  extern __shared__ int plan_smem[];
-  __shared__ int64_t sums[32][3];
+// The whole batch's plan, by all threads of a CTA, to groups, seqs and totals (of the
+// workspace, or shared memory).  scratch: shared memory of 4 N + 1 ints.
+__device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, int64_t (*sums)[2],
+                                           GroupPlan *groups, SeqPlan *seqs, Totals *totals) {
   const int S = p.num_seqs, N = p.num_groups, tid = threadIdx.x;
-  int *starts = plan_smem;       // [N + 1]
+  const bool tell = blockIdx.x == 0;
+  int *starts = scratch;         // [N + 1]
   int *eff = starts + N + 1;     // [N]: blocks that the group shares
   int *lead = eff + N;           // [N]: its first sequence with tokens
   int *count = lead + N;         // [N]: its sequences with tokens
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
   auto tokens = [&](int L) { return L <= 0 ? 0 : (int)min((int64_t)L, room); };
   const int first_L = tid < S ? p.context_lens[tid] : 0;  // (asked for ahead)
@@ -175,7 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     ok = ok && (g > 0 || x == 0) && (g < N || x == S);
     if (g < N) {
       const int b = p.shared_blocks[g];
-      if (b < 0 || b > p.max_blocks_per_seq) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+      if (tell && (b < 0 || b > p.max_blocks_per_seq)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
       eff[g] = min(max(b, 0), p.max_blocks_per_seq);
       lead[g] = 0x7FFFFFFF;
       count[g] = 0;
@@ -185,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   for (int g = tid; g < N; g += blockDim.x) ok = ok && starts[g] <= starts[g + 1];
   ok = __syncthreads_and(ok) != 0;
   // (no groups then: every sequence by itself)
-  if (!ok && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+  if (!ok && tell && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
   if (ok) {
     for (int s0 = tid & ~31; s0 < S; s0 += blockDim.x) {
       const int s = s0 + (tid & 31);
@@ -204,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     }
   }
   __syncthreads();
-  const int per_g = (N + blockDim.x - 1) / (int)blockDim.x;
+  const int per_g = N <= (int)blockDim.x ? 1 : (N + blockDim.x - 1) / (int)blockDim.x;
   const int g0 = min(tid * per_g, N), g1 = min(g0 + per_g, N);
   auto plan = [&](int g) {
     GroupPlan x;
@@ -212,82 +240,88 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     x.start = starts[g];
     x.members = blocks > 0 ? starts[g + 1] - starts[g] : 0;
     x.lead = blocks > 0 ? lead[g] : 0;
-    x.tiles = (int)(((int64_t)blocks << p.block_shift) / BN);
+    x.tiles = blocks << (p.block_shift - 6);
     x.pairs = (x.members * p.group_size + kPairRows - 1) / kPairRows;
     x.pad = 0;
     x.cost0 = 0;
     return x;
   };
+  static_assert(BN == 64, "a shift by 6");
   auto cost_of = [&](const GroupPlan &x) {
     return head_cost(x, p.group_size) * p.num_kv_heads;
   };
-  const int rows = tail_rows(D);
-  const int per = (S + blockDim.x - 1) / (int)blockDim.x;
+  const int per = S <= (int)blockDim.x ? 1 : (S + blockDim.x - 1) / (int)blockDim.x;
   const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
   auto first = [&](int s, int L, int &g) {
     g = ok ? seq_of(starts, N, s) : 0;
     return L > 0 && ok && count[g] >= 2 ? eff[g] << p.block_shift : 0;
   };
-  int64_t at[3] = {0, 0, 0}, total[3];  // cost, tiles of the tails; tiles without sharing
-  for (int g = g0; g < g1; ++g) at[0] += cost_of(plan(g));
+  // Cost of the prefixes; tiles of the tails, and without sharing (2^29 at most: both in
+  // one 64-bit sum).
+  int64_t at[2] = {0, 0}, sum[2];
+  int64_t my_cost = 0;  // (of the thread's last group, and sequence: mostly its only ones)
+  int my_g = 0, my_b = 0, my_L = 0;
+  for (int g = g0; g < g1; ++g) at[0] += my_cost = cost_of(plan(g));
   for (int s = s0; s < s1; ++s) {
-    int g;
-    const int L0 = per == 1 ? first_L : p.context_lens[s], L = tokens(L0);
-    at[1] += (L - first(s, L, g) + rows - 1) / rows;
-    at[2] += (L + rows - 1) / rows;
-    if (L != L0 || L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+    const int L0 = per == 1 ? first_L : p.context_lens[s];
+    my_L = tokens(L0);
+    my_b = first(s, my_L, my_g);
+    at[1] += (int64_t)tail_tiles(my_L - my_b, p.head_dim) << 32 | tail_tiles(my_L, p.head_dim);
+    if (tell && (my_L != L0 || my_L == 0)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
   }
-  scan_cta<3>(at, total, sums);
+  scan_cta<2>(at, sum, sums);
+  int64_t cost = sum[0];
+  int tile = (int)(at[1] >> 32), tiles = (int)(sum[1] >> 32);
   // Little work: reading every context whole takes less than a run of a prefix at its
   // best, and so nothing is shared.
   if (!p.share_always &&
-      (float)total[2] * p.num_kv_heads * tile_ns(p.group_size) + (float)kTailNs * p.ctas <=
-          (float)total[0] * kCostNs + (float)kPrefixNs * p.ctas) {
+      (float)(int)sum[1] * p.num_kv_heads * tile_ns(p.group_size) + (float)kTailNs * p.ctas <=
+          (float)cost * kCostNs + (float)kPrefixNs * p.ctas) {
     ok = false;
-    at[0] = total[0] = 0;
-    at[1] = at[2];
-    total[1] = total[2];
+    at[0] = cost = 0;
+    tile = (int)at[1];
+    tiles = (int)sum[1];
+    my_cost = my_b = my_g = 0;
+  }
+  if (tid == 0) {
+    totals->cost = cost;
+    totals->tiles = tiles;
+    totals->prefix_ctas = split_ctas(p, (float)cost, (float)tiles);
   }
   for (int g = g0; g < g1; ++g) {
     GroupPlan x = plan(g);
     x.cost0 = at[0];
-    p.groups[g] = x;
-    at[0] += cost_of(x);
+    groups[g] = x;
+    at[0] += per_g == 1 ? my_cost : cost_of(x);
   }
   for (int s = s0; s < s1; ++s) {
-    int g;
-    const int L = tokens(per == 1 ? first_L : p.context_lens[s]), b = first(s, L, g);
-    *reinterpret_cast<int4 *>(p.seqs + s) = make_int4((int)at[1], b, L, g);
-    at[1] += (L - b + rows - 1) / rows;
-  }
-  // The best of all splits, the one with the fewest CTAs on prefixes among equals.  (With
-  // work of both kinds there are two CTAs, so some split has a time.)
-  if (tid < 32) {
-    float best = INFINITY;
-    int best_n = 0;
-    for (int n = tid; n <= p.ctas; n += 32) {
-      const float t = time_with(p, (float)total[0], (float)total[1], n);
-      if (t < best) {
-        best = t;
-        best_n = n;
-      }
+    if (per > 1) {
+      my_L = tokens(p.context_lens[s]);
+      my_b = first(s, my_L, my_g);
     }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      const float t = __shfl_xor_sync(0xffffffffu, best, k);
-      const int n = __shfl_xor_sync(0xffffffffu, best_n, k);
-      if (t < best || (t == best && n < best_n)) {
-        best = t;
-        best_n = n;
-      }
-    }
-    if (tid == 0) {
-      p.totals->cost = total[0];
-      p.totals->tiles = total[1];
-      p.totals->prefix_ctas = best_n;
-    }
+    *reinterpret_cast<int4 *>(seqs + s) = make_int4(tile, my_b, my_L, my_g);
+    tile += tail_tiles(my_L - my_b, p.head_dim);
   }
 }
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p) {
+  extern __shared__ int plan_smem[];
+  __shared__ int64_t sums[32][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  plan_batch(p, plan_smem, sums, p.groups, p.seqs, p.totals);
+}
+
+// A batch's plan in shared memory: what stays, and what is where the tiles come later.
+struct NearPlan {
+  GroupPlan groups[kNearGroups];
+  Totals totals;
+};
+struct NearScratch {
+  SeqPlan seqs[kNearSeqs];
+  int64_t sums[32][2];
+  int ints[4 * kNearGroups + 1];
+};
 
 // ---------------------------------------------------------------------- 2. tails
 
@@ -310,7 +344,8 @@ struct WarpSmem {
 // fp32).  With at most four heads columns 4 to 7 repeat the heads of 0 to 3 and take the
 // second parts; eight heads need a second product.
 template <int D, int G>
-__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, uint8_t *smem_raw) {
+__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, const SeqPlan *seqs,
+                                      uint8_t *smem_raw) {
   using W = WarpSmem<D, G>;
   constexpr int kRows = W::kRows;
   constexpr int kCols = D / 8;              // 16-byte columns per row
@@ -327,7 +362,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
 
   for (int s = threadIdx.x; s < S; s += blockDim.x) {
-    const int4 x = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
+    const int4 x = *reinterpret_cast<const int4 *>(seqs + s);
     tile0[s] = x.x;
     begin[s] = x.y;
     len[s] = x.z;
@@ -622,7 +657,7 @@ __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
 template <int D>
 __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                          const SharedParams &p, const Totals &sum,
-                                         const int4 (&near)[2], uint8_t *smem_raw) {
+                                         const GroupPlan *groups, uint8_t *smem_raw) {
   using L = PrefixLayout<D>;
   constexpr int XR = D / 64;  // 128-byte swizzle regions across D
   constexpr int kKStages = L::kKStages, kVStages = L::kVStages;
@@ -729,32 +764,19 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
       while (x < x1) {
         if (x >= gp_end) {
           // The group at x: the last one that begins there or before.
-          int4 a, b;
-          if (p.num_groups <= 32) {
-            const int64_t at = (int64_t)(uint32_t)near[0].x | ((int64_t)near[0].y << 32);
-            const unsigned before = __ballot_sync(0xffffffffu, lane < p.num_groups && at <= x);
-            const int from = 31 - __clz((int)before);
-            a.x = __shfl_sync(0xffffffffu, near[0].x, from);
-            a.y = __shfl_sync(0xffffffffu, near[0].y, from);
-            a.z = __shfl_sync(0xffffffffu, near[0].z, from);
-            a.w = __shfl_sync(0xffffffffu, near[0].w, from);
-            b.x = __shfl_sync(0xffffffffu, near[1].x, from);
-            b.y = __shfl_sync(0xffffffffu, near[1].y, from);
-          } else {
-            int lo = grp, hi = p.num_groups;
-            while (hi - lo > 1) {
-              const int stride = (hi - lo + 31) / 32;
-              const int at = lo + lane * stride;
-              const bool before = at < hi && __ldcg(&p.groups[at].cost0) <= x;
-              const int k = __popc(__ballot_sync(0xffffffffu, before));
-              const int from = lo + (k - 1) * stride;
-              hi = min(hi, from + stride);
-              lo = from;
-            }
-            grp = lo;
-            a = __ldcg(reinterpret_cast<const int4 *>(p.groups + grp));
-            b = __ldcg(reinterpret_cast<const int4 *>(p.groups + grp) + 1);
+          int lo = grp, hi = p.num_groups;
+          while (hi - lo > 1) {
+            const int stride = (hi - lo + 31) / 32;
+            const int at = lo + lane * stride;
+            const bool before = at < hi && groups[at].cost0 <= x;
+            const int k = __popc(__ballot_sync(0xffffffffu, before));
+            const int from = lo + (k - 1) * stride;
+            hi = min(hi, from + stride);
+            lo = from;
           }
+          grp = lo;
+          const int4 a = reinterpret_cast<const int4 *>(groups + grp)[0];
+          const int4 b = reinterpret_cast<const int4 *>(groups + grp)[1];
           gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
           gp.start = a.z;
           gp.lead = a.w;
@@ -763,14 +785,14 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
           per_head = head_cost(gp, p.group_size);
           gp_end = gp.cost0 + per_head * p.num_kv_heads;
         }
-        u.kvh = (int)((x - gp.cost0) / per_head);
+        u.kvh = (int)quotient(x - gp.cost0, per_head);
         const int64_t head0 = gp.cost0 + u.kvh * per_head;
-        u.pair = (int)((x - head0) / full_unit_cost(gp));
+        u.pair = (int)quotient(x - head0, full_unit_cost(gp));
         const int64_t step0 = head0 + u.pair * full_unit_cost(gp) + kUnitCost;
         u.rows = min(kPairRows, gp.members * p.group_size - u.pair * kPairRows);
         const int each = step_cost(u.rows);
-        u.tile = x <= step0 ? 0 : (int)((x - step0 + each - 1) / each);
-        const int end = x1 <= step0 ? 0 : (int)min((int64_t)gp.tiles, (x1 - step0 + each - 1) / each);
+        u.tile = x <= step0 ? 0 : (int)quotient(x - step0 + each - 1, each);
+        const int end = x1 <= step0 ? 0 : (int)min((int64_t)gp.tiles, quotient(x1 - step0 + each - 1, each));
         u.n = end - u.tile;
         u.start = gp.start;
         u.lead = gp.lead;
@@ -1173,19 +1195,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (before any of tensor memory is taken, too: a kernel before the call may need it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // (the first 32 groups' plans are asked for beside the totals)
-  const int lane = threadIdx.x & 31;
-  int4 near[2] = {};
-  if (threadIdx.x < 32 && lane < p.num_groups) {
-    near[0] = __ldcg(reinterpret_cast<const int4 *>(p.groups + lane));
-    near[1] = __ldcg(reinterpret_cast<const int4 *>(p.groups + lane) + 1);
-  }
+  const GroupPlan *groups = p.groups;
+  const SeqPlan *seqs = p.seqs;
   Totals sum;
-  sum.cost = __ldcg(&p.totals->cost);
-  sum.tiles = __ldcg(&p.totals->tiles);
-  sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
-  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, p, sum, near, smem_raw);
-  else tails<D, G>(p, sum, smem_raw);
+  NearPlan *plan = reinterpret_cast<NearPlan *>(smem_raw + p.plan_at);
+  if (p.near) {
+    NearScratch *scratch = reinterpret_cast<NearScratch *>(smem_raw);
+    plan_batch(p, scratch->ints, scratch->sums, plan->groups, scratch->seqs, &plan->totals);
+    __syncthreads();
+    groups = plan->groups;
+    seqs = scratch->seqs;  // (both kinds of work have a barrier before their first tile)
+    sum = plan->totals;
+    if (blockIdx.x == 0) {  // (for the join)
+      for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x)
+        reinterpret_cast<int4 *>(p.seqs)[i] = reinterpret_cast<const int4 *>(seqs)[i];
+      for (int i = threadIdx.x; i < 2 * p.num_groups; i += blockDim.x)
+        reinterpret_cast<int4 *>(p.groups)[i] = reinterpret_cast<const int4 *>(groups)[i];
+      if (threadIdx.x == 0) *p.totals = sum;
+    }
+  } else {
+    if (p.num_groups <= kNearGroups) {  // (asked for beside the totals; read behind a barrier)
+      if (threadIdx.x < 2 * p.num_groups)
+        reinterpret_cast<int4 *>(plan->groups)[threadIdx.x] =
+            __ldcg(reinterpret_cast<const int4 *>(p.groups) + threadIdx.x);
+      groups = plan->groups;
+    }
+    sum.cost = __ldcg(&p.totals->cost);
+    sum.tiles = __ldcg(&p.totals->tiles);
+    sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
+  }
+  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, p, sum, groups, smem_raw);
+  else tails<D, G>(p, sum, seqs, smem_raw);
 }
 
 // ----------------------------------------------------------------------- 4. join
@@ -1204,7 +1244,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Shar
   const int64_t row = (int64_t)blockIdx.x * kRows + warp / kShare;
   const int s = (int)(min(row, rows - 1) / Hq), head = (int)(min(row, rows - 1) - (int64_t)s * Hq);
   const int j = head / G, g = head - j * G;
-  // (The plan is there: the launch before began after it, and this one after that.)
+  // (Planned by a launch of its own, the plan is there: the launch before began after it,
+  // and this one after that.)
+  if (p.near) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 seq = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
   Totals sum;
   sum.cost = __ldcg(&p.totals->cost);
@@ -1238,9 +1280,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Shar
     const int idx = (s - gp.start) * G + g, pair = idx / kPairRows;
     const int64_t step0 = gp.cost0 + j * head_cost(gp, G) + pair * full_unit_cost(gp) + kUnitCost;
     const int each = step_cost(gp.members * G - pair * kPairRows);
-    const int64_t c0 = step0 / len;
+    const int64_t c0 = quotient(step0, len);
     run_row = c0 * kPairRows + idx % kPairRows;
-    n_pre = (int)((step0 + (int64_t)(gp.tiles - 1) * each) / len - c0 + 1);
+    n_pre = (int)(quotient(step0 + (int64_t)(gp.tiles - 1) * each, len) - c0 + 1);
   }
   const int n = row < rows && seq.z > 0 ? n_tail + n_pre : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1387,14 +1429,22 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   if (sms <= 0) return PKV_ERR_CUDA;
   const int S = prm.num_seqs;
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
-  const int plan_smem = (4 * prm.num_groups + 1) * 4;
+  const bool near = S <= kNearSeqs && prm.num_groups <= kNearGroups &&
+                    S * room * prm.num_kv_heads * (4 * D) <= kNearBytes;
+  const int near_smem = (int)sizeof(NearPlan) + 16;
   const int seq_smem = (3 * S + 1) * 4;
-  int warps = (kMaxDynamicSmem - 1024 - seq_smem) / WarpSmem<D, G>::bytes;
+  int warps = (kMaxDynamicSmem - 1024 - seq_smem - near_smem) / WarpSmem<D, G>::bytes;
   if (warps > kWarpsMost) warps = kWarpsMost;
-  static_assert((kMaxDynamicSmem - 1024 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
+  static_assert((kMaxDynamicSmem - 2560 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
+  static_assert(sizeof(NearPlan) + 16 + 1024 <= 2560, "");
+  static_assert(PrefixLayout<D>::total + 1024 + 16 + sizeof(NearPlan) <= kMaxDynamicSmem, "");
   int smem = warps * WarpSmem<D, G>::bytes + seq_smem;
   if (smem < PrefixLayout<D>::total + 1024) smem = PrefixLayout<D>::total + 1024;
-  if (!kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr) ||
+  prm.near = near;
+  prm.plan_at = (smem + 15) & ~15;
+  smem += near_smem;
+  const int plan_smem = (4 * prm.num_groups + 1) * 4;
+  if ((!near && !kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr)) ||
       !kernel_smem_setup((const void *)shared_attn_kernel<D, G>, kThreads, smem, nullptr))
     return PKV_ERR_CUDA;
   // A CTA per SM, and no more than the longest possible batch has work for: a warp per
@@ -1410,9 +1460,10 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   if (ctas < 2) ctas = 2;
   prm.ctas = (int)ctas;
   prm.tail_warps = warps;
-  const int plan_threads = S <= 256 ? 256 : kPlanThreads;
-  cudaError_t err = launch_dependent<SharedParams, int>(shared_plan_kernel, 1, plan_threads,
-                                                        plan_smem, stream, prm, D);
+  cudaError_t err = cudaSuccess;
+  if (!near)
+    err = launch_dependent<SharedParams>(shared_plan_kernel, 1, S <= 256 ? 256 : kPlanThreads,
+                                         plan_smem, stream, prm);
   if (err == cudaSuccess)
     err = launch_dependent<CUtensorMap, CUtensorMap, SharedParams>(
         shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, prm);
@@ -1507,6 +1558,9 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.ctas = 0;
   prm.tail_warps = 0;
+  prm.near = 0;
+  prm.plan_at = 0;
+  prm.head_dim = head_dim;
   prm.loading = g_loading.load(std::memory_order_relaxed);
   prm.share_always = g_share_always.load(std::memory_order_relaxed);
   prm.qscale = scale * kLog2e;

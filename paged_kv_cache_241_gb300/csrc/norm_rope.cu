@@ -27,7 +27,12 @@ namespace {
 constexpr int kRopeWarps = 8;
 constexpr int kRopeTokens = 8;  // tokens of a CTA, where there are many
 constexpr int kRopeAhead = 2;   // tokens that a warp has asked for at a time
-constexpr int kRopePlaces = 3;  // stream: tokens that a warp has in shared memory
+// Stream: tokens that a warp has in shared memory, and warps of a CTA (one per SM).  16
+// prompts of 16 + 8 + 8 heads (537 MB): 89.5 us with 2 and 12 (88 % of a copy), 95.0 with
+// 3 and 8, 98.4 with 4 and 6, 90.7 with 2 and 10; from registers, without the copies
+// through shared memory, 100.8.
+constexpr int kRopePlaces = 2;
+constexpr int kRopeStreamWarps = 12;
 constexpr int kRopeSmem = 220 * 1024;
 constexpr int kRopeStreamTokens = 16;  // tokens per SM from which on they are streamed
 
@@ -238,10 +243,10 @@ __device__ __forceinline__ void bulk_wait_read() {  // all but the last N groups
 // A warp takes tokens by itself, every (number of warps)-th: the rows of q, k and v of
 // a token come as bulk copies into one of its places in shared memory, q and k are
 // normed and turned there, and all three leave as bulk copies, v without ever being in
-// a register.  Copies in of the next two tokens and out of the last one are under way
+// a register.  The next token's copies in and the last one's out are under way
 // meanwhile; no warp waits for another.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeWarps * 32, 1) norm_rope_stream_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;
   constexpr int kHeads = 32 / kLanes;
   extern __shared__ __align__(128) uint8_t stream_smem[];
@@ -431,7 +436,7 @@ pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
   const int64_t row = ((int64_t)prm.num_q_heads + prm.num_kv_heads * (prm.k_cache != nullptr ? 2 : 1)) * D * 2;
   const int64_t warp_bytes = (kRopePlaces * row + prm.rotary * 4 + kRopePlaces * 8 + 127) & ~(int64_t)127;
   int warps = warp_bytes <= kRopeSmem ? (int)(kRopeSmem / warp_bytes) : 0;
-  if (warps > kRopeWarps) warps = kRopeWarps;
+  if (warps > kRopeStreamWarps) warps = kRopeStreamWarps;
   if (prm.num_tokens > kRopeStreamTokens * (int64_t)sms && warps >= 4) {
     const int smem = (int)(warps * warp_bytes);
     int per_sm = 1;

@@ -10,10 +10,15 @@
 // the stack of free blocks a sequence's blocks go to or come from, and which rows of
 // the step are its own.
 //
-// One launch of one CTA, or of one cluster of eight.  Every CTA scans the lengths by
+// A launch of one CTA, or of one cluster of eight.  Every CTA scans the lengths by
 // itself (12 bytes a sequence); the sequences that end push their blocks; after a
 // cluster barrier all CTAs share the tables and the rows.  So lengths and counters
-// can be updated in place: nothing is written before everybody has read.
+// can be updated in place: nothing is written before everybody has read.  Many rows
+// (prompts) are left to a second launch over the whole GPU, which finds all it needs in
+// what the first one has written.
+//
+// Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
+// the lengths, one of blocks from the stack or a table, and the barriers between them.
 #include <cooperative_groups.h>
 
 #include "cta_scan.cuh"
@@ -30,6 +35,9 @@ constexpr int kPlanCluster = 8;     // portable cluster size
 // Up to so many rows and sequences one CTA of kPlanSmallSeqs threads does the step.
 constexpr int kPlanSmallRows = 2048;
 constexpr int kPlanSmallSeqs = 256;
+// From so many rows on they have a launch of their own.
+constexpr int kPlanManyRows = 16384;
+constexpr int kRowThreads = 256;
 
 struct PlanParams {
   const int32_t *new_lens;
@@ -51,6 +59,8 @@ struct PlanParams {
   int num_seqs;
   int max_blocks_per_seq;
   int block_shift;
+  int rows_after;    // the rows are left to plan_rows_kernel
+  int rows_16b;      // slots and positions are 16-byte aligned
 };
 
 __device__ __forceinline__ int saturated(int64_t x) {
@@ -91,6 +101,77 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s, bool tel
   return q;
 }
 
+// `each(lane, i)` for the items i < count of every lane, spread over the warp's lanes.
+template <typename F>
+__device__ __forceinline__ void for_items(int count, F each) {
+  const int lane = threadIdx.x & 31;
+  int incl = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  for (int i0 = 0; i0 < total; i0 += 32) {
+    const int i = i0 + lane;
+    int owner = 0;  // lanes whose items all come before i
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int last = __shfl_sync(0xffffffffu, incl, owner + o - 1);
+      if (last <= i) owner += o;
+    }
+    const int before = __shfl_sync(0xffffffffu, incl - count, owner & 31);
+    each(owner & 31, i - before, i < total);
+  }
+}
+
+// Slots and positions of the rows t0 .. t0 + kEach - 1.  first_row [S + 1]: the rows of
+// sequence s begin there; held[s]: tokens before them, or -1 - those when it gets no
+// slots; block_of(s, tokens before, block of the table): where its id is.
+template <int kEach, typename F>
+__device__ __forceinline__ void write_rows(const PlanParams &p, const int *first_row, const int *held,
+                                           int64_t t0, F block_of) {
+  const int shift = p.block_shift, S = p.num_seqs, rows = first_row[S];
+  int pos[kEach], blk[kEach];
+  bool real[kEach];
+  int s = -1;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t t = t0 + i;
+    pos[i] = 0;
+    blk[i] = -1;
+    real[i] = false;
+    if (t >= rows || t >= p.num_rows) continue;
+    if (s < 0) s = seq_of(first_row, S, (int)t);
+    else while (first_row[s + 1] <= t) ++s;
+    const int h = held[s], L = h < 0 ? -1 - h : h;
+    pos[i] = (int)((uint32_t)L + (uint32_t)(t - first_row[s]));
+    real[i] = h >= 0;
+    if (h >= 0) blk[i] = block_of(s, L, pos[i] >> shift);
+  }
+  int slot[kEach];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool in = blk[i] >= 0 && blk[i] < p.num_blocks;
+    bad = bad || (real[i] && !in);
+    slot[i] = in ? (blk[i] << shift) + (pos[i] & ((1 << shift) - 1)) : -1;
+  }
+  if (bad) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+  if (kEach == 4 && p.rows_16b && t0 + kEach <= p.num_rows) {
+    *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1 % kEach], slot[2 % kEach], slot[3 % kEach]);
+    *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1 % kEach], pos[2 % kEach], pos[3 % kEach]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (t0 + i < p.num_rows) {
+        p.slots[t0 + i] = slot[i];
+        p.positions[t0 + i] = pos[i];
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ int plan_smem[];
@@ -99,34 +180,35 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
   const int S = p.num_seqs, shift = p.block_shift;
   int *first_row = plan_smem;           // [S + 1]
   int *held = first_row + S + 1;        // [S]: L, or -1 - L when the sequence gets no slots
-  int *base = held + S;                 // [S]: blocks needed before it
+  int *base = held + S;                 // [S]: blocks needed before it; -1 - blocks given
+                                        // before it when it ends
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the grid is one cluster)
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int free_given = *p.num_free;
-  const int free0 = min(max(free_given, 0), p.capacity);
-  if (free0 != free_given && rank == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
-
   const int per = (S + blockDim.x - 1) / (int)blockDim.x;
   const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
   int64_t at[3] = {0, 0, 0}, total[3];  // give, need, rows
+  PlanSeq mine = {};                    // (the thread's last: its only one, mostly)
   for (int s = s0; s < s1; ++s) {
-    const PlanSeq q = plan_seq(p, s, rank == 0);
-    at[0] += q.give;
-    at[1] += q.need;
-    at[2] += q.n;
+    mine = plan_seq(p, s, rank == 0);
+    at[0] += mine.give;
+    at[1] += mine.need;
+    at[2] += mine.n;
   }
+  const int free0 = min(max(free_given, 0), p.capacity);
+  if (free0 != free_given && rank == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
   scan_cta<3>(at, total, sums3);
   const int left = (int)min((int64_t)free0 + total[0], (int64_t)p.capacity);
   if (free0 + total[0] > p.capacity && rank == 0 && tid == 0)
     flag_status(p.status, PKV_DEV_BAD_BLOCK);
   int64_t keys[1] = {0}, all_keys[1], taken = 0;
   {
-    int64_t need = at[1], row = at[2];
+    int64_t give = at[0], need = at[1], row = at[2];
     for (int s = s0; s < s1; ++s) {
-      const PlanSeq q = plan_seq(p, s, false);
+      const PlanSeq q = per == 1 ? mine : plan_seq(p, s, false);
       const bool no_blocks = q.need > 0 && need + q.need > left;
       const bool no_rows = q.n > 0 && row + q.n > p.num_rows;
       if (rank == 0 && (no_blocks || no_rows))
@@ -134,9 +216,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
       const bool refused = no_blocks || no_rows || q.out;
       first_row[s] = saturated(row);
       held[s] = refused ? -1 - q.L : q.L;
-      base[s] = saturated(need);
+      base[s] = q.ends ? -1 - saturated(min(give, (int64_t)p.capacity)) : saturated(need);
       if (!refused && q.need > 0) taken = need + q.need;
       if (!refused && !q.ends) keys[0] += q.L + q.n;
+      give += q.give;
       need += q.need;
       row += q.n;
     }
@@ -151,27 +234,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
   if (lane == 0) sums3[warp][0] = most;
   if (tid == 0) first_row[S] = saturated(total[2]);
   scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
-  // Sequences that end give their blocks back, the first one's first: at[0] of the
-  // thread's sequences are before its own.
-  {
-    int64_t give = at[0];
-    for (int s = s0; s < s1; ++s) {
-      const PlanSeq q = plan_seq(p, s, false);
-      if (!q.ends) continue;
-      // (base of a sequence that ends: where its blocks go)
-      base[s] = saturated(give);
-      give += q.give;
-    }
-  }
-  __syncthreads();
-  const int W = ctas * warps, w = rank * warps + warp;
-  for (int s = w; s < S; s += W) {
-    if (p.new_lens[s] != -1) continue;
-    const PlanSeq q = plan_seq(p, s, false);
-    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq + q.borrowed;
-    for (int i = lane; i < q.give; i += 32) {
-      const int64_t to = (int64_t)free0 + base[s] + i;
-      if (to < p.capacity) p.free_blocks[to] = row[i];
+  // Sequences that end give their blocks back, the first one's first.
+  // (few sequences to a warp: its lanes are for their blocks)
+  const int W = ctas * warps, w = warp * ctas + rank;
+  const int chunk = min((S + W - 1) / W, 32);
+  if (total[0] > 0) {
+    for (int c = w * chunk; c < S; c += W * chunk) {
+      const int s = c + lane;
+      int count = 0, from = 0, to = 0;
+      if (lane < chunk && s < S && base[s] < 0) {
+        const PlanSeq q = plan_seq(p, s, false);
+        count = q.give;
+        from = q.borrowed;
+        to = -1 - base[s];
+      }
+      for_items(count, [&](int owner, int i, bool live) {
+        const int at = __shfl_sync(0xffffffffu, from, owner) + i;
+        const int64_t place = (int64_t)free0 + __shfl_sync(0xffffffffu, to, owner) + i;
+        if (live && place < p.capacity)
+          p.free_blocks[place] = p.block_tables[(int64_t)(c + owner) * p.max_blocks_per_seq + at];
+      });
     }
   }
   // What comes back is on the stack, and nobody reads lengths or counters any more.
@@ -183,21 +265,47 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
     const int64_t i = (int64_t)left - 1 - b;
     return i >= 0 ? __ldcg(p.free_blocks + i) : -1;
   };
-  // Tables, lengths and sums: a warp per sequence; the first CTA writes the rest.
-  for (int s = w; s < S; s += W) {
-    const int L = held[s], n = first_row[s + 1] - first_row[s];
-    if (L < 0 || n == 0) continue;
-    const int bs1 = (1 << shift) - 1;
+  const int bs1 = (1 << shift) - 1;
+  // Rows: one a thread where that is enough of them.
+  const bool here = !p.rows_after || all_keys[0] >= 0x7FFFFFFF;
+  auto block_of = [&](int s, int L, int b) {
     const int have = (L + bs1) >> shift;
-    const int need = (int)(((int64_t)L + n + bs1) >> shift) - have;
-    int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq + have;
-    for (int i = lane; i < need; i += 32) row[i] = block_at((int64_t)base[s] + i);
+    return b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
+                    : block_at((int64_t)base[s] + b - have);
+  };
+  if (here) {
+    const int64_t threads = (int64_t)ctas * blockDim.x, me = (int64_t)rank * blockDim.x + tid;
+    if (p.num_rows <= threads) {
+      if (me < p.num_rows) write_rows<1>(p, first_row, held, me, block_of);
+    } else {
+      for (int64_t t0 = me * 4; t0 < p.num_rows; t0 += threads * 4)
+        write_rows<4>(p, first_row, held, t0, block_of);
+    }
   }
+  // Tables.
+  if (total[1] > 0) {
+    for (int c = w * chunk; c < S; c += W * chunk) {
+      const int s = c + lane;
+      int count = 0, have = 0, from = 0;
+      if (lane < chunk && s < S && held[s] >= 0 && base[s] >= 0) {
+        const int L = held[s], n = first_row[s + 1] - first_row[s];
+        have = (L + bs1) >> shift;
+        count = n == 0 ? 0 : (int)(((int64_t)L + n + bs1) >> shift) - have;
+        from = base[s];
+      }
+      for_items(count, [&](int owner, int i, bool live) {
+        const int at = __shfl_sync(0xffffffffu, have, owner) + i;
+        const int64_t b = (int64_t)__shfl_sync(0xffffffffu, from, owner) + i;
+        if (live) p.block_tables[(int64_t)(c + owner) * p.max_blocks_per_seq + at] = block_at(b);
+      });
+    }
+  }
+  // Lengths and sums.
   if (rank == ctas - 1) {
     int64_t key = keys[0];
     for (int s = s0; s < s1; ++s) {
       const int h = held[s], n = first_row[s + 1] - first_row[s];
-      const bool ends = p.new_lens[s] == -1 && h >= 0;
+      const bool ends = base[s] < 0 && h >= 0;
       const int after = ends ? 0 : h < 0 ? -1 : h + n;
       p.cu_q[s] = first_row[s];
       p.cu_k[s] = saturated(key);
@@ -215,45 +323,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
         flag_status(p.status, PKV_DEV_BAD_SEQLEN);
     }
   }
-  // Rows: four neighbours a thread.
-  const int rows = first_row[S];
-  const int64_t step = (int64_t)ctas * blockDim.x * 4;
-  for (int64_t t0 = ((int64_t)rank * blockDim.x + tid) * 4; t0 < p.num_rows; t0 += step) {
-    int slot[4], pos[4];
-    int s = -1, blk = -1, lb = -1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + i;
-      slot[i] = -1;
-      pos[i] = 0;
-      if (t >= rows || t >= p.num_rows) continue;
-      if (s < 0) s = seq_of(first_row, S, (int)t);
-      else while (first_row[s + 1] <= t) ++s, lb = -1;
-      const int h = held[s];
-      const int L = h < 0 ? -1 - h : h;
-      pos[i] = (int)((uint32_t)L + (uint32_t)(t - first_row[s]));
-      if (h < 0) continue;
-      const int b = pos[i] >> shift;
-      if (b != lb) {
-        lb = b;
-        const int have = (L + (1 << shift) - 1) >> shift;
-        blk = b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
-                       : block_at((int64_t)base[s] + b - have);
-        if (blk < 0 || blk >= p.num_blocks) {
-          flag_status(p.status, PKV_DEV_BAD_BLOCK);
-          blk = -1;
-        }
-      }
-      if (blk >= 0) slot[i] = (blk << shift) + (pos[i] & ((1 << shift) - 1));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t0 + i < p.num_rows) {
-        p.slots[t0 + i] = slot[i];
-        p.positions[t0 + i] = pos[i];
-      }
-    }
+}
+
+// The rows of a large step, from what plan_step_kernel has written: a sequence that was
+// refused has no keys, and its length is the one before the step.
+__global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(const PlanParams p) {
+  extern __shared__ int plan_smem[];
+  const int S = p.num_seqs;
+  int *first_row = plan_smem;     // [S + 1]
+  int *held = first_row + S + 1;  // [S] (as in plan_step_kernel)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (p.cu_k[S] == 0x7FFFFFFF) return;  // (the sums may have saturated: done by the first launch)
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    const int row = p.cu_q[s], n = p.cu_q[s + 1] - row;
+    const int after = p.new_context_lens[s];
+    first_row[s] = row;
+    const int before = after < 0 || after > room ? 0 : after;
+    held[s] = p.cu_k[s + 1] == p.cu_k[s] ? -1 - before : after - n;
   }
+  if (threadIdx.x == 0) first_row[S] = p.cu_q[S];
+  __syncthreads();
+  auto block_of = [&](int s, int, int b) { return p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]; };
+  const int64_t threads = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t t0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; t0 < p.num_rows; t0 += threads * 4)
+    write_rows<4>(p, first_row, held, t0, block_of);
 }
 
 }  // namespace
@@ -306,6 +401,9 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
 
+  prm.rows_after = num_rows >= kPlanManyRows ? 1 : 0;
+  prm.rows_16b = aligned16(slot_mapping) && aligned16(positions) ? 1 : 0;
+
   const bool small = num_rows <= kPlanSmallRows && num_seqs <= kPlanSmallSeqs;
   const int threads = small ? kPlanSmallSeqs : kPlanThreads;
   const int smem = (3 * num_seqs + 1) * 4;
@@ -324,6 +422,18 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+  cudaError_t err = cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+  if (prm.rows_after && err == cudaSuccess) {
+    const int sms = device_sm_count();
+    const int row_smem = (2 * num_seqs + 1) * 4;
+    if (sms <= 0 || !kernel_smem_setup((const void *)plan_rows_kernel, kRowThreads, row_smem, nullptr))
+      return PKV_ERR_CUDA;
+    const int64_t groups = (num_rows + 4 * kRowThreads - 1) / (4 * kRowThreads);
+    cfg.gridDim = dim3((unsigned)(groups < 2 * sms ? groups : 2 * sms));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = row_smem;
+    cfg.numAttrs = 1;  // (no cluster)
+    cudaLaunchKernelEx(&cfg, plan_rows_kernel, prm);
+  }
   return launch_status();
 }

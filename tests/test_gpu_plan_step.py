@@ -231,3 +231,39 @@ def test_agrees_with_the_block_manager(lib):
         theirs, ours = bm.slots(s, 0, n), slots[cu[s]:cu[s + 1]]
         assert (theirs % block == ours % block).all()
         assert len(set(zip(theirs // block, ours // block))) == -(-n // block)
+
+
+# From 16384 rows on they are written by a launch of their own.
+
+@pytest.mark.parametrize("seed", range(3))
+@pytest.mark.parametrize("S,high,new,block,free", [(40, 3000, 1500, 64, None), (700, 900, 120, 128, 30), (3, 100, 20000, 512, None)])
+def test_many_rows(lib, seed, S, high, new, block, free):
+    p = random_plan(seed, S, high, new, block, free=free)
+    p.rows = max(p.rows, 16384) + 3 * seed
+    p.check(lib)
+
+
+def test_many_rows_with_bad_lengths(lib):
+    wide = 1000
+    lens = [100, -5, wide * 64 + 1, 200, 256, 30, 60, 0]
+    new = [9000, 2000, 1000, 60, 1, -3, 10000, 70000]
+    p = Plan(lens, new, block=64, wide=wide, free=400, rows=25000)
+    p.check(lib)
+
+
+def test_many_rows_block_ids_out_of_range(lib):
+    p = Plan([10, 70, 64], [9000, 8000, 70], block=64)
+    p.tables[1, 1] = p.num_blocks
+    p.stack[p.free - 5] = -4
+    args = p.check(lib)
+    assert int(args["dev_status"].item()) == lib.DEV_BAD_BLOCK
+
+
+def test_many_rows_in_place_and_sums_that_saturate(lib):
+    S, wide = 3000, 1 << 14
+    p = Plan([0] * S, [1] * S, block=64, wide=wide, free=S, rows=20000)
+    p.lens = [64 * wide - 1] * S
+    p.tables[:, wide - 1] = np.arange(S) % p.num_blocks
+    args = p.device()
+    args["new_context_lens"], args["new_num_free"] = args["context_lens"], args["num_free"]
+    p.check(lib, args)
