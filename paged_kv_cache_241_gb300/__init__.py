@@ -107,6 +107,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_call = None  # the C part of the binding (csrc/pycall.c)
 
 
 class PkvError(RuntimeError):
@@ -117,7 +118,7 @@ class PkvError(RuntimeError):
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libpkv.so (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, _call
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -129,8 +130,25 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    _call = _load_call(lib)
     _lib = lib
     return lib
+
+
+def _load_call(lib):
+    """The C part of the binding: the checks and calls of the operators that are called
+    once a step or a layer and are shorter than their checks in Python."""
+    import torch
+
+    try:
+        from . import _pkv_call as call
+    except ImportError as e:
+        raise RuntimeError("the binding's C part is missing or of another interpreter: build it "
+                           "with `python -m paged_kv_cache_241_gb300.build`") from e
+    address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "pkv_plan_step", "pkv_norm_rope_store", "pkv_paged_decode_shared_attn")]
+    call.bind(torch.bfloat16, torch.int32, torch.int64, torch.uint8, *address)
+    return call
 
 
 def _check(status: int, what: str) -> None:
@@ -547,23 +565,34 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
     _check(st, "pkv_kv_evict")
 
 
-def _is_current(dev) -> bool:
-    """Whether a tensor's device is the current one (where the library launches)."""
+def _here(t, stream):
+    """(device, raw stream) of a call on tensor t, or (-1, 0) where t is not on the
+    current CUDA device (the library launches there)."""
     import torch
 
-    return dev >= 0 and torch._C._cuda_getDevice() == dev
+    dev = t.get_device()
+    if dev < 0 or torch._C._cuda_getDevice() != dev:
+        return -1, 0
+    return dev, _raw_stream(stream, dev)
 
 
-def _refuse(what, args, dev_status=None):
-    """Says what is wrong with a call's tensors: dtype, rank, layout or device.
-    args: (name, tensor or None, dtype, rank)."""
+def _refuse(what, args, dev_status):
+    """Says what is wrong with a call's tensors: dtype, rank, layout or device, or else
+    their shapes.  args: (name, tensor or None, dtype, rank)."""
+    import torch
+
     for name, t, dtype, ndim in args:
         if t is None:
             continue
         _need(t, dtype, name, ndim)
-        if not _is_current(t.get_device()):
+        if torch._C._cuda_getDevice() != t.get_device():
             raise ValueError(f"{what}: {name} is not on the current CUDA device")
-    raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
+    if dev_status is not None and (dev_status.dtype is not torch.int32 or
+                                   not dev_status.is_cuda or dev_status.numel() < 1 or
+                                   not dev_status.is_contiguous() or dev_status.dim() > 8 or
+                                   torch._C._cuda_getDevice() != dev_status.get_device()):
+        raise ValueError(f"{what}: dev_status must be an int32 tensor on the current CUDA device")
+    raise ValueError(f"{what}: inconsistent shapes")
 
 
 def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_context_lens,
@@ -576,14 +605,15 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
     new_context_lens may be context_lens, and new_num_free num_free."""
     import torch
 
-    lib = _lib or load()
-    i32 = torch.int32
-    dev = block_tables.get_device()
-    if not (_plain(dev, i32, block_tables, new_lens, context_lens, free_blocks, num_free,
-                   new_context_lens, new_num_free, slot_mapping, positions, cu_seqlens_q,
-                   cu_seqlens_k) and _is_current(dev) and
-            (borrowed_blocks is None or _plain(dev, i32, borrowed_blocks)) and
-            (dev_status is None or _plain_status(dev, dev_status)) and block_tables.dim() == 2):
+    if _call is None:
+        load()
+    dev, raw = _here(block_tables, stream)
+    st = -1 if dev < 0 else _call.plan_step(
+        dev, raw, new_lens, context_lens, block_tables, free_blocks, num_free, new_context_lens,
+        new_num_free, slot_mapping, positions, cu_seqlens_q, cu_seqlens_k, num_blocks, block_size,
+        borrowed_blocks, dev_status)
+    if st < 0:
+        i32 = torch.int32
         _refuse("plan_step", (
             ("new_lens", new_lens, i32, 1), ("context_lens", context_lens, i32, 1),
             ("block_tables", block_tables, i32, 2), ("free_blocks", free_blocks, i32, 1),
@@ -592,21 +622,6 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
             ("positions", positions, i32, 1), ("cu_seqlens_q", cu_seqlens_q, i32, 1),
             ("cu_seqlens_k", cu_seqlens_k, i32, 1),
             ("borrowed_blocks", borrowed_blocks, i32, 1)), dev_status)
-    S, wide = block_tables.shape
-    per_seq, sums, rows = (S,), (S + 1,), slot_mapping.shape
-    if new_lens.shape != per_seq or context_lens.shape != per_seq or \
-            new_context_lens.shape != per_seq or cu_seqlens_q.shape != sums or \
-            cu_seqlens_k.shape != sums or num_free.shape != (1,) or new_num_free.shape != (1,) or \
-            free_blocks.dim() != 1 or len(rows) != 1 or positions.shape != rows or \
-            (borrowed_blocks is not None and borrowed_blocks.shape != per_seq):
-        raise ValueError("plan_step: inconsistent shapes")
-    st = lib.pkv_plan_step(
-        new_lens.data_ptr(), context_lens.data_ptr(),
-        None if borrowed_blocks is None else borrowed_blocks.data_ptr(), block_tables.data_ptr(),
-        free_blocks.data_ptr(), num_free.data_ptr(), new_context_lens.data_ptr(),
-        new_num_free.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, rows[0], wide, _c_int32(block_size),
-        _c_int64(num_blocks), free_blocks.numel(), _addr(dev_status), _raw_stream(stream, dev))
     if st:
         raise PkvError(st, "pkv_plan_step")
 
@@ -626,31 +641,20 @@ def rope_turns(inv_freq, device="cuda"):
     return torch.from_numpy(turns).to(device)
 
 
-def _refuse_rows(what, rows, D):
-    """Says what is wrong with q, k or v.  rows: (name, tensor, shape)."""
+def _need_rows(t, name, dims):
+    """Checks q, k or v: [T, heads, D] with contiguous rows, at any distance (strides of
+    dims of size one, and of tokens of which there is one, say nothing)."""
     import torch
 
-    for name, t, shape in rows:
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-        if not t.is_cuda or not _is_current(t.get_device()):
-            raise ValueError(f"{name}: must be a CUDA tensor on the current device")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-        if _token_step(t, D) < 0:
-            raise ValueError(f"{name}: rows must be contiguous [heads, D]")
-
-
-def _token_step(t, D) -> int:
-    """Values between the tokens of t [T, heads, D] (0: contiguous); -1 when its rows are
-    not.  (Strides of dims of size one, and of tokens of which there is one, say nothing.)"""
-    step, head, value = t.stride()
-    if head == D and value == 1:
-        return step if t.shape[0] > 1 else 0
-    T, H, _ = t.shape
-    if (value != 1 and D > 1) or (head != D and H > 1):
-        return -1
-    return step if T > 1 else 0
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda or torch._C._cuda_getDevice() != t.get_device():
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device")
+    if t.dim() != 3 or any(d is not None and d != n for d, n in zip(dims, t.shape)):
+        raise ValueError(f"{name}: expected [T, heads, D] = {dims}, got {tuple(t.shape)}")
+    (T, H, D), (step, head, value) = t.shape, t.stride()
+    if (value != 1 and D > 1) or (head != D and H > 1) or (step <= 0 and T > 1):
+        raise ValueError(f"{name}: rows must be contiguous [heads, D], one behind the other")
 
 
 def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None,
@@ -663,60 +667,29 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
     projection).  Without caches k goes to k_out [T, Hkv, D] alone.  bf16."""
     import torch
 
-    lib = _lib or load()
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = q.get_device()
-    q_shape, k_shape = q.shape, k.shape
-    if len(q_shape) != 3 or len(k_shape) != 3:
-        raise ValueError("norm_rope_store: q and k must be [T, heads, D]")
-    T, Hq, D = q_shape
-    Hkv = k_shape[1]
-    store = k_cache is not None
-    if (v_cache is not None) is not store or (slot_mapping is not None) is not store:
-        raise ValueError("norm_rope_store: k_cache, v_cache and slot_mapping go together")
-    norm = q_weight is not None
-    if (k_weight is not None) is not norm:
-        raise ValueError("norm_rope_store: q_weight and k_weight go together")
-    kv_shape = (T, Hkv, D)
-    rows = (("q", q, q_shape), ("k", k, kv_shape), ("v", v, kv_shape)) if store else \
-        (("q", q, q_shape), ("k", k, kv_shape))
-    steps = [0, 0, 0]
-    for i, (_, t, shape) in enumerate(rows):
-        if t.dtype is not bf16 or t.get_device() != dev or t.shape != shape:
-            _refuse_rows("norm_rope_store", rows, D)
-        steps[i] = _token_step(t, D)
-    if min(steps) < 0 or not _is_current(dev):
-        _refuse_rows("norm_rope_store", rows, D)
-    if not (_plain(dev, bf16, q_out) and _plain(dev, i32, positions) and
-            _plain(dev, torch.int64, turns) and
-            (not store or _plain(dev, bf16, k_cache, v_cache) and _plain(dev, i32, slot_mapping)) and
-            (not norm or _plain(dev, bf16, q_weight, k_weight)) and
-            (k_out is None or _plain(dev, bf16, k_out)) and
-            (dev_status is None or _plain_status(dev, dev_status))):
+    if _call is None:
+        load()
+    dev, raw = _here(q, stream)
+    st = -1 if dev < 0 else _call.norm_rope_store(
+        dev, raw, q_out, q, k, v, positions, turns, k_cache, v_cache, slot_mapping, k_out,
+        q_weight, k_weight, eps, interleaved, amplitude, dev_status)
+    if st < 0:
+        bf16, i32 = torch.bfloat16, torch.int32
+        store = [t is not None for t in (k_cache, v_cache, slot_mapping)]
+        if any(store) != all(store):
+            raise ValueError("norm_rope_store: k_cache, v_cache and slot_mapping go together")
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("norm_rope_store: q_weight and k_weight go together")
+        _need_rows(q, "q", (None, None, None))
+        _need_rows(k, "k", (q.shape[0], None, q.shape[2]))
+        if store[0]:
+            _need_rows(v, "v", tuple(k.shape))
         _refuse("norm_rope_store", (
             ("q_out", q_out, bf16, 3), ("positions", positions, i32, 1),
             ("turns", turns, torch.int64, 1), ("k_out", k_out, bf16, 3),
             ("q_weight", q_weight, bf16, 1), ("k_weight", k_weight, bf16, 1),
             ("k_cache", k_cache, bf16, 4), ("v_cache", v_cache, bf16, 4),
             ("slot_mapping", slot_mapping, i32, 1)), dev_status)
-    NB = BS = 0
-    per_token = (T,)
-    if store:
-        cache_shape = k_cache.shape
-        if len(cache_shape) != 4 or cache_shape[2] != Hkv or cache_shape[3] != D or \
-                v_cache.shape != cache_shape or slot_mapping.shape != per_token:
-            raise ValueError("norm_rope_store: inconsistent shapes of the caches or slots")
-        NB, BS = cache_shape[0], cache_shape[1]
-    if q_out.shape != q_shape or positions.shape != per_token or turns.dim() != 1 or \
-            (k_out is not None and k_out.shape != k_shape) or \
-            (norm and (q_weight.shape != (D,) or k_weight.shape != (D,))):
-        raise ValueError("norm_rope_store: inconsistent shapes")
-    st = lib.pkv_norm_rope_store(
-        q_out.data_ptr(), _addr(k_out), q.data_ptr(), k.data_ptr(), v.data_ptr() if store else None,
-        _addr(k_cache), _addr(v_cache), _addr(slot_mapping), positions.data_ptr(),
-        turns.data_ptr(), _addr(q_weight), _addr(k_weight), T, Hq, Hkv, D, steps[0], steps[1],
-        steps[2], 2 * turns.numel(), 1 if interleaved else 0, float(eps), float(amplitude), NB, BS,
-        _addr(dev_status), _raw_stream(stream, dev))
     if st:
         raise PkvError(st, "pkv_norm_rope_store")
 
@@ -738,33 +711,20 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
     once (see include/pkv.h; BlockManager.prefix_groups finds groups)."""
     import torch
 
-    lib = _lib or load()
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = q.get_device()
-    q_shape, cache_shape, table_shape = q.shape, k_cache.shape, block_tables.shape
-    if not (_plain(dev, bf16, q, out, k_cache, v_cache) and _is_current(dev) and
-            _plain(dev, i32, block_tables, context_lens, group_starts, shared_blocks) and
-            _plain(dev, torch.uint8, workspace) and
-            (dev_status is None or _plain_status(dev, dev_status)) and
-            len(q_shape) == 3 and len(cache_shape) == 4 and len(table_shape) == 2):
+    if _call is None:
+        load()
+    dev, raw = _here(q, stream)
+    st = -1 if dev < 0 else _call.paged_decode_shared_attn(
+        dev, raw, out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
+        shared_blocks, scale, workspace, dev_status)
+    if st < 0:
+        bf16, i32 = torch.bfloat16, torch.int32
         _refuse("paged_decode_shared_attn", (
             ("out", out, bf16, 3), ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4),
             ("v_cache", v_cache, bf16, 4), ("block_tables", block_tables, i32, 2),
             ("context_lens", context_lens, i32, 1), ("group_starts", group_starts, i32, 1),
             ("shared_blocks", shared_blocks, i32, 1), ("workspace", workspace, torch.uint8, 1)),
             dev_status)
-    S, Hq, D = q_shape
-    NB, BS, Hkv, Dc = cache_shape
-    groups = shared_blocks.numel()
-    if Dc != D or out.shape != q_shape or table_shape[0] != S or context_lens.shape != (S,) or \
-            v_cache.shape != cache_shape or shared_blocks.dim() != 1 or \
-            group_starts.shape != (groups + 1,):
-        raise ValueError("paged_decode_shared_attn: inconsistent shapes")
-    st = lib.pkv_paged_decode_shared_attn(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        block_tables.data_ptr(), context_lens.data_ptr(), group_starts.data_ptr(),
-        shared_blocks.data_ptr(), S, groups, Hq, Hkv, D, BS, table_shape[1], NB, float(scale),
-        workspace.data_ptr(), workspace.numel(), _addr(dev_status), _raw_stream(stream, dev))
     if st:
         raise PkvError(st, "pkv_paged_decode_shared_attn")
 

@@ -3,8 +3,9 @@
     python -m paged_kv_cache_241_gb300.build
 
 Compiles every csrc/*.cu (and the host-only *.cpp) in parallel with nvcc and
-links libpkv.so next to this file.  No CMake; a rebuild only recompiles sources
-newer than their object.
+links libpkv.so next to this file; beside it the C part of the Python binding
+(csrc/pycall.c), for the interpreter that runs this.  No CMake; a rebuild only
+recompiles sources newer than their object.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -51,6 +53,25 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def call_module() -> str:
+    """Where the C part of the binding is for this interpreter."""
+    return os.path.join(HERE, "_pkv_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def _build_call_module() -> None:
+    src, out = os.path.join(CSRC, "pycall.c"), call_module()
+    if os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(src), _headers_mtime()):
+        return
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler for the Python binding")
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           src, "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose_ptxas: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
@@ -63,6 +84,7 @@ def build(verbose_ptxas: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_call_module()
     return LIB
 
 

@@ -336,3 +336,19 @@ def test_many_rows_too_wide_to_stream(lib):
     lib.norm_rope_store(r.q_out[:700], r.q[:700], r.k[:700], r.v[:700], r.positions[:700], turns, r.kc, r.vc, r.slots[:700], q_weight=r.qw, k_weight=r.kw)
     torch.cuda.synchronize()
     assert torch.equal(q[:700], r.q_out[:700])
+
+
+def test_rows_that_are_no_rows_are_refused(lib):
+    """Views whose heads or values are apart, or whose tokens are all the same one."""
+    r = Rows(6, 4, 2, 64, 64, packed=False)
+    wide = torch.zeros(6, 4, 128, dtype=torch.bfloat16, device="cuda")
+    for q in (wide[..., ::2], wide[:, :, :64], r.q[:1].expand(6, 4, 64), r.q.transpose(0, 1).contiguous().transpose(0, 1)):
+        with pytest.raises(ValueError, match="rows must be contiguous"):
+            r.call(lib, q=q)
+    for bad in (dict(k=r.k[:5]), dict(v=r.v[:, :1]), dict(positions=r.positions[:5]), dict(turns=r.positions), dict(slot_mapping=r.slots.long()),
+                dict(q_weight=r.qw[:32]), dict(q_out=r.q_out[:, :, :32]), dict(v_cache=r.vc[:1]),
+                dict(dev_status=torch.zeros(0, dtype=torch.int32, device="cuda"))):
+        with pytest.raises((ValueError, TypeError)):
+            r.call(lib, **bad)
+    with pytest.raises(ValueError, match="inconsistent shapes"):
+        lib.norm_rope_store(r.q_out, r.q, r.k, None, r.positions, lib.rope_turns(r.inv_freq), k_out=r.k_out[:3])

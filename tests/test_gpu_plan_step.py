@@ -267,3 +267,21 @@ def test_many_rows_in_place_and_sums_that_saturate(lib):
     args = p.device()
     args["new_context_lens"], args["new_num_free"] = args["context_lens"], args["num_free"]
     p.check(lib, args)
+
+
+def test_refusals_of_the_binding(lib):
+    a = Plan([5, 300], [1, 1]).device()
+    for name in a:
+        if not torch.is_tensor(a[name]):
+            continue
+        with pytest.raises((ValueError, TypeError)):
+            lib.plan_step(**{**a, name: a[name].long()})
+        if name not in ("free_blocks", "dev_status"):
+            with pytest.raises(ValueError):
+                lib.plan_step(**{**a, name: torch.cat([a[name], a[name]])})
+        with pytest.raises(ValueError):
+            lib.plan_step(**{**a, name: a[name].cpu()})
+    with pytest.raises(lib.PkvError, match="UNSUPPORTED"):
+        lib.plan_step(**{**a, "block_size": 2**32 + 256})
+    with pytest.raises(lib.PkvError, match="INVALID_ARG"):
+        lib.plan_step(**{**a, "num_blocks": -2**70})
