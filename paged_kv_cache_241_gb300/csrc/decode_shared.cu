@@ -1140,7 +1140,8 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
                                          u.kvh * p.group_size + idx % p.group_size
                                    : (int64_t)blockIdx.x * kPairRows + r;
         // (eight dims of a row at a time: the same with eight dims of all rows together,
-        // whose stores fill whole lines, ended a piece 0.5 us sooner and the join 1.5 later)
+        // whose stores fill whole lines, ended a piece 0.5 us sooner and the join 1.5 later;
+        // rows turned through shared memory into whole lines took 1 us more)
         float *o = (u.first ? p.first_o : p.run_o) + at * D;
         const int c0 = both ? 0 : h * (D / 2), c1 = both ? D : c0 + D / 2;
 #pragma unroll 1
