@@ -595,6 +595,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
 struct Piece {
   int start, lead, kvh, pair, rows, tile, n;
   int first;  // it begins where the unit does: its parts are filed by row, else by run
+  int once;   // no other unit reads its keys
 };
 
 template <int D>
@@ -750,6 +751,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
   if (warp == kKWarp) {
     // Warp 0 walks the run (handing its pieces to the other roles) and loads Q and K.
     const bool loads = (int)blockIdx.x < p.loading;
+    const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
     int iu = 0, g = 0, q_loads = 0;
     bool ok = true;
     int64_t x = x0;
@@ -797,6 +799,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
         u.start = gp.start;
         u.lead = gp.lead;
         u.first = u.tile == 0;
+        u.once = gp.members * p.group_size <= kPairRows;
         x = step0 + (int64_t)end * each;
         if (u.n > 0) {
           have = true;
@@ -845,8 +848,8 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
           }
           mbar_arrive_expect_tx(&k_full[st], L::kKVBytes);
           for (int xr = 0; xr < XR; ++xr)
-            tma_load_4d(sK + st * L::kKVBytes + xr * BN * 128, &tm_k, &k_full[st], xr * 64, u.kvh,
-                        off, from);
+            tma_load_4d_hint(sK + st * L::kKVBytes + xr * BN * 128, &tm_k, &k_full[st], xr * 64,
+                             u.kvh, off, from, u.once ? once : again);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -869,7 +872,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     constexpr int kChunks = D / 8;          // 16-byte chunks of a row
     constexpr int kRowsPer = 32 / kChunks;  // rows per warp-wide copy
     const int col = lane % kChunks, row0 = lane / kChunks;
-    const uint64_t policy = l2_policy_evict_normal();
+    const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
     int iu = 0, g = 0, published = 0;
     bool ok = true;
     Piece u;
@@ -897,7 +900,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
 #pragma unroll 8
         for (int r = 0; r < BN / kRowsPer; ++r) {
           const int at = row0 + r * kRowsPer;
-          copy16(dst + at * 128 + (((col & 7) ^ (at & 7)) << 4), src + r * step, true, policy);
+          copy16(dst + at * 128 + (((col & 7) ^ (at & 7)) << 4), src + r * step, true, u.once ? once : again);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (g - published >= kAhead) {
