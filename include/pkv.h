@@ -471,8 +471,9 @@ pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *key_weights
  * Written, for the step's num_rows rows of which cu_seqlens_q[num_seqs] are in use:
  *   slot_mapping[r], positions[r]   (-1 and 0 behind the last row in use)
  *   cu_seqlens_q, cu_seqlens_k      sums of n, and of the lengths after the step
- *   new_context_lens, *new_num_free (may be the same arrays as context_lens and
- *                                   num_free; otherwise a call can be repeated)
+ *   new_context_lens, *new_num_free (may be context_lens and num_free themselves, but
+ *                                   not overlap them otherwise, PKV_ERR_INVALID_ARG;
+ *                                   where they are others, a call can be repeated)
  *
  * A sequence whose blocks the stack does not hold is refused, PKV_DEV_NO_BLOCKS, and
  * with it all later ones that need any: those keep what they have, their rows have

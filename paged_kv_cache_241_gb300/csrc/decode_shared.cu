@@ -63,8 +63,7 @@ struct GroupPlan {
   int lead;       // the sequence whose row of the block tables is read
   int members;
   int tiles;      // steps of 64 keys (0: nothing is shared)
-  int pairs;      // units of one kv head
-  int pad;
+  int pad[2];
 };
 // The cost of a step, in kCostNs: of a unit with two row tiles 4 (its products), of one
 // with a single row tile 3 (its loads).  A unit's beginning costs kUnitCost ahead of its
@@ -174,7 +173,8 @@ __device__ __forceinline__ int split_ctas(const SharedParams &p, float cost, flo
   // a / n + kPrefixNs = b / (ctas - n) + kTailNs, solved for n: the whole number beside
   // it that ends sooner (one CTA of a kind at least).
   const float N = p.ctas, d = kPrefixNs - kTailNs, e = d * N - a - b;
-  const float n = (e + sqrtf(e * e + 4.f * d * a * N)) / (2.f * d);
+  const float root = sqrtf(e * e + 4.f * d * a * N);
+  const float n = e >= 0.f ? (e + root) / (2.f * d) : 2.f * a * N / (root - e);  // (no cancellation)
   auto time = [&](float n) {
     return fmaxf(__fdividef(a, n) + kPrefixNs, __fdividef(b, N - n) + kTailNs);
   };
@@ -241,8 +241,7 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
     x.members = blocks > 0 ? starts[g + 1] - starts[g] : 0;
     x.lead = blocks > 0 ? lead[g] : 0;
     x.tiles = blocks << (p.block_shift - 6);
-    x.pairs = (x.members * p.group_size + kPairRows - 1) / kPairRows;
-    x.pad = 0;
+    x.pad[0] = x.pad[1] = 0;
     x.cost0 = 0;
     return x;
   };
@@ -650,7 +649,7 @@ __device__ __forceinline__ int chain_steps(const Piece &u, int h) {
   return u.rows > BM ? u.n : (u.n + 1 - h) >> 1;
 }
 
-// Two bf16 cut (not rounded) from two floats, packed; the floats that they are.
+// Two floats cut (not rounded) to bf16, packed.
 __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }

@@ -379,6 +379,11 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
     return PKV_ERR_INVALID_ARG;
   if (num_rows > 0 && (!slot_mapping || !positions)) return PKV_ERR_INVALID_ARG;
   if (free_capacity > 0 && !free_blocks) return PKV_ERR_INVALID_ARG;
+  // (the same lengths in and out, or others: nothing between)
+  const uintptr_t in = reinterpret_cast<uintptr_t>(context_lens);
+  const uintptr_t after = reinterpret_cast<uintptr_t>(new_context_lens);
+  if (in != after && (in < after ? after - in : in - after) < (uintptr_t)num_seqs * 4)
+    return PKV_ERR_INVALID_ARG;
 
   PlanParams prm;
   prm.new_lens = new_lens;

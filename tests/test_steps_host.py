@@ -36,6 +36,9 @@ def test_plan_step_rejects_bad_arguments(lib):
         assert plan_call(lib, **bad) == 1, bad
     for name in ("new_lens", "lens", "tables", "free", "num_free", "new_context", "new_free", "slots", "positions", "cu_q", "cu_k"):
         assert plan_call(lib, **{name: NULL}) == 1, name
+    # the lengths after the step in a part of those before it
+    at = lambda n: ctypes.c_void_p(0x10000 + 4 * n)
+    assert plan_call(lib, new_context=at(1)) == 1 and plan_call(lib, new_context=at(3)) == 1 and plan_call(lib, new_context=at(-2)) == 1
     for bad in (dict(BS=100), dict(BS=32), dict(S=16385), dict(rows=2**31 - 1), dict(capacity=2**31), dict(NB=2**31 // 256), dict(maxb=2**23)):
         assert plan_call(lib, **bad) == 2, bad
 
@@ -229,3 +232,18 @@ def test_oracle_rotation_keeps_lengths_and_composes():
         assert np.allclose(np.einsum("hd,hd->h", a[0], a[1]), np.einsum("hd,hd->h", b[0], b[1]))
     n = steps.norm_rope(x, [0, 0, 0], f, weight=np.full(16, 2.0), eps=0.0)
     assert np.allclose((n**2).mean(-1), 4.0)
+
+
+def test_the_shared_decode_takes_tensor_memory_after_the_wait_for_the_kernel_before():
+    """Read as text: the attention is a programmatic dependent, of whatever precedes the call where it plans by itself.  Were it to
+    take all of tensor memory before it waits, a kernel before it that has yet to allocate its own on the same SM would wait for it,
+    and it for that kernel's end."""
+    import os
+    import re
+
+    text = open(os.path.join(os.path.dirname(pkv.__file__), "csrc", "decode_shared.cu")).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    kernel = text.split("shared_attn_kernel(", 1)[1]
+    assert kernel.index("griddepcontrol.wait") < kernel.index("prefixes<D>(")
+    assert "tmem_alloc(" not in kernel.split("shared_join_kernel", 1)[0]  # (it is in prefixes, called behind the wait)
+    assert text.count("tmem_alloc(") == 1 and "tmem_alloc(" in text.split("void prefixes(", 1)[1]
