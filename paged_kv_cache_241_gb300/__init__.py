@@ -630,15 +630,14 @@ def rope_turns(inv_freq, device="cuda"):
     """What norm_rope_store takes for the frequencies inv_freq (radians per
     position of each pair, in 64 bits, already scaled for long contexts where they
     are to be): int64 [rotary_dim / 2] on `device`."""
-    import numpy as np
     import torch
 
-    f = np.ascontiguousarray(torch.as_tensor(inv_freq, dtype=torch.float64).cpu().numpy())
-    if f.ndim != 1:
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if f.dim() != 1:
         raise ValueError("rope_turns: inv_freq must have one dim")
-    turns = np.empty(f.shape, dtype=np.int64)
-    _check(load().pkv_rope_turns(f.ctypes.data, f.size, turns.ctypes.data), "pkv_rope_turns")
-    return torch.from_numpy(turns).to(device)
+    turns = torch.empty(f.shape, dtype=torch.int64)
+    _check(load().pkv_rope_turns(f.data_ptr(), f.numel(), turns.data_ptr()), "pkv_rope_turns")
+    return turns.to(device)
 
 
 def _need_rows(t, name, dims):
@@ -696,10 +695,14 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
 
 def decode_shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
                             device="cuda"):
-    """Allocate a workspace for paged_decode_shared_attn."""
+    """Allocate a workspace for paged_decode_shared_attn (it needs no initialisation)."""
+    import torch
+
     n = int(load().pkv_decode_shared_workspace_size(*map(_c_int32, (
         num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim))))
-    return _workspace(n, "decode_shared_workspace", device)
+    if n == 0:
+        raise ValueError("decode_shared_workspace: no workspace for these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_lens, group_starts,

@@ -38,8 +38,8 @@ constexpr int kMaxTokens = 1 << 20;      // of a sequence
 constexpr int kPlanThreads = 1024;
 constexpr int kWarpsMost = 8;            // warps per CTA of the tails (one CTA per SM)
 constexpr int kStages = 3;               // ring of tiles per warp
-constexpr int kMaxWarps = 4096;          // warps of the tails' grid at most (places for parts)
-constexpr int kMaxCtas = 512;            // CTAs of the attention's grid at most (places for parts)
+constexpr int kMaxCtas = 160;            // CTAs of the attention's grid at most (places for
+constexpr int kMaxWarps = kMaxCtas * kWarpsMost;  // parts; a GB300 has 152 SMs)
 constexpr int kThreads = 384;            // of the attention's CTAs
 // A batch is planned by every CTA for itself where its tables have room for no more K and
 // V than kNearBytes, in at most so many sequences and groups: two short sequences 10.6 ->
@@ -1459,7 +1459,6 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   int64_t ctas = (tiles + warps - 1) / warps + steps;
   if (ctas > sms) ctas = sms;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  if (ctas * warps > kMaxWarps) ctas = kMaxWarps / warps;
   if (ctas < 2) ctas = 2;
   prm.ctas = (int)ctas;
   prm.tail_warps = warps;
