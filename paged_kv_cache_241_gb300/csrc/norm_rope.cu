@@ -58,6 +58,7 @@ struct RopeParams {
   int rotary;           // R
   int tokens_per_cta;
   int warp_bytes;       // shared memory of a warp (stream)
+  int first_heads;      // query heads of the first half of a token (stream; 0: no halves)
   float eps;
   float amplitude;
 };
@@ -240,11 +241,12 @@ __device__ __forceinline__ void bulk_wait_read() {  // all but the last N groups
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// A warp takes tokens by itself, every (number of warps)-th: the rows of q, k and v of
-// a token come as bulk copies into one of its places in shared memory, q and k are
-// normed and turned there, and all three leave as bulk copies, v without ever being in
-// a register.  The next token's copies in and the last one's out are under way
-// meanwhile; no warp waits for another.
+// A warp takes tokens by itself, every (number of warps)-th, or halves of them where
+// tokens are wide: the first half is a token's first query heads, the second the others
+// with its keys and values, about as much.  An item's rows come as bulk copies into one of
+// the warp's places in shared memory, q and k are normed and turned there, and all leave as
+// bulk copies, v without ever being in a register.  The next item's copies in and the last
+// one's out are under way meanwhile; no warp waits for another.
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;
@@ -254,8 +256,12 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
   const int R = p.rotary, half = R >> 1;
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
   const bool store = p.k_cache != nullptr, norm = p.q_weight != nullptr;
-  const uint32_t q_bytes = Hq * D * 2, kv_bytes = Hkv * D * 2;
-  const uint32_t row_bytes = q_bytes + kv_bytes * (store ? 2 : 1);
+  const int halves = p.first_heads > 0 ? 1 : 0;
+  const int Q0 = p.first_heads;  // query heads of the first half
+  const uint32_t q0_bytes = Q0 * D * 2, q1_bytes = (Hq - Q0) * D * 2, kv_bytes = Hkv * D * 2;
+  const uint32_t half1_bytes = q1_bytes + kv_bytes * (store ? 2 : 1);
+  const uint32_t row_bytes = q0_bytes > half1_bytes ? q0_bytes : half1_bytes;  // of a place
+  const int64_t items = p.num_tokens << halves;
   uint8_t *rows = stream_smem + (size_t)warp * p.warp_bytes;   // [kRopePlaces][row_bytes]
   float *angles = reinterpret_cast<float *>(rows + kRopePlaces * row_bytes);  // [cos: R/2, sin: R/2]
   uint64_t *full = reinterpret_cast<uint64_t *>(angles + R);
@@ -270,16 +276,22 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
   const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t first = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   const uint64_t policy = l2_policy_evict_first();
-  auto load = [&](int64_t t, int place) {  // (lane 0)
+  auto load = [&](int64_t item, int place) {  // (lane 0)
+    const int64_t t = item >> halves;
     uint8_t *to = rows + place * row_bytes;
-    mbar_arrive_expect_tx(&full[place], row_bytes);
-    bulk_load(to, p.q + t * p.q_stride, q_bytes, &full[place], policy);
-    bulk_load(to + q_bytes, p.k + t * p.k_stride, kv_bytes, &full[place], policy);
-    if (store) bulk_load(to + q_bytes + kv_bytes, p.v + t * p.v_stride, kv_bytes, &full[place], policy);
+    if (halves && (item & 1) == 0) {
+      mbar_arrive_expect_tx(&full[place], q0_bytes);
+      bulk_load(to, p.q + t * p.q_stride, q0_bytes, &full[place], policy);
+      return;
+    }
+    mbar_arrive_expect_tx(&full[place], half1_bytes);
+    if (q1_bytes > 0) bulk_load(to, p.q + t * p.q_stride + Q0 * D, q1_bytes, &full[place], policy);
+    bulk_load(to + q1_bytes, p.k + t * p.k_stride, kv_bytes, &full[place], policy);
+    if (store) bulk_load(to + q1_bytes + kv_bytes, p.v + t * p.v_stride, kv_bytes, &full[place], policy);
   };
   if (lane == 0)
     for (int i = 0; i < kRopePlaces - 1; ++i)
-      if (first + i * step < p.num_tokens) load(first + i * step, i);
+      if (first + i * step < items) load(first + i * step, i);
 
   const int j = lane % kLanes, sub = lane / kLanes;
   const bool rotates = 16 * j < R;
@@ -303,16 +315,18 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
     weights(p.k_weight, wk);
   }
   int position = 0, slot_next = -1;
-  if (first < p.num_tokens) {
-    if (R > 0) position = p.positions[first];
-    if (store) slot_next = p.slots[first];
+  if (first < items) {
+    if (R > 0) position = p.positions[first >> halves];
+    if (store) slot_next = p.slots[first >> halves];
   }
   int place = 0, phase = 0;
   bool ok = true;
-  for (int64_t t = first; t < p.num_tokens; t += step) {
+  for (int64_t item = first; item < items; item += step) {
+    const int64_t t = item >> halves;
+    const bool second = !halves || (item & 1);  // (with the keys and values)
     int64_t slot = slot_next;
     if (slot < -1 || slot >= p.num_slots) {
-      if (store && lane == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
+      if (store && second && lane == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
       slot = -1;
     }
     for (int a = lane; a < half; a += 32) {
@@ -323,9 +337,9 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
       angles[a] = cs * p.amplitude;
       angles[half + a] = sn * p.amplitude;
     }
-    if (t + step < p.num_tokens) {  // (the next token's, asked for ahead)
-      if (R > 0) position = p.positions[t + step];
-      if (store) slot_next = p.slots[t + step];
+    if (item + step < items) {  // (the next one's, asked for ahead)
+      if (R > 0) position = p.positions[(item + step) >> halves];
+      if (store) slot_next = p.slots[(item + step) >> halves];
     }
     __syncwarp();
     float cs[8], sn[8];
@@ -379,21 +393,25 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
         }
       }
     };
-    turn_heads(at, Hq, wq);
-    turn_heads(at + q_bytes, Hkv, wk);
+    turn_heads(at, second ? Hq - Q0 : Q0, wq);
+    if (second) turn_heads(at + q1_bytes, Hkv, wk);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      bulk_store(p.q_out + t * Hq * D, at, q_bytes);
-      if (p.k_out != nullptr) bulk_store(p.k_out + t * Hkv * D, at + q_bytes, kv_bytes);
-      if (slot >= 0) {
-        bulk_store(p.k_cache + slot * Hkv * D, at + q_bytes, kv_bytes);
-        bulk_store(p.v_cache + slot * Hkv * D, at + q_bytes + kv_bytes, kv_bytes);
+      if (!second) {
+        bulk_store(p.q_out + t * Hq * D, at, q0_bytes);
+      } else {
+        if (q1_bytes > 0) bulk_store(p.q_out + (t * Hq + Q0) * D, at, q1_bytes);
+        if (p.k_out != nullptr) bulk_store(p.k_out + t * Hkv * D, at + q1_bytes, kv_bytes);
+        if (slot >= 0) {
+          bulk_store(p.k_cache + slot * Hkv * D, at + q1_bytes, kv_bytes);
+          bulk_store(p.v_cache + slot * Hkv * D, at + q1_bytes + kv_bytes, kv_bytes);
+        }
       }
       bulk_commit();
-      // The place of the token before is read out: the next copies in go there.
-      const int64_t next = t + (kRopePlaces - 1) * step;
-      if (next < p.num_tokens) {
+      // The place of the item before is read out: the next copies in go there.
+      const int64_t next = item + (kRopePlaces - 1) * step;
+      if (next < items) {
         bulk_wait_read<1>();
         load(next, place == 0 ? kRopePlaces - 1 : place - 1);
       }
@@ -432,9 +450,22 @@ template <int D, bool kInterleaved>
 pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
-  // Many tokens: streamed, if a token's rows leave room for enough warps.
-  const int64_t row = ((int64_t)prm.num_q_heads + prm.num_kv_heads * (prm.k_cache != nullptr ? 2 : 1)) * D * 2;
-  const int64_t warp_bytes = (kRopePlaces * row + prm.rotary * 4 + kRopePlaces * 8 + 127) & ~(int64_t)127;
+  // Many tokens: streamed, whole ones if their rows leave room for all warps of a CTA, else
+  // halves, in whole blocks of heads (11 chunks of 32 + 8 + 8 heads, 12 KB a token: 47.0 us
+  // whole, 44.3 in halves; 16 prompts of 16 + 8 + 8: 88.9 and 100).
+  const int kv_heads = prm.num_kv_heads * (prm.k_cache != nullptr ? 2 : 1);
+  const int64_t heads = (int64_t)prm.num_q_heads + kv_heads;
+  auto warp_room = [&](int64_t heads) {
+    return (kRopePlaces * heads * D * 2 + prm.rotary * 4 + kRopePlaces * 8 + 127) & ~(int64_t)127;
+  };
+  int64_t warp_bytes = warp_room(heads);
+  if (warp_bytes * kRopeStreamWarps > kRopeSmem) {
+    const int block = 16 * 32 / D;
+    const int64_t half = heads / 2 / block * block;
+    prm.first_heads = (int)(half < prm.num_q_heads ? half : prm.num_q_heads);
+    const int64_t rest = heads - prm.first_heads;
+    warp_bytes = warp_room(rest > prm.first_heads ? rest : prm.first_heads);
+  }
   int warps = warp_bytes <= kRopeSmem ? (int)(kRopeSmem / warp_bytes) : 0;
   if (warps > kRopeStreamWarps) warps = kRopeStreamWarps;
   if (prm.num_tokens > kRopeStreamTokens * (int64_t)sms && warps >= 4) {
@@ -444,7 +475,8 @@ pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
     if (!kernel_smem_setup((const void *)norm_rope_stream_kernel<D, kInterleaved>, warps * 32, smem, &per_sm))
       return PKV_ERR_CUDA;
     int64_t grid = (int64_t)sms * per_sm;
-    if (grid > (prm.num_tokens + warps - 1) / warps) grid = (prm.num_tokens + warps - 1) / warps;
+    const int64_t items = prm.num_tokens << (prm.first_heads > 0 ? 1 : 0);
+    if (grid > (items + warps - 1) / warps) grid = (items + warps - 1) / warps;
     return launch_dependent(norm_rope_stream_kernel<D, kInterleaved>, (unsigned)grid, warps * 32, smem, stream, prm);
   }
   // Few tokens: one per CTA, so that the step is on as many SMs as it can be.
@@ -558,6 +590,7 @@ extern "C" pkv_status pkv_norm_rope_store(
   prm.rotary = rotary_dim;
   prm.tokens_per_cta = 0;
   prm.warp_bytes = 0;
+  prm.first_heads = 0;
   prm.eps = eps;
   prm.amplitude = amplitude;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -325,9 +325,34 @@ def test_streamed_bits_that_do_not_turn_and_bad_slots(lib):
     assert int(r.status.item()) == lib.DEV_BAD_SLOT
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 8), (41, 3), (2, 20)])
+def test_streamed_in_halves(lib, Hq, Hkv, interleaved):
+    """Rows of a token that leave shared memory room for fewer than twelve warps: most heads of q, few of them, odd numbers."""
+    r = Rows(MANY + 9, Hq, Hkv, 128, 64, packed=interleaved, block=256)
+    r.call(lib, k_out=True, interleaved=interleaved)
+    q, k, kc, vc = r.q_out.clone(), r.k_out.clone(), r.kc.clone(), r.vc.clone()
+    r.q_out.zero_(), r.k_out.zero_(), r.kc.zero_(), r.vc.zero_()
+    turns, T = lib.rope_turns(r.inv_freq), r.q.shape[0]
+    for a in range(0, T, 1000):
+        b = min(a + 1000, T)
+        lib.norm_rope_store(r.q_out[a:b], r.q[a:b], r.k[a:b], r.v[a:b], r.positions[a:b], turns, r.kc, r.vc, r.slots[a:b], k_out=r.k_out[a:b],
+                            q_weight=r.qw, k_weight=r.kw, interleaved=interleaved)
+    torch.cuda.synchronize()
+    kept = r.slots[r.slots >= 0].long()
+    assert torch.equal(q, r.q_out) and torch.equal(k, r.k_out)
+    assert torch.equal(kc.flatten(0, 1)[kept], r.kc.flatten(0, 1)[kept]) and torch.equal(vc.flatten(0, 1)[kept], r.vc.flatten(0, 1)[kept])
+    # without a store, and in place
+    again = r.q.contiguous().clone()
+    keys = r.k.contiguous().clone()
+    lib.norm_rope_store(again, again, keys, None, r.positions, turns, k_out=keys, q_weight=r.qw, k_weight=r.kw, interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert torch.equal(again, q) and torch.equal(keys, k)
+
+
 def test_many_rows_too_wide_to_stream(lib):
-    """Rows of a token that leave shared memory room for fewer than four warps."""
-    r = Rows(MANY + 3, 64, 16, 128, 16, packed=False, block=256)
+    """Rows of a token of which not even halves leave shared memory room for four warps."""
+    r = Rows(MANY + 3, 256, 64, 128, 16, packed=False, block=256)
     r.call(lib, norm=True)
     T = r.q.shape[0]
     q = r.q_out.clone()
