@@ -15,7 +15,7 @@
 //  1. plan: one CTA.  A group's prefix ends where its shortest sequence does; prefix
 //     sums of the work of groups (steps of 64 keys) and of sequences (tiles of 4 KiB
 //     of K) go to the workspace, and how many CTAs work on prefixes.  A small batch has
-//     no such launch: every CTA of the next one plans for itself, in shared memory.
+//     no such launch and shares nothing: every CTA of the next one sums up the lengths.
 //  2. attention: one CTA per SM.  Some of them take the prefixes, units of (group, kv
 //     head, 256 rows) by steps, cut into runs of equal cost, a CTA for each (tcgen05,
 //     TMA); the others the tails, all sequences' own tokens, cut into runs of equal
@@ -41,13 +41,12 @@ constexpr int kStages = 3;               // ring of tiles per warp
 constexpr int kMaxCtas = 160;            // CTAs of the attention's grid at most (places for
 constexpr int kMaxWarps = kMaxCtas * kWarpsMost;  // parts; a GB300 has 152 SMs)
 constexpr int kThreads = 384;            // of the attention's CTAs
-// A batch is planned by every CTA for itself where its tables have room for no more K and
-// V than kNearBytes, in at most so many sequences and groups: two short sequences 10.6 ->
-// 8.4 us and 2 us less on the host; 64 behind a system prompt 33.0 -> 34.9, as the join
-// can then not read the plan before it waits.
-constexpr int64_t kNearBytes = 16 << 20;
-constexpr int kNearSeqs = kThreads;
-constexpr int kNearGroups = 32;
+// A batch of at most so many sequences whose tables have room for no more K and V than
+// kSmallBytes is small: reading it whole takes 2 us or so, and a prefix's pipeline alone 6
+// (two sequences behind 256 tokens: 9.4 us without sharing, 12.6 with).
+constexpr int64_t kSmallBytes = 16 << 20;
+constexpr int kSmallSeqs = kThreads;
+constexpr int kNearGroups = 32;          // groups whose plans fit a CTA's shared memory
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 constexpr int BM = 128;                  // rows of a product
 constexpr int BN = 64;                   // keys of a step
@@ -125,8 +124,8 @@ struct SharedParams {
   int tail_warps;      // warps of a CTA that takes tails
   int loading;         // CTAs that load their prefixes: all, but in a test
   int share_always;    // whatever it saves (test)
-  int near;            // the attention's CTAs plan
-  int plan_at;         // where their plan (or groups) is in shared memory
+  int small;           // no plan was launched
+  int groups_at;       // where the groups' plans are in a CTA's shared memory
   int head_dim;
   float qscale;        // scale * log2(e)
 };
@@ -183,18 +182,18 @@ __device__ __forceinline__ int split_ctas(const SharedParams &p, float cost, flo
 }
 static_assert(kPrefixNs > kTailNs, "the equation's quadratic term");
 
-// The whole batch's plan, by all threads of a CTA, to groups, seqs and totals (of the
-// workspace, or shared memory).  scratch: shared memory of 4 N + 1 ints.
-__device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, int64_t (*sums)[2],
-                                           GroupPlan *groups, SeqPlan *seqs, Totals *totals) {
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p) {
+  extern __shared__ int plan_smem[];
+  __shared__ int64_t sums[32][2];
   const int S = p.num_seqs, N = p.num_groups, tid = threadIdx.x;
-  const bool tell = blockIdx.x == 0;
-  int *starts = scratch;         // [N + 1]
+  int *starts = plan_smem;       // [N + 1]
   int *eff = starts + N + 1;     // [N]: blocks that the group shares
   int *lead = eff + N;           // [N]: its first sequence with tokens
   int *count = lead + N;         // [N]: its sequences with tokens
   const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
   auto tokens = [&](int L) { return L <= 0 ? 0 : (int)min((int64_t)L, room); };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int first_L = tid < S ? p.context_lens[tid] : 0;  // (asked for ahead)
   bool ok = true;
   for (int g = tid; g <= N; g += blockDim.x) {
@@ -203,7 +202,7 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
     ok = ok && (g > 0 || x == 0) && (g < N || x == S);
     if (g < N) {
       const int b = p.shared_blocks[g];
-      if (tell && (b < 0 || b > p.max_blocks_per_seq)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+      if (b < 0 || b > p.max_blocks_per_seq) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
       eff[g] = min(max(b, 0), p.max_blocks_per_seq);
       lead[g] = 0x7FFFFFFF;
       count[g] = 0;
@@ -213,7 +212,7 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
   for (int g = tid; g < N; g += blockDim.x) ok = ok && starts[g] <= starts[g + 1];
   ok = __syncthreads_and(ok) != 0;
   // (no groups then: every sequence by itself)
-  if (!ok && tell && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+  if (!ok && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQLEN);
   if (ok) {
     for (int s0 = tid & ~31; s0 < S; s0 += blockDim.x) {
       const int s = s0 + (tid & 31);
@@ -266,7 +265,7 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
     my_L = tokens(L0);
     my_b = first(s, my_L, my_g);
     at[1] += (int64_t)tail_tiles(my_L - my_b, p.head_dim) << 32 | tail_tiles(my_L, p.head_dim);
-    if (tell && (my_L != L0 || my_L == 0)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+    if (my_L != L0 || my_L == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
   }
   scan_cta<2>(at, sum, sums);
   int64_t cost = sum[0];
@@ -283,14 +282,14 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
     my_cost = my_b = my_g = 0;
   }
   if (tid == 0) {
-    totals->cost = cost;
-    totals->tiles = tiles;
-    totals->prefix_ctas = split_ctas(p, (float)cost, (float)tiles);
+    p.totals->cost = cost;
+    p.totals->tiles = tiles;
+    p.totals->prefix_ctas = split_ctas(p, (float)cost, (float)tiles);
   }
   for (int g = g0; g < g1; ++g) {
     GroupPlan x = plan(g);
     x.cost0 = at[0];
-    groups[g] = x;
+    p.groups[g] = x;
     at[0] += per_g == 1 ? my_cost : cost_of(x);
   }
   for (int s = s0; s < s1; ++s) {
@@ -298,29 +297,10 @@ __device__ __forceinline__ void plan_batch(const SharedParams &p, int *scratch, 
       my_L = tokens(p.context_lens[s]);
       my_b = first(s, my_L, my_g);
     }
-    *reinterpret_cast<int4 *>(seqs + s) = make_int4(tile, my_b, my_L, my_g);
+    *reinterpret_cast<int4 *>(p.seqs + s) = make_int4(tile, my_b, my_L, my_g);
     tile += tail_tiles(my_L - my_b, p.head_dim);
   }
 }
-
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p) {
-  extern __shared__ int plan_smem[];
-  __shared__ int64_t sums[32][2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  plan_batch(p, plan_smem, sums, p.groups, p.seqs, p.totals);
-}
-
-// A batch's plan in shared memory: what stays, and what is where the tiles come later.
-struct NearPlan {
-  GroupPlan groups[kNearGroups];
-  Totals totals;
-};
-struct NearScratch {
-  SeqPlan seqs[kNearSeqs];
-  int64_t sums[32][2];
-  int ints[4 * kNearGroups + 1];
-};
 
 // ---------------------------------------------------------------------- 2. tails
 
@@ -342,9 +322,11 @@ struct WarpSmem {
 // that a weight is off by 2^-18 of itself and not by 2^-9 (paged_decode_attn keeps it in
 // fp32).  With at most four heads columns 4 to 7 repeat the heads of 0 to 3 and take the
 // second parts; eight heads need a second product.
+//
+// smem_raw: the warps' rings, then [S + 1] first tiles, [S] first tokens and [S] lengths
+// of the sequences' tails, which are there already.
 template <int D, int G>
-__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, const SeqPlan *seqs,
-                                      uint8_t *smem_raw) {
+__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, uint8_t *smem_raw) {
   using W = WarpSmem<D, G>;
   constexpr int kRows = W::kRows;
   constexpr int kCols = D / 8;              // 16-byte columns per row
@@ -360,14 +342,6 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
   const uint32_t tiles = smem_u32(mine);
   const uint32_t qslots = tiles + kStages * 2 * W::kHalf;
 
-  for (int s = threadIdx.x; s < S; s += blockDim.x) {
-    const int4 x = *reinterpret_cast<const int4 *>(seqs + s);
-    tile0[s] = x.x;
-    begin[s] = x.y;
-    len[s] = x.z;
-  }
-  if (threadIdx.x == 0) tile0[S] = (int)sum.tiles;
-  __syncthreads();
   if (warp >= warps) return;
   const int total = tile0[S];
   const int per_run = run_tiles(p, sum);
@@ -1195,40 +1169,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const SharedParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  // (before any of tensor memory is taken, too: a kernel before the call may need it)
+  // (before any of tensor memory is taken, too)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const GroupPlan *groups = p.groups;
-  const SeqPlan *seqs = p.seqs;
-  Totals sum;
-  NearPlan *plan = reinterpret_cast<NearPlan *>(smem_raw + p.plan_at);
-  if (p.near) {
-    NearScratch *scratch = reinterpret_cast<NearScratch *>(smem_raw);
-    plan_batch(p, scratch->ints, scratch->sums, plan->groups, scratch->seqs, &plan->totals);
-    __syncthreads();
-    groups = plan->groups;
-    seqs = scratch->seqs;  // (both kinds of work have a barrier before their first tile)
-    sum = plan->totals;
-    if (blockIdx.x == 0) {  // (for the join)
-      for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x)
-        reinterpret_cast<int4 *>(p.seqs)[i] = reinterpret_cast<const int4 *>(seqs)[i];
-      for (int i = threadIdx.x; i < 2 * p.num_groups; i += blockDim.x)
-        reinterpret_cast<int4 *>(p.groups)[i] = reinterpret_cast<const int4 *>(groups)[i];
-      if (threadIdx.x == 0) *p.totals = sum;
-    }
-  } else {
-    if (p.num_groups <= kNearGroups) {  // (asked for beside the totals; read behind a barrier)
-      if (threadIdx.x < 2 * p.num_groups)
-        reinterpret_cast<int4 *>(plan->groups)[threadIdx.x] =
-            __ldcg(reinterpret_cast<const int4 *>(p.groups) + threadIdx.x);
-      groups = plan->groups;
-    }
-    sum.cost = __ldcg(&p.totals->cost);
-    sum.tiles = __ldcg(&p.totals->tiles);
-    sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
+  if (p.num_groups <= kNearGroups) {  // (asked for beside the totals; read behind a barrier)
+    GroupPlan *near = reinterpret_cast<GroupPlan *>(smem_raw + p.groups_at);
+    if (threadIdx.x < 2 * p.num_groups)
+      reinterpret_cast<int4 *>(near)[threadIdx.x] =
+          __ldcg(reinterpret_cast<const int4 *>(p.groups) + threadIdx.x);
+    groups = near;
   }
-  if ((int)blockIdx.x < sum.prefix_ctas) prefixes<D>(tm_q, tm_k, p, sum, groups, smem_raw);
-  else tails<D, G>(p, sum, seqs, smem_raw);
+  Totals sum;
+  sum.cost = __ldcg(&p.totals->cost);
+  sum.tiles = __ldcg(&p.totals->tiles);
+  sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
+  if ((int)blockIdx.x < sum.prefix_ctas) {
+    prefixes<D>(tm_q, tm_k, p, sum, groups, smem_raw);
+    return;
+  }
+  int *tile0 = reinterpret_cast<int *>(smem_raw + p.tail_warps * WarpSmem<D, G>::bytes);
+  int *begin = tile0 + p.num_seqs + 1, *len = begin + p.num_seqs;
+  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
+    tile0[s] = x.x;
+    begin[s] = x.y;
+    len[s] = x.z;
+  }
+  if (threadIdx.x == 0) tile0[p.num_seqs] = (int)sum.tiles;
+  __syncthreads();
+  tails<D, G>(p, sum, smem_raw);
+}
+
+// The launch of a small batch: every context is a tail, of which each CTA knows by itself
+// where it begins.
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1) shared_small_kernel(const SharedParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ int64_t sums[32][1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int S = p.num_seqs, s = threadIdx.x;  // (kSmallSeqs: a thread each)
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  int *tile0 = reinterpret_cast<int *>(smem_raw + p.tail_warps * WarpSmem<D, G>::bytes);
+  int *begin = tile0 + S + 1, *len = begin + S;
+  const int given = s < S ? p.context_lens[s] : 1;
+  const int L = given <= 0 ? 0 : (int)min((int64_t)given, room);
+  if (blockIdx.x == 0) {  // (what the groups say is looked at, but not used)
+    if (s < S && (L != given || L == 0)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+    for (int g = threadIdx.x; g <= p.num_groups; g += blockDim.x) {
+      const int x = p.group_starts[g];
+      if (g < p.num_groups ? (g == 0 && x != 0) || p.group_starts[g + 1] < x : x != S)
+        flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+      if (g < p.num_groups && (p.shared_blocks[g] < 0 || p.shared_blocks[g] > p.max_blocks_per_seq))
+        flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+    }
+  }
+  int64_t at[1] = {s < S ? tail_tiles(L, D) : 0}, all[1];
+  scan_cta<1>(at, all, sums);
+  if (s < S) {
+    tile0[s] = (int)at[0];
+    begin[s] = 0;
+    len[s] = L;
+    if (blockIdx.x == 0)  // (for the join)
+      *reinterpret_cast<int4 *>(p.seqs + s) = make_int4((int)at[0], 0, L, 0);
+  }
+  Totals sum;
+  sum.cost = 0;
+  sum.tiles = all[0];
+  sum.prefix_ctas = 0;
+  sum.pad = 0;
+  if (s == 0) {
+    tile0[S] = (int)all[0];
+    if (blockIdx.x == 0) {
+      *p.totals = sum;
+      const int4 none = make_int4(0, 0, 0, 0);
+      reinterpret_cast<int4 *>(p.groups)[0] = none;
+      reinterpret_cast<int4 *>(p.groups)[1] = none;
+    }
+  }
+  __syncthreads();
+  tails<D, G>(p, sum, smem_raw);
 }
 
 // ----------------------------------------------------------------------- 4. join
@@ -1249,7 +1270,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Shar
   const int j = head / G, g = head - j * G;
   // (Planned by a launch of its own, the plan is there: the launch before began after it,
   // and this one after that.)
-  if (p.near) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.small) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 seq = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
   Totals sum;
   sum.cost = __ldcg(&p.totals->cost);
@@ -1425,31 +1446,47 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned th
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// q as {D, Hq, S}: a box is 64 dims x the G heads of a kv head x 128 / G sequences.
+// k_cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
+bool encode_maps(const SharedParams &p, CUtensorMap *tq, CUtensorMap *tk) {
+  const uint64_t D = p.head_dim, Hkv = p.num_kv_heads, Hq = Hkv * p.group_size;
+  const uint64_t block = (uint64_t)1 << p.block_shift;
+  const uint64_t qdims[3] = {D, Hq, (uint64_t)p.num_seqs}, qstr[2] = {D * 2, Hq * D * 2};
+  const uint32_t qbox[3] = {64u, (uint32_t)p.group_size, (uint32_t)(BM / p.group_size)};
+  const uint64_t kdims[4] = {D, Hkv, block, (uint64_t)p.num_blocks};
+  const uint64_t kstr[3] = {D * 2, Hkv * D * 2, block * Hkv * D * 2};
+  const uint32_t kbox[4] = {64u, 1u, (uint32_t)BN, 1u};
+  return encode_bf16_map(tq, p.q, 3, qdims, qstr, qbox, true) &&
+         encode_bf16_map(tk, p.k_cache, 4, kdims, kstr, kbox, true);
+}
+
 template <int D, int G>
-pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk,
-                  cudaStream_t stream) {
+pkv_status launch(SharedParams prm, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
   const int S = prm.num_seqs;
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
-  const bool near = S <= kNearSeqs && prm.num_groups <= kNearGroups &&
-                    S * room * prm.num_kv_heads * (4 * D) <= kNearBytes;
-  const int near_smem = (int)sizeof(NearPlan) + 16;
+  const bool small = S <= kSmallSeqs && S * room * prm.num_kv_heads * (4 * D) <= kSmallBytes &&
+                     !prm.share_always;
+  const int groups_smem = kNearGroups * (int)sizeof(GroupPlan) + 16;
   const int seq_smem = (3 * S + 1) * 4;
-  int warps = (kMaxDynamicSmem - 1024 - seq_smem - near_smem) / WarpSmem<D, G>::bytes;
+  int warps = (kMaxDynamicSmem - 2048 - seq_smem - groups_smem) / WarpSmem<D, G>::bytes;
   if (warps > kWarpsMost) warps = kWarpsMost;
-  static_assert((kMaxDynamicSmem - 2560 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
-  static_assert(sizeof(NearPlan) + 16 + 1024 <= 2560, "");
-  static_assert(PrefixLayout<D>::total + 1024 + 16 + sizeof(NearPlan) <= kMaxDynamicSmem, "");
+  static_assert((kMaxDynamicSmem - 4096 - (3 * kSharedMaxSeqs + 1) * 4) / WarpSmem<D, G>::bytes >= 1, "");
+  static_assert(kNearGroups * sizeof(GroupPlan) + 16 <= 2048, "");
+  static_assert(PrefixLayout<D>::total + 1024 + 16 + kNearGroups * sizeof(GroupPlan) <= kMaxDynamicSmem, "");
   int smem = warps * WarpSmem<D, G>::bytes + seq_smem;
-  if (smem < PrefixLayout<D>::total + 1024) smem = PrefixLayout<D>::total + 1024;
-  prm.near = near;
-  prm.plan_at = (smem + 15) & ~15;
-  smem += near_smem;
+  if (!small && smem < PrefixLayout<D>::total + 1024) smem = PrefixLayout<D>::total + 1024;
+  prm.small = small;
+  prm.groups_at = (smem + 15) & ~15;
+  if (!small) smem += groups_smem;
   const int plan_smem = (4 * prm.num_groups + 1) * 4;
-  if ((!near && !kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr)) ||
-      !kernel_smem_setup((const void *)shared_attn_kernel<D, G>, kThreads, smem, nullptr))
+  if (small ? !kernel_smem_setup((const void *)shared_small_kernel<D, G>, kThreads, smem, nullptr)
+            : !kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr) ||
+                  !kernel_smem_setup((const void *)shared_attn_kernel<D, G>, kThreads, smem, nullptr))
     return PKV_ERR_CUDA;
+  CUtensorMap tq, tk;
+  if (!small && !encode_maps(prm, &tq, &tk)) return PKV_ERR_CUDA;
   // A CTA per SM, and no more than the longest possible batch has work for: a warp per
   // tile and kv head, a CTA per step of the prefixes.  (Two at least: one of a kind.)
   const int rows = tail_rows(D);
@@ -1462,13 +1499,18 @@ pkv_status launch(SharedParams prm, const CUtensorMap &tq, const CUtensorMap &tk
   if (ctas < 2) ctas = 2;
   prm.ctas = (int)ctas;
   prm.tail_warps = warps;
-  cudaError_t err = cudaSuccess;
-  if (!near)
+  cudaError_t err;
+  if (small) {
+    err = launch_dependent<SharedParams>(shared_small_kernel<D, G>, (unsigned)ctas, kThreads, smem,
+                                         stream, prm);
+  } else {
+    // (few sequences: fewer threads to wait for; 100 of them 22.4 -> 21.3 us, 1000 72.9 -> 77.3)
     err = launch_dependent<SharedParams>(shared_plan_kernel, 1, S <= 256 ? 256 : kPlanThreads,
                                          plan_smem, stream, prm);
-  if (err == cudaSuccess)
-    err = launch_dependent<CUtensorMap, CUtensorMap, SharedParams>(
-        shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, prm);
+    if (err == cudaSuccess)
+      err = launch_dependent<CUtensorMap, CUtensorMap, SharedParams>(
+          shared_attn_kernel<D, G>, (unsigned)ctas, kThreads, smem, stream, tq, tk, prm);
+  }
   if (err == cudaSuccess) {
     // As many warps to a row as leave the join's CTAs one turn on the GPU (eight to an SM):
     // 1024 rows of about 20 parts took 6.7 us with one and 4.4 with two, 4096 of 6 the
@@ -1560,30 +1602,16 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.ctas = 0;
   prm.tail_warps = 0;
-  prm.near = 0;
-  prm.plan_at = 0;
+  prm.small = 0;
+  prm.groups_at = 0;
   prm.head_dim = head_dim;
   prm.loading = g_loading.load(std::memory_order_relaxed);
   prm.share_always = g_share_always.load(std::memory_order_relaxed);
   prm.qscale = scale * kLog2e;
 
-  // q as {D, Hq, S}: a box is 64 dims x the G heads of a kv head x 128 / G sequences.
-  const uint64_t qdims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)num_seqs};
-  const uint64_t qstr[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
-  const uint32_t qbox[3] = {64u, (uint32_t)G, (uint32_t)(BM / G)};
-  // k_cache as {D, Hkv, block_size, NB}: a box is 64 dims x 1 head x 64 tokens x 1 block.
-  const uint64_t kdims[4] = {(uint64_t)head_dim, (uint64_t)num_kv_heads, (uint64_t)block_size,
-                             (uint64_t)num_blocks};
-  const uint64_t kstr[3] = {(uint64_t)head_dim * 2, (uint64_t)num_kv_heads * head_dim * 2,
-                            (uint64_t)block_size * num_kv_heads * head_dim * 2};
-  const uint32_t kbox[4] = {64u, 1u, (uint32_t)BN, 1u};
-  CUtensorMap tq, tk;
-  if (!encode_bf16_map(&tq, q, 3, qdims, qstr, qbox, true) ||
-      !encode_bf16_map(&tk, k_cache, 4, kdims, kstr, kbox, true))
-    return PKV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define PKV_CASE(DD, GG) \
-  if (head_dim == DD && G == GG) return launch<DD, GG>(prm, tq, tk, st);
+  if (head_dim == DD && G == GG) return launch<DD, GG>(prm, st);
   PKV_CASE(64, 1)
   PKV_CASE(64, 2)
   PKV_CASE(64, 4)

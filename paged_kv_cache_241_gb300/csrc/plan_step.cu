@@ -32,11 +32,14 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxSeqs = 16384;
 constexpr int kPlanCluster = 8;     // portable cluster size
-// Up to so many rows and sequences one CTA of kPlanSmallSeqs threads does the step.
+// Up to so many rows and sequences one CTA of kPlanSmallSeqs threads does the step, else a
+// cluster (256 decode rows 5.1 and 6.8 us, 400 7.4 and 7.1; eight prompts with 2000 rows
+// 5.8 and 5.7, with 4000 8.3 and 5.7).
 constexpr int kPlanSmallRows = 2048;
 constexpr int kPlanSmallSeqs = 256;
-// From so many rows on they have a launch of their own.
-constexpr int kPlanManyRows = 16384;
+// From so many rows on they have a launch of their own (64 prompts: 29 thousand rows 8.3
+// us without and 8.8 with, 115 thousand 12.7 and 9.3).
+constexpr int kPlanManyRows = 49152;
 constexpr int kRowThreads = 256;
 
 struct PlanParams {

@@ -233,26 +233,27 @@ def test_agrees_with_the_block_manager(lib):
         assert len(set(zip(theirs // block, ours // block))) == -(-n // block)
 
 
-# From 16384 rows on they are written by a launch of their own.
+# From 49152 rows on they are written by a launch of their own.
 
 @pytest.mark.parametrize("seed", range(3))
 @pytest.mark.parametrize("S,high,new,block,free", [(40, 3000, 1500, 64, None), (700, 900, 120, 128, 30), (3, 100, 20000, 512, None)])
-def test_many_rows(lib, seed, S, high, new, block, free):
+@pytest.mark.parametrize("least", [0, 49152])
+def test_many_rows(lib, seed, S, high, new, block, free, least):
     p = random_plan(seed, S, high, new, block, free=free)
-    p.rows = max(p.rows, 16384) + 3 * seed
+    p.rows = max(p.rows, least) + 3 * seed
     p.check(lib)
 
 
 def test_many_rows_with_bad_lengths(lib):
     wide = 1000
     lens = [100, -5, wide * 64 + 1, 200, 256, 30, 60, 0]
-    new = [9000, 2000, 1000, 60, 1, -3, 10000, 70000]
-    p = Plan(lens, new, block=64, wide=wide, free=400, rows=25000)
+    new = [29000, 2000, 1000, 60, 1, -3, 30000, 70000]
+    p = Plan(lens, new, block=64, wide=wide, free=1000, rows=65000)
     p.check(lib)
 
 
 def test_many_rows_block_ids_out_of_range(lib):
-    p = Plan([10, 70, 64], [9000, 8000, 70], block=64)
+    p = Plan([10, 70, 64], [39000, 18000, 70], block=64)
     p.tables[1, 1] = p.num_blocks
     p.stack[p.free - 5] = -4
     args = p.check(lib)
@@ -261,7 +262,7 @@ def test_many_rows_block_ids_out_of_range(lib):
 
 def test_many_rows_in_place_and_sums_that_saturate(lib):
     S, wide = 3000, 1 << 14
-    p = Plan([0] * S, [1] * S, block=64, wide=wide, free=S, rows=20000)
+    p = Plan([0] * S, [1] * S, block=64, wide=wide, free=S, rows=60000)
     p.lens = [64 * wide - 1] * S
     p.tables[:, wide - 1] = np.arange(S) % p.num_blocks
     args = p.device()
