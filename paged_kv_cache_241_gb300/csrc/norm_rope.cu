@@ -25,7 +25,7 @@ namespace pkv {
 namespace {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeTokens = 8;  // tokens of a CTA, where there are many
+constexpr int kRopeTokens = 8;  // tokens of a CTA, where there are many, too wide to stream
 constexpr int kRopeAhead = 2;   // tokens that a warp has asked for at a time
 // Stream: tokens that a warp has in shared memory, and warps of a CTA (one per SM).  16
 // prompts of 16 + 8 + 8 heads (537 MB): 89.5 us with 2 and 12 (88 % of a copy), 95.0 with
@@ -34,7 +34,12 @@ constexpr int kRopeAhead = 2;   // tokens that a warp has asked for at a time
 constexpr int kRopePlaces = 2;
 constexpr int kRopeStreamWarps = 12;
 constexpr int kRopeSmem = 220 * 1024;
-constexpr int kRopeStreamTokens = 16;  // tokens per SM from which on they are streamed
+// Tokens per SM from which on they are streamed, in halves, and from which on whole (us,
+// of 16 + 8 + 8 heads: one token to a CTA, eight, streamed in halves, streamed whole):
+//   150 tokens 2.8 6.7 4.0 6.1, 600 5.3 7.4 4.2 6.1, 1800 12.0 9.9 7.9 8.1,
+//   3500 25.7 13.6 14.9 15.6, 6000 41.8 23.2 23.1 24.5, 12000 80.6 42.8 41.0 38.6
+constexpr int kRopeStreamTokens = 3;
+constexpr int kRopeWholeTokens = 64;
 
 struct RopeParams {
   uint16_t *q_out;
@@ -450,16 +455,17 @@ template <int D, bool kInterleaved>
 pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return PKV_ERR_CUDA;
-  // Many tokens: streamed, whole ones if their rows leave room for all warps of a CTA, else
-  // halves, in whole blocks of heads (11 chunks of 32 + 8 + 8 heads, 12 KB a token: 47.0 us
-  // whole, 44.3 in halves; 16 prompts of 16 + 8 + 8: 88.9 and 100).
+  // More than a few tokens: streamed; in halves, in whole blocks of heads, where there are
+  // not very many, or where whole ones leave no room for all warps of a CTA (11 chunks of
+  // 32 + 8 + 8 heads, 12 KB a token: 47.0 us whole, 44.3 in halves; 16 prompts of 16 + 8 +
+  // 8: 88.9 and 100).
   const int kv_heads = prm.num_kv_heads * (prm.k_cache != nullptr ? 2 : 1);
   const int64_t heads = (int64_t)prm.num_q_heads + kv_heads;
   auto warp_room = [&](int64_t heads) {
     return (kRopePlaces * heads * D * 2 + prm.rotary * 4 + kRopePlaces * 8 + 127) & ~(int64_t)127;
   };
   int64_t warp_bytes = warp_room(heads);
-  if (warp_bytes * kRopeStreamWarps > kRopeSmem) {
+  if (prm.num_tokens <= kRopeWholeTokens * (int64_t)sms || warp_bytes * kRopeStreamWarps > kRopeSmem) {
     const int block = 16 * 32 / D;
     const int64_t half = heads / 2 / block * block;
     prm.first_heads = (int)(half < prm.num_q_heads ? half : prm.num_q_heads);
@@ -480,7 +486,7 @@ pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
     return launch_dependent(norm_rope_stream_kernel<D, kInterleaved>, (unsigned)grid, warps * 32, smem, stream, prm);
   }
   // Few tokens: one per CTA, so that the step is on as many SMs as it can be.
-  prm.tokens_per_cta = prm.num_tokens <= 8 * (int64_t)sms ? 1 : kRopeTokens;
+  prm.tokens_per_cta = prm.num_tokens <= kRopeStreamTokens * (int64_t)sms ? 1 : kRopeTokens;
   const int64_t grid = (prm.num_tokens + prm.tokens_per_cta - 1) / prm.tokens_per_cta;
   if (grid > 0x7FFFFFFFLL) return PKV_ERR_UNSUPPORTED;
   return launch_dependent(norm_rope_kernel<D, kInterleaved>, (unsigned)grid, kRopeWarps * 32,

@@ -121,10 +121,11 @@ def test_shapes(lib, T, Hq, Hkv, D, R, norm, interleaved):
     Rows(T, Hq, Hkv, D, R, packed=T % 2 == 0).check(lib, norm=norm, interleaved=interleaved)
 
 
+@pytest.mark.parametrize("T", [3 * 152, 3 * 152 + 1, 8 * 152 + 13])
 @pytest.mark.parametrize("D", [64, 128])
-def test_many_rows(lib, D):
-    """More tokens than one per CTA: several of a CTA, the last one ragged."""
-    Rows(8 * 152 + 13, 2, 1, D, 32).check(lib, norm=True)
+def test_many_rows(lib, D, T):
+    """The most tokens of one per CTA, and more."""
+    Rows(T, 2, 1, D, 32).check(lib, norm=True)
 
 
 @pytest.mark.parametrize("store,k_out", [(True, True), (False, True)])
@@ -270,8 +271,9 @@ def test_offsets_past_32_bits(lib):
     assert torch.equal(vc.view(-1, Hkv, D)[r.slots.long()], r.v)
 
 
-# More tokens than this per SM are streamed through shared memory, a token to a warp.
-MANY = 16 * 152
+# More than 3 tokens per SM are streamed through shared memory, half a token to a warp at a
+# time; more than 64 a whole one.
+MANY, FEW, WHOLE = 16 * 152, 400, 64 * 152
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -285,15 +287,16 @@ def test_streamed_keys_as_a_tensor(lib, store, k_out):
     Rows(MANY + 1, 2, 1, 64, 32, packed=store).check(lib, store=store, k_out=k_out)
 
 
-def test_streamed_rows_are_those_of_few(lib):
+@pytest.mark.parametrize("T", [FEW + 100, MANY + 5, WHOLE + 301])
+def test_streamed_rows_are_those_of_few(lib, T):
     """The same tokens, streamed and a part of them at a time: the same bits (ordinary head counts, a whole head turned)."""
-    r = Rows(3 * MANY + 5, 16, 8, 128, 128)
+    r = Rows(T, 16, 8, 128, 128)
     r.call(lib, k_out=True)
     q, k, kc, vc = r.q_out.clone(), r.k_out.clone(), r.kc.clone(), r.vc.clone()
     r.q_out.zero_(), r.k_out.zero_(), r.kc.zero_(), r.vc.zero_()
     turns, T = lib.rope_turns(r.inv_freq), r.q.shape[0]
-    for a in range(0, T, 1000):
-        b = min(a + 1000, T)
+    for a in range(0, T, FEW):
+        b = min(a + FEW, T)
         lib.norm_rope_store(r.q_out[a:b], r.q[a:b], r.k[a:b], r.v[a:b], r.positions[a:b], turns, r.kc, r.vc, r.slots[a:b], k_out=r.k_out[a:b],
                             q_weight=r.qw, k_weight=r.kw)
     torch.cuda.synchronize()
@@ -334,8 +337,8 @@ def test_streamed_in_halves(lib, Hq, Hkv, interleaved):
     q, k, kc, vc = r.q_out.clone(), r.k_out.clone(), r.kc.clone(), r.vc.clone()
     r.q_out.zero_(), r.k_out.zero_(), r.kc.zero_(), r.vc.zero_()
     turns, T = lib.rope_turns(r.inv_freq), r.q.shape[0]
-    for a in range(0, T, 1000):
-        b = min(a + 1000, T)
+    for a in range(0, T, FEW):
+        b = min(a + FEW, T)
         lib.norm_rope_store(r.q_out[a:b], r.q[a:b], r.k[a:b], r.v[a:b], r.positions[a:b], turns, r.kc, r.vc, r.slots[a:b], k_out=r.k_out[a:b],
                             q_weight=r.qw, k_weight=r.kw, interleaved=interleaved)
     torch.cuda.synchronize()
@@ -358,9 +361,10 @@ def test_many_rows_too_wide_to_stream(lib):
     q = r.q_out.clone()
     turns = lib.rope_turns(r.inv_freq)
     r.q_out.zero_()
-    lib.norm_rope_store(r.q_out[:700], r.q[:700], r.k[:700], r.v[:700], r.positions[:700], turns, r.kc, r.vc, r.slots[:700], q_weight=r.qw, k_weight=r.kw)
+    n = FEW
+    lib.norm_rope_store(r.q_out[:n], r.q[:n], r.k[:n], r.v[:n], r.positions[:n], turns, r.kc, r.vc, r.slots[:n], q_weight=r.qw, k_weight=r.kw)
     torch.cuda.synchronize()
-    assert torch.equal(q[:700], r.q_out[:700])
+    assert torch.equal(q[:n], r.q_out[:n])
 
 
 def test_rows_that_are_no_rows_are_refused(lib):
