@@ -324,9 +324,11 @@ struct PrefixGroups {
     // at level i (i = level[r]: r itself); better[r][i]: r is a group when that one is.
     std::vector<std::vector<int64_t>> inside(n_ranges);
     std::vector<std::vector<bool>> better(n_ranges);
-    for (size_t r = 0; r < n_ranges; ++r) inside[r].assign(level[r] + 1, 0);
     for (size_t r = n_ranges; r-- > 1;) {
       const Range &x = ranges[r];
+      // (room when first needed: in a chain of ranges for two of them at a time)
+      inside[r].resize(level[r] + 1);
+      inside[x.parent].resize(level[r]);
       const int64_t own = inside[r][level[r]] + (int64_t)(direct[r] - 1) * x.depth;
       better[r].assign(level[r], false);
       int up = x.parent;

@@ -416,6 +416,79 @@ def test_shared_or_not_as_it_pays(lib, groups, G, D):
     Shared(groups, 4 * G, 4, D, 64).check(lib)
 
 
+# Batches whose tables have little room are read whole, with no plan of the groups.
+
+@pytest.mark.by_choice
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (4, 1), (16, 2)])
+def test_a_small_batch(lib, Hq, Hkv, D):
+    Shared([(1, [0, 1, 63]), (2, [5, 70]), (0, [1, 15, 16, 17, 33])], Hq, Hkv, D).check(lib)
+
+
+@pytest.mark.by_choice
+def test_the_most_sequences_of_a_small_batch(lib):
+    """384 of them, and one more, which is planned."""
+    for n in (384, 385):
+        Shared([(1, [i % 60 for i in range(n)])], 2, 1, 64, 64).check(lib)
+
+
+@pytest.mark.by_choice
+def test_a_small_batch_with_empty_and_clamped_contexts(lib):
+    s = Shared([(2, [None, 5, 64]), (0, [None, 64, None])], 4, 2, 64)
+    s.check(lib, status=lib.DEV_BAD_CONTEXT)
+    s = Shared([(2, [64, 64, 10])], 4, 2, 64, 64)
+    s.ctx[1] = 10**6
+    s.check(lib, status=lib.DEV_BAD_CONTEXT)
+    s = Shared([(0, [None, None])], 4, 2, 64)
+    s.check(lib, status=lib.DEV_BAD_CONTEXT)
+
+
+@pytest.mark.by_choice
+@pytest.mark.parametrize("starts,shared", [([1, 2, 5], [3, 2]), ([0, 2, 4], [3, 2]), ([0, 6, 5], [3, 2]), ([0, -3, 5], [3, 2]), ([0, 2, 5], [-1, 2]),
+                                           ([0, 2, 5], [3, 1000])])
+def test_a_small_batch_with_bad_groups(lib, starts, shared):
+    s = Shared([(3, [4, 70]), (2, [5, 9, 30])], 4, 2, 64)
+    flag = lib.DEV_BAD_SEQLEN if starts != s.starts else lib.DEV_BAD_CONTEXT
+    s.starts, s.shared = starts, shared
+    s.check(lib, status=flag)
+
+
+@pytest.mark.by_choice
+def test_a_small_batch_with_block_ids_out_of_range(lib):
+    s = Shared([(2, [4, 70]), (2, [5, 9]), (0, [30])], 4, 2, 64, poison=False)
+    s.tables[0, 1] = s.kc.shape[0]
+    s.tables[3, 2] = -1
+    lib.paged_decode_shared_attn(**s.args(lib))
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == lib.DEV_BAD_BLOCK
+    s.compare(only={1, 2, 4})
+
+
+@pytest.mark.by_choice
+def test_small_and_large_batches_in_turn(lib):
+    """On one stream and workspace, none waited for on the host; then from a graph."""
+    few = Shared([(1, [5, 9]), (0, [100, 3])], 8, 2, 128)
+    many = Shared([(200, [(31 * i) % 200 for i in range(2)]), (0, [700, 1])], 8, 2, 128)
+    a, b = few.args(lib), many.args(lib)
+    assert a["workspace"].numel() == b["workspace"].numel()
+    b["workspace"] = a["workspace"]
+    for _ in range(4):
+        lib.paged_decode_shared_attn(**a)
+        lib.paged_decode_shared_attn(**b)
+    torch.cuda.synchronize()
+    few.compare(), many.compare()
+    want = few.out.clone(), many.out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            lib.paged_decode_shared_attn(**b)
+            lib.paged_decode_shared_attn(**a)
+    few.out.zero_(), many.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(few.out, want[0]) and torch.equal(many.out, want[1])
+
+
 @pytest.mark.parametrize("loading", [0, 1, 20])
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_wait_that_runs_out_then_the_next_call(lib, loading, D):

@@ -305,6 +305,40 @@ def test_streamed_rows_are_those_of_few(lib, T):
     assert torch.equal(kc.flatten(0, 1)[kept], r.kc.flatten(0, 1)[kept]) and torch.equal(vc.flatten(0, 1)[kept], r.vc.flatten(0, 1)[kept])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,R,store,k_out", [(1, 1, 64, 64, True, False), (3, 1, 128, 48, True, True), (5, 2, 64, 16, False, True)])
+def test_streamed_as_whole_rows(lib, Hq, Hkv, D, R, store, k_out, interleaved):
+    Rows(WHOLE + 7, Hq, Hkv, D, R, packed=store).check(lib, store=store, k_out=k_out, interleaved=interleaved)
+
+
+@pytest.mark.parametrize("T", [FEW + 100, WHOLE + 301])
+def test_streamed_on_streams_and_from_a_graph(lib, T):
+    """Two calls at a time, and a captured one, replayed on other positions."""
+    r = Rows(T, 16, 8, 128, 128)
+    turns = lib.rope_turns(r.inv_freq)
+    call = lambda out, kc, vc, stream=None: lib.norm_rope_store(out, r.q, r.k, r.v, r.positions, turns, kc, vc, r.slots, q_weight=r.qw, k_weight=r.kw, stream=stream)
+    call(r.q_out, r.kc, r.vc)
+    sets = [(torch.zeros_like(r.q_out), r.kc.clone().zero_(), r.vc.clone().zero_()) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for st, x in zip(streams, sets):
+            call(*x, stream=st)
+    torch.cuda.synchronize()
+    kept = r.slots[r.slots >= 0].long()
+    for out, kc, vc in sets:
+        assert torch.equal(out, r.q_out)
+        assert torch.equal(kc.flatten(0, 1)[kept], r.kc.flatten(0, 1)[kept]) and torch.equal(vc.flatten(0, 1)[kept], r.vc.flatten(0, 1)[kept])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*sets[0])
+    r.positions.add_(1)
+    graph.replay()
+    call(r.q_out, r.kc, r.vc)
+    torch.cuda.synchronize()
+    assert torch.equal(sets[0][0], r.q_out) and not torch.equal(sets[1][0], r.q_out)
+
+
 def test_streamed_in_place(lib):
     r = Rows(MANY + 50, 6, 2, 128, 128, packed=False)
     r.call(lib, k_out=True)

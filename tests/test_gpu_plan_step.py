@@ -270,6 +270,37 @@ def test_many_rows_in_place_and_sums_that_saturate(lib):
     p.check(lib, args)
 
 
+@pytest.mark.parametrize("rows", [300, 5000, 60000])
+def test_on_streams_and_from_a_graph(lib, rows):
+    """Two steps at a time over batches of their own, then both captured and replayed (one CTA, a cluster, rows in their own launch)."""
+    plans = [Plan([70 * s % 500 for s in range(30)], [rows // 30 + seed] * 30, block=64, seed=seed) for seed in range(2)]
+    args = [p.device() for p in plans]
+    wants = [p.want()[0] for p in plans]
+    given = [{k: v.clone() for k, v in a.items() if torch.is_tensor(v)} for a in args]
+    streams = [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+
+    def same():
+        torch.cuda.synchronize()
+        for a, want in zip(args, wants):
+            for name, values in want.items():
+                assert a[name].cpu().numpy().reshape(-1).tolist() == np.asarray(values, dtype=np.int64).reshape(-1).tolist(), name
+
+    for _ in range(3):
+        for st, a in zip(streams, args):
+            lib.plan_step(**a, stream=st)  # (lengths and count are not in place: it can be repeated)
+    same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for a in args:
+            lib.plan_step(**a)
+    for a, was in zip(args, given):
+        for name, t in was.items():
+            a[name].copy_(t)
+    graph.replay()
+    same()
+
+
 def test_refusals_of_the_binding(lib):
     a = Plan([5, 300], [1, 1]).device()
     for name in a:
