@@ -11,16 +11,15 @@
 // the step are its own.
 //
 // A launch of one CTA, or of one cluster of eight.  Every CTA scans the lengths by
-// itself (12 bytes a sequence); the sequences that end push their blocks; after a
-// cluster barrier all CTAs share the tables and the rows.  So lengths and counters
-// can be updated in place: nothing is written before everybody has read.  Many rows
-// (prompts) are left to a second launch over the whole GPU, which finds all it needs in
-// what the first one has written.
+// itself (12 bytes a sequence), and all share the rows, the tables and the stack.  A block
+// that is given back and taken again in the same step is looked up in the table that it
+// comes from, not on the stack, so nothing that is read is written in the same step but
+// lengths and counters (in place): those last, once everybody has read.  Many rows
+// (prompts) have a launch over the whole GPU ahead of that, which scans for itself too;
+// the launch behind it scans beside it, and waits only before it writes the lengths.
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
 // the lengths, one of blocks from the stack or a table, and the barriers between them.
-#include <cooperative_groups.h>
-
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
@@ -32,15 +31,22 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxSeqs = 16384;
 constexpr int kPlanCluster = 8;     // portable cluster size
-// Up to so many rows and sequences one CTA of kPlanSmallSeqs threads does the step, else a
-// cluster (256 decode rows 5.1 and 6.8 us, 400 7.4 and 7.1; eight prompts with 2000 rows
-// 5.8 and 5.7, with 4000 8.3 and 5.7).
+// Up to so many rows and sequences one CTA does the step, else a cluster (decode: 256 rows
+// 5.2 and 6.8 us, 400 6.1 and 7.5, 700 8.2 and 7.9; eight prompts with 2000 rows 5.7 and
+// 5.7, with 4000 8.1 and 5.9).  Its threads: 256, or 512 for more sequences (64 rows 4.1 us
+// with 256 and 5.8 with 1024, which wait for each other longer).
 constexpr int kPlanSmallRows = 2048;
-constexpr int kPlanSmallSeqs = 256;
-// From so many rows on they have a launch of their own (64 prompts: 29 thousand rows 8.3
-// us without and 8.8 with, 115 thousand 12.7 and 9.3).
-constexpr int kPlanManyRows = 49152;
-constexpr int kRowThreads = 256;
+constexpr int kPlanSmallSeqs = 512;
+// From so many rows on they have a launch of their own ahead (16 prompts with 8 thousand rows
+// 6.7 us without and 5.4 with, with 16 thousand 8.5 and 5.4, 64 with 115 thousand 13.4 and
+// 7.3; a second launch costs the host 2 us, which is why it is not 2048).
+constexpr int kPlanManyRows = 16384;
+// Threads of a CTA of theirs: two CTAs of 512 have an SM's registers, so that the launches
+// overlap (16 thousand rows: with 1024 threads 7.0 us), but many sequences are scanned
+// faster by 1024 (4000 of them: 15.5 and 14.0).
+constexpr int kPlanManyThreads = 512, kPlanManySeqs = 2048;
+
+enum { kAll, kRows, kState };
 
 struct PlanParams {
   const int32_t *new_lens;
@@ -62,7 +68,7 @@ struct PlanParams {
   int num_seqs;
   int max_blocks_per_seq;
   int block_shift;
-  int rows_after;    // the rows are left to plan_rows_kernel
+  int part;          // kAll, or with many rows kRows and kState
   int rows_16b;      // slots and positions are 16-byte aligned
 };
 
@@ -176,37 +182,47 @@ __device__ __forceinline__ void write_rows(const PlanParams &p, const int *first
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
-  namespace cg = cooperative_groups;
-  extern __shared__ int plan_smem[];
+    extern __shared__ int plan_smem[];
   __shared__ int64_t sums3[32][3];
   __shared__ int64_t sums1[32][1];
-  const int S = p.num_seqs, shift = p.block_shift;
+  const int S = p.num_seqs, shift = p.block_shift, bs1 = (1 << shift) - 1;
   int *first_row = plan_smem;           // [S + 1]
-  int *held = first_row + S + 1;        // [S]: L, or -1 - L when the sequence gets no slots
+  int *held = first_row + S + 1;        // [S]: L, or -1 - L when the sequence gets no slots;
+                                        // when it ends the first block that it gives
   int *base = held + S;                 // [S]: blocks needed before it; -1 - blocks given
                                         // before it when it ends
+  uint16_t *ending = reinterpret_cast<uint16_t *>(base + S);  // [those that end]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the grid is one cluster)
+  const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the grid is one cluster, or the rows')
+  const bool tells = p.part != kRows && rank == 0;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (The launch behind the rows' began after all of that one's CTAs had waited for what came
+  // before them both.)
+  if (p.part != kState) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   const int free_given = *p.num_free;
   const int per = (S + blockDim.x - 1) / (int)blockDim.x;
   const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
-  int64_t at[3] = {0, 0, 0}, total[3];  // give, need, rows
+  // Blocks given (2^38 at most) and, above them, sequences that end; need; rows.
+  constexpr int kEnds = 44;
+  constexpr int64_t kGive = ((int64_t)1 << kEnds) - 1;
+  int64_t at[3] = {0, 0, 0}, total[3];
   PlanSeq mine = {};                    // (the thread's last: its only one, mostly)
   for (int s = s0; s < s1; ++s) {
-    mine = plan_seq(p, s, rank == 0);
-    at[0] += mine.give;
+    mine = plan_seq(p, s, tells);
+    at[0] += mine.give + ((int64_t)mine.ends << kEnds);
     at[1] += mine.need;
     at[2] += mine.n;
   }
   const int free0 = min(max(free_given, 0), p.capacity);
-  if (free0 != free_given && rank == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+  if (free0 != free_given && tells && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
   scan_cta<3>(at, total, sums3);
-  const int left = (int)min((int64_t)free0 + total[0], (int64_t)p.capacity);
-  if (free0 + total[0] > p.capacity && rank == 0 && tid == 0)
-    flag_status(p.status, PKV_DEV_BAD_BLOCK);
+  const int64_t given = total[0] & kGive;
+  const int ends = (int)(total[0] >> kEnds);
+  const int left = (int)min((int64_t)free0 + given, (int64_t)p.capacity);
+  if (free0 + given > p.capacity && tells && tid == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
   int64_t keys[1] = {0}, all_keys[1], taken = 0;
   {
     int64_t give = at[0], need = at[1], row = at[2];
@@ -214,15 +230,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
       const PlanSeq q = per == 1 ? mine : plan_seq(p, s, false);
       const bool no_blocks = q.need > 0 && need + q.need > left;
       const bool no_rows = q.n > 0 && row + q.n > p.num_rows;
-      if (rank == 0 && (no_blocks || no_rows))
+      if (tells && (no_blocks || no_rows))
         flag_status(p.status, (no_blocks ? PKV_DEV_NO_BLOCKS : 0) | (no_rows ? PKV_DEV_BAD_SEQLEN : 0));
       const bool refused = no_blocks || no_rows || q.out;
       first_row[s] = saturated(row);
-      held[s] = refused ? -1 - q.L : q.L;
-      base[s] = q.ends ? -1 - saturated(min(give, (int64_t)p.capacity)) : saturated(need);
+      held[s] = q.ends ? q.borrowed : refused ? -1 - q.L : q.L;
+      base[s] = q.ends ? -1 - saturated(min(give & kGive, (int64_t)p.capacity)) : saturated(need);
+      if (q.ends) ending[give >> kEnds] = (uint16_t)s;
       if (!refused && q.need > 0) taken = need + q.need;
       if (!refused && !q.ends) keys[0] += q.L + q.n;
-      give += q.give;
+      give += q.give + ((int64_t)q.ends << kEnds);
       need += q.need;
       row += q.n;
     }
@@ -237,47 +254,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
   if (lane == 0) sums3[warp][0] = most;
   if (tid == 0) first_row[S] = saturated(total[2]);
   scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
-  // Sequences that end give their blocks back, the first one's first.
-  // (few sequences to a warp: its lanes are for their blocks)
-  const int W = ctas * warps, w = warp * ctas + rank;
-  const int chunk = min((S + W - 1) / W, 32);
-  if (total[0] > 0) {
-    for (int c = w * chunk; c < S; c += W * chunk) {
-      const int s = c + lane;
-      int count = 0, from = 0, to = 0;
-      if (lane < chunk && s < S && base[s] < 0) {
-        const PlanSeq q = plan_seq(p, s, false);
-        count = q.give;
-        from = q.borrowed;
-        to = -1 - base[s];
-      }
-      for_items(count, [&](int owner, int i, bool live) {
-        const int at = __shfl_sync(0xffffffffu, from, owner) + i;
-        const int64_t place = (int64_t)free0 + __shfl_sync(0xffffffffu, to, owner) + i;
-        if (live && place < p.capacity)
-          p.free_blocks[place] = p.block_tables[(int64_t)(c + owner) * p.max_blocks_per_seq + at];
-      });
-    }
-  }
-  // What comes back is on the stack, and nobody reads lengths or counters any more.
-  if (ctas > 1) cg::this_cluster().sync();
-  else __syncthreads();
+  // (nobody reads lengths or counters any more)
+  if (ctas > 1 && p.part != kRows) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
+  // The e-th of the sequences that end gives its blocks from held[s] on as numbers
+  // given_before(e), ... of those that come back.
+  auto given_before = [&](int e) { return -1 - base[ending[e]]; };
   // Block number b of the blocks needed, from the top of the stack.
   auto block_at = [&](int64_t b) -> int {
     const int64_t i = (int64_t)left - 1 - b;
-    return i >= 0 ? __ldcg(p.free_blocks + i) : -1;
+    if (i < free0) return i >= 0 ? p.free_blocks[i] : -1;
+    const int k = (int)(i - free0);
+    int lo = 0, hi = ends;  // the last one with given_before <= k
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (given_before(mid) <= k) lo = mid;
+      else hi = mid;
+    }
+    const int s = ending[lo];
+    return p.block_tables[(int64_t)s * p.max_blocks_per_seq + held[s] + k - given_before(lo)];
   };
-  const int bs1 = (1 << shift) - 1;
   // Rows: one a thread where that is enough of them.
-  const bool here = !p.rows_after || all_keys[0] >= 0x7FFFFFFF;
-  auto block_of = [&](int s, int L, int b) {
-    const int have = (L + bs1) >> shift;
-    return b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
-                    : block_at((int64_t)base[s] + b - have);
-  };
-  if (here) {
-    const int64_t threads = (int64_t)ctas * blockDim.x, me = (int64_t)rank * blockDim.x + tid;
+  const int64_t threads = (int64_t)ctas * blockDim.x, me = (int64_t)rank * blockDim.x + tid;
+  if (p.part != kState) {
+    auto block_of = [&](int s, int L, int b) {
+      const int have = (L + bs1) >> shift;
+      return b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
+                      : block_at((int64_t)base[s] + b - have);
+    };
     if (p.num_rows <= threads) {
       if (me < p.num_rows) write_rows<1>(p, first_row, held, me, block_of);
     } else {
@@ -285,9 +289,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
         write_rows<4>(p, first_row, held, t0, block_of);
     }
   }
+  if (p.part == kRows) return;
+  // Few rows: the stack and the tables are for other warps than the rows (each waits for a
+  // load of its own).
+  const int W = ctas * warps, w = warp * ctas + rank;
+  const int row_warps = ctas == 1 && p.part == kAll && 64 * p.num_rows <= 32 * threads ? (int)(p.num_rows + 31) >> 5 : 0;
+  // Sequences that end give their blocks back, the first one's first.
+  // (few of them to a warp: its lanes are for their blocks)
+  {
+    const int chunk = min((ends + W - 1) / W, 32);
+    for (int c = (w + W - row_warps) % W * chunk; c < ends; c += W * chunk) {
+      const int e = c + lane;
+      int count = 0, to = 0;
+      int64_t from = 0;
+      if (lane < chunk && e < ends) {
+        const int s = ending[e];
+        to = given_before(e);
+        count = (e + 1 < ends ? given_before(e + 1) : (int)min(given, (int64_t)p.capacity)) - to;
+        from = (int64_t)s * p.max_blocks_per_seq + held[s];
+      }
+      for_items(count, [&](int owner, int i, bool live) {
+        const int64_t at = __shfl_sync(0xffffffffu, from, owner) + i;
+        const int64_t place = (int64_t)free0 + __shfl_sync(0xffffffffu, to, owner) + i;
+        if (live && place < p.capacity) p.free_blocks[place] = p.block_tables[at];
+      });
+    }
+  }
   // Tables.
   if (total[1] > 0) {
-    for (int c = w * chunk; c < S; c += W * chunk) {
+    const int first = row_warps > 0 ? W / 2 : 0, some = W - first;
+    const int chunk = min((S + some - 1) / some, 32);
+    for (int c = (w - first) * chunk; w >= first && c < S; c += some * chunk) {
       const int s = c + lane;
       int count = 0, have = 0, from = 0;
       if (lane < chunk && s < S && held[s] >= 0 && base[s] >= 0) {
@@ -303,13 +335,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
       });
     }
   }
-  // Lengths and sums.
+  // Lengths and sums, once every CTA has read those from before.
+  if (p.part == kState) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   if (rank == ctas - 1) {
     int64_t key = keys[0];
     for (int s = s0; s < s1; ++s) {
       const int h = held[s], n = first_row[s + 1] - first_row[s];
-      const bool ends = base[s] < 0 && h >= 0;
-      const int after = ends ? 0 : h < 0 ? -1 : h + n;
+      const int after = base[s] < 0 ? 0 : h < 0 ? -1 : h + n;
       p.cu_q[s] = first_row[s];
       p.cu_k[s] = saturated(key);
       if (after > 0) key += after;
@@ -326,32 +362,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
         flag_status(p.status, PKV_DEV_BAD_SEQLEN);
     }
   }
-}
-
-// The rows of a large step, from what plan_step_kernel has written: a sequence that was
-// refused has no keys, and its length is the one before the step.
-__global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(const PlanParams p) {
-  extern __shared__ int plan_smem[];
-  const int S = p.num_seqs;
-  int *first_row = plan_smem;     // [S + 1]
-  int *held = first_row + S + 1;  // [S] (as in plan_step_kernel)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (p.cu_k[S] == 0x7FFFFFFF) return;  // (the sums may have saturated: done by the first launch)
-  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
-  for (int s = threadIdx.x; s < S; s += blockDim.x) {
-    const int row = p.cu_q[s], n = p.cu_q[s + 1] - row;
-    const int after = p.new_context_lens[s];
-    first_row[s] = row;
-    const int before = after < 0 || after > room ? 0 : after;
-    held[s] = p.cu_k[s + 1] == p.cu_k[s] ? -1 - before : after - n;
-  }
-  if (threadIdx.x == 0) first_row[S] = p.cu_q[S];
-  __syncthreads();
-  auto block_of = [&](int s, int, int b) { return p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]; };
-  const int64_t threads = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t t0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; t0 < p.num_rows; t0 += threads * 4)
-    write_rows<4>(p, first_row, held, t0, block_of);
 }
 
 }  // namespace
@@ -409,39 +419,45 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
 
-  prm.rows_after = num_rows >= kPlanManyRows ? 1 : 0;
+  prm.part = kAll;
   prm.rows_16b = aligned16(slot_mapping) && aligned16(positions) ? 1 : 0;
 
   const bool small = num_rows <= kPlanSmallRows && num_seqs <= kPlanSmallSeqs;
-  const int threads = small ? kPlanSmallSeqs : kPlanThreads;
-  const int smem = (3 * num_seqs + 1) * 4;
-  if (!kernel_smem_setup((const void *)plan_step_kernel, threads, smem, nullptr))
+  const bool many = num_rows >= kPlanManyRows;
+  const int threads = small ? (num_seqs <= 256 ? 256 : 512)
+                      : many && num_seqs <= kPlanManySeqs ? kPlanManyThreads
+                                                          : kPlanThreads;
+  const int smem = (3 * num_seqs + 1) * 4 + (num_seqs * 2 + 3) / 4 * 4;
+  static_assert((3 * kPlanMaxSeqs + 1) * 4 + kPlanMaxSeqs * 2 + 1024 <= 232448, "shared memory");
+  if (!kernel_smem_setup((const void *)plan_step_kernel, kPlanThreads, smem, nullptr))
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(small ? 1 : kPlanCluster);
-  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cfg.gridDim.x;
+  attr[1].val.clusterDim.x = small ? 1 : kPlanCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t err = cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
-  if (prm.rows_after && err == cudaSuccess) {
+  cudaError_t err = cudaSuccess;
+  if (many) {
     const int sms = device_sm_count();
-    const int row_smem = (2 * num_seqs + 1) * 4;
-    if (sms <= 0 || !kernel_smem_setup((const void *)plan_rows_kernel, kRowThreads, row_smem, nullptr))
-      return PKV_ERR_CUDA;
-    const int64_t groups = (num_rows + 4 * kRowThreads - 1) / (4 * kRowThreads);
-    cfg.gridDim = dim3((unsigned)(groups < 2 * sms ? groups : 2 * sms));
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = row_smem;
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int64_t ctas = (num_rows + threads - 1) / threads;
+    cfg.gridDim = dim3((unsigned)(ctas < sms ? ctas : sms));
+    cfg.blockDim = dim3(threads);
     cfg.numAttrs = 1;  // (no cluster)
-    cudaLaunchKernelEx(&cfg, plan_rows_kernel, prm);
+    prm.part = kRows;
+    err = cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+    prm.part = kState;
+  }
+  if (err == cudaSuccess) {
+    cfg.gridDim = dim3(small ? 1 : kPlanCluster);
+    cfg.blockDim = dim3(threads);
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
   }
   return launch_status();
 }

@@ -82,6 +82,11 @@ def test_random_steps(lib, seed, S, high, new, block):
     random_plan(seed, S, high, new, block).check(lib)
 
 
+@pytest.mark.parametrize("S", [256, 257, 512, 513])
+def test_as_many_sequences_as_threads(lib, S):
+    random_plan(S, S, 600, 2, 64).check(lib)
+
+
 @pytest.mark.parametrize("seed", range(4))
 @pytest.mark.parametrize("free", [0, 1, 7])
 @pytest.mark.parametrize("S", [40, 600])
@@ -233,11 +238,11 @@ def test_agrees_with_the_block_manager(lib):
         assert len(set(zip(theirs // block, ours // block))) == -(-n // block)
 
 
-# From 49152 rows on they are written by a launch of their own.
+# From 16384 rows on they are written by a launch of their own.
 
 @pytest.mark.parametrize("seed", range(3))
 @pytest.mark.parametrize("S,high,new,block,free", [(40, 3000, 1500, 64, None), (700, 900, 120, 128, 30), (3, 100, 20000, 512, None)])
-@pytest.mark.parametrize("least", [0, 49152])
+@pytest.mark.parametrize("least", [0, 16384, 49152])
 def test_many_rows(lib, seed, S, high, new, block, free, least):
     p = random_plan(seed, S, high, new, block, free=free)
     p.rows = max(p.rows, least) + 3 * seed
