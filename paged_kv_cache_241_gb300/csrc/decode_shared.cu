@@ -21,6 +21,15 @@
 //     TMA); the others the tails, all sequences' own tokens, cut into runs of equal
 //     length, a warp for each run and kv head (m16n8k16, cp.async; bound by HBM).
 //  3. join.
+//
+// What bounds it: long prefixes HBM and the tensor cores (16 sequences of 8 x 8 heads: 0.65
+// us per 1000 shared tokens, 6.3 TB/s; 128 of 4 x 8, two row tiles: 1.26 us per 64 keys of
+// a CTA, 2000 of 2400 cycles in products; with S of 128 keys at a time 1.38); tails HBM
+// (5.4 TB/s); and all of it a fixed part of 15 to 19 us: the plan 4 us, from the beginning
+// of a CTA to its first product 4, from a run's last product to its stores 3, the join 3,
+// what is between the launches 1 to 2.  In a graph of calls, floors by bytes in brackets:
+//   64 sequences behind 2048 tokens 32.4 us [21.8], 50 in 6 groups 27.9 [9.7],
+//   16 on a document of 32,000 39.9 [20.9], 128 behind 8192 50.0 [25.5], 2 short 6.4
 #include <math.h>
 
 #include <atomic>
@@ -43,7 +52,8 @@ constexpr int kMaxWarps = kMaxCtas * kWarpsMost;  // parts; a GB300 has 152 SMs)
 constexpr int kThreads = 384;            // of the attention's CTAs
 // A batch of at most so many sequences whose tables have room for no more K and V than
 // kSmallBytes is small: reading it whole takes 2 us or so, and a prefix's pipeline alone 6
-// (two sequences behind 256 tokens: 9.4 us without sharing, 12.6 with).
+// (two sequences behind 256 tokens: 6.4 us in the two launches, 9.4 planned but not shared,
+// 12.6 shared).
 constexpr int64_t kSmallBytes = 16 << 20;
 constexpr int kSmallSeqs = kThreads;
 constexpr int kNearGroups = 32;          // groups whose plans fit a CTA's shared memory
@@ -271,7 +281,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   int64_t cost = sum[0];
   int tile = (int)(at[1] >> 32), tiles = (int)(sum[1] >> 32);
   // Little work: reading every context whole takes less than a run of a prefix at its
-  // best, and so nothing is shared.
+  // best, and so nothing is shared (8 sequences behind 1024 tokens: 14.2 us so and 14.5
+  // shared; behind 2048 15.7 and 15.7, behind 8192 30.6 and 22.5).
   if (!p.share_always &&
       (float)(int)sum[1] * p.num_kv_heads * tile_ns(p.group_size) + (float)kTailNs * p.ctas <=
           (float)cost * kCostNs + (float)kPrefixNs * p.ctas) {

