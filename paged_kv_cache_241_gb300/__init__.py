@@ -107,7 +107,7 @@ SIGNATURES = {
 }
 
 _lib = None
-_call = None  # the C part of the binding (csrc/pycall.c)
+_call = None  # the C++ part of the binding (csrc/pycall.cc)
 
 
 class PkvError(RuntimeError):
@@ -136,18 +136,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _load_call(lib):
-    """The C part of the binding: the checks and calls of the operators that are called
+    """The C++ part of the binding: the checks and calls of the operators that are called
     once a step or a layer and are shorter than their checks in Python."""
     import torch
 
-    try:
-        from . import _pkv_call as call
-    except ImportError as e:
-        raise RuntimeError("the binding's C part is missing or of another interpreter: build it "
-                           "with `python -m paged_kv_cache_241_gb300.build`") from e
     address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "pkv_plan_step", "pkv_norm_rope_store", "pkv_paged_decode_shared_attn")]
-    call.bind(torch.bfloat16, torch.int32, torch.int64, torch.uint8, *address)
+    try:
+        from . import _pkv_call as call
+        call.bind(torch.__version__, *address)
+    except ImportError as e:
+        raise RuntimeError("the binding's C++ part is missing, or for another interpreter or "
+                           "torch: build it with `python -m paged_kv_cache_241_gb300.build`") from e
     return call
 
 
@@ -565,15 +565,9 @@ def kv_evict(k_cache, v_cache, key_weights, block_tables, context_lens, budget, 
     _check(st, "pkv_kv_evict")
 
 
-def _here(t, stream):
-    """(device, raw stream) of a call on tensor t, or (-1, 0) where t is not on the
-    current CUDA device (the library launches there)."""
-    import torch
-
-    dev = t.get_device()
-    if dev < 0 or torch._C._cuda_getDevice() != dev:
-        return -1, 0
-    return dev, _raw_stream(stream, dev)
+def _raw(stream):
+    """A stream as the C++ part takes it: None (torch's current one) or its address."""
+    return None if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def _refuse(what, args, dev_status):
@@ -603,16 +597,15 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
     borrowed_blocks [S]; block_tables [S, max_blocks]; free_blocks [any], num_free and
     new_num_free [1]; slot_mapping, positions [rows]; cu_seqlens_q, cu_seqlens_k [S + 1].
     new_context_lens may be context_lens, and new_num_free num_free."""
-    import torch
-
     if _call is None:
         load()
-    dev, raw = _here(block_tables, stream)
-    st = -1 if dev < 0 else _call.plan_step(
-        dev, raw, new_lens, context_lens, block_tables, free_blocks, num_free, new_context_lens,
-        new_num_free, slot_mapping, positions, cu_seqlens_q, cu_seqlens_k, num_blocks, block_size,
-        borrowed_blocks, dev_status)
+    st = _call.plan_step(
+        _raw(stream), new_lens, context_lens, block_tables, free_blocks, num_free,
+        new_context_lens, new_num_free, slot_mapping, positions, cu_seqlens_q, cu_seqlens_k,
+        num_blocks, block_size, borrowed_blocks, dev_status)
     if st < 0:
+        import torch
+
         i32 = torch.int32
         _refuse("plan_step", (
             ("new_lens", new_lens, i32, 1), ("context_lens", context_lens, i32, 1),
@@ -664,15 +657,14 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
     rope_turns: the first R dims turn), and the store of k and v at slot_mapping [T] of
     the caches, in one pass.  q, k and v may be strided by token (parts of one
     projection).  Without caches k goes to k_out [T, Hkv, D] alone.  bf16."""
-    import torch
-
     if _call is None:
         load()
-    dev, raw = _here(q, stream)
-    st = -1 if dev < 0 else _call.norm_rope_store(
-        dev, raw, q_out, q, k, v, positions, turns, k_cache, v_cache, slot_mapping, k_out,
+    st = _call.norm_rope_store(
+        _raw(stream), q_out, q, k, v, positions, turns, k_cache, v_cache, slot_mapping, k_out,
         q_weight, k_weight, eps, interleaved, amplitude, dev_status)
     if st < 0:
+        import torch
+
         bf16, i32 = torch.bfloat16, torch.int32
         store = [t is not None for t in (k_cache, v_cache, slot_mapping)]
         if any(store) != all(store):
@@ -712,15 +704,14 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
     group_starts[g] .. group_starts[g + 1] - 1 (int32 [groups + 1]), and the first
     shared_blocks[g] (int32 [groups]) blocks of its sequences are the same ones, read
     once (see include/pkv.h; BlockManager.prefix_groups finds groups)."""
-    import torch
-
     if _call is None:
         load()
-    dev, raw = _here(q, stream)
-    st = -1 if dev < 0 else _call.paged_decode_shared_attn(
-        dev, raw, out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
+    st = _call.paged_decode_shared_attn(
+        _raw(stream), out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
         shared_blocks, scale, workspace, dev_status)
     if st < 0:
+        import torch
+
         bf16, i32 = torch.bfloat16, torch.int32
         _refuse("paged_decode_shared_attn", (
             ("out", out, bf16, 3), ("q", q, bf16, 3), ("k_cache", k_cache, bf16, 4),

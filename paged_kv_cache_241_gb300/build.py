@@ -3,8 +3,8 @@
     python -m paged_kv_cache_241_gb300.build
 
 Compiles every csrc/*.cu (and the host-only *.cpp) in parallel with nvcc and
-links libpkv.so next to this file; beside it the C part of the Python binding
-(csrc/pycall.c), for the interpreter that runs this.  No CMake; a rebuild only
+links libpkv.so next to this file; beside it the C++ part of the Python binding
+(csrc/pycall.cc), for the interpreter and the torch that run this.  No CMake; a rebuild only
 recompiles sources newer than their object.
 """
 from __future__ import annotations
@@ -54,37 +54,47 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def call_module() -> str:
-    """Where the C part of the binding is for this interpreter."""
+    """Where the C++ part of the binding is for this interpreter."""
     return os.path.join(HERE, "_pkv_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
 def _build_call_module() -> None:
-    src, out = os.path.join(CSRC, "pycall.c"), call_module()
-    if os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(src), _headers_mtime()):
+    import torch
+
+    src, out = os.path.join(CSRC, "pycall.cc"), call_module()
+    home = os.path.dirname(torch.__file__)
+    inputs = [src, os.path.join(INCLUDE, "pkv.h"), os.path.join(home, "version.py")]
+    if os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, inputs)):
         return
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        raise RuntimeError("no C compiler for the Python binding")
-    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-           src, "-o", out]
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler for the Python binding")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DPKV_TORCH_VERSION="{torch.__version__}"',
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-isystem", os.path.join(home, "include"), "-isystem", cuda, src, "-o", out,
+           "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cxx} failed for {src}:\n{r.stdout}\n{r.stderr}")
 
 
 def build(verbose_ptxas: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        call = ex.submit(_build_call_module)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        call.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    _build_call_module()
     return LIB
 
 

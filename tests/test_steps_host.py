@@ -143,6 +143,25 @@ def test_host_tensors_and_wrong_dtypes_are_refused(call, args):
         f(**{**a, first: a[first].double()})
 
 
+@pytest.mark.parametrize("call,args", [("plan_step", plan_args), ("norm_rope_store", rope_args), ("paged_decode_shared_attn", shared_args)])
+def test_tensors_without_storage_and_no_tensors_are_refused(call, args):
+    f = getattr(pkv, call)
+    a = args()
+    for name, t in a.items():
+        if torch.is_tensor(t):
+            for other in (t.to("meta"), torch.zeros(2).to_sparse(), t.tolist(), "x", 7):
+                with pytest.raises((TypeError, ValueError, AttributeError)):
+                    f(**{**a, name: other})
+
+
+def test_the_bindings_module_is_for_one_torch():
+    pkv.load()
+    with pytest.raises(ImportError, match="built for torch"):
+        pkv._call.bind("0.1", 1, 2, 3)
+    assert pkv._call.bind(torch.__version__, *[ctypes.cast(getattr(pkv.load(), "pkv_" + n), ctypes.c_void_p).value for n in
+                                                ("plan_step", "norm_rope_store", "paged_decode_shared_attn")]) is None
+
+
 def test_parts_that_go_together():
     a = rope_args()
     for missing in ("k_cache", "v_cache", "slot_mapping"):
