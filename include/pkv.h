@@ -489,9 +489,9 @@ pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *key_weights
  * twice, nor held and free, but in borrowed places.  Sums saturate at 2^31 - 1
  * (flagged BAD_SEQLEN).
  *
- * One launch, two from 16384 rows on.  Supported: block_size in {64, 128, 256, 512};
- * num_seqs <= 16384; max_blocks_per_seq * block_size at most 2^30; num_blocks *
- * block_size and free_capacity below 2^31, num_rows below 2^31 - 1.
+ * One launch for up to 256 sequences and 1024 rows, else two.  Supported: block_size in
+ * {64, 128, 256, 512}; num_seqs <= 16384; max_blocks_per_seq * block_size at most 2^30;
+ * num_blocks * block_size and free_capacity below 2^31, num_rows below 2^31 - 1.
  */
 pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *context_lens,
                          const int32_t *borrowed_blocks, int32_t *block_tables,

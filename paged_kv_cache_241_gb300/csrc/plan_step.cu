@@ -10,13 +10,13 @@
 // the stack of free blocks a sequence's blocks go to or come from, and which rows of
 // the step are its own.
 //
-// A launch of one CTA, or of one cluster of eight.  Every CTA scans the lengths by
-// itself (12 bytes a sequence), and all share the rows, the tables and the stack.  A block
-// that is given back and taken again in the same step is looked up in the table that it
-// comes from, not on the stack, so nothing that is read is written in the same step but
-// lengths and counters (in place): those last, once everybody has read.  Many rows
-// (prompts) have a launch over the whole GPU ahead of that, which scans for itself too;
-// the launch behind it scans beside it, and waits only before it writes the lengths.
+// A small step is one CTA's.  For a larger one a launch over the whole GPU writes the rows,
+// and a cluster of eight the tables, the stack and the lengths; every CTA scans the lengths
+// by itself (12 bytes a sequence).  A block that is given back and taken again in the same
+// step is looked up in the table that it comes from, not on the stack, so nothing that is
+// read is written in the same step but lengths and counters (in place): those last, once
+// everybody has read.  So the second launch scans beside the first, and waits for it only
+// before it writes the lengths.
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
 // the lengths, one of blocks from the stack or a table, and the barriers between them: 4.1
@@ -29,23 +29,19 @@
 namespace pkv {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxSeqs = 16384;
 constexpr int kPlanCluster = 8;     // portable cluster size
-// Up to so many rows and sequences one CTA does the step, else a cluster (decode: 256 rows
-// 5.2 and 6.8 us, 400 6.1 and 7.5, 700 8.2 and 7.9; eight prompts with 2000 rows 5.7 and
-// 5.7, with 4000 8.1 and 5.9).  Its threads: 256, or 512 for more sequences (64 rows 4.1 us
-// with 256 and 5.8 with 1024, which wait for each other longer).
-constexpr int kPlanSmallRows = 2048;
-constexpr int kPlanSmallSeqs = 512;
-// From so many rows on they have a launch of their own ahead (16 prompts with 8 thousand rows
-// 6.7 us without and 5.4 with, with 16 thousand 8.5 and 5.4, 64 with 115 thousand 13.4 and
-// 7.3; a second launch costs the host 2 us, which is why it is not 2048).
-constexpr int kPlanManyRows = 16384;
-// Threads of a CTA of theirs: two CTAs of 512 have an SM's registers, so that the launches
-// overlap (16 thousand rows: with 1024 threads 7.0 us), but many sequences are scanned
-// faster by 1024 (4000 of them: 15.5 and 14.0).
-constexpr int kPlanManyThreads = 512, kPlanManySeqs = 2048;
+// Up to so many rows and sequences one CTA of as many threads as sequences does the step, a
+// thread four rows at most (decode: 256 rows 5.2 us, in two launches 5.6; eight prompts with
+// 1000 rows 4.7 and 5.0, with 1500 5.8 and 5.0; 500 sequences by one CTA of 512 threads 6.2,
+// in two launches 5.8).  A single launch of the cluster alone did 1000 rows in 8.3 us and
+// 16 thousand in 8.5 (two launches: 6.8 and 5.3).
+constexpr int kPlanSmallRows = 1024;
+constexpr int kPlanSmallSeqs = 256;
+// Threads of a CTA of a larger step: two CTAs of 512 have an SM's registers, so that the
+// launches overlap (1000 rows 6.8 us, 7.9 with 1024 threads), but many sequences are scanned
+// faster by 1024 (4000 of them: 15.3 and 13.8).
+constexpr int kPlanThreads = 512, kPlanManyThreads = 1024, kPlanManySeqs = 2048;
 
 enum { kAll, kRows, kState };
 
@@ -69,7 +65,7 @@ struct PlanParams {
   int num_seqs;
   int max_blocks_per_seq;
   int block_shift;
-  int part;          // kAll, or with many rows kRows and kState
+  int part;          // kAll, or in two launches kRows and kState
   int rows_16b;      // slots and positions are 16-byte aligned
 };
 
@@ -182,7 +178,7 @@ __device__ __forceinline__ void write_rows(const PlanParams &p, const int *first
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
+__global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanParams p) {
     extern __shared__ int plan_smem[];
   __shared__ int64_t sums3[32][3];
   __shared__ int64_t sums1[32][1];
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
                                         // before it when it ends
   uint16_t *ending = reinterpret_cast<uint16_t *>(base + S);  // [those that end]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the grid is one cluster, or the rows')
+  const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the rows' grid, else one cluster)
   const bool tells = p.part != kRows && rank == 0;
 
   // (The launch behind the rows' began after all of that one's CTAs had waited for what came
@@ -420,17 +416,13 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   prm.max_blocks_per_seq = max_blocks_per_seq;
   prm.block_shift = 31 - __builtin_clz((unsigned)block_size);
 
-  prm.part = kAll;
   prm.rows_16b = aligned16(slot_mapping) && aligned16(positions) ? 1 : 0;
 
   const bool small = num_rows <= kPlanSmallRows && num_seqs <= kPlanSmallSeqs;
-  const bool many = num_rows >= kPlanManyRows;
-  const int threads = small ? (num_seqs <= 256 ? 256 : 512)
-                      : many && num_seqs <= kPlanManySeqs ? kPlanManyThreads
-                                                          : kPlanThreads;
+  const int threads = small ? kPlanSmallSeqs : num_seqs <= kPlanManySeqs ? kPlanThreads : kPlanManyThreads;
   const int smem = (3 * num_seqs + 1) * 4 + (num_seqs * 2 + 3) / 4 * 4;
   static_assert((3 * kPlanMaxSeqs + 1) * 4 + kPlanMaxSeqs * 2 + 1024 <= 232448, "shared memory");
-  if (!kernel_smem_setup((const void *)plan_step_kernel, kPlanThreads, smem, nullptr))
+  if (!kernel_smem_setup((const void *)plan_step_kernel, threads, smem, nullptr))
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = smem;
@@ -443,7 +435,7 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cudaError_t err = cudaSuccess;
-  if (many) {
+  if (!small && num_rows > 0) {
     const int sms = device_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     const int64_t ctas = (num_rows + threads - 1) / threads;
@@ -452,9 +444,9 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
     cfg.numAttrs = 1;  // (no cluster)
     prm.part = kRows;
     err = cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
-    prm.part = kState;
   }
   if (err == cudaSuccess) {
+    prm.part = small || num_rows == 0 ? kAll : kState;
     cfg.gridDim = dim3(small ? 1 : kPlanCluster);
     cfg.blockDim = dim3(threads);
     cfg.numAttrs = 2;

@@ -82,7 +82,17 @@ def test_random_steps(lib, seed, S, high, new, block):
     random_plan(seed, S, high, new, block).check(lib)
 
 
-@pytest.mark.parametrize("S", [256, 257, 512, 513])
+@pytest.mark.parametrize("rows", [1023, 1024, 1025])
+def test_about_as_many_rows_as_one_cta_writes(lib, rows):
+    Plan([100, 0, 63, 700], [300, rows - 301, 0, 1], block=64).check(lib)
+
+
+def test_many_sequences_none_with_rows(lib):
+    """All of them pause or end: no rows at all."""
+    Plan([(37 * s) % 700 for s in range(600)], [-(s % 2) for s in range(600)], block=64, rows=0).check(lib)
+
+
+@pytest.mark.parametrize("S", [256, 257, 512, 513, 2048, 2049])
 def test_as_many_sequences_as_threads(lib, S):
     random_plan(S, S, 600, 2, 64).check(lib)
 
@@ -238,11 +248,11 @@ def test_agrees_with_the_block_manager(lib):
         assert len(set(zip(theirs // block, ours // block))) == -(-n // block)
 
 
-# From 16384 rows on they are written by a launch of their own.
+# Steps of more than 256 sequences or 1024 rows have two launches.
 
 @pytest.mark.parametrize("seed", range(3))
 @pytest.mark.parametrize("S,high,new,block,free", [(40, 3000, 1500, 64, None), (700, 900, 120, 128, 30), (3, 100, 20000, 512, None)])
-@pytest.mark.parametrize("least", [0, 16384, 49152])
+@pytest.mark.parametrize("least", [0, 1025, 16384, 49152, 400000])
 def test_many_rows(lib, seed, S, high, new, block, free, least):
     p = random_plan(seed, S, high, new, block, free=free)
     p.rows = max(p.rows, least) + 3 * seed
@@ -277,7 +287,7 @@ def test_many_rows_in_place_and_sums_that_saturate(lib):
 
 @pytest.mark.parametrize("rows", [300, 5000, 60000])
 def test_on_streams_and_from_a_graph(lib, rows):
-    """Two steps at a time over batches of their own, then both captured and replayed (one CTA, a cluster, rows in their own launch)."""
+    """Two steps at a time over batches of their own, then both captured and replayed (one CTA, two launches)."""
     plans = [Plan([70 * s % 500 for s in range(30)], [rows // 30 + seed] * 30, block=64, seed=seed) for seed in range(2)]
     args = [p.device() for p in plans]
     wants = [p.want()[0] for p in plans]
