@@ -172,11 +172,13 @@ __device__ __forceinline__ int64_t run_cost(const Totals &t) {
 // tile of a tail (K and V of tail_rows tokens, a kv head) for all of a CTA's warps, and
 // of their beginning.
 constexpr int kCostNs = 340, kPrefixNs = 6000, kTailNs = 2500;
-// (eight heads take two products with V)
-__device__ __forceinline__ float tile_ns(int G) { return G == 8 ? 175.f : 145.f; }
+// (A tile of 64 dims is two slices of 16 tokens, and eight heads take two products with V.)
+__device__ __forceinline__ float tile_ns(const SharedParams &p) {
+  return p.head_dim == 64 ? (p.group_size == 8 ? 200.f : 165.f) : p.group_size == 8 ? 175.f : 115.f;
+}
 
 __device__ __forceinline__ int split_ctas(const SharedParams &p, float cost, float tiles) {
-  const float a = cost * kCostNs, b = tiles * p.num_kv_heads * tile_ns(p.group_size);
+  const float a = cost * kCostNs, b = tiles * p.num_kv_heads * tile_ns(p);
   if (a == 0.f) return 0;
   if (b == 0.f) return p.ctas;
   // a / n + kPrefixNs = b / (ctas - n) + kTailNs, solved for n: the whole number beside
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   // best, and so nothing is shared (8 sequences behind 1024 tokens: 14.2 us so and 14.5
   // shared; behind 2048 15.7 and 15.7, behind 8192 30.6 and 22.5).
   if (!p.share_always &&
-      (float)(int)sum[1] * p.num_kv_heads * tile_ns(p.group_size) + (float)kTailNs * p.ctas <=
+      (float)(int)sum[1] * p.num_kv_heads * tile_ns(p) + (float)kTailNs * p.ctas <=
           (float)cost * kCostNs + (float)kPrefixNs * p.ctas) {
     ok = false;
     at[0] = cost = 0;
@@ -617,6 +619,20 @@ struct PrefixCols {
   static constexpr uint32_t kS = 2 * D;
 };
 
+// One thread of the warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// A value that all of the warp has, as one of the warp.
+__device__ __forceinline__ int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   const bool ok = mbar_wait_bounded(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
@@ -673,7 +689,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
 
   float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int64_t len = run_cost(sum);
   const int64_t x0 = (int64_t)blockIdx.x * len;
   if (x0 >= sum.cost) return;
@@ -719,7 +735,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     tc_fence_before_sync();
     named_bar_sync(1, kThreads - 64);
     tc_fence_after_sync();
-    tmem = *tmem_slot;
+    tmem = warp_same(*tmem_slot);
   }
 
   auto next_piece = [&](int &iu, Piece &u) -> bool {
@@ -899,7 +915,9 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == kSWarp || warp == kPVWarp) {
     // Issuers: warp 1 S = Q K^T, warp 3 O += P V.  gh[h]: steps of chain h so far, uh[h]:
-    // pieces of which it had any.
+    // pieces of which it had any.  All of the warp goes through the steps and an elected
+    // thread issues, so that addresses and descriptors are the warp's (with one thread's a
+    // product took 100 cycles to issue, more than to compute).
     int iu = 0, g = 0;
     int gh[2] = {0, 0}, uh[2] = {0, 0};
     bool ok = true;
@@ -909,88 +927,89 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
       const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = umma_desc_sw128(smem_u32(sK), 16, 1024);
       while (ok && next_piece(iu, u)) {
-        const bool both = u.rows > BM;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(q_full, (iu - 1) & 1, abort_flag);
-          for (int i = 0; i < u.n && ok; ++i, ++g) {
-            const int st = g % kKStages;
-            ok = mbar_wait_bounded(&k_full[st], (g / kKStages) & 1, abort_flag);
-            const uint64_t dk_st = dk + (uint64_t)((st * L::kKVBytes) >> 4);
+        const bool both = warp_same(u.rows) > BM;
+        const int n = warp_same(u.n);
+        ok = warp_wait(q_full, (iu - 1) & 1, abort_flag);
+        for (int i = 0; i < n && ok; ++i, ++g) {
+          const int st = g % kKStages;
+          ok = warp_wait(&k_full[st], (g / kKStages) & 1, abort_flag);
+          const uint64_t dk_st = dk + (uint64_t)((st * L::kKVBytes) >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!ok) break;
-              if (!both && h != (i & 1)) continue;
-              const int gt = gh[h] + (both ? i : i >> 1), b = gt & 1;
-              if (gt >= 2)
-                ok = mbar_wait_bounded(&p_free[2 * h + b], ((gt - 2) >> 1) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after_sync();
-              const uint32_t d = tmem + kSCol + (2 * h + b) * BN;
+          for (int h = 0; h < 2; ++h) {
+            if (!ok) break;
+            if (!both && h != (i & 1)) continue;
+            const int gt = gh[h] + (both ? i : i >> 1), b = gt & 1;
+            if (gt >= 2) ok = warp_wait(&p_free[2 * h + b], ((gt - 2) >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + kSCol + (2 * h + b) * BN;
+            const uint64_t dq_h = dq + (uint64_t)((both ? h * L::kQBytes : 0) >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk & 3) * 32;
-                umma_bf16(d, dq + (uint64_t)(((both ? h * L::kQBytes : 0) + (kk / 4) * BM * 128 + off) >> 4),
+                umma_bf16(d, dq_h + (uint64_t)(((kk / 4) * BM * 128 + off) >> 4),
                           dk_st + (uint64_t)(((kk / 4) * BN * 128 + off) >> 4), idesc_s,
                           kk > 0 ? 1u : 0u);
               }
               umma_commit(&s_full[2 * h + b]);
             }
-            if (ok) umma_commit(&k_empty[st]);
+            __syncwarp();
           }
-          if (ok) umma_commit(q_empty);
+          if (ok && elect_one()) umma_commit(&k_empty[st]);
+          __syncwarp();
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        g = __shfl_sync(0xffffffffu, g, 0);
-        gh[0] += chain_steps(u, 0);
-        gh[1] += chain_steps(u, 1);
+        if (ok && elect_one()) umma_commit(q_empty);
+        __syncwarp();
+        gh[0] += both ? n : (n + 1) >> 1;
+        gh[1] += both ? n : n >> 1;
       }
     } else {
       constexpr uint32_t idesc_o = umma_idesc_bf16(BM, D, false, true);
       const uint64_t dv = umma_desc_sw128(smem_u32(sV), BN * 128, 1024);
       while (ok && next_piece(iu, u)) {
-        const bool both = u.rows > BM;
-        if (lane == 0) {
-          for (int i = 0; i < u.n && ok; ++i, ++g) {
-            const int st = g % kVStages;
-            ok = mbar_wait_bounded(&v_full[st], (g / kVStages) & 1, abort_flag);
-            const uint64_t dv_st = dv + (uint64_t)((st * L::kKVBytes) >> 4);
+        const bool both = warp_same(u.rows) > BM;
+        const int n = warp_same(u.n);
+        for (int i = 0; i < n && ok; ++i, ++g) {
+          const int st = g % kVStages;
+          ok = warp_wait(&v_full[st], (g / kVStages) & 1, abort_flag);
+          const uint64_t dv_st = dv + (uint64_t)((st * L::kKVBytes) >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!ok) break;
-              if (!both && h != (i & 1)) continue;
-              const int ih = both ? i : i >> 1;  // the chain's own number of the step
-              const int gt = gh[h] + ih, b = gt & 1;
-              ok = mbar_wait_bounded(&p_full[2 * h + b], (gt >> 1) & 1, abort_flag);
-              if (ok && ih == 0 && uh[h] >= 1)
-                ok = mbar_wait_bounded(&o_free[h], (uh[h] - 1) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after_sync();
-              const uint32_t pa = tmem + kSCol + (2 * h + b) * BN;
-              // Both terms of P: columns 0-31 and 32-63 of the buffer.
+          for (int h = 0; h < 2; ++h) {
+            if (!ok) break;
+            if (!both && h != (i & 1)) continue;
+            const int ih = both ? i : i >> 1;  // the chain's own number of the step
+            const int gt = gh[h] + ih, b = gt & 1;
+            ok = warp_wait(&p_full[2 * h + b], (gt >> 1) & 1, abort_flag);
+            if (ok && ih == 0 && uh[h] >= 1) ok = warp_wait(&o_free[h], (uh[h] - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t pa = tmem + kSCol + (2 * h + b) * BN;
+            const uint32_t onto = ih > 0 ? 1u : 0u;
+            // Both terms of P: columns 0-31 and 32-63 of the buffer.
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < BN / 8; ++kk)
                 umma_bf16_tmem_a(tmem + h * D, pa + kk * 8,
                                  dv_st + (uint64_t)(((kk % (BN / 16)) * 16 * 128) >> 4), idesc_o,
-                                 (ih > 0 || kk > 0) ? 1u : 0u);
+                                 kk > 0 ? 1u : onto);
               umma_commit(&p_free[2 * h + b]);
             }
-            if (ok) umma_commit(&v_empty[st]);
+            __syncwarp();
           }
+          if (ok && elect_one()) umma_commit(&v_empty[st]);
+          __syncwarp();
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        g = __shfl_sync(0xffffffffu, g, 0);
         for (int h = 0; h < 2; ++h) {
-          const int n = chain_steps(u, h);
-          gh[h] += n;
-          uh[h] += n > 0 ? 1 : 0;
+          const int m = both ? n : (n + 1 - h) >> 1;
+          gh[h] += m;
+          uh[h] += m > 0 ? 1 : 0;
         }
       }
     }
-    if (lane == 0) {
-      // Wait for the products of both issuers before tensor memory is freed.
-      umma_commit(drain);
-      if (!mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
-    }
+    // Wait for the products of both issuers before tensor memory is freed.
+    if (elect_one()) umma_commit(drain);
+    if (lane == 0 && !mbar_wait_bounded(drain, 0, nullptr)) flag_status(p.status, PKV_DEV_TIMEOUT);
   } else {
     // Softmax: four warps per chain, a thread per row (chain 0: warps 4, 5, 10, 11).
     const int h = (((warp - 4) >> 1) ^ ((warp - 4) >> 2)) & 1;
