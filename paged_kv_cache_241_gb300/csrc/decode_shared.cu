@@ -74,14 +74,15 @@ struct GroupPlan {
   int tiles;      // steps of 64 keys (0: nothing is shared)
   int pad[2];
 };
-// The cost of a step, in kCostNs: of a unit with two row tiles 4 (its products), of one
+// The cost of a step, in cost_ns: of a unit with two row tiles 5 (its products), of one
 // with a single row tile 3 (its loads).  A unit's beginning costs kUnitCost ahead of its
 // steps (a run that goes through the end of one into the next drains its pipeline there);
 // a kv head's units follow one another.
-constexpr int kUnitCost = 14;
-__device__ __forceinline__ int step_cost(int rows) { return rows > BM ? 4 : 3; }
+constexpr int kUnitCost = 20;
+constexpr int kPairCost = 5, kSingleCost = 3;
+__device__ __forceinline__ int step_cost(int rows) { return rows > BM ? kPairCost : kSingleCost; }
 __device__ __forceinline__ int64_t full_unit_cost(const GroupPlan &g) {  // of 256 rows
-  return kUnitCost + 4 * (int64_t)g.tiles;
+  return kUnitCost + kPairCost * (int64_t)g.tiles;
 }
 __device__ __forceinline__ int64_t head_cost(const GroupPlan &g, int group_size) {
   const int rows = g.members * group_size, last = rows % kPairRows;
@@ -162,7 +163,7 @@ __device__ __forceinline__ int run_tiles(const SharedParams &p, const Totals &t)
 // between a unit's first and last has a step of it).
 __device__ __forceinline__ int64_t run_cost(const Totals &t) {
   const int n = max(t.prefix_ctas, 1);
-  return max(quotient(t.cost + n - 1, n), (int64_t)4);
+  return max(quotient(t.cost + n - 1, n), (int64_t)kPairCost);
 }
 
 // ----------------------------------------------------------------------- 1. plan
@@ -170,15 +171,18 @@ __device__ __forceinline__ int64_t run_cost(const Totals &t) {
 // How many of the CTAs take the prefixes: what lets both kinds end together.  Times in
 // nanoseconds, as measured: of a unit of cost, and the beginning and end of a run; of a
 // tile of a tail (K and V of tail_rows tokens, a kv head) for all of a CTA's warps, and
-// of their beginning.
-constexpr int kCostNs = 340, kPrefixNs = 6000, kTailNs = 2500;
+// of their beginning; and what sharing costs beside.
+constexpr int kPrefixNs = 6000, kTailNs = 2500, kSharingNs = 2800;
+__device__ __forceinline__ float cost_ns(const SharedParams &p) {
+  return p.head_dim == 64 ? 220.f : 255.f;
+}
 // (A tile of 64 dims is two slices of 16 tokens, and eight heads take two products with V.)
 __device__ __forceinline__ float tile_ns(const SharedParams &p) {
-  return p.head_dim == 64 ? (p.group_size == 8 ? 200.f : 165.f) : p.group_size == 8 ? 175.f : 115.f;
+  return p.head_dim == 64 ? (p.group_size == 8 ? 165.f : 150.f) : p.group_size == 8 ? 140.f : 115.f;
 }
 
 __device__ __forceinline__ int split_ctas(const SharedParams &p, float cost, float tiles) {
-  const float a = cost * kCostNs, b = tiles * p.num_kv_heads * tile_ns(p);
+  const float a = cost * cost_ns(p), b = tiles * p.num_kv_heads * tile_ns(p);
   if (a == 0.f) return 0;
   if (b == 0.f) return p.ctas;
   // a / n + kPrefixNs = b / (ctas - n) + kTailNs, solved for n: the whole number beside
@@ -283,11 +287,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   int64_t cost = sum[0];
   int tile = (int)(at[1] >> 32), tiles = (int)(sum[1] >> 32);
   // Little work: reading every context whole takes less than a run of a prefix at its
-  // best, and so nothing is shared (8 sequences behind 1024 tokens: 14.2 us so and 14.5
-  // shared; behind 2048 15.7 and 15.7, behind 8192 30.6 and 22.5).
+  // best, and so nothing is shared (of 8 x 2 heads: 8 sequences behind 1024 tokens 13.0 us
+  // so and 15.1 shared, behind 2048 14.9 and 16.8, 16 behind 2048 19.2 and 16.8).
   if (!p.share_always &&
       (float)(int)sum[1] * p.num_kv_heads * tile_ns(p) + (float)kTailNs * p.ctas <=
-          (float)cost * kCostNs + (float)kPrefixNs * p.ctas) {
+          (float)cost * cost_ns(p) + (float)(kPrefixNs + kSharingNs) * p.ctas) {
     ok = false;
     at[0] = cost = 0;
     tile = (int)at[1];
