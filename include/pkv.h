@@ -590,10 +590,10 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  *
  * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
  *
- * Three launches, two for small batches.  Supported: head_dim in {64, 128}; Hq/Hkv in
- * {1, 2, 4, 8}; block_size in {64, 128, 256, 512}; num_seqs <= 8192, 1 <= num_groups <= num_seqs
- * (else PKV_ERR_INVALID_ARG); at most 4096 kv heads; max_blocks_per_seq * block_size at
- * most 2^20.
+ * Three launches, two for small batches and one for those of few and short contexts.
+ * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in {64, 128, 256,
+ * 512}; num_seqs <= 8192, 1 <= num_groups <= num_seqs (else PKV_ERR_INVALID_ARG); at most
+ * 4096 kv heads; max_blocks_per_seq * block_size at most 2^20.
  */
 pkv_status pkv_paged_decode_shared_attn(
     uint16_t *out, const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,

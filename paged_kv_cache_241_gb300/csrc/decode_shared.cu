@@ -11,25 +11,28 @@
 // decode.  All parts (M, l, o) of a row are then joined:
 //   out = sum_i exp(M_i - M) o_i / sum_i exp(M_i - M) l_i.
 //
-// Three launches, each a programmatic dependent of the one before, or two:
+// Three launches, each a programmatic dependent of the one before:
 //  1. plan: one CTA.  A group's prefix ends where its shortest sequence does; prefix
 //     sums of the work of groups (steps of 64 keys) and of sequences (tiles of 4 KiB
-//     of K) go to the workspace, and how many CTAs work on prefixes.  A small batch has
-//     no such launch and shares nothing: every CTA of the next one sums up the lengths.
+//     of K) go to the workspace, and how many CTAs work on prefixes.
 //  2. attention: one CTA per SM.  Some of them take the prefixes, units of (group, kv
 //     head, 256 rows) by steps, cut into runs of equal cost, a CTA for each (tcgen05,
 //     TMA); the others the tails, all sequences' own tokens, cut into runs of equal
 //     length, a warp for each run and kv head (m16n8k16, cp.async; bound by HBM).
 //  3. join.
+// A small batch shares nothing and has two: in place of the plan every CTA of the second
+// sums up the lengths.  One of few and short contexts has a single launch, of a CTA for each
+// sequence and kv head.
 //
-// What bounds it: long prefixes HBM and the tensor cores (16 sequences of 8 x 8 heads: 0.65
-// us per 1000 shared tokens, 6.3 TB/s; 128 of 4 x 8, two row tiles: 1.26 us per 64 keys of
-// a CTA, 2000 of 2400 cycles in products; with S of 128 keys at a time 1.38); tails HBM
-// (5.4 TB/s); and all of it a fixed part of 15 to 19 us: the plan 4 us, from the beginning
-// of a CTA to its first product 4, from a run's last product to its stores 3, the join 3,
-// what is between the launches 1 to 2.  In a graph of calls, floors by bytes in brackets:
-//   64 sequences behind 2048 tokens 32.4 us [21.8], 50 in 6 groups 27.9 [9.7],
-//   16 on a document of 32,000 39.9 [20.9], 128 behind 8192 50.0 [25.5], 2 short 6.4
+// What bounds it: long prefixes HBM and the tensor cores (of 128 rows, D = 128, 0.74 us per
+// 64 keys of a CTA, 6.7 TB/s over the GPU; of 256 rows 1.29 us, its products with S about
+// 600 of 2470 cycles, those with V 460, for each row tile: one of 128 x 64 takes nearly as
+// long as one of 128 x 128, but with S of 128 keys at a time, which leaves one S buffer to a
+// chain, a step took 1.43); tails HBM; and all of it a fixed part of 15 to 19 us: the plan 4
+// us, from the beginning of a CTA to its first product 4, from a run's last product to its
+// stores 3, the join 3, what is between the launches 1 to 2.  In a graph of calls, floors by
+// bytes in brackets: 64 sequences behind 2048 tokens 32.0 us [21.8], 50 in 6 groups 26.6
+// [9.7], 16 on a document of 32,000 37.8 [20.9], 128 behind 8192 48.7 [25.5], 2 short 3.7.
 #include <math.h>
 
 #include <atomic>
@@ -52,10 +55,18 @@ constexpr int kMaxWarps = kMaxCtas * kWarpsMost;  // parts; a GB300 has 152 SMs)
 constexpr int kThreads = 384;            // of the attention's CTAs
 // A batch of at most so many sequences whose tables have room for no more K and V than
 // kSmallBytes is small: reading it whole takes 2 us or so, and a prefix's pipeline alone 6
-// (two sequences behind 256 tokens: 6.4 us in the two launches, 9.4 planned but not shared,
-// 12.6 shared).
+// (two sequences behind 256 tokens: 6.3 us in two launches, 9.4 planned but not shared, 12.6
+// shared).
 constexpr int64_t kSmallBytes = 16 << 20;
 constexpr int kSmallSeqs = kThreads;
+// One whose tables have room for at most so many tokens a sequence (half as many with eight
+// heads to a kv head), and of so many sequences and kv heads per SM, is done in a single
+// launch (us so and otherwise; 2 x 2 heads of 64 dims, 2 sequences behind 256 tokens 3.2 and
+// 6.3, 1024 5.3 and 6.6, 2048 8.3 and 7.7; 2 x 8 of 128, 8 behind 1024 8.1 and 13.7, 32 behind
+// 1024 15.5 and 16.2, 100 behind 256 21.2 and 16.7; 8 x 8 of 128, 2 behind 512 7.6 and 8.7,
+// behind 1024 11.3 and 10.5).
+constexpr int kShortTokens = 1024;
+constexpr int kShortCtas = 2;
 constexpr int kNearGroups = 32;          // groups whose plans fit a CTA's shared memory
 constexpr int kMaxDynamicSmem = 232448;  // opt-in shared memory per CTA on sm_103 (227 KiB)
 constexpr int BM = 128;                  // rows of a product
@@ -341,9 +352,12 @@ struct WarpSmem {
 // second parts; eight heads need a second product.
 //
 // smem_raw: the warps' rings, then [S + 1] first tiles, [S] first tokens and [S] lengths
-// of the sequences' tails, which are there already.
-template <int D, int G>
-__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, uint8_t *smem_raw) {
+// of the sequences' tails, which are there already.  kOne: there is one sequence, `seq`, of
+// which a CTA's warps share the tiles for kv head `kvh`, and their parts go to `parts` in
+// shared memory, [warps, G] rows of D values of O, then of (max, sum).
+template <int D, int G, bool kOne>
+__device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, uint8_t *smem_raw,
+                                      int seq, int kvh, float *parts) {
   using W = WarpSmem<D, G>;
   constexpr int kRows = W::kRows;
   constexpr int kCols = D / 8;              // 16-byte columns per row
@@ -352,7 +366,8 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = p.tail_warps;
   uint8_t *mine = smem_raw + warp * W::bytes;
-  const int S = p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
+  const int S = kOne ? 1 : p.num_seqs, Hkv = p.num_kv_heads, shift = p.block_shift;
+  const int32_t *tables = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
   int *tile0 = reinterpret_cast<int *>(smem_raw + warps * W::bytes);  // [S + 1]
   int *begin = tile0 + S + 1;                                         // [S]
   int *len = begin + S;                                               // [S]
@@ -361,14 +376,14 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
 
   if (warp >= warps) return;
   const int total = tile0[S];
-  const int per_run = run_tiles(p, sum);
+  const int per_run = kOne ? max((total + warps - 1) / warps, 1) : run_tiles(p, sum);
   const int runs = (total + per_run - 1) / per_run;
-  const int64_t jobs = (int64_t)runs * Hkv;  // (run, head), heads innermost
+  const int64_t jobs = kOne ? runs : (int64_t)runs * Hkv;  // (run, head), heads innermost
   const uint64_t policy = l2_policy_evict_first();
   const int col = lane % kCols, row0 = lane / kCols;
-  for (int64_t job = (int64_t)(blockIdx.x - sum.prefix_ctas) * warps + warp; job < jobs;
-       job += (int64_t)(p.ctas - sum.prefix_ctas) * warps) {
-    const int r = (int)(job / Hkv), j = (int)(job - (int64_t)r * Hkv);
+  for (int64_t job = kOne ? warp : (int64_t)(blockIdx.x - sum.prefix_ctas) * warps + warp; job < jobs;
+       job += kOne ? jobs : (int64_t)(p.ctas - sum.prefix_ctas) * warps) {
+    const int r = kOne ? warp : (int)(job / Hkv), j = kOne ? kvh : (int)(job - (int64_t)r * Hkv);
     const int t_begin = r * per_run, t_end = min(t_begin + per_run, total);
 
     // The loading side: tile in_t of the batch, at token in_tok of sequence in_s (in_L
@@ -379,7 +394,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
     int in_slot = 0, in_q = 0;
     bool in_first = true;  // the sequence's first tile of this run
     auto block_of = [&](int s, int tok) {
-      int blk = p.block_tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
+      int blk = tables[(int64_t)s * p.max_blocks_per_seq + (tok >> shift)];
       if (blk < 0 || blk >= p.num_blocks) {
         if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
         blk = 0;
@@ -400,7 +415,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
     auto issue = [&]() {
       if (in_t < t_end) {
         if (in_first) {
-          const uint16_t *q = p.q + ((int64_t)in_s * Hkv + j) * G * D;
+          const uint16_t *q = p.q + ((int64_t)(seq + in_s) * Hkv + j) * G * D;
           for (int x = lane; x < G * kCols; x += 32)
             copy16(qslots + in_q * W::kQ + tile_at<D>(x / kCols, x % kCols), q + x * 8, true, policy);
           in_q = in_q + 1 == kStages ? 0 : in_q + 1;
@@ -554,8 +569,8 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
           for (int x = 0; x < 4; ++x) o[i][x] += __shfl_xor_sync(0xffffffffu, o[i][x], 2);
       }
       if (owner) {
-        const int64_t part = ((int64_t)(s + r) * Hkv + j) * G + h0;
-        float *po = p.tail_o + part * D;
+        const int64_t part = kOne ? warp * G + h0 : ((int64_t)(s + r) * Hkv + j) * G + h0;
+        float *po = (kOne ? parts : p.tail_o) + part * D;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int d = i * 16 + (lane >> 2);
@@ -567,7 +582,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
           }
         }
         if (lane < 4) {
-          float2 *ml = reinterpret_cast<float2 *>(p.tail_ml) + part;
+          float2 *ml = reinterpret_cast<float2 *>(kOne ? parts + warps * G * D : p.tail_ml) + part;
           ml[0] = make_float2(m0, l0);
           if (G > 1) ml[1] = make_float2(m1, l1);
         }
@@ -1232,7 +1247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) tile0[p.num_seqs] = (int)sum.tiles;
   __syncthreads();
-  tails<D, G>(p, sum, smem_raw);
+  tails<D, G, false>(p, sum, smem_raw, 0, 0, nullptr);
+}
+
+// What the groups say is looked at, but not used, where nothing is shared.
+__device__ __forceinline__ void check_groups(const SharedParams &p) {
+  for (int g = threadIdx.x; g <= p.num_groups; g += blockDim.x) {
+    const int x = p.group_starts[g];
+    if (g < p.num_groups ? (g == 0 && x != 0) || p.group_starts[g + 1] < x : x != p.num_seqs)
+      flag_status(p.status, PKV_DEV_BAD_SEQLEN);
+    if (g < p.num_groups && (p.shared_blocks[g] < 0 || p.shared_blocks[g] > p.max_blocks_per_seq))
+      flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+  }
 }
 
 // The launch of a small batch: every context is a tail, of which each CTA knows by itself
@@ -1249,15 +1275,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_small_kernel(const SharedP
   int *begin = tile0 + S + 1, *len = begin + S;
   const int given = s < S ? p.context_lens[s] : 1;
   const int L = given <= 0 ? 0 : (int)min((int64_t)given, room);
-  if (blockIdx.x == 0) {  // (what the groups say is looked at, but not used)
+  if (blockIdx.x == 0) {
     if (s < S && (L != given || L == 0)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
-    for (int g = threadIdx.x; g <= p.num_groups; g += blockDim.x) {
-      const int x = p.group_starts[g];
-      if (g < p.num_groups ? (g == 0 && x != 0) || p.group_starts[g + 1] < x : x != S)
-        flag_status(p.status, PKV_DEV_BAD_SEQLEN);
-      if (g < p.num_groups && (p.shared_blocks[g] < 0 || p.shared_blocks[g] > p.max_blocks_per_seq))
-        flag_status(p.status, PKV_DEV_BAD_CONTEXT);
-    }
+    check_groups(p);
   }
   int64_t at[1] = {s < S ? tail_tiles(L, D) : 0}, all[1];
   scan_cta<1>(at, all, sums);
@@ -1283,7 +1303,55 @@ __global__ void __launch_bounds__(kThreads, 1) shared_small_kernel(const SharedP
     }
   }
   __syncthreads();
-  tails<D, G>(p, sum, smem_raw);
+  tails<D, G, false>(p, sum, smem_raw, 0, 0, nullptr);
+}
+
+// The launch of a batch whose contexts are short, all of it: a CTA for each sequence and kv
+// head, whose warps share the tiles; their parts are joined in shared memory.
+template <int D, int G>
+__global__ void __launch_bounds__(kWarpsMost * 32, 1) shared_short_kernel(const SharedParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warps = p.tail_warps, seq = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - seq * p.num_kv_heads;
+  const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
+  const int given = p.context_lens[seq];
+  const int L = given <= 0 ? 0 : (int)min((int64_t)given, room);
+  if (kvh == 0 && threadIdx.x == 0 && (L != given || L == 0)) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
+  if (blockIdx.x == 0) check_groups(p);
+  if (L == 0) return;  // (left as it was)
+  uint8_t *behind = smem_raw + warps * WarpSmem<D, G>::bytes;
+  int *one = reinterpret_cast<int *>(behind);  // (see tails)
+  float *parts = reinterpret_cast<float *>(behind + 16);
+  if (threadIdx.x == 0) {
+    one[0] = one[2] = 0;
+    one[1] = tail_tiles(L, D);
+    one[3] = L;
+  }
+  __syncthreads();
+  tails<D, G, true>(p, Totals{}, smem_raw, seq, kvh, parts);
+  __syncthreads();
+  const float2 *ml = reinterpret_cast<const float2 *>(parts + warps * G * D);
+  const int tiles = tail_tiles(L, D), per_run = (tiles + warps - 1) / warps;
+  const int n = (tiles + per_run - 1) / per_run;
+  for (int i = threadIdx.x * 2; i < G * D; i += blockDim.x * 2) {
+    const int row = i / D, d = i % D;
+    float M = -INFINITY;
+    for (int w = 0; w < n; ++w) M = fmaxf(M, ml[w * G + row].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f, a = 0.f, b = 0.f;
+    for (int w = 0; w < n; ++w) {
+      const float2 x = ml[w * G + row];
+      const float2 o = *reinterpret_cast<const float2 *>(parts + (w * G + row) * D + d);
+      const float weight = fast_exp2(x.x - ref);
+      l = fmaf(x.y, weight, l);
+      a = fmaf(o.x, weight, a);
+      b = fmaf(o.y, weight, b);
+    }
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint32_t *>(p.out + (((int64_t)seq * p.num_kv_heads + kvh) * G + row) * D + d) =
+        pack_bf16x2(a * inv, b * inv);
+  }
 }
 
 // ----------------------------------------------------------------------- 4. join
@@ -1502,6 +1570,19 @@ pkv_status launch(SharedParams prm, cudaStream_t stream) {
   const int64_t room = (int64_t)prm.max_blocks_per_seq << prm.block_shift;
   const bool small = S <= kSmallSeqs && S * room * prm.num_kv_heads * (4 * D) <= kSmallBytes &&
                      !prm.share_always;
+  if (room <= (G == 8 ? kShortTokens / 2 : kShortTokens) &&
+      (int64_t)S * prm.num_kv_heads <= kShortCtas * sms && !prm.share_always) {
+    constexpr int each = WarpSmem<D, G>::bytes + G * (D * 4 + 8);  // of a warp, with its part
+    constexpr int fit = (kMaxDynamicSmem - 16) / each;
+    prm.tail_warps = fit < kWarpsMost ? fit : kWarpsMost;
+    prm.ctas = S * prm.num_kv_heads;
+    const int smem = prm.tail_warps * each + 16;
+    if (!kernel_smem_setup((const void *)shared_short_kernel<D, G>, prm.tail_warps * 32, smem, nullptr))
+      return PKV_ERR_CUDA;
+    launch_dependent<SharedParams>(shared_short_kernel<D, G>, (unsigned)prm.ctas, prm.tail_warps * 32, smem,
+                                   stream, prm);
+    return launch_status();
+  }
   const int groups_smem = kNearGroups * (int)sizeof(GroupPlan) + 16;
   const int seq_smem = (3 * S + 1) * 4;
   int warps = (kMaxDynamicSmem - 2048 - seq_smem - groups_smem) / WarpSmem<D, G>::bytes;

@@ -416,13 +416,60 @@ def test_shared_or_not_as_it_pays(lib, groups, G, D):
     Shared(groups, 4 * G, 4, D, 64).check(lib)
 
 
-# Batches whose tables have little room are read whole, with no plan of the groups.
+# Batches whose tables have little room are read whole, with no plan of the groups: with room
+# for up to 1024 tokens (512 at eight heads to a kv head) in a single launch.  wide: columns of
+# the tables that nobody uses.
+SHORT_OR_SMALL = pytest.mark.parametrize("wide", [0, 20])
+
+
+@pytest.mark.by_choice
+@SHORT_OR_SMALL
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (4, 1), (16, 2)])
+def test_a_small_batch(lib, Hq, Hkv, D, wide):
+    Shared([(1, [0, 1, 63]), (2, [5, 70]), (0, [1, 15, 16, 17, 33])], Hq, Hkv, D, wide=wide).check(lib)
+
 
 @pytest.mark.by_choice
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (4, 1), (16, 2)])
-def test_a_small_batch(lib, Hq, Hkv, D):
-    Shared([(1, [0, 1, 63]), (2, [5, 70]), (0, [1, 15, 16, 17, 33])], Hq, Hkv, D).check(lib)
+@pytest.mark.parametrize("G,tokens", [(1, 1024), (4, 1023), (4, 1025), (8, 512), (8, 513), (2, 961), (8, 449)])
+def test_about_as_long_as_a_short_context_can_be(lib, G, tokens, D):
+    """Every warp has tiles, and from one to all but one of them less than the others."""
+    Shared([(3, [tokens - 192, 100, 0]), (0, [tokens, 7])], 2 * G, 2, D).check(lib)
+
+
+@pytest.mark.by_choice
+@pytest.mark.parametrize("n", [304, 305])
+def test_about_as_many_sequences_as_a_short_batch_can_have(lib, n):
+    Shared([(1, [(7 * i) % 150 for i in range(n)])], 2, 1, 64, 64).check(lib)
+
+
+@pytest.mark.by_choice
+def test_a_short_batch_on_streams_and_from_a_graph(lib):
+    s = Shared([(2, [30, 5, 64]), (0, [200])], 8, 2, 128)
+    a = s.args(lib)
+    lib.paged_decode_shared_attn(**a)
+    torch.cuda.synchronize()
+    want = bits(s.out)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(s.out) for _ in streams]
+    spaces = [torch.empty_like(a["workspace"]) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, out, ws in zip(streams, outs, spaces):
+            lib.paged_decode_shared_attn(**{**a, "out": out, "workspace": ws, "stream": st})
+    torch.cuda.synchronize()
+    for out in outs:
+        assert (bits(out) == want).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.paged_decode_shared_attn(**a)
+    s.q.copy_(torch.randn_like(s.q, dtype=torch.float32).to(torch.bfloat16))
+    s.ctx = [L - 1 for L in s.ctx]
+    a["context_lens"].copy_(torch.tensor(s.ctx, dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    s.compare()
 
 
 @pytest.mark.by_choice
@@ -433,29 +480,35 @@ def test_the_most_sequences_of_a_small_batch(lib):
 
 
 @pytest.mark.by_choice
-def test_a_small_batch_with_empty_and_clamped_contexts(lib):
-    s = Shared([(2, [None, 5, 64]), (0, [None, 64, None])], 4, 2, 64)
-    s.check(lib, status=lib.DEV_BAD_CONTEXT)
-    s = Shared([(2, [64, 64, 10])], 4, 2, 64, 64)
+@SHORT_OR_SMALL
+def test_a_small_batch_with_empty_contexts(lib, wide):
+    Shared([(2, [None, 5, 64]), (0, [None, 64, None])], 4, 2, 64, wide=wide).check(lib, status=lib.DEV_BAD_CONTEXT)
+    Shared([(0, [None, None])], 4, 2, 64, wide=wide).check(lib, status=lib.DEV_BAD_CONTEXT)
+
+
+@pytest.mark.by_choice
+@pytest.mark.parametrize("blocks", [2, 20])
+def test_a_small_batch_with_clamped_contexts(lib, blocks):
+    s = Shared([(blocks, [64, 64, 10])], 4, 2, 64, 64)
     s.ctx[1] = 10**6
-    s.check(lib, status=lib.DEV_BAD_CONTEXT)
-    s = Shared([(0, [None, None])], 4, 2, 64)
     s.check(lib, status=lib.DEV_BAD_CONTEXT)
 
 
 @pytest.mark.by_choice
 @pytest.mark.parametrize("starts,shared", [([1, 2, 5], [3, 2]), ([0, 2, 4], [3, 2]), ([0, 6, 5], [3, 2]), ([0, -3, 5], [3, 2]), ([0, 2, 5], [-1, 2]),
                                            ([0, 2, 5], [3, 1000])])
-def test_a_small_batch_with_bad_groups(lib, starts, shared):
-    s = Shared([(3, [4, 70]), (2, [5, 9, 30])], 4, 2, 64)
+@SHORT_OR_SMALL
+def test_a_small_batch_with_bad_groups(lib, starts, shared, wide):
+    s = Shared([(3, [4, 70]), (2, [5, 9, 30])], 4, 2, 64, wide=wide)
     flag = lib.DEV_BAD_SEQLEN if starts != s.starts else lib.DEV_BAD_CONTEXT
     s.starts, s.shared = starts, shared
     s.check(lib, status=flag)
 
 
 @pytest.mark.by_choice
-def test_a_small_batch_with_block_ids_out_of_range(lib):
-    s = Shared([(2, [4, 70]), (2, [5, 9]), (0, [30])], 4, 2, 64, poison=False)
+@SHORT_OR_SMALL
+def test_a_small_batch_with_block_ids_out_of_range(lib, wide):
+    s = Shared([(2, [4, 70]), (2, [5, 9]), (0, [30])], 4, 2, 64, poison=False, wide=wide)
     s.tables[0, 1] = s.kc.shape[0]
     s.tables[3, 2] = -1
     lib.paged_decode_shared_attn(**s.args(lib))
@@ -465,9 +518,10 @@ def test_a_small_batch_with_block_ids_out_of_range(lib):
 
 
 @pytest.mark.by_choice
-def test_small_and_large_batches_in_turn(lib):
+@SHORT_OR_SMALL
+def test_small_and_large_batches_in_turn(lib, wide):
     """On one stream and workspace, none waited for on the host; then from a graph."""
-    few = Shared([(1, [5, 9]), (0, [100, 3])], 8, 2, 128)
+    few = Shared([(1, [5, 9]), (0, [100, 3])], 8, 2, 128, wide=wide)
     many = Shared([(200, [(31 * i) % 200 for i in range(2)]), (0, [700, 1])], 8, 2, 128)
     a, b = few.args(lib), many.args(lib)
     assert a["workspace"].numel() == b["workspace"].numel()
