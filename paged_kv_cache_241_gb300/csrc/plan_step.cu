@@ -20,7 +20,7 @@
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
 // the lengths, one of blocks from the stack or a table, and the barriers between them: 4.1
-// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 8.5).
+// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 7.1).
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
@@ -241,16 +241,20 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
       row += q.n;
     }
   }
-  // Blocks taken: those up to the last sequence that takes any.
-  int64_t most = taken;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int64_t y = __shfl_xor_sync(0xffffffffu, most, o);
-    most = y > most ? y : most;
-  }
-  if (lane == 0) sums3[warp][0] = most;
   if (tid == 0) first_row[S] = saturated(total[2]);
-  scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
+  if (p.part == kRows) {
+    __syncthreads();
+  } else {
+    // Blocks taken: those up to the last sequence that takes any.
+    int64_t most = taken;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int64_t y = __shfl_xor_sync(0xffffffffu, most, o);
+      most = y > most ? y : most;
+    }
+    if (lane == 0) sums3[warp][0] = most;
+    scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
+  }
   // (nobody reads lengths or counters any more)
   if (ctas > 1 && p.part != kRows) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
@@ -438,7 +442,10 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   if (!small && num_rows > 0) {
     const int sms = device_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
-    const int64_t ctas = (num_rows + threads - 1) / threads;
+    // A row a thread on up to half of the SMs, else four (115 thousand rows 7.0 us with one
+    // and 6.0 with four, which leave SMs to the launch behind; 1000 6.8 and 7.0).
+    int64_t ctas = (num_rows + threads - 1) / threads;
+    if (ctas > sms / 2) ctas = (num_rows + 4 * threads - 1) / (4 * threads);
     cfg.gridDim = dim3((unsigned)(ctas < sms ? ctas : sms));
     cfg.blockDim = dim3(threads);
     cfg.numAttrs = 1;  // (no cluster)
