@@ -106,13 +106,29 @@ struct SeqPlan {
   int tile0;  // tiles of the tails before it
   int begin;  // its first token
   int len;    // tokens of the sequence (0: no output)
-  int group;
+  int pad;
 };
 
+// What the join needs of a sequence, in the workspace.
+struct JoinPlan {
+  int row0;      // the sequence's number and its tail's first run (tail_ml, tail_o)
+  int tails;     // parts of its tail
+  int place;     // of the sequence in its group
+  int members;   // GroupPlan of its group
+  int tiles;     // (0, too, where the sequence has no tokens)
+  int pad;
+  int64_t cost0;
+  int64_t run_cost;  // Totals
+  int64_t pad2;
+};
+static_assert(sizeof(JoinPlan) == 48, "three loads");
+
 struct Totals {
-  int64_t cost;     // of all prefixes
-  int64_t tiles;    // of all tails
-  int prefix_ctas;  // CTAs that take the prefixes; the others take the tails
+  int64_t cost;      // of all prefixes
+  int64_t run_cost;  // of a run of them
+  int tiles;         // of all tails
+  int run_tiles;     // of a run of them
+  int prefix_ctas;   // CTAs that take the prefixes; the others take the tails
   int pad;
 };
 
@@ -128,6 +144,7 @@ struct SharedParams {
   Totals *totals;
   GroupPlan *groups;   // [num_groups]
   SeqPlan *seqs;       // [num_seqs]
+  JoinPlan *joins;     // [num_seqs]
   float *tail_ml;      // [num_seqs + runs, Hkv, G, 2]   (max in log2 units, sum)
   float *tail_o;       // [num_seqs + runs, Hkv, G, D]
   float *first_ml;     // [num_seqs, Hq, 2]: a unit's first part
@@ -165,16 +182,29 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // Tiles per run of the tails; run r's part of sequence s is filed under s + r (a part
-// begins where a sequence or a run does, so no two have the same number).
-__device__ __forceinline__ int run_tiles(const SharedParams &p, const Totals &t) {
+// begins where a sequence or a run does, so no two have the same number).  Cost per run of
+// the prefixes (at least that of the dearest step, so that every run between a unit's first
+// and last has a step of it).
+__device__ __forceinline__ void cut_runs(const SharedParams &p, Totals &t) {
   const int runs = max((p.ctas - t.prefix_ctas) * p.tail_warps / p.num_kv_heads, 1);
-  return max((int)quotient(t.tiles + runs - 1, runs), 1);
-}
-// Cost per run of the prefixes (at least that of the dearest step, so that every run
-// between a unit's first and last has a step of it).
-__device__ __forceinline__ int64_t run_cost(const Totals &t) {
+  t.run_tiles = max((t.tiles + runs - 1) / runs, 1);
   const int n = max(t.prefix_ctas, 1);
-  return max(quotient(t.cost + n - 1, n), (int64_t)kPairCost);
+  t.run_cost = max(quotient(t.cost + n - 1, n), (int64_t)kPairCost);
+}
+__device__ __forceinline__ JoinPlan join_plan(const Totals &t, int s, int tile0, int tiles, int place,
+                                              const GroupPlan &g, bool live) {
+  JoinPlan x;
+  const int r0 = tile0 / t.run_tiles;
+  x.row0 = s + r0;
+  x.tails = tiles > 0 ? (tile0 + tiles - 1) / t.run_tiles - r0 + 1 : 0;
+  x.place = place;
+  x.members = g.members;
+  x.tiles = live ? g.tiles : 0;
+  x.cost0 = g.cost0;
+  x.run_cost = t.run_cost;
+  x.pad = 0;
+  x.pad2 = 0;
+  return x;
 }
 
 // ----------------------------------------------------------------------- 1. plan
@@ -217,6 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   int *eff = starts + N + 1;     // [N]: blocks that the group shares
   int *lead = eff + N;           // [N]: its first sequence with tokens
   int *count = lead + N;         // [N]: its sequences with tokens
+  int64_t *cost0 = reinterpret_cast<int64_t *>(plan_smem + ((4 * N + 2) & ~1));  // [N]
   const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
   auto tokens = [&](int L) { return L <= 0 ? 0 : (int)min((int64_t)L, room); };
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -246,7 +277,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       const int L = s < S ? tokens(s == tid ? first_L : p.context_lens[s]) : 0;
       const int g = s < S ? seq_of(starts, N, s) : -1;
       // (a warp's sequences are neighbours: mostly one group)
-      const unsigned peers = __match_any_sync(0xffffffffu, L > 0 ? g : -1 - (tid & 31));
+      const unsigned peers = __match_any_sync(0xffffffffu, L > 0 ? g : -1);
       if (L > 0) {
         const int least = __reduce_min_sync(peers, L >> p.block_shift);
         if ((tid & 31) == __ffs(peers) - 1) {
@@ -309,24 +340,31 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     tiles = (int)sum[1];
     my_cost = my_b = my_g = 0;
   }
-  if (tid == 0) {
-    p.totals->cost = cost;
-    p.totals->tiles = tiles;
-    p.totals->prefix_ctas = split_ctas(p, (float)cost, (float)tiles);
-  }
+  Totals t;
+  t.cost = cost;
+  t.tiles = tiles;
+  t.prefix_ctas = split_ctas(p, (float)cost, (float)tiles);
+  t.pad = 0;
+  cut_runs(p, t);
+  if (tid == 0) *p.totals = t;
   for (int g = g0; g < g1; ++g) {
     GroupPlan x = plan(g);
-    x.cost0 = at[0];
+    x.cost0 = cost0[g] = at[0];
     p.groups[g] = x;
     at[0] += per_g == 1 ? my_cost : cost_of(x);
   }
+  __syncthreads();
   for (int s = s0; s < s1; ++s) {
     if (per > 1) {
       my_L = tokens(p.context_lens[s]);
       my_b = first(s, my_L, my_g);
     }
-    *reinterpret_cast<int4 *>(p.seqs + s) = make_int4(tile, my_b, my_L, my_g);
-    tile += tail_tiles(my_L - my_b, p.head_dim);
+    *reinterpret_cast<int4 *>(p.seqs + s) = make_int4(tile, my_b, my_L, 0);
+    const int mine = tail_tiles(my_L - my_b, p.head_dim);
+    GroupPlan x = plan(my_g);
+    x.cost0 = cost0[my_g];
+    p.joins[s] = join_plan(t, s, tile, mine, s - x.start, x, my_L > 0);
+    tile += mine;
   }
 }
 
@@ -376,7 +414,7 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
 
   if (warp >= warps) return;
   const int total = tile0[S];
-  const int per_run = kOne ? max((total + warps - 1) / warps, 1) : run_tiles(p, sum);
+  const int per_run = kOne ? max((total + warps - 1) / warps, 1) : sum.run_tiles;
   const int runs = (total + per_run - 1) / per_run;
   const int64_t jobs = kOne ? runs : (int64_t)runs * Hkv;  // (run, head), heads innermost
   const uint64_t policy = l2_policy_evict_first();
@@ -709,37 +747,24 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
   float2 *ex = reinterpret_cast<float2 *>(smem + L::ex);
 
   const int warp = warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int64_t len = run_cost(sum);
+  const int64_t len = sum.run_cost;
   const int64_t x0 = (int64_t)blockIdx.x * len;
   if (x0 >= sum.cost) return;
   const int64_t x1 = x0 + len < sum.cost ? x0 + len : sum.cost;
 
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&p_free[i], 1);
-    }
-    mbar_init(&o_free[0], 8);  // every softmax warp, or a chain's own four twice
-    mbar_init(&o_free[1], 8);
-    for (int i = 0; i < kUnitSlots; ++i) {
-      mbar_init(&unit_full[i], 1);
-      mbar_init(&unit_empty[i], 1 + 2 + 8);  // V loader, issuers, softmax warps
-    }
-    mbar_init(ex_full, 8);
-    mbar_init(drain, 2);
-    *abort_flag = 0;
+  if (threadIdx.x < L::kNumBars) {  // a thread each
+    uint64_t *bar = bars + threadIdx.x;
+    int count = 1;
+    if (bar >= p_full && bar < p_free) count = 128;
+    if (bar >= o_free && bar < unit_full) count = 8;  // every softmax warp, or a chain's own four twice
+    if (bar >= unit_empty && bar < ex_full) count = 1 + 2 + 8;  // V loader, issuers, softmax warps
+    if (bar == ex_full) count = 8;
+    if (bar == drain) count = 2;
+    mbar_init(bar, count);
     fence_barrier_init();
+  }
+  if (threadIdx.x == kThreads - 1) {
+    *abort_flag = 0;
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_k);
   }
@@ -1231,7 +1256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   Totals sum;
   sum.cost = __ldcg(&p.totals->cost);
+  sum.run_cost = __ldcg(&p.totals->run_cost);
   sum.tiles = __ldcg(&p.totals->tiles);
+  sum.run_tiles = __ldcg(&p.totals->run_tiles);
   sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
   if ((int)blockIdx.x < sum.prefix_ctas) {
     prefixes<D>(tm_q, tm_k, p, sum, groups, smem_raw);
@@ -1245,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin[s] = x.y;
     len[s] = x.z;
   }
-  if (threadIdx.x == 0) tile0[p.num_seqs] = (int)sum.tiles;
+  if (threadIdx.x == 0) tile0[p.num_seqs] = sum.tiles;
   __syncthreads();
   tails<D, G, false>(p, sum, smem_raw, 0, 0, nullptr);
 }
@@ -1281,27 +1308,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_small_kernel(const SharedP
   }
   int64_t at[1] = {s < S ? tail_tiles(L, D) : 0}, all[1];
   scan_cta<1>(at, all, sums);
+  Totals sum;
+  sum.cost = 0;
+  sum.tiles = (int)all[0];
+  sum.prefix_ctas = 0;
+  cut_runs(p, sum);
   if (s < S) {
     tile0[s] = (int)at[0];
     begin[s] = 0;
     len[s] = L;
-    if (blockIdx.x == 0)  // (for the join)
-      *reinterpret_cast<int4 *>(p.seqs + s) = make_int4((int)at[0], 0, L, 0);
+    if (blockIdx.x == 0)
+      p.joins[s] = join_plan(sum, s, (int)at[0], tail_tiles(L, D), 0, GroupPlan{}, true);
   }
-  Totals sum;
-  sum.cost = 0;
-  sum.tiles = all[0];
-  sum.prefix_ctas = 0;
-  sum.pad = 0;
-  if (s == 0) {
-    tile0[S] = (int)all[0];
-    if (blockIdx.x == 0) {
-      *p.totals = sum;
-      const int4 none = make_int4(0, 0, 0, 0);
-      reinterpret_cast<int4 *>(p.groups)[0] = none;
-      reinterpret_cast<int4 *>(p.groups)[1] = none;
-    }
-  }
+  if (s == 0) tile0[S] = (int)all[0];
   __syncthreads();
   tails<D, G, false>(p, sum, smem_raw, 0, 0, nullptr);
 }
@@ -1373,44 +1392,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Shar
   // (Planned by a launch of its own, the plan is there: the launch before began after it,
   // and this one after that.)
   if (p.small) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 seq = __ldcg(reinterpret_cast<const int4 *>(p.seqs + s));
-  Totals sum;
-  sum.cost = __ldcg(&p.totals->cost);
-  sum.tiles = __ldcg(&p.totals->tiles);
-  sum.prefix_ctas = __ldcg(&p.totals->prefix_ctas);
-  GroupPlan gp;
-  {
-    const int4 *src = reinterpret_cast<const int4 *>(p.groups + seq.w);
-    const int4 a = __ldcg(src), b = __ldcg(src + 1);
-    gp.cost0 = (int64_t)(uint32_t)a.x | ((int64_t)a.y << 32);
-    gp.start = a.z;
-    gp.members = b.x;
-    gp.tiles = b.y;
-  }
+  const int4 *plan = reinterpret_cast<const int4 *>(p.joins + s);
+  const int4 a = __ldcg(plan), b = __ldcg(plan + 1), c = __ldcg(plan + 2);
   // The parts of the tail: of runs r0, r0 + 1, ...
-  const int t0 = seq.x, tiles = (seq.z - seq.y + tail_rows(D) - 1) / tail_rows(D);
-  int n_tail = 0;
-  int64_t tail_row = 0;
-  if (tiles > 0) {
-    const int per_run = run_tiles(p, sum);
-    const int r0 = t0 / per_run;
-    n_tail = (t0 + tiles - 1) / per_run - r0 + 1;
-    tail_row = ((int64_t)(s + r0) * Hkv + j) * G + g;
-  }
+  const int n_tail = a.y;
+  const int64_t tail_row = ((int64_t)a.x * Hkv + j) * G + g;
   // Those of the prefix: of the unit that has the row, its first step's and of the runs
   // behind that one.
   int n_pre = 0;
   int64_t run_row = 0;
-  if (gp.tiles > 0) {
-    const int64_t len = run_cost(sum);
-    const int idx = (s - gp.start) * G + g, pair = idx / kPairRows;
+  if (b.x > 0) {
+    GroupPlan gp = {};
+    gp.members = a.w;
+    gp.tiles = b.x;
+    gp.cost0 = (int64_t)(uint32_t)b.z | ((int64_t)b.w << 32);
+    const int64_t len = (int64_t)(uint32_t)c.x | ((int64_t)c.y << 32);
+    const int idx = a.z * G + g, pair = idx / kPairRows;
     const int64_t step0 = gp.cost0 + j * head_cost(gp, G) + pair * full_unit_cost(gp) + kUnitCost;
     const int each = step_cost(gp.members * G - pair * kPairRows);
     const int64_t c0 = quotient(step0, len);
     run_row = c0 * kPairRows + idx % kPairRows;
     n_pre = (int)(quotient(step0 + (int64_t)(gp.tiles - 1) * each, len) - c0 + 1);
   }
-  const int n = row < rows && seq.z > 0 ? n_tail + n_pre : 0;
+  const int n = row < rows ? n_tail + n_pre : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // A warp's parts: 32 of their maxima at a time, a lane each.
   float m = -INFINITY, l = 0.f;
@@ -1516,13 +1520,14 @@ std::atomic<int> g_share_always{0};
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Workspace {
-  size_t totals, groups, seqs, tail_ml, tail_o, first_ml, first_o, run_ml, run_o, total;
+  size_t totals, groups, seqs, joins, tail_ml, tail_o, first_ml, first_o, run_ml, run_o, total;
   Workspace(int64_t S, int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
     const int64_t parts = S * Hq + (kMaxWarps + Hkv) * (Hq / Hkv);  // (num_seqs + runs) of each head
     totals = 0;
     groups = 256;
     seqs = groups + align256((size_t)N * sizeof(GroupPlan));
-    tail_ml = seqs + align256((size_t)S * sizeof(SeqPlan));
+    joins = seqs + align256((size_t)S * sizeof(SeqPlan));
+    tail_ml = joins + align256((size_t)S * sizeof(JoinPlan));
     tail_o = tail_ml + align256((size_t)parts * 8);
     first_ml = tail_o + align256((size_t)(parts * D) * 4);
     first_o = first_ml + align256((size_t)(S * Hq) * 8);
@@ -1595,7 +1600,7 @@ pkv_status launch(SharedParams prm, cudaStream_t stream) {
   prm.small = small;
   prm.groups_at = (smem + 15) & ~15;
   if (!small) smem += groups_smem;
-  const int plan_smem = (4 * prm.num_groups + 1) * 4;
+  const int plan_smem = ((4 * prm.num_groups + 2) & ~1) * 4 + prm.num_groups * 8;
   if (small ? !kernel_smem_setup((const void *)shared_small_kernel<D, G>, kThreads, smem, nullptr)
             : !kernel_smem_setup((const void *)shared_plan_kernel, kPlanThreads, plan_smem, nullptr) ||
                   !kernel_smem_setup((const void *)shared_attn_kernel<D, G>, kThreads, smem, nullptr))
@@ -1701,6 +1706,7 @@ extern "C" pkv_status pkv_paged_decode_shared_attn(
   prm.totals = reinterpret_cast<Totals *>(ws + lay.totals);
   prm.groups = reinterpret_cast<GroupPlan *>(ws + lay.groups);
   prm.seqs = reinterpret_cast<SeqPlan *>(ws + lay.seqs);
+  prm.joins = reinterpret_cast<JoinPlan *>(ws + lay.joins);
   prm.tail_ml = reinterpret_cast<float *>(ws + lay.tail_ml);
   prm.tail_o = reinterpret_cast<float *>(ws + lay.tail_o);
   prm.first_ml = reinterpret_cast<float *>(ws + lay.first_ml);
