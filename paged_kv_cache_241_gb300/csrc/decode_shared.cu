@@ -28,11 +28,11 @@
 // 64 keys of a CTA, 6.7 TB/s over the GPU; of 256 rows 1.29 us, its products with S about
 // 600 of 2470 cycles, those with V 460, for each row tile: one of 128 x 64 takes nearly as
 // long as one of 128 x 128, but with S of 128 keys at a time, which leaves one S buffer to a
-// chain, a step took 1.43); tails HBM; and all of it a fixed part of 15 to 19 us: the plan 4
-// us, from the beginning of a CTA to its first product 4, from a run's last product to its
-// stores 3, the join 3, what is between the launches 1 to 2.  In a graph of calls, floors by
-// bytes in brackets: 64 sequences behind 2048 tokens 32.0 us [21.8], 50 in 6 groups 26.6
-// [9.7], 16 on a document of 32,000 37.8 [20.9], 128 behind 8192 48.7 [25.5], 2 short 3.7.
+// chain, a step took 1.43); tails HBM; and all of it a fixed part of 15 to 18 us: the plan 3
+// us, from the beginning of a CTA to its first product 4.5, from a run's last product to its
+// stores 2.5, the join 2.5, what is between the launches 3.  In a graph of calls, floors by
+// bytes in brackets: 64 sequences behind 2048 tokens 31.6 us [21.8], 50 in 6 groups 26.6
+// [9.7], 16 on a document of 32,000 37.0 [20.9], 128 behind 8192 48.9 [25.5], 2 short 3.7.
 #include <math.h>
 
 #include <atomic>
