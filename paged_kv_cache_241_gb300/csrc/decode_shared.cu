@@ -31,8 +31,8 @@
 // chain, a step took 1.43); tails HBM; and all of it a fixed part of 15 to 18 us: the plan 3
 // us, from the beginning of a CTA to its first product 4.5, from a run's last product to its
 // stores 2.5, the join 2.5, what is between the launches 3.  In a graph of calls, floors by
-// bytes in brackets: 64 sequences behind 2048 tokens 31.6 us [21.8], 50 in 6 groups 26.6
-// [9.7], 16 on a document of 32,000 37.0 [20.9], 128 behind 8192 48.9 [25.5], 2 short 3.7.
+// bytes in brackets: 64 sequences behind 2048 tokens 31.6 us [21.8], 50 in 6 groups 26.1
+// [9.7], 16 on a document of 32,000 37.4 [20.9], 128 behind 8192 48.9 [25.5], 2 short 3.7.
 #include <math.h>
 
 #include <atomic>
@@ -89,7 +89,7 @@ struct GroupPlan {
 // with a single row tile 3 (its loads).  A unit's beginning costs kUnitCost ahead of its
 // steps (a run that goes through the end of one into the next drains its pipeline there);
 // a kv head's units follow one another.
-constexpr int kUnitCost = 20;
+constexpr int kUnitCost = 15;
 constexpr int kPairCost = 5, kSingleCost = 3;
 __device__ __forceinline__ int step_cost(int rows) { return rows > BM ? kPairCost : kSingleCost; }
 __device__ __forceinline__ int64_t full_unit_cost(const GroupPlan &g) {  // of 256 rows
