@@ -32,6 +32,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
@@ -117,8 +118,10 @@ class PkvError(RuntimeError):
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libpkv.so (once).  Raises if it has not been built."""
-    global _lib, _call
+    """Load libpkv.so (once).  Raises if it has not been built.  It needs no torch; where
+    torch is in use already the binding's C++ part is bound with it, and where that cannot be
+    the calls that need it say so."""
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -130,25 +133,34 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _call = _load_call(lib)
     _lib = lib
+    if "torch" in sys.modules:
+        try:
+            _load_call()
+        except RuntimeError:
+            pass
     return lib
 
 
-def _load_call(lib):
-    """The C++ part of the binding: the checks and calls of the operators that are called
-    once a step or a layer and are shorter than their checks in Python."""
-    import torch
-
+def _load_call() -> None:
+    """Bind the C++ part of the binding: the checks and calls of the operators that are called
+    once a step or a layer and are shorter than their checks in Python.  Raises if it has not
+    been built for this interpreter and torch."""
+    global _call
+    lib = load()
+    if _call is not None:
+        return
     address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "pkv_plan_step", "pkv_norm_rope_store", "pkv_paged_decode_shared_attn")]
     try:
+        import torch
+
         from . import _pkv_call as call
         call.bind(torch.__version__, *address)
     except ImportError as e:
         raise RuntimeError("the binding's C++ part is missing, or for another interpreter or "
                            "torch: build it with `python -m paged_kv_cache_241_gb300.build`") from e
-    return call
+    _call = call
 
 
 def _check(status: int, what: str) -> None:
@@ -598,7 +610,7 @@ def plan_step(new_lens, context_lens, block_tables, free_blocks, num_free, new_c
     new_num_free [1]; slot_mapping, positions [rows]; cu_seqlens_q, cu_seqlens_k [S + 1].
     new_context_lens may be context_lens, and new_num_free num_free."""
     if _call is None:
-        load()
+        _load_call()
     st = _call.plan_step(
         _raw(stream), new_lens, context_lens, block_tables, free_blocks, num_free,
         new_context_lens, new_num_free, slot_mapping, positions, cu_seqlens_q, cu_seqlens_k,
@@ -658,7 +670,7 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
     the caches, in one pass.  q, k and v may be strided by token (parts of one
     projection).  Without caches k goes to k_out [T, Hkv, D] alone.  bf16."""
     if _call is None:
-        load()
+        _load_call()
     st = _call.norm_rope_store(
         _raw(stream), q_out, q, k, v, positions, turns, k_cache, v_cache, slot_mapping, k_out,
         q_weight, k_weight, eps, interleaved, amplitude, dev_status)
@@ -705,7 +717,7 @@ def paged_decode_shared_attn(out, q, k_cache, v_cache, block_tables, context_len
     shared_blocks[g] (int32 [groups]) blocks of its sequences are the same ones, read
     once (see include/pkv.h; BlockManager.prefix_groups finds groups)."""
     if _call is None:
-        load()
+        _load_call()
     st = _call.paged_decode_shared_attn(
         _raw(stream), out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
         shared_blocks, scale, workspace, dev_status)
