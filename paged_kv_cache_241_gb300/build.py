@@ -63,9 +63,6 @@ def _build_call_module() -> None:
 
     src, out = os.path.join(CSRC, "pycall.cc"), call_module()
     home = os.path.dirname(torch.__file__)
-    inputs = [src, os.path.join(INCLUDE, "pkv.h"), os.path.join(home, "version.py")]
-    if os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, inputs)):
-        return
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         raise RuntimeError("no C++ compiler for the Python binding")
@@ -76,9 +73,21 @@ def _build_call_module() -> None:
            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-isystem", os.path.join(home, "include"), "-isystem", cuda, src, "-o", out,
            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    # Beside the objects, the command that made the module: with another torch, interpreter or
+    # toolkit it is another one, whatever their files' times say.
+    made_by = os.path.join(OBJ_DIR, os.path.basename(out) + ".txt")
+    inputs = [src, os.path.join(INCLUDE, "pkv.h"), os.path.join(home, "version.py")]
+    if os.path.exists(out) and os.path.exists(made_by):
+        with open(made_by) as f:
+            same = f.read() == repr(cmd)
+        if same and os.path.getmtime(out) >= max(map(os.path.getmtime, inputs)):
+            return
+        os.remove(made_by)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(made_by, "w") as f:
+        f.write(repr(cmd))
 
 
 def build(verbose_ptxas: bool = False) -> str:
