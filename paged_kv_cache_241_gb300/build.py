@@ -4,8 +4,8 @@
 
 Compiles every csrc/*.cu (and the host-only *.cpp) in parallel with nvcc and
 links libpkv.so next to this file; beside it the C++ part of the Python binding
-(csrc/pycall.cc), for the interpreter and the torch that run this.  No CMake; a rebuild only
-recompiles sources newer than their object.
+(csrc/pycall.cc), for the interpreter and the torch that run this (left out where torch is
+missing or without CUDA).  No CMake; a rebuild only recompiles sources newer than their object.
 """
 from __future__ import annotations
 
@@ -59,8 +59,15 @@ def call_module() -> str:
 
 
 def _build_call_module() -> None:
-    import torch
-
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    if torch is None or torch.version.cuda is None:
+        # (the rest of the library needs neither)
+        sys.stderr.write("the binding's C++ part is left out: "
+                         + ("no torch\n" if torch is None else "this torch has no CUDA\n"))
+        return
     src, out = os.path.join(CSRC, "pycall.cc"), call_module()
     home = os.path.dirname(torch.__file__)
     cxx = shutil.which("g++") or shutil.which("c++")
@@ -97,13 +104,13 @@ def build(verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
         call = ex.submit(_build_call_module)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        call.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    call.result()  # (its error, with the library in place)
     return LIB
 
 

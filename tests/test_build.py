@@ -1,6 +1,7 @@
 """When the build makes the binding's C++ part anew (the compiler is a stand-in that writes the
 file; no GPU needed)."""
 import os
+import sys
 import types
 
 import pytest
@@ -71,3 +72,40 @@ def test_a_compilation_that_fails_is_tried_again(compiler, monkeypatch):
     monkeypatch.setattr(torch, "__version__", version)
     compiler.code = 0
     assert made(compiler) == 1 and made(compiler) == 0
+
+
+@pytest.fixture
+def library(monkeypatch, tmp_path):
+    """The whole build with a stand-in for every compiler, in a folder of its own."""
+    def run(cmd, **kw):
+        assert "pycall.cc" not in " ".join(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").write("made")
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    for name, to in (("HERE", ""), ("OBJ_DIR", "objects"), ("LIB", "libpkv.so")):
+        monkeypatch.setattr(build, name, str(tmp_path / to))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return tmp_path / "libpkv.so"
+
+
+def test_the_library_is_built_without_torch(library, monkeypatch, capsys):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert build.build() == str(library) and library.exists()
+    assert "torch" in capsys.readouterr().err
+
+
+def test_the_library_is_built_with_a_torch_that_has_no_cuda(library, monkeypatch, capsys):
+    monkeypatch.setattr(torch.version, "cuda", None)
+    assert build.build() == str(library) and library.exists()
+    assert "CUDA" in capsys.readouterr().err
+
+
+def test_the_library_is_built_where_the_module_cannot_be(library, monkeypatch):
+    """Its error is told of behind the library's link."""
+    def no_module():
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(build, "_build_call_module", no_module)
+    with pytest.raises(RuntimeError, match="g.. failed"):
+        build.build()
+    assert library.exists()
