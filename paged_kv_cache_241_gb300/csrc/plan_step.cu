@@ -20,7 +20,7 @@
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
 // the lengths, one of blocks from the stack or a table, and the barriers between them: 4.1
-// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 7.1).
+// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 7.0).
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
@@ -43,7 +43,7 @@ constexpr int kPlanSmallSeqs = 256;
 // faster by 1024 (4000 of them: 15.3 and 13.8).
 constexpr int kPlanThreads = 512, kPlanManyThreads = 1024, kPlanManySeqs = 2048;
 
-enum { kAll, kRows, kState };
+enum { kAll, kRows, kState };  // what a launch does: all of it, or in two launches a part each
 
 struct PlanParams {
   const int32_t *new_lens;
@@ -65,12 +65,19 @@ struct PlanParams {
   int num_seqs;
   int max_blocks_per_seq;
   int block_shift;
-  int part;          // kAll, or in two launches kRows and kState
   int rows_16b;      // slots and positions are 16-byte aligned
 };
 
 __device__ __forceinline__ int saturated(int64_t x) {
   return x > 0x7FFFFFFF ? 0x7FFFFFFF : (int)x;
+}
+
+// A value of the lengths, tables or stack.  The launch beside the rows' reads them without a
+// wait of its own (they are in memory: every CTA of the rows' launch has waited for what wrote
+// them): past the SM's L1, which may hold them as they were before.
+template <int kPart>
+__device__ __forceinline__ int load(const int32_t *x) {
+  return kPart == kState ? __ldcg(x) : *x;
 }
 
 // A sequence's lengths, checked.
@@ -81,11 +88,9 @@ struct PlanSeq {
   bool ends, out;  // out: its lengths do not fit, it takes no part but for its rows
 };
 
-__device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s, bool tell) {
+__device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int L, int n, int borrowed, bool tell) {
   PlanSeq q;
   const int64_t room = (int64_t)p.max_blocks_per_seq << p.block_shift;
-  const int L = p.context_lens[s], n = p.new_lens[s];
-  int borrowed = p.borrowed != nullptr ? p.borrowed[s] : 0;
   int bad = 0;
   q.out = L < 0 || L > room;
   q.L = q.out ? 0 : L;
@@ -178,8 +183,9 @@ __device__ __forceinline__ void write_rows(const PlanParams &p, const int *first
   }
 }
 
+template <int kPart>
 __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanParams p) {
-    extern __shared__ int plan_smem[];
+  extern __shared__ int plan_smem[];
   __shared__ int64_t sums3[32][3];
   __shared__ int64_t sums1[32][1];
   const int S = p.num_seqs, shift = p.block_shift, bs1 = (1 << shift) - 1;
@@ -191,15 +197,15 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
   uint16_t *ending = reinterpret_cast<uint16_t *>(base + S);  // [those that end]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (the rows' grid, else one cluster)
-  const bool tells = p.part != kRows && rank == 0;
+  const bool tells = kPart != kRows && rank == 0;
 
   // (The launch behind the rows' began after all of that one's CTAs had waited for what came
   // before them both.)
-  if (p.part != kState) {
+  if (kPart != kState) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  const int free_given = *p.num_free;
+  const int free_given = load<kPart>(p.num_free);
   const int per = (S + blockDim.x - 1) / (int)blockDim.x;
   const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
   // Blocks given (2^38 at most) and, above them, sequences that end; need; rows.
@@ -207,8 +213,19 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
   constexpr int64_t kGive = ((int64_t)1 << kEnds) - 1;
   int64_t at[3] = {0, 0, 0}, total[3];
   PlanSeq mine = {};                    // (the thread's last: its only one, mostly)
+  auto lengths_of = [&](int s, bool tell) {
+    const int L = load<kPart>(p.context_lens + s), n = load<kPart>(p.new_lens + s);
+    return plan_seq(p, L, n, p.borrowed != nullptr ? load<kPart>(p.borrowed + s) : 0, tell);
+  };
   for (int s = s0; s < s1; ++s) {
-    mine = plan_seq(p, s, tells);
+    if (kPart == kState && per > 1) {  // (the thread's second look, too: 1000 rows 7.1 -> 6.9 us)
+      held[s] = load<kPart>(p.context_lens + s);
+      first_row[s] = load<kPart>(p.new_lens + s);
+      base[s] = p.borrowed != nullptr ? load<kPart>(p.borrowed + s) : 0;
+      mine = plan_seq(p, held[s], first_row[s], base[s], tells);
+    } else {
+      mine = lengths_of(s, tells);
+    }
     at[0] += mine.give + ((int64_t)mine.ends << kEnds);
     at[1] += mine.need;
     at[2] += mine.n;
@@ -224,7 +241,9 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
   {
     int64_t give = at[0], need = at[1], row = at[2];
     for (int s = s0; s < s1; ++s) {
-      const PlanSeq q = per == 1 ? mine : plan_seq(p, s, false);
+      const PlanSeq q = per == 1          ? mine
+                        : kPart == kState ? plan_seq(p, held[s], first_row[s], base[s], false)
+                                          : lengths_of(s, false);
       const bool no_blocks = q.need > 0 && need + q.need > left;
       const bool no_rows = q.n > 0 && row + q.n > p.num_rows;
       if (tells && (no_blocks || no_rows))
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
     }
   }
   if (tid == 0) first_row[S] = saturated(total[2]);
-  if (p.part == kRows) {
+  if (kPart == kRows) {
     __syncthreads();
   } else {
     // Blocks taken: those up to the last sequence that takes any.
@@ -256,7 +275,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
     scan_cta<1>(keys, all_keys, sums1);  // (its barriers also publish the arrays)
   }
   // (nobody reads lengths or counters any more)
-  if (ctas > 1 && p.part != kRows) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  if (ctas > 1 && kPart != kRows) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
   // The e-th of the sequences that end gives its blocks from held[s] on as numbers
   // given_before(e), ... of those that come back.
@@ -264,7 +283,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
   // Block number b of the blocks needed, from the top of the stack.
   auto block_at = [&](int64_t b) -> int {
     const int64_t i = (int64_t)left - 1 - b;
-    if (i < free0) return i >= 0 ? p.free_blocks[i] : -1;
+    if (i < free0) return i >= 0 ? load<kPart>(p.free_blocks + i) : -1;
     const int k = (int)(i - free0);
     int lo = 0, hi = ends;  // the last one with given_before <= k
     while (hi - lo > 1) {
@@ -273,14 +292,14 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
       else hi = mid;
     }
     const int s = ending[lo];
-    return p.block_tables[(int64_t)s * p.max_blocks_per_seq + held[s] + k - given_before(lo)];
+    return load<kPart>(p.block_tables + (int64_t)s * p.max_blocks_per_seq + held[s] + k - given_before(lo));
   };
   // Rows: one a thread where that is enough of them.
   const int64_t threads = (int64_t)ctas * blockDim.x, me = (int64_t)rank * blockDim.x + tid;
-  if (p.part != kState) {
+  if (kPart != kState) {
     auto block_of = [&](int s, int L, int b) {
       const int have = (L + bs1) >> shift;
-      return b < have ? p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]
+      return b < have ? load<kPart>(p.block_tables + (int64_t)s * p.max_blocks_per_seq + b)
                       : block_at((int64_t)base[s] + b - have);
     };
     if (p.num_rows <= threads) {
@@ -290,11 +309,11 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
         write_rows<4>(p, first_row, held, t0, block_of);
     }
   }
-  if (p.part == kRows) return;
+  if (kPart == kRows) return;
   // Few rows: the stack and the tables are for other warps than the rows (each waits for a
   // load of its own).
   const int W = ctas * warps, w = warp * ctas + rank;
-  const int row_warps = ctas == 1 && p.part == kAll && 64 * p.num_rows <= 32 * threads ? (int)(p.num_rows + 31) >> 5 : 0;
+  const int row_warps = ctas == 1 && kPart == kAll && 64 * p.num_rows <= 32 * threads ? (int)(p.num_rows + 31) >> 5 : 0;
   // Sequences that end give their blocks back, the first one's first.
   // (few of them to a warp: its lanes are for their blocks)
   {
@@ -312,7 +331,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
       for_items(count, [&](int owner, int i, bool live) {
         const int64_t at = __shfl_sync(0xffffffffu, from, owner) + i;
         const int64_t place = (int64_t)free0 + __shfl_sync(0xffffffffu, to, owner) + i;
-        if (live && place < p.capacity) p.free_blocks[place] = p.block_tables[at];
+        if (live && place < p.capacity) p.free_blocks[place] = load<kPart>(p.block_tables + at);
       });
     }
   }
@@ -337,7 +356,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
     }
   }
   // Lengths and sums, once every CTA has read those from before.
-  if (p.part == kState) {
+  if (kPart == kState) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
@@ -351,7 +370,7 @@ __global__ void __launch_bounds__(kPlanManyThreads) plan_step_kernel(const PlanP
       p.cu_k[s] = saturated(key);
       if (after > 0) key += after;
       if (after >= 0) p.new_context_lens[s] = after;
-      else p.new_context_lens[s] = p.context_lens[s];  // as it was
+      else p.new_context_lens[s] = load<kPart>(p.context_lens + s);  // as it was
     }
     if (tid == 0) {
       int64_t got = 0;
@@ -426,7 +445,10 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   const int threads = small ? kPlanSmallSeqs : num_seqs <= kPlanManySeqs ? kPlanThreads : kPlanManyThreads;
   const int smem = (3 * num_seqs + 1) * 4 + (num_seqs * 2 + 3) / 4 * 4;
   static_assert((3 * kPlanMaxSeqs + 1) * 4 + kPlanMaxSeqs * 2 + 1024 <= 232448, "shared memory");
-  if (!kernel_smem_setup((const void *)plan_step_kernel, threads, smem, nullptr))
+  const bool rows_apart = !small && num_rows > 0;
+  const auto kernel = rows_apart ? plan_step_kernel<kState> : plan_step_kernel<kAll>;
+  if (!kernel_smem_setup((const void *)kernel, threads, smem, nullptr) ||
+      (rows_apart && !kernel_smem_setup((const void *)plan_step_kernel<kRows>, threads, smem, nullptr)))
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = smem;
@@ -439,7 +461,7 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cudaError_t err = cudaSuccess;
-  if (!small && num_rows > 0) {
+  if (rows_apart) {
     const int sms = device_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     // A row a thread on up to half of the SMs, else four (115 thousand rows 7.0 us with one
@@ -449,15 +471,13 @@ extern "C" pkv_status pkv_plan_step(const int32_t *new_lens, const int32_t *cont
     cfg.gridDim = dim3((unsigned)(ctas < sms ? ctas : sms));
     cfg.blockDim = dim3(threads);
     cfg.numAttrs = 1;  // (no cluster)
-    prm.part = kRows;
-    err = cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+    err = cudaLaunchKernelEx(&cfg, plan_step_kernel<kRows>, prm);
   }
   if (err == cudaSuccess) {
-    prm.part = small || num_rows == 0 ? kAll : kState;
     cfg.gridDim = dim3(small ? 1 : kPlanCluster);
     cfg.blockDim = dim3(threads);
     cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, plan_step_kernel, prm);
+    cudaLaunchKernelEx(&cfg, kernel, prm);
   }
   return launch_status();
 }
