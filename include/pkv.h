@@ -535,7 +535,9 @@ pkv_status pkv_rope_turns(const double *inv_freq, int num_pairs, uint64_t *turns
  * k_out k, where those are contiguous; other overlaps of outputs and inputs return
  * PKV_ERR_INVALID_ARG (caches are not checked).  slot_mapping as for kv_store: -1
  * skips (q_out and k_out are written all the same), other slots out of range are
- * flagged (PKV_DEV_BAD_SLOT) and skipped, slots >= 0 must be unique.
+ * flagged (PKV_DEV_BAD_SLOT) and skipped, slots >= 0 must be unique.  A wait that runs
+ * out (PKV_DEV_TIMEOUT; only calls of many tokens wait) leaves the call's rows of q_out
+ * and k_out and its slots of the caches undefined, and nothing else touched.
  *
  * One launch.  Supported: head_dim in {64, 128}; rotary_dim a multiple of 16 from 0
  * (then turns and positions may be NULL) to head_dim; at most 65536 heads of a kind.
@@ -551,6 +553,15 @@ pkv_status pkv_norm_rope_store(uint16_t *q_out, uint16_t *k_out, const uint16_t 
                                int64_t v_token_stride, int rotary_dim, int interleaved, float eps,
                                float amplitude, int64_t num_blocks, int block_size,
                                int32_t *dev_status, void *stream);
+
+/*
+ * test_rope_fault -- TEST-ONLY, for norm_rope_store: sets, for the current device, the
+ * wall-clock limit of every wait (default 1 s) and, for the process, how many CTAs of a
+ * call of many tokens load them (the others wait for theirs in vain, PKV_DEV_TIMEOUT;
+ * -1: all, the default).  Restore with pkv_test_rope_fault(1000000000, -1).
+ * Synchronous.  Returns PKV_ERR_INVALID_ARG for wait_limit_ns <= 0 or loading_ctas < -1.
+ */
+pkv_status pkv_test_rope_fault(int64_t wait_limit_ns, int loading_ctas);
 
 /*
  * Bytes of device workspace paged_decode_shared_attn needs: the plan of the batch and

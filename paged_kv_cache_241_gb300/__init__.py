@@ -88,6 +88,7 @@ SIGNATURES = {
     "pkv_norm_rope_store": (_c_int, [_p] * 12 + [_c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64,
                                                  _c_i64, _c_int, _c_int, _c_f, _c_f, _c_i64,
                                                  _c_int, _p, _p]),
+    "pkv_test_rope_fault": (_c_int, [_c_i64, _c_int]),
     "pkv_decode_shared_workspace_size": (_c_sz, [_c_int] * 5),
     "pkv_paged_decode_shared_attn": (_c_int, [_p] * 8 + [_c_int] * 7 + [_c_i64, _c_f, _p, _c_sz,
                                                                         _p, _p]),
@@ -695,6 +696,13 @@ def norm_rope_store(q_out, q, k, v, positions, turns, k_cache=None, v_cache=None
             ("slot_mapping", slot_mapping, i32, 1)), dev_status)
     if st:
         raise PkvError(st, "pkv_norm_rope_store")
+
+
+def test_rope_fault(wait_limit_ns: int, loading_ctas: int) -> None:
+    """TEST ONLY: shorten the wait limit of norm_rope_store on the current device, and let
+    only the first `loading_ctas` CTAs of a call of many tokens load them (-1: all).
+    Restore with test_rope_fault(10**9, -1)."""
+    _check(load().pkv_test_rope_fault(int(wait_limit_ns), int(loading_ctas)), "test_rope_fault")
 
 
 def decode_shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,

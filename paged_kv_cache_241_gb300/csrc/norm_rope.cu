@@ -21,6 +21,8 @@
 // us in a graph of calls: one load, the angles, one store).
 #include <math.h>
 
+#include <atomic>
+
 #include "host_common.h"
 #include "pkv_common.cuh"
 
@@ -67,6 +69,7 @@ struct RopeParams {
   int tokens_per_cta;
   int warp_bytes;       // shared memory of a warp (stream)
   int first_heads;      // query heads of the first half of a token (stream; 0: no halves)
+  int loading;          // CTAs that load their tokens (stream): all, but in a test
   float eps;
   float amplitude;
 };
@@ -284,7 +287,9 @@ __global__ void __launch_bounds__(kRopeStreamWarps * 32, 1) norm_rope_stream_ker
   const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t first = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   const uint64_t policy = l2_policy_evict_first();
+  const bool loads = (int)blockIdx.x < p.loading;
   auto load = [&](int64_t item, int place) {  // (lane 0)
+    if (!loads) return;
     const int64_t t = item >> halves;
     uint8_t *to = rows + place * row_bytes;
     if (halves && (item & 1) == 0) {
@@ -496,6 +501,10 @@ pkv_status launch_rope(RopeParams prm, cudaStream_t stream) {
                           (int)(prm.tokens_per_cta * (prm.rotary * sizeof(float) + sizeof(int64_t))), stream, prm);
 }
 
+// Test-only, set by pkv_test_rope_fault: RopeParams::loading of the process's calls.
+constexpr int kRopeAllLoad = 0x7FFFFFFF;
+std::atomic<int> g_loading{kRopeAllLoad};
+
 // [a, a + n) and [b, b + m) values of 16 bits have any in common.
 bool overlap16(const uint16_t *a, int64_t n, const uint16_t *b, int64_t m) {
   if (a == nullptr || b == nullptr || n <= 0 || m <= 0) return false;
@@ -600,10 +609,20 @@ extern "C" pkv_status pkv_norm_rope_store(
   prm.tokens_per_cta = 0;
   prm.warp_bytes = 0;
   prm.first_heads = 0;
+  prm.loading = g_loading.load(std::memory_order_relaxed);
   prm.eps = eps;
   prm.amplitude = amplitude;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (head_dim == 128)
     return interleaved ? launch_rope<128, true>(prm, st) : launch_rope<128, false>(prm, st);
   return interleaved ? launch_rope<64, true>(prm, st) : launch_rope<64, false>(prm, st);
+}
+
+extern "C" pkv_status pkv_test_rope_fault(int64_t wait_limit_ns, int loading_ctas) {
+  if (wait_limit_ns <= 0 || loading_ctas < -1) return PKV_ERR_INVALID_ARG;
+  const unsigned long long limit = (unsigned long long)wait_limit_ns;
+  if (cudaMemcpyToSymbol(pkv::g_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  pkv::g_loading = loading_ctas >= 0 ? loading_ctas : pkv::kRopeAllLoad;
+  return PKV_OK;
 }
