@@ -565,7 +565,7 @@ pkv_status pkv_test_rope_fault(int64_t wait_limit_ns, int loading_ctas);
 
 /*
  * Bytes of device workspace paged_decode_shared_attn needs: the plan of the batch and
- * the parts of its rows.  Returns 0 for invalid sizes.
+ * the parts of its rows.  Returns 0 for invalid sizes, more than 8192 sequences among them.
  */
 size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                         int num_kv_heads, int head_dim);

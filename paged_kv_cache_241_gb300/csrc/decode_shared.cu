@@ -1654,7 +1654,10 @@ extern "C" size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups,
   using namespace pkv;
   if (num_seqs <= 0 || num_groups <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0)
     return 0;
-  if (num_q_heads > (1 << 16) || head_dim > (1 << 16) || num_q_heads < num_kv_heads) return 0;
+  // (more sequences than any call takes: their bytes need not fit 64 bits)
+  if (num_seqs > kSharedMaxSeqs || num_q_heads > (1 << 16) || head_dim > (1 << 16) ||
+      num_q_heads < num_kv_heads)
+    return 0;
   return Workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim).total;
 }
 
