@@ -384,8 +384,8 @@ struct WarpSmem {
 // two tiles ahead and across sequences; nothing in the loop waits for another warp, and
 // the warps of the other kv heads of the same tokens run beside it.  Per 16 tokens:
 // S = K q^T (tokens x dims x heads) and O^T += V^T P (dims x tokens x heads).  P is an
-// operand in bf16: it goes in as the sum of two, its rounding and what that leaves, so
-// that a weight is off by 2^-18 of itself and not by 2^-9 (paged_decode_attn keeps it in
+// operand in bf16: it goes in as the sum of two, the weight cut and what that leaves, so
+// that it is off by 2^-16 of itself and not by 2^-8 (paged_decode_attn keeps it in
 // fp32).  With at most four heads columns 4 to 7 repeat the heads of 0 to 3 and take the
 // second parts; eight heads need a second product.
 //
@@ -570,9 +570,9 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
           }
           // P as the second operand of the next product, in two parts (see above);
           // the sums keep the fp32 weights.
-          uint32_t first0 = pack_bf16x2(p0, p1), first1 = pack_bf16x2(p2, p3);
-          const uint32_t rest0 = pack_bf16x2(p0 - bf16lo(first0), p1 - bf16hi(first0));
-          const uint32_t rest1 = pack_bf16x2(p2 - bf16lo(first1), p3 - bf16hi(first1));
+          uint32_t first0 = cut_bf16x2(p0, p1), first1 = cut_bf16x2(p2, p3);
+          const uint32_t rest0 = rest_bf16x2(p0 - bf16lo(first0), p1 - bf16hi(first0));
+          const uint32_t rest1 = rest_bf16x2(p2 - bf16lo(first1), p3 - bf16hi(first1));
           if (G < 8 && (lane & 2)) {
             first0 = rest0;
             first1 = rest1;
@@ -705,11 +705,6 @@ __device__ __forceinline__ void store32(float *ptr, const float (&v)[32], int i)
 // Steps [0, n) of a piece that chain h takes.
 __device__ __forceinline__ int chain_steps(const Piece &u, int h) {
   return u.rows > BM ? u.n : (u.n + 1 - h) >> 1;
-}
-
-// Two floats cut (not rounded) to bf16, packed.
-__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 template <int D>
@@ -1117,11 +1112,11 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
               const int w = (c - hf * 32) / 2;
               hi[w] = __uint_as_float(h01);
               hi[w + 1] = __uint_as_float(h23);
-              // (what the cut leaves, exact in fp32, is rounded: 2^-17 of the weight)
+              // (what the cut leaves is exact in fp32)
               const float2 d01 = __fadd2_rn(p01, make_float2(-bf16lo(h01), -bf16hi(h01)));
               const float2 d23 = __fadd2_rn(p23, make_float2(-bf16lo(h23), -bf16hi(h23)));
-              lo[w] = __uint_as_float(pack_bf16x2(d01.x, d01.y));
-              lo[w + 1] = __uint_as_float(pack_bf16x2(d23.x, d23.y));
+              lo[w] = __uint_as_float(rest_bf16x2(d01.x, d01.y));
+              lo[w + 1] = __uint_as_float(rest_bf16x2(d23.x, d23.y));
             }
             tmem_store16_async(sp + hf * 16, hi);
             tmem_store16_async(sp + 32 + hf * 16, lo);

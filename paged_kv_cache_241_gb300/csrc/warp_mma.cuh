@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "pkv_common.cuh"
+
 namespace pkv {
 
 // 16-byte asynchronous copy; zeros instead when !take.
@@ -42,6 +44,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A weight p >= 0 as the sum of two bf16 for a product with V: cut (not rounded), and what that
+// leaves, rounded, off by 2^-16 of the weight.  Two weights at a time, packed.  The second part
+// is 2^-126 at least: zero or below it would make NaN of an infinite value, whose product with
+// the first is right.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) {  // (of p less its cut)
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_bf16x2(lo, hi)), "r"(0x00800080u));
+  return r;
 }
 
 // Byte offset of 16-byte column c of row r in a tile of rows of D values: the
