@@ -323,9 +323,10 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
  *   key_weights(slot of p, j)  = a[s,j,p]  for p = context_lens[s] - 1
  * (the newest token is this call's own: its slot's old sum was another's).
  * fp32 logits and statistics; for the product with V alone the weights are
- * taken as the sum of two bf16 (off by 2^-18 of a weight).  The batch's tokens are cut
- * into runs of equal length, so the last bits of a sequence's results can
- * change with the other sequences' lengths; the same call gives the same bits.
+ * taken as the sum of two bf16 (off by 2^-17 of a weight; an infinite value may give
+ * NaN, its weight's second part being zero or below).  The batch's tokens are cut into
+ * runs of equal length, so the last bits of a sequence's results can change with the
+ * other sequences' lengths; the same call gives the same bits.
  *
  * workspace: device memory of at least pkv_decode_weights_workspace_size(...)
  * bytes, 256-byte aligned; it needs no initialisation (a call reads what it has
@@ -474,6 +475,7 @@ pkv_status pkv_kv_evict(uint16_t *k_cache, uint16_t *v_cache, float *key_weights
  *   new_context_lens, *new_num_free (may be context_lens and num_free themselves, but
  *                                   not overlap them otherwise, PKV_ERR_INVALID_ARG;
  *                                   where they are others, a call can be repeated)
+ * No other two of the arrays may overlap (not checked).
  *
  * A sequence whose blocks the stack does not hold is refused, PKV_DEV_NO_BLOCKS, and
  * with it all later ones that need any: those keep what they have, their rows have
@@ -527,8 +529,9 @@ pkv_status pkv_rope_turns(const double *inv_freq, int num_pairs, uint64_t *turns
  * y' of q goes to q_out [T, Hq, D], that of k to slot slot_mapping[t] of k_cache and, if
  * k_out is not NULL, to k_out [T, Hkv, D]; v goes to v_cache as it is, to the bit.
  * k_cache, v_cache and slot_mapping all NULL: nothing is stored, v is not read and
- * k_out is required.  All arithmetic in fp32, rounded once, to bf16.  positions may be
- * any int32 (negative ones turn backwards).
+ * k_out is required.  All arithmetic in fp32, rounded once, to bf16 (a head whose squares
+ * add up to 2^128 or more has an infinite norm and comes out as zeros).  positions may
+ * be any int32 (negative ones turn backwards).
  *
  * q, k, v: as in kv_store, values between tokens given by their strides (0 =
  * contiguous), so that all three may be parts of one projection.  q_out may be q, and
@@ -584,7 +587,7 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  * is attended like any other sequence, and so is every one where all contexts together
  * are so short that reading them whole is faster.  pkv_bm_prefix_groups finds groups.
  * fp32 logits and statistics; for the product with V alone the weights are taken as the
- * sum of two bf16 (off by 2^-17 of a weight).  How the work is split depends on the
+ * sum of two bf16 (off by 2^-16 of a weight).  How the work is split depends on the
  * batch, and with it the last bits; the same call gives the same bits.
  *
  * A sequence of context length <= 0 is flagged (PKV_DEV_BAD_CONTEXT) and its row of out
@@ -601,7 +604,11 @@ size_t pkv_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_
  *
  * scale: finite, and scale * log2(e) too (else PKV_ERR_INVALID_ARG).
  *
- * Three launches, two for small batches and one for those of few and short contexts.
+ * out may be q.  Three launches, chosen by sizes and not by the lengths, which the host
+ * does not know: two where num_seqs <= 384 and the tables have room for at most 16 MiB of
+ * K and V (num_seqs * max_blocks_per_seq blocks), one where they have room for at most
+ * 1024 tokens a sequence (512 for Hq/Hkv of 8) and num_seqs * num_kv_heads is at most two
+ * per SM.  So tables trimmed to the batch make a call of few short contexts faster.
  * Supported: head_dim in {64, 128}; Hq/Hkv in {1, 2, 4, 8}; block_size in {64, 128, 256,
  * 512}; num_seqs <= 8192, 1 <= num_groups <= num_seqs (else PKV_ERR_INVALID_ARG); at most
  * 4096 kv heads; max_blocks_per_seq * block_size at most 2^20.

@@ -31,8 +31,9 @@
 // chain, a step took 1.43); tails HBM; and all of it a fixed part of 15 to 18 us: the plan 3
 // us, from the beginning of a CTA to its first product 4.5, from a run's last product to its
 // stores 2.5, the join 2.5, what is between the launches 3.  In a graph of calls, floors by
-// bytes in brackets: 64 sequences behind 2048 tokens 31.6 us [21.8], 50 in 6 groups 26.1
-// [9.7], 16 on a document of 32,000 37.4 [20.9], 128 behind 8192 48.9 [25.5], 2 short 3.7.
+// bytes in brackets: 64 sequences behind 2048 tokens 31.1 us [21.8], 50 in 6 groups 26.3
+// [9.7], 16 on a document of 32,000 37.3 [20.9], 128 behind 8192 48.9 [25.5], 2 short 3.8
+// (in tables of two blocks; of 8192 tokens 6.5).
 #include <math.h>
 
 #include <atomic>

@@ -153,7 +153,7 @@ struct WarpSmem {
 // run at: the loop is there to keep loads in flight (128 KB per SM).
 //
 // P is an operand in bf16: it goes in as the sum of two, its rounding and what
-// that leaves, so that a weight is off by 2^-18 of itself and not by 2^-9 (the
+// that leaves, so that a weight is off by 2^-17 of itself and not by 2^-8 (the
 // attention of paged_decode_attn keeps it in fp32; the outputs of the two then
 // differ by their own rounding alone).  A group of at most four heads has columns
 // to spare: columns 4 to 7 repeat the heads of 0 to 3 and take the second parts,

@@ -17,7 +17,7 @@
 //
 // Bound by HBM where there are many tokens, as every value is read once and written once:
 // 16 prompts of 16 + 8 + 8 heads (537 MB) 89 us, 89 % of a copy's rate, 11 far chunks of
-// 32 + 8 + 8 (258 MB) 44.3 us, 86 %.  By latency where there are few (up to 64 tokens 2.7
+// 32 + 8 + 8 (258 MB) 44.3 us, 86 %.  By latency where there are few (up to 64 tokens 2.8
 // us in a graph of calls: one load, the angles, one store).
 #include <math.h>
 
@@ -43,6 +43,10 @@ constexpr int kRopeSmem = 220 * 1024;
 // of 16 + 8 + 8 heads: one token to a CTA, eight, streamed in halves, streamed whole):
 //   150 tokens 2.8 6.7 4.0 6.1, 600 5.3 7.4 4.2 6.1, 1800 12.0 9.9 7.9 8.1,
 //   3500 25.7 13.6 14.9 15.6, 6000 41.8 23.2 23.1 24.5, 12000 80.6 42.8 41.0 38.6
+// (From about 2000 to 5000 tokens eight to a CTA are up to a tenth faster.  Other layouts,
+// us by these rules and floors of bytes at a copy's rate: of 4 + 2 + 2 heads of 64 dims 600
+// tokens 3.3 and 0.2, 3500 5.1 and 1.1, 12000 14.2 and 3.6; of 32 + 8 + 8 of 128 600 5.7 and
+// 2.2, 3500 19.8 and 12.7, 12000 55.3 and 43.4.)
 constexpr int kRopeStreamTokens = 3;
 constexpr int kRopeWholeTokens = 64;
 

@@ -20,7 +20,7 @@
 //
 // Bound by latency: a step of 64 sequences reads and writes 2 KB, and takes one load of
 // the lengths, one of blocks from the stack or a table, and the barriers between them: 4.1
-// us in a graph of calls (two sequences 3.0, 500 prompts with 2 MB of rows and tables 7.0).
+// us in a graph of calls (two sequences 2.9, 500 prompts with 2 MB of rows and tables 6.9).
 #include "cta_scan.cuh"
 #include "host_common.h"
 #include "pkv_common.cuh"
