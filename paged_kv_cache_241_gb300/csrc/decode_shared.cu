@@ -572,8 +572,8 @@ __device__ __forceinline__ void tails(const SharedParams &p, const Totals &sum, 
           // P as the second operand of the next product, in two parts (see above);
           // the sums keep the fp32 weights.
           uint32_t first0 = cut_bf16x2(p0, p1), first1 = cut_bf16x2(p2, p3);
-          const uint32_t rest0 = rest_bf16x2(p0 - bf16lo(first0), p1 - bf16hi(first0));
-          const uint32_t rest1 = rest_bf16x2(p2 - bf16lo(first1), p3 - bf16hi(first1));
+          const uint32_t rest0 = rest_bf16x2(p0, p1, first0);
+          const uint32_t rest1 = rest_bf16x2(p2, p3, first1);
           if (G < 8 && (lane & 2)) {
             first0 = rest0;
             first1 = rest1;
@@ -1097,6 +1097,7 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
           // (a maximum of -inf: every weight so far is zero, whatever the reference)
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 q2 = make_float2(qs, qs), nm2 = make_float2(-ref, -ref);
+          const float2 up2 = make_float2(kAboveCut, kAboveCut);
           float2 r01 = make_float2(0.f, 0.f), r23 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -1113,11 +1114,11 @@ __device__ __forceinline__ void prefixes(const CUtensorMap &tm_q, const CUtensor
               const int w = (c - hf * 32) / 2;
               hi[w] = __uint_as_float(h01);
               hi[w + 1] = __uint_as_float(h23);
-              // (what the cut leaves is exact in fp32)
-              const float2 d01 = __fadd2_rn(p01, make_float2(-bf16lo(h01), -bf16hi(h01)));
-              const float2 d23 = __fadd2_rn(p23, make_float2(-bf16lo(h23), -bf16hi(h23)));
-              lo[w] = __uint_as_float(rest_bf16x2(d01.x, d01.y));
-              lo[w + 1] = __uint_as_float(rest_bf16x2(d23.x, d23.y));
+              // (rest_bf16x2, two at a time)
+              const float2 d01 = __ffma2_rn(p01, up2, make_float2(-bf16lo(h01), -bf16hi(h01)));
+              const float2 d23 = __ffma2_rn(p23, up2, make_float2(-bf16lo(h23), -bf16hi(h23)));
+              lo[w] = __uint_as_float(pack_bf16x2(d01.x, d01.y));
+              lo[w + 1] = __uint_as_float(pack_bf16x2(d23.x, d23.y));
             }
             tmem_store16_async(sp + hf * 16, hi);
             tmem_store16_async(sp + 32 + hf * 16, lo);

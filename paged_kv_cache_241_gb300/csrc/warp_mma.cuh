@@ -47,16 +47,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // A weight p >= 0 as the sum of two bf16 for a product with V: cut (not rounded), and what that
-// leaves, rounded, off by 2^-16 of the weight.  Two weights at a time, packed.  The second part
-// is 2^-126 at least: zero or below it would make NaN of an infinite value, whose product with
-// the first is right.
+// leaves, rounded, off by 2^-16 of the weight.  Two weights at a time, packed.  What the cut
+// leaves is taken of p and 2^-23 of it, fma(p, kAboveCut, -cut), and so above zero (from p =
+// 2^-110 on; 0 of p = 0): a second part of zero or below would make NaN of an infinite value,
+// whose product with the first is right.
+constexpr float kAboveCut = 1.f + 0x1p-23f;
 __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
-__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) {  // (of p less its cut)
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_bf16x2(lo, hi)), "r"(0x00800080u));
-  return r;
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi, uint32_t cut) {
+  return pack_bf16x2(fmaf(lo, kAboveCut, -bf16lo(cut)), fmaf(hi, kAboveCut, -bf16hi(cut)));
 }
 
 // Byte offset of 16-byte column c of row r in a tile of rows of D values: the

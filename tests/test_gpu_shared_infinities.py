@@ -66,3 +66,26 @@ def test_a_context_whose_logits_are_all_minus_infinity(lib, groups, wide, always
     assert bool(s.out[last].isnan().all())
     # (all but the last sequence: it shares nothing)
     assert torch.equal(s.out[:last], want[:last])
+
+
+@pytest.mark.parametrize("always", [pytest.param(False, marks=pytest.mark.by_choice), True])
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 64), (8, 2, 128), (8, 1, 64)])
+@pytest.mark.parametrize("groups", [[(0, [5, 100, 3])], [(2, [1, 70, 64]), (0, [300])]])
+@pytest.mark.parametrize("wide", [0, 40])
+def test_huge_values_of_tokens_that_weigh_nothing(lib, groups, Hq, Hkv, D, wide, always):
+    """Zero times the largest bf16 is zero: not a part of a weight that is kept above zero for infinities' sake."""
+    s = Shared(groups, Hq, Hkv, D, wide=wide)
+    s.q.abs_()
+    places = [(int(s.tables[i, p // s.block]), p % s.block) for i, L in enumerate(s.ctx) for p in {0, L // 2} if L > 1]
+    for block, at in places:
+        s.kc[block, at] = -INF
+    outs = []
+    for value in (0.0, torch.finfo(torch.bfloat16).max):
+        for block, at in places:
+            s.vc[block, at] = value
+        s.out.fill_(7.0)
+        lib.paged_decode_shared_attn(**s.args(lib))
+        torch.cuda.synchronize()
+        outs.append(s.out.clone())
+    some = [i for i, L in enumerate(s.ctx) if L > 2]
+    assert bool(outs[0][some].isfinite().all()) and torch.equal(outs[0][some], outs[1][some])
